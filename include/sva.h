@@ -71,6 +71,9 @@ typedef enum { SV_BF16 = 0, SV_F32 = 1 } sv_dtype;
 #define SV_FLAG_WAIT_TIMEOUT 0x4u     /* a pipeline wait gave up (never hangs) */
 #define SV_FLAG_STALE_WORKSPACE 0x8u  /* a per-(b, h) merge word held a count left by an
                                          earlier call (sv_reset_workspace repairs it) */
+#define SV_FLAG_NO_PAGE 0x10u         /* sv_build_tables: the free pages ran out          */
+#define SV_FLAG_BAD_LENGTH 0x20u      /* a length, offset or count in device memory lies
+                                         outside its range (it was clamped to it)         */
 
 /* Problem shape. Stacked query rows per KV head: R = T * (Hq / Hkv). */
 typedef struct {
@@ -420,6 +423,118 @@ sv_status sv_sparse_attend_noalloc(const sv_shape* shape, const void* q, const s
                                    const void* draft_k, const void* draft_v,
                                    const int32_t* draft_parent, void* out, uint32_t* flags_out,
                                    void* stream);
+
+/* ------------------------------------------------------------------------
+ * The paged cache around verification: pages for requests, prompts into
+ * pages, attention of prompts, verification of a batch with a common prefix.
+ * A request's life: sv_build_tables gives it pages and its new tokens slots,
+ * sv_write_kv stores their K/V, sv_prompt_attend attends over them (the whole
+ * prompt, a chunk of it, or one token), sv_build_reps pools the filled
+ * blocks, then sv_verify_layer or sv_prefix_attend verifies drafts and
+ * sv_append_kv stores the accepted ones.
+ * ------------------------------------------------------------------------ */
+
+/* Block tables and slot maps from request lengths. Request b goes from
+ * old_len[b] to new_len[b] tokens; with nb(x) = ceil(x / blk):
+ *   - a request that shrinks (new_len 0: it ends) lets go of its blocks
+ *     max(nb(new), pinned[b]) .. nb(old) - 1, pushed on the stack of free
+ *     pages in descending (request, block) order; pinned (may be NULL = all
+ *     0) counts leading blocks whose pages it does not own, such as a prefix
+ *     shared with other requests;
+ *   - a request that grows gets pages for blocks nb(old) .. nb(new) - 1,
+ *     taken from the top of the stack in ascending (request, block) order
+ *     after all releases of the call. A release is thereby the exact inverse
+ *     of the allocation it mirrors;
+ *   - cu_new[b] = new tokens of the requests before b, cu_new[B] of all;
+ *   - new token i of the call (requests in order, positions ascending) at
+ *     position p of request b gets slot_map[i] = page * blk + p % blk and,
+ *     when positions is not NULL, positions[i] = p; entries from cu_new[B]
+ *     up to n_max are -1, which sv_write_kv skips (a captured step can run
+ *     padded).
+ * block_table: [B, nb_max], entries of the blocks taken are written, all
+ * others are left as they are. free_pages: [num_pages], the stack;
+ * free_count[0] of its entries are free before the call; *free_count_out
+ * (may be free_count itself) receives the count after it. A page must not
+ * be free and held, or held by two requests unpinned, at the same time: the
+ * call cannot see it. Every array is DEVICE memory: nothing is read back, so
+ * the call can be captured.
+ * Flags in the workspace status word (workspace may be NULL):
+ * SV_FLAG_NO_PAGE when the stack ran out (the remaining blocks, in order,
+ * and their slots are -1, and *free_count_out is 0), SV_FLAG_BAD_PAGE for an
+ * entry of the stack or the table outside [0, num_pages) (its slots are -1),
+ * SV_FLAG_BAD_LENGTH for a length outside [0, nb_max * blk] or a count
+ * outside [0, num_pages] (clamped), more new tokens than n_max (the excess
+ * gets pages but no slots) or more free pages than num_pages.
+ * Limits: B <= 4096; num_pages * blk and nb_max * blk < 2^31. */
+sv_status sv_build_tables(int B, int blk, const int32_t* old_len, const int32_t* new_len,
+                          const int32_t* pinned, int32_t* block_table, int nb_max,
+                          int num_pages, int32_t* free_pages, const int32_t* free_count,
+                          int32_t* free_count_out, int32_t* cu_new, int32_t* slot_map,
+                          int32_t* positions, int n_max, void* workspace, void* stream);
+
+/* Packed K/V rows into the paged cache: for i < n with slot s = slot_map[i]
+ * >= 0, k_pool[s / blk][h][s % blk][:] = k[i][h][:] for every KV head h, and
+ * V alike. Slots of -1 are skipped; slots of the others must differ (of two
+ * rows with one slot, any 16-byte piece of either may stay). k, v:
+ * [n, Hkv, d], rows k_stride and v_stride ELEMENTS apart (>= Hkv * d; slices
+ * of a fused projection need no copy), 16-byte aligned with strides of a
+ * multiple of 16 bytes. shape: Hkv, d, blk and dtype are used. A slot
+ * outside the pool is skipped and raises SV_FLAG_BAD_PAGE (workspace may be
+ * NULL). Representatives are not touched: see sv_build_reps. */
+sv_status sv_write_kv(const sv_shape* shape, const void* k, long long k_stride, const void* v,
+                      long long v_stride, const int32_t* slot_map, int n, void* k_pool,
+                      void* v_pool, int num_pages, void* workspace, void* stream);
+
+/* Bytes of workspace for sv_prompt_attend calls of up to n_rows query rows
+ * with this shape (B, Hq, Hkv, d; the largest B is enough), and for
+ * sv_prefix_attend calls with this shape. The whole workspace must be zero
+ * before its first use, every completed call leaves its counts zero, and two
+ * calls that may overlap on the GPU must not share one. The first 256 bytes
+ * hold the status word (sv_read_status, sv_clear_status). After a call that
+ * raised SV_FLAG_WAIT_TIMEOUT or SV_FLAG_STALE_WORKSPACE zero the workspace
+ * again. 0 on an invalid shape. Host only. */
+size_t sv_prompt_workspace_bytes(const sv_shape* shape, int n_rows);
+size_t sv_prefix_workspace_bytes(const sv_shape* shape);
+
+/* Causal attention of packed query rows over the paged cache. Rows
+ * cu_q[b] .. cu_q[b+1] - 1 of q are the LAST n_b = cu_q[b+1] - cu_q[b] of the
+ * seq_ctx[b] tokens that sequence b has in the cache (their own K/V
+ * included); row i of them attends, with softmax scale 1/sqrt(d), to keys
+ * 0 .. seq_ctx[b] - n_b + i. So n_b = seq_ctx[b] is a whole prompt, n_b <
+ * seq_ctx[b] a chunk on top of what is cached, n_b = 1 a decoding step; one
+ * call may mix them. A row that sees no key (seq_ctx[b] < n_b; flagged) is
+ * zero. Rows behind cu_q[B] are not read or written.
+ * q: [n_rows, Hq, d], rows q_stride ELEMENTS apart (>= Hq * d, a multiple of
+ * 16 bytes); out: [n_rows, Hq, d] dense. seq_ctx [B] and cu_q [B + 1] are
+ * DEVICE int32 (cu_q ascending from 0, cu_q[B] <= n_rows): nothing is read
+ * back, so a captured call follows the lengths. shape->T is not used.
+ * block_table: [B, nb_max]; only entries of blocks below ceil(seq_ctx / blk)
+ * are read, and of a last block only its first seq_ctx % blk tokens count,
+ * whatever the rest of its page holds. A page outside the pool raises
+ * SV_FLAG_BAD_PAGE and its keys count as zeros; lengths and offsets outside
+ * their range raise SV_FLAG_BAD_LENGTH and are clamped.
+ * Limits: B <= 1024; nb_max * blk, B * nb_max and num_pages * Hkv * blk
+ * < 2^31. */
+sv_status sv_prompt_attend(const sv_shape* shape, const void* q, long long q_stride, int n_rows,
+                           const void* k_pool, const void* v_pool, const int32_t* block_table,
+                           int nb_max, int num_pages, const int32_t* seq_ctx,
+                           const int32_t* cu_q, void* out, void* workspace, size_t ws_bytes,
+                           void* stream);
+
+/* Full verification of a batch whose sequences share their first n_shared
+ * blocks: the result of sv_sparse_attend with sel == NULL, but the shared
+ * blocks are read once for the whole batch instead of once per sequence. The
+ * rows of all B * T drafts are stacked against the shared pages (those of
+ * sequence 0's table row; the other rows' first n_shared entries are not
+ * read), each sequence's own blocks and drafts are attended apart, and the
+ * parts are joined by log-sum-exp. T = 1 is the single-token step.
+ * n_shared * blk <= every sequence's context; 0 shares nothing. q, draft_k,
+ * draft_v, draft_parent and out as in sv_sparse_attend; workspace from
+ * sv_prefix_workspace_bytes. Limits: B <= 1024. */
+sv_status sv_prefix_attend(const sv_shape* shape, const void* q, const sv_kv* kv, int n_shared,
+                           const void* draft_k, const void* draft_v,
+                           const int32_t* draft_parent, void* out, void* workspace,
+                           size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

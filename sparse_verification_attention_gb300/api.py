@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(_PKG, "libsva.so")
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_UNSUPPORTED, SV_ERR_WORKSPACE, SV_ERR_CUDA, \
     SV_ERR_DEVICE_FAULT = range(6)
 SV_BF16, SV_F32 = 0, 1
-SV_FLAG_BAD_BLOCK_INDEX, SV_FLAG_BAD_PAGE, SV_FLAG_WAIT_TIMEOUT, SV_FLAG_STALE_WORKSPACE = 1, 2, 4, 8
+SV_FLAG_BAD_BLOCK_INDEX, SV_FLAG_BAD_PAGE, SV_FLAG_WAIT_TIMEOUT, SV_FLAG_STALE_WORKSPACE, \
+    SV_FLAG_NO_PAGE, SV_FLAG_BAD_LENGTH = 1, 2, 4, 8, 16, 32
 
 SV_PATH_CUDA_CORES, SV_PATH_MMA_SYNC, SV_PATH_TCGEN05 = 0, 1, 2
 ABI_VERSION = 4  # SV_ABI_VERSION the structures below match
@@ -31,7 +32,9 @@ EXPORTED = ("sv_abi_version", "sv_last_error", "sv_budget_blocks", "sv_workspace
             "sv_clear_status", "sv_read_status", "sv_build_reps", "sv_score_blocks",
             "sv_select_blocks", "sv_score_select", "sv_sparse_attend", "sv_attend_plan",
             "sv_verify_layer", "sv_sparse_attend_noalloc", "sv_append_kv",
-            "sv_selection_overlap", "sv_reset_workspace", "sv_verify_layer_host")
+            "sv_selection_overlap", "sv_reset_workspace", "sv_verify_layer_host",
+            "sv_build_tables", "sv_write_kv", "sv_prompt_workspace_bytes",
+            "sv_prefix_workspace_bytes", "sv_prompt_attend", "sv_prefix_attend")
 
 
 class SvError(RuntimeError):
@@ -99,7 +102,7 @@ def lib() -> C.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "sparse_verification_attention_gb300.build_lib.build()")
         L = C.CDLL(LIB_PATH)
-        vp, i, sz = C.c_void_p, C.c_int, C.c_size_t
+        vp, i, sz, ll = C.c_void_p, C.c_int, C.c_size_t, C.c_longlong
         sig = {
             "sv_abi_version": (i, []),
             "sv_last_error": (C.c_char_p, []),
@@ -128,6 +131,14 @@ def lib() -> C.CDLL:
                                          C.POINTER(BudgetC), vp, vp, vp, vp,
                                          C.POINTER(C.c_int32), i, C.POINTER(SelSlotC),
                                          C.POINTER(C.c_int), vp, vp, vp, sz, vp, vp, vp]),
+            "sv_build_tables": (i, [i, i, vp, vp, vp, vp, i, i, vp, vp, vp, vp, vp, vp, i, vp, vp]),
+            "sv_write_kv": (i, [C.POINTER(Shape), vp, ll, vp, ll, vp, i, vp, vp, i, vp, vp]),
+            "sv_prompt_workspace_bytes": (sz, [C.POINTER(Shape), i]),
+            "sv_prefix_workspace_bytes": (sz, [C.POINTER(Shape)]),
+            "sv_prompt_attend": (i, [C.POINTER(Shape), vp, ll, i, vp, vp, vp, i, i, vp, vp, vp, vp,
+                                     sz, vp]),
+            "sv_prefix_attend": (i, [C.POINTER(Shape), vp, C.POINTER(KV), i, vp, vp,
+                                     C.POINTER(C.c_int32), vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -344,6 +355,137 @@ def sv_verify_layer_host(shape: Shape, q_host, q, kv: KV, reps, budget: Optional
         None if slot is None else C.byref(slot.c), C.byref(k), _ptr(out_host), _ptr(out), _ptr(ws),
         0 if ws is None else ws.numel(), _stream(stream), ci, co))
     return k.value
+
+
+# ------------------------------------------------------------------ paged cache
+def _call(fn, tensors, stream, *args):
+    """fn(*args, stream) with the tensors' device current. None stands for an
+    argument that is left out; the others must lie on one CUDA device."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda or (dev is not None and t.device != dev):
+            raise ValueError("the tensors of a call must lie on one CUDA device")
+        dev = t.device
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)))
+
+
+def _ints(name: str, t: Optional[torch.Tensor], *shape):
+    """Refuse t unless it is a dense int32 tensor of this shape (None: any size)."""
+    if t is None:
+        return
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape) or \
+            any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+
+
+def _dense(name: str, t: torch.Tensor, code: int, *shape):
+    """Refuse t unless it is a dense tensor of the call's dtype and this shape."""
+    if dtype_code(t.dtype) != code or not t.is_contiguous() or t.dim() != len(shape) or \
+            any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be contiguous, of the shape's dtype and of shape {list(shape)}")
+
+
+def _rows(name: str, t: torch.Tensor, code: int, heads: int, d: int) -> int:
+    """The distance of t's rows [n, heads, d], in elements; rows may be strided."""
+    if dtype_code(t.dtype) != code or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or \
+            (t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d))):
+        raise ValueError(f"{name} must be rows [n, {heads}, {d}] of the shape's dtype, each row dense")
+    return t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def sv_build_tables(blk: int, old_len, new_len, block_table, free_pages, free_count, free_count_out,
+                    cu_new, slot_map, positions=None, pinned=None, ws=None, stream=None):
+    """Pages for requests that go from old_len to new_len tokens, and the slots
+    (and positions) of their new tokens. All tensors int32 on the device:
+    old_len, new_len, pinned [B]; block_table [B, nb_max]; free_pages
+    [num_pages], a stack of which free_count[0] entries are free; free_count_out
+    [1] (may be free_count); cu_new [B + 1]; slot_map, positions [n_max]."""
+    B, nb_max = block_table.shape
+    _ints("old_len", old_len, B)
+    _ints("new_len", new_len, B)
+    _ints("pinned", pinned, B)
+    _ints("block_table", block_table, B, nb_max)
+    _ints("free_pages", free_pages, None)
+    _ints("free_count", free_count, 1)
+    _ints("free_count_out", free_count_out, 1)
+    _ints("cu_new", cu_new, B + 1)
+    _ints("slot_map", slot_map, None)
+    _ints("positions", positions, slot_map.shape[0])
+    _call(lib().sv_build_tables, (old_len, new_len, pinned, block_table, free_pages, free_count,
+                                  free_count_out, cu_new, slot_map, positions, ws), stream,
+          B, blk, _ptr(old_len), _ptr(new_len), _ptr(pinned), _ptr(block_table), nb_max,
+          free_pages.shape[0], _ptr(free_pages), _ptr(free_count), _ptr(free_count_out),
+          _ptr(cu_new), _ptr(slot_map), _ptr(positions), slot_map.shape[0], _ptr(ws))
+
+
+def sv_write_kv(shape: Shape, k, v, slot_map, k_pool, v_pool, ws=None, stream=None):
+    """Store the rows k, v [n, Hkv, d] (slices of a fused projection are fine) at
+    their slots of the paged cache; slots of -1 are skipped."""
+    ks = _rows("k", k, shape.dtype, shape.Hkv, shape.d)
+    vs = _rows("v", v, shape.dtype, shape.Hkv, shape.d)
+    if k.shape[0] != v.shape[0]:
+        raise ValueError(f"{k.shape[0]} key rows and {v.shape[0]} value rows")
+    _ints("slot_map", slot_map, k.shape[0])
+    _dense("k_pool", k_pool, shape.dtype, None, shape.Hkv, shape.blk, shape.d)
+    _dense("v_pool", v_pool, shape.dtype, k_pool.shape[0], shape.Hkv, shape.blk, shape.d)
+    _call(lib().sv_write_kv, (k, v, slot_map, k_pool, v_pool, ws), stream, C.byref(shape), _ptr(k),
+          ks, _ptr(v), vs, _ptr(slot_map), k.shape[0], _ptr(k_pool), _ptr(v_pool), k_pool.shape[0],
+          _ptr(ws))
+
+
+def _alloc_zeroed(n: int, device) -> torch.Tensor:
+    if n == 0:
+        raise SvError(SV_ERR_INVALID_ARG, "invalid shape for a workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def alloc_prompt_workspace(shape: Shape, n_rows: int, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for sv_prompt_attend calls of up to n_rows rows."""
+    return _alloc_zeroed(lib().sv_prompt_workspace_bytes(C.byref(shape), n_rows), device)
+
+
+def alloc_prefix_workspace(shape: Shape, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for sv_prefix_attend calls with this shape."""
+    return _alloc_zeroed(lib().sv_prefix_workspace_bytes(C.byref(shape)), device)
+
+
+def sv_prompt_attend(shape: Shape, q, k_pool, v_pool, block_table, seq_ctx, cu_q, out, ws,
+                     stream=None):
+    """Causal attention of the packed rows q [n, Hq, d] (rows may be strided)
+    over the paged cache: rows cu_q[b] .. cu_q[b+1] are the last of the
+    seq_ctx[b] cached tokens of sequence b. out: [n, Hq, d]."""
+    qs = _rows("q", q, shape.dtype, shape.Hq, shape.d)
+    _dense("out", out, shape.dtype, q.shape[0], shape.Hq, shape.d)
+    _dense("k_pool", k_pool, shape.dtype, None, shape.Hkv, shape.blk, shape.d)
+    _dense("v_pool", v_pool, shape.dtype, k_pool.shape[0], shape.Hkv, shape.blk, shape.d)
+    _ints("block_table", block_table, shape.B, None)
+    _ints("seq_ctx", seq_ctx, shape.B)
+    _ints("cu_q", cu_q, shape.B + 1)
+    _call(lib().sv_prompt_attend, (q, k_pool, v_pool, block_table, seq_ctx, cu_q, out, ws), stream,
+          C.byref(shape), _ptr(q), qs, q.shape[0], _ptr(k_pool), _ptr(v_pool), _ptr(block_table),
+          block_table.shape[1], k_pool.shape[0], _ptr(seq_ctx), _ptr(cu_q), _ptr(out), _ptr(ws),
+          0 if ws is None else ws.numel())
+
+
+def sv_prefix_attend(shape: Shape, q, kv: KV, n_shared: int, draft_k, draft_v, parents, out, ws,
+                     stream=None):
+    """sv_sparse_attend over every block for a batch whose sequences share
+    their first n_shared blocks: those are read once for all of them."""
+    _dense("q", q, shape.dtype, shape.B, shape.T, shape.Hq, shape.d)
+    _dense("out", out, shape.dtype, shape.B, shape.T, shape.Hq, shape.d)
+    _dense("draft_k", draft_k, shape.dtype, shape.B, shape.T, shape.Hkv, shape.d)
+    _dense("draft_v", draft_v, shape.dtype, shape.B, shape.T, shape.Hkv, shape.d)
+    if parents is not None and len(parents) != shape.T:
+        raise ValueError(f"{len(parents)} draft parents for T={shape.T} drafts")
+    _call(lib().sv_prefix_attend, (q, draft_k, draft_v, out, ws), stream, C.byref(shape), _ptr(q),
+          C.byref(kv), n_shared, _ptr(draft_k), _ptr(draft_v), _parents(parents), _ptr(out),
+          _ptr(ws), 0 if ws is None else ws.numel())
 
 
 VERIFY_COMPUTE, VERIFY_REUSE, VERIFY_FULL = 0, 1, 2  # sv_verify_layer's reuse values

@@ -10,8 +10,7 @@
 #include <mutex>
 #include <string>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "host.h"
 #include "internal.h"
 
 namespace sva {
@@ -34,6 +33,8 @@ int sm_count() {
 namespace {
 
 thread_local std::string g_err;
+
+}  // namespace
 
 sv_status fail(sv_status st, const char* fmt, ...) {
   char buf[512];
@@ -100,6 +101,8 @@ sv_status check_kv(const sv_shape* s, const sv_kv* kv, bool need_v) {
   }
   return SV_OK;
 }
+
+namespace {
 
 // Full blocks and partial-block tokens of every sequence of a (validated)
 // cache: uniform, or per sequence when kv->seq_ctx is given.
@@ -197,6 +200,8 @@ int plan_cluster(int pairs, int n_units, int per_sm, int* bps, MaxClusters max_c
   return (n_units + per - 1) / per;
 }
 
+}  // namespace
+
 void fill_ancestors(const int32_t* parent, int T, unsigned long long* anc) {
   for (int t = 0; t < kMaxT; ++t) anc[t] = 0ull;
   for (int t = 0; t < T; ++t) {
@@ -232,6 +237,8 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
   });
   return fn;
 }
+
+namespace {
 
 // Encoded tensor maps, kept by what the encoding depends on (which map,
 // base address, sizes): a map describes only an address range and its
@@ -760,17 +767,6 @@ static int budgets_of(const sv_budget* bd, const sv_kv* kv, const Ctxs& c, int B
 }  // namespace sva
 
 using namespace sva;
-
-namespace {
-// An NVTX range named after the C-ABI call, around its whole host side
-// (validation, planning, launches), for timeline tools; a no-op without one.
-struct CallRange {
-  explicit CallRange(const char* name) { nvtxRangePushA(name); }
-  ~CallRange() { nvtxRangePop(); }
-  CallRange(const CallRange&) = delete;
-  CallRange& operator=(const CallRange&) = delete;
-};
-}  // namespace
 
 extern "C" {
 
