@@ -41,6 +41,8 @@ cudaError_t launch_write_kv(const WriteArgs& a, cudaStream_t st);
 constexpr int kMaxSegs = 1025;      // row segments of one call: sequences, and a shared prefix
 constexpr int kMaxPlanCtas = 640;   // CTAs that the split rule counts on (see make_plan)
 constexpr int kSimtRows = 64;       // rows of an item on the CUDA cores
+constexpr int kTcRows = 128;        // rows of a set on the tensor cores; an item has two
+constexpr int kMaxTcCtas = 160;
 
 // One attention over the paged cache. Its query rows lie in segments: runs of
 // consecutive rows ("tokens", Hq heads each) that attend to one sequence of
@@ -88,5 +90,8 @@ inline void paged_heads(PagedArgs* a, int rows) {
 }
 
 cudaError_t launch_paged_simt(PagedArgs a, int dtype, cudaStream_t st);
+// bf16, head dims up to 128, pages that tile 128 keys (or 128 keys a page).
+bool paged_tc_applies(const PagedArgs& a, int dtype);
+cudaError_t launch_paged_tc(PagedArgs a, cudaStream_t st);
 
 }  // namespace sva

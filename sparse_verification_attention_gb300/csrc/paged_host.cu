@@ -29,7 +29,9 @@ PagedLayout paged_layout(size_t counts, size_t rows, int d) {
 }
 
 // Partial rows: items of cut segments are at most 4 per CTA (make_plan), an
-// item has at most the rows of its tile, and of the call.
+// item has at most the rows of its tile, and of the call. 640 CTAs of 64 rows
+// cover 160 of 256 (tensor cores) as well.
+static_assert(kMaxPlanCtas * kSimtRows >= kMaxTcCtas * 2 * kTcRows, "partial rows");
 PagedLayout prompt_layout(const sv_shape& s, int n_rows) {
   const long long own = (long long)std::max(n_rows, 1) * (s.Hq / s.Hkv);
   const size_t rows = (size_t)4 * kMaxPlanCtas * std::min<long long>(kSimtRows, own);
@@ -44,9 +46,9 @@ PagedLayout prefix_layout(const sv_shape& s) {
   a.Hkv = s.Hkv;
   a.G = s.Hq / s.Hkv;
   size_t most = 0, counts = 0;
-  for (int rows : {kSimtRows}) {
+  for (int rows : {kSimtRows, kTcRows}) {
     paged_heads(&a, rows);
-    const int tile = rows / a.gs;
+    const int tile = rows / a.gs * (rows == kTcRows ? 2 : 1);
     auto padded = [&](long long n) {  // rows of the partial tiles of n tokens
       return (size_t)((n + tile - 1) / tile) * std::min<long long>(tile, n) * a.gs * a.hv;
     };
@@ -80,6 +82,10 @@ void fill_paged(PagedArgs* a, const sv_shape* s, void* ws, const PagedLayout& L)
   a->d = s->d;
   a->blk = s->blk;
   a->scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s->d));
+}
+
+cudaError_t launch_paged(const PagedArgs& a, int dtype, cudaStream_t st) {
+  return paged_tc_applies(a, dtype) ? launch_paged_tc(a, st) : launch_paged_simt(a, dtype, st);
 }
 
 size_t elt_bytes(const sv_shape* s) { return s->dtype == SV_BF16 ? 2 : 4; }
@@ -182,7 +188,7 @@ sv_status sv_prompt_attend(const sv_shape* shape, const void* q, long long q_str
   if (shape->B > kMaxSegs - 1)
     return fail(SV_ERR_UNSUPPORTED, "B=%d sequences exceeds %d", shape->B, kMaxSegs - 1);
   if ((r = check_pool(shape, k_pool, v_pool, num_pages)) != SV_OK) return r;
-  if ((long long)nb_max * shape->blk >= kInt || (long long)shape->B * nb_max >= kInt)
+  if ((long long)nb_max * shape->blk >= kInt - 1024 || (long long)shape->B * nb_max >= kInt)
     return fail(SV_ERR_UNSUPPORTED, "block table of %d x %d blocks of %d tokens is too large",
                 shape->B, nb_max, shape->blk);
   if ((long long)n_rows * shape->Hq >= kInt)
@@ -208,7 +214,7 @@ sv_status sv_prompt_attend(const sv_shape* shape, const void* q, long long q_str
   a.seq_ctx = seq_ctx;
   a.cu_q = cu_q;
   a.out = out;
-  const cudaError_t e = launch_paged_simt(a, shape->dtype, (cudaStream_t)stream);
+  const cudaError_t e = launch_paged(a, shape->dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "prompt_attend launch");
 }
 
@@ -259,7 +265,7 @@ sv_status sv_prefix_attend(const sv_shape* shape, const void* q, const sv_kv* kv
   a.var = kv->seq_ctx != nullptr;
   for (int b = 0; a.var && b < shape->B; ++b) a.seq_len[b] = kv->seq_ctx[b];
   fill_ancestors(draft_parent, shape->T, a.anc);
-  const cudaError_t e = launch_paged_simt(a, shape->dtype, (cudaStream_t)stream);
+  const cudaError_t e = launch_paged(a, shape->dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "prefix_attend launch");
 }
 

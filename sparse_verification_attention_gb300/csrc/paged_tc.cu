@@ -1,0 +1,785 @@
+// Attention of packed or stacked query rows over the paged cache on the
+// 5th-generation tensor cores (tcgen05, TMEM accumulators): bf16, head dims up
+// to 128 (64 and 128 exactly, others padded with zeros by the copies).
+//
+// One pass over the keys with a softmax's running maximum and sum: S = Q K^T
+// for 128 rows x 128 keys into TMEM; one thread per row reads it back, forms
+// P = 2^(s - m) in bf16 (fp32 sums) over S in TMEM, and O += P V accumulates in
+// TMEM. O is rescaled only when some row's maximum grew by more than 2^8. P is
+// rounded to bf16 because it is an operand of the second product; its sum is
+// taken before the rounding.
+//
+// The gs query heads of a KV head are stacked with the tokens into the 128
+// rows of a set (128 / gs tokens), so K and V are read once for all heads and a
+// single token still fills gs rows. A CTA runs two sets:
+//   pair:        an item's first and second 128 rows, each over all key tiles;
+//   alternating: one set of rows, set 0 taking the even key tiles and set 1
+//                the odd ones, folded at the end (items of few rows).
+// Either way two independent softmax chains overlap with each other's products.
+//
+// Warps: 0-3 and 4-7 the softmax of set 0 and 1, 8 issues every MMA, 9 takes
+// items from the scheduler, looks pages up and issues the TMA copies, 10-11
+// clear non-finite values out of V tiles that the mask cuts (below).
+// Per set and key tile the MMA warp issues P V of one tile and then S of the
+// next, so that the tensor cores work on the other set while this one's
+// softmax runs.
+//
+// Masked keys have P = 0, but 0 times a non-finite V is not 0: V tiles with a
+// masked key (behind the diagonal, past the context, drafts another draft does
+// not see, and the undefined rest of a last page) are scanned in shared memory,
+// non-finite elements are zeroed and their keys noted, and a row that does see
+// such a key gets the element added again at the end.
+#include <algorithm>
+#include <atomic>
+
+#include "host.h"
+#include "internal.h"
+#include "paged.cuh"
+#include "ptx.h"
+#include "tc.h"
+
+namespace sva {
+namespace {
+
+using namespace paged;
+
+constexpr int kKeys = 128;            // keys of a tile
+constexpr int kRows = kTcRows;        // rows of a set
+constexpr int kBox = 128 * 128;       // 128 rows of 64 columns, bytes
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10;
+constexpr int kItems = 4;             // item ring
+constexpr int kItemReaders = 11;      // MMA, 8 softmax and 2 cleaning warps
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int kMaxMasked = 4;         // masked key tiles of an item, at most 3 (see masked_from)
+// registers per thread of the softmax warps and of the others (the launch
+// gives 168 to each of 384 threads: 2 * 128 * 208 + 128 * 80 <= 384 * 168)
+constexpr int kRegsSoftmax = 208, kRegsOther = 80;
+
+// TMEM columns of set s: S (128 fp32; P, 64 columns of bf16 pairs, takes its
+// place) and O (128 fp32)
+__device__ constexpr uint32_t col_s(int s) { return s ? 128u : 0u; }
+__device__ constexpr uint32_t col_o(int s) { return s ? 384u : 256u; }
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTile = kHalves * kBox;  // a K, V or Q tile, bytes
+  static constexpr int kStages = 131072 / kTile;
+  static constexpr int kSmem = 2 * kTile + kStages * kTile + 1024;
+};
+
+struct Control {
+  uint64_t full[8], empty[8], vclean[8];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_done[2];
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t meet, drained;
+  uint32_t tmem;
+  int abort;
+  int nunits[2];
+  int units[2][257];
+  uint32_t nonfinite[kItems][kMaxMasked][4];  // keys of an item's masked tiles, from the last
+  float2 ml[2][kRows];
+  unsigned long long anc[kMaxT];
+  Item items[kItems];
+  Plan plan;
+};
+
+// What every role derives from an item.
+struct Run {
+  int pair;     // 1: two row sets over all tiles, 0: one over alternating tiles
+  int n[2];     // key tiles of each set
+  int masked;   // first key tile (of the run) with a masked key
+};
+
+__device__ __forceinline__ Run run_of(const Item& it, int tt) {
+  Run r;
+  r.pair = it.ntok > tt;
+  if (r.pair) {
+    r.n[0] = it.causal ? min(it.nk, max(0, ceil_div(max(0, it.vis0 + tt - 1), kKeys) - it.k0)) : it.nk;
+    r.n[1] = it.nk;
+  } else {
+    r.n[0] = (it.nk + 1) / 2;
+    r.n[1] = it.nk / 2;
+  }
+  // Tile j is cut by the mask when some row misses some of its keys: from the
+  // tile that holds key vis0 on (causal), the context's end, and the drafts.
+  // Those tiles span fewer than 256 + 128 keys: at most three.
+  r.masked = max(0, max(0, it.causal ? it.vis0 : it.ctx) / kKeys - it.k0);
+  if (it.draft) r.masked = min(r.masked, it.nk - 1);
+  return r;
+}
+
+// Ring positions of the K and V tiles of an item of n key tiles, relative to
+// its first: the order in which the MMA warp needs them (pair: K0 V0 K1 V1 ...;
+// alternating: K0 K1 V0 K2 V1 ...).
+__device__ __forceinline__ uint32_t pos_k(const Run& r, int j) {
+  return r.pair ? 2 * j : (j == 0 ? 0 : 2 * j - 1);
+}
+__device__ __forceinline__ uint32_t pos_v(const Run& r, int j, int n) {
+  return r.pair || j == n - 1 ? 2 * j + 1 : 2 * j + 2;
+}
+
+// The V tile at ring position pos, -1 where a K tile lies.
+__device__ __forceinline__ int v_at(const Run& r, int pos, int n) {
+  if (r.pair || pos == 2 * n - 1) return pos & 1 ? pos >> 1 : -1;
+  return pos > 0 && !(pos & 1) ? (pos >> 1) - 1 : -1;
+}
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_grow() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_shrink() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Set the non-finite bf16 elements of four words to zero; true if there were any.
+__device__ __forceinline__ bool clear_nonfinite(uint4* w) {
+  uint32_t* x = reinterpret_cast<uint32_t*>(w);
+  uint32_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad |= ((x[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+  if (!bad) return false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = ((x[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+    if (b & 0x8000u) x[i] &= 0xFFFF0000u;
+    if (b & 0x80000000u) x[i] &= 0x0000FFFFu;
+  }
+  return true;
+}
+
+// Add the non-finite V elements that a row sees in the tiles that were
+// cleared to columns [c0, c0 + 32) of its sums.
+__device__ __noinline__ void add_nonfinite(const PagedArgs& a, const Item& it,
+                                           const uint32_t (*bits)[4], int nmasked, int vis,
+                                           unsigned long long anc, int c0, float* f) {
+  const __nv_bfloat16* pool = static_cast<const __nv_bfloat16*>(a.v_pool);
+  const __nv_bfloat16* dv = static_cast<const __nv_bfloat16*>(a.draft_v);
+  for (int e = 0; e < nmasked; ++e) {
+    const bool drafts = it.draft && e == 0;
+    const int base = (it.k0 + it.nk - 1 - e) * kKeys;
+    for (int k = 0; k < kKeys; ++k) {
+      if (!(bits[e][k >> 5] >> (k & 31) & 1u)) continue;
+      const __nv_bfloat16* row;
+      if (drafts) {
+        if (k >= a.T || !(anc >> k & 1ull)) continue;
+        row = dv + (((size_t)it.seq * a.T + k) * a.Hkv + it.kvh) * a.d;
+      } else {
+        const int key = base + k;
+        if (key >= vis) continue;
+        const int page = a.block_table[it.tab + key / a.blk];
+        if (page < 0 || page >= a.num_pages) continue;
+        row = pool + (((size_t)page * a.Hkv + it.kvh) * a.blk + key % a.blk) * a.d;
+      }
+      for (int c = 0; c < 32 && c0 + c < a.d; ++c) {
+        const float x = __bfloat162float(row[c0 + c]);
+        if (!(fabsf(x) < INFINITY)) f[c] += x;
+      }
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_dk,
+                    const __grid_constant__ CUtensorMap tm_dv, const __grid_constant__ PagedArgs a) {
+  using C = Cfg<D>;
+  constexpr int NS = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Control sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t q_base = smem_u32(smem), ring = q_base + 2 * C::kTile;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tt = kRows / a.gs, tile = 2 * tt;
+  volatile int* abort = &sh.abort;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), 1);
+      mbar_init(smem_u32(&sh.vclean[i]), 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.q_full[i]), 1);
+      mbar_init(smem_u32(&sh.q_empty[i]), 1);
+      mbar_init(smem_u32(&sh.s_full[i]), 1);
+      mbar_init(smem_u32(&sh.p_ready[i]), 4);
+      mbar_init(smem_u32(&sh.o_done[i]), 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(smem_u32(&sh.item_full[i]), 1);
+      mbar_init(smem_u32(&sh.item_empty[i]), kItemReaders);
+    }
+    mbar_init(smem_u32(&sh.meet), 8);
+    mbar_init(smem_u32(&sh.drained), 1);
+    sh.abort = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+    prefetch_tensormap(&tm_q);
+  }
+  if (warp == kMmaWarp) {
+    tc::alloc(smem_u32(&sh.tmem), kTmemCols);
+    tc::relinquish();
+  }
+  if (a.prefix)
+    for (int t = threadIdx.x; t < a.T; t += kThreads) sh.anc[t] = a.anc[t];
+  pdl_wait();
+  pdl_trigger();
+  tc::fence_before();
+  make_plan(a, &sh.plan, tile, kKeys, 2);
+  tc::fence_after();
+  const uint32_t tmem = sh.tmem;
+  auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) {
+    return mbar_wait_abortable(smem_u32(bar), parity, abort, a.status, site);
+  };
+  // the seq-th item of this CTA, copied out of the item ring
+  auto take_item = [&](uint32_t seq, Item* it) {
+    const int s = seq % kItems;
+    if (!__all_sync(0xffffffffu, wait(&sh.item_full[s], (seq / kItems) & 1, 20u))) return false;
+    *it = sh.items[s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.item_empty[s]));
+    return it->valid != 0;
+  };
+
+  if (warp >= kMmaWarp) regs_shrink<kRegsOther>();
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ items, copies
+    const int box_rows = min(a.blk, kKeys), ppt = kKeys / box_rows;
+    const int oob = a.num_pages * a.Hkv * a.blk;  // past the pool: TMA fills zeros
+    // lane -> (page of the tile, column half) of one box
+    const int pg = lane / C::kHalves, half = lane % C::kHalves;
+    const bool mine = lane < ppt * C::kHalves;
+    uint32_t at = 0, q_uses[2] = {0, 0}, alt = 0;
+    int idx = blockIdx.x;
+    bool ok = true;
+    for (uint32_t seq = 0; ok; ++seq) {
+      const int slot = seq % kItems;
+      if (seq >= kItems &&
+          !__all_sync(0xffffffffu, wait(&sh.item_empty[slot], ((seq / kItems) & 1) ^ 1, 1u)))
+        break;
+      if (lane == 0) sh.items[slot] = decode_item(a, &sh.plan, idx, tile, kKeys);
+      __syncwarp();
+      const Item it = sh.items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.item_full[slot]));
+      if (!it.valid) break;
+      int next = 0;
+      if (lane == 0) next = next_item(a);  // arrives while this item's copies go out
+      const Run r = run_of(it, tt);
+      // the pool row of this lane's box of key tile j
+      auto lookup = [&](int j) {
+        int row = oob;
+        if (mine && j < it.nk && !(it.draft && j == it.nk - 1)) {
+          const int key = (it.k0 + j) * kKeys + pg * box_rows;
+          if (key < it.ctx) {
+            const int page = __ldg(a.block_table + it.tab + key / a.blk);
+            if (page >= 0 && page < a.num_pages)
+              row = (page * a.Hkv + it.kvh) * a.blk + key % a.blk;
+            else if (half == 0)
+              atomicOr(a.status, SV_FLAG_BAD_PAGE);
+          }
+        }
+        return row;
+      };
+      auto load = [&](bool v, int j, int row) {
+        const uint32_t x = at + (v ? pos_v(r, j, it.nk) : pos_k(r, j));
+        const int s = x % NS;
+        if (x >= NS && !__all_sync(0xffffffffu, wait(&sh.empty[s], ((x / NS) & 1) ^ 1, 2u))) return false;
+        const uint32_t bar = smem_u32(&sh.full[s]), dst = ring + s * C::kTile;
+        const bool drafts = it.draft && j == it.nk - 1;
+        if (lane == 0) mbar_arrive_expect_tx(bar, drafts ? C::kTile / 2 : C::kTile);
+        __syncwarp();
+        if (drafts) {
+          if (lane < C::kHalves)
+            tma_load_4d(dst + lane * kBox, v ? &tm_dv : &tm_dk, 64 * lane, it.kvh, 0, it.seq, bar);
+        } else if (mine) {
+          tma_load_2d(dst + half * kBox + pg * box_rows * 128, v ? &tm_v : &tm_k, 64 * half, row, bar);
+        }
+        return true;
+      };
+      int row0 = lookup(0), row1 = lookup(1);
+      if (it.nk > 0) {
+        // Q: both slots (pair), or the slots in turn
+        for (int s = 0; s < 2 && ok; ++s) {
+          if (!r.pair && s != (int)(alt & 1)) continue;
+          if (q_uses[s] && !__all_sync(0xffffffffu, wait(&sh.q_empty[s], (q_uses[s] - 1) & 1, 3u))) {
+            ok = false;
+            break;
+          }
+          ++q_uses[s];
+          const uint32_t bar = smem_u32(&sh.q_full[s]);
+          if (lane == 0) mbar_arrive_expect_tx(bar, C::kHalves * tt * a.gs * 128);
+          __syncwarp();
+          if (lane < C::kHalves)
+            tma_load_3d(q_base + s * C::kTile + lane * kBox, &tm_q, 64 * lane, it.head0,
+                        it.tok0 + (r.pair ? s * tt : 0), bar);
+        }
+        if (!r.pair) ++alt;
+        if (ok && !r.pair) ok = load(false, 0, row0);
+        for (int j = 0; j < it.nk && ok; ++j) {
+          const int row2 = lookup(j + 2);
+          ok = r.pair ? load(false, j, row0) : j + 1 >= it.nk || load(false, j + 1, row1);
+          ok = ok && load(true, j, row0);
+          row0 = row1;
+          row1 = row2;
+        }
+        at += 2 * it.nk;
+      }
+      idx = __shfl_sync(0xffffffffu, next, 0);
+    }
+    // never leave with a copy still in flight
+    __syncwarp();
+    if (*abort) {
+      for (uint32_t s = 0; s < NS; ++s)
+        for (int ph = 0; ph < 2; ++ph) mbar_wait_drain(smem_u32(&sh.full[s]), ph);
+      for (int s = 0; s < 2; ++s)
+        for (int ph = 0; ph < 2; ++ph) mbar_wait_drain(smem_u32(&sh.q_full[s]), ph);
+    }
+    if (lane == 0) leave(a);
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue
+    constexpr uint32_t id_s = tc::idesc_bf16(128, kKeys, false, false);
+    constexpr uint32_t id_o = tc::idesc_bf16(128, D, false, true);
+    const uint64_t dq0 = tc::smem_desc(q_base, 16, 1024);
+    const uint64_t dk0 = tc::smem_desc(ring, 16, 1024);
+    const uint64_t dv0 = tc::smem_desc(ring, kBox, 1024);
+    uint32_t at = 0, q_uses[2] = {0, 0}, alt = 0, p_uses[2] = {0, 0};
+    bool ok = true;
+    Item it;
+    for (uint32_t seq = 0; ok && take_item(seq, &it); ++seq) {
+      const Run r = run_of(it, tt);
+      if (it.nk == 0) continue;
+      if (lane == 0) {
+        auto stage = [&](uint32_t pos) { return (at + pos) % NS; };
+        auto phase = [&](uint32_t pos) { return ((at + pos) / NS) & 1; };
+        auto k_wait = [&](int j) { return wait(&sh.full[stage(pos_k(r, j))], phase(pos_k(r, j)), 4u); };
+        auto v_wait = [&](int j) {
+          const uint32_t p = pos_v(r, j, it.nk);
+          return wait(&sh.vclean[stage(p)], phase(p), 5u);
+        };
+        auto p_wait = [&](int s) { return wait(&sh.p_ready[s], p_uses[s]++ & 1, 6u); };
+        auto issue_s = [&](int s, int qs, int j) {
+          tc::fence_after();
+          const uint64_t dq = dq0 + (uint64_t)(qs * (C::kTile >> 4));
+          const uint64_t dk = dk0 + (uint64_t)(stage(pos_k(r, j)) * (C::kTile >> 4));
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+            tc::mma_ss(tmem + col_s(s), dq + off, dk + off, id_s, kk > 0 ? 1u : 0u);
+          }
+          tc::commit(smem_u32(&sh.s_full[s]));
+        };
+        auto issue_o = [&](int s, int j, bool first) {
+          tc::fence_after();
+          const uint64_t dv = dv0 + (uint64_t)(stage(pos_v(r, j, it.nk)) * (C::kTile >> 4));
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            tc::mma_ts(tmem + col_o(s), tmem + col_s(s) + kk * 8, dv + (uint64_t)((kk * 2048) >> 4),
+                       id_o, !first || kk > 0 ? 1u : 0u);
+        };
+        auto free_k = [&](int j) { tc::commit(smem_u32(&sh.empty[stage(pos_k(r, j))])); };
+        auto free_v = [&](int j) { tc::commit(smem_u32(&sh.empty[stage(pos_v(r, j, it.nk))])); };
+        if (r.pair) {
+          ok = wait(&sh.q_full[0], q_uses[0]++ & 1, 7u) && wait(&sh.q_full[1], q_uses[1]++ & 1, 7u) &&
+               k_wait(0);
+          if (ok) {
+            if (r.n[0] > 0) issue_s(0, 0, 0);
+            issue_s(1, 1, 0);
+            free_k(0);
+          }
+          for (int j = 0; ok && j < it.nk; ++j) {
+            const bool more = j + 1 < it.nk;
+            if (j < r.n[0]) {
+              if (!(ok = p_wait(0) && v_wait(j))) break;
+              issue_o(0, j, j == 0);
+              if (j + 1 < r.n[0]) {
+                if (!(ok = k_wait(j + 1))) break;
+                issue_s(0, 0, j + 1);
+              } else {
+                tc::commit(smem_u32(&sh.o_done[0]));
+              }
+            }
+            if (!(ok = p_wait(1) && v_wait(j))) break;
+            issue_o(1, j, j == 0);
+            free_v(j);
+            if (more) {
+              if (!(ok = k_wait(j + 1))) break;
+              issue_s(1, 1, j + 1);
+              free_k(j + 1);
+            } else {
+              tc::commit(smem_u32(&sh.o_done[1]));
+            }
+            if (j + 2 == it.nk || it.nk == 1) {  // the item's last S is out
+              tc::commit(smem_u32(&sh.q_empty[0]));
+              tc::commit(smem_u32(&sh.q_empty[1]));
+            }
+          }
+        } else {
+          const int qs = alt++ & 1;
+          ok = wait(&sh.q_full[qs], q_uses[qs]++ & 1, 7u) && k_wait(0);
+          if (ok) {
+            issue_s(0, qs, 0);
+            free_k(0);
+            if (it.nk > 1 && (ok = k_wait(1))) {
+              issue_s(1, qs, 1);
+              free_k(1);
+            }
+            if (it.nk <= 2) tc::commit(smem_u32(&sh.q_empty[qs]));
+          }
+          for (int j = 0; ok && j < it.nk; ++j) {
+            const int s = j & 1;
+            if (!(ok = p_wait(s) && v_wait(j))) break;
+            issue_o(s, j, j < 2);
+            free_v(j);
+            if (j + 2 < it.nk) {
+              if (!(ok = k_wait(j + 2))) break;
+              issue_s(s, qs, j + 2);
+              free_k(j + 2);
+              if (j + 3 == it.nk) tc::commit(smem_u32(&sh.q_empty[qs]));
+            } else {
+              tc::commit(smem_u32(&sh.o_done[s]));
+            }
+          }
+        }
+      }
+      at += 2 * it.nk;
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    }
+    if (lane == 0) {
+      tc::commit(smem_u32(&sh.drained));  // TMEM is given back after every MMA
+      mbar_wait_drain(smem_u32(&sh.drained), 0);
+    }
+    __syncwarp();
+  } else if (warp >= kCleanWarp) {
+    // ------------------------------------------------------------ V tiles
+    const int w = warp - kCleanWarp;  // keys [64 w, 64 w + 64)
+    uint32_t at = 0;
+    bool ok = true;
+    Item it;
+    for (uint32_t seq = 0; ok && take_item(seq, &it); ++seq) {
+      const Run r = run_of(it, tt);
+      // every ring position in order: a V tile that needs it is cleared, and the
+      // stage's barrier advances once per use whatever the stage holds
+      for (int pos = 0; pos < 2 * it.nk; ++pos) {
+        const uint32_t x = at + pos;
+        const int s = x % NS;
+        if (!(ok = __all_sync(0xffffffffu, wait(&sh.full[s], (x / NS) & 1, 8u)))) break;
+        const int j = v_at(r, pos, it.nk);
+        if (j >= r.masked) {
+          uint8_t* v = smem + 2 * C::kTile + s * C::kTile;
+          uint32_t bits[2] = {0, 0};
+#pragma unroll 4
+          for (int i = 0; i < 16 * C::kHalves; ++i) {
+            // 16-byte chunks of a 128-byte row of 64 columns; the swizzle
+            // moves chunks within their row only
+            const int row = 64 * w + (i & 15) * 4 + (lane >> 3);
+            uint4* p = reinterpret_cast<uint4*>(v + (i >> 4) * kBox + row * 128 + (lane & 7) * 16);
+            uint4 x4 = *p;
+            if (clear_nonfinite(&x4)) {
+              *p = x4;
+              bits[(row >> 5) & 1] |= 1u << (row & 31);
+            }
+          }
+          bits[0] = __reduce_or_sync(0xffffffffu, bits[0]);
+          bits[1] = __reduce_or_sync(0xffffffffu, bits[1]);
+          if (bits[0] | bits[1]) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (lane < 2)
+            sh.nonfinite[seq % kItems][min(kMaxMasked - 1, it.nk - 1 - j)][2 * w + lane] = bits[lane];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.vclean[s]));
+      }
+      at += 2 * it.nk;
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    regs_grow<kRegsSoftmax>();
+    const int X = warp >> 2, q4 = warp & 3, r = 32 * q4 + lane;
+    const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
+    const uint32_t tS = tmem + lane_base + col_s(X), tO = tmem + lane_base + col_o(X);
+    const int rt = r / a.gs, rg = r % a.gs;  // token of the set and head of the group
+    uint32_t s_uses = 0, o_uses = 0, meets = 0, parts = 0;
+    bool ok = true;
+    // all eight softmax warps meet
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.meet));
+      return __all_sync(0xffffffffu, wait(&sh.meet, meets++ & 1, 9u)) != 0;
+    };
+    Item it;
+    for (uint32_t seq = 0; ok && take_item(seq, &it); ++seq) {
+      const Run run = run_of(it, tt);
+      const int off = run.pair && X ? tt : 0;  // the set's first token
+      const int tok = off + rt;
+      const bool valid = rt < tt && tok < it.ntok && rg < it.heads;
+      const bool live = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps step
+      const int vis = max(0, it.causal ? it.vis0 + tok : it.ctx);
+      const int vis_set = it.causal ? it.vis0 + off : it.ctx;  // the set's first row sees the fewest
+      const unsigned long long anc = it.draft && valid ? sh.anc[it.draft0 + tok] : 0ull;
+      float m_run = -INFINITY, l_run = 0.f;
+      const int n = X ? run.n[1] : run.n[0];
+      for (int j = 0; j < n; ++j) {
+        const int kt = run.pair ? j : 2 * j + X;
+        if (!(ok = __all_sync(0xffffffffu, wait(&sh.s_full[X], s_uses++ & 1, 10u)))) break;
+        if (live) {
+          tc::fence_after();
+          uint32_t v[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tc::ld32(tS + 32 * c, v[c]);
+          tc::wait_ld();
+          const int base = (it.k0 + kt) * kKeys;
+          const bool drafts = it.draft && kt == it.nk - 1;
+          if (drafts || base + kKeys > vis_set) {
+            const int lim = vis - base;  // keys of this tile that the row sees
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t keep;
+              if (drafts)
+                keep = c < 2 ? (uint32_t)(anc >> (32 * c)) : 0u;
+              else
+                keep = lim >= 32 * c + 32 ? 0xffffffffu : lim <= 32 * c ? 0u : (1u << (lim - 32 * c)) - 1u;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(keep >> i & 1u)) v[c][i] = 0xff800000u;  // -inf
+            }
+          }
+          float mx[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            mx[c] = __uint_as_float(v[c][0]);
+#pragma unroll
+            for (int i = 1; i < 32; ++i) mx[c] = fmaxf(mx[c], __uint_as_float(v[c][i]));
+          }
+          const float mrow = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+          // S of this tile was issued behind the set's previous P V, so that
+          // product is complete and O may be rescaled
+          if (__any_sync(0xffffffffu, mrow > m_run + kRescaleLog2)) {
+            const float m_new = fmaxf(m_run, mrow);
+            const float alpha = m_new == -INFINITY ? 1.f : exp2f(m_run - m_new);
+            if (j > 0) {
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tc::ld32(tO + 32 * c, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tc::st32(tO + 32 * c, o);
+              }
+            }
+            l_run *= alpha;
+            m_run = m_new;
+          }
+          const float nb = m_run == -INFINITY ? 0.f : -m_run;
+          const uint64_t nb2 = pack2(nb, nb), sc2 = pack2(a.scale_log2, a.scale_log2);
+          uint64_t sum = 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 e = unpack2(fma2(pack2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])),
+                                            sc2, nb2));
+              const float x = exp2f(e.x), y = exp2f(e.y);
+              sum = add2(sum, pack2(x, y));
+              p[i] = pack_bf16(x, y);
+            }
+            tc::st16(tS + 16 * c, p);
+          }
+          const float2 s2 = unpack2(sum);
+          l_run += s2.x + s2.y;
+          tc::wait_st();
+          tc::fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[X]));
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- results
+      if (n > 0) {
+        if (!(ok = __all_sync(0xffffffffu, wait(&sh.o_done[X], o_uses++ & 1, 11u)))) break;
+        tc::fence_after();
+      }
+      const int pp = parts & 1;  // unit list of this item
+      if (it.part >= 0 && threadIdx.x == 0) sh.nunits[pp] = 0;
+      // non-finite V in a cleared tile
+      const int nmasked = min(kMaxMasked, max(0, it.nk - run.masked));
+      const uint32_t(*nf)[4] = sh.nonfinite[seq % kItems];
+      uint32_t any_nf = 0;
+      for (int e = 0; e < nmasked; ++e) any_nf |= nf[e][0] | nf[e][1] | nf[e][2] | nf[e][3];
+      // columns [c0, c1) of the row are this thread's: all (pair), or half of
+      // both sets' sums (alternating)
+      float w[2] = {X ? 0.f : 1.f, X ? 1.f : 0.f}, m_out = m_run, l_out = l_run;
+      int c0 = 0, c1 = D;
+      if (!run.pair) {
+        sh.ml[X][r] = make_float2(m_run, l_run);
+        if (!(ok = meet())) break;
+        tc::fence_after();
+        const float2 ma = sh.ml[0][r], mb = sh.ml[1][r];
+        m_out = fmaxf(ma.x, mb.x);
+        w[0] = ma.x == -INFINITY ? 0.f : exp2f(ma.x - m_out);
+        w[1] = mb.x == -INFINITY ? 0.f : exp2f(mb.x - m_out);
+        l_out = w[0] * ma.y + w[1] * mb.y;
+        c0 = X * (D / 2);
+        c1 = c0 + D / 2;
+      }
+      if (live) {
+        const float inv = l_out == 0.f ? 0.f : 1.0f / l_out;
+        const bool use0 = (run.pair ? X == 0 : true) && run.n[0] > 0;
+        const bool use1 = (run.pair ? X == 1 : true) && run.n[1] > 0;
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 32) {
+          __syncwarp();
+          float f[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) f[e] = 0.f;
+          uint32_t o[32];
+          if (use0) {
+            tc::ld32(tmem + lane_base + col_o(0) + c, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = w[0] != 0.f ? w[0] * __uint_as_float(o[e]) : 0.f;
+          }
+          if (use1) {
+            tc::ld32(tmem + lane_base + col_o(1) + c, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] += w[1] != 0.f ? w[1] * __uint_as_float(o[e]) : 0.f;
+          }
+          if (!valid) continue;
+          if (any_nf) add_nonfinite(a, it, nf, nmasked, vis, anc, c, f);
+          if (it.part < 0) {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
+                                 ((size_t)(it.tok0 + tok) * a.Hq + it.head0 + rg) * a.d + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              if (c + e < a.d)
+                *reinterpret_cast<uint4*>(dst + e) =
+                    make_uint4(pack_bf16(f[e] * inv, f[e + 1] * inv), pack_bf16(f[e + 2] * inv, f[e + 3] * inv),
+                               pack_bf16(f[e + 4] * inv, f[e + 5] * inv), pack_bf16(f[e + 6] * inv, f[e + 7] * inv));
+          } else {
+            float* dst = a.part_o + ((size_t)it.part + tok * a.gs + rg) * a.d + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              if (c + e < a.d)
+                *reinterpret_cast<float4*>(dst + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+          }
+        }
+        if (valid && it.part >= 0 && (run.pair || X == 0))
+          a.part_ml[(size_t)it.part + tok * a.gs + rg] = make_float2(m_out, l_out);
+      }
+      tc::fence_before();  // O is read: the next item's products may overwrite it
+      if (it.part >= 0) {
+        __threadfence();
+        if (!(ok = meet())) break;
+        arrive_item(a, &sh.plan, it, tile, threadIdx.x, 256, sh.units[pp], &sh.nunits[pp]);
+        if (!(ok = meet())) break;
+        const int nu = sh.nunits[pp];
+        if (nu > 0) __threadfence();
+        for (int u = 0; u < nu; ++u)
+          merge_unit<__nv_bfloat16>(a, &sh.plan, it, sh.units[pp][u], tile, warp, 8);
+        ++parts;
+      } else if (!run.pair) {
+        if (!(ok = meet())) break;
+      }
+    }
+  }
+
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after();
+    tc::dealloc(tmem, kTmemCols);
+  }
+}
+
+bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+  const auto enc = get_encode();
+  if (!enc) return false;
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box,
+             step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_cfg(const PagedArgs& a, const CUtensorMap* m, cudaStream_t st) {
+  const int dev = current_device();
+  static std::atomic<int> ready[kMaxDevices];
+  if (!ready[dev].load()) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        paged_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    ready[dev].store(1);
+  }
+  return launch_pdl(paged_tc_kernel<D>, dim3(std::min(sm_count(), kMaxTcCtas)), dim3(kThreads),
+                    Cfg<D>::kSmem, st, m[0], m[1], m[2], m[3], m[4], a);
+}
+
+}  // namespace
+
+bool paged_tc_applies(const PagedArgs& a, int dtype) {
+  // a key tile is whole pages, or part of one; boxes of 8 rows or more keep
+  // the swizzle's pattern
+  return dtype == SV_BF16 && a.d <= 128 && a.blk >= 8 &&
+         (a.blk % kKeys == 0 || kKeys % a.blk == 0);
+}
+
+cudaError_t launch_paged_tc(PagedArgs a, cudaStream_t st) {
+  paged_heads(&a, kRows);
+  CUtensorMap m[5];
+  const cuuint64_t d = a.d, hd = (cuuint64_t)a.Hkv * a.d;
+  {
+    const cuuint64_t dims[2] = {d, (cuuint64_t)a.num_pages * a.Hkv * a.blk}, strides[1] = {d * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)std::min(a.blk, kKeys)};
+    if (!encode(&m[0], a.k_pool, 2, dims, strides, box) || !encode(&m[1], a.v_pool, 2, dims, strides, box))
+      return cudaErrorInvalidValue;
+  }
+  {
+    const cuuint64_t dims[3] = {d, (cuuint64_t)a.Hq, (cuuint64_t)a.n_rows};
+    const cuuint64_t strides[2] = {d * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.gs, (cuuint32_t)(kRows / a.gs)};
+    if (!encode(&m[2], a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  m[3] = m[4] = m[2];
+  if (a.prefix) {
+    const cuuint64_t dims[4] = {d, (cuuint64_t)a.Hkv, (cuuint64_t)a.T, (cuuint64_t)a.B};
+    const cuuint64_t strides[3] = {d * 2, hd * 2, hd * 2 * a.T};
+    const cuuint32_t box[4] = {64, 1, 64, 1};
+    if (!encode(&m[3], a.draft_k, 4, dims, strides, box) || !encode(&m[4], a.draft_v, 4, dims, strides, box))
+      return cudaErrorInvalidValue;
+  }
+  return a.d <= 64 ? launch_cfg<64>(a, m, st) : launch_cfg<128>(a, m, st);
+}
+
+}  // namespace sva
