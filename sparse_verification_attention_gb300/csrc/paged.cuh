@@ -6,9 +6,9 @@
 // is one row tile of one head group over a run of key tiles. Lengths may live
 // in device memory only, so every CTA derives the same plan from them: a
 // segment whose row tiles see more than C key tiles is cut into s =
-// ceil(kt / C) runs, with C such that the grid gets about two items per CTA.
-// That bounds the partial rows by a number the host knows: the items of cut
-// segments are at most twice sum(tiles * kt) / C <= 4 * CTAs.
+// ceil(kt / C) runs, with C such that the grid gets about kItemsPerCta items per
+// CTA. That bounds the partial rows by a number the host knows: the items of
+// cut segments are at most twice sum(tiles * kt) / C <= 2 * kItemsPerCta * CTAs.
 #pragma once
 
 #include "paged.h"
@@ -52,49 +52,76 @@ __device__ __forceinline__ Seg seg_of(const PagedArgs& a, int i) {
 
 __device__ __forceinline__ int n_segs(const PagedArgs& a) { return a.prefix ? a.B + 1 : a.B; }
 
-// The plan in shared memory.
+// The plan in shared memory: segments in the order in which their items are
+// handed out.
 struct Plan {
   int items[kMaxSegs + 1];  // first item of every segment; [nseg] = all items
   int rows[kMaxSegs];       // first partial row of every segment
   int split[kMaxSegs];      // runs of key tiles (>= 1)
+  int order[kMaxSegs];      // the segment
 };
+constexpr int kPlanScratch = 2 * (kMaxSegs + 3);  // ints that make_plan needs besides
+
+constexpr long long kL2Keys = 32ll << 20;  // a quarter of L2
 
 __device__ __forceinline__ int ceil_div(int x, int y) { return (x + y - 1) / y; }
 
-// Fill `p` (all threads of the CTA call it; a barrier follows inside). tile:
-// tokens per row tile, keys: tokens per key tile, min_run: the fewest key
-// tiles that a run is worth.
-__device__ inline void make_plan(const PagedArgs& a, Plan* p, int tile, int keys, int min_run) {
-  const int nseg = n_segs(a), lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < nseg; i += blockDim.x) {
+// Fill `p` (all threads of the CTA call it; barriers inside). scratch:
+// kPlanScratch ints of shared memory on a 16-byte boundary.
+//
+// Prompt segments go out in descending order of key tiles, so that what starts
+// last is short (a dynamic schedule is as good as its last items are small).
+// The prefix form keeps its order: the shared segment comes first.
+__device__ inline void make_plan(const PagedArgs& a, Plan* p, int* scratch) {
+  const int nseg = n_segs(a), lane = threadIdx.x & 31, padded = (nseg + 3) & ~3;
+  int* kts = scratch;                    // key tiles of segment i
+  int* ns = scratch + ((kMaxSegs + 3) & ~3);  // rows of segment i
+  for (int i = threadIdx.x; i < padded; i += blockDim.x) {
+    kts[i] = -1;
+    if (i >= nseg) continue;
     const Seg s = seg_of(a, i);
     if (s.bad && blockIdx.x == 0) atomicOr(a.status, SV_FLAG_BAD_LENGTH);
-    p->rows[i] = s.n;
-    p->split[i] = s.n ? ceil_div(s.ctx, keys) + s.draft : 0;  // key tiles
+    ns[i] = s.n;
+    kts[i] = s.n ? ceil_div(s.ctx, a.keys) + s.draft : 0;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < nseg; i += blockDim.x) {
+    int rank = i;
+    if (!a.prefix && nseg > 1) {
+      const int kt = kts[i];
+      rank = 0;
+      for (int j = 0; j < padded; j += 4) {
+        const int4 k = *reinterpret_cast<const int4*>(kts + j);
+        rank += (k.x > kt || (k.x == kt && j < i)) + (k.y > kt || (k.y == kt && j + 1 < i)) +
+                (k.z > kt || (k.z == kt && j + 2 < i)) + (k.w > kt || (k.w == kt && j + 3 < i));
+      }
+    }
+    p->order[rank] = i;
   }
   __syncthreads();
   if (threadIdx.x < 32) {
     const int per = ceil_div(nseg, 32), b0 = min(nseg, lane * per), b1 = min(nseg, b0 + per);
     unsigned long long units = 0;
     for (int i = b0; i < b1; ++i)
-      units += (unsigned long long)ceil_div(p->rows[i], tile) * a.hv * p->split[i];
+      units += (unsigned long long)ceil_div(ns[i], a.tile) * a.hv * kts[i];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) units += __shfl_xor_sync(0xffffffffu, units, off);
-    const unsigned long long ctas = min((int)gridDim.x, kMaxPlanCtas);
-    const unsigned long long want = (units + 2 * ctas - 1) / (2 * ctas);
-    const int run = (int)min(max(want, (unsigned long long)min_run), 1ull << 30);
+    const unsigned long long parts = (unsigned long long)a.per_cta * a.ctas;
+    const unsigned long long want = (units + parts - 1) / parts;
+    const int run = (int)min(max(want, (unsigned long long)a.min_run), 1ull << 30);
     // items and partial rows of every segment, scanned
     int items = 0, rows = 0;
     for (int i = b0; i < b1; ++i) {
-      const int kt = p->split[i], n = p->rows[i];
+      const int kt = kts[p->order[i]], n = ns[p->order[i]];
       int s = kt > run ? ceil_div(kt, run) : 1;
       if (s > 1) s = ceil_div(kt, ceil_div(kt, s));  // no empty run
-      const int it = ceil_div(n, tile) * a.hv * s;
+      const int it = ceil_div(n, a.tile) * a.hv * s;
+      const int r = s > 1 || a.prefix ? it * min(a.tile, n) * a.gs : 0;
       p->split[i] = s;
-      items += it;
-      rows += s > 1 || a.prefix ? it * min(tile, n) * a.gs : 0;
-      p->rows[i] = s > 1 || a.prefix ? it * min(tile, n) * a.gs : 0;
       p->items[i] = it;
+      p->rows[i] = r;
+      items += it;
+      rows += r;
     }
     int ix = items, rx = rows;
 #pragma unroll
@@ -132,12 +159,13 @@ struct Item {
   int seq;            // sequence (drafts)
   int tab;            // first block-table entry of the segment's keys
   int part;           // first partial row, -1: the run is the whole row (written to out)
-  // the unit that the item's partial rows belong to (prompt form): first
-  // partial row of its first run, runs, rows between runs
+  // the partial rows of all runs of this row tile and head group: the first
+  // one, the number of runs, rows between runs
   int unit, runs, run_rows;
 };
 
-__device__ inline Item decode_item(const PagedArgs& a, const Plan* p, int idx, int tile, int keys) {
+__device__ inline Item decode_item(const PagedArgs& a, const Plan* p, int idx) {
+  const int tile = a.tile, keys = a.keys;
   Item it;
   const int nseg = n_segs(a);
   it.valid = idx < p->items[nseg];
@@ -148,12 +176,18 @@ __device__ inline Item decode_item(const PagedArgs& a, const Plan* p, int idx, i
     if (p->items[m] <= idx) lo = m;
     else hi = m;
   }
-  const Seg s = seg_of(a, lo);
-  const int runs = p->split[lo], tiles = ceil_div(s.n, tile), local = idx - p->items[lo];
-  // neighbours in the list share a head's run of keys (they meet in L2), the
-  // rows that see most first
-  const int t = tiles - 1 - local % tiles, rest = local / tiles;
-  const int run = rest % runs, hv = rest / runs;
+  const int id = p->order[lo];
+  const Seg s = seg_of(a, id);
+  const int runs = p->split[lo], tiles = ceil_div(s.n, tile);
+  // Neighbours in the list share keys (they meet in L2): groups of heads whose
+  // keys and values fit kL2Keys, in a group run by run, in a run the rows
+  // that see most first.
+  const long long kv = (long long)s.ctx * a.d * 2 * a.elt + 1;
+  const int fit = (int)min(max(kL2Keys / kv, 1ll), (long long)a.hv);
+  const int gh = ceil_div(a.hv, ceil_div(a.hv, fit)), per = gh * tiles * runs;
+  const int local = idx - p->items[lo], h0 = local / per * gh, in = local % per;
+  const int gw = min(gh, a.hv - h0), hv = h0 + in % gw;
+  const int t = tiles - 1 - in / gw % tiles, run = in / gw / tiles;
   it.tok0 = s.tok0 + t * tile;
   it.ntok = min(tile, s.n - t * tile);
   it.kvh = hv / a.hs;
@@ -169,7 +203,7 @@ __device__ inline Item decode_item(const PagedArgs& a, const Plan* p, int idx, i
   it.nk = max(0, min(kt, it.k0 + len) - it.k0);
   it.draft = s.draft && it.nk > 0 && it.k0 + it.nk == kt;
   it.draft0 = t * tile;
-  it.seq = a.prefix ? lo - 1 : lo;
+  it.seq = a.prefix ? id - 1 : id;
   it.tab = s.tab;
   it.runs = runs;
   it.run_rows = min(tile, s.n) * a.gs;
@@ -225,7 +259,7 @@ __device__ inline void merge_row(const PagedArgs& a, const Group (&g)[2], T* dst
       // a run without a visible key has weight 0 (a NaN maximum stays one)
     }
     const int nj = min(32, total - j0);
-#pragma unroll 4
+#pragma unroll 8
     for (int j = 0; j < nj; ++j) {
       const float wj = __shfl_sync(0xffffffffu, w, j);
       L += __shfl_sync(0xffffffffu, wl, j);
@@ -251,62 +285,25 @@ __device__ inline void merge_row(const PagedArgs& a, const Group (&g)[2], T* dst
   }
 }
 
-// What a finished item leaves to merge: in the prompt form its own unit, in
-// the prefix form the drafts of (sequence, head group) pairs. `units` (shared
-// memory) receives the units that this arrival completed. Called by `nthr`
-// threads (tid in [0, nthr)) after every partial row of the item is written
-// and ordered before (barrier and device-scope fence); the caller
-// synchronises before reading the list. *n must be 0 on entry.
-__device__ inline void arrive_item(const PagedArgs& a, const Plan* p, const Item& it, int tile,
-                                   int tid, int nthr, int* units, int* n) {
-  const int hv = it.kvh * a.hs + (it.head0 - it.kvh * a.G) / a.gs;
-  if (!a.prefix) {
-    if (tid == 0) {
-      const unsigned old = arrive_acq_rel(a.unit_ctr + it.unit);
-      if (old + 1 == (unsigned)it.runs) units[(*n)++] = 0;
-      else if (old >= (unsigned)it.runs) atomicOr(a.status, SV_FLAG_STALE_WORKSPACE);
-    }
-    return;
-  }
-  const int b0 = it.tok0 / a.T, b1 = (it.tok0 + it.ntok - 1) / a.T;
-  for (int b = b0 + tid; b <= b1; b += nthr) {
-    // arrivals that complete the pair: the runs of every shared row tile its
-    // drafts lie in, and its own
-    int need = ceil_div(a.T, tile) * p->split[b + 1];
-    if (a.n_shared) need += ((b * a.T + a.T - 1) / tile - b * a.T / tile + 1) * p->split[0];
-    const unsigned old = arrive_acq_rel(a.unit_ctr + b * a.hv + hv);
-    if (old + 1 == (unsigned)need) units[atomicAdd(n, 1)] = b;
-    else if (old >= (unsigned)need) atomicOr(a.status, SV_FLAG_STALE_WORKSPACE);
-  }
+// A prompt item's partial rows are written and ordered (barrier and
+// device-scope fence): true when they were the last of their unit, which the
+// caller then merges. One thread calls it.
+__device__ __forceinline__ bool arrive_unit(const PagedArgs& a, const Item& it) {
+  const unsigned old = arrive_acq_rel(a.unit_ctr + it.unit);
+  if (old >= (unsigned)it.runs) atomicOr(a.status, SV_FLAG_STALE_WORKSPACE);
+  return old + 1 == (unsigned)it.runs;
 }
 
-// Merge one completed unit (see arrive_item) with `nwarp` warps and return
-// its count to zero.
+// Merge a prompt item's unit with `nwarp` warps and return its count to zero.
 template <typename T>
-__device__ inline void merge_unit(const PagedArgs& a, const Plan* p, const Item& it, int unit,
-                                  int tile, int warp, int nwarp) {
+__device__ inline void merge_unit(const PagedArgs& a, const Item& it, int warp, int nwarp) {
   T* out = static_cast<T*>(a.out);
-  if (!a.prefix) {
-    for (int r = warp; r < it.ntok * it.heads; r += nwarp) {
-      const int t = r / it.heads, g = r % it.heads;
-      const Group gr[2] = {{it.unit + t * a.gs + g, it.run_rows, it.runs}, {0, 0, 0}};
-      merge_row<T>(a, gr, out + ((size_t)(it.tok0 + t) * a.Hq + it.head0 + g) * a.d);
-    }
-    if (warp == 0 && (threadIdx.x & 31) == 0) a.unit_ctr[it.unit] = 0;
-    return;
+  for (int r = warp; r < it.ntok * it.heads; r += nwarp) {
+    const int t = r / it.heads, g = r % it.heads;
+    const Group gr[2] = {{it.unit + t * a.gs + g, it.run_rows, it.runs}, {0, 0, 0}};
+    merge_row<T>(a, gr, out + ((size_t)(it.tok0 + t) * a.Hq + it.head0 + g) * a.d);
   }
-  const int b = unit, hv = it.kvh * a.hs + (it.head0 - it.kvh * a.G) / a.gs;
-  const int n0 = a.n_shared ? a.B * a.T : 0, tiles0 = ceil_div(n0, tile), rr0 = min(tile, n0) * a.gs;
-  const int tiles1 = ceil_div(a.T, tile), rr1 = min(tile, a.T) * a.gs;
-  const int s0 = a.n_shared ? p->split[0] : 0, s1 = p->split[b + 1];
-  for (int r = warp; r < a.T * it.heads; r += nwarp) {
-    const int t = r / it.heads, g = r % it.heads, tok = b * a.T + t;
-    const Group gr[2] = {
-        {p->rows[0] + (long long)(hv * tiles0 + tok / tile) * s0 * rr0 + tok % tile * a.gs + g, rr0, s0},
-        {p->rows[b + 1] + (long long)(hv * tiles1 + t / tile) * s1 * rr1 + t % tile * a.gs + g, rr1, s1}};
-    merge_row<T>(a, gr, out + ((size_t)tok * a.Hq + it.head0 + g) * a.d);
-  }
-  if (warp == 0 && (threadIdx.x & 31) == 0) a.unit_ctr[b * a.hv + hv] = 0;
+  if (warp == 0 && (threadIdx.x & 31) == 0) a.unit_ctr[it.unit] = 0;
 }
 
 // The scheduler hands out item gridDim.x + old count; the last CTA to leave

@@ -39,7 +39,8 @@ cudaError_t launch_write_kv(const WriteArgs& a, cudaStream_t st);
 
 // ---------------------------------------------------------------- attention
 constexpr int kMaxSegs = 1025;      // row segments of one call: sequences, and a shared prefix
-constexpr int kMaxPlanCtas = 640;   // CTAs that the split rule counts on (see make_plan)
+constexpr int kMaxPlanCtas = 640;   // CTAs of a launch at most
+constexpr int kItemsPerCta = 2;     // see make_plan
 constexpr int kSimtRows = 64;       // rows of an item on the CUDA cores
 constexpr int kTcRows = 128;        // rows of a set on the tensor cores; an item has two
 constexpr int kMaxTcCtas = 160;
@@ -60,8 +61,8 @@ struct PagedArgs {
   const int32_t* block_table; // [B, nb_max]
   const int32_t* seq_ctx;     // prompt form: device [B]
   const int32_t* cu_q;        // prompt form: device [B + 1]
-  // workspace: status word, then the scheduler's two words, the units'
-  // arrival counts (all zero between calls) and the partial rows
+  // workspace: status word, then the scheduler's two words, in the prompt form
+  // the units' arrival counts (all zero between calls), and the partial rows
   unsigned* status;
   unsigned* sched;
   unsigned* unit_ctr;
@@ -72,6 +73,10 @@ struct PagedArgs {
   // a KV head's G query heads in hs groups of at most gs heads, so that the
   // gs rows of one token fit a row tile; hv = Hkv * hs
   int gs, hs, hv;
+  // the launch's work split (make_plan): CTAs, items per CTA to aim at, the
+  // fewest key tiles that a run is worth, tokens of a row tile, keys of a key tile
+  int ctas, per_cta, min_run, tile, keys;
+  int elt;                    // bytes of an element
   float scale_log2;           // log2(e) / sqrt(d)
   int prefix;                 // 0: prompt form, 1: prefix form
   int T, n_shared;
@@ -89,9 +94,14 @@ inline void paged_heads(PagedArgs* a, int rows) {
   a->hv = a->Hkv * a->hs;
 }
 
+// Each launches the attention and, in the prefix form, the merge of its
+// partial rows.
 cudaError_t launch_paged_simt(PagedArgs a, int dtype, cudaStream_t st);
 // bf16, head dims up to 128, pages that tile 128 keys (or 128 keys a page).
 bool paged_tc_applies(const PagedArgs& a, int dtype);
 cudaError_t launch_paged_tc(PagedArgs a, cudaStream_t st);
+// Prefix form: join every row's partial rows (the plan of `a`, which the
+// attention kernel launched before ran).
+cudaError_t launch_prefix_merge(const PagedArgs& a, int dtype, cudaStream_t st);
 
 }  // namespace sva

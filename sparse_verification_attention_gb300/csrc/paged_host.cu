@@ -11,6 +11,8 @@ namespace {
 
 constexpr long long kInt = 1ll << 31;
 
+size_t elt_bytes(const sv_shape* s) { return s->dtype == SV_BF16 ? 2 : 4; }
+
 // Workspace of the attention calls (offsets in bytes): status word, the
 // scheduler's words, the units' arrival counts, then partial (m, l) and o
 // rows. Only what lies before `ml` has to be zero between calls.
@@ -28,24 +30,23 @@ PagedLayout paged_layout(size_t counts, size_t rows, int d) {
   return L;
 }
 
-// Partial rows: items of cut segments are at most 4 per CTA (make_plan), an
+// Partial rows: items of cut segments are at most 2 * kItemsPerCta per CTA (make_plan), an
 // item has at most the rows of its tile, and of the call. 640 CTAs of 64 rows
 // cover 160 of 256 (tensor cores) as well.
 static_assert(kMaxPlanCtas * kSimtRows >= kMaxTcCtas * 2 * kTcRows, "partial rows");
 PagedLayout prompt_layout(const sv_shape& s, int n_rows) {
   const long long own = (long long)std::max(n_rows, 1) * (s.Hq / s.Hkv);
-  const size_t rows = (size_t)4 * kMaxPlanCtas * std::min<long long>(kSimtRows, own);
+  const size_t rows = (size_t)2 * kItemsPerCta * kMaxPlanCtas * std::min<long long>(kSimtRows, own);
   return paged_layout(rows, rows, s.d);
 }
 
 // Partial rows: every row once in its shared tile and once in its own, and
-// two items per CTA that cutting adds. Counts: one per sequence and head
-// group (groups are smallest on the CUDA cores).
+// the kItemsPerCta items per CTA that cutting adds. No counts.
 PagedLayout prefix_layout(const sv_shape& s) {
   PagedArgs a{};
   a.Hkv = s.Hkv;
   a.G = s.Hq / s.Hkv;
-  size_t most = 0, counts = 0;
+  size_t most = 0;
   for (int rows : {kSimtRows, kTcRows}) {
     paged_heads(&a, rows);
     const int tile = rows / a.gs * (rows == kTcRows ? 2 : 1);
@@ -53,11 +54,10 @@ PagedLayout prefix_layout(const sv_shape& s) {
       return (size_t)((n + tile - 1) / tile) * std::min<long long>(tile, n) * a.gs * a.hv;
     };
     const size_t r = padded((long long)s.B * s.T) + s.B * padded(s.T) +
-                     (size_t)2 * kMaxPlanCtas * kSimtRows;
+                     (size_t)kItemsPerCta * kMaxPlanCtas * kSimtRows;
     most = std::max(most, r);
-    counts = std::max(counts, (size_t)s.B * a.hv);
   }
-  return paged_layout(counts, most, s.d);
+  return paged_layout(0, most, s.d);
 }
 
 sv_status check_paged_ws(const PagedLayout& L, const void* ws, size_t bytes) {
@@ -81,14 +81,13 @@ void fill_paged(PagedArgs* a, const sv_shape* s, void* ws, const PagedLayout& L)
   a->G = s->Hq / s->Hkv;
   a->d = s->d;
   a->blk = s->blk;
+  a->elt = (int)elt_bytes(s);
   a->scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s->d));
 }
 
 cudaError_t launch_paged(const PagedArgs& a, int dtype, cudaStream_t st) {
   return paged_tc_applies(a, dtype) ? launch_paged_tc(a, st) : launch_paged_simt(a, dtype, st);
 }
-
-size_t elt_bytes(const sv_shape* s) { return s->dtype == SV_BF16 ? 2 : 4; }
 
 // A strided row array: base and stride on 16-byte boundaries, rows apart.
 sv_status check_rows(const sv_shape* s, const char* name, const void* p, long long stride, int heads) {

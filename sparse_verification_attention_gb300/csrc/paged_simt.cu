@@ -49,10 +49,10 @@ constexpr int simt_smem() {  // NC: 64-column groups of the head dim
 
 template <typename T, int NC>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_constant__ PagedArgs a) {
-  extern __shared__ float smem[];
+  extern __shared__ __align__(16) float smem[];
   __shared__ Plan plan;
   __shared__ Item s_item;
-  __shared__ int s_units[kRows + 1], s_nunits;
+  __shared__ int s_last;
   constexpr int kPitch = 64 * NC + 4;
   float* sq = smem;                      // [kRows][kPitch]
   float* sk = sq + kRows * kPitch;       // [kKeys][kPitch], then P [kRows][kPPitch]
@@ -60,18 +60,14 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
   float* sv = sk + (kKeys * kPitch > kRows * kPPitch ? kKeys * kPitch : kRows * kPPitch);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5;
   const T* q = static_cast<const T*>(a.q);
-  const int tile = kRows / a.gs;
 
   pdl_wait();
   pdl_trigger();
-  make_plan(a, &plan, tile, kKeys, 4);
+  make_plan(a, &plan, reinterpret_cast<int*>(smem));
 
   int idx = blockIdx.x;
   while (true) {
-    if (tid == 0) {
-      s_item = decode_item(a, &plan, idx, tile, kKeys);
-      s_nunits = 0;
-    }
+    if (tid == 0) s_item = decode_item(a, &plan, idx);
     __syncthreads();
     const Item it = s_item;
     if (!it.valid) break;
@@ -237,23 +233,24 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
         if (tx == 0) a.part_ml[row] = make_float2(m[i], l[i]);
       }
     }
-    if (it.part >= 0) {
+    if (it.part >= 0 && !a.prefix) {
       __threadfence();
       __syncthreads();
-      arrive_item(a, &plan, it, tile, tid, kThreads, s_units, &s_nunits);
+      if (tid == 0) s_last = arrive_unit(a, it);
       __syncthreads();
-      const int n = s_nunits;
-      if (n > 0) __threadfence();
-      for (int u = 0; u < n; ++u) merge_unit<T>(a, &plan, it, s_units[u], tile, warp, kThreads / 32);
+      if (s_last) {
+        __threadfence();
+        merge_unit<T>(a, it, warp, kThreads / 32);
+      }
     }
     if (tid == 0) idx = next;
-    __syncthreads();  // s_item, the unit list and the tiles are free again
+    __syncthreads();  // s_item, s_last and the tiles are free again
   }
   if (tid == 0) leave(a);
 }
 
 template <typename T, int NC>
-cudaError_t launch_cfg(const PagedArgs& a, cudaStream_t st) {
+cudaError_t launch_cfg(PagedArgs a, int dtype, cudaStream_t st) {
   const int dev = current_device();
   static std::atomic<int> per_sm[kMaxDevices];
   int n = per_sm[dev].load();
@@ -267,23 +264,29 @@ cudaError_t launch_cfg(const PagedArgs& a, cudaStream_t st) {
     if (n < 1) return cudaErrorInvalidConfiguration;
     per_sm[dev].store(n);
   }
-  const int ctas = std::min(sm_count() * n, kMaxPlanCtas);
-  return launch_pdl(paged_simt_kernel<T, NC>, dim3(ctas), dim3(kThreads), simt_smem<NC>(), st, a);
+  a.ctas = std::min(sm_count() * n, kMaxPlanCtas);
+  const cudaError_t e = launch_pdl(paged_simt_kernel<T, NC>, dim3(a.ctas), dim3(kThreads),
+                                   simt_smem<NC>(), st, a);
+  return e == cudaSuccess && a.prefix ? launch_prefix_merge(a, dtype, st) : e;
 }
 
 template <typename T>
-cudaError_t launch_type(const PagedArgs& a, cudaStream_t st) {
-  if (a.d <= 64) return launch_cfg<T, 1>(a, st);
-  if (a.d <= 128) return launch_cfg<T, 2>(a, st);
-  if (a.d <= 192) return launch_cfg<T, 3>(a, st);
-  return launch_cfg<T, 4>(a, st);
+cudaError_t launch_type(const PagedArgs& a, int dtype, cudaStream_t st) {
+  if (a.d <= 64) return launch_cfg<T, 1>(a, dtype, st);
+  if (a.d <= 128) return launch_cfg<T, 2>(a, dtype, st);
+  if (a.d <= 192) return launch_cfg<T, 3>(a, dtype, st);
+  return launch_cfg<T, 4>(a, dtype, st);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_simt(PagedArgs a, int dtype, cudaStream_t st) {
   paged_heads(&a, kRows);
-  return dtype == SV_BF16 ? launch_type<__nv_bfloat16>(a, st) : launch_type<float>(a, st);
+  a.per_cta = kItemsPerCta;
+  a.min_run = 4;
+  a.tile = kRows / a.gs;
+  a.keys = kKeys;
+  return dtype == SV_BF16 ? launch_type<__nv_bfloat16>(a, dtype, st) : launch_type<float>(a, dtype, st);
 }
 
 }  // namespace sva

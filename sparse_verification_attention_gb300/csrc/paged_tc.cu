@@ -3,7 +3,7 @@
 // to 128 (64 and 128 exactly, others padded with zeros by the copies).
 //
 // One pass over the keys with a softmax's running maximum and sum: S = Q K^T
-// for 128 rows x 128 keys into TMEM; one thread per row reads it back, forms
+// for 128 rows x 128 keys into TMEM; two threads per row read it back, form
 // P = 2^(s - m) in bf16 (fp32 sums) over S in TMEM, and O += P V accumulates in
 // TMEM. O is rescaled only when some row's maximum grew by more than 2^8. P is
 // rounded to bf16 because it is an operand of the second product; its sum is
@@ -17,9 +17,11 @@
 //                the odd ones, folded at the end (items of few rows).
 // Either way two independent softmax chains overlap with each other's products.
 //
-// Warps: 0-3 and 4-7 the softmax of set 0 and 1, 8 issues every MMA, 9 takes
-// items from the scheduler, looks pages up and issues the TMA copies, 10-11
-// clear non-finite values out of V tiles that the mask cuts (below).
+// Warps: 0-7 and 8-15 the softmax of set 0 and 1, 16 issues every MMA, 17 takes
+// items from the scheduler, looks pages up and issues the TMA copies, 18-19
+// clear non-finite values out of V tiles that the mask cuts (below). Two
+// threads share a row: each takes half of a tile's keys and they exchange
+// their maxima.
 // Per set and key tile the MMA warp issues P V of one tile and then S of the
 // next, so that the tensor cores work on the other set while this one's
 // softmax runs.
@@ -46,19 +48,20 @@ using namespace paged;
 constexpr int kKeys = 128;            // keys of a tile
 constexpr int kRows = kTcRows;        // rows of a set
 constexpr int kBox = 128 * 128;       // 128 rows of 64 columns, bytes
-constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10;
+constexpr int kThreads = 640;
+constexpr int kMmaWarp = 16, kLoadWarp = 17, kCleanWarp = 18;
 constexpr int kItems = 4;             // item ring
-constexpr int kItemReaders = 11;      // MMA, 8 softmax and 2 cleaning warps
+constexpr int kItemReaders = 19;      // MMA, 16 softmax and 2 cleaning warps
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRescaleLog2 = 8.0f;
+constexpr float kRescaleLog2 = 8.0f;   // O follows the maximum in steps of more than 2^8
+constexpr float kRedoLog2 = 64.0f;
 constexpr int kMaxMasked = 4;         // masked key tiles of an item, at most 3 (see masked_from)
 // registers per thread of the softmax warps and of the others (the launch
-// gives 168 to each of 384 threads: 2 * 128 * 208 + 128 * 80 <= 384 * 168)
-constexpr int kRegsSoftmax = 208, kRegsOther = 80;
+// gives 96 to each of 640 threads: 512 * 104 + 128 * 64 = 640 * 96)
+constexpr int kRegsSoftmax = 104, kRegsOther = 64;
 
-// TMEM columns of set s: S (128 fp32; P, 64 columns of bf16 pairs, takes its
-// place) and O (128 fp32)
+// TMEM columns of set s: S (128 fp32; P, bf16 pairs, takes its place: 32 columns
+// at the start of each half of 64 keys) and O (128 fp32)
 __device__ constexpr uint32_t col_s(int s) { return s ? 128u : 0u; }
 __device__ constexpr uint32_t col_o(int s) { return s ? 384u : 256u; }
 
@@ -72,15 +75,16 @@ struct Cfg {
 
 struct Control {
   uint64_t full[8], empty[8], vclean[8];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_done[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_done[2];
+  uint64_t halves[2][4];  // the two warps of a set's lane quarter
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t meet, drained;
   uint32_t tmem;
   int abort;
-  int nunits[2];
-  int units[2][257];
+  int last[2];  // the item was the last of its unit (by item parity)
   uint32_t nonfinite[kItems][kMaxMasked][4];  // keys of an item's masked tiles, from the last
-  float2 ml[2][kRows];
+  float mx[2][2][kRows];   // a tile's maxima by set and half
+  float2 ml[2][2][kRows];  // maximum and sum by set and half
   unsigned long long anc[kMaxT];
   Item items[kItems];
   Plan plan;
@@ -148,6 +152,54 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// MMA issue by a converged warp: the operands are computed by all lanes, so
+// that descriptors stay in uniform registers, and one elected lane issues
+// (lead != 0 there). Issued from a branch that only lane 0 takes, every MMA
+// cost its thread about 100 cycles, which bounded the kernel.
+__device__ __forceinline__ uint32_t elect_lead() {
+  uint32_t lead;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(lead));
+  return lead;
+}
+__device__ __forceinline__ void lead_mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void lead_mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void lead_commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void regs_grow() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -155,6 +207,28 @@ __device__ __forceinline__ void regs_grow() {
 template <int N>
 __device__ __forceinline__ void regs_shrink() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Wait on a phase of an mbarrier by polling: the hand-offs of the inner loop
+// (S to the softmax, P back to the MMA warp) are on its critical path, and a
+// thread that try_wait suspended wakes late. The clock and the abort flag are
+// looked at every 256 polls.
+__device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity, volatile int* abort,
+                                     unsigned* status, unsigned site) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; !mbar_test_wait(bar, parity); ++n) {
+    if (n & 255u) continue;
+    if (*abort) return false;
+    const uint64_t t = globaltimer_ns();
+    if (!t0) t0 = t;
+    if (t - t0 > kWaitBudgetNs) {
+      *abort = 1;
+      atomicOr(status, SV_FLAG_WAIT_TIMEOUT);
+      atomicMax(status + 1, site);
+      return false;
+    }
+  }
+  return true;
 }
 
 // Set the non-finite bf16 elements of four words to zero; true if there were any.
@@ -174,10 +248,11 @@ __device__ __forceinline__ bool clear_nonfinite(uint4* w) {
 }
 
 // Add the non-finite V elements that a row sees in the tiles that were
-// cleared to columns [c0, c0 + 32) of its sums.
+// cleared to columns [c0, c1) of its stored result (out, or the partial row).
 __device__ __noinline__ void add_nonfinite(const PagedArgs& a, const Item& it,
                                            const uint32_t (*bits)[4], int nmasked, int vis,
-                                           unsigned long long anc, int c0, float* f) {
+                                           unsigned long long anc, int c0, int c1,
+                                           __nv_bfloat16* out, float* part) {
   const __nv_bfloat16* pool = static_cast<const __nv_bfloat16*>(a.v_pool);
   const __nv_bfloat16* dv = static_cast<const __nv_bfloat16*>(a.draft_v);
   for (int e = 0; e < nmasked; ++e) {
@@ -196,9 +271,11 @@ __device__ __noinline__ void add_nonfinite(const PagedArgs& a, const Item& it,
         if (page < 0 || page >= a.num_pages) continue;
         row = pool + (((size_t)page * a.Hkv + it.kvh) * a.blk + key % a.blk) * a.d;
       }
-      for (int c = 0; c < 32 && c0 + c < a.d; ++c) {
-        const float x = __bfloat162float(row[c0 + c]);
-        if (!(fabsf(x) < INFINITY)) f[c] += x;
+      for (int c = c0; c < c1 && c < a.d; ++c) {
+        const float x = __bfloat162float(row[c]);
+        if (fabsf(x) < INFINITY) continue;
+        if (out) out[c] = __float2bfloat16(__bfloat162float(out[c]) + x);
+        else part[c] += x;
       }
     }
   }
@@ -217,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~uintptr_t(1023));
   const uint32_t q_base = smem_u32(smem), ring = q_base + 2 * C::kTile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tt = kRows / a.gs, tile = 2 * tt;
+  const int tt = kRows / a.gs;  // tokens of a set; an item's tile is two of them
   volatile int* abort = &sh.abort;
 
   if (threadIdx.x == 0) {
@@ -230,14 +307,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sh.q_full[i]), 1);
       mbar_init(smem_u32(&sh.q_empty[i]), 1);
       mbar_init(smem_u32(&sh.s_full[i]), 1);
-      mbar_init(smem_u32(&sh.p_ready[i]), 4);
+      for (int h = 0; h < 2; ++h) mbar_init(smem_u32(&sh.p_ready[i][h]), 4);
+      for (int q = 0; q < 4; ++q) mbar_init(smem_u32(&sh.halves[i][q]), 2);
       mbar_init(smem_u32(&sh.o_done[i]), 1);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(smem_u32(&sh.item_full[i]), 1);
       mbar_init(smem_u32(&sh.item_empty[i]), kItemReaders);
     }
-    mbar_init(smem_u32(&sh.meet), 8);
+    mbar_init(smem_u32(&sh.meet), 16);
     mbar_init(smem_u32(&sh.drained), 1);
     sh.abort = 0;
     fence_barrier_init();
@@ -254,20 +332,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
   tc::fence_before();
-  make_plan(a, &sh.plan, tile, kKeys, 2);
+  make_plan(a, &sh.plan, reinterpret_cast<int*>(smem));
   tc::fence_after();
   const uint32_t tmem = sh.tmem;
   auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) {
     return mbar_wait_abortable(smem_u32(bar), parity, abort, a.status, site);
   };
-  // the seq-th item of this CTA, copied out of the item ring
-  auto take_item = [&](uint32_t seq, Item* it) {
+  auto poll = [&](uint64_t* bar, uint32_t parity, unsigned site) {
+    return spin(smem_u32(bar), parity, abort, a.status, site);
+  };
+  auto poll_all = [&](uint64_t* bar, uint32_t parity, unsigned site) {
+    return __all_sync(0xffffffffu, poll(bar, parity, site)) != 0;
+  };
+  // the seq-th item of this CTA; read in place until done_item
+  auto take_item = [&](uint32_t seq) {
     const int s = seq % kItems;
-    if (!__all_sync(0xffffffffu, wait(&sh.item_full[s], (seq / kItems) & 1, 20u))) return false;
-    *it = sh.items[s];
+    return __all_sync(0xffffffffu, wait(&sh.item_full[s], (seq / kItems) & 1, 20u)) &&
+           sh.items[s].valid != 0;
+  };
+  auto done_item = [&](uint32_t seq) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sh.item_empty[s]));
-    return it->valid != 0;
+    if (lane == 0) mbar_arrive(smem_u32(&sh.item_empty[seq % kItems]));
   };
 
   if (warp >= kMmaWarp) regs_shrink<kRegsOther>();
@@ -286,10 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (seq >= kItems &&
           !__all_sync(0xffffffffu, wait(&sh.item_empty[slot], ((seq / kItems) & 1) ^ 1, 1u)))
         break;
-      if (lane == 0) sh.items[slot] = decode_item(a, &sh.plan, idx, tile, kKeys);
+      if (lane == 0) sh.items[slot] = decode_item(a, &sh.plan, idx);
       __syncwarp();
-      const Item it = sh.items[slot];
-      __syncwarp();
+      const Item& it = sh.items[slot];
       if (lane == 0) mbar_arrive(smem_u32(&sh.item_full[slot]));
       if (!it.valid) break;
       int next = 0;
@@ -373,20 +457,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dk0 = tc::smem_desc(ring, 16, 1024);
     const uint64_t dv0 = tc::smem_desc(ring, kBox, 1024);
     uint32_t at = 0, q_uses[2] = {0, 0}, alt = 0, p_uses[2] = {0, 0};
+    const uint32_t lead = elect_lead();
     bool ok = true;
-    Item it;
-    for (uint32_t seq = 0; ok && take_item(seq, &it); ++seq) {
+    for (uint32_t seq = 0; ok && take_item(seq); ++seq) {
+      const Item& it = sh.items[seq % kItems];
       const Run r = run_of(it, tt);
-      if (it.nk == 0) continue;
-      if (lane == 0) {
+      const int nk = it.nk;
+      if (nk > 0) {
         auto stage = [&](uint32_t pos) { return (at + pos) % NS; };
         auto phase = [&](uint32_t pos) { return ((at + pos) / NS) & 1; };
-        auto k_wait = [&](int j) { return wait(&sh.full[stage(pos_k(r, j))], phase(pos_k(r, j)), 4u); };
+        auto k_wait = [&](int j) { return poll_all(&sh.full[stage(pos_k(r, j))], phase(pos_k(r, j)), 4u); };
         auto v_wait = [&](int j) {
-          const uint32_t p = pos_v(r, j, it.nk);
-          return wait(&sh.vclean[stage(p)], phase(p), 5u);
+          const uint32_t p = pos_v(r, j, nk);
+          return poll_all(&sh.vclean[stage(p)], phase(p), 5u);
         };
-        auto p_wait = [&](int s) { return wait(&sh.p_ready[s], p_uses[s]++ & 1, 6u); };
         auto issue_s = [&](int s, int qs, int j) {
           tc::fence_after();
           const uint64_t dq = dq0 + (uint64_t)(qs * (C::kTile >> 4));
@@ -394,106 +478,111 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
-            tc::mma_ss(tmem + col_s(s), dq + off, dk + off, id_s, kk > 0 ? 1u : 0u);
+            lead_mma_ss(lead, tmem + col_s(s), dq + off, dk + off, id_s, kk > 0 ? 1u : 0u);
           }
-          tc::commit(smem_u32(&sh.s_full[s]));
+          lead_commit(lead, smem_u32(&sh.s_full[s]));
         };
+        // O += P V as the halves of P get ready
         auto issue_o = [&](int s, int j, bool first) {
+          if (!poll_all(&sh.p_ready[s][0], p_uses[s] & 1, 6u)) return false;
           tc::fence_after();
-          const uint64_t dv = dv0 + (uint64_t)(stage(pos_v(r, j, it.nk)) * (C::kTile >> 4));
+          const uint64_t dv = dv0 + (uint64_t)(stage(pos_v(r, j, nk)) * (C::kTile >> 4));
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            tc::mma_ts(tmem + col_o(s), tmem + col_s(s) + kk * 8, dv + (uint64_t)((kk * 2048) >> 4),
+          for (int kk = 0; kk < kKeys / 32; ++kk)
+            lead_mma_ts(lead, tmem + col_o(s), tmem + col_s(s) + kk * 8, dv + (uint64_t)((kk * 2048) >> 4),
                        id_o, !first || kk > 0 ? 1u : 0u);
+          if (!poll_all(&sh.p_ready[s][1], p_uses[s]++ & 1, 12u)) return false;
+          tc::fence_after();
+#pragma unroll
+          for (int kk = kKeys / 32; kk < kKeys / 16; ++kk)
+            lead_mma_ts(lead, tmem + col_o(s), tmem + col_s(s) + 32 + kk * 8, dv + (uint64_t)((kk * 2048) >> 4),
+                       id_o, 1u);
+          return true;
         };
-        auto free_k = [&](int j) { tc::commit(smem_u32(&sh.empty[stage(pos_k(r, j))])); };
-        auto free_v = [&](int j) { tc::commit(smem_u32(&sh.empty[stage(pos_v(r, j, it.nk))])); };
+        auto free_k = [&](int j) { lead_commit(lead, smem_u32(&sh.empty[stage(pos_k(r, j))])); };
+        auto free_v = [&](int j) { lead_commit(lead, smem_u32(&sh.empty[stage(pos_v(r, j, nk))])); };
         if (r.pair) {
-          ok = wait(&sh.q_full[0], q_uses[0]++ & 1, 7u) && wait(&sh.q_full[1], q_uses[1]++ & 1, 7u) &&
+          ok = poll_all(&sh.q_full[0], q_uses[0]++ & 1, 7u) && poll_all(&sh.q_full[1], q_uses[1]++ & 1, 7u) &&
                k_wait(0);
           if (ok) {
             if (r.n[0] > 0) issue_s(0, 0, 0);
             issue_s(1, 1, 0);
             free_k(0);
           }
-          for (int j = 0; ok && j < it.nk; ++j) {
-            const bool more = j + 1 < it.nk;
+          for (int j = 0; ok && j < nk; ++j) {
+            const bool more = j + 1 < nk;
+            // what the two products need is waited for ahead of P
+            if (!(ok = v_wait(j) && (!more || k_wait(j + 1)))) break;
             if (j < r.n[0]) {
-              if (!(ok = p_wait(0) && v_wait(j))) break;
-              issue_o(0, j, j == 0);
+              if (!(ok = issue_o(0, j, j == 0))) break;
               if (j + 1 < r.n[0]) {
-                if (!(ok = k_wait(j + 1))) break;
                 issue_s(0, 0, j + 1);
               } else {
-                tc::commit(smem_u32(&sh.o_done[0]));
+                lead_commit(lead, smem_u32(&sh.o_done[0]));
               }
             }
-            if (!(ok = p_wait(1) && v_wait(j))) break;
-            issue_o(1, j, j == 0);
+            if (!(ok = issue_o(1, j, j == 0))) break;
             free_v(j);
             if (more) {
-              if (!(ok = k_wait(j + 1))) break;
               issue_s(1, 1, j + 1);
               free_k(j + 1);
             } else {
-              tc::commit(smem_u32(&sh.o_done[1]));
+              lead_commit(lead, smem_u32(&sh.o_done[1]));
             }
-            if (j + 2 == it.nk || it.nk == 1) {  // the item's last S is out
-              tc::commit(smem_u32(&sh.q_empty[0]));
-              tc::commit(smem_u32(&sh.q_empty[1]));
+            if (j + 2 == nk || nk == 1) {  // the item's last S is out
+              lead_commit(lead, smem_u32(&sh.q_empty[0]));
+              lead_commit(lead, smem_u32(&sh.q_empty[1]));
             }
           }
         } else {
           const int qs = alt++ & 1;
-          ok = wait(&sh.q_full[qs], q_uses[qs]++ & 1, 7u) && k_wait(0);
+          ok = poll_all(&sh.q_full[qs], q_uses[qs]++ & 1, 7u) && k_wait(0);
           if (ok) {
             issue_s(0, qs, 0);
             free_k(0);
-            if (it.nk > 1 && (ok = k_wait(1))) {
+            if (nk > 1 && (ok = k_wait(1))) {
               issue_s(1, qs, 1);
               free_k(1);
             }
-            if (it.nk <= 2) tc::commit(smem_u32(&sh.q_empty[qs]));
+            if (nk <= 2) lead_commit(lead, smem_u32(&sh.q_empty[qs]));
           }
-          for (int j = 0; ok && j < it.nk; ++j) {
+          for (int j = 0; ok && j < nk; ++j) {
             const int s = j & 1;
-            if (!(ok = p_wait(s) && v_wait(j))) break;
-            issue_o(s, j, j < 2);
+            if (!(ok = v_wait(j) && (j + 2 >= nk || k_wait(j + 2)))) break;
+            if (!(ok = issue_o(s, j, j < 2))) break;
             free_v(j);
-            if (j + 2 < it.nk) {
-              if (!(ok = k_wait(j + 2))) break;
+            if (j + 2 < nk) {
               issue_s(s, qs, j + 2);
               free_k(j + 2);
-              if (j + 3 == it.nk) tc::commit(smem_u32(&sh.q_empty[qs]));
+              if (j + 3 == nk) lead_commit(lead, smem_u32(&sh.q_empty[qs]));
             } else {
-              tc::commit(smem_u32(&sh.o_done[s]));
+              lead_commit(lead, smem_u32(&sh.o_done[s]));
             }
           }
         }
       }
-      at += 2 * it.nk;
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      at += 2 * nk;
+      done_item(seq);
     }
-    if (lane == 0) {
-      tc::commit(smem_u32(&sh.drained));  // TMEM is given back after every MMA
-      mbar_wait_drain(smem_u32(&sh.drained), 0);
-    }
+    lead_commit(lead, smem_u32(&sh.drained));  // TMEM is given back after every MMA
+    mbar_wait_drain(smem_u32(&sh.drained), 0);
     __syncwarp();
   } else if (warp >= kCleanWarp) {
     // ------------------------------------------------------------ V tiles
     const int w = warp - kCleanWarp;  // keys [64 w, 64 w + 64)
     uint32_t at = 0;
     bool ok = true;
-    Item it;
-    for (uint32_t seq = 0; ok && take_item(seq, &it); ++seq) {
+    for (uint32_t seq = 0; ok && take_item(seq); ++seq) {
+      const Item& it = sh.items[seq % kItems];
       const Run r = run_of(it, tt);
+      const int nk = it.nk;
       // every ring position in order: a V tile that needs it is cleared, and the
       // stage's barrier advances once per use whatever the stage holds
-      for (int pos = 0; pos < 2 * it.nk; ++pos) {
+      for (int pos = 0; pos < 2 * nk; ++pos) {
         const uint32_t x = at + pos;
         const int s = x % NS;
         if (!(ok = __all_sync(0xffffffffu, wait(&sh.full[s], (x / NS) & 1, 8u)))) break;
-        const int j = v_at(r, pos, it.nk);
+        const int j = v_at(r, pos, nk);
         if (j >= r.masked) {
           uint8_t* v = smem + 2 * C::kTile + s * C::kTile;
           uint32_t bits[2] = {0, 0};
@@ -513,204 +602,253 @@ __global__ void __launch_bounds__(kThreads, 1)
           bits[1] = __reduce_or_sync(0xffffffffu, bits[1]);
           if (bits[0] | bits[1]) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           if (lane < 2)
-            sh.nonfinite[seq % kItems][min(kMaxMasked - 1, it.nk - 1 - j)][2 * w + lane] = bits[lane];
+            sh.nonfinite[seq % kItems][min(kMaxMasked - 1, nk - 1 - j)][2 * w + lane] = bits[lane];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.vclean[s]));
       }
-      at += 2 * it.nk;
+      at += 2 * nk;
+      done_item(seq);
     }
   } else {
     // ------------------------------------------------------------ softmax
     regs_grow<kRegsSoftmax>();
-    const int X = warp >> 2, q4 = warp & 3, r = 32 * q4 + lane;
-    const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
-    const uint32_t tS = tmem + lane_base + col_s(X), tO = tmem + lane_base + col_o(X);
+    const int X = warp >> 3, H = warp >> 2 & 1, q4 = warp & 3, r = 32 * q4 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
+    const uint32_t tS = lane_base + col_s(X) + 64 * H, tP = tS;
+    const uint32_t tO = lane_base + col_o(X) + D / 2 * H;
     const int rt = r / a.gs, rg = r % a.gs;  // token of the set and head of the group
-    uint32_t s_uses = 0, o_uses = 0, meets = 0, parts = 0;
+    uint32_t s_uses = 0, o_uses = 0, h_uses = 0, meets = 0, parts = 0;
     bool ok = true;
-    // all eight softmax warps meet
+    // all softmax warps meet
     auto meet = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.meet));
-      return __all_sync(0xffffffffu, wait(&sh.meet, meets++ & 1, 9u)) != 0;
+      return __all_sync(0xffffffffu, poll(&sh.meet, meets++ & 1, 9u)) != 0;
     };
-    Item it;
-    for (uint32_t seq = 0; ok && take_item(seq, &it); ++seq) {
+    // the two warps of this set's rows meet
+    auto meet_half = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.halves[X][q4]));
+      return __all_sync(0xffffffffu, poll(&sh.halves[X][q4], h_uses++ & 1, 13u)) != 0;
+    };
+    for (uint32_t seq = 0; ok && take_item(seq); ++seq) {
+      const Item& it = sh.items[seq % kItems];
       const Run run = run_of(it, tt);
       const int off = run.pair && X ? tt : 0;  // the set's first token
       const int tok = off + rt;
       const bool valid = rt < tt && tok < it.ntok && rg < it.heads;
       const bool live = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps step
-      const int vis = max(0, it.causal ? it.vis0 + tok : it.ctx);
-      const int vis_set = it.causal ? it.vis0 + off : it.ctx;  // the set's first row sees the fewest
-      const unsigned long long anc = it.draft && valid ? sh.anc[it.draft0 + tok] : 0ull;
-      float m_run = -INFINITY, l_run = 0.f;
       const int n = X ? run.n[1] : run.n[0];
+      // relative to the run's first key: keys that the row sees, and that the
+      // set's first row sees (it sees the fewest)
+      const int vis = (it.causal ? it.vis0 + tok : it.ctx) - it.k0 * kKeys - 64 * H;
+      const int vis_set = (it.causal ? it.vis0 + off : it.ctx) - it.k0 * kKeys - 64 * H;
+      const int draft_tile = it.draft ? it.nk - 1 : -1;
+      const int stride = run.pair ? 1 : 2, first = run.pair ? 0 : X;
+      float m_run = -INFINITY, m_next = -INFINITY, l_run = 0.f;
+      // move the row's reference to m: O (this thread's half of its columns) and
+      // the sum so far follow
+      auto rescale = [&](float m) {
+        const float alpha = m == -INFINITY ? 1.f : exp2f(m_run - m);
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += 16) {
+          uint32_t o[16];
+          tc::ld16(tO + c, o);
+          tc::wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tc::st16(tO + c, o);
+        }
+        l_run *= alpha;
+        m_run = m;
+      };
+      // P = 2^(s - m) of this thread's 64 keys into TMEM, and its sum
+      auto exponentials = [&](const uint32_t(&v)[2][32]) {
+        const float nb = m_run == -INFINITY ? 0.f : -m_run;
+        const uint64_t nb2 = pack2(nb, nb), sc2 = pack2(a.scale_log2, a.scale_log2);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t* s16 = v[c >> 1] + 16 * (c & 1);
+          uint32_t p[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 e = unpack2(
+                fma2(pack2(__uint_as_float(s16[2 * i]), __uint_as_float(s16[2 * i + 1])), sc2, nb2));
+            const float x = exp2f(e.x), y = exp2f(e.y);
+            sum[i & 1] = add2(sum[i & 1], pack2(x, y));
+            p[i] = pack_bf16(x, y);
+          }
+          tc::st8(tP + 8 * c, p);
+        }
+        return add2(sum[0], sum[1]);
+      };
       for (int j = 0; j < n; ++j) {
-        const int kt = run.pair ? j : 2 * j + X;
-        if (!(ok = __all_sync(0xffffffffu, wait(&sh.s_full[X], s_uses++ & 1, 10u)))) break;
+        const int kt = first + stride * j;
+        if (!(ok = __all_sync(0xffffffffu, poll(&sh.s_full[X], s_uses++ & 1, 10u)))) break;
         if (live) {
           tc::fence_after();
-          uint32_t v[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tc::ld32(tS + 32 * c, v[c]);
+          uint32_t v[2][32];
+          tc::ld32(tS, v[0]);
+          tc::ld32(tS + 32, v[1]);
           tc::wait_ld();
-          const int base = (it.k0 + kt) * kKeys;
-          const bool drafts = it.draft && kt == it.nk - 1;
-          if (drafts || base + kKeys > vis_set) {
-            const int lim = vis - base;  // keys of this tile that the row sees
+          if (kt == draft_tile || kt * kKeys + 64 > vis_set) {
+            uint32_t keep[2];  // keys of this half that the row sees
+            if (kt == draft_tile) {  // drafts 0..63: all in the first half
+              const unsigned long long see = valid && H == 0 ? sh.anc[it.draft0 + tok] : 0ull;
+              keep[0] = (uint32_t)see;
+              keep[1] = (uint32_t)(see >> 32);
+            } else {
+              const int lim = vis - kt * kKeys;
+              keep[0] = lim >= 32 ? 0xffffffffu : lim <= 0 ? 0u : (1u << lim) - 1u;
+              keep[1] = lim >= 64 ? 0xffffffffu : lim <= 32 ? 0u : (1u << (lim - 32)) - 1u;
+            }
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t keep;
-              if (drafts)
-                keep = c < 2 ? (uint32_t)(anc >> (32 * c)) : 0u;
-              else
-                keep = lim >= 32 * c + 32 ? 0xffffffffu : lim <= 32 * c ? 0u : (1u << (lim - 32 * c)) - 1u;
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(keep >> i & 1u)) v[c][i] = 0xff800000u;  // -inf
+            for (int i = 0; i < 32; ++i) {
+              if (!(keep[0] >> i & 1u)) v[0][i] = 0xff800000u;  // -inf
+              if (!(keep[1] >> i & 1u)) v[1][i] = 0xff800000u;
             }
           }
+          // The row's maximum over all tiles before this one is m_next: the
+          // exponentials need not wait for this tile's own. P may then exceed
+          // 1, but what it exceeds by only moves exponents. In an item's first
+          // tile, and where a row's maximum grows by more than 2^64 in one
+          // tile (a row that has seen nothing so far among them), this tile's
+          // maximum is taken first.
+          if (j > 0 && __any_sync(0xffffffffu, m_next > m_run)) {
+            // S of this tile was issued behind the set's previous P V, so that
+            // product is complete and O may be rescaled
+            rescale(m_next);
+          }
+          uint64_t sum = 0;
+          if (j > 0) sum = exponentials(v);
           float mx[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            mx[c] = __uint_as_float(v[c][0]);
+            const uint32_t* x = v[c >> 1] + 16 * (c & 1);
+            mx[c] = __uint_as_float(x[0]);
 #pragma unroll
-            for (int i = 1; i < 32; ++i) mx[c] = fmaxf(mx[c], __uint_as_float(v[c][i]));
+            for (int i = 1; i < 15; i += 2)
+              mx[c] = max3(mx[c], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            mx[c] = fmaxf(mx[c], __uint_as_float(x[15]));
           }
-          const float mrow = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-          // S of this tile was issued behind the set's previous P V, so that
-          // product is complete and O may be rescaled
-          if (__any_sync(0xffffffffu, mrow > m_run + kRescaleLog2)) {
-            const float m_new = fmaxf(m_run, mrow);
-            const float alpha = m_new == -INFINITY ? 1.f : exp2f(m_run - m_new);
-            if (j > 0) {
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tc::ld32(tO + 32 * c, o);
-                tc::wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                tc::st32(tO + 32 * c, o);
-              }
-            }
-            l_run *= alpha;
-            m_run = m_new;
+          const float mine = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          sh.mx[X][H][r] = mine;
+          if (!(ok = meet_half())) break;
+          const float mrow = fmaxf(mine, sh.mx[X][H ^ 1][r]) * a.scale_log2;
+          if (j == 0) {
+            m_run = mrow;
+            sum = exponentials(v);
+          } else if (__any_sync(0xffffffffu, mrow > m_run + kRedoLog2)) {
+            rescale(fmaxf(m_run, mrow));
+            sum = exponentials(v);
           }
-          const float nb = m_run == -INFINITY ? 0.f : -m_run;
-          const uint64_t nb2 = pack2(nb, nb), sc2 = pack2(a.scale_log2, a.scale_log2);
-          uint64_t sum = 0;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 e = unpack2(fma2(pack2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])),
-                                            sc2, nb2));
-              const float x = exp2f(e.x), y = exp2f(e.y);
-              sum = add2(sum, pack2(x, y));
-              p[i] = pack_bf16(x, y);
-            }
-            tc::st16(tS + 16 * c, p);
-          }
+          m_next = mrow > m_run + kRescaleLog2 ? mrow : m_run;
           const float2 s2 = unpack2(sum);
           l_run += s2.x + s2.y;
           tc::wait_st();
           tc::fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[X]));
+        if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[X][H]));
       }
       if (!ok) break;
       // ---------------------------------------------------------- results
       if (n > 0) {
-        if (!(ok = __all_sync(0xffffffffu, wait(&sh.o_done[X], o_uses++ & 1, 11u)))) break;
+        if (!(ok = __all_sync(0xffffffffu, poll(&sh.o_done[X], o_uses++ & 1, 11u)))) break;
         tc::fence_after();
       }
-      const int pp = parts & 1;  // unit list of this item
-      if (it.part >= 0 && threadIdx.x == 0) sh.nunits[pp] = 0;
-      // non-finite V in a cleared tile
-      const int nmasked = min(kMaxMasked, max(0, it.nk - run.masked));
-      const uint32_t(*nf)[4] = sh.nonfinite[seq % kItems];
-      uint32_t any_nf = 0;
-      for (int e = 0; e < nmasked; ++e) any_nf |= nf[e][0] | nf[e][1] | nf[e][2] | nf[e][3];
-      // columns [c0, c1) of the row are this thread's: all (pair), or half of
-      // both sets' sums (alternating)
+      // the row's maximum and sum over both halves (and, alternating, both sets)
       float w[2] = {X ? 0.f : 1.f, X ? 1.f : 0.f}, m_out = m_run, l_out = l_run;
-      int c0 = 0, c1 = D;
-      if (!run.pair) {
-        sh.ml[X][r] = make_float2(m_run, l_run);
+      sh.ml[X][H][r] = make_float2(m_run, l_run);
+      if (run.pair) {
+        if (!(ok = meet_half())) break;
+        l_out += sh.ml[X][H ^ 1][r].y;
+      } else {
         if (!(ok = meet())) break;
         tc::fence_after();
-        const float2 ma = sh.ml[0][r], mb = sh.ml[1][r];
-        m_out = fmaxf(ma.x, mb.x);
-        w[0] = ma.x == -INFINITY ? 0.f : exp2f(ma.x - m_out);
-        w[1] = mb.x == -INFINITY ? 0.f : exp2f(mb.x - m_out);
-        l_out = w[0] * ma.y + w[1] * mb.y;
-        c0 = X * (D / 2);
-        c1 = c0 + D / 2;
+        const float2 m0 = sh.ml[0][0][r], m1 = sh.ml[1][0][r];
+        m_out = fmaxf(m0.x, m1.x);
+        w[0] = m0.x == -INFINITY ? 0.f : exp2f(m0.x - m_out);
+        w[1] = m1.x == -INFINITY ? 0.f : exp2f(m1.x - m_out);
+        l_out = w[0] * (m0.y + sh.ml[0][1][r].y) + w[1] * (m1.y + sh.ml[1][1][r].y);
       }
       if (live) {
+        // non-finite V in a cleared tile
+        const int nmasked = min(kMaxMasked, max(0, it.nk - run.masked));
+        const uint32_t(*nf)[4] = sh.nonfinite[seq % kItems];
+        uint32_t any_nf = 0;
+        for (int e = 0; e < nmasked; ++e) any_nf |= nf[e][0] | nf[e][1] | nf[e][2] | nf[e][3];
         const float inv = l_out == 0.f ? 0.f : 1.0f / l_out;
         const bool use0 = (run.pair ? X == 0 : true) && run.n[0] > 0;
         const bool use1 = (run.pair ? X == 1 : true) && run.n[1] > 0;
+        const size_t prow = (size_t)max(it.part, 0) + tok * a.gs + rg;
+        // 16 columns at a time: this thread's share of the row's D is its half
+        // (pair), or a quarter of both sets' sums (alternating)
+        const int c0 = run.pair ? D / 2 * H : D / 4 * (2 * X + H), c1 = c0 + (run.pair ? D / 2 : D / 4);
 #pragma unroll 1
-        for (int c = c0; c < c1; c += 32) {
+        for (int c = c0; c < c1; c += 16) {
           __syncwarp();
-          float f[32];
+          float f[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) f[e] = 0.f;
-          uint32_t o[32];
+          for (int e = 0; e < 16; ++e) f[e] = 0.f;
+          uint32_t o[16];
           if (use0) {
-            tc::ld32(tmem + lane_base + col_o(0) + c, o);
+            tc::ld16(lane_base + col_o(0) + c, o);
             tc::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] = w[0] != 0.f ? w[0] * __uint_as_float(o[e]) : 0.f;
+            for (int e = 0; e < 16; ++e) f[e] = w[0] != 0.f ? w[0] * __uint_as_float(o[e]) : 0.f;
           }
           if (use1) {
-            tc::ld32(tmem + lane_base + col_o(1) + c, o);
+            tc::ld16(lane_base + col_o(1) + c, o);
             tc::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] += w[1] != 0.f ? w[1] * __uint_as_float(o[e]) : 0.f;
+            for (int e = 0; e < 16; ++e) f[e] += w[1] != 0.f ? w[1] * __uint_as_float(o[e]) : 0.f;
           }
           if (!valid) continue;
-          if (any_nf) add_nonfinite(a, it, nf, nmasked, vis, anc, c, f);
           if (it.part < 0) {
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
                                  ((size_t)(it.tok0 + tok) * a.Hq + it.head0 + rg) * a.d + c;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
+            for (int e = 0; e < 16; e += 8)
               if (c + e < a.d)
                 *reinterpret_cast<uint4*>(dst + e) =
                     make_uint4(pack_bf16(f[e] * inv, f[e + 1] * inv), pack_bf16(f[e + 2] * inv, f[e + 3] * inv),
                                pack_bf16(f[e + 4] * inv, f[e + 5] * inv), pack_bf16(f[e + 6] * inv, f[e + 7] * inv));
           } else {
-            float* dst = a.part_o + ((size_t)it.part + tok * a.gs + rg) * a.d + c;
+            float* dst = a.part_o + prow * a.d + c;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
+            for (int e = 0; e < 16; e += 4)
               if (c + e < a.d)
                 *reinterpret_cast<float4*>(dst + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
           }
         }
-        if (valid && it.part >= 0 && (run.pair || X == 0))
-          a.part_ml[(size_t)it.part + tok * a.gs + rg] = make_float2(m_out, l_out);
+        if (any_nf && valid)
+          add_nonfinite(a, it, nf, nmasked, it.causal ? it.vis0 + tok : it.ctx,
+                        it.draft ? sh.anc[it.draft0 + tok] : 0ull, c0, c1,
+                        it.part < 0 ? static_cast<__nv_bfloat16*>(a.out) +
+                                          ((size_t)(it.tok0 + tok) * a.Hq + it.head0 + rg) * a.d
+                                    : nullptr,
+                        a.part_o + prow * a.d);
+        if (valid && it.part >= 0 && H == 0 && (run.pair || X == 0)) a.part_ml[prow] = make_float2(m_out, l_out);
       }
       tc::fence_before();  // O is read: the next item's products may overwrite it
-      if (it.part >= 0) {
+      if (it.part >= 0 && !a.prefix) {
         __threadfence();
         if (!(ok = meet())) break;
-        arrive_item(a, &sh.plan, it, tile, threadIdx.x, 256, sh.units[pp], &sh.nunits[pp]);
+        const int pp = parts++ & 1;
+        if (threadIdx.x == 0) sh.last[pp] = arrive_unit(a, it);
         if (!(ok = meet())) break;
-        const int nu = sh.nunits[pp];
-        if (nu > 0) __threadfence();
-        for (int u = 0; u < nu; ++u)
-          merge_unit<__nv_bfloat16>(a, &sh.plan, it, sh.units[pp][u], tile, warp, 8);
-        ++parts;
-      } else if (!run.pair) {
-        if (!(ok = meet())) break;
+        if (sh.last[pp]) {
+          __threadfence();
+          merge_unit<__nv_bfloat16>(a, it, warp, 16);
+        }
+      } else {
+        // both halves (pair) or all warps (alternating) have read sums and O
+        if (!(ok = run.pair ? meet_half() : meet())) break;
       }
+      done_item(seq);
     }
   }
 
@@ -733,7 +871,7 @@ bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims
 }
 
 template <int D>
-cudaError_t launch_cfg(const PagedArgs& a, const CUtensorMap* m, cudaStream_t st) {
+cudaError_t launch_cfg(PagedArgs a, const CUtensorMap* m, cudaStream_t st) {
   const int dev = current_device();
   static std::atomic<int> ready[kMaxDevices];
   if (!ready[dev].load()) {
@@ -742,8 +880,10 @@ cudaError_t launch_cfg(const PagedArgs& a, const CUtensorMap* m, cudaStream_t st
     if (e != cudaSuccess) return e;
     ready[dev].store(1);
   }
-  return launch_pdl(paged_tc_kernel<D>, dim3(std::min(sm_count(), kMaxTcCtas)), dim3(kThreads),
-                    Cfg<D>::kSmem, st, m[0], m[1], m[2], m[3], m[4], a);
+  a.ctas = std::min(sm_count(), kMaxTcCtas);
+  const cudaError_t e = launch_pdl(paged_tc_kernel<D>, dim3(a.ctas), dim3(kThreads), Cfg<D>::kSmem, st,
+                                   m[0], m[1], m[2], m[3], m[4], a);
+  return e == cudaSuccess && a.prefix ? launch_prefix_merge(a, SV_BF16, st) : e;
 }
 
 }  // namespace
@@ -757,6 +897,15 @@ bool paged_tc_applies(const PagedArgs& a, int dtype) {
 
 cudaError_t launch_paged_tc(PagedArgs a, cudaStream_t st) {
   paged_heads(&a, kRows);
+#ifndef PER_CTA_PROMPT
+#define PER_CTA_PROMPT 2
+#define PER_CTA_PREFIX 2
+#define MIN_RUN 2
+#endif
+  a.per_cta = a.prefix ? PER_CTA_PREFIX : PER_CTA_PROMPT;
+  a.min_run = MIN_RUN;
+  a.tile = 2 * (kRows / a.gs);
+  a.keys = kKeys;
   CUtensorMap m[5];
   const cuuint64_t d = a.d, hd = (cuuint64_t)a.Hkv * a.d;
   {
