@@ -487,12 +487,11 @@ sv_status sv_write_kv(const sv_shape* shape, const void* k, long long k_stride, 
 
 /* Bytes of workspace for sv_prompt_attend calls of up to n_rows query rows
  * with this shape (B, Hq, Hkv, d; the largest B is enough), and for
- * sv_prefix_attend calls with this shape. The whole workspace must be zero
- * before its first use, every completed call leaves its counts zero, and two
- * calls that may overlap on the GPU must not share one. The first 256 bytes
- * hold the status word (sv_read_status, sv_clear_status). After a call that
- * raised SV_FLAG_WAIT_TIMEOUT or SV_FLAG_STALE_WORKSPACE zero the workspace
- * again. 0 on an invalid shape. Host only. */
+ * sv_prefix_attend calls with this shape. The whole workspace must be
+ * zero before its first use, and two calls that may overlap on the GPU must
+ * not share one. The first 256 bytes hold the status word (sv_read_status, sv_clear_status). After a call that
+ * raised SV_FLAG_WAIT_TIMEOUT zero the workspace's first 512 bytes. 0 on an
+ * invalid shape. Host only. */
 size_t sv_prompt_workspace_bytes(const sv_shape* shape, int n_rows);
 size_t sv_prefix_workspace_bytes(const sv_shape* shape);
 

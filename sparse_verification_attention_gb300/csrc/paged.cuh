@@ -2,13 +2,10 @@
 // attention kernels share (device code).
 //
 // A segment's rows are cut into tiles of `tile` tokens, its keys into tiles
-// of `keys` tokens (the prefix form's drafts are one more key tile). An item
-// is one row tile of one head group over a run of key tiles. Lengths may live
-// in device memory only, so every CTA derives the same plan from them: a
-// segment whose row tiles see more than C key tiles is cut into s =
-// ceil(kt / C) runs, with C such that the grid gets about kItemsPerCta items per
-// CTA. That bounds the partial rows by a number the host knows: the items of
-// cut segments are at most twice sum(tiles * kt) / C <= 2 * kItemsPerCta * CTAs.
+// of `keys` tokens (the prefix form's drafts are one more key tile). A unit is
+// one row tile of one head group, an item a unit or a run of its key tiles.
+// Lengths may live in device memory only, so every CTA derives the same plan
+// from them (make_plan).
 #pragma once
 
 #include "paged.h"
@@ -52,29 +49,54 @@ __device__ __forceinline__ Seg seg_of(const PagedArgs& a, int i) {
 
 __device__ __forceinline__ int n_segs(const PagedArgs& a) { return a.prefix ? a.B + 1 : a.B; }
 
-// The plan in shared memory: segments in the order in which their items are
+// The plan in shared memory: segments in the order in which their units are
 // handed out.
 struct Plan {
-  int items[kMaxSegs + 1];  // first item of every segment; [nseg] = all items
-  int rows[kMaxSegs];       // first partial row of every segment
-  int split[kMaxSegs];      // runs of key tiles (>= 1)
+  int first[kMaxSegs + 1];  // what lies before a segment: items, or (stream) cost
   int order[kMaxSegs];      // the segment
+  int rows[kMaxSegs];       // prefix form: first partial row
+  int split[kMaxSegs];      // prefix form: runs of key tiles (>= 1)
+  int stream;               // prompt form: equal shares of the flattened units
 };
 constexpr int kPlanScratch = 2 * (kMaxSegs + 3);  // ints that make_plan needs besides
 
 constexpr long long kL2Keys = 32ll << 20;  // a quarter of L2
 
 __device__ __forceinline__ int ceil_div(int x, int y) { return (x + y - 1) / y; }
+__device__ __forceinline__ int key_tiles(const PagedArgs& a, int keys) {
+  return (int)(((unsigned)keys + (1u << a.key_shift) - 1) >> a.key_shift);
+}
+// What a key tile of an item of n tokens costs: two sets of rows take twice
+// the tensor cores' time.
+__device__ __forceinline__ int weight_of(const PagedArgs& a, int n) { return n > a.one_set ? 2 : 1; }
+
+// Prompt form: what a unit costs, in key tiles of one set: its tiles, and what
+// starting and ending an item takes besides.
+__device__ __forceinline__ int unit_cost(const PagedArgs& a, const Seg& s) {
+  return key_tiles(a, s.ctx) * weight_of(a, s.n) + kItemCost;
+}
 
 // Fill `p` (all threads of the CTA call it; barriers inside). scratch:
 // kPlanScratch ints of shared memory on a 16-byte boundary.
 //
-// Prompt segments go out in descending order of key tiles, so that what starts
-// last is short (a dynamic schedule is as good as its last items are small).
-// The prefix form keeps its order: the shared segment comes first.
+// Prefix form: every segment's keys are cut into runs so that the grid gets
+// about kItemsPerCta items per CTA; the shared segment comes first. Its partial
+// rows are then at most those of the uncut segments and kItemsPerCta items per
+// CTA more.
+//
+// Prompt form, one of two ways, whichever is expected to end earlier:
+//   whole units, handed out dynamically, segments in descending order of key
+//     tiles, so that what starts last is short. Ends at about the average load
+//     plus half the longest unit (at least at the longest);
+//   stream: the units laid end to end, CTA c taking the c-th equal share, at
+//     most two cut units each. Ends at the average load, counting for every row
+//     tile the keys of its segment's last one, and the join of the cut units.
+// Few rows over long contexts stream (16 ragged decoding sequences: 154 us cut
+// into runs and scheduled, CTAs ending between 60 and 100% of it), whole
+// prompts do not.
 __device__ inline void make_plan(const PagedArgs& a, Plan* p, int* scratch) {
   const int nseg = n_segs(a), lane = threadIdx.x & 31, padded = (nseg + 3) & ~3;
-  int* kts = scratch;                    // key tiles of segment i
+  int* kts = scratch;                         // cost of a unit of segment i
   int* ns = scratch + ((kMaxSegs + 3) & ~3);  // rows of segment i
   for (int i = threadIdx.x; i < padded; i += blockDim.x) {
     kts[i] = -1;
@@ -82,68 +104,128 @@ __device__ inline void make_plan(const PagedArgs& a, Plan* p, int* scratch) {
     const Seg s = seg_of(a, i);
     if (s.bad && blockIdx.x == 0) atomicOr(a.status, SV_FLAG_BAD_LENGTH);
     ns[i] = s.n;
-    kts[i] = s.n ? ceil_div(s.ctx, a.keys) + s.draft : 0;
+    kts[i] = !s.n ? 0 : a.prefix ? key_tiles(a, s.ctx) + s.draft : unit_cost(a, s);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < nseg; i += blockDim.x) {
-    int rank = i;
-    if (!a.prefix && nseg > 1) {
+  if (!a.prefix && nseg > 1) {
+    for (int i = threadIdx.x; i < nseg; i += blockDim.x) {
       const int kt = kts[i];
-      rank = 0;
+      int rank = 0;
       for (int j = 0; j < padded; j += 4) {
         const int4 k = *reinterpret_cast<const int4*>(kts + j);
         rank += (k.x > kt || (k.x == kt && j < i)) + (k.y > kt || (k.y == kt && j + 1 < i)) +
                 (k.z > kt || (k.z == kt && j + 2 < i)) + (k.w > kt || (k.w == kt && j + 3 < i));
       }
+      p->order[rank] = i;
     }
-    p->order[rank] = i;
+    __syncthreads();
   }
-  __syncthreads();
   if (threadIdx.x < 32) {
-    const int per = ceil_div(nseg, 32), b0 = min(nseg, lane * per), b1 = min(nseg, b0 + per);
-    unsigned long long units = 0;
-    for (int i = b0; i < b1; ++i)
-      units += (unsigned long long)ceil_div(ns[i], a.tile) * a.hv * kts[i];
+    const int per = nseg > 32 ? (nseg + 31) >> 5 : 1, b0 = min(nseg, lane * per), b1 = min(nseg, b0 + per);
+    int at = 0, row = 0;  // this lane's totals, then what lies before them
+    if (a.prefix) {
+      unsigned long long units = 0;
+      for (int i = b0; i < b1; ++i)
+        units += (unsigned long long)ceil_div(ns[i], a.tile) * a.hv * kts[i];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) units += __shfl_xor_sync(0xffffffffu, units, off);
-    const unsigned long long parts = (unsigned long long)a.per_cta * a.ctas;
-    const unsigned long long want = (units + parts - 1) / parts;
-    const int run = (int)min(max(want, (unsigned long long)a.min_run), 1ull << 30);
-    // items and partial rows of every segment, scanned
-    int items = 0, rows = 0;
-    for (int i = b0; i < b1; ++i) {
-      const int kt = kts[p->order[i]], n = ns[p->order[i]];
-      int s = kt > run ? ceil_div(kt, run) : 1;
-      if (s > 1) s = ceil_div(kt, ceil_div(kt, s));  // no empty run
-      const int it = ceil_div(n, a.tile) * a.hv * s;
-      const int r = s > 1 || a.prefix ? it * min(a.tile, n) * a.gs : 0;
-      p->split[i] = s;
-      p->items[i] = it;
-      p->rows[i] = r;
-      items += it;
-      rows += r;
-    }
-    int ix = items, rx = rows;
+      for (int off = 16; off > 0; off >>= 1) units += __shfl_xor_sync(0xffffffffu, units, off);
+      const unsigned parts = kItemsPerCta * a.ctas;
+      const unsigned long long want =
+          units >> 31 ? (units + parts - 1) / parts : ((unsigned)units + parts - 1) / parts;
+      const int run = (int)min(max(want, (unsigned long long)a.min_run), 1ull << 30);
+      for (int i = b0; i < b1; ++i) {
+        const int kt = kts[i], n = ns[i];
+        int s = kt > run ? ceil_div(kt, run) : 1;
+        if (s > 1) s = ceil_div(kt, ceil_div(kt, s));  // no empty run
+        const int it = ceil_div(n, a.tile) * a.hv * s;
+        p->order[i] = i;
+        p->split[i] = s;
+        p->first[i] = it;
+        p->rows[i] = it * min(a.tile, n) * a.gs;
+        at += it;
+        row += p->rows[i];
+      }
+    } else {
+      float cost = 0.f, seen = 0.f, units = 0.f, most = 0.f;
+      for (int i = b0; i < b1; ++i) {
+        const int id = nseg > 1 ? p->order[i] : 0, kt = kts[id], n = ns[id];
+        if (nseg == 1) p->order[0] = 0;
+        const float u = (float)(ceil_div(n, a.tile) * a.hv);
+        units += u;
+        cost += u * kt;
+        // causal: from the keys before the rows to all of them, on average
+        const float before = (float)max(kItemCost, kt - weight_of(a, n) * key_tiles(a, n));
+        seen += u * 0.5f * (before + kt);
+        most = fmaxf(most, (float)kt);
+      }
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, ix, off), z = __shfl_up_sync(0xffffffffu, rx, off);
-      if (lane >= off) {
-        ix += y;
-        rx += z;
+      for (int off = 16; off > 0; off >>= 1) {
+        cost += __shfl_xor_sync(0xffffffffu, cost, off);
+        seen += __shfl_xor_sync(0xffffffffu, seen, off);
+        units += __shfl_xor_sync(0xffffffffu, units, off);
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+      }
+      const float ctas = (float)a.ctas;
+      const float whole = units <= ctas ? most : fmaxf(most, seen / ctas + 0.5f * most);
+      const bool stream = cost < 1e9f && cost / ctas + kStreamCost < whole;
+      if (lane == 0) p->stream = stream;
+      for (int i = b0; i < b1; ++i) {
+        const int id = p->order[i], n = ns[id];
+        p->first[i] = ceil_div(n, a.tile) * a.hv * (stream ? kts[id] : 1);
+        at += p->first[i];
       }
     }
-    int at = ix - items, row = rx - rows;
-    for (int i = b0; i < b1; ++i) {
-      const int it = p->items[i], r = p->rows[i];
-      p->items[i] = at;
-      p->rows[i] = row;
-      at += it;
-      row += r;
+    int ax = at, rx = row;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, ax, off), y = __shfl_up_sync(0xffffffffu, rx, off);
+      if (lane >= off) {
+        ax += x;
+        rx += y;
+      }
     }
-    if (lane == 31) p->items[nseg] = at;
+    at = ax - at;
+    row = rx - row;
+    for (int i = b0; i < b1; ++i) {
+      const int x = p->first[i];
+      p->first[i] = at;
+      at += x;
+      if (a.prefix) {
+        const int r = p->rows[i];
+        p->rows[i] = row;
+        row += r;
+      }
+    }
+    if (lane == 31) p->first[nseg] = at;
   }
   __syncthreads();
 }
+
+// The last segment (in plan order) that starts at or before x.
+__device__ __forceinline__ int find_seg(const Plan* p, int nseg, int x) {
+  int lo = 0, hi = nseg;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (p->first[m] <= x) lo = m;
+    else hi = m;
+  }
+  return lo;
+}
+
+// Stream: where CTA c's share of a total starts, and the CTA that position x
+// lies in.
+__device__ __forceinline__ int share_start(int total, int ctas, int c) {
+  const int q = total / ctas, r = total % ctas;
+  return c * q + min(c, r);
+}
+__device__ __forceinline__ int share_of(int total, int ctas, int x) {
+  const int q = total / ctas, r = total % ctas, head = r * (q + 1);
+  return x < head ? x / (q + 1) : r + (x - head) / q;
+}
+// Stream: partial rows of a cut unit lie in slots of slot_rows rows, two per
+// CTA: 2 c for the end (or middle) of a unit that CTA c starts with, 2 c + 1 for
+// the beginning of the unit that it ends with.
+__device__ __forceinline__ int slot_rows(const PagedArgs& a) { return min(a.tile, a.n_rows) * a.gs; }
 
 struct Item {
   int valid;
@@ -159,56 +241,91 @@ struct Item {
   int seq;            // sequence (drafts)
   int tab;            // first block-table entry of the segment's keys
   int part;           // first partial row, -1: the run is the whole row (written to out)
-  // the partial rows of all runs of this row tile and head group: the first
-  // one, the number of runs, rows between runs
-  int unit, runs, run_rows;
 };
 
-__device__ inline Item decode_item(const PagedArgs& a, const Plan* p, int idx) {
-  const int tile = a.tile, keys = a.keys;
+// The item of row tile t and head group hv of segment `id` over key tiles
+// [k0, k1).
+__device__ __forceinline__ Item make_item(const PagedArgs& a, const Seg& s, int id, int t, int hv, int k0,
+                                          int k1) {
   Item it;
+  it.valid = 1;
+  it.tok0 = s.tok0 + t * a.tile;
+  it.ntok = min(a.tile, s.n - t * a.tile);
+  it.kvh = a.hs > 1 ? hv / a.hs : hv;
+  const int sub = (hv - it.kvh * a.hs) * a.gs;
+  it.head0 = it.kvh * a.G + sub;
+  it.heads = min(a.gs, a.G - sub);
+  it.causal = !a.prefix;
+  it.ctx = s.ctx;
+  it.vis0 = a.prefix ? s.ctx : s.ctx - s.n + t * a.tile + 1;
+  const int last = a.prefix ? s.ctx : max(0, it.vis0 + it.ntok - 1);
+  const int kt = key_tiles(a, last) + s.draft;
+  it.k0 = k0;
+  it.nk = max(0, min(kt, k1) - k0);
+  it.draft = s.draft && it.nk > 0 && k0 + it.nk == kt;
+  it.draft0 = t * a.tile;
+  it.seq = a.prefix ? id - 1 : id;
+  it.tab = s.tab;
+  it.part = -1;
+  return it;
+}
+
+// A CTA's place in the plan.
+struct Cursor {
+  int at, end;  // item number, or (stream) position in the flattened cost
+};
+
+__device__ __forceinline__ Cursor start_cursor(const PagedArgs& a, const Plan* p) {
+  if (a.prefix || !p->stream) return {(int)blockIdx.x, 0};
+  const int total = p->first[n_segs(a)];
+  return {share_start(total, a.ctas, blockIdx.x), share_start(total, a.ctas, blockIdx.x + 1)};
+}
+
+// The item at the cursor (valid = 0 behind the last one), and the cursor
+// moved on. One thread calls it.
+__device__ inline Item next_item(const PagedArgs& a, const Plan* p, Cursor* c) {
   const int nseg = n_segs(a);
-  it.valid = idx < p->items[nseg];
-  if (!it.valid) return it;
-  int lo = 0, hi = nseg;  // the last segment whose items start at or before idx
-  while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if (p->items[m] <= idx) lo = m;
-    else hi = m;
+  if (!a.prefix && p->stream) {
+    if (c->at >= c->end) {
+      Item it;
+      it.valid = 0;
+      return it;
+    }
+    const int lo = find_seg(p, nseg, c->at), id = p->order[lo];
+    const Seg s = seg_of(a, id);
+    const int w = weight_of(a, s.n), cost = unit_cost(a, s);
+    const int local = c->at - p->first[lo], unit = local / cost, off = local - unit * cost;
+    const int upto = min(cost, off + c->end - c->at);
+    const int tiles = ceil_div(s.n, a.tile), hv = unit / tiles;
+    Item it = make_item(a, s, id, tiles - 1 - (unit - hv * tiles), hv,
+                        (max(0, off - kItemCost) + w - 1) >> (w - 1),
+                        (max(0, upto - kItemCost) + w - 1) >> (w - 1));
+    if (off > 0 || upto < cost) it.part = (2 * blockIdx.x + (off > 0 ? 0 : 1)) * slot_rows(a);
+    c->at += upto - off;
+    return it;
   }
-  const int id = p->order[lo];
+  if (c->at >= p->first[nseg]) {
+    Item it;
+    it.valid = 0;
+    return it;
+  }
+  const int lo = find_seg(p, nseg, c->at), id = p->order[lo];
   const Seg s = seg_of(a, id);
-  const int runs = p->split[lo], tiles = ceil_div(s.n, tile);
+  const int runs = a.prefix ? p->split[lo] : 1, tiles = ceil_div(s.n, a.tile);
   // Neighbours in the list share keys (they meet in L2): groups of heads whose
   // keys and values fit kL2Keys, in a group run by run, in a run the rows
   // that see most first.
-  const long long kv = (long long)s.ctx * a.d * 2 * a.elt + 1;
-  const int fit = (int)min(max(kL2Keys / kv, 1ll), (long long)a.hv);
-  const int gh = ceil_div(a.hv, ceil_div(a.hv, fit)), per = gh * tiles * runs;
-  const int local = idx - p->items[lo], h0 = local / per * gh, in = local % per;
-  const int gw = min(gh, a.hv - h0), hv = h0 + in % gw;
-  const int t = tiles - 1 - in / gw % tiles, run = in / gw / tiles;
-  it.tok0 = s.tok0 + t * tile;
-  it.ntok = min(tile, s.n - t * tile);
-  it.kvh = hv / a.hs;
-  it.head0 = it.kvh * a.G + hv % a.hs * a.gs;
-  it.heads = min(a.gs, a.G - hv % a.hs * a.gs);
-  it.causal = !a.prefix;
-  it.ctx = s.ctx;
-  it.vis0 = a.prefix ? s.ctx : s.ctx - s.n + t * tile + 1;
-  const int last = a.prefix ? s.ctx : max(0, it.vis0 + it.ntok - 1);
-  const int kt = ceil_div(last, keys) + s.draft;
-  const int len = ceil_div(ceil_div(s.ctx, keys) + s.draft, runs);
-  it.k0 = run * len;
-  it.nk = max(0, min(kt, it.k0 + len) - it.k0);
-  it.draft = s.draft && it.nk > 0 && it.k0 + it.nk == kt;
-  it.draft0 = t * tile;
-  it.seq = a.prefix ? id - 1 : id;
-  it.tab = s.tab;
-  it.runs = runs;
-  it.run_rows = min(tile, s.n) * a.gs;
-  it.unit = p->rows[lo] + (hv * tiles + t) * runs * it.run_rows;
-  it.part = runs > 1 || a.prefix ? it.unit + run * it.run_rows : -1;
+  const unsigned kv = (unsigned)(((long long)s.ctx * a.d * a.elt) >> 9) + 1;  // KB of keys and values
+  const int fit = min((int)((unsigned)(kL2Keys >> 10) / kv) + 1, a.hv);
+  const int gh = fit < a.hv ? ceil_div(a.hv, ceil_div(a.hv, fit)) : a.hv, per = gh * tiles * runs;
+  const int local = c->at - p->first[lo], h0 = local / per * gh, in = local % per;
+  const int gw = min(gh, a.hv - h0), u = in / gw, hv = h0 + in - u * gw;
+  const int run = u / tiles, t = tiles - 1 - (u - run * tiles);
+  const int len = a.prefix ? ceil_div(key_tiles(a, s.ctx) + s.draft, runs) : 1 << 28;
+  Item it = make_item(a, s, id, t, hv, run * len, (run + 1) * len);
+  // partial rows of a segment lie by head group, row tile, run, token, head
+  if (a.prefix) it.part = p->rows[lo] + ((hv * tiles + t) * runs + run) * min(a.tile, s.n) * a.gs;
+  c->at = (int)gridDim.x + (int)atomicAdd(a.sched, 1u);
   return it;
 }
 
@@ -285,32 +402,8 @@ __device__ inline void merge_row(const PagedArgs& a, const Group (&g)[2], T* dst
   }
 }
 
-// A prompt item's partial rows are written and ordered (barrier and
-// device-scope fence): true when they were the last of their unit, which the
-// caller then merges. One thread calls it.
-__device__ __forceinline__ bool arrive_unit(const PagedArgs& a, const Item& it) {
-  const unsigned old = arrive_acq_rel(a.unit_ctr + it.unit);
-  if (old >= (unsigned)it.runs) atomicOr(a.status, SV_FLAG_STALE_WORKSPACE);
-  return old + 1 == (unsigned)it.runs;
-}
-
-// Merge a prompt item's unit with `nwarp` warps and return its count to zero.
-template <typename T>
-__device__ inline void merge_unit(const PagedArgs& a, const Item& it, int warp, int nwarp) {
-  T* out = static_cast<T*>(a.out);
-  for (int r = warp; r < it.ntok * it.heads; r += nwarp) {
-    const int t = r / it.heads, g = r % it.heads;
-    const Group gr[2] = {{it.unit + t * a.gs + g, it.run_rows, it.runs}, {0, 0, 0}};
-    merge_row<T>(a, gr, out + ((size_t)(it.tok0 + t) * a.Hq + it.head0 + g) * a.d);
-  }
-  if (warp == 0 && (threadIdx.x & 31) == 0) a.unit_ctr[it.unit] = 0;
-}
-
-// The scheduler hands out item gridDim.x + old count; the last CTA to leave
-// returns both words to zero.
-__device__ __forceinline__ int next_item(const PagedArgs& a) {
-  return (int)gridDim.x + (int)atomicAdd(a.sched, 1u);
-}
+// A CTA has drawn its last item; the last CTA to leave returns the scheduler's
+// words to zero.
 __device__ __forceinline__ void leave(const PagedArgs& a) {
   if (arrive_acq_rel(a.sched + 1) + 1 == gridDim.x) {
     a.sched[0] = 0;

@@ -41,6 +41,8 @@ cudaError_t launch_write_kv(const WriteArgs& a, cudaStream_t st);
 constexpr int kMaxSegs = 1025;      // row segments of one call: sequences, and a shared prefix
 constexpr int kMaxPlanCtas = 640;   // CTAs of a launch at most
 constexpr int kItemsPerCta = 2;     // see make_plan
+constexpr int kItemCost = 4;        // key tiles' time that an item takes besides its own (make_plan)
+constexpr float kStreamCost = 8.f;  // key tiles' time that joining cut units takes (make_plan)
 constexpr int kSimtRows = 64;       // rows of an item on the CUDA cores
 constexpr int kTcRows = 128;        // rows of a set on the tensor cores; an item has two
 constexpr int kMaxTcCtas = 160;
@@ -61,11 +63,10 @@ struct PagedArgs {
   const int32_t* block_table; // [B, nb_max]
   const int32_t* seq_ctx;     // prompt form: device [B]
   const int32_t* cu_q;        // prompt form: device [B + 1]
-  // workspace: status word, then the scheduler's two words, in the prompt form
-  // the units' arrival counts (all zero between calls), and the partial rows
+  // workspace: status word, the scheduler's two words (zero between calls), and
+  // the partial rows
   unsigned* status;
   unsigned* sched;
-  unsigned* unit_ctr;
   float* part_o;              // [partial rows, d]
   float2* part_ml;            // [partial rows]: running maximum (log2 domain), sum
   long long q_stride;
@@ -73,10 +74,12 @@ struct PagedArgs {
   // a KV head's G query heads in hs groups of at most gs heads, so that the
   // gs rows of one token fit a row tile; hv = Hkv * hs
   int gs, hs, hv;
-  // the launch's work split (make_plan): CTAs, items per CTA to aim at, the
-  // fewest key tiles that a run is worth, tokens of a row tile, keys of a key tile
-  int ctas, per_cta, min_run, tile, keys;
+  // the launch's work split (make_plan): CTAs, the fewest key tiles that a run
+  // is worth, tokens of a row tile, tokens above which its rows are two sets,
+  // log2 of the keys of a key tile
+  int ctas, min_run, tile, one_set, key_shift;
   int elt;                    // bytes of an element
+  int out_wide;               // rows of out lie on 32-byte boundaries
   float scale_log2;           // log2(e) / sqrt(d)
   int prefix;                 // 0: prompt form, 1: prefix form
   int T, n_shared;
@@ -94,14 +97,13 @@ inline void paged_heads(PagedArgs* a, int rows) {
   a->hv = a->Hkv * a->hs;
 }
 
-// Each launches the attention and, in the prefix form, the merge of its
-// partial rows.
+// Each launches the attention and the merge of its partial rows.
 cudaError_t launch_paged_simt(PagedArgs a, int dtype, cudaStream_t st);
 // bf16, head dims up to 128, pages that tile 128 keys (or 128 keys a page).
 bool paged_tc_applies(const PagedArgs& a, int dtype);
 cudaError_t launch_paged_tc(PagedArgs a, cudaStream_t st);
-// Prefix form: join every row's partial rows (the plan of `a`, which the
-// attention kernel launched before ran).
-cudaError_t launch_prefix_merge(const PagedArgs& a, int dtype, cudaStream_t st);
+// Join the partial rows that the attention kernel launched just before left
+// (the same arguments: it rebuilds that launch's plan).
+cudaError_t launch_paged_merge(const PagedArgs& a, int dtype, cudaStream_t st);
 
 }  // namespace sva

@@ -14,34 +14,32 @@ constexpr long long kInt = 1ll << 31;
 size_t elt_bytes(const sv_shape* s) { return s->dtype == SV_BF16 ? 2 : 4; }
 
 // Workspace of the attention calls (offsets in bytes): status word, the
-// scheduler's words, the units' arrival counts, then partial (m, l) and o
-// rows. Only what lies before `ml` has to be zero between calls.
+// scheduler's words (zero between calls), then partial (m, l) and o rows.
 struct PagedLayout {
-  size_t sched, ctr, ml, o, total;
+  size_t sched, ml, o, total;
 };
 
-PagedLayout paged_layout(size_t counts, size_t rows, int d) {
+PagedLayout paged_layout(size_t rows, int d) {
   PagedLayout L;
   L.sched = kStatusBytes;
-  L.ctr = L.sched + 256;
-  L.ml = L.ctr + align256(counts * sizeof(uint32_t));
+  L.ml = L.sched + 256;
   L.o = L.ml + align256(rows * sizeof(float2));
   L.total = L.o + align256(rows * (size_t)d * sizeof(float));
   return L;
 }
 
-// Partial rows: items of cut segments are at most 2 * kItemsPerCta per CTA (make_plan), an
-// item has at most the rows of its tile, and of the call. 640 CTAs of 64 rows
-// cover 160 of 256 (tensor cores) as well.
+// Partial rows: two slots per CTA (make_plan), a slot has the rows of a tile, or
+// of the call if it has fewer. 640 CTAs of 64 rows cover 160 of 256 (tensor
+// cores) as well.
 static_assert(kMaxPlanCtas * kSimtRows >= kMaxTcCtas * 2 * kTcRows, "partial rows");
 PagedLayout prompt_layout(const sv_shape& s, int n_rows) {
   const long long own = (long long)std::max(n_rows, 1) * (s.Hq / s.Hkv);
-  const size_t rows = (size_t)2 * kItemsPerCta * kMaxPlanCtas * std::min<long long>(kSimtRows, own);
-  return paged_layout(rows, rows, s.d);
+  const size_t rows = (size_t)2 * kMaxPlanCtas * std::min<long long>(kSimtRows, own);
+  return paged_layout(rows, s.d);
 }
 
 // Partial rows: every row once in its shared tile and once in its own, and
-// the kItemsPerCta items per CTA that cutting adds. No counts.
+// the kItemsPerCta items per CTA that cutting adds.
 PagedLayout prefix_layout(const sv_shape& s) {
   PagedArgs a{};
   a.Hkv = s.Hkv;
@@ -57,7 +55,7 @@ PagedLayout prefix_layout(const sv_shape& s) {
                      (size_t)kItemsPerCta * kMaxPlanCtas * kSimtRows;
     most = std::max(most, r);
   }
-  return paged_layout(0, most, s.d);
+  return paged_layout(most, s.d);
 }
 
 sv_status check_paged_ws(const PagedLayout& L, const void* ws, size_t bytes) {
@@ -72,7 +70,6 @@ void fill_paged(PagedArgs* a, const sv_shape* s, void* ws, const PagedLayout& L)
   uint8_t* w = static_cast<uint8_t*>(ws);
   a->status = reinterpret_cast<unsigned*>(w);
   a->sched = reinterpret_cast<unsigned*>(w + L.sched);
-  a->unit_ctr = reinterpret_cast<unsigned*>(w + L.ctr);
   a->part_ml = reinterpret_cast<float2*>(w + L.ml);
   a->part_o = reinterpret_cast<float*>(w + L.o);
   a->B = s->B;

@@ -52,7 +52,6 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
   extern __shared__ __align__(16) float smem[];
   __shared__ Plan plan;
   __shared__ Item s_item;
-  __shared__ int s_last;
   constexpr int kPitch = 64 * NC + 4;
   float* sq = smem;                      // [kRows][kPitch]
   float* sk = sq + kRows * kPitch;       // [kKeys][kPitch], then P [kRows][kPPitch]
@@ -65,15 +64,12 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
   pdl_trigger();
   make_plan(a, &plan, reinterpret_cast<int*>(smem));
 
-  int idx = blockIdx.x;
+  Cursor cursor = start_cursor(a, &plan);  // thread 0's counts
   while (true) {
-    if (tid == 0) s_item = decode_item(a, &plan, idx);
+    if (tid == 0) s_item = next_item(a, &plan, &cursor);
     __syncthreads();
     const Item it = s_item;
     if (!it.valid) break;
-    // the next item's number, fetched while this one runs (thread 0 only)
-    int next = 0;
-    if (tid == 0) next = next_item(a);
     const int rows = it.ntok * it.heads;
     // Q rows r = token * heads + head; rows past the tile's are zero
     for (int e = tid; e < kRows * 16 * NC; e += kThreads) {
@@ -233,18 +229,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
         if (tx == 0) a.part_ml[row] = make_float2(m[i], l[i]);
       }
     }
-    if (it.part >= 0 && !a.prefix) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) s_last = arrive_unit(a, it);
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        merge_unit<T>(a, it, warp, kThreads / 32);
-      }
-    }
-    if (tid == 0) idx = next;
-    __syncthreads();  // s_item, s_last and the tiles are free again
+    __syncthreads();  // s_item and the tiles are free again
   }
   if (tid == 0) leave(a);
 }
@@ -267,7 +252,7 @@ cudaError_t launch_cfg(PagedArgs a, int dtype, cudaStream_t st) {
   a.ctas = std::min(sm_count() * n, kMaxPlanCtas);
   const cudaError_t e = launch_pdl(paged_simt_kernel<T, NC>, dim3(a.ctas), dim3(kThreads),
                                    simt_smem<NC>(), st, a);
-  return e == cudaSuccess && a.prefix ? launch_prefix_merge(a, dtype, st) : e;
+  return e == cudaSuccess ? launch_paged_merge(a, dtype, st) : e;
 }
 
 template <typename T>
@@ -282,10 +267,9 @@ cudaError_t launch_type(const PagedArgs& a, int dtype, cudaStream_t st) {
 
 cudaError_t launch_paged_simt(PagedArgs a, int dtype, cudaStream_t st) {
   paged_heads(&a, kRows);
-  a.per_cta = kItemsPerCta;
   a.min_run = 4;
-  a.tile = kRows / a.gs;
-  a.keys = kKeys;
+  a.tile = a.one_set = kRows / a.gs;
+  a.key_shift = 6;
   return dtype == SV_BF16 ? launch_type<__nv_bfloat16>(a, dtype, st) : launch_type<float>(a, dtype, st);
 }
 

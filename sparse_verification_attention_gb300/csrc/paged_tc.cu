@@ -81,7 +81,6 @@ struct Control {
   uint64_t meet, drained;
   uint32_t tmem;
   int abort;
-  int last[2];  // the item was the last of its unit (by item parity)
   uint32_t nonfinite[kItems][kMaxMasked][4];  // keys of an item's masked tiles, from the last
   float mx[2][2][kRows];   // a tile's maxima by set and half
   float2 ml[2][2][kRows];  // maximum and sum by set and half
@@ -152,6 +151,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -200,6 +204,24 @@ __device__ __forceinline__ void lead_commit(uint32_t lead, uint32_t bar) {
       : "memory");
 }
 
+// 32 lanes x 32 (8) columns of TMEM into r[0..32) (r[0..8)).
+__device__ __forceinline__ void ld32_at(uint32_t taddr, uint32_t* r) {
+  tc::ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(r));
+}
+__device__ __forceinline__ void ld8_at(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+
+// 32 bytes (a whole sector) to a 32-byte boundary.
+__device__ __forceinline__ void store32(void* p, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]),
+               "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void regs_grow() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -207,28 +229,6 @@ __device__ __forceinline__ void regs_grow() {
 template <int N>
 __device__ __forceinline__ void regs_shrink() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// Wait on a phase of an mbarrier by polling: the hand-offs of the inner loop
-// (S to the softmax, P back to the MMA warp) are on its critical path, and a
-// thread that try_wait suspended wakes late. The clock and the abort flag are
-// looked at every 256 polls.
-__device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity, volatile int* abort,
-                                     unsigned* status, unsigned site) {
-  uint64_t t0 = 0;
-  for (uint32_t n = 1; !mbar_test_wait(bar, parity); ++n) {
-    if (n & 255u) continue;
-    if (*abort) return false;
-    const uint64_t t = globaltimer_ns();
-    if (!t0) t0 = t;
-    if (t - t0 > kWaitBudgetNs) {
-      *abort = 1;
-      atomicOr(status, SV_FLAG_WAIT_TIMEOUT);
-      atomicMax(status + 1, site);
-      return false;
-    }
-  }
-  return true;
 }
 
 // Set the non-finite bf16 elements of four words to zero; true if there were any.
@@ -338,16 +338,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) {
     return mbar_wait_abortable(smem_u32(bar), parity, abort, a.status, site);
   };
-  auto poll = [&](uint64_t* bar, uint32_t parity, unsigned site) {
-    return spin(smem_u32(bar), parity, abort, a.status, site);
-  };
-  auto poll_all = [&](uint64_t* bar, uint32_t parity, unsigned site) {
-    return __all_sync(0xffffffffu, poll(bar, parity, site)) != 0;
+  auto wait_all = [&](uint64_t* bar, uint32_t parity, unsigned site) {
+    return __all_sync(0xffffffffu, wait(bar, parity, site)) != 0;
   };
   // the seq-th item of this CTA; read in place until done_item
   auto take_item = [&](uint32_t seq) {
     const int s = seq % kItems;
-    return __all_sync(0xffffffffu, wait(&sh.item_full[s], (seq / kItems) & 1, 20u)) &&
+    return wait_all(&sh.item_full[s], (seq / kItems) & 1, 20u) &&
            sh.items[s].valid != 0;
   };
   auto done_item = [&](uint32_t seq) {
@@ -363,21 +360,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     // lane -> (page of the tile, column half) of one box
     const int pg = lane / C::kHalves, half = lane % C::kHalves;
     const bool mine = lane < ppt * C::kHalves;
-    uint32_t at = 0, q_uses[2] = {0, 0}, alt = 0;
-    int idx = blockIdx.x;
+    uint32_t at = 0, alt = 0;
+    uint32_t q_used = 0, q_phase = 0;  // bit s: slot s has been used; the phase of its release
     bool ok = true;
-    for (uint32_t seq = 0; ok; ++seq) {
+    Cursor cursor = start_cursor(a, &sh.plan);  // lane 0's counts
+    // decode item `seq` into the ring (the number of the item after it, asked for
+    // on the way, is there by the next call)
+    auto prepare = [&](uint32_t seq) {
       const int slot = seq % kItems;
       if (seq >= kItems &&
-          !__all_sync(0xffffffffu, wait(&sh.item_empty[slot], ((seq / kItems) & 1) ^ 1, 1u)))
-        break;
-      if (lane == 0) sh.items[slot] = decode_item(a, &sh.plan, idx);
+          !wait_all(&sh.item_empty[slot], ((seq / kItems) & 1) ^ 1, 1u))
+        return false;
+      if (lane == 0) sh.items[slot] = next_item(a, &sh.plan, &cursor);
       __syncwarp();
-      const Item& it = sh.items[slot];
       if (lane == 0) mbar_arrive(smem_u32(&sh.item_full[slot]));
+      return true;
+    };
+    ok = prepare(0);
+    for (uint32_t seq = 0; ok; ++seq) {
+      const Item& it = sh.items[seq % kItems];
       if (!it.valid) break;
-      int next = 0;
-      if (lane == 0) next = next_item(a);  // arrives while this item's copies go out
       const Run r = run_of(it, tt);
       // the pool row of this lane's box of key tile j
       auto lookup = [&](int j) {
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto load = [&](bool v, int j, int row) {
         const uint32_t x = at + (v ? pos_v(r, j, it.nk) : pos_k(r, j));
         const int s = x % NS;
-        if (x >= NS && !__all_sync(0xffffffffu, wait(&sh.empty[s], ((x / NS) & 1) ^ 1, 2u))) return false;
+        if (x >= NS && !wait_all(&sh.empty[s], ((x / NS) & 1) ^ 1, 2u)) return false;
         const uint32_t bar = smem_u32(&sh.full[s]), dst = ring + s * C::kTile;
         const bool drafts = it.draft && j == it.nk - 1;
         if (lane == 0) mbar_arrive_expect_tx(bar, drafts ? C::kTile / 2 : C::kTile);
@@ -415,11 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Q: both slots (pair), or the slots in turn
         for (int s = 0; s < 2 && ok; ++s) {
           if (!r.pair && s != (int)(alt & 1)) continue;
-          if (q_uses[s] && !__all_sync(0xffffffffu, wait(&sh.q_empty[s], (q_uses[s] - 1) & 1, 3u))) {
-            ok = false;
-            break;
+          if (q_used >> s & 1) {
+            if (!(ok = wait_all(&sh.q_empty[s], q_phase >> s & 1, 3u))) break;
+            q_phase ^= 1u << s;
           }
-          ++q_uses[s];
+          q_used |= 1u << s;
           const uint32_t bar = smem_u32(&sh.q_full[s]);
           if (lane == 0) mbar_arrive_expect_tx(bar, C::kHalves * tt * a.gs * 128);
           __syncwarp();
@@ -430,6 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!r.pair) ++alt;
         if (ok && !r.pair) ok = load(false, 0, row0);
         for (int j = 0; j < it.nk && ok; ++j) {
+          // the next item is decoded while the ring is full of this one's tiles
+          if (j == 2 && !(ok = prepare(seq + 1))) break;
           const int row2 = lookup(j + 2);
           ok = r.pair ? load(false, j, row0) : j + 1 >= it.nk || load(false, j + 1, row1);
           ok = ok && load(true, j, row0);
@@ -438,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         at += 2 * it.nk;
       }
-      idx = __shfl_sync(0xffffffffu, next, 0);
+      if (ok && it.nk <= 2) ok = prepare(seq + 1);
     }
     // never leave with a copy still in flight
     __syncwarp();
@@ -456,7 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dq0 = tc::smem_desc(q_base, 16, 1024);
     const uint64_t dk0 = tc::smem_desc(ring, 16, 1024);
     const uint64_t dv0 = tc::smem_desc(ring, kBox, 1024);
-    uint32_t at = 0, q_uses[2] = {0, 0}, alt = 0, p_uses[2] = {0, 0};
+    uint32_t at = 0, alt = 0;
+    uint32_t q_phase = 0, p_phase = 0;  // bit s: the next phase of slot (set) s
     const uint32_t lead = elect_lead();
     bool ok = true;
     for (uint32_t seq = 0; ok && take_item(seq); ++seq) {
@@ -466,10 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nk > 0) {
         auto stage = [&](uint32_t pos) { return (at + pos) % NS; };
         auto phase = [&](uint32_t pos) { return ((at + pos) / NS) & 1; };
-        auto k_wait = [&](int j) { return poll_all(&sh.full[stage(pos_k(r, j))], phase(pos_k(r, j)), 4u); };
+        auto k_wait = [&](int j) { return wait_all(&sh.full[stage(pos_k(r, j))], phase(pos_k(r, j)), 4u); };
         auto v_wait = [&](int j) {
           const uint32_t p = pos_v(r, j, nk);
-          return poll_all(&sh.vclean[stage(p)], phase(p), 5u);
+          return wait_all(&sh.vclean[stage(p)], phase(p), 5u);
         };
         auto issue_s = [&](int s, int qs, int j) {
           tc::fence_after();
@@ -484,14 +489,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // O += P V as the halves of P get ready
         auto issue_o = [&](int s, int j, bool first) {
-          if (!poll_all(&sh.p_ready[s][0], p_uses[s] & 1, 6u)) return false;
+          if (!wait_all(&sh.p_ready[s][0], p_phase >> s & 1, 6u)) return false;
           tc::fence_after();
           const uint64_t dv = dv0 + (uint64_t)(stage(pos_v(r, j, nk)) * (C::kTile >> 4));
 #pragma unroll
           for (int kk = 0; kk < kKeys / 32; ++kk)
             lead_mma_ts(lead, tmem + col_o(s), tmem + col_s(s) + kk * 8, dv + (uint64_t)((kk * 2048) >> 4),
                        id_o, !first || kk > 0 ? 1u : 0u);
-          if (!poll_all(&sh.p_ready[s][1], p_uses[s]++ & 1, 12u)) return false;
+          if (!wait_all(&sh.p_ready[s][1], p_phase >> s & 1, 12u)) return false;
+          p_phase ^= 1u << s;
           tc::fence_after();
 #pragma unroll
           for (int kk = kKeys / 32; kk < kKeys / 16; ++kk)
@@ -502,8 +508,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto free_k = [&](int j) { lead_commit(lead, smem_u32(&sh.empty[stage(pos_k(r, j))])); };
         auto free_v = [&](int j) { lead_commit(lead, smem_u32(&sh.empty[stage(pos_v(r, j, nk))])); };
         if (r.pair) {
-          ok = poll_all(&sh.q_full[0], q_uses[0]++ & 1, 7u) && poll_all(&sh.q_full[1], q_uses[1]++ & 1, 7u) &&
+          ok = wait_all(&sh.q_full[0], q_phase & 1, 7u) && wait_all(&sh.q_full[1], q_phase >> 1 & 1, 7u) &&
                k_wait(0);
+          q_phase ^= 3u;
           if (ok) {
             if (r.n[0] > 0) issue_s(0, 0, 0);
             issue_s(1, 1, 0);
@@ -536,7 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           const int qs = alt++ & 1;
-          ok = poll_all(&sh.q_full[qs], q_uses[qs]++ & 1, 7u) && k_wait(0);
+          ok = wait_all(&sh.q_full[qs], q_phase >> qs & 1, 7u) && k_wait(0);
+          q_phase ^= 1u << qs;
           if (ok) {
             issue_s(0, qs, 0);
             free_k(0);
@@ -581,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int pos = 0; pos < 2 * nk; ++pos) {
         const uint32_t x = at + pos;
         const int s = x % NS;
-        if (!(ok = __all_sync(0xffffffffu, wait(&sh.full[s], (x / NS) & 1, 8u)))) break;
+        if (!(ok = wait_all(&sh.full[s], (x / NS) & 1, 8u))) break;
         const int j = v_at(r, pos, nk);
         if (j >= r.masked) {
           uint8_t* v = smem + 2 * C::kTile + s * C::kTile;
@@ -615,22 +623,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_grow<kRegsSoftmax>();
     const int X = warp >> 3, H = warp >> 2 & 1, q4 = warp & 3, r = 32 * q4 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
-    const uint32_t tS = lane_base + col_s(X) + 64 * H, tP = tS;
+    const uint32_t tS = lane_base + col_s(X) + 64 * H;
     const uint32_t tO = lane_base + col_o(X) + D / 2 * H;
     const int rt = r / a.gs, rg = r % a.gs;  // token of the set and head of the group
-    uint32_t s_uses = 0, o_uses = 0, h_uses = 0, meets = 0, parts = 0;
+    uint32_t s_uses = 0, o_uses = 0, h_uses = 0, meets = 0;
     bool ok = true;
     // all softmax warps meet
     auto meet = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.meet));
-      return __all_sync(0xffffffffu, poll(&sh.meet, meets++ & 1, 9u)) != 0;
+      return wait_all(&sh.meet, meets++ & 1, 9u);
     };
     // the two warps of this set's rows meet
-    auto meet_half = [&]() {
+    auto half_arrive = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.halves[X][q4]));
-      return __all_sync(0xffffffffu, poll(&sh.halves[X][q4], h_uses++ & 1, 13u)) != 0;
+    };
+    auto half_wait = [&]() {
+      return wait_all(&sh.halves[X][q4], h_uses++ & 1, 13u);
+    };
+    auto meet_half = [&]() {
+      half_arrive();
+      return half_wait();
     };
     for (uint32_t seq = 0; ok && take_item(seq); ++seq) {
       const Item& it = sh.items[seq % kItems];
@@ -646,52 +660,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int vis_set = (it.causal ? it.vis0 + off : it.ctx) - it.k0 * kKeys - 64 * H;
       const int draft_tile = it.draft ? it.nk - 1 : -1;
       const int stride = run.pair ? 1 : 2, first = run.pair ? 0 : X;
-      float m_run = -INFINITY, m_next = -INFINITY, l_run = 0.f;
-      // move the row's reference to m: O (this thread's half of its columns) and
-      // the sum so far follow
-      auto rescale = [&](float m) {
-        const float alpha = m == -INFINITY ? 1.f : exp2f(m_run - m);
-#pragma unroll 1
-        for (int c = 0; c < D / 2; c += 16) {
-          uint32_t o[16];
-          tc::ld16(tO + c, o);
-          tc::wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tc::st16(tO + c, o);
-        }
-        l_run *= alpha;
-        m_run = m;
-      };
-      // P = 2^(s - m) of this thread's 64 keys into TMEM, and its sum
-      auto exponentials = [&](const uint32_t(&v)[2][32]) {
-        const float nb = m_run == -INFINITY ? 0.f : -m_run;
-        const uint64_t nb2 = pack2(nb, nb), sc2 = pack2(a.scale_log2, a.scale_log2);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t* s16 = v[c >> 1] + 16 * (c & 1);
-          uint32_t p[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 e = unpack2(
-                fma2(pack2(__uint_as_float(s16[2 * i]), __uint_as_float(s16[2 * i + 1])), sc2, nb2));
-            const float x = exp2f(e.x), y = exp2f(e.y);
-            sum[i & 1] = add2(sum[i & 1], pack2(x, y));
-            p[i] = pack_bf16(x, y);
-          }
-          tc::st8(tP + 8 * c, p);
-        }
-        return add2(sum[0], sum[1]);
-      };
+      float m_run = -INFINITY, l_run = 0.f;
+      float m_next = -INFINITY;  // what the row's reference m_run moves to before the next exponentials
       for (int j = 0; j < n; ++j) {
         const int kt = first + stride * j;
-        if (!(ok = __all_sync(0xffffffffu, poll(&sh.s_full[X], s_uses++ & 1, 10u)))) break;
+        if (!(ok = wait_all(&sh.s_full[X], s_uses++ & 1, 10u))) break;
         if (live) {
           tc::fence_after();
-          uint32_t v[2][32];
-          tc::ld32(tS, v[0]);
-          tc::ld32(tS + 32, v[1]);
+          uint32_t v[64];
+          ld32_at(tS, v);
+          ld32_at(tS + 32, v + 32);
           tc::wait_ld();
           if (kt == draft_tile || kt * kKeys + 64 > vis_set) {
             uint32_t keep[2];  // keys of this half that the row sees
@@ -705,47 +683,92 @@ __global__ void __launch_bounds__(kThreads, 1)
               keep[1] = lim >= 64 ? 0xffffffffu : lim <= 32 ? 0u : (1u << (lim - 32)) - 1u;
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (!(keep[0] >> i & 1u)) v[0][i] = 0xff800000u;  // -inf
-              if (!(keep[1] >> i & 1u)) v[1][i] = 0xff800000u;
-            }
+            for (int i = 0; i < 64; ++i)
+              if (!(keep[i >> 5] >> (i & 31) & 1u)) v[i] = 0xff800000u;  // -inf
           }
-          // The row's maximum over all tiles before this one is m_next: the
-          // exponentials need not wait for this tile's own. P may then exceed
-          // 1, but what it exceeds by only moves exponents. In an item's first
-          // tile, and where a row's maximum grows by more than 2^64 in one
-          // tile (a row that has seen nothing so far among them), this tile's
-          // maximum is taken first.
-          if (j > 0 && __any_sync(0xffffffffu, m_next > m_run)) {
-            // S of this tile was issued behind the set's previous P V, so that
-            // product is complete and O may be rescaled
-            rescale(m_next);
-          }
-          uint64_t sum = 0;
-          if (j > 0) sum = exponentials(v);
           float mx[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint32_t* x = v[c >> 1] + 16 * (c & 1);
-            mx[c] = __uint_as_float(x[0]);
+            mx[c] = __uint_as_float(v[16 * c]);
 #pragma unroll
             for (int i = 1; i < 15; i += 2)
-              mx[c] = max3(mx[c], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-            mx[c] = fmaxf(mx[c], __uint_as_float(x[15]));
+              mx[c] = max3(mx[c], __uint_as_float(v[16 * c + i]), __uint_as_float(v[16 * c + i + 1]));
+            mx[c] = fmaxf(mx[c], __uint_as_float(v[16 * c + 15]));
           }
           const float mine = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
           sh.mx[X][H][r] = mine;
-          if (!(ok = meet_half())) break;
-          const float mrow = fmaxf(mine, sh.mx[X][H ^ 1][r]) * a.scale_log2;
-          if (j == 0) {
-            m_run = mrow;
-            sum = exponentials(v);
-          } else if (__any_sync(0xffffffffu, mrow > m_run + kRedoLog2)) {
-            rescale(fmaxf(m_run, mrow));
-            sum = exponentials(v);
+          half_arrive();
+          // The exponentials take the maximum of the tiles before (m_run) and need
+          // not wait for the other half's. P may then exceed 1, but what it exceeds
+          // by only moves exponents. In an item's first tile, and where a row's
+          // maximum grows by more than 2^64 in one tile (a row that has seen nothing
+          // so far among them), they are (re)done with this tile's maximum.
+          bool waited = j == 0 || __any_sync(0xffffffffu, m_next > m_run), again;
+          if (waited) {
+            if (!(ok = half_wait())) break;
+            const float mrow = fmaxf(mine, sh.mx[X][H ^ 1][r]) * a.scale_log2;
+            m_next = fmaxf(m_next, mrow);
+            if (j == 0) m_run = m_next;
           }
-          m_next = mrow > m_run + kRescaleLog2 ? mrow : m_run;
-          const float2 s2 = unpack2(sum);
+          uint64_t sum[2];
+          do {
+            if (__any_sync(0xffffffffu, m_next > m_run)) {
+              // move the row's reference: O (this thread's half of its columns) and
+              // the sum so far follow. S of this tile was issued behind the set's
+              // previous P V, so that product is complete.
+              const float alpha = m_next == -INFINITY ? 1.f : ex2(m_run - m_next);
+#pragma unroll 1
+              for (int c = 0; c < D / 2; c += 8) {
+                uint32_t o[8];
+                ld8_at(tO + c, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tc::st8(tO + c, o);
+              }
+              l_run *= alpha;
+              m_run = m_next;
+              // the first half's P starts the next product, which adds to all of O:
+              // both halves have to have rescaled theirs (they decide alike)
+              tc::wait_st();
+              tc::fence_before();
+              if (!(ok = meet_half())) break;
+            }
+            // P = 2^(s - m) into TMEM, 16 keys at a time, and its sum
+            const float nb = m_run == -INFINITY ? 0.f : -m_run;
+            sum[0] = sum[1] = 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint64_t e[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                e[i] = fma2(pack2(__uint_as_float(v[16 * c + 2 * i]), __uint_as_float(v[16 * c + 2 * i + 1])),
+                            pack2(a.scale_log2, a.scale_log2), pack2(nb, nb));
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 x = unpack2(e[i]);
+                e[i] = pack2(ex2(x.x), ex2(x.y));
+              }
+              uint32_t p[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 x = unpack2(e[i]);
+                p[i] = pack_bf16(x.x, x.y);
+                sum[i & 1] = add2(sum[i & 1], e[i]);
+              }
+              tc::st8(tS + 8 * c, p);
+            }
+            again = false;
+            if (!waited) {
+              if (!(ok = half_wait())) break;
+              waited = true;
+              const float mrow = fmaxf(mine, sh.mx[X][H ^ 1][r]) * a.scale_log2;
+              again = __any_sync(0xffffffffu, mrow > m_run + kRedoLog2);
+              m_next = mrow > m_run + (again ? 0.f : kRescaleLog2) ? mrow : m_run;
+            }
+          } while (again);
+          if (!ok) break;
+          const float2 s2 = unpack2(add2(sum[0], sum[1]));
           l_run += s2.x + s2.y;
           tc::wait_st();
           tc::fence_before();
@@ -756,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // ---------------------------------------------------------- results
       if (n > 0) {
-        if (!(ok = __all_sync(0xffffffffu, poll(&sh.o_done[X], o_uses++ & 1, 11u)))) break;
+        if (!(ok = wait_all(&sh.o_done[X], o_uses++ & 1, 11u))) break;
         tc::fence_after();
       }
       // the row's maximum and sum over both halves (and, alternating, both sets)
@@ -807,21 +830,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 16; ++e) f[e] += w[1] != 0.f ? w[1] * __uint_as_float(o[e]) : 0.f;
           }
           if (!valid) continue;
+          uint32_t x[16];
           if (it.part < 0) {
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
                                  ((size_t)(it.tok0 + tok) * a.Hq + it.head0 + rg) * a.d + c;
 #pragma unroll
-            for (int e = 0; e < 16; e += 8)
-              if (c + e < a.d)
-                *reinterpret_cast<uint4*>(dst + e) =
-                    make_uint4(pack_bf16(f[e] * inv, f[e + 1] * inv), pack_bf16(f[e + 2] * inv, f[e + 3] * inv),
-                               pack_bf16(f[e + 4] * inv, f[e + 5] * inv), pack_bf16(f[e + 6] * inv, f[e + 7] * inv));
+            for (int e = 0; e < 8; ++e) x[e] = pack_bf16(f[2 * e] * inv, f[2 * e + 1] * inv);
+            if (a.out_wide) {  // d is a multiple of 16
+              if (c < a.d) store32(dst, x);
+            } else {
+              if (c < a.d) *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+              if (c + 8 < a.d) *reinterpret_cast<uint4*>(dst + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+            }
           } else {
-            float* dst = a.part_o + prow * a.d + c;
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              if (c + e < a.d)
-                *reinterpret_cast<float4*>(dst + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(f[e]);
+            float* dst = a.part_o + prow * a.d + c;
+            if (c < a.d) store32(dst, x);
+            if (c + 8 < a.d) store32(dst + 8, x + 8);
           }
         }
         if (any_nf && valid)
@@ -834,20 +860,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (valid && it.part >= 0 && H == 0 && (run.pair || X == 0)) a.part_ml[prow] = make_float2(m_out, l_out);
       }
       tc::fence_before();  // O is read: the next item's products may overwrite it
-      if (it.part >= 0 && !a.prefix) {
-        __threadfence();
-        if (!(ok = meet())) break;
-        const int pp = parts++ & 1;
-        if (threadIdx.x == 0) sh.last[pp] = arrive_unit(a, it);
-        if (!(ok = meet())) break;
-        if (sh.last[pp]) {
-          __threadfence();
-          merge_unit<__nv_bfloat16>(a, it, warp, 16);
-        }
-      } else {
-        // both halves (pair) or all warps (alternating) have read sums and O
-        if (!(ok = run.pair ? meet_half() : meet())) break;
-      }
+      // both halves (pair) or all warps (alternating) have read sums and O
+      if (!(ok = run.pair ? meet_half() : meet())) break;
       done_item(seq);
     }
   }
@@ -883,7 +897,7 @@ cudaError_t launch_cfg(PagedArgs a, const CUtensorMap* m, cudaStream_t st) {
   a.ctas = std::min(sm_count(), kMaxTcCtas);
   const cudaError_t e = launch_pdl(paged_tc_kernel<D>, dim3(a.ctas), dim3(kThreads), Cfg<D>::kSmem, st,
                                    m[0], m[1], m[2], m[3], m[4], a);
-  return e == cudaSuccess && a.prefix ? launch_prefix_merge(a, SV_BF16, st) : e;
+  return e == cudaSuccess ? launch_paged_merge(a, SV_BF16, st) : e;
 }
 
 }  // namespace
@@ -897,15 +911,11 @@ bool paged_tc_applies(const PagedArgs& a, int dtype) {
 
 cudaError_t launch_paged_tc(PagedArgs a, cudaStream_t st) {
   paged_heads(&a, kRows);
-#ifndef PER_CTA_PROMPT
-#define PER_CTA_PROMPT 2
-#define PER_CTA_PREFIX 2
-#define MIN_RUN 2
-#endif
-  a.per_cta = a.prefix ? PER_CTA_PREFIX : PER_CTA_PROMPT;
-  a.min_run = MIN_RUN;
-  a.tile = 2 * (kRows / a.gs);
-  a.keys = kKeys;
+  a.min_run = 2;
+  a.one_set = kRows / a.gs;
+  a.tile = 2 * a.one_set;
+  a.key_shift = 7;
+  a.out_wide = a.d % 16 == 0 && aligned(a.out, 32);
   CUtensorMap m[5];
   const cuuint64_t d = a.d, hd = (cuuint64_t)a.Hkv * a.d;
   {

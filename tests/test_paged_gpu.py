@@ -281,6 +281,24 @@ def test_prompt_large_scores():
         P.check(c["out"], *prompt_want(c, [700, 300], [700, 1]))
 
 
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 128), (4, 4, 64), (16, 1, 128)])
+def test_prompt_growing_scores(Hq, Hkv, d):
+    """Keys that grow along the context: the running maximum of most rows moves
+    by several powers of two in most key tiles, so that every tile rescales."""
+    ctx, new = [4000, 2500], [1500, 2500]
+    c = prompt_case(14, BF16, Hq, Hkv, d, 64, ctx, new, hole=0.0)
+    for b, n in enumerate(ctx):
+        i = torch.arange(n, device="cuda")
+        page = c["block_table"][b].long()[i // 64]
+        c["k_pool"][page, :, i % 64] *= (1 + i / 60)[:, None, None]
+    want, tol = prompt_want(c, ctx, new)
+    ws = api.alloc_prompt_workspace(c["shape"], sum(new))
+    for _ in range(5):
+        c["out"].fill_(7.0)
+        assert run_prompt(c, ws) == 0
+        P.check(c["out"], want, tol)
+
+
 def test_prompt_bad_pages_and_offsets():
     c = prompt_case(15, BF16, 4, 2, 128, 64, [200, 100], [200, 100])
     c["block_table"][0, 1] = 99
