@@ -54,7 +54,7 @@ constexpr int kItems = 4;             // item ring
 constexpr int kItemReaders = 19;      // MMA, 16 softmax and 2 cleaning warps
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;   // O follows the maximum in steps of more than 2^8
-constexpr float kRedoLog2 = 64.0f;
+constexpr float kFixLog2 = 64.0f;
 constexpr int kMaxMasked = 4;         // masked key tiles of an item, at most 3 (see masked_from)
 // registers per thread of the softmax warps and of the others (the launch
 // gives 96 to each of 640 threads: 512 * 104 + 128 * 64 = 640 * 96)
@@ -75,14 +75,14 @@ struct Cfg {
 
 struct Control {
   uint64_t full[8], empty[8], vclean[8];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_done[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_done[2];
   uint64_t halves[2][4];  // the two warps of a set's lane quarter
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t meet, drained;
   uint32_t tmem;
   int abort;
   uint32_t nonfinite[kItems][kMaxMasked][4];  // keys of an item's masked tiles, from the last
-  float mx[2][2][kRows];   // a tile's maxima by set and half
+  float mx[2][2][2][kRows];  // maxima of even and odd tiles by set and half
   float2 ml[2][2][kRows];  // maximum and sum by set and half
   unsigned long long anc[kMaxT];
   Item items[kItems];
@@ -215,6 +215,64 @@ __device__ __forceinline__ void ld8_at(uint32_t taddr, uint32_t* r) {
                : "memory");
 }
 
+// The largest of 64 scores.
+__device__ __forceinline__ float max64(const uint32_t (&v)[64]) {
+  float mx[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    mx[c] = __uint_as_float(v[16 * c]);
+#pragma unroll
+    for (int i = 1; i < 15; i += 2)
+      mx[c] = max3(mx[c], __uint_as_float(v[16 * c + i]), __uint_as_float(v[16 * c + i + 1]));
+    mx[c] = fmaxf(mx[c], __uint_as_float(v[16 * c + 15]));
+  }
+  return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+}
+
+// P = 2^(s - m) of 64 keys into 32 columns of TMEM at taddr, and its sum (even
+// and odd keys apart).
+__device__ __forceinline__ uint64_t exponentials(const uint32_t (&v)[64], uint32_t taddr, float m,
+                                                 float scale) {
+  const float nb = m == -INFINITY ? 0.f : -m;
+  uint64_t sum[2] = {0, 0};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint64_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      e[i] = fma2(pack2(__uint_as_float(v[16 * c + 2 * i]), __uint_as_float(v[16 * c + 2 * i + 1])),
+                  pack2(scale, scale), pack2(nb, nb));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 x = unpack2(e[i]);
+      e[i] = pack2(ex2(x.x), ex2(x.y));
+    }
+    uint32_t p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 x = unpack2(e[i]);
+      p[i] = pack_bf16(x.x, x.y);
+      sum[i & 1] = add2(sum[i & 1], e[i]);
+    }
+    tc::st8(taddr + 8 * c, p);
+  }
+  return add2(sum[0], sum[1]);
+}
+
+// 64 keys of P in TMEM times alpha.
+__device__ __noinline__ void scale_p(uint32_t taddr, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < 32; c += 8) {
+    uint32_t p[8];
+    ld8_at(taddr + c, p);
+    tc::wait_ld();
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      p[e] = pack_bf16(__uint_as_float(p[e] << 16) * alpha, __uint_as_float(p[e] & 0xffff0000u) * alpha);
+    tc::st8(taddr + c, p);
+  }
+}
+
 // 32 bytes (a whole sector) to a 32-byte boundary.
 __device__ __forceinline__ void store32(void* p, const uint32_t* x) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]),
@@ -307,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sh.q_full[i]), 1);
       mbar_init(smem_u32(&sh.q_empty[i]), 1);
       mbar_init(smem_u32(&sh.s_full[i]), 1);
-      for (int h = 0; h < 2; ++h) mbar_init(smem_u32(&sh.p_ready[i][h]), 4);
+      mbar_init(smem_u32(&sh.p_ready[i]), 8);
       for (int q = 0; q < 4; ++q) mbar_init(smem_u32(&sh.halves[i][q]), 2);
       mbar_init(smem_u32(&sh.o_done[i]), 1);
     }
@@ -487,22 +545,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           lead_commit(lead, smem_u32(&sh.s_full[s]));
         };
-        // O += P V as the halves of P get ready
+        // O += P V, once both halves of P (and of O, if it was rescaled) are ready
         auto issue_o = [&](int s, int j, bool first) {
-          if (!wait_all(&sh.p_ready[s][0], p_phase >> s & 1, 6u)) return false;
+          if (!wait_all(&sh.p_ready[s], p_phase >> s & 1, 6u)) return false;
+          p_phase ^= 1u << s;
           tc::fence_after();
           const uint64_t dv = dv0 + (uint64_t)(stage(pos_v(r, j, nk)) * (C::kTile >> 4));
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 32; ++kk)
-            lead_mma_ts(lead, tmem + col_o(s), tmem + col_s(s) + kk * 8, dv + (uint64_t)((kk * 2048) >> 4),
-                       id_o, !first || kk > 0 ? 1u : 0u);
-          if (!wait_all(&sh.p_ready[s][1], p_phase >> s & 1, 12u)) return false;
-          p_phase ^= 1u << s;
-          tc::fence_after();
-#pragma unroll
-          for (int kk = kKeys / 32; kk < kKeys / 16; ++kk)
-            lead_mma_ts(lead, tmem + col_o(s), tmem + col_s(s) + 32 + kk * 8, dv + (uint64_t)((kk * 2048) >> 4),
-                       id_o, 1u);
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            lead_mma_ts(lead, tmem + col_o(s), tmem + col_s(s) + (kk >> 2) * 64 + (kk & 3) * 8,
+                        dv + (uint64_t)((kk * 2048) >> 4), id_o, !first || kk > 0 ? 1u : 0u);
           return true;
         };
         auto free_k = [&](int j) { lead_commit(lead, smem_u32(&sh.empty[stage(pos_k(r, j))])); };
@@ -624,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int X = warp >> 3, H = warp >> 2 & 1, q4 = warp & 3, r = 32 * q4 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
     const uint32_t tS = lane_base + col_s(X) + 64 * H;
-    const uint32_t tO = lane_base + col_o(X) + D / 2 * H;
+    const uint32_t tO = lane_base + col_o(X);
     const int rt = r / a.gs, rg = r % a.gs;  // token of the set and head of the group
     uint32_t s_uses = 0, o_uses = 0, h_uses = 0, meets = 0;
     bool ok = true;
@@ -660,17 +712,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int vis_set = (it.causal ? it.vis0 + off : it.ctx) - it.k0 * kKeys - 64 * H;
       const int draft_tile = it.draft ? it.nk - 1 : -1;
       const int stride = run.pair ? 1 : 2, first = run.pair ? 0 : X;
-      float m_run = -INFINITY, l_run = 0.f;
-      float m_next = -INFINITY;  // what the row's reference m_run moves to before the next exponentials
+      float m_run = -INFINITY, l_run = 0.f, mine = -INFINITY;
+      // columns [c0, c1) of the row's O times alpha; all products into O are complete
+      auto scale_o = [&](int c0, int c1, float alpha) {
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 8) {
+          uint32_t o[8];
+          ld8_at(tO + c, o);
+          tc::wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tc::st8(tO + c, o);
+        }
+      };
+      // move the row's reference to m; alpha: what its sum and O are multiplied by
+      auto move_ref = [&](float m) {
+        const float alpha = m == -INFINITY ? 1.f : ex2(m_run - m);
+        l_run *= alpha;
+        m_run = m;
+        return alpha;
+      };
+      // The two threads of a row agree on its reference without waiting for each
+      // other: exponentials take what both knew of the tiles before (their maxima
+      // lie in sh.mx), so P may exceed 1, but what it exceeds by only moves
+      // exponents. When one of them finds a maximum more than 2^kFixLog2 above the
+      // reference, its warp moves it at once for both halves; the other half
+      // recognises that in the next tile, by the same comparison.
+      auto catch_up = [&](float other) {  // the other half's maximum of the last tile
+        if (__any_sync(0xffffffffu, other > m_run + kFixLog2)) move_ref(fmaxf(m_run, fmaxf(mine, other)));
+      };
       for (int j = 0; j < n; ++j) {
         const int kt = first + stride * j;
         if (!(ok = wait_all(&sh.s_full[X], s_uses++ & 1, 10u))) break;
         if (live) {
           tc::fence_after();
+          const float other = j > 0 ? sh.mx[(j - 1) & 1][X][H ^ 1][r] : -INFINITY;
           uint32_t v[64];
-          ld32_at(tS, v);
+          ld32_at(tS, v);  // (nothing may touch v before the wait)
           ld32_at(tS + 32, v + 32);
           tc::wait_ld();
+          if (j > 0) {
+            // O follows the maximum in steps of more than 2^kRescaleLog2, each half its
+            // columns: S of this tile was issued behind the P V of the last
+            catch_up(other);
+            const float both = fmaxf(mine, other);
+            if (__any_sync(0xffffffffu, both > m_run + kRescaleLog2))
+              scale_o(D / 2 * H, D / 2 * H + D / 2, move_ref(fmaxf(m_run, both)));
+          }
           if (kt == draft_tile || kt * kKeys + 64 > vis_set) {
             uint32_t keep[2];  // keys of this half that the row sees
             if (kt == draft_tile) {  // drafts 0..63: all in the first half
@@ -686,95 +774,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 64; ++i)
               if (!(keep[i >> 5] >> (i & 31) & 1u)) v[i] = 0xff800000u;  // -inf
           }
-          float mx[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            mx[c] = __uint_as_float(v[16 * c]);
-#pragma unroll
-            for (int i = 1; i < 15; i += 2)
-              mx[c] = max3(mx[c], __uint_as_float(v[16 * c + i]), __uint_as_float(v[16 * c + i + 1]));
-            mx[c] = fmaxf(mx[c], __uint_as_float(v[16 * c + 15]));
+          if (j == 0) {
+            mine = max64(v) * a.scale_log2;
+            sh.mx[0][X][H][r] = mine;
+            if (!(ok = meet_half())) break;
+            m_run = fmaxf(mine, sh.mx[0][X][H ^ 1][r]);
           }
-          const float mine = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-          sh.mx[X][H][r] = mine;
-          half_arrive();
-          // The exponentials take the maximum of the tiles before (m_run) and need
-          // not wait for the other half's. P may then exceed 1, but what it exceeds
-          // by only moves exponents. In an item's first tile, and where a row's
-          // maximum grows by more than 2^64 in one tile (a row that has seen nothing
-          // so far among them), they are (re)done with this tile's maximum.
-          bool waited = j == 0 || __any_sync(0xffffffffu, m_next > m_run), again;
-          if (waited) {
-            if (!(ok = half_wait())) break;
-            const float mrow = fmaxf(mine, sh.mx[X][H ^ 1][r]) * a.scale_log2;
-            m_next = fmaxf(m_next, mrow);
-            if (j == 0) m_run = m_next;
-          }
-          uint64_t sum[2];
-          do {
-            if (__any_sync(0xffffffffu, m_next > m_run)) {
-              // move the row's reference: O (this thread's half of its columns) and
-              // the sum so far follow. S of this tile was issued behind the set's
-              // previous P V, so that product is complete.
-              const float alpha = m_next == -INFINITY ? 1.f : ex2(m_run - m_next);
-#pragma unroll 1
-              for (int c = 0; c < D / 2; c += 8) {
-                uint32_t o[8];
-                ld8_at(tO + c, o);
-                tc::wait_ld();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                tc::st8(tO + c, o);
-              }
-              l_run *= alpha;
-              m_run = m_next;
-              // the first half's P starts the next product, which adds to all of O:
-              // both halves have to have rescaled theirs (they decide alike)
-              tc::wait_st();
-              tc::fence_before();
-              if (!(ok = meet_half())) break;
-            }
-            // P = 2^(s - m) into TMEM, 16 keys at a time, and its sum
-            const float nb = m_run == -INFINITY ? 0.f : -m_run;
-            sum[0] = sum[1] = 0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint64_t e[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                e[i] = fma2(pack2(__uint_as_float(v[16 * c + 2 * i]), __uint_as_float(v[16 * c + 2 * i + 1])),
-                            pack2(a.scale_log2, a.scale_log2), pack2(nb, nb));
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 x = unpack2(e[i]);
-                e[i] = pack2(ex2(x.x), ex2(x.y));
-              }
-              uint32_t p[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 x = unpack2(e[i]);
-                p[i] = pack_bf16(x.x, x.y);
-                sum[i & 1] = add2(sum[i & 1], e[i]);
-              }
-              tc::st8(tS + 8 * c, p);
-            }
-            again = false;
-            if (!waited) {
+          uint64_t sum = exponentials(v, tS, m_run, a.scale_log2);
+          if (j > 0) {
+            mine = max64(v) * a.scale_log2;
+            sh.mx[j & 1][X][H][r] = mine;
+            const bool fix = __any_sync(0xffffffffu, mine > m_run + kFixLog2);
+            tc::wait_st();
+            tc::fence_before();
+            half_arrive();  // P is written; or, on a fix, it will be
+            ++h_uses;
+            if (fix) {
+              --h_uses;
               if (!(ok = half_wait())) break;
-              waited = true;
-              const float mrow = fmaxf(mine, sh.mx[X][H ^ 1][r]) * a.scale_log2;
-              again = __any_sync(0xffffffffu, mrow > m_run + kRedoLog2);
-              m_next = mrow > m_run + (again ? 0.f : kRescaleLog2) ? mrow : m_run;
+              tc::fence_after();
+              const float other = sh.mx[j & 1][X][H ^ 1][r];
+              const bool alone = !__any_sync(0xffffffffu, other > m_run + kFixLog2);
+              const float alpha = move_ref(fmaxf(m_run, fmaxf(mine, other)));
+              // alone: the other half's P is written, against the old reference
+              scale_o(alone ? 0 : D / 2 * H, alone ? D : D / 2 * H + D / 2, alpha);
+              if (alone) scale_p(lane_base + col_s(X) + 64 * (H ^ 1), alpha);
+              sum = exponentials(v, tS, m_run, a.scale_log2);
             }
-          } while (again);
-          if (!ok) break;
-          const float2 s2 = unpack2(add2(sum[0], sum[1]));
+          }
+          const float2 s2 = unpack2(sum);
           l_run += s2.x + s2.y;
           tc::wait_st();
           tc::fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[X][H]));
+        if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[X]));
       }
       if (!ok) break;
       // ---------------------------------------------------------- results
@@ -782,6 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_all(&sh.o_done[X], o_uses++ & 1, 11u))) break;
         tc::fence_after();
       }
+      if (live && n > 0) catch_up(sh.mx[(n - 1) & 1][X][H ^ 1][r]);
       // the row's maximum and sum over both halves (and, alternating, both sets)
       float w[2] = {X ? 0.f : 1.f, X ? 1.f : 0.f}, m_out = m_run, l_out = l_run;
       sh.ml[X][H][r] = make_float2(m_run, l_run);

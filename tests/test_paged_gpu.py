@@ -299,6 +299,27 @@ def test_prompt_growing_scores(Hq, Hkv, d):
         P.check(c["out"], want, tol)
 
 
+@pytest.mark.parametrize("jump", [30.0, 300.0])
+def test_prompt_jumping_scores(jump):
+    """Scores that jump by more than 2^64 inside a key tile, in the first or the
+    second half of its keys, in both, for some rows only, up and down."""
+    ctx = [1500]
+    for Hq, Hkv, d in ((4, 1, 128), (2, 2, 64)):
+        c = prompt_case(16, BF16, Hq, Hkv, d, 64, ctx, ctx, hole=0.0)
+        t = c["block_table"][0].long()
+        u = torch.zeros(d, device="cuda")
+        u[3] = 1.0
+        c["q"][:, :, 3] = 8.0 * (torch.arange(1500, device="cuda")[:, None] % 3 != 1)  # not every row
+        for i, size in ((200, 1), (340, 2), (400, 2.5), (450, 2.5), (700, 4), (901, 3), (1280, 5), (1344, 5)):
+            c["k_pool"][t[i // 64], :, i % 64] = (jump * size * u).to(BF16)
+        c["k_pool"][t[300 // 64], :, 300 % 64] = (-jump * 9 * u).to(BF16)
+        want, tol = prompt_want(c, ctx, ctx)
+        for _ in range(3):
+            c["out"].fill_(7.0)
+            assert run_prompt(c) == 0
+            P.check(c["out"], want, tol)
+
+
 def test_prompt_bad_pages_and_offsets():
     c = prompt_case(15, BF16, 4, 2, 128, 64, [200, 100], [200, 100])
     c["block_table"][0, 1] = 99
