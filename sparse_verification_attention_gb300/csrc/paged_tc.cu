@@ -33,6 +33,7 @@
 // such a key gets the element added again at the end.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "host.h"
 #include "internal.h"
@@ -257,6 +258,19 @@ __device__ __forceinline__ uint64_t exponentials(const uint32_t (&v)[64], uint32
     tc::st8(taddr + 8 * c, p);
   }
   return add2(sum[0], sum[1]);
+}
+
+// n columns of a row's O times alpha (all products into O are complete).
+__device__ __noinline__ void scale_o(uint32_t taddr, int n, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < n; c += 8) {
+    uint32_t o[8];
+    ld8_at(taddr + c, o);
+    tc::wait_ld();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+    tc::st8(taddr + c, o);
+  }
 }
 
 // 64 keys of P in TMEM times alpha.
@@ -713,18 +727,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int draft_tile = it.draft ? it.nk - 1 : -1;
       const int stride = run.pair ? 1 : 2, first = run.pair ? 0 : X;
       float m_run = -INFINITY, l_run = 0.f, mine = -INFINITY;
-      // columns [c0, c1) of the row's O times alpha; all products into O are complete
-      auto scale_o = [&](int c0, int c1, float alpha) {
-#pragma unroll 1
-        for (int c = c0; c < c1; c += 8) {
-          uint32_t o[8];
-          ld8_at(tO + c, o);
-          tc::wait_ld();
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tc::st8(tO + c, o);
-        }
-      };
       // move the row's reference to m; alpha: what its sum and O are multiplied by
       auto move_ref = [&](float m) {
         const float alpha = m == -INFINITY ? 1.f : ex2(m_run - m);
@@ -741,25 +743,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto catch_up = [&](float other) {  // the other half's maximum of the last tile
         if (__any_sync(0xffffffffu, other > m_run + kFixLog2)) move_ref(fmaxf(m_run, fmaxf(mine, other)));
       };
-      for (int j = 0; j < n; ++j) {
-        const int kt = first + stride * j;
-        if (!(ok = wait_all(&sh.s_full[X], s_uses++ & 1, 10u))) break;
+      // Tile j of the set, key tile kt of the run. General: the set's first tile and
+      // those with a masked key; the others run a copy without that code.
+      auto softmax_tile = [&](int j, int kt, auto tag) {
+        constexpr bool general = decltype(tag)::value;
+        if (!wait_all(&sh.s_full[X], s_uses++ & 1, 10u)) return false;
         if (live) {
           tc::fence_after();
-          const float other = j > 0 ? sh.mx[(j - 1) & 1][X][H ^ 1][r] : -INFINITY;
+          const float other = !general || j > 0 ? sh.mx[(j - 1) & 1][X][H ^ 1][r] : -INFINITY;
           uint32_t v[64];
           ld32_at(tS, v);  // (nothing may touch v before the wait)
           ld32_at(tS + 32, v + 32);
           tc::wait_ld();
-          if (j > 0) {
-            // O follows the maximum in steps of more than 2^kRescaleLog2, each half its
-            // columns: S of this tile was issued behind the P V of the last
+          // O follows the maximum in steps of more than 2^kRescaleLog2, each half its
+          // columns: S of this tile was issued behind the P V of the last
+          if (__any_sync(0xffffffffu, fmaxf(mine, other) > m_run + kRescaleLog2) && (!general || j > 0)) {
             catch_up(other);
             const float both = fmaxf(mine, other);
             if (__any_sync(0xffffffffu, both > m_run + kRescaleLog2))
-              scale_o(D / 2 * H, D / 2 * H + D / 2, move_ref(fmaxf(m_run, both)));
+              scale_o(tO + D / 2 * H, D / 2, move_ref(fmaxf(m_run, both)));
           }
-          if (kt == draft_tile || kt * kKeys + 64 > vis_set) {
+          if (general && (kt == draft_tile || kt * kKeys + 64 > vis_set)) {
             uint32_t keep[2];  // keys of this half that the row sees
             if (kt == draft_tile) {  // drafts 0..63: all in the first half
               const unsigned long long see = valid && H == 0 ? sh.anc[it.draft0 + tok] : 0ull;
@@ -774,14 +778,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 64; ++i)
               if (!(keep[i >> 5] >> (i & 31) & 1u)) v[i] = 0xff800000u;  // -inf
           }
-          if (j == 0) {
+          if (general && j == 0) {
             mine = max64(v) * a.scale_log2;
             sh.mx[0][X][H][r] = mine;
-            if (!(ok = meet_half())) break;
+            if (!meet_half()) return false;
             m_run = fmaxf(mine, sh.mx[0][X][H ^ 1][r]);
           }
           uint64_t sum = exponentials(v, tS, m_run, a.scale_log2);
-          if (j > 0) {
+          if (!general || j > 0) {
             mine = max64(v) * a.scale_log2;
             sh.mx[j & 1][X][H][r] = mine;
             const bool fix = __any_sync(0xffffffffu, mine > m_run + kFixLog2);
@@ -791,13 +795,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++h_uses;
             if (fix) {
               --h_uses;
-              if (!(ok = half_wait())) break;
+              if (!half_wait()) return false;
               tc::fence_after();
-              const float other = sh.mx[j & 1][X][H ^ 1][r];
-              const bool alone = !__any_sync(0xffffffffu, other > m_run + kFixLog2);
-              const float alpha = move_ref(fmaxf(m_run, fmaxf(mine, other)));
+              const float now = sh.mx[j & 1][X][H ^ 1][r];
+              const bool alone = !__any_sync(0xffffffffu, now > m_run + kFixLog2);
+              const float alpha = move_ref(fmaxf(m_run, fmaxf(mine, now)));
               // alone: the other half's P is written, against the old reference
-              scale_o(alone ? 0 : D / 2 * H, alone ? D : D / 2 * H + D / 2, alpha);
+              scale_o(tO + (alone ? 0 : D / 2 * H), alone ? D : D / 2, alpha);
               if (alone) scale_p(lane_base + col_s(X) + 64 * (H ^ 1), alpha);
               sum = exponentials(v, tS, m_run, a.scale_log2);
             }
@@ -809,6 +813,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[X]));
+        return true;
+      };
+      // key tiles before `plain` show all their keys to all rows of the set
+      const int plain = min(draft_tile < 0 ? 1 << 30 : draft_tile, vis_set < 64 ? 0 : (vis_set + 64) / kKeys);
+      for (int j = 0; j < n && ok; ++j) {
+        const int kt = first + stride * j;
+        ok = j > 0 && kt < plain ? softmax_tile(j, kt, std::false_type{}) : softmax_tile(j, kt, std::true_type{});
       }
       if (!ok) break;
       // ---------------------------------------------------------- results
