@@ -86,6 +86,7 @@ struct Control {
   float mx[2][2][2][kRows];  // maxima of even and odd tiles by set and half
   float2 ml[2][2][kRows];  // maximum and sum by set and half
   unsigned long long anc[kMaxT];
+  uint32_t place[kRows];   // token (high half) and head of a set's row
   Item items[kItems];
   Plan plan;
 };
@@ -96,6 +97,16 @@ struct Run {
   int n[2];     // key tiles of each set
   int masked;   // first key tile (of the run) with a masked key
 };
+
+struct Row {
+  int tok, head;
+  bool valid;  // the row is one of the item's
+};
+
+// Keys of the segment that token tok of an item sees.
+__device__ __forceinline__ int keys_of(const Item& it, int tok) {
+  return it.causal ? it.vis0 + tok : it.ctx;
+}
 
 __device__ __forceinline__ Run run_of(const Item& it, int tt) {
   Run r;
@@ -399,6 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::alloc(smem_u32(&sh.tmem), kTmemCols);
     tc::relinquish();
   }
+  if (threadIdx.x < kRows)
+    sh.place[threadIdx.x] = threadIdx.x / a.gs << 16 | threadIdx.x % a.gs;
   if (a.prefix)
     for (int t = threadIdx.x; t < a.T; t += kThreads) sh.anc[t] = a.anc[t];
   pdl_wait();
@@ -691,7 +704,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
     const uint32_t tS = lane_base + col_s(X) + 64 * H;
     const uint32_t tO = lane_base + col_o(X);
-    const int rt = r / a.gs, rg = r % a.gs;  // token of the set and head of the group
     uint32_t s_uses = 0, o_uses = 0, h_uses = 0, meets = 0;
     bool ok = true;
     // all softmax warps meet
@@ -712,20 +724,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       half_arrive();
       return half_wait();
     };
+    // token (of the item) and head (of the group) of row r of set s
+    auto row_of = [&](const Item& it, const Run& run, int s, int r) {
+      const uint32_t place = sh.place[r];
+      Row row{(int)(place >> 16), (int)(place & 0xffff), false};
+      row.valid = row.tok < tt;
+      if (run.pair && s) row.tok += tt;
+      row.valid = row.valid && row.tok < it.ntok && row.head < it.heads;
+      return row;
+    };
     for (uint32_t seq = 0; ok && take_item(seq); ++seq) {
       const Item& it = sh.items[seq % kItems];
-      const Run run = run_of(it, tt);
-      const int off = run.pair && X ? tt : 0;  // the set's first token
-      const int tok = off + rt;
-      const bool valid = rt < tt && tok < it.ntok && rg < it.heads;
-      const bool live = __any_sync(0xffffffffu, valid);  // a warp without rows only keeps step
-      const int n = X ? run.n[1] : run.n[0];
-      // relative to the run's first key: keys that the row sees, and that the
-      // set's first row sees (it sees the fewest)
-      const int vis = (it.causal ? it.vis0 + tok : it.ctx) - it.k0 * kKeys - 64 * H;
-      const int vis_set = (it.causal ? it.vis0 + off : it.ctx) - it.k0 * kKeys - 64 * H;
-      const int draft_tile = it.draft ? it.nk - 1 : -1;
-      const int stride = run.pair ? 1 : 2, first = run.pair ? 0 : X;
+      // Little of an item is kept in registers over its key tiles (the inner
+      // loop needs them all): what the mask and the results need is read again
+      // from shared memory.
+      bool live;  // a warp without rows only keeps step
+      int kt, kt_end, stride, plain;
+      {
+        const Run run = run_of(it, tt);
+        live = __any_sync(0xffffffffu, row_of(it, run, X, r).valid);
+        kt = run.pair ? 0 : X;
+        kt_end = run.pair ? run.n[X] : it.nk;
+        stride = run.pair ? 1 : 2;
+        // key tiles before `plain` show all their keys to all rows of the set
+        const int least = keys_of(it, run.pair && X ? tt : 0) - (it.k0 * kKeys + 64 * H);
+        plain = least < 64 ? 0 : (least + 64) / kKeys;
+        if (it.draft) plain = min(plain, it.nk - 1);
+      }
+      const bool empty = kt >= kt_end;
       float m_run = -INFINITY, l_run = 0.f, mine = -INFINITY;
       // move the row's reference to m; alpha: what its sum and O are multiplied by
       auto move_ref = [&](float m) {
@@ -743,34 +769,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto catch_up = [&](float other) {  // the other half's maximum of the last tile
         if (__any_sync(0xffffffffu, other > m_run + kFixLog2)) move_ref(fmaxf(m_run, fmaxf(mine, other)));
       };
-      // Tile j of the set, key tile kt of the run. General: the set's first tile and
-      // those with a masked key; the others run a copy without that code.
-      auto softmax_tile = [&](int j, int kt, auto tag) {
+      // One key tile of the set. General: the set's first tile of the item and those
+      // with a masked key; the others run a copy without that code.
+      auto softmax_tile = [&](bool start, auto tag) {
         constexpr bool general = decltype(tag)::value;
+        const uint32_t odd = s_uses & 1;
         if (!wait_all(&sh.s_full[X], s_uses++ & 1, 10u)) return false;
         if (live) {
           tc::fence_after();
-          const float other = !general || j > 0 ? sh.mx[(j - 1) & 1][X][H ^ 1][r] : -INFINITY;
+          const float other = general && start ? -INFINITY : sh.mx[odd ^ 1][X][H ^ 1][r];
           uint32_t v[64];
           ld32_at(tS, v);  // (nothing may touch v before the wait)
           ld32_at(tS + 32, v + 32);
           tc::wait_ld();
           // O follows the maximum in steps of more than 2^kRescaleLog2, each half its
           // columns: S of this tile was issued behind the P V of the last
-          if (__any_sync(0xffffffffu, fmaxf(mine, other) > m_run + kRescaleLog2) && (!general || j > 0)) {
+          if (__any_sync(0xffffffffu, fmaxf(mine, other) > m_run + kRescaleLog2) && !(general && start)) {
             catch_up(other);
             const float both = fmaxf(mine, other);
             if (__any_sync(0xffffffffu, both > m_run + kRescaleLog2))
               scale_o(tO + D / 2 * H, D / 2, move_ref(fmaxf(m_run, both)));
           }
-          if (general && (kt == draft_tile || kt * kKeys + 64 > vis_set)) {
+          if (general && kt >= plain) {
             uint32_t keep[2];  // keys of this half that the row sees
-            if (kt == draft_tile) {  // drafts 0..63: all in the first half
-              const unsigned long long see = valid && H == 0 ? sh.anc[it.draft0 + tok] : 0ull;
+            const Row row = row_of(it, run_of(it, tt), X, r);
+            if (it.draft && kt == it.nk - 1) {  // drafts 0..63: all in the first half
+              const unsigned long long see = row.valid && H == 0 ? sh.anc[it.draft0 + row.tok] : 0ull;
               keep[0] = (uint32_t)see;
               keep[1] = (uint32_t)(see >> 32);
             } else {
-              const int lim = vis - kt * kKeys;
+              const int lim = keys_of(it, row.tok) - (it.k0 + kt) * kKeys - 64 * H;
               keep[0] = lim >= 32 ? 0xffffffffu : lim <= 0 ? 0u : (1u << lim) - 1u;
               keep[1] = lim >= 64 ? 0xffffffffu : lim <= 32 ? 0u : (1u << (lim - 32)) - 1u;
             }
@@ -778,16 +806,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 64; ++i)
               if (!(keep[i >> 5] >> (i & 31) & 1u)) v[i] = 0xff800000u;  // -inf
           }
-          if (general && j == 0) {
+          if (general && start) {
             mine = max64(v) * a.scale_log2;
-            sh.mx[0][X][H][r] = mine;
+            sh.mx[odd][X][H][r] = mine;
             if (!meet_half()) return false;
-            m_run = fmaxf(mine, sh.mx[0][X][H ^ 1][r]);
+            m_run = fmaxf(mine, sh.mx[odd][X][H ^ 1][r]);
           }
           uint64_t sum = exponentials(v, tS, m_run, a.scale_log2);
-          if (!general || j > 0) {
+          if (!(general && start)) {
             mine = max64(v) * a.scale_log2;
-            sh.mx[j & 1][X][H][r] = mine;
+            sh.mx[odd][X][H][r] = mine;
             const bool fix = __any_sync(0xffffffffu, mine > m_run + kFixLog2);
             tc::wait_st();
             tc::fence_before();
@@ -797,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               --h_uses;
               if (!half_wait()) return false;
               tc::fence_after();
-              const float now = sh.mx[j & 1][X][H ^ 1][r];
+              const float now = sh.mx[odd][X][H ^ 1][r];
               const bool alone = !__any_sync(0xffffffffu, now > m_run + kFixLog2);
               const float alpha = move_ref(fmaxf(m_run, fmaxf(mine, now)));
               // alone: the other half's P is written, against the old reference
@@ -815,19 +843,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[X]));
         return true;
       };
-      // key tiles before `plain` show all their keys to all rows of the set
-      const int plain = min(draft_tile < 0 ? 1 << 30 : draft_tile, vis_set < 64 ? 0 : (vis_set + 64) / kKeys);
-      for (int j = 0; j < n && ok; ++j) {
-        const int kt = first + stride * j;
-        ok = j > 0 && kt < plain ? softmax_tile(j, kt, std::false_type{}) : softmax_tile(j, kt, std::true_type{});
-      }
+      for (bool start = true; ok && kt < kt_end; kt += stride, start = false)
+        ok = start || kt >= plain ? softmax_tile(start, std::true_type{})
+                                  : softmax_tile(false, std::false_type{});
       if (!ok) break;
       // ---------------------------------------------------------- results
-      if (n > 0) {
+      const Run run = run_of(it, tt);
+      const Row row = row_of(it, run, X, r);
+      if (!empty) {
         if (!(ok = wait_all(&sh.o_done[X], o_uses++ & 1, 11u))) break;
         tc::fence_after();
+        if (live) catch_up(sh.mx[(s_uses & 1) ^ 1][X][H ^ 1][r]);
       }
-      if (live && n > 0) catch_up(sh.mx[(n - 1) & 1][X][H ^ 1][r]);
       // the row's maximum and sum over both halves (and, alternating, both sets)
       float w[2] = {X ? 0.f : 1.f, X ? 1.f : 0.f}, m_out = m_run, l_out = l_run;
       sh.ml[X][H][r] = make_float2(m_run, l_run);
@@ -852,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = l_out == 0.f ? 0.f : 1.0f / l_out;
         const bool use0 = (run.pair ? X == 0 : true) && run.n[0] > 0;
         const bool use1 = (run.pair ? X == 1 : true) && run.n[1] > 0;
-        const size_t prow = (size_t)max(it.part, 0) + tok * a.gs + rg;
+        const size_t prow = (size_t)max(it.part, 0) + row.tok * a.gs + row.head;
         // 16 columns at a time: this thread's share of the row's D is its half
         // (pair), or a quarter of both sets' sums (alternating)
         const int c0 = run.pair ? D / 2 * H : D / 4 * (2 * X + H), c1 = c0 + (run.pair ? D / 2 : D / 4);
@@ -875,11 +902,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) f[e] += w[1] != 0.f ? w[1] * __uint_as_float(o[e]) : 0.f;
           }
-          if (!valid) continue;
+          if (!row.valid) continue;
           uint32_t x[16];
           if (it.part < 0) {
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
-                                 ((size_t)(it.tok0 + tok) * a.Hq + it.head0 + rg) * a.d + c;
+                                 ((size_t)(it.tok0 + row.tok) * a.Hq + it.head0 + row.head) * a.d + c;
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = pack_bf16(f[2 * e] * inv, f[2 * e + 1] * inv);
             if (a.out_wide) {  // d is a multiple of 16
@@ -896,14 +923,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c + 8 < a.d) store32(dst + 8, x + 8);
           }
         }
-        if (any_nf && valid)
-          add_nonfinite(a, it, nf, nmasked, it.causal ? it.vis0 + tok : it.ctx,
-                        it.draft ? sh.anc[it.draft0 + tok] : 0ull, c0, c1,
+        if (any_nf && row.valid)
+          add_nonfinite(a, it, nf, nmasked, keys_of(it, row.tok),
+                        it.draft ? sh.anc[it.draft0 + row.tok] : 0ull, c0, c1,
                         it.part < 0 ? static_cast<__nv_bfloat16*>(a.out) +
-                                          ((size_t)(it.tok0 + tok) * a.Hq + it.head0 + rg) * a.d
+                                          ((size_t)(it.tok0 + row.tok) * a.Hq + it.head0 + row.head) * a.d
                                     : nullptr,
                         a.part_o + prow * a.d);
-        if (valid && it.part >= 0 && H == 0 && (run.pair || X == 0)) a.part_ml[prow] = make_float2(m_out, l_out);
+        if (row.valid && it.part >= 0 && H == 0 && (run.pair || X == 0)) a.part_ml[prow] = make_float2(m_out, l_out);
       }
       tc::fence_before();  // O is read: the next item's products may overwrite it
       // both halves (pair) or all warps (alternating) have read sums and O
