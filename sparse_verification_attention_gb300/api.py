@@ -358,45 +358,60 @@ def sv_verify_layer_host(shape: Shape, q_host, q, kv: KV, reps, budget: Optional
 
 
 # ------------------------------------------------------------------ paged cache
+# A decoding step makes these calls once per layer, and their kernels take a few
+# microseconds: the checks read each attribute of a tensor once, and pointers and
+# streams go to ctypes as plain integers.
+_DTYPES = (torch.bfloat16, torch.float32)  # by dtype code
+
+
 def _call(fn, tensors, stream, *args):
     """fn(*args, stream) with the tensors' device current. None stands for an
     argument that is left out; the others must lie on one CUDA device."""
-    dev = None
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda or (dev is not None and t.device != dev):
-            raise ValueError("the tensors of a call must lie on one CUDA device")
-        dev = t.device
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
+        if t is not None and t.get_device() != dev:
+            dev = -1
+            break
+    if dev < 0:
+        raise ValueError("the tensors of a call must lie on one CUDA device")
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)))
+            status = fn(*args, stream)
+    if status != SV_OK:
+        _check(status)
 
 
-def _ints(name: str, t: Optional[torch.Tensor], *shape):
-    """Refuse t unless it is a dense int32 tensor of this shape (None: any size)."""
-    if t is None:
-        return
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape) or \
-            any(n is not None and n != m for n, m in zip(shape, t.shape)):
+def _ints(name: str, t: torch.Tensor, *shape) -> int:
+    """The address of t, which must be a dense int32 tensor of this shape."""
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+    return t.data_ptr()
 
 
-def _dense(name: str, t: torch.Tensor, code: int, *shape):
-    """Refuse t unless it is a dense tensor of the call's dtype and this shape."""
-    if dtype_code(t.dtype) != code or not t.is_contiguous() or t.dim() != len(shape) or \
-            any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must be contiguous, of the shape's dtype and of shape {list(shape)}")
+def _dense(name: str, t: torch.Tensor, dtype: torch.dtype, *shape) -> int:
+    """The address of t, which must be a dense tensor of the call's dtype and this shape."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of dtype {dtype} and of shape {list(shape)}")
+    return t.data_ptr()
 
 
-def _rows(name: str, t: torch.Tensor, code: int, heads: int, d: int) -> int:
+def _rows(name: str, t: torch.Tensor, dtype: torch.dtype, heads: int, d: int) -> int:
     """The distance of t's rows [n, heads, d], in elements; rows may be strided."""
-    if dtype_code(t.dtype) != code or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or \
-            (t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d))):
-        raise ValueError(f"{name} must be rows [n, {heads}, {d}] of the shape's dtype, each row dense")
-    return t.stride(0) if t.shape[0] > 1 else heads * d
+    shape, stride = t.shape, t.stride()
+    if t.dtype != dtype or len(shape) != 3 or shape[1] != heads or shape[2] != d or \
+            (shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != d))):
+        raise ValueError(f"{name} must be rows [n, {heads}, {d}] of dtype {dtype}, each row dense")
+    return stride[0] if shape[0] > 1 else heads * d
+
+
+def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def sv_build_tables(blk: int, old_len, new_len, block_table, free_pages, free_count, free_count_out,
@@ -407,36 +422,32 @@ def sv_build_tables(blk: int, old_len, new_len, block_table, free_pages, free_co
     [num_pages], a stack of which free_count[0] entries are free; free_count_out
     [1] (may be free_count); cu_new [B + 1]; slot_map, positions [n_max]."""
     B, nb_max = block_table.shape
-    _ints("old_len", old_len, B)
-    _ints("new_len", new_len, B)
-    _ints("pinned", pinned, B)
-    _ints("block_table", block_table, B, nb_max)
-    _ints("free_pages", free_pages, None)
-    _ints("free_count", free_count, 1)
-    _ints("free_count_out", free_count_out, 1)
-    _ints("cu_new", cu_new, B + 1)
-    _ints("slot_map", slot_map, None)
-    _ints("positions", positions, slot_map.shape[0])
-    _call(lib().sv_build_tables, (old_len, new_len, pinned, block_table, free_pages, free_count,
-                                  free_count_out, cu_new, slot_map, positions, ws), stream,
-          B, blk, _ptr(old_len), _ptr(new_len), _ptr(pinned), _ptr(block_table), nb_max,
-          free_pages.shape[0], _ptr(free_pages), _ptr(free_count), _ptr(free_count_out),
-          _ptr(cu_new), _ptr(slot_map), _ptr(positions), slot_map.shape[0], _ptr(ws))
+    (n_max,), (num_pages,) = slot_map.shape, free_pages.shape
+    _call(lib().sv_build_tables,
+          (old_len, new_len, pinned, block_table, free_pages, free_count, free_count_out, cu_new,
+           slot_map, positions, ws), stream,
+          B, blk, _ints("old_len", old_len, B), _ints("new_len", new_len, B),
+          None if pinned is None else _ints("pinned", pinned, B),
+          _ints("block_table", block_table, B, nb_max), nb_max, num_pages,
+          _ints("free_pages", free_pages, num_pages), _ints("free_count", free_count, 1),
+          _ints("free_count_out", free_count_out, 1), _ints("cu_new", cu_new, B + 1),
+          _ints("slot_map", slot_map, n_max),
+          None if positions is None else _ints("positions", positions, n_max), n_max, _addr(ws))
 
 
 def sv_write_kv(shape: Shape, k, v, slot_map, k_pool, v_pool, ws=None, stream=None):
     """Store the rows k, v [n, Hkv, d] (slices of a fused projection are fine) at
     their slots of the paged cache; slots of -1 are skipped."""
-    ks = _rows("k", k, shape.dtype, shape.Hkv, shape.d)
-    vs = _rows("v", v, shape.dtype, shape.Hkv, shape.d)
-    if k.shape[0] != v.shape[0]:
-        raise ValueError(f"{k.shape[0]} key rows and {v.shape[0]} value rows")
-    _ints("slot_map", slot_map, k.shape[0])
-    _dense("k_pool", k_pool, shape.dtype, None, shape.Hkv, shape.blk, shape.d)
-    _dense("v_pool", v_pool, shape.dtype, k_pool.shape[0], shape.Hkv, shape.blk, shape.d)
-    _call(lib().sv_write_kv, (k, v, slot_map, k_pool, v_pool, ws), stream, C.byref(shape), _ptr(k),
-          ks, _ptr(v), vs, _ptr(slot_map), k.shape[0], _ptr(k_pool), _ptr(v_pool), k_pool.shape[0],
-          _ptr(ws))
+    H, d, dtype = shape.Hkv, shape.d, _DTYPES[shape.dtype]
+    ks, vs = _rows("k", k, dtype, H, d), _rows("v", v, dtype, H, d)
+    n, pages = k.shape[0], k_pool.shape[0]
+    if v.shape[0] != n:
+        raise ValueError(f"{n} key rows and {v.shape[0]} value rows")
+    pool = (pages, H, shape.blk, d)
+    _call(lib().sv_write_kv, (k, v, slot_map, k_pool, v_pool, ws), stream, C.byref(shape),
+          k.data_ptr(), ks, v.data_ptr(), vs, _ints("slot_map", slot_map, n), n,
+          _dense("k_pool", k_pool, dtype, *pool), _dense("v_pool", v_pool, dtype, *pool), pages,
+          _addr(ws))
 
 
 def _alloc_zeroed(n: int, device) -> torch.Tensor:
@@ -460,32 +471,30 @@ def sv_prompt_attend(shape: Shape, q, k_pool, v_pool, block_table, seq_ctx, cu_q
     """Causal attention of the packed rows q [n, Hq, d] (rows may be strided)
     over the paged cache: rows cu_q[b] .. cu_q[b+1] are the last of the
     seq_ctx[b] cached tokens of sequence b. out: [n, Hq, d]."""
-    qs = _rows("q", q, shape.dtype, shape.Hq, shape.d)
-    _dense("out", out, shape.dtype, q.shape[0], shape.Hq, shape.d)
-    _dense("k_pool", k_pool, shape.dtype, None, shape.Hkv, shape.blk, shape.d)
-    _dense("v_pool", v_pool, shape.dtype, k_pool.shape[0], shape.Hkv, shape.blk, shape.d)
-    _ints("block_table", block_table, shape.B, None)
-    _ints("seq_ctx", seq_ctx, shape.B)
-    _ints("cu_q", cu_q, shape.B + 1)
+    B, Hq, d, dtype = shape.B, shape.Hq, shape.d, _DTYPES[shape.dtype]
+    qs = _rows("q", q, dtype, Hq, d)
+    n, pages, nb_max = q.shape[0], k_pool.shape[0], block_table.shape[-1]
+    pool = (pages, shape.Hkv, shape.blk, d)
     _call(lib().sv_prompt_attend, (q, k_pool, v_pool, block_table, seq_ctx, cu_q, out, ws), stream,
-          C.byref(shape), _ptr(q), qs, q.shape[0], _ptr(k_pool), _ptr(v_pool), _ptr(block_table),
-          block_table.shape[1], k_pool.shape[0], _ptr(seq_ctx), _ptr(cu_q), _ptr(out), _ptr(ws),
-          0 if ws is None else ws.numel())
+          C.byref(shape), q.data_ptr(), qs, n, _dense("k_pool", k_pool, dtype, *pool),
+          _dense("v_pool", v_pool, dtype, *pool), _ints("block_table", block_table, B, nb_max),
+          nb_max, pages, _ints("seq_ctx", seq_ctx, B), _ints("cu_q", cu_q, B + 1),
+          _dense("out", out, dtype, n, Hq, d), _addr(ws), 0 if ws is None else ws.numel())
 
 
 def sv_prefix_attend(shape: Shape, q, kv: KV, n_shared: int, draft_k, draft_v, parents, out, ws,
                      stream=None):
     """sv_sparse_attend over every block for a batch whose sequences share
     their first n_shared blocks: those are read once for all of them."""
-    _dense("q", q, shape.dtype, shape.B, shape.T, shape.Hq, shape.d)
-    _dense("out", out, shape.dtype, shape.B, shape.T, shape.Hq, shape.d)
-    _dense("draft_k", draft_k, shape.dtype, shape.B, shape.T, shape.Hkv, shape.d)
-    _dense("draft_v", draft_v, shape.dtype, shape.B, shape.T, shape.Hkv, shape.d)
-    if parents is not None and len(parents) != shape.T:
-        raise ValueError(f"{len(parents)} draft parents for T={shape.T} drafts")
-    _call(lib().sv_prefix_attend, (q, draft_k, draft_v, out, ws), stream, C.byref(shape), _ptr(q),
-          C.byref(kv), n_shared, _ptr(draft_k), _ptr(draft_v), _parents(parents), _ptr(out),
-          _ptr(ws), 0 if ws is None else ws.numel())
+    B, T, d, dtype = shape.B, shape.T, shape.d, _DTYPES[shape.dtype]
+    rows, drafts = (B, T, shape.Hq, d), (B, T, shape.Hkv, d)
+    if parents is not None and len(parents) != T:
+        raise ValueError(f"{len(parents)} draft parents for T={T} drafts")
+    _call(lib().sv_prefix_attend, (q, draft_k, draft_v, out, ws), stream, C.byref(shape),
+          _dense("q", q, dtype, *rows), C.byref(kv), n_shared,
+          _dense("draft_k", draft_k, dtype, *drafts), _dense("draft_v", draft_v, dtype, *drafts),
+          _parents(parents), _dense("out", out, dtype, *rows), _addr(ws),
+          0 if ws is None else ws.numel())
 
 
 VERIFY_COMPUTE, VERIFY_REUSE, VERIFY_FULL = 0, 1, 2  # sv_verify_layer's reuse values
