@@ -79,14 +79,16 @@ __device__ __forceinline__ int unit_cost(const PagedArgs& a, const Seg& s) {
 // Fill `p` (all threads of the CTA call it; barriers inside). scratch:
 // kPlanScratch ints of shared memory on a 16-byte boundary.
 //
+// Segments go out in descending order of their units' cost, so that what starts
+// last is short (the prefix form's shared segment first).
+//
 // Prefix form: every segment's keys are cut into runs so that the grid gets
-// about kItemsPerCta items per CTA; the shared segment comes first. Its partial
-// rows are then at most those of the uncut segments and kItemsPerCta items per
-// CTA more.
+// about kItemsPerCta items per CTA, handed out dynamically. Its partial rows
+// are then at most those of the uncut segments and kItemsPerCta items per CTA
+// more.
 //
 // Prompt form, one of two ways, whichever is expected to end earlier:
-//   whole units, handed out dynamically, segments in descending order of key
-//     tiles, so that what starts last is short. Ends at about the average load
+//   whole units, handed out dynamically. Ends at about the average load
 //     plus half the longest unit (at least at the longest);
 //   stream: the units laid end to end, CTA c taking the c-th equal share, at
 //     most two cut units each. Ends at the average load, counting for every row
@@ -107,7 +109,7 @@ __device__ inline void make_plan(const PagedArgs& a, Plan* p, int* scratch) {
     kts[i] = !s.n ? 0 : a.prefix ? key_tiles(a, s.ctx) + s.draft : unit_cost(a, s);
   }
   __syncthreads();
-  if (!a.prefix && nseg > 1) {
+  if (nseg > 1) {
     for (int i = threadIdx.x; i < nseg; i += blockDim.x) {
       const int kt = kts[i];
       int rank = 0;
@@ -116,6 +118,8 @@ __device__ inline void make_plan(const PagedArgs& a, Plan* p, int* scratch) {
         rank += (k.x > kt || (k.x == kt && j < i)) + (k.y > kt || (k.y == kt && j + 1 < i)) +
                 (k.z > kt || (k.z == kt && j + 2 < i)) + (k.w > kt || (k.w == kt && j + 3 < i));
       }
+      // the shared segment counts as the costliest
+      if (a.prefix) rank = i == 0 ? 0 : rank + (kts[0] < kt);
       p->order[rank] = i;
     }
     __syncthreads();
@@ -134,11 +138,10 @@ __device__ inline void make_plan(const PagedArgs& a, Plan* p, int* scratch) {
           units >> 31 ? (units + parts - 1) / parts : ((unsigned)units + parts - 1) / parts;
       const int run = (int)min(max(want, (unsigned long long)a.min_run), 1ull << 30);
       for (int i = b0; i < b1; ++i) {
-        const int kt = kts[i], n = ns[i];
+        const int kt = kts[p->order[i]], n = ns[p->order[i]];
         int s = kt > run ? ceil_div(kt, run) : 1;
         if (s > 1) s = ceil_div(kt, ceil_div(kt, s));  // no empty run
         const int it = ceil_div(n, a.tile) * a.hv * s;
-        p->order[i] = i;
         p->split[i] = s;
         p->first[i] = it;
         p->rows[i] = it * min(a.tile, n) * a.gs;
@@ -227,6 +230,13 @@ __device__ __forceinline__ int share_of(int total, int ctas, int x) {
 // the beginning of the unit that it ends with.
 __device__ __forceinline__ int slot_rows(const PagedArgs& a) { return min(a.tile, a.n_rows) * a.gs; }
 
+// What the merge launch needs of the prefix form's plan, by segment.
+__device__ inline void save_plan(const PagedArgs& a, const Plan* p) {
+  if (!a.prefix || blockIdx.x) return;
+  for (int i = threadIdx.x; i < n_segs(a); i += blockDim.x)
+    a.segs[p->order[i]] = make_int2(p->rows[i], p->split[i]);
+}
+
 struct Item {
   int valid;
   int tok0, ntok;     // rows of the tile
@@ -275,14 +285,16 @@ struct Cursor {
   int at, end;  // item number, or (stream) position in the flattened cost
 };
 
+// One thread calls it, and next_item.
 __device__ __forceinline__ Cursor start_cursor(const PagedArgs& a, const Plan* p) {
+  if (!a.prefix) a.joins[blockIdx.x].more = 0;
   if (a.prefix || !p->stream) return {(int)blockIdx.x, 0};
   const int total = p->first[n_segs(a)];
   return {share_start(total, a.ctas, blockIdx.x), share_start(total, a.ctas, blockIdx.x + 1)};
 }
 
 // The item at the cursor (valid = 0 behind the last one), and the cursor
-// moved on. One thread calls it.
+// moved on.
 __device__ inline Item next_item(const PagedArgs& a, const Plan* p, Cursor* c) {
   const int nseg = n_segs(a);
   if (!a.prefix && p->stream) {
@@ -301,6 +313,9 @@ __device__ inline Item next_item(const PagedArgs& a, const Plan* p, Cursor* c) {
                         (max(0, off - kItemCost) + w - 1) >> (w - 1),
                         (max(0, upto - kItemCost) + w - 1) >> (w - 1));
     if (off > 0 || upto < cost) it.part = (2 * blockIdx.x + (off > 0 ? 0 : 1)) * slot_rows(a);
+    if (off == 0 && upto < cost)  // begun here, ended by others: the merge's to join
+      a.joins[blockIdx.x] = {share_of(p->first[nseg], a.ctas, c->at + cost - 1) - (int)blockIdx.x,
+                             it.tok0, it.ntok, it.head0, it.heads};
     c->at += upto - off;
     return it;
   }

@@ -47,6 +47,12 @@ constexpr int kSimtRows = 64;       // rows of an item on the CUDA cores
 constexpr int kTcRows = 128;        // rows of a set on the tensor cores; an item has two
 constexpr int kMaxTcCtas = 160;
 
+// A unit that was cut behind its beginning: how many CTAs hold the rest of it
+// (0: none was), and its rows.
+struct PagedJoin {
+  int more, tok0, ntok, head0, heads;
+};
+
 // One attention over the paged cache. Its query rows lie in segments: runs of
 // consecutive rows ("tokens", Hq heads each) that attend to one sequence of
 // keys. Prompt form: segment b = the rows cu_q[b]..cu_q[b+1], the last of
@@ -63,10 +69,12 @@ struct PagedArgs {
   const int32_t* block_table; // [B, nb_max]
   const int32_t* seq_ctx;     // prompt form: device [B]
   const int32_t* cu_q;        // prompt form: device [B + 1]
-  // workspace: status word, the scheduler's two words (zero between calls), and
-  // the partial rows
+  // workspace: status word, the scheduler's two words (zero between calls), what
+  // the attention leaves to the merge launch, and the partial rows
   unsigned* status;
   unsigned* sched;
+  PagedJoin* joins;           // prompt form: [CTAs]
+  int2* segs;                 // prefix form: first partial row and runs of each segment
   float* part_o;              // [partial rows, d]
   float2* part_ml;            // [partial rows]: running maximum (log2 domain), sum
   long long q_stride;
@@ -103,7 +111,7 @@ cudaError_t launch_paged_simt(PagedArgs a, int dtype, cudaStream_t st);
 bool paged_tc_applies(const PagedArgs& a, int dtype);
 cudaError_t launch_paged_tc(PagedArgs a, cudaStream_t st);
 // Join the partial rows that the attention kernel launched just before left
-// (the same arguments: it rebuilds that launch's plan).
+// (the same arguments).
 cudaError_t launch_paged_merge(const PagedArgs& a, int dtype, cudaStream_t st);
 
 }  // namespace sva

@@ -14,15 +14,17 @@ constexpr long long kInt = 1ll << 31;
 size_t elt_bytes(const sv_shape* s) { return s->dtype == SV_BF16 ? 2 : 4; }
 
 // Workspace of the attention calls (offsets in bytes): status word, the
-// scheduler's words (zero between calls), then partial (m, l) and o rows.
+// scheduler's words (zero between calls), what the merge launch needs, then
+// partial (m, l) and o rows.
 struct PagedLayout {
-  size_t sched, ml, o, total;
+  size_t sched, merge, ml, o, total;
 };
 
 PagedLayout paged_layout(size_t rows, int d) {
   PagedLayout L;
   L.sched = kStatusBytes;
-  L.ml = L.sched + 256;
+  L.merge = L.sched + 256;
+  L.ml = L.merge + align256(std::max(kMaxPlanCtas * sizeof(PagedJoin), kMaxSegs * sizeof(int2)));
   L.o = L.ml + align256(rows * sizeof(float2));
   L.total = L.o + align256(rows * (size_t)d * sizeof(float));
   return L;
@@ -70,6 +72,8 @@ void fill_paged(PagedArgs* a, const sv_shape* s, void* ws, const PagedLayout& L)
   uint8_t* w = static_cast<uint8_t*>(ws);
   a->status = reinterpret_cast<unsigned*>(w);
   a->sched = reinterpret_cast<unsigned*>(w + L.sched);
+  a->joins = reinterpret_cast<PagedJoin*>(w + L.merge);
+  a->segs = reinterpret_cast<int2*>(w + L.merge);
   a->part_ml = reinterpret_cast<float2*>(w + L.ml);
   a->part_o = reinterpret_cast<float*>(w + L.o);
   a->B = s->B;

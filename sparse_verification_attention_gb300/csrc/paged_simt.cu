@@ -64,7 +64,9 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
   pdl_trigger();
   make_plan(a, &plan, reinterpret_cast<int*>(smem));
 
-  Cursor cursor = start_cursor(a, &plan);  // thread 0's counts
+  save_plan(a, &plan);
+  Cursor cursor{};  // thread 0's
+  if (tid == 0) cursor = start_cursor(a, &plan);
   while (true) {
     if (tid == 0) s_item = next_item(a, &plan, &cursor);
     __syncthreads();

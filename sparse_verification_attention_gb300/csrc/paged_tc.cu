@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   tc::fence_before();
   make_plan(a, &sh.plan, reinterpret_cast<int*>(smem));
+  save_plan(a, &sh.plan);
   tc::fence_after();
   const uint32_t tmem = sh.tmem;
   auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) {
@@ -448,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t at = 0, alt = 0;
     uint32_t q_used = 0, q_phase = 0;  // bit s: slot s has been used; the phase of its release
     bool ok = true;
-    Cursor cursor = start_cursor(a, &sh.plan);  // lane 0's counts
+    Cursor cursor{};  // lane 0's
+    if (lane == 0) cursor = start_cursor(a, &sh.plan);
     // decode item `seq` into the ring (the number of the item after it, asked for
     // on the way, is there by the next call)
     auto prepare = [&](uint32_t seq) {
