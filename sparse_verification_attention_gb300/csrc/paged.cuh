@@ -70,10 +70,32 @@ __device__ __forceinline__ int key_tiles(const PagedArgs& a, int keys) {
 // the tensor cores' time.
 __device__ __forceinline__ int weight_of(const PagedArgs& a, int n) { return n > a.one_set ? 2 : 1; }
 
-// Prompt form: what a unit costs, in key tiles of one set: its tiles, and what
-// starting and ending an item takes besides.
-__device__ __forceinline__ int unit_cost(const PagedArgs& a, const Seg& s) {
-  return key_tiles(a, s.ctx) * weight_of(a, s.n) + kItemCost;
+// Prompt form: what the units of one head group of a segment cost, in keys of
+// one set of rows. Row tile t sees the keys before the segment's rows and
+// (t + 1) * tile of its own; starting and ending an item takes as long as
+// kItemCost key tiles besides.
+struct Cost {
+  int w, base, tile, tiles;
+
+  // before unit t, and of unit t
+  __device__ __forceinline__ int before(int t) const { return w * (t * base + tile * (t * (t + 1) / 2)); }
+  __device__ __forceinline__ int of(int t) const { return w * (base + tile * (t + 1)); }
+  __device__ __forceinline__ float total() const {
+    return (float)w * tiles * (base + 0.5f * tile * (tiles + 1));
+  }
+  // the unit that position x of the group lies in
+  __device__ __forceinline__ int unit_at(int x) const {
+    const float b = base + 0.5f * tile, y = (float)x / (w * tile);
+    const float p = b / tile;
+    int t = min(max((int)(sqrtf(p * p + 2.f * y) - p), 0), tiles - 1);
+    while (t > 0 && before(t) > x) --t;
+    while (t + 1 < tiles && before(t + 1) <= x) ++t;
+    return t;
+  }
+};
+
+__device__ __forceinline__ Cost cost_of(const PagedArgs& a, int n, int ctx) {
+  return {weight_of(a, n), max(0, ctx - n) + (kItemCost << a.key_shift), a.tile, ceil_div(n, a.tile)};
 }
 
 // Fill `p` (all threads of the CTA call it; barriers inside). scratch:
@@ -89,24 +111,31 @@ __device__ __forceinline__ int unit_cost(const PagedArgs& a, const Seg& s) {
 //
 // Prompt form, one of two ways, whichever is expected to end earlier:
 //   whole units, handed out dynamically. Ends at about the average load
-//     plus half the longest unit (at least at the longest);
+//     plus part of the longest unit (at least at the longest);
 //   stream: the units laid end to end, CTA c taking the c-th equal share, at
-//     most two cut units each. Ends at the average load, counting for every row
-//     tile the keys of its segment's last one, and the join of the cut units.
+//     most two cut units each. Ends at the average load and the join of the cut
+//     units, but CTAs on the same keys are far apart in them.
 // Few rows over long contexts stream (16 ragged decoding sequences: 154 us cut
-// into runs and scheduled, CTAs ending between 60 and 100% of it), whole
-// prompts do not.
+// into runs and scheduled, CTAs ending between 60 and 100% of it, 119 us as
+// equal shares), long prompts do not.
 __device__ inline void make_plan(const PagedArgs& a, Plan* p, int* scratch) {
   const int nseg = n_segs(a), lane = threadIdx.x & 31, padded = (nseg + 3) & ~3;
-  int* kts = scratch;                         // cost of a unit of segment i
+  int* kts = scratch;                         // cost of segment i's last unit
   int* ns = scratch + ((kMaxSegs + 3) & ~3);  // rows of segment i
+  int* ctxs = p->rows;                        // prompt form: keys of segment i
   for (int i = threadIdx.x; i < padded; i += blockDim.x) {
     kts[i] = -1;
     if (i >= nseg) continue;
     const Seg s = seg_of(a, i);
     if (s.bad && blockIdx.x == 0) atomicOr(a.status, SV_FLAG_BAD_LENGTH);
     ns[i] = s.n;
-    kts[i] = !s.n ? 0 : a.prefix ? key_tiles(a, s.ctx) + s.draft : unit_cost(a, s);
+    if (a.prefix) {
+      kts[i] = s.n ? key_tiles(a, s.ctx) + s.draft : 0;
+    } else {
+      const Cost c = cost_of(a, s.n, s.ctx);
+      kts[i] = s.n ? (int)fminf((float)c.w * ((float)c.base + (float)c.tile * c.tiles), 1e9f) : 0;
+      ctxs[i] = s.ctx;
+    }
   }
   __syncthreads();
   if (nseg > 1) {
@@ -149,32 +178,30 @@ __device__ inline void make_plan(const PagedArgs& a, Plan* p, int* scratch) {
         row += p->rows[i];
       }
     } else {
-      float cost = 0.f, seen = 0.f, units = 0.f, most = 0.f;
+      float cost = 0.f, units = 0.f, most = 0.f;
       for (int i = b0; i < b1; ++i) {
-        const int id = nseg > 1 ? p->order[i] : 0, kt = kts[id], n = ns[id];
         if (nseg == 1) p->order[0] = 0;
-        const float u = (float)(ceil_div(n, a.tile) * a.hv);
-        units += u;
-        cost += u * kt;
-        // causal: from the keys before the rows to all of them, on average
-        const float before = (float)max(kItemCost, kt - weight_of(a, n) * key_tiles(a, n));
-        seen += u * 0.5f * (before + kt);
-        most = fmaxf(most, (float)kt);
+        const int id = p->order[i];
+        if (ns[id] == 0) continue;
+        const Cost c = cost_of(a, ns[id], ctxs[id]);
+        units += (float)c.tiles * a.hv;
+        cost += c.total() * a.hv;
+        most = fmaxf(most, (float)(kts[id] - c.w * (kItemCost << a.key_shift)));  // (both ways have the ends)
       }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) {
         cost += __shfl_xor_sync(0xffffffffu, cost, off);
-        seen += __shfl_xor_sync(0xffffffffu, seen, off);
         units += __shfl_xor_sync(0xffffffffu, units, off);
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
       }
-      const float ctas = (float)a.ctas;
-      const float whole = units <= ctas ? most : fmaxf(most, seen / ctas + 0.5f * most);
-      const bool stream = cost < 1e9f && cost / ctas + kStreamCost < whole;
+      const float ctas = (float)a.ctas, load = cost / ctas;
+      const float whole = units <= ctas ? most : fmaxf(most, load + (units < 4.f * ctas ? 0.5f : 0.1f) * most);
+      const bool stream = cost < 1e9f && 1.05f * load + (kStreamCost << a.key_shift) < whole;
       if (lane == 0) p->stream = stream;
       for (int i = b0; i < b1; ++i) {
-        const int id = p->order[i], n = ns[id];
-        p->first[i] = ceil_div(n, a.tile) * a.hv * (stream ? kts[id] : 1);
+        const int id = p->order[i];
+        const Cost c = cost_of(a, ns[id], ctxs[id]);
+        p->first[i] = a.hv * (stream ? c.before(c.tiles) : c.tiles);
         at += p->first[i];
       }
     }
@@ -305,13 +332,15 @@ __device__ inline Item next_item(const PagedArgs& a, const Plan* p, Cursor* c) {
     }
     const int lo = find_seg(p, nseg, c->at), id = p->order[lo];
     const Seg s = seg_of(a, id);
-    const int w = weight_of(a, s.n), cost = unit_cost(a, s);
-    const int local = c->at - p->first[lo], unit = local / cost, off = local - unit * cost;
-    const int upto = min(cost, off + c->end - c->at);
-    const int tiles = ceil_div(s.n, a.tile), hv = unit / tiles;
-    Item it = make_item(a, s, id, tiles - 1 - (unit - hv * tiles), hv,
-                        (max(0, off - kItemCost) + w - 1) >> (w - 1),
-                        (max(0, upto - kItemCost) + w - 1) >> (w - 1));
+    const Cost k = cost_of(a, s.n, s.ctx);
+    const int group = k.before(k.tiles), local = c->at - p->first[lo], hv = local / group;
+    const int t = k.unit_at(local - hv * group), cost = k.of(t);
+    const int off = local - hv * group - k.before(t), upto = min(cost, off + c->end - c->at);
+    // the key tile that position x of a unit lies in
+    auto tile_at = [&](int x) {
+      return key_tiles(a, max(0, (x + k.w - 1) / k.w - (kItemCost << a.key_shift)));
+    };
+    Item it = make_item(a, s, id, t, hv, tile_at(off), upto == cost ? 1 << 28 : tile_at(upto));
     if (off > 0 || upto < cost) it.part = (2 * blockIdx.x + (off > 0 ? 0 : 1)) * slot_rows(a);
     if (off == 0 && upto < cost)  // begun here, ended by others: the merge's to join
       a.joins[blockIdx.x] = {share_of(p->first[nseg], a.ctas, c->at + cost - 1) - (int)blockIdx.x,

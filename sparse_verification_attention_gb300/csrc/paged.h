@@ -42,7 +42,7 @@ constexpr int kMaxSegs = 1025;      // row segments of one call: sequences, and 
 constexpr int kMaxPlanCtas = 640;   // CTAs of a launch at most
 constexpr int kItemsPerCta = 2;     // see make_plan
 constexpr int kItemCost = 4;        // key tiles' time that an item takes besides its own (make_plan)
-constexpr float kStreamCost = 8.f;  // key tiles' time that joining cut units takes (make_plan)
+constexpr int kStreamCost = 8;      // key tiles' time that joining cut units takes (make_plan)
 constexpr int kSimtRows = 64;       // rows of an item on the CUDA cores
 constexpr int kTcRows = 128;        // rows of a set on the tensor cores; an item has two
 constexpr int kMaxTcCtas = 160;

@@ -40,24 +40,40 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
   return make_float4(lo.x, lo.y, hi.x, hi.y);
 }
 
-template <int NC>
-constexpr int simt_smem() {  // NC: 64-column groups of the head dim
-  constexpr int pitch = 64 * NC + 4;
-  constexpr int kp = kKeys * pitch > kRows * kPPitch ? kKeys * pitch : kRows * kPPitch;
-  return (kRows * pitch + kp + kKeys * pitch) * 4;
+// 16 bytes global -> shared without registers, zeros where src is null.
+__device__ __forceinline__ void copy16(float* dst, const void* src, const void* any) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src ? src : any),
+               "r"(src ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Shared memory: Q, and stages of K (whose place P takes) and V. NC: 64-column
+// groups of d.
+template <int NC>
+struct SimtCfg {
+  static constexpr int kPitch = 64 * NC + 4;
+  static constexpr int kStages = NC <= 2 ? 2 : 1;
+  static constexpr int kStage = 2 * kKeys * kPitch;
+  static constexpr int kSmem = (kRows * kPitch + kStages * kStage) * 4;
+  static constexpr int kCtas = NC == 1 ? 2 : 1;  // per SM, where their stages fit
+  static_assert(kRows * kPPitch <= kKeys * kPitch, "P takes the place of K");
+};
+
 template <typename T, int NC>
-__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_constant__ PagedArgs a) {
+__global__ void __launch_bounds__(kThreads, SimtCfg<NC>::kCtas) paged_simt_kernel(const __grid_constant__ PagedArgs a) {
   extern __shared__ __align__(16) float smem[];
   __shared__ Plan plan;
   __shared__ Item s_item;
-  constexpr int kPitch = 64 * NC + 4;
-  float* sq = smem;                      // [kRows][kPitch]
-  float* sk = sq + kRows * kPitch;       // [kKeys][kPitch], then P [kRows][kPPitch]
-  float* sp = sk;
-  float* sv = sk + (kKeys * kPitch > kRows * kPPitch ? kKeys * kPitch : kRows * kPPitch);
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5;
+  using C = SimtCfg<NC>;
+  constexpr int kPitch = C::kPitch, kStages = C::kStages, kStage = C::kStage;
+  float* sq = smem;                 // [kRows][kPitch]
+  float* ring = sq + kRows * kPitch;  // stages of K and V, [kKeys][kPitch] each
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const T* q = static_cast<const T*>(a.q);
 
   pdl_wait();
@@ -95,46 +111,71 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
 #pragma unroll
       for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.f;
     }
+    // K and V rows of key tile kt into its stage, four threads per key; keys past the
+    // context, and pages outside the pool, are zero. The page was looked up a
+    // tile ahead (-1: none).
+    auto lookup = [&](int kt) {
+      const int key = (it.k0 + kt) * kKeys + (tid >> 2);
+      if (kt >= it.nk || (it.draft && kt == it.nk - 1) || key >= it.ctx) return -1;
+      const int page = __ldg(a.block_table + it.tab + key / a.blk);
+      if (page >= 0 && page < a.num_pages) return page;
+      if ((tid & 3) == 0) atomicOr(a.status, SV_FLAG_BAD_PAGE);
+      return -1;
+    };
+    auto load = [&](int kt, int page) {
+      const int r = tid >> 2;
+      const T *kr = nullptr, *vr = nullptr;
+      if (it.draft && kt == it.nk - 1) {
+        if (r < a.T) {
+          const size_t off = (((size_t)it.seq * a.T + r) * a.Hkv + it.kvh) * a.d;
+          kr = static_cast<const T*>(a.draft_k) + off;
+          vr = static_cast<const T*>(a.draft_v) + off;
+        }
+      } else if (page >= 0) {
+        const int key = (it.k0 + kt) * kKeys + r;
+        const size_t off = (((size_t)page * a.Hkv + it.kvh) * a.blk + key % a.blk) * a.d;
+        kr = static_cast<const T*>(a.k_pool) + off;
+        vr = static_cast<const T*>(a.v_pool) + off;
+      }
+      float* dk = ring + kt % kStages * kStage + r * kPitch;
+      float* dv = dk + kKeys * kPitch;
+#pragma unroll
+      for (int c0 = 0; c0 < 64 * NC; c0 += 16) {
+        const int c = c0 + 4 * (tid & 3);
+        const bool in = kr && c < a.d;
+        if constexpr (sizeof(T) == 4) {
+          copy16(dk + c, in ? kr + c : nullptr, a.k_pool);
+          copy16(dv + c, in ? vr + c : nullptr, a.k_pool);
+        } else {
+          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+          *reinterpret_cast<float4*>(dk + c) = in ? load4<T>(kr + c) : zero;
+          *reinterpret_cast<float4*>(dv + c) = in ? load4<T>(vr + c) : zero;
+        }
+      }
+    };
+    int page = lookup(0);
+    if (it.nk > 0) load(0, page);
+    copies_issued();
+    page = lookup(1);
     for (int kt = 0; kt < it.nk; ++kt) {
       const int key0 = (it.k0 + kt) * kKeys;
       const bool drafts = it.draft && kt == it.nk - 1;
-      // K and V rows: four threads per key; keys past the context, and pages
-      // outside the pool, are zero
-      __syncthreads();
-      {
-        const int r = tid >> 2, key = key0 + r;
-        const T *kr = nullptr, *vr = nullptr;
-        if (drafts) {
-          if (r < a.T) {
-            const size_t off = (((size_t)it.seq * a.T + r) * a.Hkv + it.kvh) * a.d;
-            kr = static_cast<const T*>(a.draft_k) + off;
-            vr = static_cast<const T*>(a.draft_v) + off;
-          }
-        } else if (key < it.ctx) {
-          const int page = __ldg(a.block_table + it.tab + key / a.blk);
-          if (page >= 0 && page < a.num_pages) {
-            const size_t off = (((size_t)page * a.Hkv + it.kvh) * a.blk + key % a.blk) * a.d;
-            kr = static_cast<const T*>(a.k_pool) + off;
-            vr = static_cast<const T*>(a.v_pool) + off;
-          } else if ((tid & 3) == 0) {
-            atomicOr(a.status, SV_FLAG_BAD_PAGE);
-          }
-        }
-#pragma unroll
-        for (int c0 = 0; c0 < 64 * NC; c0 += 16) {
-          const int c = c0 + 4 * (tid & 3);
-          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-          *reinterpret_cast<float4*>(sk + r * kPitch + c) = kr && c < a.d ? load4<T>(kr + c) : zero;
-          *reinterpret_cast<float4*>(sv + r * kPitch + c) = vr && c < a.d ? load4<T>(vr + c) : zero;
-        }
+      float* sk = ring + kt % kStages * kStage;  // then P [kRows][kPPitch]
+      float* sp = sk;
+      const float* sv = sk + kKeys * kPitch;
+      if (kStages > 1) {
+        if (kt + 1 < it.nk) load(kt + 1, page);
+        copies_issued();
+        page = lookup(kt + 2);
       }
+      copies_wait<kStages - 1>();  // this tile's
       __syncthreads();
       float s[4][4];  // rows ty * 4 + i, keys tx + 16 * j
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
+#pragma unroll 2
       for (int c = 0; c < 64 * NC; c += 4) {
         float4 x[4], y[4];
 #pragma unroll
@@ -204,6 +245,12 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
           }
         }
       }
+      __syncthreads();  // the stage is free again
+      if (kStages == 1) {
+        if (kt + 1 < it.nk) load(kt + 1, page);
+        copies_issued();
+        page = lookup(kt + 2);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -243,17 +290,17 @@ cudaError_t launch_cfg(PagedArgs a, int dtype, cudaStream_t st) {
   int n = per_sm[dev].load();
   if (n <= 0) {
     cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<T, NC>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, simt_smem<NC>());
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, SimtCfg<NC>::kSmem);
     if (e == cudaSuccess)
       e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_simt_kernel<T, NC>, kThreads,
-                                                        simt_smem<NC>());
+                                                        SimtCfg<NC>::kSmem);
     if (e != cudaSuccess) return e;
     if (n < 1) return cudaErrorInvalidConfiguration;
     per_sm[dev].store(n);
   }
   a.ctas = std::min(sm_count() * n, kMaxPlanCtas);
   const cudaError_t e = launch_pdl(paged_simt_kernel<T, NC>, dim3(a.ctas), dim3(kThreads),
-                                   simt_smem<NC>(), st, a);
+                                   SimtCfg<NC>::kSmem, st, a);
   return e == cudaSuccess ? launch_paged_merge(a, dtype, st) : e;
 }
 
@@ -270,7 +317,8 @@ cudaError_t launch_type(const PagedArgs& a, int dtype, cudaStream_t st) {
 cudaError_t launch_paged_simt(PagedArgs a, int dtype, cudaStream_t st) {
   paged_heads(&a, kRows);
   a.min_run = 4;
-  a.tile = a.one_set = kRows / a.gs;
+  a.tile = kRows / a.gs;
+  a.one_set = 1 << 30;
   a.key_shift = 6;
   return dtype == SV_BF16 ? launch_type<__nv_bfloat16>(a, dtype, st) : launch_type<float>(a, dtype, st);
 }
