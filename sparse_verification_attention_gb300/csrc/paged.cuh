@@ -73,7 +73,7 @@ __device__ __forceinline__ int weight_of(const PagedArgs& a, int n) { return n >
 // Prompt form: what the units of one head group of a segment cost, in keys of
 // one set of rows. Row tile t sees the keys before the segment's rows and
 // (t + 1) * tile of its own; starting and ending an item takes as long as
-// kItemCost key tiles besides.
+// item_cost key tiles besides.
 struct Cost {
   int w, base, tile, tiles;
 
@@ -95,7 +95,7 @@ struct Cost {
 };
 
 __device__ __forceinline__ Cost cost_of(const PagedArgs& a, int n, int ctx) {
-  return {weight_of(a, n), max(0, ctx - n) + (kItemCost << a.key_shift), a.tile, ceil_div(n, a.tile)};
+  return {weight_of(a, n), max(0, ctx - n) + (a.item_cost << a.key_shift), a.tile, ceil_div(n, a.tile)};
 }
 
 // Fill `p` (all threads of the CTA call it; barriers inside). scratch:
@@ -186,7 +186,7 @@ __device__ inline void make_plan(const PagedArgs& a, Plan* p, int* scratch) {
         const Cost c = cost_of(a, ns[id], ctxs[id]);
         units += (float)c.tiles * a.hv;
         cost += c.total() * a.hv;
-        most = fmaxf(most, (float)(kts[id] - c.w * (kItemCost << a.key_shift)));  // (both ways have the ends)
+        most = fmaxf(most, (float)(kts[id] - c.w * (a.item_cost << a.key_shift)));  // (both ways have the ends)
       }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) {
@@ -338,7 +338,7 @@ __device__ inline Item next_item(const PagedArgs& a, const Plan* p, Cursor* c) {
     const int off = local - hv * group - k.before(t), upto = min(cost, off + c->end - c->at);
     // the key tile that position x of a unit lies in
     auto tile_at = [&](int x) {
-      return key_tiles(a, max(0, (x + k.w - 1) / k.w - (kItemCost << a.key_shift)));
+      return key_tiles(a, max(0, (x + k.w - 1) / k.w - (a.item_cost << a.key_shift)));
     };
     Item it = make_item(a, s, id, t, hv, tile_at(off), upto == cost ? 1 << 28 : tile_at(upto));
     if (off > 0 || upto < cost) it.part = (2 * blockIdx.x + (off > 0 ? 0 : 1)) * slot_rows(a);

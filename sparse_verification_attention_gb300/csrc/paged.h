@@ -23,6 +23,7 @@ struct TablesArgs {
   int32_t* positions;         // [n_max] or null
   unsigned* status;           // may be null
   int B, blk, nb_max, num_pages, n_max;
+  int blk_shift;              // log2(blk), -1 if blk is no power of two
 };
 cudaError_t launch_build_tables(const TablesArgs& a, cudaStream_t st);
 
@@ -41,7 +42,6 @@ cudaError_t launch_write_kv(const WriteArgs& a, cudaStream_t st);
 constexpr int kMaxSegs = 1025;      // row segments of one call: sequences, and a shared prefix
 constexpr int kMaxPlanCtas = 640;   // CTAs of a launch at most
 constexpr int kItemsPerCta = 2;     // see make_plan
-constexpr int kItemCost = 4;        // key tiles' time that an item takes besides its own (make_plan)
 constexpr int kStreamCost = 8;      // key tiles' time that joining cut units takes (make_plan)
 constexpr int kSimtRows = 64;       // rows of an item on the CUDA cores
 constexpr int kTcRows = 128;        // rows of a set on the tensor cores; an item has two
@@ -84,8 +84,8 @@ struct PagedArgs {
   int gs, hs, hv;
   // the launch's work split (make_plan): CTAs, the fewest key tiles that a run
   // is worth, tokens of a row tile, tokens above which its rows are two sets,
-  // log2 of the keys of a key tile
-  int ctas, min_run, tile, one_set, key_shift;
+  // log2 of the keys of a key tile, key tiles' time that an item takes besides its own
+  int ctas, min_run, tile, one_set, key_shift, item_cost;
   int elt;                    // bytes of an element
   int out_wide;               // rows of out lie on 32-byte boundaries
   float scale_log2;           // log2(e) / sqrt(d)

@@ -130,7 +130,7 @@ sv_status sv_build_tables(int B, int blk, const int32_t* old_len, const int32_t*
                 "num_pages=%d n_max=%d)",
                 B, blk, nb_max, num_pages, n_max);
   if (B > kMaxRequests) return fail(SV_ERR_UNSUPPORTED, "B=%d requests exceeds %d", B, kMaxRequests);
-  if ((long long)num_pages * blk >= kInt || (long long)nb_max * blk >= kInt)
+  if ((long long)num_pages * blk >= kInt || (long long)nb_max * blk >= kInt - blk)
     return fail(SV_ERR_UNSUPPORTED, "num_pages=%d or nb_max=%d of %d tokens reaches 2^31", num_pages,
                 nb_max, blk);
   if (!old_len || !new_len || !block_table || !free_pages || !free_count || !free_count_out ||
@@ -140,7 +140,7 @@ sv_status sv_build_tables(int B, int blk, const int32_t* old_len, const int32_t*
                 "is NULL");
   const TablesArgs a{old_len, new_len, pinned, block_table, free_pages, free_count, free_count_out,
                      cu_new, slot_map, positions, static_cast<unsigned*>(workspace), B, blk, nb_max,
-                     num_pages, n_max};
+                     num_pages, n_max, blk & (blk - 1) ? -1 : __builtin_ctz(blk)};
   const cudaError_t e = launch_build_tables(a, (cudaStream_t)stream);
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "build_tables launch");
 }

@@ -11,6 +11,7 @@
 // a time; a thread computes 4 x 4 of S and 4 x 4 per 64 columns of O.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "internal.h"
 #include "paged.cuh"
@@ -223,28 +224,34 @@ __global__ void __launch_bounds__(kThreads, SimtCfg<NC>::kCtas) paged_simt_kerne
         for (int c = 0; c < 4 * NC; ++c) o[i][c] *= alpha;
       }
       __syncwarp();  // a row's P is written and read by the same half-warp
-      for (int k = 0; k < kKeys; k += 4) {
-        float4 p[4];
+      // O += P V; where the tile is masked, a masked key's V is not touched
+      auto product = [&](auto tag) {
+        constexpr bool select = decltype(tag)::value;
+        for (int k = 0; k < kKeys; k += 4) {
+          float4 p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (ty * 4 + i) * kPPitch + k);
+          for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (ty * 4 + i) * kPPitch + k);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
+          for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
-          for (int cg = 0; cg < NC; ++cg) {
-            const float4 v = *reinterpret_cast<const float4*>(sv + (k + kk) * kPitch + 64 * cg + 4 * tx);
+            for (int cg = 0; cg < NC; ++cg) {
+              const float4 v = *reinterpret_cast<const float4*>(sv + (k + kk) * kPitch + 64 * cg + 4 * tx);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
-              if (!masked || w >= 0.f || w != w) {
-                o[i][4 * cg] = fmaf(w, v.x, o[i][4 * cg]);
-                o[i][4 * cg + 1] = fmaf(w, v.y, o[i][4 * cg + 1]);
-                o[i][4 * cg + 2] = fmaf(w, v.z, o[i][4 * cg + 2]);
-                o[i][4 * cg + 3] = fmaf(w, v.w, o[i][4 * cg + 3]);
+              for (int i = 0; i < 4; ++i) {
+                const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+                if (!select || w >= 0.f || w != w) {
+                  o[i][4 * cg] = fmaf(w, v.x, o[i][4 * cg]);
+                  o[i][4 * cg + 1] = fmaf(w, v.y, o[i][4 * cg + 1]);
+                  o[i][4 * cg + 2] = fmaf(w, v.z, o[i][4 * cg + 2]);
+                  o[i][4 * cg + 3] = fmaf(w, v.w, o[i][4 * cg + 3]);
+                }
               }
             }
           }
         }
-      }
+      };
+      if (masked) product(std::true_type{});
+      else product(std::false_type{});
       __syncthreads();  // the stage is free again
       if (kStages == 1) {
         if (kt + 1 < it.nk) load(kt + 1, page);
@@ -319,6 +326,7 @@ cudaError_t launch_paged_simt(PagedArgs a, int dtype, cudaStream_t st) {
   a.min_run = 4;
   a.tile = kRows / a.gs;
   a.one_set = 1 << 30;
+  a.item_cost = 1;
   a.key_shift = 6;
   return dtype == SV_BF16 ? launch_type<__nv_bfloat16>(a, dtype, st) : launch_type<float>(a, dtype, st);
 }

@@ -990,6 +990,7 @@ cudaError_t launch_paged_tc(PagedArgs a, cudaStream_t st) {
   a.one_set = kRows / a.gs;
   a.tile = 2 * a.one_set;
   a.key_shift = 7;
+  a.item_cost = 4;
   a.out_wide = a.d % 16 == 0 && aligned(a.out, 32);
   CUtensorMap m[5];
   const cuuint64_t d = a.d, hd = (cuuint64_t)a.Hkv * a.d;
