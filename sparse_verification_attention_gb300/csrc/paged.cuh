@@ -104,10 +104,12 @@ __device__ __forceinline__ Cost cost_of(const PagedArgs& a, int n, int ctx) {
 // Segments go out in descending order of their units' cost, so that what starts
 // last is short (the prefix form's shared segment first).
 //
-// Prefix form: every segment's keys are cut into runs so that the grid gets
-// about kItemsPerCta items per CTA, handed out dynamically. Its partial rows
-// are then at most those of the uncut segments and kItemsPerCta items per CTA
-// more.
+// Prefix form: items go out dynamically. The shared segment's keys are cut into
+// the number of runs that is expected to end first (8 trees of 16 drafts over
+// 65536 shared tokens: 144 items for 152 CTAs 139 us, 160 items 185 us, 304 items
+// 156 us), the sequences' own so that they are about kOwnItemsPerCta items per CTA.
+// The partial rows are then at most those of the uncut segments and
+// kOwnItemsPerCta + kSharedItemsPerCta items per CTA more.
 //
 // Prompt form, one of two ways, whichever is expected to end earlier:
 //   whole units, handed out dynamically. Ends at about the average load
@@ -158,17 +160,49 @@ __device__ inline void make_plan(const PagedArgs& a, Plan* p, int* scratch) {
     int at = 0, row = 0;  // this lane's totals, then what lies before them
     if (a.prefix) {
       unsigned long long units = 0;
-      for (int i = b0; i < b1; ++i)
-        units += (unsigned long long)ceil_div(ns[i], a.tile) * a.hv * kts[i];
+      float own = 0.f;  // cost of the sequences' own units, in key tiles of one set
+      for (int i = b0; i < b1; ++i) {
+        const int n = ceil_div(ns[i], a.tile) * a.hv;
+        units += (unsigned long long)n * kts[i];
+        if (i) own += (float)n * (kts[i] * weight_of(a, ns[i]) + a.item_cost);
+      }
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) units += __shfl_xor_sync(0xffffffffu, units, off);
-      const unsigned parts = kItemsPerCta * a.ctas;
+      for (int off = 16; off > 0; off >>= 1) {
+        units += __shfl_xor_sync(0xffffffffu, units, off);
+        own += __shfl_xor_sync(0xffffffffu, own, off);
+      }
+      const unsigned parts = kOwnItemsPerCta * a.ctas;
       const unsigned long long want =
           units >> 31 ? (units + parts - 1) / parts : ((unsigned)units + parts - 1) / parts;
       const int run = (int)min(max(want, (unsigned long long)a.min_run), 1ull << 30);
+      // Lane l tries l + 1 runs and l + 33: rounds of shared items on every CTA, the
+      // last one shared with the own ones, and what joining takes.
+      const int kt0 = kts[0], n0 = ceil_div(ns[0], a.tile) * a.hv;
+      float best = INFINITY;
+      int shared = 1;
+      for (int s = lane + 1; s <= 64; s += 32) {
+        if (s > 1 && (n0 * (s - 1) > kSharedItemsPerCta * a.ctas || s * a.min_run > kt0)) continue;
+        const int len = ceil_div(kt0, s), items = n0 * (len ? ceil_div(kt0, len) : 0);
+        const float cost = (float)(len * weight_of(a, ns[0]) + a.item_cost);
+        const int rounds = items / a.ctas, rest = items - rounds * a.ctas;
+        const float end = rounds * cost + fmaxf(rest ? cost : 0.f, (rest * cost + own) / a.ctas) + 0.25f * s;
+        if (end < best) {
+          best = end;
+          shared = s;
+        }
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        const float e = __shfl_xor_sync(0xffffffffu, best, off);
+        const int s = __shfl_xor_sync(0xffffffffu, shared, off);
+        if (e < best || (e == best && s < shared)) {
+          best = e;
+          shared = s;
+        }
+      }
       for (int i = b0; i < b1; ++i) {
-        const int kt = kts[p->order[i]], n = ns[p->order[i]];
-        int s = kt > run ? ceil_div(kt, run) : 1;
+        const int id = p->order[i], kt = kts[id], n = ns[id];
+        int s = id == 0 ? shared : kt > run ? ceil_div(kt, run) : 1;
         if (s > 1) s = ceil_div(kt, ceil_div(kt, s));  // no empty run
         const int it = ceil_div(n, a.tile) * a.hv * s;
         p->split[i] = s;

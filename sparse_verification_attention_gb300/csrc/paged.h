@@ -41,7 +41,7 @@ cudaError_t launch_write_kv(const WriteArgs& a, cudaStream_t st);
 // ---------------------------------------------------------------- attention
 constexpr int kMaxSegs = 1025;      // row segments of one call: sequences, and a shared prefix
 constexpr int kMaxPlanCtas = 640;   // CTAs of a launch at most
-constexpr int kItemsPerCta = 2;     // see make_plan
+constexpr int kOwnItemsPerCta = 2, kSharedItemsPerCta = 2;  // prefix form, see make_plan
 constexpr int kStreamCost = 8;      // key tiles' time that joining cut units takes (make_plan)
 constexpr int kSimtRows = 64;       // rows of an item on the CUDA cores
 constexpr int kTcRows = 128;        // rows of a set on the tensor cores; an item has two

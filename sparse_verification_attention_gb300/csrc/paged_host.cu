@@ -41,7 +41,7 @@ PagedLayout prompt_layout(const sv_shape& s, int n_rows) {
 }
 
 // Partial rows: every row once in its shared tile and once in its own, and
-// the kItemsPerCta items per CTA that cutting adds.
+// the items per CTA that cutting adds (make_plan).
 PagedLayout prefix_layout(const sv_shape& s) {
   PagedArgs a{};
   a.Hkv = s.Hkv;
@@ -54,7 +54,7 @@ PagedLayout prefix_layout(const sv_shape& s) {
       return (size_t)((n + tile - 1) / tile) * std::min<long long>(tile, n) * a.gs * a.hv;
     };
     const size_t r = padded((long long)s.B * s.T) + s.B * padded(s.T) +
-                     (size_t)kItemsPerCta * kMaxPlanCtas * kSimtRows;
+                     (size_t)(kOwnItemsPerCta + kSharedItemsPerCta) * kMaxPlanCtas * kSimtRows;
     most = std::max(most, r);
   }
   return paged_layout(most, s.d);

@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kThreads, SimtCfg<NC>::kCtas) paged_simt_kerne
     const Item it = s_item;
     if (!it.valid) break;
     const int rows = it.ntok * it.heads;
+    const bool live = (tid >> 5) * 8 < rows;  // the warp's eight rows hold any
     // Q rows r = token * heads + head; rows past the tile's are zero
     for (int e = tid; e < kRows * 16 * NC; e += kThreads) {
       const int r = e / (16 * NC), c = e % (16 * NC) * 4;
@@ -176,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, SimtCfg<NC>::kCtas) paged_simt_kerne
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+      if (live)
 #pragma unroll 2
       for (int c = 0; c < 64 * NC; c += 4) {
         float4 x[4], y[4];
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, SimtCfg<NC>::kCtas) paged_simt_kerne
       // P = -1 and their V is not touched (it may hold anything)
       const bool masked = drafts || key0 + kKeys > (it.causal ? it.vis0 : it.ctx);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4 && live; ++i) {
         bool keep[4];
         float mx = -INFINITY;
 #pragma unroll
@@ -250,8 +252,10 @@ __global__ void __launch_bounds__(kThreads, SimtCfg<NC>::kCtas) paged_simt_kerne
           }
         }
       };
-      if (masked) product(std::true_type{});
-      else product(std::false_type{});
+      if (live) {
+        if (masked) product(std::true_type{});
+        else product(std::false_type{});
+      }
       __syncthreads();  // the stage is free again
       if (kStages == 1) {
         if (kt + 1 < it.nk) load(kt + 1, page);
@@ -323,7 +327,7 @@ cudaError_t launch_type(const PagedArgs& a, int dtype, cudaStream_t st) {
 
 cudaError_t launch_paged_simt(PagedArgs a, int dtype, cudaStream_t st) {
   paged_heads(&a, kRows);
-  a.min_run = 4;
+  a.min_run = 1;
   a.tile = kRows / a.gs;
   a.one_set = 1 << 30;
   a.item_cost = 1;
