@@ -178,6 +178,7 @@ __device__ inline void make_plan(const PagedArgs& a, Plan* p, int* scratch) {
       // Lane l tries l + 1 runs and l + 33: rounds of shared items on every CTA, the
       // last one shared with the own ones, and what joining takes.
       const int kt0 = kts[0], n0 = ceil_div(ns[0], a.tile) * a.hv;
+      const float join = (float)a.n_rows * a.Hq * (1.f / 16384.f);
       float best = INFINITY;
       int shared = 1;
       for (int s = lane + 1; s <= 64; s += 32) {
@@ -185,7 +186,7 @@ __device__ inline void make_plan(const PagedArgs& a, Plan* p, int* scratch) {
         const int len = ceil_div(kt0, s), items = n0 * (len ? ceil_div(kt0, len) : 0);
         const float cost = (float)(len * weight_of(a, ns[0]) + a.item_cost);
         const int rounds = items / a.ctas, rest = items - rounds * a.ctas;
-        const float end = rounds * cost + fmaxf(rest ? cost : 0.f, (rest * cost + own) / a.ctas) + 0.25f * s;
+        const float end = rounds * cost + fmaxf(rest ? cost : 0.f, (rest * cost + own) / a.ctas) + join * s;
         if (end < best) {
           best = end;
           shared = s;

@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(smem_u32(&sh.full[i]), 1);
-      mbar_init(smem_u32(&sh.empty[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), 3);  // the MMAs that read it, and both cleaning warps
       mbar_init(smem_u32(&sh.vclean[i]), 2);
     }
     for (int i = 0; i < 2; ++i) {
@@ -694,7 +694,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             sh.nonfinite[seq % kItems][min(kMaxMasked - 1, nk - 1 - j)][2 * w + lane] = bits[lane];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.vclean[s]));
+        // The stage is not filled again before this warp has seen it: a warp that
+        // came late to a K tile (which nothing else makes it hurry for) could
+        // otherwise find its barrier two phases on, and wait for ever.
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sh.vclean[s]));
+          mbar_arrive(smem_u32(&sh.empty[s]));
+        }
       }
       at += 2 * nk;
       done_item(seq);

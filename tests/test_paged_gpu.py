@@ -342,6 +342,23 @@ def test_prompt_many_sequences():
     P.check(c["out"], *prompt_want(c, ctx, new))
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,blk", [(32, 8, 128, 64), (8, 8, 64, 16)])
+def test_prompt_repeated_decoding_steps(Hq, Hkv, d, blk):
+    """Some thousand steps of many short items: no wait of any role ever runs out,
+    and every step gives the same bits."""
+    ctx = [(i * 997) % 1500 + 1 for i in range(40)] + [9000, 4097]
+    c = prompt_case(18, BF16, Hq, Hkv, d, blk, ctx, [1] * 42)
+    ws = api.alloc_prompt_workspace(c["shape"], 42)
+    assert run_prompt(c, ws) == 0
+    P.check(c["out"], *prompt_want(c, ctx, [1] * 42))
+    first = c["out"].clone()
+    for _ in range(4):
+        for _ in range(1000):
+            api.sv_prompt_attend(ws=ws, **c)
+        assert api.sv_read_status(ws) == 0
+        assert torch.equal(c["out"], first)
+
+
 def test_prompt_other_stream_and_graph():
     """On a side stream, and captured: a replay follows the lengths in device memory."""
     ctx, new = [400, 300], [100, 60]
