@@ -465,7 +465,8 @@ sv_status sv_sparse_attend_noalloc(const sv_shape* shape, const void* q, const s
  * SV_FLAG_BAD_LENGTH for a length outside [0, nb_max * blk] or a count
  * outside [0, num_pages] (clamped), more new tokens than n_max (the excess
  * gets pages but no slots) or more free pages than num_pages.
- * Limits: B <= 4096; num_pages * blk and nb_max * blk < 2^31. */
+ * Limits: B <= 4096; num_pages * blk, nb_max * blk and B * nb_max < 2^31;
+ * n_max <= 2^30. */
 sv_status sv_build_tables(int B, int blk, const int32_t* old_len, const int32_t* new_len,
                           const int32_t* pinned, int32_t* block_table, int nb_max,
                           int num_pages, int32_t* free_pages, const int32_t* free_count,

@@ -94,7 +94,7 @@ cudaError_t launch_paged(const PagedArgs& a, int dtype, cudaStream_t st) {
 sv_status check_rows(const sv_shape* s, const char* name, const void* p, long long stride, int heads) {
   if (!aligned(p, 16)) return fail(SV_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
   if (stride < (long long)heads * s->d || stride * (long long)elt_bytes(s) % 16 ||
-      stride >= (1ll << 40))
+      stride >= (1ll << 38))
     return fail(SV_ERR_INVALID_ARG,
                 "%s rows are %lld elements apart: need at least %d and a multiple of 16 bytes", name,
                 stride, heads * s->d);
@@ -129,6 +129,9 @@ sv_status sv_build_tables(int B, int blk, const int32_t* old_len, const int32_t*
                 "need B, blk, nb_max, num_pages >= 1 and n_max >= 0 (B=%d blk=%d nb_max=%d "
                 "num_pages=%d n_max=%d)",
                 B, blk, nb_max, num_pages, n_max);
+  if ((long long)B * nb_max >= kInt - (1 << 20) || n_max > 1 << 30)
+    return fail(SV_ERR_UNSUPPORTED, "a table of %d x %d blocks or n_max=%d new tokens is too large", B,
+                nb_max, n_max);
   if (B > kMaxRequests) return fail(SV_ERR_UNSUPPORTED, "B=%d requests exceeds %d", B, kMaxRequests);
   if ((long long)num_pages * blk >= kInt || (long long)nb_max * blk >= kInt - blk)
     return fail(SV_ERR_UNSUPPORTED, "num_pages=%d or nb_max=%d of %d tokens reaches 2^31", num_pages,

@@ -31,11 +31,11 @@ template <typename T>
 __device__ __forceinline__ float4 load4(const T* p);
 template <>
 __device__ __forceinline__ float4 load4<float>(const float* p) {
-  return __ldg(reinterpret_cast<const float4*>(p));
+  return __ldcg(reinterpret_cast<const float4*>(p));
 }
 template <>
 __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+  const uint2 u = __ldcg(reinterpret_cast<const uint2*>(p));
   const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
   const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
   return make_float4(lo.x, lo.y, hi.x, hi.y);
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, SimtCfg<NC>::kCtas) paged_simt_kerne
     auto lookup = [&](int kt) {
       const int key = (it.k0 + kt) * kKeys + (tid >> 2);
       if (kt >= it.nk || (it.draft && kt == it.nk - 1) || key >= it.ctx) return -1;
-      const int page = __ldg(a.block_table + it.tab + key / a.blk);
+      const int page = __ldcg(a.block_table + it.tab + key / a.blk);
       if (page >= 0 && page < a.num_pages) return page;
       if ((tid & 3) == 0) atomicOr(a.status, SV_FLAG_BAD_PAGE);
       return -1;

@@ -441,6 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kMmaWarp) regs_shrink<kRegsOther>();
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------ items, copies
+    // earlier kernels' plain stores to the pools come before this one's bulk copies
+    asm volatile("fence.proxy.async.global;" ::: "memory");
     const int box_rows = min(a.blk, kKeys), ppt = kKeys / box_rows;
     const int oob = a.num_pages * a.Hkv * a.blk;  // past the pool: TMA fills zeros
     // lane -> (page of the tile, column half) of one box
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mine && j < it.nk && !(it.draft && j == it.nk - 1)) {
           const int key = (it.k0 + j) * kKeys + pg * box_rows;
           if (key < it.ctx) {
-            const int page = __ldg(a.block_table + it.tab + key / a.blk);
+            const int page = __ldcg(a.block_table + it.tab + key / a.blk);
             if (page >= 0 && page < a.num_pages)
               row = (page * a.Hkv + it.kvh) * a.blk + key % a.blk;
             else if (half == 0)

@@ -37,6 +37,8 @@ def test_build_tables_refusals(L):
         refused(L, f, with_arg(ok, i, 0), api.SV_ERR_INVALID_ARG, "need B")
     refused(L, f, with_arg(ok, 14, -1), api.SV_ERR_INVALID_ARG, "n_max")
     refused(L, f, with_arg(ok, 0, 4097), api.SV_ERR_UNSUPPORTED, "4097 requests")
+    refused(L, f, with_arg(ok, 14, (1 << 30) + 1), api.SV_ERR_UNSUPPORTED, "too large")
+    refused(L, f, with_arg(with_arg(ok, 0, 4096), 6, 1 << 19), api.SV_ERR_UNSUPPORTED, "too large")
     refused(L, f, with_arg(ok, 7, 1 << 27), api.SV_ERR_UNSUPPORTED, "2^31")
     refused(L, f, with_arg(ok, 6, 1 << 27), api.SV_ERR_UNSUPPORTED, "2^31")
     for i in (2, 3, 5, 8, 9, 10, 11, 12):
