@@ -440,8 +440,10 @@ __device__ inline void merge_row(const PagedArgs& a, const Group (&g)[2], T* dst
     return j < g[0].runs ? g[0].row + (long long)j * g[0].step
                          : g[1].row + (long long)(j - g[0].runs) * g[1].step;
   };
-  float M = -INFINITY;
-  for (int j = lane; j < total; j += 32) M = fmaxf(M, __ldcg(a.part_ml + row_at(j)).x);
+  float2 ml = make_float2(-INFINITY, 0.f);  // of partial row j0 + lane
+  if (lane < total) ml = __ldcg(a.part_ml + row_at(lane));
+  float M = ml.x;
+  for (int j = lane + 32; j < total; j += 32) M = fmaxf(M, __ldcg(a.part_ml + row_at(j)).x);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
@@ -449,10 +451,10 @@ __device__ inline void merge_row(const PagedArgs& a, const Group (&g)[2], T* dst
   for (int j0 = 0; j0 < total; j0 += 32) {
     float w = 0.f, wl = 0.f;
     if (j0 + lane < total) {
-      const float2 ml = __ldcg(a.part_ml + row_at(j0 + lane));
+      if (j0) ml = __ldcg(a.part_ml + row_at(j0 + lane));
+      // a run without a visible key has weight 0 (a NaN sum stays one)
       w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
       wl = w * ml.y;
-      // a run without a visible key has weight 0 (a NaN maximum stays one)
     }
     const int nj = min(32, total - j0);
 #pragma unroll 8

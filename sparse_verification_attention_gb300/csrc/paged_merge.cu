@@ -3,7 +3,11 @@
 // inside the attention: one CTA merging a tile's rows held up its next item
 // (a 16-sequence decoding step waited about 5 us an item), and in the prefix form
 // the last shared item completes the rows of the whole batch at once (that
-// merge took longer than the attention).
+// merge took longer than the attention: 48 single-token steps over a shared
+// prefix 228 us with it, 182 us without).
+//
+// Bound by latency: three dependent loads (what to join, the maxima and sums, the
+// rows) behind the attention's end, 4 to 10 us of a launch measured alone.
 #include <algorithm>
 
 #include "internal.h"

@@ -18,13 +18,27 @@
 // Either way two independent softmax chains overlap with each other's products.
 //
 // Warps: 0-7 and 8-15 the softmax of set 0 and 1, 16 issues every MMA, 17 takes
-// items from the scheduler, looks pages up and issues the TMA copies, 18-19
-// clear non-finite values out of V tiles that the mask cuts (below). Two
-// threads share a row: each takes half of a tile's keys and they exchange
-// their maxima.
+// items off the plan, looks pages up and issues the TMA copies, 18-19 clear
+// non-finite values out of V tiles that the mask cuts (below). Two threads share a
+// row: each takes half of a tile's keys. They agree on the row's reference m from
+// the tiles before, so neither waits for the other inside a tile (see softmax).
 // Per set and key tile the MMA warp issues P V of one tile and then S of the
-// next, so that the tensor cores work on the other set while this one's
-// softmax runs.
+// next, so that the tensor cores work on the other set while this one's softmax
+// runs; TMEM has no room for a second S, P and O of 128 x 128 per set.
+//
+// What bounds it, long prompts: the tensor cores and their hand-offs. A 32768-token
+// prompt of 32/8 heads takes 5.63 ms, 1.56 PFLOP/s, 0.82 of the measured bf16
+// burst rate and 0.91 of the sustained one (1.98 GHz at the power limit); with the
+// softmax cut down to a copy it took 5.36 ms. What the steps gave, at that size: one
+// thread a row and an MMA warp issuing from a branch of one lane 7.64 ms;
+// warp-uniform issue and two threads a row 6.86; waiters suspended instead of
+// polling (the polls took issue slots from the softmax) 6.39; the halves agreeing a
+// tile late 6.19; unmasked tiles in a copy of their own 6.04; the item's geometry in
+// shared memory instead of registers 5.67. Halves of S as separate products of 64
+// keys (four chains instead of two) were slower, 6.90: at N = 64 the operands'
+// shared-memory reads bound the product.
+// Few rows over long contexts: HBM, with the ring's 128 KB in flight per SM. A
+// 16-sequence decoding step reads 645 MB in 121 us, 0.78 of the measured copy rate.
 //
 // Masked keys have P = 0, but 0 times a non-finite V is not 0: V tiles with a
 // masked key (behind the diagonal, past the context, drafts another draft does
@@ -56,7 +70,7 @@ constexpr int kItemReaders = 19;      // MMA, 16 softmax and 2 cleaning warps
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;   // O follows the maximum in steps of more than 2^8
 constexpr float kFixLog2 = 64.0f;
-constexpr int kMaxMasked = 4;         // masked key tiles of an item, at most 3 (see masked_from)
+constexpr int kMaxMasked = 4;         // masked key tiles of an item, at most 3 (see run_of)
 // registers per thread of the softmax warps and of the others (the launch
 // gives 96 to each of 640 threads: 512 * 104 + 128 * 64 = 640 * 96)
 constexpr int kRegsSoftmax = 104, kRegsOther = 64;
