@@ -205,7 +205,8 @@ HEADS = [  # dtype, Hq, Hkv, d, blk
     (BF16, 8, 2, 128, 64), (BF16, 4, 4, 64, 16), (BF16, 7, 1, 128, 32), (BF16, 6, 2, 96, 64),
     (BF16, 8, 1, 128, 128), (BF16, 2, 1, 40, 8), (BF16, 4, 2, 256, 64), (BF16, 3, 1, 128, 48),
     (BF16, 40, 1, 64, 256), (BF16, 129, 1, 64, 16), (F32, 4, 2, 64, 16), (F32, 3, 3, 128, 64),
-    (F32, 5, 1, 200, 5), (F32, 70, 1, 16, 16)]
+    (F32, 5, 1, 200, 5), (F32, 70, 1, 16, 16), (BF16, 2, 2, 8, 32), (BF16, 5, 1, 128, 512),
+    (BF16, 128, 1, 64, 16), (F32, 2, 1, 256, 7)]
 LENS = [  # ctx, new
     ([1], [1]), ([2, 1, 3], [2, 1, 3]), ([63, 64, 65, 127, 128, 129], [63, 64, 65, 127, 128, 129]),
     ([300, 1000, 5], [300, 7, 1]), ([700], [700]), ([1500, 1, 2049], [1, 1, 1]),
@@ -234,6 +235,40 @@ def test_prompt_split_runs(dtype, d):
         P.check(first, *prompt_want(c, ctx, new))
         assert run_prompt(c, ws) == 0  # the counts are back at zero ...
         assert torch.equal(first, c["out"])  # ... and the result does not depend on the order
+
+
+def test_prompt_very_long_context():
+    ctx, new = [200001, 7], [2, 7]
+    c = prompt_case(4, BF16, 4, 1, 64, 64, ctx, new)
+    assert run_prompt(c) == 0
+    P.check(c["out"], *prompt_want(c, ctx, new))
+
+
+@pytest.mark.parametrize("dtype,pages", [(BF16, 36000), (F32, 18000)])
+def test_pools_past_4_gib(dtype, pages):
+    """Pages whose bytes lie past 2^32 of the pool (and elements past 2^31 in bf16):
+    rows written, attended as a prompt and as a shared prefix."""
+    Hq, Hkv, d, blk, n, T = 16, 8, 128, 64, 300, 2
+    g = gen(6)
+    kp, vp = (torch.empty(pages, Hkv, blk, d, dtype=dtype, device="cuda") for _ in range(2))
+    table = i32([[pages - 1, pages - 3, 0, pages - 2, 7]])
+    q, k, v = (torch.randn(n, h, d, generator=g).to(dtype).cuda() for h in (Hq, Hkv, Hkv))
+    p = torch.arange(n, device="cuda")
+    slots = (table[0].long()[p // blk] * blk + p % blk).to(torch.int32)
+    shape = api.make_shape(1, Hq, Hkv, d, blk, T, dtype)
+    ws = api.alloc_prompt_workspace(shape, n)
+    out = torch.empty_like(q)
+    api.sv_write_kv(shape, k, v, slots, kp, vp, ws)
+    api.sv_prompt_attend(shape, q, kp, vp, table, i32([n]), i32([0, n]), out, ws)
+    assert api.sv_read_status(ws) == 0
+    P.check(out, *P.attend(q, k, v, P.causal(n, n, "cuda")))
+    kv = api.make_kv(kp, vp, table, n)
+    dq, dk, dv, dout = q[None, :T].contiguous(), k[None, :T].contiguous(), v[None, :T].contiguous(), out[None, :T].clone()
+    wp = api.alloc_prefix_workspace(shape)
+    api.sv_prefix_attend(shape, dq, kv, 3, dk, dv, None, dout, wp)
+    assert api.sv_read_status(wp) == 0
+    see = torch.cat([torch.ones(T, n, dtype=torch.bool, device="cuda"), P.draft_mask(None, T, "cuda")], 1)
+    P.check(dout[0], *P.attend(dq[0], torch.cat([k, dk[0]]), torch.cat([v, dv[0]]), see))
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -464,6 +499,26 @@ def test_prefix_infinities_behind_the_mask():
         touched[0, :, :2, 5] = sees[:, None]
         P.check(c["out"][~touched], want[~touched], tol[~touched])
         assert (c["out"][touched] == float("inf")).all()
+
+
+def test_prefix_captured():
+    """A captured call replays on new drafts, on another stream, after other calls."""
+    c, want, tol = prefix_case(37, BF16, 8, 2, 128, 64, 4, 9, [100, 30, 0])
+    ws = api.alloc_prefix_workspace(c["shape"])
+    api.sv_prefix_attend(ws=ws, **c)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.sv_prefix_attend(ws=ws, **c)
+    c["q"].neg_()
+    other = torch.empty_like(c["out"])
+    api.sv_prefix_attend(ws=ws, **{**c, "out": other})
+    c["q"].neg_()
+    c["out"].fill_(7.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert api.sv_read_status(ws) == 0
+    P.check(c["out"], want, tol)
+    assert not torch.equal(other, c["out"])
 
 
 # ------------------------------------------------------------------ together
