@@ -197,7 +197,7 @@ def make_kv(k_pool: torch.Tensor, v_pool: Optional[torch.Tensor], block_table: t
                              f"{block_table.shape[0]} sequences")
         arr = (C.c_int32 * len(seq_ctx))(*[int(c) for c in seq_ctx])
         kv._seq_ctx_keep = arr
-        kv.seq_ctx = C.cast(arr, C.POINTER(C.c_int32))
+        kv.seq_ctx = arr
     return kv
 
 
