@@ -263,6 +263,8 @@ __device__ inline void make_plan(const PagedArgs& a, Plan* p, int* scratch) {
     }
     if (lane == 31) p->first[nseg] = at;
   }
+  // the scratch is done with: the bulk copies that the caller may send there come behind it
+  fence_proxy_async_shared();
   __syncthreads();
 }
 

@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           bits[0] = __reduce_or_sync(0xffffffffu, bits[0]);
           bits[1] = __reduce_or_sync(0xffffffffu, bits[1]);
-          if (bits[0] | bits[1]) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (bits[0] | bits[1]) fence_proxy_async_shared();
           if (lane < 2)
             sh.nonfinite[seq % kItems][min(kMaxMasked - 1, nk - 1 - j)][2 * w + lane] = bits[lane];
         }
