@@ -503,7 +503,8 @@ size_t sv_prefix_workspace_bytes(const sv_shape* shape);
  * 0 .. seq_ctx[b] - n_b + i. So n_b = seq_ctx[b] is a whole prompt, n_b <
  * seq_ctx[b] a chunk on top of what is cached, n_b = 1 a decoding step; one
  * call may mix them. A row that sees no key (seq_ctx[b] < n_b; flagged) is
- * zero. Rows behind cu_q[B] are not read or written.
+ * zero. Rows of q behind cu_q[B] may hold anything (a copy may fetch them; no
+ * result depends on them), rows of out behind it are not written.
  * q: [n_rows, Hq, d], rows q_stride ELEMENTS apart (>= Hq * d, a multiple of
  * 16 bytes); out: [n_rows, Hq, d] dense. seq_ctx [B] and cu_q [B + 1] are
  * DEVICE int32 (cu_q ascending from 0, cu_q[B] <= n_rows): nothing is read

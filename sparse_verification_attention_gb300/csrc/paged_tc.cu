@@ -762,11 +762,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Little of an item is kept in registers over its key tiles (the inner
       // loop needs them all): what the mask and the results need is read again
       // from shared memory.
-      bool live;  // a warp without rows only keeps step
+      bool mine_valid, live;  // a warp without rows only keeps step
       int kt, kt_end, stride, plain;
       {
         const Run run = run_of(it, tt);
-        live = __any_sync(0xffffffffu, row_of(it, run, X, r).valid);
+        mine_valid = row_of(it, run, X, r).valid;
+        live = __any_sync(0xffffffffu, mine_valid);
         kt = run.pair ? 0 : X;
         kt_end = run.pair ? run.n[X] : it.nk;
         stride = run.pair ? 1 : 2;
@@ -790,6 +791,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // exponents. When one of them finds a maximum more than 2^kFixLog2 above the
       // reference, its warp moves it at once for both halves; the other half
       // recognises that in the next tile, by the same comparison.
+      // This half's maximum of a row that is not one of the item's is -inf: such a row
+      // (another sequence's queries, padding, or what the slot held before) must not
+      // move the references of the rows beside it, whose rounding goes with them.
+      auto top_score = [&](const uint32_t(&v)[64]) {
+        return mine_valid ? max64(v) * a.scale_log2 : -INFINITY;
+      };
       auto catch_up = [&](float other) {  // the other half's maximum of the last tile
         if (__any_sync(0xffffffffu, other > m_run + kFixLog2)) move_ref(fmaxf(m_run, fmaxf(mine, other)));
       };
@@ -831,14 +838,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(keep[i >> 5] >> (i & 31) & 1u)) v[i] = 0xff800000u;  // -inf
           }
           if (general && start) {
-            mine = max64(v) * a.scale_log2;
+            mine = top_score(v);
             sh.mx[odd][X][H][r] = mine;
             if (!meet_half()) return false;
             m_run = fmaxf(mine, sh.mx[odd][X][H ^ 1][r]);
           }
           uint64_t sum = exponentials(v, tS, m_run, a.scale_log2);
           if (!(general && start)) {
-            mine = max64(v) * a.scale_log2;
+            mine = top_score(v);
             sh.mx[odd][X][H][r] = mine;
             const bool fix = __any_sync(0xffffffffu, mine > m_run + kFixLog2);
             tc::wait_st();
