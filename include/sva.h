@@ -444,7 +444,8 @@ sv_status sv_sparse_attend_noalloc(const sv_shape* shape, const void* q, const s
  *   - a request that grows gets pages for blocks nb(old) .. nb(new) - 1,
  *     taken from the top of the stack in ascending (request, block) order
  *     after all releases of the call. A release is thereby the exact inverse
- *     of the allocation it mirrors;
+ *     of the allocation it mirrors, also of one that ran out of pages: a
+ *     released block whose table entry is -1 has no page, and none is pushed;
  *   - cu_new[b] = new tokens of the requests before b, cu_new[B] of all;
  *   - new token i of the call (requests in order, positions ascending) at
  *     position p of request b gets slot_map[i] = page * blk + p % blk and,

@@ -49,6 +49,38 @@ __device__ __forceinline__ int owner(const int* start, int B, int i) {
   return lo;
 }
 
+// Block of item i of the releases, in [0, num_pages), -1 for an entry outside the
+// pool, kNoPage for a block that never got one.
+constexpr int kNoPage = -2;
+__device__ __forceinline__ int released_page(const TablesArgs& a, const int* s_rel, int i) {
+  const int b = owner(s_rel, a.B, i);
+  const int page = a.block_table[(size_t)b * a.nb_max + lens_of(a, b).keep + i - s_rel[b]];
+  return page == -1 ? kNoPage : page < 0 || page >= a.num_pages ? -1 : page;
+}
+
+// Push the releases again, the blocks without a page left out (all threads of one
+// CTA): from the last one on, a round of kTabThreads at a time. Returns their number.
+__device__ inline int push_held(const TablesArgs& a, const int* s_rel, int R, int count) {
+  __shared__ int s_held[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int before = 0;
+  for (int end = R; end > 0; end -= kTabThreads) {
+    const int i = end - 1 - (int)threadIdx.x;
+    const int page = i >= 0 ? released_page(a, s_rel, i) : kNoPage;
+    const unsigned held = __ballot_sync(0xffffffffu, page != kNoPage);
+    if (lane == 0) s_held[warp] = __popc(held);
+    __syncthreads();
+    int rank = before + __popc(held & ((1u << lane) - 1u));
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) rank += s_held[w];
+      before += s_held[w];
+    }
+    if (page != kNoPage && (long long)count + rank < a.num_pages) a.free_pages[count + rank] = page;
+    __syncthreads();
+  }
+  return before;
+}
+
 // One thread-block cluster does the whole call. Every CTA scans the lengths
 // of all requests into shared memory (three exclusive sums: blocks let go,
 // blocks taken, new tokens); the CTAs then share the lists' items. The
@@ -56,7 +88,10 @@ __device__ __forceinline__ int owner(const int* start, int B, int i) {
 // (request, block) list of releases goes to stack[count + R - 1 - i], item i
 // of the allocations comes from stack[count + R - 1 - i], so the result does
 // not depend on the order of execution and a release undoes the allocation it
-// mirrors. One cluster barrier separates the two.
+// mirrors. One cluster barrier separates the two. (Blocks for which an earlier call
+// found no page have none to give back and break that numbering: where a thread
+// meets one, all CTAs are told ahead of the barrier, and one CTA pushes the
+// releases again, counted.)
 //
 // Latency bound (a step of a decoding batch moves a few KB): one launch, no
 // atomics, two dependent rounds of loads before the barrier, two after. Both a
@@ -73,6 +108,15 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const __grid_
   const int ncta = gridDim.x, rank = blockIdx.x;
   const int step = ncta * kTabThreads, first = rank * kTabThreads + tid;
   unsigned flags = 0;
+  __shared__ int s_missing, s_pushed;  // written by any CTA of the cluster
+  if (tid == 0) s_missing = 0;
+  __syncwarp();
+  if (ncta > 1) cluster_arrive();
+  auto tell = [&](int* word, int value) {
+    for (int r = 0; r < ncta; ++r)
+      if (ncta > 1) st_cluster_u32(cluster_map(smem_u32(word), r), value);
+      else *word = value;
+  };
 
   pdl_wait();
   pdl_trigger();
@@ -142,24 +186,36 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const __grid_
   __syncthreads();
 
   const int count = min(max(*a.free_count, 0), a.num_pages);
-  const int top = min((long long)count + R, (long long)a.num_pages);
-  if (count != *a.free_count || (long long)count + R > a.num_pages || N > a.n_max)
-    flags |= SV_FLAG_BAD_LENGTH;
+  if (count != *a.free_count || N > a.n_max) flags |= SV_FLAG_BAD_LENGTH;
 
   // releases, onto the stack in descending (request, block) order
+  bool missing = false;
   for (int i = first; i < R; i += step) {
-    const int b = owner(s_rel, a.B, i);
-    const int j = lens_of(a, b).keep + i - s_rel[b];
-    int page = a.block_table[(size_t)b * a.nb_max + j];
-    if (page < 0 || page >= a.num_pages) {
-      flags |= SV_FLAG_BAD_PAGE;
-      page = -1;
-    }
+    const int page = released_page(a, s_rel, i);
+    if (page == -1) flags |= SV_FLAG_BAD_PAGE;
+    missing |= page == kNoPage;
     const long long at = (long long)count + R - 1 - i;
     if (at < a.num_pages) a.free_pages[at] = page;
   }
+  __syncwarp();
+  if (ncta > 1) cluster_wait();  // every s_missing has been set to zero
+  if (missing) tell(&s_missing, 1);
+  __syncwarp();
   if (ncta > 1) cluster_sync_all();
   else __syncthreads();
+  int pushed = R;
+  if (s_missing) {
+    if (rank == 0) {
+      pushed = push_held(a, s_rel, R, count);
+      if (tid == 0) tell(&s_pushed, pushed);
+      __syncwarp();
+    }
+    if (ncta > 1) cluster_sync_all();
+    else __syncthreads();
+    pushed = s_pushed;
+  }
+  const int top = min((long long)count + pushed, (long long)a.num_pages);
+  if ((long long)count + pushed > a.num_pages) flags |= SV_FLAG_BAD_LENGTH;
 
   // allocations, from the top of the stack in ascending (request, block) order
   auto taken = [&](int i) {

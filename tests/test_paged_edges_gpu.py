@@ -1,6 +1,8 @@
 """The paged-cache operators where calls of the documentation meet edges: plans
 of very many sequences, rows that are not part of a tile, empty caches, pools
 that ran out, large batches."""
+import random
+
 import pytest
 import torch
 
@@ -105,3 +107,63 @@ def test_attention_after_other_calls_changes_no_bit(Hq, Hkv, d):
             P.check(got[1], want, tol)
         for x, y in zip(got, first):
             same(x, y, f"after a call with rows of size {size}")
+
+
+# ------------------------------------------------------------------ pools that run out
+def test_tables_release_undoes_an_allocation_that_ran_out():
+    """8 blocks wanted, 6 pages there: giving the blocks back gives back these 6 pages."""
+    got = G.run_tables(4, [0, 0], [12, 20], [[-7] * 5, [-7] * 5], [0, 1, 2, 3, 4, 5], 6, 32)
+    assert got[6] == api.SV_FLAG_NO_PAGE and got[2] == [0]
+    assert got[0] == [[5, 4, 3, -7, -7], [2, 1, 0, -1, -1]]
+    back = G.run_tables(4, [12, 20], [0, 0], got[0], got[1], 0, 0)
+    assert back[6] == 0 and back[2] == [6] and back[1] == [0, 1, 2, 3, 4, 5]
+
+
+def model(blk, old, new, pinned, table, stack, count):
+    """sv_build_tables on lists, blocks without a page (-1) and an empty stack included."""
+    table, stack = [list(r) for r in table], list(stack)
+    for b in reversed(range(len(old))):
+        for j in reversed(range(max(P.nb(new[b], blk), pinned[b]), P.nb(old[b], blk))):
+            if table[b][j] != -1:
+                stack[count] = table[b][j]
+                count += 1
+    cu, slots, pos, short, held = [0], [], [], False, False
+    for b in range(len(old)):
+        for j in range(P.nb(old[b], blk), P.nb(new[b], blk)):
+            count, table[b][j] = (count - 1, stack[count - 1]) if count else (0, -1)
+            short |= table[b][j] < 0
+        for p in range(old[b], new[b]):
+            page = table[b][p // blk]
+            held |= page < 0 and p // blk < P.nb(old[b], blk)
+            slots.append(page * blk + p % blk if page >= 0 else -1)
+            pos.append(p)
+        cu.append(len(slots))
+    flags = (api.SV_FLAG_NO_PAGE if short else 0) | (api.SV_FLAG_BAD_PAGE if held else 0)
+    return table, stack, count, cu, slots, pos, flags
+
+
+@pytest.mark.parametrize("B,blk,most,n_max", [
+    (5, 4, 30, 200), (300, 8, 60, 4096), (300, 8, 60, 20000), (90, 16, 900, 70000), (4000, 3, 20, 90000)])
+@pytest.mark.parametrize("share", [0.3, 0.8])
+def test_tables_steps_around_an_empty_pool(B, blk, most, n_max, share):
+    """Requests come, grow and end while the pool keeps running out: no page is lost or
+    held twice, on one CTA, eight and sixteen."""
+    r = random.Random(B + int(10 * share))
+    nb_max = P.nb(most, blk) + 1
+    pages = max(3, int(share * B * nb_max / 2))
+    table, stack, count = [[-1] * nb_max for _ in range(B)], list(range(pages)), pages
+    r.shuffle(stack)
+    old = [0] * B
+    for _ in range(6):
+        new = [r.choice([0, n, min(n + 1, most), r.randint(0, most), r.randint(0, most)]) for n in old]
+        want = model(blk, old, new, [0] * B, table, stack, count)
+        got = G.run_tables(blk, old, new, table, stack, count, n_max, in_place=True)
+        rest = [-1] * (n_max - len(want[4]))
+        assert len(want[4]) <= n_max and got[6] == want[6]
+        assert got[2] == [want[2]] and got[3] == want[3]
+        assert got[0] == want[0]
+        assert got[1][:want[2]] == want[1][:want[2]]
+        assert got[4] == want[4] + rest and got[5] == want[5] + rest
+        table, stack, count, old = got[0], got[1], got[2][0], new
+        held = [p for row, n in zip(table, old) for p in row[:P.nb(n, blk)] if p >= 0]
+        assert sorted(held + stack[:count]) == list(range(pages))
