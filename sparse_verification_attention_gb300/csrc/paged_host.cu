@@ -253,13 +253,16 @@ sv_status sv_prefix_attend(const sv_shape* shape, const void* q, const sv_kv* kv
   a.q = q;
   a.q_stride = (long long)shape->Hq * shape->d;
   a.n_rows = shape->B * shape->T;
-  a.k_pool = kv->k_pool;
-  a.v_pool = kv->v_pool;
+  int most = kv->ctx;  // the longest context
+  for (int b = 0; kv->seq_ctx && b < shape->B; ++b) most = b ? std::max(most, kv->seq_ctx[b]) : kv->seq_ctx[b];
+  // without a single token there need not be a pool (check_kv): none is read
+  a.k_pool = most ? kv->k_pool : draft_k;
+  a.v_pool = most ? kv->v_pool : draft_v;
   a.draft_k = draft_k;
   a.draft_v = draft_v;
   a.block_table = kv->block_table;
   a.nb_max = kv->nb_max;
-  a.num_pages = kv->num_pages;
+  a.num_pages = most ? kv->num_pages : 0;
   a.out = out;
   a.prefix = 1;
   a.T = shape->T;

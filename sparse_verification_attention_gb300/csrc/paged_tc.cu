@@ -1024,18 +1024,18 @@ cudaError_t launch_paged_tc(PagedArgs a, cudaStream_t st) {
   CUtensorMap m[5];
   const cuuint64_t d = a.d, hd = (cuuint64_t)a.Hkv * a.d;
   {
-    const cuuint64_t dims[2] = {d, (cuuint64_t)a.num_pages * a.Hkv * a.blk}, strides[1] = {d * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)std::min(a.blk, kKeys)};
-    if (!encode(&m[0], a.k_pool, 2, dims, strides, box) || !encode(&m[1], a.v_pool, 2, dims, strides, box))
-      return cudaErrorInvalidValue;
-  }
-  {
     const cuuint64_t dims[3] = {d, (cuuint64_t)a.Hq, (cuuint64_t)a.n_rows};
     const cuuint64_t strides[2] = {d * 2, (cuuint64_t)a.q_stride * 2};
     const cuuint32_t box[3] = {64, (cuuint32_t)a.gs, (cuuint32_t)(kRows / a.gs)};
     if (!encode(&m[2], a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  m[3] = m[4] = m[2];
+  m[0] = m[1] = m[3] = m[4] = m[2];  // (a map that no copy uses has to be one all the same)
+  if (a.num_pages > 0) {
+    const cuuint64_t dims[2] = {d, (cuuint64_t)a.num_pages * a.Hkv * a.blk}, strides[1] = {d * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)std::min(a.blk, kKeys)};
+    if (!encode(&m[0], a.k_pool, 2, dims, strides, box) || !encode(&m[1], a.v_pool, 2, dims, strides, box))
+      return cudaErrorInvalidValue;
+  }
   if (a.prefix) {
     const cuuint64_t dims[4] = {d, (cuuint64_t)a.Hkv, (cuuint64_t)a.T, (cuuint64_t)a.B};
     const cuuint64_t strides[3] = {d * 2, hd * 2, hd * 2 * a.T};

@@ -167,3 +167,27 @@ def test_tables_steps_around_an_empty_pool(B, blk, most, n_max, share):
         table, stack, count, old = got[0], got[1], got[2][0], new
         held = [p for row, n in zip(table, old) for p in row[:P.nb(n, blk)] if p >= 0]
         assert sorted(held + stack[:count]) == list(range(pages))
+
+
+# ------------------------------------------------------------------ empty caches
+@pytest.mark.parametrize("dtype,d,T", [(BF16, 128, 4), (BF16, 64, 1), (BF16, 256, 3), (F32, 64, 4), (F32, 200, 1)])
+@pytest.mark.parametrize("pool", ["none", "no pages", "pages"])
+def test_prefix_of_an_empty_cache(dtype, d, T, pool):
+    """No sequence has a token: the drafts see the drafts, with or without a pool, as in
+    sv_sparse_attend over every block."""
+    B, Hq, Hkv, blk = 3, 4, 2, 16
+    g = G.gen(71)
+    q, dk, dv = (torch.randn(B, T, h, d, generator=g).to(dtype).cuda() for h in (Hq, Hkv, Hkv))
+    shape = api.make_shape(B, Hq, Hkv, d, blk, T, dtype)
+    pages = torch.full((2 if pool == "pages" else 0, Hkv, blk, d), float("nan"), dtype=dtype, device="cuda")
+    table = torch.full((B, 1), -1, dtype=torch.int32, device="cuda")
+    kv = api.KV(None, None, None, 0, 0, 0) if pool == "none" else api.make_kv(pages, pages, table, 0)
+    out, plain = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+    ws, w0 = api.alloc_prefix_workspace(shape), api.alloc_workspace(shape, 1, 1)
+    api.sv_prefix_attend(shape, q, kv, 0, dk, dv, None, out, ws)
+    api.sv_sparse_attend(shape, q, kv, None, 0, 0, dk, dv, None, plain, w0)
+    assert api.sv_read_status(ws) == api.sv_read_status(w0) == 0
+    for b in range(B):
+        want, tol = P.attend(q[b], dk[b], dv[b], P.draft_mask(None, T, "cuda"))
+        P.check(out[b], want, tol)
+        P.check(plain[b], want, tol)
