@@ -187,10 +187,11 @@ def make_kv(k_pool: torch.Tensor, v_pool: Optional[torch.Tensor], block_table: t
             ctx: int, seq_ctx: Optional[Sequence[int]] = None) -> KV:
     """The cache descriptor. seq_ctx (one prefix length per sequence, kept on
     the host) replaces the uniform ctx; the returned structure owns the
-    array it points to. The library reads B entries of it, so it must have
-    one per row of the block table."""
+    array it points to, and keeps the tensors. The library reads B entries of
+    seq_ctx, so it must have one per row of the block table."""
     kv = KV(k_pool.data_ptr(), None if v_pool is None else v_pool.data_ptr(),
             block_table.data_ptr(), block_table.shape[1], k_pool.shape[0], ctx)
+    kv._tensors = k_pool, v_pool, block_table
     if seq_ctx is not None:
         if len(seq_ctx) != block_table.shape[0]:
             raise ValueError(f"seq_ctx has {len(seq_ctx)} entries for "
@@ -490,7 +491,17 @@ def sv_prefix_attend(shape: Shape, q, kv: KV, n_shared: int, draft_k, draft_v, p
     rows, drafts = (B, T, shape.Hq, d), (B, T, shape.Hkv, d)
     if parents is not None and len(parents) != T:
         raise ValueError(f"{len(parents)} draft parents for T={T} drafts")
-    _call(lib().sv_prefix_attend, (q, draft_k, draft_v, out, ws), stream, C.byref(shape),
+    cache = getattr(kv, "_tensors", ())  # none in a descriptor filled by hand
+    if cache:
+        k_pool, v_pool, table = cache
+        if table.shape[0] < B:
+            raise ValueError(f"the block_table of kv has {table.shape[0]} rows for {B} sequences")
+        _ints("block_table", table, *table.shape)
+        pool = (k_pool.shape[0], shape.Hkv, shape.blk, d)
+        _dense("k_pool", k_pool, dtype, *pool)
+        if v_pool is not None:  # (refused by the call where it has to be there)
+            _dense("v_pool", v_pool, dtype, *pool)
+    _call(lib().sv_prefix_attend, (q, draft_k, draft_v, out, ws, *cache), stream, C.byref(shape),
           _dense("q", q, dtype, *rows), C.byref(kv), n_shared,
           _dense("draft_k", draft_k, dtype, *drafts), _dense("draft_v", draft_v, dtype, *drafts),
           _parents(parents), _dense("out", out, dtype, *rows), _addr(ws),

@@ -191,3 +191,14 @@ def test_prefix_of_an_empty_cache(dtype, d, T, pool):
         want, tol = P.attend(q[b], dk[b], dv[b], P.draft_mask(None, T, "cuda"))
         P.check(out[b], want, tol)
         P.check(plain[b], want, tol)
+
+
+def test_prefix_refuses_a_cache_on_another_device():
+    """A descriptor of host tensors does not reach the library beside queries on the GPU."""
+    c, _, _ = G.prefix_case(73, F32, 4, 2, 64, 16, 2, 1, [5, 9])
+    k, v, table = c["kv"].keep
+    ws = api.alloc_prefix_workspace(c["shape"])
+    for tensors in ((k.cpu(), v, table), (k, v.cpu(), table), (k, v, table.cpu())):
+        kv = api.make_kv(*tensors, 16, [21, 25])
+        with pytest.raises(ValueError, match="one CUDA device"):
+            api.sv_prefix_attend(ws=ws, **{**c, "kv": kv})

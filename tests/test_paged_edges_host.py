@@ -1,0 +1,46 @@
+"""What the paged-cache calls take and refuse, on the host: no GPU is touched."""
+import pytest
+import torch
+
+from sparse_verification_attention_gb300 import api, build_lib
+
+
+@pytest.fixture(scope="module")
+def L():
+    build_lib.build()
+    return api.lib()
+
+
+def i32(*n):
+    return torch.zeros(*n, dtype=torch.int32)
+
+
+def test_prefix_refuses_a_cache_of_another_shape(L):
+    """A descriptor made for fewer sequences, other heads, pages or types than the call's
+    would be read past its ends."""
+    B, T, Hq, Hkv, d, blk = 3, 2, 4, 2, 64, 16
+    s = api.make_shape(B, Hq, Hkv, d, blk, T, torch.float32)
+    q, dk = torch.zeros(B, T, Hq, d), torch.zeros(B, T, Hkv, d)
+    ws = torch.zeros(1 << 10, dtype=torch.uint8)
+
+    def call(k, v, table, seq_ctx=None):
+        kv = api.make_kv(k, v, table, 16, seq_ctx)
+        api.sv_prefix_attend(s, q, kv, 0, dk, dk, None, torch.zeros_like(q), ws)
+
+    pool, table = torch.zeros(5, Hkv, blk, d), i32(B, 4)
+    for name, bad in (("block_table", dict(table=i32(B - 1, 4))),
+                      ("block_table", dict(table=i32(B - 1, 4), seq_ctx=[16] * (B - 1))),
+                      ("block_table", dict(table=i32(B, 4).long())),
+                      ("block_table", dict(table=i32(4, B).t())),
+                      ("k_pool", dict(k=torch.zeros(5, Hkv, 8, d))),
+                      ("k_pool", dict(k=torch.zeros(5, 1, blk, d))),
+                      ("k_pool", dict(k=pool.bfloat16())),
+                      ("k_pool", dict(k=torch.zeros(5, Hkv, d, blk).transpose(2, 3))),
+                      ("v_pool", dict(v=pool[:4])),
+                      ("v_pool", dict(v=torch.zeros(5, Hkv, blk, 32))),
+                      ("v_pool", dict(v=pool.double()))):
+        with pytest.raises(ValueError, match=name):
+            call(**{**dict(k=pool, v=pool, table=table), **bad})
+    for good in ({}, dict(table=i32(B + 1, 4)), dict(seq_ctx=[16, 0, 7])):
+        with pytest.raises(ValueError, match="one CUDA device"):  # right, but not on a GPU
+            call(**{**dict(k=pool, v=pool, table=table), **good})
