@@ -40,7 +40,7 @@
  *   - Limits: 1 <= T <= 64; Hq % Hkv == 0; d % 8 == 0 and 8 <= d <= 256;
  *     NB = ctx/blk full blocks <= 16384; a partial last block (ctx % blk
  *     tokens) is allowed; B <= 64 when the cache gives per-sequence
- *     lengths (sv_kv.seq_ctx).
+ *     lengths (sv_kv.seq_ctx), B <= 1024 in sv_prefix_attend.
  */
 #ifndef SVA_H_
 #define SVA_H_
@@ -126,10 +126,10 @@ typedef struct {
   int nb_max;               /* row stride of block_table, >= ceil(ctx/blk) */
   int num_pages;
   int ctx;                  /* prefix tokens per sequence (same for all)   */
-  /* Per-sequence prefix lengths, HOST memory, B entries (B <= 64), or NULL
-   * for the uniform ctx above (which is then ignored when non-NULL). Read
-   * during the call only; the caller keeps ownership. With per-sequence
-   * lengths every budget is taken per sequence (the piecewise rule of each
+  /* Per-sequence prefix lengths, HOST memory, B entries (B <= 64; 1024 in
+   * sv_prefix_attend), or NULL for the uniform ctx above (which is then
+   * ignored when non-NULL). Read during the call only; the caller keeps
+   * ownership. With per-sequence lengths every budget is taken per sequence (the piecewise rule of each
    * sequence's own ctx), sel rows hold k_b valid entries followed by -1, and
    * nb_max must cover the longest sequence. */
   const int32_t* seq_ctx;
@@ -532,7 +532,9 @@ sv_status sv_prompt_attend(const sv_shape* shape, const void* q, long long q_str
  * parts are joined by log-sum-exp. T = 1 is the single-token step.
  * n_shared * blk <= every sequence's context; 0 shares nothing. q, draft_k,
  * draft_v, draft_parent and out as in sv_sparse_attend; workspace from
- * sv_prefix_workspace_bytes. Limits: B <= 1024. */
+ * sv_prefix_workspace_bytes. The lengths are read on the host: a captured
+ * call keeps those it was captured with. Limits: B <= 1024, with or without
+ * per-sequence contexts. */
 sv_status sv_prefix_attend(const sv_shape* shape, const void* q, const sv_kv* kv, int n_shared,
                            const void* draft_k, const void* draft_v,
                            const int32_t* draft_parent, void* out, void* workspace,

@@ -15,7 +15,8 @@ sv_status cuda_fail(cudaError_t e, const char* what);
 bool aligned(const void* p, size_t a);
 
 sv_status check_shape(const sv_shape* s);
-sv_status check_kv(const sv_shape* s, const sv_kv* kv, bool need_v);
+// most: sequences that may have contexts of their own.
+sv_status check_kv(const sv_shape* s, const sv_kv* kv, bool need_v, int most = kMaxVarB);
 sv_status check_parents(const int32_t* parent, int T);
 // anc[t]: bit u set when draft t sees draft u.
 void fill_ancestors(const int32_t* parent, int T, unsigned long long* anc);

@@ -93,7 +93,7 @@ struct PagedArgs {
   int T, n_shared;
   int ctx;                    // prefix form: uniform context ...
   int var;                    // ... or per sequence in seq_len
-  int32_t seq_len[kMaxVarB];
+  int32_t seq_len[kMaxSegs - 1];
   unsigned long long anc[kMaxT];
 };
 

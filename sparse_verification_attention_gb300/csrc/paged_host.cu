@@ -228,7 +228,7 @@ sv_status sv_prefix_attend(const sv_shape* shape, const void* q, const sv_kv* kv
   const CallRange range("sv_prefix_attend");
   sv_status r = check_shape(shape);
   if (r != SV_OK) return r;
-  if ((r = check_kv(shape, kv, true)) != SV_OK) return r;
+  if ((r = check_kv(shape, kv, true, kMaxSegs - 1)) != SV_OK) return r;
   if (shape->B > kMaxSegs - 1)
     return fail(SV_ERR_UNSUPPORTED, "B=%d sequences exceeds %d", shape->B, kMaxSegs - 1);
   if (n_shared < 0) return fail(SV_ERR_INVALID_ARG, "n_shared=%d is negative", n_shared);

@@ -68,13 +68,12 @@ sv_status check_shape(const sv_shape* s) {
   return SV_OK;
 }
 
-sv_status check_kv(const sv_shape* s, const sv_kv* kv, bool need_v) {
+sv_status check_kv(const sv_shape* s, const sv_kv* kv, bool need_v, int most) {
   if (!kv) return fail(SV_ERR_INVALID_ARG, "kv is NULL");
   int nb = 0, nblocks = 0;  // the largest over the sequences
   if (kv->seq_ctx) {
-    if (s->B > kMaxVarB)
-      return fail(SV_ERR_UNSUPPORTED, "B=%d sequences with per-sequence ctx exceeds %d", s->B,
-                  kMaxVarB);
+    if (s->B > most)
+      return fail(SV_ERR_UNSUPPORTED, "B=%d sequences with per-sequence ctx exceeds %d", s->B, most);
     for (int b = 0; b < s->B; ++b) {
       const int c = kv->seq_ctx[b];
       if (c < 0) return fail(SV_ERR_INVALID_ARG, "seq_ctx[%d]=%d is negative", b, c);

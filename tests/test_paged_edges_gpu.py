@@ -202,3 +202,15 @@ def test_prefix_refuses_a_cache_on_another_device():
         kv = api.make_kv(*tensors, 16, [21, 25])
         with pytest.raises(ValueError, match="one CUDA device"):
             api.sv_prefix_attend(ws=ws, **{**c, "kv": kv})
+
+
+# ------------------------------------------------------------------ large batches
+@pytest.mark.parametrize("dtype,B,T", [(BF16, 65, 1), (BF16, 300, 3), (F32, 129, 1), (BF16, 1024, 1)])
+def test_prefix_of_a_large_ragged_batch(dtype, B, T):
+    """More samples of one prompt than the verification calls take, each with its own tail."""
+    own = [(37 * b) % 90 for b in range(B)]
+    c, want, tol = G.prefix_case(75, dtype, 8, 2, 64, 16, T, 20, own)
+    ws = api.alloc_prefix_workspace(c["shape"])
+    api.sv_prefix_attend(ws=ws, **c)
+    assert api.sv_read_status(ws) == 0
+    P.check(c["out"], want, tol)

@@ -1,4 +1,6 @@
 """What the paged-cache calls take and refuse, on the host: no GPU is touched."""
+import ctypes as C
+
 import pytest
 import torch
 
@@ -44,3 +46,17 @@ def test_prefix_refuses_a_cache_of_another_shape(L):
     for good in ({}, dict(table=i32(B + 1, 4)), dict(seq_ctx=[16, 0, 7])):
         with pytest.raises(ValueError, match="one CUDA device"):  # right, but not on a GPU
             call(**{**dict(k=pool, v=pool, table=table), **good})
+
+
+def test_prefix_takes_as_many_contexts_as_sequences(L):
+    """Per-sequence contexts for all of the 1024 sequences that a call may have."""
+    fake = 1 << 20  # never dereferenced: the workspace is refused
+    for B in (64, 65, 1024, 1025):
+        s = api.make_shape(B, 4, 2, 64, 16, 4, torch.float32)
+        lens = (C.c_int32 * B)(*[16 + b % 50 for b in range(B)])
+        kv = api.KV(fake, fake, fake, 10, 64, 0)
+        kv.seq_ctx = lens
+        st = L.sv_prefix_attend(C.byref(s), fake, C.byref(kv), 1, fake, fake, None, fake, fake, 0, None)
+        assert st == (api.SV_ERR_WORKSPACE if B <= 1024 else api.SV_ERR_UNSUPPORTED), B
+        st = L.sv_sparse_attend(C.byref(s), fake, C.byref(kv), None, 0, 0, fake, fake, None, fake, fake, 0, None)
+        assert st == (api.SV_ERR_WORKSPACE if B <= 64 else api.SV_ERR_UNSUPPORTED), B
