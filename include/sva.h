@@ -129,9 +129,9 @@ typedef struct {
   /* Per-sequence prefix lengths, HOST memory, B entries (B <= 64; 1024 in
    * sv_prefix_attend), or NULL for the uniform ctx above (which is then
    * ignored when non-NULL). Read during the call only; the caller keeps
-   * ownership. With per-sequence lengths every budget is taken per sequence (the piecewise rule of each
-   * sequence's own ctx), sel rows hold k_b valid entries followed by -1, and
-   * nb_max must cover the longest sequence. */
+   * ownership. With per-sequence lengths every budget is taken per sequence
+   * (the piecewise rule of each sequence's own ctx), sel rows hold k_b valid
+   * entries followed by -1, and nb_max must cover the longest sequence. */
   const int32_t* seq_ctx;
 } sv_kv;
 

@@ -411,8 +411,14 @@ def _rows(name: str, t: torch.Tensor, dtype: torch.dtype, heads: int, d: int) ->
     return stride[0] if shape[0] > 1 else heads * d
 
 
-def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+def _workspace(ws: Optional[torch.Tensor]):
+    """Address and bytes of a workspace (or of a status word), None and 0 without one."""
+    if ws is None:
+        return None, 0
+    n = ws.numel() * ws.element_size()
+    if n < 4 or not ws.is_contiguous():
+        raise ValueError("the workspace must be a dense tensor that holds a status word at least")
+    return ws.data_ptr(), n
 
 
 def sv_build_tables(blk: int, old_len, new_len, block_table, free_pages, free_count, free_count_out,
@@ -433,7 +439,7 @@ def sv_build_tables(blk: int, old_len, new_len, block_table, free_pages, free_co
           _ints("free_pages", free_pages, num_pages), _ints("free_count", free_count, 1),
           _ints("free_count_out", free_count_out, 1), _ints("cu_new", cu_new, B + 1),
           _ints("slot_map", slot_map, n_max),
-          None if positions is None else _ints("positions", positions, n_max), n_max, _addr(ws))
+          None if positions is None else _ints("positions", positions, n_max), n_max, _workspace(ws)[0])
 
 
 def sv_write_kv(shape: Shape, k, v, slot_map, k_pool, v_pool, ws=None, stream=None):
@@ -448,7 +454,7 @@ def sv_write_kv(shape: Shape, k, v, slot_map, k_pool, v_pool, ws=None, stream=No
     _call(lib().sv_write_kv, (k, v, slot_map, k_pool, v_pool, ws), stream, C.byref(shape),
           k.data_ptr(), ks, v.data_ptr(), vs, _ints("slot_map", slot_map, n), n,
           _dense("k_pool", k_pool, dtype, *pool), _dense("v_pool", v_pool, dtype, *pool), pages,
-          _addr(ws))
+          _workspace(ws)[0])
 
 
 def _alloc_zeroed(n: int, device) -> torch.Tensor:
@@ -480,7 +486,7 @@ def sv_prompt_attend(shape: Shape, q, k_pool, v_pool, block_table, seq_ctx, cu_q
           C.byref(shape), q.data_ptr(), qs, n, _dense("k_pool", k_pool, dtype, *pool),
           _dense("v_pool", v_pool, dtype, *pool), _ints("block_table", block_table, B, nb_max),
           nb_max, pages, _ints("seq_ctx", seq_ctx, B), _ints("cu_q", cu_q, B + 1),
-          _dense("out", out, dtype, n, Hq, d), _addr(ws), 0 if ws is None else ws.numel())
+          _dense("out", out, dtype, n, Hq, d), *_workspace(ws))
 
 
 def sv_prefix_attend(shape: Shape, q, kv: KV, n_shared: int, draft_k, draft_v, parents, out, ws,
@@ -504,8 +510,7 @@ def sv_prefix_attend(shape: Shape, q, kv: KV, n_shared: int, draft_k, draft_v, p
     _call(lib().sv_prefix_attend, (q, draft_k, draft_v, out, ws, *cache), stream, C.byref(shape),
           _dense("q", q, dtype, *rows), C.byref(kv), n_shared,
           _dense("draft_k", draft_k, dtype, *drafts), _dense("draft_v", draft_v, dtype, *drafts),
-          _parents(parents), _dense("out", out, dtype, *rows), _addr(ws),
-          0 if ws is None else ws.numel())
+          _parents(parents), _dense("out", out, dtype, *rows), *_workspace(ws))
 
 
 VERIFY_COMPUTE, VERIFY_REUSE, VERIFY_FULL = 0, 1, 2  # sv_verify_layer's reuse values

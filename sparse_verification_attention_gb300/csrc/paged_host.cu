@@ -2,6 +2,7 @@
 // launches. Declarations and contracts: include/sva.h.
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 
 #include "host.h"
 #include "paged.h"
@@ -90,6 +91,13 @@ cudaError_t launch_paged(const PagedArgs& a, int dtype, cudaStream_t st) {
   return paged_tc_applies(a, dtype) ? launch_paged_tc(a, st) : launch_paged_simt(a, dtype, st);
 }
 
+// int32 arrays that the kernels address word by word (null: not given).
+sv_status check_words(const char* names, std::initializer_list<const void*> arrays) {
+  for (const void* p : arrays)
+    if (!aligned(p, 4)) return fail(SV_ERR_INVALID_ARG, "%s must be 4-byte aligned", names);
+  return SV_OK;
+}
+
 // A strided row array: base and stride on 16-byte boundaries, rows apart.
 sv_status check_rows(const sv_shape* s, const char* name, const void* p, long long stride, int heads) {
   if (!aligned(p, 16)) return fail(SV_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
@@ -141,6 +149,10 @@ sv_status sv_build_tables(int B, int blk, const int32_t* old_len, const int32_t*
     return fail(SV_ERR_INVALID_ARG,
                 "old_len/new_len/block_table/free_pages/free_count/free_count_out/cu_new/slot_map "
                 "is NULL");
+  const sv_status r = check_words("the arrays and the workspace",
+                                  {old_len, new_len, pinned, block_table, free_pages, free_count,
+                                   free_count_out, cu_new, slot_map, positions, workspace});
+  if (r != SV_OK) return r;
   const TablesArgs a{old_len, new_len, pinned, block_table, free_pages, free_count, free_count_out,
                      cu_new, slot_map, positions, static_cast<unsigned*>(workspace), B, blk, nb_max,
                      num_pages, n_max, blk & (blk - 1) ? -1 : __builtin_ctz(blk)};
@@ -160,6 +172,7 @@ sv_status sv_write_kv(const sv_shape* shape, const void* k, long long k_stride, 
   if (!k || !v || !slot_map) return fail(SV_ERR_INVALID_ARG, "k/v/slot_map is NULL");
   if ((r = check_rows(shape, "k", k, k_stride, shape->Hkv)) != SV_OK) return r;
   if ((r = check_rows(shape, "v", v, v_stride, shape->Hkv)) != SV_OK) return r;
+  if ((r = check_words("slot_map and the workspace", {slot_map, workspace})) != SV_OK) return r;
   const long long es = (long long)elt_bytes(shape);
   const WriteArgs a{k, v, slot_map, k_pool, v_pool, static_cast<unsigned*>(workspace), k_stride * es,
                     v_stride * es, n, shape->Hkv, shape->blk, num_pages, (int)(shape->d * es)};
@@ -198,6 +211,7 @@ sv_status sv_prompt_attend(const sv_shape* shape, const void* q, long long q_str
     return fail(SV_ERR_UNSUPPORTED, "n_rows=%d rows of %d heads reach 2^31", n_rows, shape->Hq);
   if (!block_table || !seq_ctx || !cu_q)
     return fail(SV_ERR_INVALID_ARG, "block_table/seq_ctx/cu_q is NULL");
+  if ((r = check_words("block_table/seq_ctx/cu_q", {block_table, seq_ctx, cu_q})) != SV_OK) return r;
   const PagedLayout L = prompt_layout(*shape, n_rows);
   if ((r = check_paged_ws(L, workspace, ws_bytes)) != SV_OK) return r;
   if (n_rows == 0) return SV_OK;
@@ -245,6 +259,7 @@ sv_status sv_prefix_attend(const sv_shape* shape, const void* q, const sv_kv* kv
     return fail(SV_ERR_INVALID_ARG, "q/draft_k/draft_v/out is NULL");
   if (!aligned(q, 16) || !aligned(draft_k, 16) || !aligned(draft_v, 16) || !aligned(out, 16))
     return fail(SV_ERR_INVALID_ARG, "q/draft_k/draft_v/out must be 16-byte aligned");
+  if ((r = check_words("block_table", {kv->block_table})) != SV_OK) return r;
   if ((r = check_parents(draft_parent, shape->T)) != SV_OK) return r;
   const PagedLayout L = prefix_layout(*shape);
   if ((r = check_paged_ws(L, workspace, ws_bytes)) != SV_OK) return r;

@@ -60,3 +60,49 @@ def test_prefix_takes_as_many_contexts_as_sequences(L):
         assert st == (api.SV_ERR_WORKSPACE if B <= 1024 else api.SV_ERR_UNSUPPORTED), B
         st = L.sv_sparse_attend(C.byref(s), fake, C.byref(kv), None, 0, 0, fake, fake, None, fake, fake, 0, None)
         assert st == (api.SV_ERR_WORKSPACE if B <= 64 else api.SV_ERR_UNSUPPORTED), B
+
+
+def test_misaligned_words_are_refused(L):
+    """int32 arrays and the status word off a 4-byte boundary would fault in the kernels."""
+    fake = 1 << 20
+    s = api.make_shape(2, 4, 2, 64, 16, 4, torch.float32)
+
+    def refused(f, args, at, step=2):
+        args = list(args)
+        args[at] = fake + step
+        st = f(*args)
+        msg = L.sv_last_error().decode()
+        assert st == api.SV_ERR_INVALID_ARG and "aligned" in msg, (at, st, msg)
+
+    tables = [2, 16, fake, fake, fake, fake, 8, 32, fake, fake, fake, fake, fake, fake, 10, fake, None]
+    for i in (2, 3, 4, 5, 8, 9, 10, 11, 12, 13, 15):
+        refused(L.sv_build_tables, tables, i)
+    write = [C.byref(s), fake, 128, fake, 128, fake, 5, fake, fake, 8, fake, None]
+    for i in (5, 10):
+        refused(L.sv_write_kv, write, i)
+    n = L.sv_prompt_workspace_bytes(C.byref(s), 50)
+    prompt = [C.byref(s), fake, 256, 50, fake, fake, fake, 8, 32, fake, fake, fake, fake, n, None]
+    for i in (6, 9, 10):
+        refused(L.sv_prompt_attend, prompt, i)
+    n = L.sv_prefix_workspace_bytes(C.byref(s))
+    kv = api.KV(fake, fake, fake + 1, 10, 64, 100)
+    prefix = [C.byref(s), fake, C.byref(kv), 6, fake, fake, None, fake, fake, n, None]
+    refused(L.sv_prefix_attend, prefix, 1, 0)  # (the table's address is off)
+
+
+def test_workspaces_must_be_dense(L):
+    """A strided or expanded workspace spans other bytes than its size says."""
+    s = api.make_shape(2, 4, 2, 64, 16, 4, torch.float32)
+    pool, rows = torch.zeros(4, 2, 16, 64), torch.zeros(3, 2, 64)
+    q, out = torch.zeros(5, 4, 64), torch.zeros(5, 4, 64)
+    q4, dk = torch.zeros(2, 4, 4, 64), torch.zeros(2, 4, 2, 64)
+    kv = api.make_kv(pool, pool, i32(2, 3), 16)
+    one = torch.zeros(1, dtype=torch.uint8)
+    for ws in (torch.zeros(1 << 11, dtype=torch.uint8)[::2], one.expand(1 << 30), one[:0]):
+        for call in (lambda: api.sv_prompt_attend(s, q, pool, pool, i32(2, 3), i32(2), i32(3), out, ws),
+                     lambda: api.sv_prefix_attend(s, q4, kv, 1, dk, dk, None, torch.zeros_like(q4), ws),
+                     lambda: api.sv_write_kv(s, rows, rows, i32(3), pool, pool, ws),
+                     lambda: api.sv_build_tables(16, i32(2), i32(2), i32(2, 3), i32(9), i32(1), i32(1),
+                                                 i32(3), i32(4), ws=ws)):
+            with pytest.raises(ValueError, match="workspace"):
+                call()
