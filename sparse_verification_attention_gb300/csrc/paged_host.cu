@@ -42,20 +42,24 @@ PagedLayout prompt_layout(const sv_shape& s, int n_rows) {
 }
 
 // Partial rows: every row once in its shared tile and once in its own, and
-// the items per CTA that cutting adds (make_plan).
+// the items per CTA that cutting adds (make_plan): each holds a tile's rows, or those
+// of its segment (the batch, a sequence's drafts) if that has fewer.
 PagedLayout prefix_layout(const sv_shape& s) {
   PagedArgs a{};
   a.Hkv = s.Hkv;
   a.G = s.Hq / s.Hkv;
+  const long long batch = (long long)s.B * s.T;
   size_t most = 0;
   for (int rows : {kSimtRows, kTcRows}) {
     paged_heads(&a, rows);
     const int tile = rows / a.gs * (rows == kTcRows ? 2 : 1);
+    const size_t ctas = rows == kTcRows ? kMaxTcCtas : kMaxPlanCtas;
+    auto item = [&](long long n) { return (size_t)std::min<long long>(tile, n) * a.gs; };
     auto padded = [&](long long n) {  // rows of the partial tiles of n tokens
-      return (size_t)((n + tile - 1) / tile) * std::min<long long>(tile, n) * a.gs * a.hv;
+      return (size_t)((n + tile - 1) / tile) * a.hv * item(n);
     };
-    const size_t r = padded((long long)s.B * s.T) + s.B * padded(s.T) +
-                     (size_t)(kOwnItemsPerCta + kSharedItemsPerCta) * kMaxPlanCtas * kSimtRows;
+    const size_t r = padded(batch) + s.B * padded(s.T) +
+                     ctas * (kOwnItemsPerCta * item(s.T) + kSharedItemsPerCta * item(batch));
     most = std::max(most, r);
   }
   return paged_layout(most, s.d);

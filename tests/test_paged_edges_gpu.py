@@ -214,3 +214,22 @@ def test_prefix_of_a_large_ragged_batch(dtype, B, T):
     api.sv_prefix_attend(ws=ws, **c)
     assert api.sv_read_status(ws) == 0
     P.check(c["out"], want, tol)
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,d,T,shared,own", [
+    (BF16, 8, 2, 128, 1, 900, [3000, 5]), (BF16, 4, 1, 64, 5, 40, [9000]),
+    (BF16, 32, 4, 128, 16, 400, [700] * 6), (BF16, 200, 1, 64, 3, 300, [4000, 40]),
+    (BF16, 4, 4, 64, 1, 700, [(61 * b) % 800 for b in range(200)]),
+    (BF16, 4, 2, 256, 2, 500, [2000, 9]), (F32, 4, 2, 64, 1, 900, [6000, 5]),
+    (F32, 6, 2, 64, 20, 200, [3000, 100, 0]), (F32, 4, 4, 64, 1, 300, [(61 * b) % 400 for b in range(150)])])
+def test_prefix_stays_in_its_workspace(dtype, Hq, Hkv, d, T, shared, own):
+    """Plans with many cut runs: not a byte behind the workspace's size is written (what
+    follows it here is as large as the partial rows of the widest plan)."""
+    c, want, tol = G.prefix_case(77, dtype, Hq, Hkv, d, 16, T, shared, own)
+    n = api.alloc_prefix_workspace(c["shape"]).numel()
+    room = torch.zeros(n + 4 * 640 * 64 * (4 * d + 8), dtype=torch.uint8, device="cuda")
+    room[n:] = 0xA5
+    api.sv_prefix_attend(ws=room[:n], **c)
+    assert api.sv_read_status(room[:n]) == 0
+    assert bool((room[n:] == 0xA5).all())
+    P.check(c["out"], want, tol)

@@ -106,3 +106,15 @@ def test_workspaces_must_be_dense(L):
                                                  i32(3), i32(4), ws=ws)):
             with pytest.raises(ValueError, match="workspace"):
                 call()
+
+
+def test_prefix_workspace_follows_the_batch(L):
+    """The partial rows of a small batch are few: a cut run holds no more rows than there are."""
+    size = lambda **k: L.sv_prefix_workspace_bytes(C.byref(api.make_shape(**k)))  # noqa: E731
+    base = dict(Hq=8, Hkv=2, d=128, blk=64, dtype=torch.bfloat16)
+    assert size(B=2, T=1, **base) < 16 << 20
+    assert size(B=2, T=1, **{**base, "dtype": torch.float32}) < 16 << 20
+    last = 0
+    for B in (1, 2, 8, 64, 512, 1024):
+        assert size(B=B, T=4, **base) > last
+        last = size(B=B, T=4, **base)
