@@ -233,3 +233,54 @@ def test_prefix_stays_in_its_workspace(dtype, Hq, Hkv, d, T, shared, own):
     assert api.sv_read_status(room[:n]) == 0
     assert bool((room[n:] == 0xA5).all())
     P.check(c["out"], want, tol)
+
+
+# ------------------------------------------------------------------ plans of large calls
+@pytest.mark.parametrize("B,blk,nb_max", [(300, 16, 30), (4096, 8, 6)])
+def test_tables_of_a_large_admission(B, blk, nb_max):
+    """More than 32768 new tokens, and padding behind them: a cluster of sixteen CTAs."""
+    r = random.Random(B)
+    old = [r.choice([0, 0, r.randint(0, nb_max * blk // 3)]) for _ in range(B)]
+    new = [r.choice([0, r.randint(nb_max * blk // 2, nb_max * blk)]) if r.random() < 0.9 else n for n in old]
+    pages = B * nb_max
+    perm = list(range(pages))
+    r.shuffle(perm)
+    table, at = [], 0
+    for n in old:
+        h = P.nb(n, blk)
+        table.append(perm[at:at + h] + [-7] * (nb_max - h))
+        at += h
+    want = P.tables(blk, old, new, [0] * B, table, perm[at:] + [0] * at, pages - at)
+    n = want[3][-1]
+    assert n > 32768
+    got = G.run_tables(blk, old, new, table, perm[at:] + [0] * at, pages - at, n + 1000)
+    assert got[6] == 0 and got[2] == [want[2]] and got[3] == want[3]
+    assert got[0] == want[0] and got[1] == want[1]
+    assert got[4] == want[4] + [-1] * 1000 and got[5] == want[5] + [-1] * 1000
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,n,every", [
+    (BF16, 8, 8, 30000, 97), (F32, 8, 8, 15000, 61), (BF16, 32, 8, 32768, 251), (BF16, 14, 7, 30000, 97)])
+def test_prompt_of_many_rows_over_large_heads(dtype, Hq, Hkv, n, every):
+    """One long prompt: heads go out in groups whose keys fit a quarter of L2, and the
+    last group is smaller where they do not divide (8 heads by three, 7 by three). Rows
+    all along the prompt against 64 bits."""
+    d, blk = 128, 64
+    c = G.prompt_case(81, dtype, Hq, Hkv, d, blk, [n], [n])
+    assert G.run_prompt(c) == 0
+    rows = torch.arange(0, n, every, device="cuda")
+    k, v = (P.gather(c[p], c["block_table"][0], n, blk) for p in ("k_pool", "v_pool"))
+    see = torch.arange(n, device="cuda") <= rows[:, None]
+    P.check(c["out"][rows], *P.attend(c["q"][rows], k, v, see))
+    assert bool(c["out"].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype,Hkv,shared", [(BF16, 8, 30000), (F32, 7, 15008)])
+def test_prefix_over_large_heads(dtype, Hkv, shared):
+    """The same for a shared prefix whose heads do not fit a quarter of L2 together."""
+    own = [(211 * b) % 500 for b in range(12)]
+    c, want, tol = G.prefix_case(83, dtype, Hkv, Hkv, 128, 16, 4, shared // 16, own)
+    ws = api.alloc_prefix_workspace(c["shape"])
+    api.sv_prefix_attend(ws=ws, **c)
+    assert api.sv_read_status(ws) == 0
+    P.check(c["out"], want, tol)
