@@ -778,12 +778,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool empty = kt >= kt_end;
       float m_run = -INFINITY, l_run = 0.f, mine = -INFINITY;
-      // move the row's reference to m; alpha: what its sum and O are multiplied by
+      // Move the row's reference to m or up to one above it, by a whole number: alpha, by
+      // which its sum, its O and, where they are there already, its weights are
+      // multiplied, is a power of two, and weights in bf16 are not rounded a second time.
+      // (The first reference is the maximum itself: a single key has the weight 1.)
       auto move_ref = [&](float m) {
-        const float alpha = m == -INFINITY ? 1.f : ex2(m_run - m);
+        const bool first = m_run == -INFINITY;  // nothing is summed yet
+        const float step = ceilf(m - m_run), alpha = first ? (m == -INFINITY ? 1.f : 0.f) : ex2(-step);
         l_run *= alpha;
-        m_run = m;
+        m_run = first ? m : m_run + step;
         return alpha;
+      };
+      // This half's maximum of a row that is not one of the item's is -inf: such a row
+      // (another sequence's queries, padding, or what the slot held before) must not
+      // move the references of the rows beside it, whose rounding goes with them.
+      auto top_score = [&](const uint32_t(&v)[64]) {
+        return mine_valid ? max64(v) * a.scale_log2 : -INFINITY;
       };
       // The two threads of a row agree on its reference without waiting for each
       // other: exponentials take what both knew of the tiles before (their maxima
@@ -791,12 +801,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // exponents. When one of them finds a maximum more than 2^kFixLog2 above the
       // reference, its warp moves it at once for both halves; the other half
       // recognises that in the next tile, by the same comparison.
-      // This half's maximum of a row that is not one of the item's is -inf: such a row
-      // (another sequence's queries, padding, or what the slot held before) must not
-      // move the references of the rows beside it, whose rounding goes with them.
-      auto top_score = [&](const uint32_t(&v)[64]) {
-        return mine_valid ? max64(v) * a.scale_log2 : -INFINITY;
-      };
       auto catch_up = [&](float other) {  // the other half's maximum of the last tile
         if (__any_sync(0xffffffffu, other > m_run + kFixLog2)) move_ref(fmaxf(m_run, fmaxf(mine, other)));
       };

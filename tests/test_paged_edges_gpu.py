@@ -284,3 +284,37 @@ def test_prefix_over_large_heads(dtype, Hkv, shared):
     api.sv_prefix_attend(ws=ws, **c)
     assert api.sv_read_status(ws) == 0
     P.check(c["out"], want, tol)
+
+
+# ------------------------------------------------------------------ roundings
+def test_prompt_weights_are_rounded_once():
+    """A row whose scores rise by 2^100 in the first half of a key tile moves the softmax
+    reference of its warp's rows after the other half's weights were rounded to bf16. Only that
+    half's values are not zero and its weights are alike, so a second rounding shows."""
+    ctx, blk, d, H = [900] * 48, 64, 64, 4
+    c = G.prompt_case(93, BF16, H, H, d, blk, ctx, ctx, hole=0.0)
+    q, k, v, t = c["q"], c["k_pool"], c["v_pool"], c["block_table"].long()
+    log2 = d ** 0.5 / 1.442695  # a product of two entries that makes a score of 2^1
+    r = torch.Generator(device="cuda").manual_seed(1)
+    for x in (q, k, v):
+        x.zero_()
+    q[:, :, 0] = (torch.arange(len(q), device="cuda") % 16 == 7)[:, None]
+    k[t[:, 700 // blk], :, 700 % blk, 0] = 100 * log2
+    q[:, :, 1] = torch.rand(len(q), H, generator=r, device="cuda") * log2  # the second half's scores
+    q[:, :, 2] = torch.rand(len(q), H, generator=r, device="cuda") * log2  # one of the first half's
+    k[t[:, 641 // blk], :, 641 % blk, 2] = 1
+    for i in range(704, 768):
+        k[t[:, i // blk], :, i % blk, 1] = 1
+        v[t[:, i // blk], :, i % blk] = 1
+    assert G.run_prompt(c) == 0
+    P.check(c["out"], *G.prompt_want(c, ctx, ctx))
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,d", [(BF16, 8, 2, 128), (BF16, 3, 3, 64), (BF16, 2, 1, 256), (F32, 4, 2, 64)])
+def test_a_row_of_one_key_is_its_value(dtype, Hq, Hkv, d):
+    ctx = [1, 300, 1, 70]
+    c = G.prompt_case(95, dtype, Hq, Hkv, d, 16, ctx, ctx)
+    assert G.run_prompt(c) == 0
+    for b in range(4):
+        value = P.gather(c["v_pool"], c["block_table"][b], 1, 16)[0]
+        same(c["out"][int(c["cu_q"][b])], value.repeat_interleave(Hq // Hkv, 0), "from the value")
