@@ -505,7 +505,10 @@ size_t sv_prefix_workspace_bytes(const sv_shape* shape);
  * seq_ctx[b] a chunk on top of what is cached, n_b = 1 a decoding step; one
  * call may mix them. A row that sees no key (seq_ctx[b] < n_b; flagged) is
  * zero. Rows of q behind cu_q[B] may hold anything (a copy may fetch them; no
- * result depends on them), rows of out behind it are not written.
+ * result depends on them), rows of out behind it are not written. In bf16
+ * softmax weights are rounded to bf16 ahead of the product with V (their sum is
+ * fp32 and taken before), as in sv_sparse_attend, and values up to 2^78 in
+ * magnitude do not overflow on the way.
  * q: [n_rows, Hq, d], rows q_stride ELEMENTS apart (>= Hq * d, a multiple of
  * 16 bytes); out: [n_rows, Hq, d] dense. seq_ctx [B] and cu_q [B + 1] are
  * DEVICE int32 (cu_q ascending from 0, cu_q[B] <= n_rows): nothing is read
@@ -529,7 +532,8 @@ sv_status sv_prompt_attend(const sv_shape* shape, const void* q, long long q_str
  * rows of all B * T drafts are stacked against the shared pages (those of
  * sequence 0's table row; the other rows' first n_shared entries are not
  * read), each sequence's own blocks and drafts are attended apart, and the
- * parts are joined by log-sum-exp. T = 1 is the single-token step.
+ * parts are joined by log-sum-exp. T = 1 is the single-token step. Rounding
+ * and range of bf16 as in sv_prompt_attend.
  * n_shared * blk <= every sequence's context; 0 shares nothing. q, draft_k,
  * draft_v, draft_parent and out as in sv_sparse_attend; workspace from
  * sv_prefix_workspace_bytes. The lengths are read on the host: a captured

@@ -69,7 +69,10 @@ constexpr int kItems = 4;             // item ring
 constexpr int kItemReaders = 19;      // MMA, 16 softmax and 2 cleaning warps
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;   // O follows the maximum in steps of more than 2^8
-constexpr float kFixLog2 = 64.0f;
+// ... and never lies more than 2^kFixLog2 below a score of the tile: P stays under 2^32. A
+// tile of 128 keys and the join of 640 runs then take sums of values up to 2^78 (with
+// 2^64 up to 2^46).
+constexpr float kFixLog2 = 32.0f;
 constexpr int kMaxMasked = 4;         // masked key tiles of an item, at most 3 (see run_of)
 // registers per thread of the softmax warps and of the others (the launch
 // gives 96 to each of 640 threads: 512 * 104 + 128 * 64 = 640 * 96)

@@ -318,3 +318,22 @@ def test_a_row_of_one_key_is_its_value(dtype, Hq, Hkv, d):
     for b in range(4):
         value = P.gather(c["v_pool"], c["block_table"][b], 1, 16)[0]
         same(c["out"][int(c["cu_q"][b])], value.repeat_interleave(Hq // Hkv, 0), "from the value")
+# ------------------------------------------------------------------ large values
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 1, 128), (2, 2, 64)])
+@pytest.mark.parametrize("octaves", [20, 31, 33, 50, 63, 66])
+def test_prompt_large_values_behind_a_jump(Hq, Hkv, d, octaves):
+    """Values of 1e24 (sums of 128 of them are far inside fp32) and a score that rises by up to
+    2^66 inside a key tile: the result is a mean of values, and finite."""
+    ctx, blk = [900] * 48, 64  # (so many that no sequence's keys are cut into runs)
+    c = G.prompt_case(91, BF16, Hq, Hkv, d, blk, ctx, ctx, hole=0.0)
+    t = c["block_table"].long()
+    c["q"][:, :, 3] = 4.0
+    c["k_pool"][:, :, :, 3] = 0.0
+    for i, part in ((333, 1.0), (450, 2.0), (700, 3.0)):  # scores of 2^0, then these
+        c["k_pool"][t[:, i // blk], :, i % blk] = 0.0
+        c["k_pool"][t[:, i // blk], :, i % blk, 3] = part * octaves * 0.6931 * d ** 0.5 / 4.0
+    c["v_pool"].mul_(1e24)
+    want, tol = G.prompt_want(c, ctx, ctx)
+    assert bool(want.abs().max() < 1e26)
+    assert G.run_prompt(c) == 0
+    P.check(c["out"], want, tol)
