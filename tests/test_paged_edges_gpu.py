@@ -337,3 +337,49 @@ def test_prompt_large_values_behind_a_jump(Hq, Hkv, d, octaves):
     assert bool(want.abs().max() < 1e26)
     assert G.run_prompt(c) == 0
     P.check(c["out"], want, tol)
+
+
+# ------------------------------------------------------------------ calls at the same time
+def test_calls_on_two_streams_with_a_workspace_each():
+    """Calls that overlap, each with a workspace of its own, give the bits that they give alone."""
+    a = G.prompt_case(97, BF16, 8, 2, 128, 64, [3000, 1, 700], [3000, 1, 64])
+    b = G.prompt_case(98, F32, 8, 2, 64, 16, [900, 300], [900, 300])
+    p, _, _ = G.prefix_case(99, BF16, 8, 1, 128, 64, 4, 30, [300, 0, 77])
+    wa, wb = (api.alloc_prompt_workspace(c["shape"], c["q"].shape[0]) for c in (a, b))
+    wp = api.alloc_prefix_workspace(p["shape"])
+    len0, len1 = G.i32([0, 40, 7]), G.i32([90, 0, 300])
+    grow = dict(old_len=len0, new_len=len1, free_pages=G.i32(list(range(64))), free_count=G.i32([60]),
+                free_count_out=G.i32([0]), cu_new=G.i32([0] * 4), slot_map=G.i32([0] * 400))
+    tables = [torch.full((3, 32), 63, dtype=torch.int32, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+
+    def first(table):
+        api.sv_build_tables(16, block_table=table, ws=wa, **grow)
+        api.sv_prompt_attend(ws=wa, **a)
+
+    def second():
+        api.sv_prefix_attend(ws=wp, **p)
+        api.sv_prompt_attend(ws=wb, **b)
+
+    first(tables[0])
+    second()
+    torch.cuda.synchronize()
+    outs = [a["out"], b["out"], p["out"]]
+    alone = [x.clone() for x in outs] + [grow["slot_map"].clone()]
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(30):
+        for x in outs:
+            x.fill_(7.0)
+        grow["free_pages"].copy_(G.i32(list(range(64))))
+        tables[1].fill_(63)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            with torch.cuda.stream(t):
+                second()
+        with torch.cuda.stream(s):
+            first(tables[1])
+        torch.cuda.synchronize()
+        for x, y in zip(outs + [grow["slot_map"]], alone):
+            same(x, y, "beside calls on another stream")
+        assert torch.equal(tables[0], tables[1])
+    assert all(api.sv_read_status(w) == 0 for w in (wa, wb, wp))
