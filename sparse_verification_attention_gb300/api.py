@@ -489,6 +489,19 @@ def sv_prompt_attend(shape: Shape, q, k_pool, v_pool, block_table, seq_ctx, cu_q
           _dense("out", out, dtype, n, Hq, d), *_workspace(ws))
 
 
+def _check_cache(shape: Shape, dtype: torch.dtype, k_pool, v_pool, table):
+    """A descriptor's tensors must be a cache of this shape, for shape.B sequences at least."""
+    pages = k_pool.shape
+    if pages[1:] != (shape.Hkv, shape.blk, shape.d) or k_pool.dtype != dtype or not k_pool.is_contiguous():
+        raise ValueError(f"the k_pool of kv must be contiguous, of dtype {dtype} and of shape "
+                         f"[pages, {shape.Hkv}, {shape.blk}, {shape.d}]")
+    if v_pool is not None and \
+            (v_pool.shape != pages or v_pool.dtype != dtype or not v_pool.is_contiguous()):
+        raise ValueError("the v_pool of kv must be as its k_pool")
+    if table.shape[0] < shape.B or table.dtype != torch.int32 or not table.is_contiguous():
+        raise ValueError(f"the block_table of kv must be contiguous, int32 and have {shape.B} rows")
+
+
 def sv_prefix_attend(shape: Shape, q, kv: KV, n_shared: int, draft_k, draft_v, parents, out, ws,
                      stream=None):
     """sv_sparse_attend over every block for a batch whose sequences share
@@ -499,14 +512,7 @@ def sv_prefix_attend(shape: Shape, q, kv: KV, n_shared: int, draft_k, draft_v, p
         raise ValueError(f"{len(parents)} draft parents for T={T} drafts")
     cache = getattr(kv, "_tensors", ())  # none in a descriptor filled by hand
     if cache:
-        k_pool, v_pool, table = cache
-        if table.shape[0] < B:
-            raise ValueError(f"the block_table of kv has {table.shape[0]} rows for {B} sequences")
-        _ints("block_table", table, *table.shape)
-        pool = (k_pool.shape[0], shape.Hkv, shape.blk, d)
-        _dense("k_pool", k_pool, dtype, *pool)
-        if v_pool is not None:  # (refused by the call where it has to be there)
-            _dense("v_pool", v_pool, dtype, *pool)
+        _check_cache(shape, dtype, *cache)
     _call(lib().sv_prefix_attend, (q, draft_k, draft_v, out, ws, *cache), stream, C.byref(shape),
           _dense("q", q, dtype, *rows), C.byref(kv), n_shared,
           _dense("draft_k", draft_k, dtype, *drafts), _dense("draft_v", draft_v, dtype, *drafts),
