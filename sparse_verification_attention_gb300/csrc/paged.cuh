@@ -119,7 +119,10 @@ __device__ __forceinline__ Cost cost_of(const PagedArgs& a, int n, int ctx) {
 //     units, but CTAs on the same keys are far apart in them.
 // Few rows over long contexts stream (16 ragged decoding sequences: 154 us cut
 // into runs and scheduled, CTAs ending between 60 and 100% of it, 119 us as
-// equal shares), long prompts do not.
+// equal shares), long prompts do not. What whole units lose at their end (half of the
+// longest unit, a tenth when every CTA has four or more), the 5% by which streaming has to
+// win and kStreamCost are estimates from such runs; they have not been swept around
+// the point where the two ways meet.
 __device__ inline void make_plan(const PagedArgs& a, Plan* p, int* scratch) {
   const int nseg = n_segs(a), lane = threadIdx.x & 31, padded = (nseg + 3) & ~3;
   int* kts = scratch;                         // cost of segment i's last unit

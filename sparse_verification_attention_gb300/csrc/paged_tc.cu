@@ -27,9 +27,10 @@
 // runs; TMEM has no room for a second S, P and O of 128 x 128 per set.
 //
 // What bounds it, long prompts: the tensor cores and their hand-offs. A 32768-token
-// prompt of 32/8 heads takes 5.63 ms, 1.56 PFLOP/s, 0.82 of the measured bf16
-// burst rate and 0.91 of the sustained one (1.98 GHz at the power limit); with the
-// softmax cut down to a copy it took 5.36 ms. What the steps gave, at that size: one
+// prompt of 32/8 heads takes 5.6 to 6.0 ms, as the power limit allows: 1.47 to 1.56
+// PFLOP/s, 0.77 to 0.82 of the measured bf16 burst rate and 0.86 to 0.91 of the
+// sustained one; with the softmax cut down to a copy it took 5.36 ms beside 5.63.
+// What the steps gave, at that size, in one session: one
 // thread a row and an MMA warp issuing from a branch of one lane 7.64 ms;
 // warp-uniform issue and two threads a row 6.86; waiters suspended instead of
 // polling (the polls took issue slots from the softmax) 6.39; the halves agreeing a
@@ -38,7 +39,8 @@
 // keys (four chains instead of two) were slower, 6.90: at N = 64 the operands'
 // shared-memory reads bound the product.
 // Few rows over long contexts: HBM, with the ring's 128 KB in flight per SM. A
-// 16-sequence decoding step reads 645 MB in 121 us, 0.78 of the measured copy rate.
+// 16-sequence decoding step reads 645 MB in 121 to 124 us, 0.77 of the measured copy
+// rate.
 //
 // Masked keys have P = 0, but 0 times a non-finite V is not 0: V tiles with a
 // masked key (behind the diagonal, past the context, drafts another draft does

@@ -94,9 +94,9 @@ __device__ inline int push_held(const TablesArgs& a, const int* s_rel, int R, in
 // releases again, counted.)
 //
 // Latency bound (a step of a decoding batch moves a few KB): one launch, no
-// atomics, two dependent rounds of loads before the barrier, two after. Both a
-// step of 8 requests and the admission of 144 prompts (74,000 tokens) take about
-// 10 us a call, which is what the host needs to make it.
+// atomics, two dependent rounds of loads before the barrier, two after. In a
+// replayed graph a step of 8 requests takes 4.9 us and the admission of 144 prompts
+// (74,000 tokens) 9.9 us; making the call takes the host about 10 us.
 __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const __grid_constant__ TablesArgs a) {
   extern __shared__ int s_start[];
   int* s_rel = s_start;                  // [B + 1]
