@@ -14,6 +14,12 @@
 namespace sva {
 namespace paged {
 
+// Order this thread's plain accesses to shared memory before bulk copies and
+// MMAs that a barrier orders behind it.
+__device__ __forceinline__ void fence_proxy_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 struct Seg {
   int tok0, n;  // first row and number of rows
   int ctx;      // keys

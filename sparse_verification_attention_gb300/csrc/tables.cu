@@ -14,6 +14,18 @@ constexpr int kTabThreads = 1024;
 constexpr int kTabPer = kMaxRequests / kTabThreads;  // requests per thread
 constexpr int kTabTokens = 4;                        // tokens per thread and round
 
+// A store to shared memory of any CTA of the cluster, and the two halves of
+// cluster_sync_all.
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // x / blk of a non-negative x: pages are powers of two nearly always.
 __device__ __forceinline__ int block_of(const TablesArgs& a, int x) {
   return a.blk_shift >= 0 ? x >> a.blk_shift : x / a.blk;
