@@ -462,7 +462,8 @@ sv_status sv_sparse_attend_noalloc(const sv_shape* shape, const void* q, const s
  * Flags in the workspace status word (workspace may be NULL):
  * SV_FLAG_NO_PAGE when the stack ran out (the remaining blocks, in order,
  * and their slots are -1, and *free_count_out is 0), SV_FLAG_BAD_PAGE for an
- * entry of the stack or the table outside [0, num_pages) (its slots are -1),
+ * entry of the stack or the table outside [0, num_pages) (its slots are -1;
+ * the -1 of a released block without a page raises nothing),
  * SV_FLAG_BAD_LENGTH for a length outside [0, nb_max * blk] or a count
  * outside [0, num_pages] (clamped), more new tokens than n_max (the excess
  * gets pages but no slots) or more free pages than num_pages.
