@@ -545,6 +545,146 @@ sv_status sv_prefix_attend(const sv_shape* shape, const void* q, const sv_kv* kv
                            const int32_t* draft_parent, void* out, void* workspace,
                            size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Between a fused projection and attention: head norms with the position
+ * rotation (rows to rows, or keys straight into the paged cache), and the same
+ * serving loop over a cache held in 4 bits. Lengths, slots and positions are
+ * DEVICE memory in all of these calls: nothing is read back, so a captured step
+ * follows them.
+ * ------------------------------------------------------------------------ */
+
+/* Norm and rotation of the heads of q and k. A head's row x of d elements
+ *   - is multiplied by weight / sqrt(mean(x^2) + eps) when the weight of its
+ *     side (q_weight, k_weight: [d], the shape's dtype, 16-byte aligned) is not
+ *     NULL;
+ *   - is then rotated in its first rot dims: pair i < rot / 2, the dims
+ *     (i, i + rot / 2) or, interleaved, (2 i, 2 i + 1), becomes
+ *     (a c - b s, b c + a s) with c = table[p][i], s = table[p][rot / 2 + i]
+ *     at the row's position p. The other dims stay.
+ * All of it in fp32, rounded once. rot: a multiple of 8 in [0, d]; 0 rotates
+ * nothing, and table and positions may be NULL. table: DEVICE fp32
+ * [max_pos, rot]. (A table and not frequencies: angles of far positions need
+ * more than 32 bits, and every model scales them in its own way.) */
+typedef struct {
+  const void* q_weight;
+  const void* k_weight;
+  const float* table;
+  float eps;
+  int max_pos;
+  int rot;
+  int interleaved;
+} sv_rope;
+
+/* Norm and rotation of n rows, rows to rows: what the drafts of a verification
+ * step need, whose keys enter the cache only when they are accepted.
+ * q, q_out: [n, Hq, d]; k, k_out: [n, Hkv, d]; rows the given strides apart
+ * (ELEMENTS, >= heads * d; base and stride multiples of 16 bytes), q_out may be
+ * q itself with its stride (in place), and k_out k; outputs must not overlap
+ * inputs otherwise. q may be NULL (keys only). positions: int32 [n], -1 for a
+ * row that is left out (padding of a captured step): its outputs stay as they
+ * are. A position outside [-1, max_pos) raises SV_FLAG_BAD_LENGTH in the status
+ * word (workspace may be NULL) and its row is left out too. shape: Hq, Hkv, d and
+ * dtype are used. */
+sv_status sv_norm_rope(const sv_shape* shape, const sv_rope* rope, const int32_t* positions, int n,
+                       const void* q, long long q_stride, const void* k, long long k_stride, void* q_out,
+                       long long q_out_stride, void* k_out, long long k_out_stride, void* workspace,
+                       void* stream);
+
+/* sv_norm_rope with the keys going straight into the paged cache, and the
+ * values beside them: sv_write_kv(sv_norm_rope(k), v) in one pass over the fused
+ * projection's rows, q to q_out in the same pass (q may be NULL). Slots as in
+ * sv_write_kv: -1 stores no key and value of the row (its q is still done), a
+ * slot outside the pool likewise and raises SV_FLAG_BAD_PAGE. */
+sv_status sv_rope_write_kv(const sv_shape* shape, const sv_rope* rope, const int32_t* positions, int n,
+                           const void* q, long long q_stride, void* q_out, long long q_out_stride,
+                           const void* k, long long k_stride, const void* v, long long v_stride,
+                           const int32_t* slot_map, void* k_pool, void* v_pool, int num_pages,
+                           void* workspace, void* stream);
+
+/* A paged K/V cache in 4 bits. Every 16 dims of a head of a token share a scale:
+ *   value = code * scale * 2^exp[h],
+ * code in E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), scale in E4M3
+ * (finite ones up to 448, the smallest 2^-9). The exponents, one per KV head
+ * and side, clamped to [-32, 32], move a head's values into the scales' range;
+ * NULL: all 0. They are the caller's and must be those the pages were written
+ * with. 4.5 bits an element.
+ * A pool is [num_pages][Hkv][blk / 16] pieces of 16 tokens, 9 d bytes each,
+ * sv_kv4_page_bytes() a page; a piece has 8 d bytes of codes, then d of scales:
+ *   k_pool: codes [d / 16][16 tokens][8], byte j = dims 2 j (low 4 bits) and
+ *           2 j + 1 of the group; scales [16 tokens][d / 16]
+ *   v_pool: codes [d / 16][8][16 tokens], byte c = dims c (low 4 bits) and
+ *           c + 8 of the group; scales [d / 16][16 tokens]
+ * Every byte belongs to one token. Needs d % 16 == 0 and blk % 16 == 0. Pools
+ * are 16-byte aligned device memory; any bytes are a valid page. block_table:
+ * [B, nb_max] as in sv_kv; seq_ctx: DEVICE int32 [B], the tokens of each
+ * sequence. The row calls (sv_write_kv4, sv_read_kv4) use neither. */
+typedef struct {
+  void* k_pool;
+  void* v_pool;
+  const int32_t* block_table;
+  const int32_t* seq_ctx;
+  const int32_t* k_exp;
+  const int32_t* v_exp;
+  int nb_max;
+  int num_pages;
+} sv_kv4;
+
+/* Bytes of one page of either pool, 0 on a shape that has no 4-bit cache. Host
+ * only. */
+size_t sv_kv4_page_bytes(const sv_shape* shape);
+
+/* Packed K/V rows into the 4-bit cache; rows, strides, slots and flags as in
+ * sv_write_kv. A group's scale is amax / 6 and a code element / scale, each
+ * rounded to the nearest value of its format, ties to even, beyond the largest
+ * one to it: infinities and what is too large become 6 * 448 * 2^exp. A group
+ * with a NaN reads back as NaNs. */
+sv_status sv_write_kv4(const sv_shape* shape, const void* k, long long k_stride, const void* v,
+                       long long v_stride, const int32_t* slot_map, int n, const sv_kv4* kv,
+                       void* workspace, void* stream);
+
+/* The inverse: rows k_out, v_out [n, Hkv, d] of the values at the slots (exact in
+ * bf16 and fp32), for a sequence that moves to another cache, or a chunk whose
+ * attention runs over an unquantised copy. Rows of slots -1, and of slots outside
+ * the pool (SV_FLAG_BAD_PAGE), stay as they are. Slots may repeat. */
+sv_status sv_read_kv4(const sv_shape* shape, const sv_kv4* kv, const int32_t* slot_map, int n,
+                      void* k_out, long long k_stride, void* v_out, long long v_stride, void* workspace,
+                      void* stream);
+
+/* Block representatives (sv_build_reps) of a 4-bit cache: the mean of the
+ * values of a block's keys, for the blocks from_len[b] / blk .. seq_ctx[b] / blk
+ * - 1 of every sequence, at most max_blocks of them (the first). from_len: DEVICE
+ * int32 [B], the lengths before the last writes, or NULL: from the beginning.
+ * reps: [B, Hkv, nb_max, d] fp32; the scoring calls take them as they are (their
+ * sv_kv descriptor names any pool: they read none). Blocks on a page outside the pool
+ * raise SV_FLAG_BAD_PAGE and are left out, lengths outside [0, nb_max * blk]
+ * raise SV_FLAG_BAD_LENGTH and are clamped (workspace may be NULL). */
+sv_status sv_build_reps_kv4(const sv_shape* shape, const sv_kv4* kv, const int32_t* from_len,
+                            int max_blocks, float* reps, void* workspace, void* stream);
+
+/* Bytes of workspace of sv_attend_kv4 calls with this shape. The whole
+ * workspace must be zero before its first use, and two calls that may overlap
+ * on the GPU must not share one. Its first 256 bytes hold the status word. 0 on
+ * an invalid shape. Host only. */
+size_t sv_kv4_workspace_bytes(const sv_shape* shape);
+
+/* Verification attention over a 4-bit cache: sv_sparse_attend (q, drafts,
+ * draft_parent, sel, out alike, softmax scale 1/sqrt(d)) with the values the
+ * cache stands for. T = 1 is a decoding step: the token's own key and value are
+ * the one draft. The drafts are not quantised.
+ * sel == NULL attends to every block; else [B, Hkv, sel_stride] with n_sel
+ * entries a row, n_sel <= sel_stride and nb_max, of which -1 holds nothing (the
+ * rows of sequences with smaller budgets) and others outside the sequence's full
+ * blocks are left out and raise SV_FLAG_BAD_BLOCK_INDEX. A partial last block is
+ * attended in every case, its first seq_ctx % blk tokens; the rest of its page
+ * may hold anything. Keys on a page outside the pool are left out
+ * (SV_FLAG_BAD_PAGE), lengths are clamped as above.
+ * Limits: B <= 1024; nb_max * blk, B * nb_max, B * T * Hq * 4 and
+ * num_pages * Hkv * blk < 2^31, B * nb_max * blk < 2^35. */
+sv_status sv_attend_kv4(const sv_shape* shape, const void* q, const sv_kv4* kv, const int32_t* sel,
+                        int n_sel, int sel_stride, const void* draft_k, const void* draft_v,
+                        const int32_t* draft_parent, void* out, void* workspace, size_t ws_bytes,
+                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif

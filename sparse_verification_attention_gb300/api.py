@@ -34,7 +34,9 @@ EXPORTED = ("sv_abi_version", "sv_last_error", "sv_budget_blocks", "sv_workspace
             "sv_verify_layer", "sv_sparse_attend_noalloc", "sv_append_kv",
             "sv_selection_overlap", "sv_reset_workspace", "sv_verify_layer_host",
             "sv_build_tables", "sv_write_kv", "sv_prompt_workspace_bytes",
-            "sv_prefix_workspace_bytes", "sv_prompt_attend", "sv_prefix_attend")
+            "sv_prefix_workspace_bytes", "sv_prompt_attend", "sv_prefix_attend", "sv_norm_rope",
+            "sv_rope_write_kv", "sv_kv4_page_bytes", "sv_write_kv4", "sv_read_kv4",
+            "sv_build_reps_kv4", "sv_kv4_workspace_bytes", "sv_attend_kv4")
 
 
 class SvError(RuntimeError):
@@ -58,6 +60,17 @@ class KV(C.Structure):
     _fields_ = [("k_pool", C.c_void_p), ("v_pool", C.c_void_p), ("block_table", C.c_void_p),
                 ("nb_max", C.c_int), ("num_pages", C.c_int), ("ctx", C.c_int),
                 ("seq_ctx", C.POINTER(C.c_int32))]
+
+
+class Rope(C.Structure):
+    _fields_ = [("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("table", C.c_void_p),
+                ("eps", C.c_float), ("max_pos", C.c_int), ("rot", C.c_int), ("interleaved", C.c_int)]
+
+
+class KV4(C.Structure):
+    _fields_ = [("k_pool", C.c_void_p), ("v_pool", C.c_void_p), ("block_table", C.c_void_p),
+                ("seq_ctx", C.c_void_p), ("k_exp", C.c_void_p), ("v_exp", C.c_void_p),
+                ("nb_max", C.c_int), ("num_pages", C.c_int)]
 
 
 class SelSlotC(C.Structure):
@@ -139,6 +152,17 @@ def lib() -> C.CDLL:
                                      sz, vp]),
             "sv_prefix_attend": (i, [C.POINTER(Shape), vp, C.POINTER(KV), i, vp, vp,
                                      C.POINTER(C.c_int32), vp, vp, sz, vp]),
+            "sv_norm_rope": (i, [C.POINTER(Shape), C.POINTER(Rope), vp, i, vp, ll, vp, ll, vp, ll, vp,
+                                 ll, vp, vp]),
+            "sv_rope_write_kv": (i, [C.POINTER(Shape), C.POINTER(Rope), vp, i, vp, ll, vp, ll, vp, ll,
+                                     vp, ll, vp, vp, vp, i, vp, vp]),
+            "sv_kv4_page_bytes": (sz, [C.POINTER(Shape)]),
+            "sv_write_kv4": (i, [C.POINTER(Shape), vp, ll, vp, ll, vp, i, C.POINTER(KV4), vp, vp]),
+            "sv_read_kv4": (i, [C.POINTER(Shape), C.POINTER(KV4), vp, i, vp, ll, vp, ll, vp, vp]),
+            "sv_build_reps_kv4": (i, [C.POINTER(Shape), C.POINTER(KV4), vp, i, vp, vp, vp]),
+            "sv_kv4_workspace_bytes": (sz, [C.POINTER(Shape)]),
+            "sv_attend_kv4": (i, [C.POINTER(Shape), vp, C.POINTER(KV4), vp, i, i, vp, vp,
+                                  C.POINTER(C.c_int32), vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -516,6 +540,194 @@ def sv_prefix_attend(shape: Shape, q, kv: KV, n_shared: int, draft_k, draft_v, p
     _call(lib().sv_prefix_attend, (q, draft_k, draft_v, out, ws, *cache), stream, C.byref(shape),
           _dense("q", q, dtype, *rows), C.byref(kv), n_shared,
           _dense("draft_k", draft_k, dtype, *drafts), _dense("draft_v", draft_v, dtype, *drafts),
+          _parents(parents), _dense("out", out, dtype, *rows), *_workspace(ws))
+
+
+# ------------------------------------------------------------------ head norms, rotation, 4-bit cache
+def rope_table(max_pos: int, rot: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Cosines and sines [max_pos, rot] fp32 of the plain rotation: pair i of
+    position p turns by p * theta^(-2 i / rot). Angles are taken in 64 bits; a
+    model with scaled frequencies makes its own table of this layout."""
+    if max_pos < 1 or rot < 8 or rot % 8:
+        raise ValueError("max_pos >= 1 and rot a positive multiple of 8")
+    freq = theta ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    angle = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def make_rope(table: Optional[torch.Tensor] = None, rot: Optional[int] = None, interleaved: bool = False,
+              q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+              eps: float = 1e-6) -> Rope:
+    """The norm and rotation of a model's heads. table: fp32 [max_pos, rot] (see
+    rope_table), None rotates nothing; weights [d], None norms nothing. The
+    returned structure keeps the tensors."""
+    if table is None:
+        if rot:
+            raise ValueError(f"a rotation of {rot} dims needs a table")
+        max_pos, rot = 0, 0
+    else:
+        if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous() or \
+                rot not in (None, table.shape[1]):
+            raise ValueError(f"table must be a contiguous float32 tensor [max_pos, rot]{'' if rot is None else f', rot {rot}'}")
+        max_pos, rot = table.shape
+    r = Rope(None if q_weight is None else q_weight.data_ptr(),
+             None if k_weight is None else k_weight.data_ptr(),
+             None if table is None else table.data_ptr(), eps, max_pos, rot, int(interleaved))
+    r._tensors = table, q_weight, k_weight
+    return r
+
+
+def _check_rope(rope: Rope, dtype: torch.dtype, d: int):
+    """The tensors of a rope descriptor, the weights checked against the call's heads."""
+    kept = getattr(rope, "_tensors", ())  # none in a descriptor filled by hand
+    for w in kept[1:]:
+        if w is not None and (w.dtype != dtype or w.shape != (d,) or not w.is_contiguous()):
+            raise ValueError(f"norm weights must be contiguous, of dtype {dtype} and of shape [{d}]")
+    return kept
+
+
+def sv_norm_rope(shape: Shape, rope: Rope, positions, q, k, q_out, k_out, ws=None, stream=None):
+    """Norm and rotate the heads of the rows q [n, Hq, d] (or None) and k [n, Hkv,
+    d]; rows may be strided, q_out may be q and k_out k. positions: int32 [n],
+    -1 leaves a row out (None when nothing is rotated)."""
+    d, dtype = shape.d, _DTYPES[shape.dtype]
+    n = k.shape[0]
+    ks, kos = _rows("k", k, dtype, shape.Hkv, d), _rows("k_out", k_out, dtype, shape.Hkv, d)
+    if k_out.shape[0] != n:
+        raise ValueError(f"{n} key rows and {k_out.shape[0]} rows to write")
+    qp, qs, qop, qos = _q_rows(shape, dtype, n, q, q_out)
+    _call(lib().sv_norm_rope, (k, q, q_out, k_out, positions, ws, *_check_rope(rope, dtype, d)), stream,
+          C.byref(shape), C.byref(rope), None if positions is None else _ints("positions", positions, n),
+          n, qp, qs, k.data_ptr(), ks, qop, qos, k_out.data_ptr(), kos, _workspace(ws)[0])
+
+
+def _q_rows(shape: Shape, dtype: torch.dtype, n: int, q, q_out):
+    """Addresses and strides of a call's query rows and of where they go."""
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out are given together")
+    if q is None:
+        return None, 0, None, 0
+    qs, qos = _rows("q", q, dtype, shape.Hq, shape.d), _rows("q_out", q_out, dtype, shape.Hq, shape.d)
+    if q.shape[0] != n or q_out.shape[0] != n:
+        raise ValueError(f"{n} key rows, {q.shape[0]} query rows and {q_out.shape[0]} rows to write")
+    return q.data_ptr(), qs, q_out.data_ptr(), qos
+
+
+def sv_rope_write_kv(shape: Shape, rope: Rope, positions, q, k, v, q_out, slot_map, k_pool, v_pool, ws=None,
+                     stream=None):
+    """sv_norm_rope with the keys, and the values v [n, Hkv, d] beside them, stored
+    at their slots of the paged cache; q and q_out may be None."""
+    H, d, dtype = shape.Hkv, shape.d, _DTYPES[shape.dtype]
+    n, pages = k.shape[0], k_pool.shape[0]
+    ks, vs = _rows("k", k, dtype, H, d), _rows("v", v, dtype, H, d)
+    if v.shape[0] != n:
+        raise ValueError(f"{n} key rows and {v.shape[0]} value rows")
+    qp, qs, qop, qos = _q_rows(shape, dtype, n, q, q_out)
+    pool = (pages, H, shape.blk, d)
+    _call(lib().sv_rope_write_kv,
+          (k, v, q, q_out, positions, slot_map, k_pool, v_pool, ws, *_check_rope(rope, dtype, d)), stream,
+          C.byref(shape), C.byref(rope), None if positions is None else _ints("positions", positions, n),
+          n, qp, qs, qop, qos, k.data_ptr(), ks, v.data_ptr(), vs, _ints("slot_map", slot_map, n),
+          _dense("k_pool", k_pool, dtype, *pool), _dense("v_pool", v_pool, dtype, *pool), pages,
+          _workspace(ws)[0])
+
+
+def alloc_kv4_pool(shape: Shape, pages: int, device="cuda") -> torch.Tensor:
+    """A zeroed pool of a 4-bit cache: uint8 [pages, Hkv, blk / 16, 9 d]."""
+    if lib().sv_kv4_page_bytes(C.byref(shape)) == 0:
+        _check(SV_ERR_INVALID_ARG)
+    return torch.zeros(pages, shape.Hkv, shape.blk // 16, 9 * shape.d, dtype=torch.uint8, device=device)
+
+
+def make_kv4(k_pool: torch.Tensor, v_pool: torch.Tensor, block_table: Optional[torch.Tensor] = None,
+             seq_ctx: Optional[torch.Tensor] = None, k_exp: Optional[torch.Tensor] = None,
+             v_exp: Optional[torch.Tensor] = None) -> KV4:
+    """The descriptor of a 4-bit cache. seq_ctx (int32 [B]) lies on the device; the
+    row calls need neither it nor block_table. k_exp, v_exp: int32 [Hkv], the heads'
+    exponents. The returned structure keeps the tensors."""
+    ptr = [None if t is None else t.data_ptr() for t in (k_pool, v_pool, block_table, seq_ctx, k_exp, v_exp)]
+    kv = KV4(*ptr, 0 if block_table is None else block_table.shape[-1], k_pool.shape[0])
+    kv._tensors = k_pool, v_pool, block_table, seq_ctx, k_exp, v_exp
+    return kv
+
+
+def _check_kv4(shape: Shape, kv: KV4, seqs: bool):
+    """A descriptor's tensors, which must be a 4-bit cache of this shape (and hold
+    shape.B sequences)."""
+    kept = getattr(kv, "_tensors", ())  # none in a descriptor filled by hand
+    if not kept:
+        return kept
+    k_pool, v_pool, table, seq_ctx, k_exp, v_exp = kept
+    pool = (k_pool.shape[0], shape.Hkv, shape.blk // 16, 9 * shape.d)
+    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+        if t.dtype != torch.uint8 or t.shape != pool or not t.is_contiguous():
+            raise ValueError(f"the {name} of kv must be contiguous, uint8 and of shape {list(pool)}")
+    for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
+        if t is not None:
+            _ints(f"the {name} of kv", t, shape.Hkv)
+    if seqs:
+        if table is None or seq_ctx is None:
+            raise ValueError("kv needs a block_table and seq_ctx for this call")
+        _ints("the block_table of kv", table, shape.B, table.shape[-1])
+        _ints("the seq_ctx of kv", seq_ctx, shape.B)
+    return kept
+
+
+def sv_write_kv4(shape: Shape, k, v, slot_map, kv: KV4, ws=None, stream=None):
+    """Store the rows k, v [n, Hkv, d] (slices of a fused projection are fine) in 4
+    bits at their slots; slots of -1 are skipped."""
+    H, d, dtype = shape.Hkv, shape.d, _DTYPES[shape.dtype]
+    ks, vs, n = _rows("k", k, dtype, H, d), _rows("v", v, dtype, H, d), k.shape[0]
+    if v.shape[0] != n:
+        raise ValueError(f"{n} key rows and {v.shape[0]} value rows")
+    _call(lib().sv_write_kv4, (k, v, slot_map, ws, *_check_kv4(shape, kv, False)), stream, C.byref(shape),
+          k.data_ptr(), ks, v.data_ptr(), vs, _ints("slot_map", slot_map, n), n, C.byref(kv),
+          _workspace(ws)[0])
+
+
+def sv_read_kv4(shape: Shape, kv: KV4, slot_map, k_out, v_out, ws=None, stream=None):
+    """The rows k_out, v_out [n, Hkv, d] of the values at the slots of a 4-bit cache;
+    rows of slots -1 stay as they are."""
+    H, d, dtype = shape.Hkv, shape.d, _DTYPES[shape.dtype]
+    ks, vs, n = _rows("k_out", k_out, dtype, H, d), _rows("v_out", v_out, dtype, H, d), k_out.shape[0]
+    if v_out.shape[0] != n:
+        raise ValueError(f"{n} key rows and {v_out.shape[0]} value rows")
+    _call(lib().sv_read_kv4, (k_out, v_out, slot_map, ws, *_check_kv4(shape, kv, False)), stream,
+          C.byref(shape), C.byref(kv), _ints("slot_map", slot_map, n), n, k_out.data_ptr(), ks,
+          v_out.data_ptr(), vs, _workspace(ws)[0])
+
+
+def sv_build_reps_kv4(shape: Shape, kv: KV4, max_blocks: int, reps, from_len=None, ws=None, stream=None):
+    """Representatives of the blocks that sequences filled since they had from_len
+    tokens (int32 [B], None: since the beginning), at most max_blocks each. reps:
+    float32 [B, Hkv, nb_max, d]."""
+    B = shape.B
+    _call(lib().sv_build_reps_kv4, (reps, from_len, ws, *_check_kv4(shape, kv, True)), stream,
+          C.byref(shape), C.byref(kv), None if from_len is None else _ints("from_len", from_len, B),
+          max_blocks, _dense("reps", reps, torch.float32, B, shape.Hkv, kv.nb_max, shape.d),
+          _workspace(ws)[0])
+
+
+def alloc_kv4_workspace(shape: Shape, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for sv_attend_kv4 calls with this shape."""
+    return _alloc_zeroed(lib().sv_kv4_workspace_bytes(C.byref(shape)), device)
+
+
+def sv_attend_kv4(shape: Shape, q, kv: KV4, sel, draft_k, draft_v, parents, out, ws,
+                  n_sel: Optional[int] = None, stream=None):
+    """Verification attention over a 4-bit cache: every block when sel is None, else
+    the first n_sel (all, when None) entries of the rows sel [B, Hkv, kmax]; -1
+    entries hold nothing. T = 1 is a decoding step."""
+    B, T, H, d, dtype = shape.B, shape.T, shape.Hkv, shape.d, _DTYPES[shape.dtype]
+    rows, drafts = (B, T, shape.Hq, d), (B, T, H, d)
+    if parents is not None and len(parents) != T:
+        raise ValueError(f"{len(parents)} draft parents for T={T} drafts")
+    stride = 0 if sel is None else sel.shape[-1]
+    # an empty selection has no address, and none would mean every block: any other does, as no entry is read
+    sel_ptr = None if sel is None else _ints("sel", sel, B, H, stride) or kv.block_table
+    _call(lib().sv_attend_kv4, (q, sel, draft_k, draft_v, out, ws, *_check_kv4(shape, kv, True)), stream,
+          C.byref(shape), _dense("q", q, dtype, *rows), C.byref(kv),
+          sel_ptr, stride if n_sel is None else n_sel, stride, _dense("draft_k", draft_k, dtype, *drafts), _dense("draft_v", draft_v, dtype, *drafts),
           _parents(parents), _dense("out", out, dtype, *rows), *_workspace(ws))
 
 

@@ -1,0 +1,172 @@
+// Device code that the 4-bit cache kernels share: the two 4- and 8-bit formats,
+// and the attention's work split.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "kv4.h"
+#include "ptx.h"
+
+namespace sva {
+namespace kv4 {
+
+// ---------------------------------------------------------------- formats
+// Two E2M1 codes of one byte (low bits first) as a pair of halves, exact.
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(r) : "r"(byte));
+  return r;
+}
+// Two E4M3 scales (low byte first) as a pair of halves, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t x) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+__device__ __forceinline__ float e4m3_to_f32(uint32_t byte) { return f16x2_to_f32(e4m3x2_to_f16x2(byte & 0xffu)).x; }
+// lo and hi, rounded to E2M1 (ties to even, 6 at most), in one byte.
+__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+// x >= 0 rounded to E4M3 (ties to even, 448 at most; NaN to NaN).
+__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
+  return r & 0xffu;
+}
+
+constexpr int kMaxExp = 32;  // a head's exponent lies in [-32, 32]
+__device__ __forceinline__ int head_exp(const int32_t* e, int h) {
+  return e ? min(max(e[h], -kMaxExp), kMaxExp) : 0;
+}
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((127 + e) << 23); }
+
+// ---------------------------------------------------------------- work split
+__device__ __forceinline__ int ctx_of(const Attend4Args& a, int b) {
+  return min(max(a.seq_ctx[b], 0), a.nb_max * a.blk);
+}
+__device__ __forceinline__ int pieces_of(const Attend4Args& a, int ctx) {
+  const int full = ctx / a.blk, rest = ctx - full * a.blk;
+  return (a.sel ? a.n_sel : full) * a.ppb + (rest + kPiece - 1) / kPiece;
+}
+
+// Prefix sums of the key tiles (one warp): cu[0 .. B]. Returns whether a length was
+// clamped, in any lane that saw one.
+__device__ __forceinline__ bool scan_tiles(const Attend4Args& a, int* cu) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  bool bad = false;
+  if (lane == 0) cu[0] = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    int x = 0;
+    if (b < a.B) {
+      const int c = ctx_of(a, b);
+      bad |= c != a.seq_ctx[b];
+      x = (pieces_of(a, c) + a.ppt - 1) / a.ppt;
+    }
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    if (b < a.B) cu[b + 1] = carry + x;
+    carry += __shfl_sync(0xffffffffu, x, 31);
+  }
+  return bad;
+}
+
+// The line of all key tiles and the CTAs that share it.
+struct Line {
+  long long total;
+  int ctas;
+  __device__ __forceinline__ long long first(int c) const { return c * total / ctas; }
+  // the CTA that has tile x
+  __device__ __forceinline__ int cta_of(long long x) const { return (int)(((x + 1) * ctas - 1) / total); }
+};
+__device__ __forceinline__ Line line_of(const Attend4Args& a, int tiles) {
+  Line l;
+  l.total = (long long)tiles * a.Hkv * a.row_tiles;
+  l.ctas = (int)min((long long)a.ctas, l.total);  // every CTA has a tile
+  return l;
+}
+
+struct Segment {
+  int b, h, rt;      // the pair
+  int tile0, tiles;  // its key tiles
+  int ctx, pieces;
+  long long slot;
+};
+// The segment that begins at position x of the line (x < end, the CTA's share's end).
+__device__ __forceinline__ Segment segment_at(const Attend4Args& a, const int* cu, long long x,
+                                              long long end, int cta) {
+  Segment s;
+  const int per = a.Hkv * a.row_tiles;
+  const int y = (int)(x / per);
+  int lo = 0, hi = a.B;  // the last b with cu[b] <= y; the sequences without keys before it do not count
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (cu[m] <= y) lo = m;
+    else hi = m;
+  }
+  s.b = lo;
+  const int n = cu[lo + 1] - cu[lo];
+  const long long in = x - (long long)cu[lo] * per;
+  const int pair = (int)(in / n);
+  s.tile0 = (int)(in - (long long)pair * n);
+  s.h = pair / a.row_tiles;
+  s.rt = pair - s.h * a.row_tiles;
+  s.tiles = (int)min((long long)(n - s.tile0), end - x);
+  s.ctx = ctx_of(a, lo);
+  s.pieces = pieces_of(a, s.ctx);
+  s.slot = (long long)lo * per + pair + cta;
+  return s;
+}
+
+// Where piece i of a segment's (sequence, head) lies in the pools (in pieces, -1:
+// nowhere), and how many of its tokens count.
+__device__ __forceinline__ long long piece_at(const Attend4Args& a, const Segment& s, int i, int* valid,
+                                              unsigned* flags) {
+  *valid = 0;
+  if (i >= s.pieces) return -1;
+  const int full = s.ctx / a.blk, slots = a.sel ? a.n_sel : full;
+  const int at = i / a.ppb;
+  int block = at, sub = i - at * a.ppb;
+  if (at >= slots) {  // the partial last block
+    block = full;
+    sub = i - slots * a.ppb;
+    *valid = min(kPiece, s.ctx - full * a.blk - sub * kPiece);
+  } else {
+    if (a.sel) {
+      block = a.sel[((long long)s.b * a.Hkv + s.h) * a.sel_stride + at];
+      if (block < 0 || block >= full) {
+        if (block != -1) *flags |= SV_FLAG_BAD_BLOCK_INDEX;
+        return -1;
+      }
+    }
+    *valid = kPiece;
+  }
+  const int page = a.block_table[(long long)s.b * a.nb_max + block];
+  if (page < 0 || page >= a.num_pages) {
+    *flags |= SV_FLAG_BAD_PAGE;
+    *valid = 0;
+    return -1;
+  }
+  return ((long long)page * a.Hkv + s.h) * a.ppb + sub;
+}
+
+// Row r of a (sequence, head): draft t, query head h * G + g, r = t * G + g.
+__device__ __forceinline__ long long row_at(const Attend4Args& a, int b, int h, int r) {
+  const int t = r / a.G;
+  return ((long long)b * a.T + t) * a.Hq + h * a.G + (r - t * a.G);
+}
+
+}  // namespace kv4
+}  // namespace sva

@@ -1,0 +1,130 @@
+// The drafts, and the join of a row's segments: what sv_attend_kv4 does behind the
+// attention over the cache. A row's own drafts stay in the call's type; there are at
+// most 64 of them, so fp32 on the CUDA cores costs little and needs no tile.
+#include "kv4.cuh"
+
+namespace sva {
+namespace {
+
+using namespace kv4;
+
+constexpr int kThreads = 256;
+
+// Four consecutive elements as floats, and back.
+__device__ __forceinline__ float4 load4(const float* p) { return __ldcg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = __ldcg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+}
+__device__ __forceinline__ float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w; }
+__device__ __forceinline__ void axpy4(float4& o, float w, float4 x) {
+  o.x += w * x.x;
+  o.y += w * x.y;
+  o.z += w * x.z;
+  o.w += w * x.w;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// One warp per output row; a lane has dims 4 lane .. + 3 (and 128 + that for d > 128).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) join4_kernel(const __grid_constant__ Attend4Args a) {
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  pdl_wait();
+  pdl_trigger();
+  if (row >= (long long)a.B * a.T * a.Hq) return;
+  const int tok = (int)(row / a.Hq), head = (int)(row - (long long)tok * a.Hq), b = tok / a.T, t = tok - b * a.T;
+  const int h = head / a.G, r = t * a.G + head - h * a.G, rt = r / a.rows;
+  const bool has[2] = {lane * 4 < a.d, 128 + lane * 4 < a.d};
+  float4 q[2], o[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    q[i] = o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (has[i]) q[i] = load4(static_cast<const T*>(a.q) + row * a.d + 128 * i + lane * 4);
+  }
+  // the drafts that t sees: scores of the i-th in lane i % 32
+  const unsigned long long see = a.anc[t];
+  const int n = __popcll(see);
+  const T* dk = static_cast<const T*>(a.draft_k) + ((long long)b * a.T * a.Hkv + h) * a.d;
+  const T* dv = static_cast<const T*>(a.draft_v) + ((long long)b * a.T * a.Hkv + h) * a.d;
+  const long long step = (long long)a.Hkv * a.d;
+  float s0 = -INFINITY, s1 = -INFINITY;
+  int i = 0;
+  for (unsigned long long w = see; w; w &= w - 1, ++i) {
+    const T* k = dk + (__ffsll(w) - 1) * step;
+    float x = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (has[j]) x += dot4(q[j], load4(k + 128 * j + lane * 4));
+    x = warp_sum(x) * a.scale_log2;
+    if (lane == (i & 31)) (i < 32 ? s0 : s1) = x;
+  }
+  // the row's segments: CTAs c0 .. c1 of the line
+  const int start = a.cu[b], tiles = a.cu[b + 1] - start, per = a.Hkv * a.row_tiles;
+  const int pair = h * a.row_tiles + rt;
+  const Line line = line_of(a, a.cu[a.B]);
+  const long long first = (long long)start * per + (long long)pair * tiles;
+  int c0 = 0, c1 = -1;
+  if (tiles) {
+    c0 = line.cta_of(first);
+    c1 = line.cta_of(first + tiles - 1);
+  }
+  const long long at0 = ((long long)b * per + pair + c0) * a.rows + r - rt * a.rows;
+  // the largest reference, of the segments and of the drafts
+  float m = fmaxf(s0, s1);
+  for (int c = lane; c <= c1 - c0; c += 32) m = fmaxf(m, a.part_ml[at0 + (long long)c * a.rows].x);
+  m = warp_max(m);
+  const float p0 = lane < n ? exp2f(s0 - m) : 0.f, p1 = lane + 32 < n ? exp2f(s1 - m) : 0.f;
+  float l = warp_sum(p0 + p1);
+  const float unit = exp2i(head_exp(a.v_exp, h));
+  for (int c = 0; c <= c1 - c0; ++c) {
+    const long long at = at0 + (long long)c * a.rows;
+    const float2 ml = __ldcg(a.part_ml + at);
+    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // no key of the segment counted
+    const float w = exp2f(ml.x - m);
+    l += w * ml.y;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (has[j]) axpy4(o[j], w * unit, load4(a.part_o + at * a.d + 128 * j + lane * 4));
+  }
+  i = 0;
+  for (unsigned long long w = see; w; w &= w - 1, ++i) {
+    const T* v = dv + (__ffsll(w) - 1) * step;
+    const float p = __shfl_sync(0xffffffffu, i < 32 ? p0 : p1, i & 31);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (has[j]) axpy4(o[j], p, load4(v + 128 * j + lane * 4));
+  }
+  const float inv = __frcp_rn(l);
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (has[j]) {
+      const float4 y = make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv);
+      store4(static_cast<T*>(a.out) + row * a.d + 128 * j + lane * 4, y);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_join4(const Attend4Args& a, int dtype, cudaStream_t st) {
+  const long long rows = (long long)a.B * a.T * a.Hq;
+  const dim3 grid((unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32)));
+  return dtype == SV_BF16 ? launch_pdl(join4_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, a)
+                          : launch_pdl(join4_kernel<float>, grid, dim3(kThreads), 0, st, a);
+}
+
+}  // namespace sva
