@@ -678,6 +678,10 @@ size_t sv_kv4_workspace_bytes(const sv_shape* shape);
  * attended in every case, its first seq_ctx % blk tokens; the rest of its page
  * may hold anything. Keys on a page outside the pool are left out
  * (SV_FLAG_BAD_PAGE), lengths are clamped as above.
+ * On the tensor cores the products take values and weights in f16: values are
+ * exact, q is scaled by a power of two per row (exact down to 2^-24 of the row's
+ * largest element), a softmax weight is rounded to f16 (2^-11) ahead of the
+ * product with V, its sum is taken before, in fp32.
  * Limits: B <= 1024; nb_max * blk, B * nb_max, B * T * Hq * 4 and
  * num_pages * Hkv * blk < 2^31, B * nb_max * blk < 2^35. */
 sv_status sv_attend_kv4(const sv_shape* shape, const void* q, const sv_kv4* kv, const int32_t* sel,

@@ -66,7 +66,9 @@ cudaError_t launch_reps_kv4(const Reps4Args& a, cudaStream_t st);
 // ---------------------------------------------------------------- attention
 constexpr int kMaxB4 = 1024;         // sequences of a call
 constexpr int kSimt4Rows = 32;       // row tile on the CUDA cores
+constexpr int kTc4Rows = 128;        // ... and on the tensor cores, at most
 constexpr int kMaxSimt4Ctas = 640;   // CTAs of a launch at most
+constexpr int kMaxTc4Ctas = 160;
 
 // The T * G stacked rows of a (sequence, KV head) are cut into row tiles; a pair
 // is one row tile of one (sequence, head). A pair's pieces (16 keys each) make
@@ -95,6 +97,9 @@ struct Attend4Args {
 };
 // Each launches the attention over the cache and then the join with the drafts.
 cudaError_t launch_attend4_simt(Attend4Args a, int dtype, cudaStream_t st);
+// bf16, head dims up to 128.
+bool attend4_tc_applies(const Attend4Args& a, int dtype);
+cudaError_t launch_attend4_tc(Attend4Args a, cudaStream_t st);
 // Adds the drafts to what the attention launched just before left (the same
 // arguments) and writes out.
 cudaError_t launch_join4(const Attend4Args& a, int dtype, cudaStream_t st);

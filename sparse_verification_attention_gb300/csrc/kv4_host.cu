@@ -126,8 +126,13 @@ struct Layout4 {
   size_t cu, ml, o, total;
 };
 Layout4 layout4(const sv_shape& s) {
-  const long long stacked = (long long)s.T * (s.Hq / s.Hkv), r = std::min<long long>(kSimt4Rows, stacked);
-  const size_t rows = (size_t)(((stacked + r - 1) / r * s.B * s.Hkv + kMaxSimt4Ctas) * r);
+  size_t rows = 0;
+  const long long stacked = (long long)s.T * (s.Hq / s.Hkv), pairs = (long long)s.B * s.Hkv;
+  const int most[2] = {kSimt4Rows, kTc4Rows}, ctas[2] = {kMaxSimt4Ctas, kMaxTc4Ctas};
+  for (int i = 0; i < 2; ++i) {
+    const long long tiles = (stacked + most[i] - 1) / most[i], r = std::min<long long>(most[i], stacked);
+    rows = std::max(rows, (size_t)((tiles * pairs + ctas[i]) * r));
+  }
   Layout4 L;
   L.cu = kStatusBytes;
   L.ml = L.cu + align256((s.B + 1) * sizeof(int));
@@ -343,7 +348,8 @@ sv_status sv_attend_kv4(const sv_shape* shape, const void* q, const sv_kv4* kv, 
   a.ppb = shape->blk / kPiece;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)shape->d));
   fill_ancestors(draft_parent, shape->T, a.anc);
-  const cudaError_t e = launch_attend4_simt(a, shape->dtype, (cudaStream_t)stream);
+  const cudaError_t e = attend4_tc_applies(a, shape->dtype) ? launch_attend4_tc(a, (cudaStream_t)stream)
+                                                            : launch_attend4_simt(a, shape->dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? SV_OK : cuda_fail(e, "attend_kv4 launch");
 }
 
