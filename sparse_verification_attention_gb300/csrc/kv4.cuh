@@ -11,13 +11,44 @@ namespace sva {
 namespace kv4 {
 
 // ---------------------------------------------------------------- formats
-// Two E2M1 codes of one byte (low bits first) as a pair of halves, exact.
+// E2M1 codes of the four bytes of a word (low bits first) as pairs of halves, exact. The
+// word is taken apart by a move: with shifts and masks a conversion cost 6 issue
+// slots instead of 2 to 3 (and a converter is half a slot wide).
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t* r) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+// ... of bytes 0 and 2 alone.
+__device__ __forceinline__ void e2m1x4_to_f16(uint32_t w, uint32_t& r0, uint32_t& r2) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, c;\n\t}"
+      : "=r"(r0), "=r"(r2)
+      : "r"(w));
+}
 __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
   uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(r) : "r"(byte));
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
+      : "=r"(r)
+      : "r"(byte));
   return r;
 }
-// Two E4M3 scales (low byte first) as a pair of halves, exact.
+// E4M3 scales of the four bytes of a word as two pairs of halves, exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& r01, uint32_t& r23) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(r01), "=r"(r23)
+      : "r"(w));
+}
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));

@@ -109,6 +109,9 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
   return r;
 }
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t x) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+}
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   uint32_t r;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
@@ -136,6 +139,14 @@ __device__ __forceinline__ float redux_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
+// The rest of a wait, out of line: four roles' loops share an SM quarter's instruction
+// cache, and with every wait's clock and limit inline (and the loops unrolled) they did
+// not fit. 128 K tokens x 4 took 495 us, most of it waiting for instructions.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* status,
+                                     unsigned site) {
+  return mbar_wait_abortable(bar, parity, abort, status, site);
+}
+
 // DG: groups of 16 dims (8: d = 128), 0: any number up to 8.
 template <int N, int DG>
 __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) attend4_tc_kernel(const __grid_constant__ Attend4Args a, int stages) {
@@ -194,7 +205,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) attend4_tc_kernel(const _
   const long long begin = cta < line.ctas ? line.first(cta) : 0, end = cta < line.ctas ? line.first(cta + 1) : 0;
   const uint32_t tiles = (uint32_t)(end - begin);
   auto wait = [&](uint64_t& bar, uint32_t parity, unsigned site) {
-    return mbar_wait_abortable(smem_u32(&bar), parity & 1u, &sh.abort, a.status, site);
+    const uint32_t addr = smem_u32(&bar);
+    return mbar_try_wait(addr, parity & 1u) || wait_on(addr, parity & 1u, &sh.abort, a.status, site);
   };
 
   if (warp < 4) {
@@ -207,28 +219,24 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) attend4_tc_kernel(const _
       tc::fence_after();
       const uint32_t codes = ring + st * stage_bytes + piece * pb, scales = codes + groups * 128 + tok * groups;
       const uint32_t to = tmem + tlane + kColK + (i & 1) * 64;
-      uint32_t sc[4];
-      if constexpr (DG == 8) {
-        const uint2 s8 = lds64(scales);
-        sc[0] = e4m3x2_to_f16x2(s8.x & 0xffffu);
-        sc[1] = e4m3x2_to_f16x2(s8.x >> 16);
-        sc[2] = e4m3x2_to_f16x2(s8.y & 0xffffu);
-        sc[3] = e4m3x2_to_f16x2(s8.y >> 16);
-      }
-#pragma unroll
-      for (int g = 0; g < (DG ? DG : 8); g += 2) {
+#pragma unroll 1
+      for (int g = 0; g < groups; g += 2) {
         uint32_t r[16];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          uint32_t two;
-          if constexpr (DG == 8) two = __byte_perm(sc[g / 2], 0, j ? 0x3232 : 0x1010);
-          else two = g + j < groups ? __byte_perm(e4m3x2_to_f16x2(lds8(scales + g + j)), 0, 0x1010) : 0u;
-          const uint2 w = DG || g + j < groups ? lds64(codes + (g + j) * 128 + tok * 8) : make_uint2(0, 0);
+          if (!DG && g + j >= groups) {  // the second half of the last pair
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            r[8 * j + e] = mul_f16x2(e2m1x2_to_f16x2((e < 4 ? w.x : w.y) >> (e % 4 * 8) & 0xffu), two);
+            for (int e = 0; e < 8; ++e) r[8 * j + e] = 0;
+            continue;
+          }
+          const uint32_t two = __byte_perm(e4m3x2_to_f16x2(lds8(scales + g + j)), 0, 0x1010);
+          const uint2 w = lds64(codes + (g + j) * 128 + tok * 8);
+          e2m1x8_to_f16(w.x, r + 8 * j);
+          e2m1x8_to_f16(w.y, r + 8 * j + 4);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r[8 * j + e] = mul_f16x2(r[8 * j + e], two);
         }
-        if (DG || g < groups) tc::st16(to + g * 8, r);
+        tc::st16(to + g * 8, r);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.empty[st]));
@@ -248,34 +256,39 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) attend4_tc_kernel(const _
       tc::fence_after();
       const uint64_t valid = sh.info[i % kInfo].valid;
       const uint32_t from = ring + st * stage_bytes + side;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int g = 2 * w + j;
-        if (!DG && g >= groups) break;
-        const uint32_t to = tmem + ((uint32_t)(w * 32 + j * 16) << 16) + kColV + (i & 1) * 64;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t r[16];
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const uint32_t at = from + (4 * half + p) * pb;
-            const uint32_t c = lds32(at + g * 128 + lane * 4);
-            uint32_t s = lds32(at + groups * 128 + g * 16 + t4 * 4);
-            if (valid != kAllValid) {  // tokens that do not count: whatever their bytes hold, zero
-              const int n = (int)(valid >> (8 * (4 * half + p)) & 0xff) - (int)t4 * 4;
-              s = n >= 4 ? s : n <= 0 ? 0u : s & ((1u << (8 * n)) - 1u);
-            }
-            const uint32_t c4 = c >> 4, c8 = c >> 8;
-            const uint32_t lo = (c & 0x000f000fu) | (c4 & 0xfff0fff0u);   // bytes 0, 2: tokens (0, 1), (2, 3)
-            const uint32_t hi = (c4 & 0x000f000fu) | (c8 & 0xfff0fff0u);  // ... of the dim 8 behind
-            const uint32_t s01 = e4m3x2_to_f16x2(s & 0xffffu), s23 = e4m3x2_to_f16x2(s >> 16);
-            r[4 * p] = mul_f16x2(e2m1x2_to_f16x2(lo & 0xffu), s01);
-            r[4 * p + 1] = mul_f16x2(e2m1x2_to_f16x2(lo >> 16 & 0xffu), s23);
-            r[4 * p + 2] = mul_f16x2(e2m1x2_to_f16x2(hi & 0xffu), s01);
-            r[4 * p + 3] = mul_f16x2(e2m1x2_to_f16x2(hi >> 16 & 0xffu), s23);
-          }
-          st_16x256b_x4(to + half * 32, r);
+      if (valid != kAllValid) {
+        // tokens that do not count get a scale of zero, whatever their bytes hold: the
+        // warp's two groups x 128 tokens, 4 tokens at a time
+        for (int e = lane; e < 64; e += 32) {
+          const int g = 2 * w + (e >> 5), p = e >> 2 & 7, n = (int)(valid >> (8 * p) & 0xff) - (e & 3) * 4;
+          const uint32_t at = from + p * pb + groups * 128 + g * 16 + (e & 3) * 4;
+          if (g < groups && n < 4) sts32(at, n <= 0 ? 0u : lds32(at) & ((1u << (8 * n)) - 1u));
         }
+        fence_proxy_async_shared();  // ahead of the next copy into the stage
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {  // group q / 2 of the warp's two, half q % 2 of the keys
+        const int g = 2 * w + (q >> 1);
+        if (!DG && g >= groups) break;
+        const uint32_t code = from + (q & 1) * 4 * pb + g * 128 + lane * 4;
+        const uint32_t scale = from + (q & 1) * 4 * pb + groups * 128 + g * 16 + t4 * 4;
+        uint32_t r[16];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t c = lds32(code + p * pb), s = lds32(scale + p * pb), c4 = c >> 4, c8 = c >> 8;
+          const uint32_t lo = (c & 0x000f000fu) | (c4 & 0xfff0fff0u);   // bytes 0, 2: tokens (0, 1), (2, 3)
+          const uint32_t hi = (c4 & 0x000f000fu) | (c8 & 0xfff0fff0u);  // ... of the dim 8 behind
+          uint32_t s01, s23;
+          e4m3x4_to_f16(s, s01, s23);
+          e2m1x4_to_f16(lo, r[4 * p], r[4 * p + 1]);
+          e2m1x4_to_f16(hi, r[4 * p + 2], r[4 * p + 3]);
+          r[4 * p] = mul_f16x2(r[4 * p], s01);
+          r[4 * p + 1] = mul_f16x2(r[4 * p + 1], s23);
+          r[4 * p + 2] = mul_f16x2(r[4 * p + 2], s01);
+          r[4 * p + 3] = mul_f16x2(r[4 * p + 3], s23);
+        }
+        st_16x256b_x4(tmem + ((uint32_t)(w * 32 + (q >> 1) * 16) << 16) + kColV + (i & 1) * 64 + (q & 1) * 32, r);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.empty[st]));
