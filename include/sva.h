@@ -683,7 +683,8 @@ size_t sv_kv4_workspace_bytes(const sv_shape* shape);
  * largest element), a softmax weight is rounded to f16 (2^-11) ahead of the
  * product with V, its sum is taken before, in fp32.
  * Limits: B <= 1024; nb_max * blk, B * nb_max, B * T * Hq * 4 and
- * num_pages * Hkv * blk < 2^31, B * nb_max * blk < 2^35. */
+ * num_pages * Hkv * blk < 2^31, B * nb_max * blk < 2^35 and, with the
+ * ceil(T * Hq / Hkv / 32) row tiles, B * nb_max * blk * Hkv * row tiles < 2^37. */
 sv_status sv_attend_kv4(const sv_shape* shape, const void* q, const sv_kv4* kv, const int32_t* sel,
                         int n_sel, int sel_stride, const void* draft_k, const void* draft_v,
                         const int32_t* draft_parent, void* out, void* workspace, size_t ws_bytes,

@@ -12,8 +12,8 @@ namespace kv4 {
 
 // ---------------------------------------------------------------- formats
 // E2M1 codes of the four bytes of a word (low bits first) as pairs of halves, exact. The
-// word is taken apart by a move: with shifts and masks a conversion cost 6 issue
-// slots instead of 2 to 3 (and a converter is half a slot wide).
+// word is taken apart by a move, which leaves one instruction a byte: with shifts and
+// masks it was three, all for the same half-rate pipe.
 __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t* r) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "mov.b32 {a, b, c, d}, %4;\n\t"
@@ -24,13 +24,13 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t* r) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
       : "r"(w));
 }
-// ... of bytes 0 and 2 alone.
-__device__ __forceinline__ void e2m1x4_to_f16(uint32_t w, uint32_t& r0, uint32_t& r2) {
+// ... of bytes 1 and 3 alone.
+__device__ __forceinline__ void e2m1x4_to_f16(uint32_t w, uint32_t& r1, uint32_t& r3) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "mov.b32 {a, b, c, d}, %2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, c;\n\t}"
-      : "=r"(r0), "=r"(r2)
+      "cvt.rn.f16x2.e2m1x2 %0, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, d;\n\t}"
+      : "=r"(r1), "=r"(r3)
       : "r"(w));
 }
 __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
@@ -80,17 +80,18 @@ __device__ __forceinline__ int head_exp(const int32_t* e, int h) {
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((127 + e) << 23); }
 
 // ---------------------------------------------------------------- work split
-__device__ __forceinline__ int ctx_of(const Attend4Args& a, int b) {
-  return min(max(a.seq_ctx[b], 0), a.nb_max * a.blk);
-}
+// One division for all of a kernel: an int division is some thirty instructions, and
+// what runs once costs the fetch of its code (about 12 cycles an instruction).
+static __device__ __noinline__ int quotient(int x, int y) { return x / y; }
+
 __device__ __forceinline__ int pieces_of(const Attend4Args& a, int ctx) {
-  const int full = ctx / a.blk, rest = ctx - full * a.blk;
+  const int full = quotient(ctx, a.blk), rest = ctx - full * a.blk;
   return (a.sel ? a.n_sel : full) * a.ppb + (rest + kPiece - 1) / kPiece;
 }
 
-// Prefix sums of the key tiles (one warp): cu[0 .. B]. Returns whether a length was
-// clamped, in any lane that saw one.
-__device__ __forceinline__ bool scan_tiles(const Attend4Args& a, int* cu) {
+// Prefix sums of the key tiles (one warp): cu[0 .. B], and the contexts. Returns whether
+// a length was clamped, in any lane that saw one.
+__device__ __forceinline__ bool scan_tiles(const Attend4Args& a, int* cu, int* ctx) {
   const int lane = threadIdx.x & 31;
   int carry = 0;
   bool bad = false;
@@ -99,9 +100,10 @@ __device__ __forceinline__ bool scan_tiles(const Attend4Args& a, int* cu) {
     const int b = b0 + lane;
     int x = 0;
     if (b < a.B) {
-      const int c = ctx_of(a, b);
-      bad |= c != a.seq_ctx[b];
-      x = (pieces_of(a, c) + a.ppt - 1) / a.ppt;
+      const int c = a.seq_ctx[b], n = min(max(c, 0), a.nb_max * a.blk);
+      bad |= c != n;
+      ctx[b] = n;
+      x = (pieces_of(a, n) + a.ppt - 1) >> a.ppt_shift;
     }
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -114,33 +116,37 @@ __device__ __forceinline__ bool scan_tiles(const Attend4Args& a, int* cu) {
   return bad;
 }
 
-// The line of all key tiles and the CTAs that share it.
+// The line of all key tiles and the CTAs that share it: the first `more` have one tile
+// more than the others, none has none.
 struct Line {
-  long long total;
-  int ctas;
-  __device__ __forceinline__ long long first(int c) const { return c * total / ctas; }
+  int ctas, each, more;
+  __device__ __forceinline__ int first(int c) const { return c * each + min(c, more); }
   // the CTA that has tile x
-  __device__ __forceinline__ int cta_of(long long x) const { return (int)(((x + 1) * ctas - 1) / total); }
+  __device__ __forceinline__ int cta_of(int x) const {
+    const int big = more * (each + 1);
+    return x < big ? quotient(x, each + 1) : more + quotient(x - big, each);
+  }
 };
 __device__ __forceinline__ Line line_of(const Attend4Args& a, int tiles) {
+  const int total = tiles * a.Hkv * a.row_tiles;  // (below 2^31: the call's limits)
   Line l;
-  l.total = (long long)tiles * a.Hkv * a.row_tiles;
-  l.ctas = (int)min((long long)a.ctas, l.total);  // every CTA has a tile
+  l.ctas = min(a.ctas, total);
+  l.each = l.ctas ? quotient(total, l.ctas) : 0;
+  l.more = total - l.each * l.ctas;
   return l;
 }
 
 struct Segment {
   int b, h, rt;      // the pair
   int tile0, tiles;  // its key tiles
-  int ctx, pieces;
-  long long slot;
+  int ctx, full, pieces;  // tokens, full blocks, pieces of the (sequence, head)
+  int slot;
 };
-// The segment that begins at position x of the line (x < end, the CTA's share's end).
-__device__ __forceinline__ Segment segment_at(const Attend4Args& a, const int* cu, long long x,
-                                              long long end, int cta) {
+// The segment that begins at position x of the line (x < end, the end of the CTA's share).
+__device__ __forceinline__ Segment segment_at(const Attend4Args& a, const int* cu, const int* ctx, int x, int end,
+                                              int cta) {
   Segment s;
-  const int per = a.Hkv * a.row_tiles;
-  const int y = (int)(x / per);
+  const int per = a.Hkv * a.row_tiles, y = quotient(x, per);
   int lo = 0, hi = a.B;  // the last b with cu[b] <= y; the sequences without keys before it do not count
   while (hi - lo > 1) {
     const int m = (lo + hi) >> 1;
@@ -148,16 +154,15 @@ __device__ __forceinline__ Segment segment_at(const Attend4Args& a, const int* c
     else hi = m;
   }
   s.b = lo;
-  const int n = cu[lo + 1] - cu[lo];
-  const long long in = x - (long long)cu[lo] * per;
-  const int pair = (int)(in / n);
-  s.tile0 = (int)(in - (long long)pair * n);
-  s.h = pair / a.row_tiles;
+  const int n = cu[lo + 1] - cu[lo], in = x - cu[lo] * per, pair = quotient(in, n);
+  s.tile0 = in - pair * n;
+  s.h = a.row_tiles == 1 ? pair : quotient(pair, a.row_tiles);
   s.rt = pair - s.h * a.row_tiles;
-  s.tiles = (int)min((long long)(n - s.tile0), end - x);
-  s.ctx = ctx_of(a, lo);
-  s.pieces = pieces_of(a, s.ctx);
-  s.slot = (long long)lo * per + pair + cta;
+  s.tiles = min(n - s.tile0, end - x);
+  s.ctx = ctx[lo];
+  s.full = quotient(s.ctx, a.blk);
+  s.pieces = (a.sel ? a.n_sel : s.full) * a.ppb + (s.ctx - s.full * a.blk + kPiece - 1) / kPiece;
+  s.slot = lo * per + pair + cta;
   return s;
 }
 
@@ -167,17 +172,16 @@ __device__ __forceinline__ long long piece_at(const Attend4Args& a, const Segmen
                                               unsigned* flags) {
   *valid = 0;
   if (i >= s.pieces) return -1;
-  const int full = s.ctx / a.blk, slots = a.sel ? a.n_sel : full;
-  const int at = i / a.ppb;
+  const int slots = a.sel ? a.n_sel : s.full, at = quotient(i, a.ppb);
   int block = at, sub = i - at * a.ppb;
   if (at >= slots) {  // the partial last block
-    block = full;
+    block = s.full;
     sub = i - slots * a.ppb;
-    *valid = min(kPiece, s.ctx - full * a.blk - sub * kPiece);
+    *valid = min(kPiece, s.ctx - s.full * a.blk - sub * kPiece);
   } else {
     if (a.sel) {
       block = a.sel[((long long)s.b * a.Hkv + s.h) * a.sel_stride + at];
-      if (block < 0 || block >= full) {
+      if (block < 0 || block >= s.full) {
         if (block != -1) *flags |= SV_FLAG_BAD_BLOCK_INDEX;
         return -1;
       }
@@ -195,7 +199,7 @@ __device__ __forceinline__ long long piece_at(const Attend4Args& a, const Segmen
 
 // Row r of a (sequence, head): draft t, query head h * G + g, r = t * G + g.
 __device__ __forceinline__ long long row_at(const Attend4Args& a, int b, int h, int r) {
-  const int t = r / a.G;
+  const int t = quotient(r, a.G);
   return ((long long)b * a.T + t) * a.Hq + h * a.G + (r - t * a.G);
 }
 

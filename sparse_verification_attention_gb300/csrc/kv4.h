@@ -75,7 +75,7 @@ constexpr int kMaxTc4Ctas = 160;
 // key tiles of `ppt` pieces. The pairs' key tiles are laid end to end and cut into
 // equal shares, one per CTA; what a CTA has of a pair is a segment. Segment
 // (pair p, CTA c) leaves its rows' sums in slot p + c (p and c only grow along the
-// line, so no two segments share one).
+// line, so no two segments share one), once for each of its `streams`.
 struct Attend4Args {
   const void *q, *draft_k, *draft_v;
   void* out;
@@ -86,11 +86,12 @@ struct Attend4Args {
   const int32_t *k_exp, *v_exp;  // [Hkv] or null
   unsigned* status;
   int* cu;        // workspace [B + 1]: key tiles of one pair, summed over the sequences before
-  float2* part_ml;  // [slots, rows]: reference (log2 domain) and sum
-  float* part_o;    // [slots, rows, d], in units of 2^v_exp
+  float2* part_ml;  // [slots, streams, rows]: reference (log2 domain) and sum
+  float* part_o;    // [slots, streams, rows, d], in units of 2^v_exp
   int B, T, Hq, Hkv, G, d, blk, nb_max, num_pages, n_sel, sel_stride;
   int rows, row_tiles;  // rows of a row tile (of all but the last), row tiles of a (b, h)
-  int ppb, ppt;   // pieces of a block and of a key tile
+  int streams;    // 2: a segment's even and odd tiles are summed apart
+  int ppb, ppt, ppt_shift;  // pieces of a block and of a key tile (a power of two)
   int ctas;
   float scale_log2;  // log2(e) / sqrt(d)
   unsigned long long anc[kMaxT];

@@ -131,7 +131,9 @@ Layout4 layout4(const sv_shape& s) {
   const int most[2] = {kSimt4Rows, kTc4Rows}, ctas[2] = {kMaxSimt4Ctas, kMaxTc4Ctas};
   for (int i = 0; i < 2; ++i) {
     const long long tiles = (stacked + most[i] - 1) / most[i], r = std::min<long long>(most[i], stacked);
-    rows = std::max(rows, (size_t)((tiles * pairs + ctas[i]) * r));
+    // (up to 64 rows the tensor cores sum in two streams)
+    const int streams = i == 1 && r <= 64 ? 2 : 1;
+    rows = std::max(rows, (size_t)((tiles * pairs + ctas[i]) * streams * r));
   }
   Layout4 L;
   L.cu = kStatusBytes;
@@ -302,6 +304,10 @@ sv_status sv_attend_kv4(const sv_shape* shape, const void* q, const sv_kv4* kv, 
   if ((r = check_seqs4(shape, kv)) != SV_OK) return r;
   if ((long long)shape->B * (kv->nb_max + 1ll) * shape->blk >= kInt * 16)
     return fail(SV_ERR_UNSUPPORTED, "B=%d: the batch's tokens are too many", shape->B);
+  // the line of key tiles (64 tokens at least, 32 rows at least) is counted in 31 bits
+  const long long row_tiles = (shape->T * (shape->Hq / shape->Hkv) + kSimt4Rows - 1) / kSimt4Rows;
+  if (((long long)shape->B * (kv->nb_max + 1ll) * shape->blk >> 6) + shape->B >= kInt / (shape->Hkv * row_tiles))
+    return fail(SV_ERR_UNSUPPORTED, "B=%d, %d heads: the batch's tokens are too many", shape->B, shape->Hkv);
   if (sel && (n_sel < 0 || n_sel > sel_stride || n_sel > kv->nb_max))
     return fail(SV_ERR_INVALID_ARG, "n_sel=%d outside [0, sel_stride=%d] or beyond nb_max=%d", n_sel, sel_stride,
                 kv->nb_max);

@@ -77,21 +77,22 @@ __global__ void __launch_bounds__(kThreads) join4_kernel(const __grid_constant__
   const int start = a.cu[b], tiles = a.cu[b + 1] - start, per = a.Hkv * a.row_tiles;
   const int pair = h * a.row_tiles + rt;
   const Line line = line_of(a, a.cu[a.B]);
-  const long long first = (long long)start * per + (long long)pair * tiles;
+  const int first = start * per + pair * tiles;
   int c0 = 0, c1 = -1;
   if (tiles) {
     c0 = line.cta_of(first);
     c1 = line.cta_of(first + tiles - 1);
   }
-  const long long at0 = ((long long)b * per + pair + c0) * a.rows + r - rt * a.rows;
+  const long long at0 = ((long long)b * per + pair + c0) * a.streams * a.rows + r - rt * a.rows;
+  const int parts = (c1 - c0 + 1) * a.streams;
   // the largest reference, of the segments and of the drafts
   float m = fmaxf(s0, s1);
-  for (int c = lane; c <= c1 - c0; c += 32) m = fmaxf(m, a.part_ml[at0 + (long long)c * a.rows].x);
+  for (int c = lane; c < parts; c += 32) m = fmaxf(m, a.part_ml[at0 + (long long)c * a.rows].x);
   m = warp_max(m);
   const float p0 = lane < n ? exp2f(s0 - m) : 0.f, p1 = lane + 32 < n ? exp2f(s1 - m) : 0.f;
   float l = warp_sum(p0 + p1);
   const float unit = exp2i(head_exp(a.v_exp, h));
-  for (int c = 0; c <= c1 - c0; ++c) {
+  for (int c = 0; c < parts; ++c) {
     const long long at = at0 + (long long)c * a.rows;
     const float2 ml = __ldcg(a.part_ml + at);
     if (ml.x == -INFINITY && ml.y == 0.f) continue;  // no key of the segment counted

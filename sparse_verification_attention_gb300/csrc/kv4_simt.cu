@@ -14,11 +14,11 @@ using namespace kv4;
 
 constexpr int kThreads = 256;
 constexpr int kRows = kSimt4Rows;
-constexpr int kKeys = 64, kPieces = kKeys / kPiece;
+constexpr int kKeys = 64, kPieces = kKeys / kPiece;  // (ppt_shift)
 constexpr int kGroup = 16;
 
 struct Control {
-  int cu[kMaxB4 + 1];
+  int cu[kMaxB4 + 1], ctx[kMaxB4];
   long long piece[kPieces];
   int valid[kPieces];
   float m[kRows], l[kRows];
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) attend4_simt_kernel(const __grid_con
   pdl_wait();
   pdl_trigger();
   if (tid < 32) {
-    const bool bad = scan_tiles(a, sh.cu);
+    const bool bad = scan_tiles(a, sh.cu, sh.ctx);
     if (bad) flags |= SV_FLAG_BAD_LENGTH;
   }
   __syncthreads();
@@ -57,9 +57,9 @@ __global__ void __launch_bounds__(kThreads) attend4_simt_kernel(const __grid_con
     for (int b = tid; b <= a.B; b += kThreads) a.cu[b] = sh.cu[b];
   const Line line = line_of(a, sh.cu[a.B]);
   const int cta = blockIdx.x;
-  const long long end = cta < line.ctas ? line.first(cta + 1) : 0;
-  for (long long x = cta < line.ctas ? line.first(cta) : 0; x < end;) {
-    const Segment s = segment_at(a, sh.cu, x, end, cta);
+  const int end = cta < line.ctas ? line.first(cta + 1) : 0;
+  for (int x = cta < line.ctas ? line.first(cta) : 0; x < end;) {
+    const Segment s = segment_at(a, sh.cu, sh.ctx, x, end, cta);
     x += s.tiles;
     const int row0 = s.rt * a.rows, rows = min(a.rows, a.T * a.G - row0);
     const float scale = a.scale_log2 * exp2i(head_exp(a.k_exp, s.h));
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) attend4_simt_kernel(const __grid_con
     for (int i = 0; i < 2; ++i) {
       const int r = ty + 16 * i;
       if (r >= rows) continue;
-      const long long at = s.slot * a.rows + r;
+      const long long at = (long long)s.slot * a.rows + r;
       if (tx == 0) a.part_ml[at] = make_float2(m[i], l[i]);
 #pragma unroll
       for (int j = 0; j < D4; ++j)
@@ -217,6 +217,8 @@ cudaError_t launch_attend4_simt(Attend4Args a, int dtype, cudaStream_t st) {
   a.rows = std::min(kRows, a.T * a.G);
   a.row_tiles = (a.T * a.G + a.rows - 1) / a.rows;
   a.ppt = kPieces;
+  a.ppt_shift = 2;
+  a.streams = 1;
   return dtype == SV_BF16 ? launch_as<__nv_bfloat16>(a, st) : launch_as<float>(a, st);
 }
 

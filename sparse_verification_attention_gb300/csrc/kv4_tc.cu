@@ -13,14 +13,26 @@
 // scaled by a power of two per row so that its largest element lies in [2^14, 2^15),
 // exact as well; factor and exponents go into the softmax's scale.
 //
-// Warps: 0-3 K, 4-7 V (codes to halves), then the softmax (one warpgroup for up to
-// 32 rows, else two that share the columns), one that takes the CTA's segments off
-// the line, looks pages up, copies them and lays out Q, one that issues the MMAs.
+// Warpgroups: K and V (codes to halves), two of softmax, and one whose warps copy (take
+// the CTA's segments off the line, look pages up), issue the MMAs of the one and of the other
+// product, and lay out Q. (One warp for both products spent 1750 cycles a tile on its own
+// waits, issue and commits, 216 us; two: see below.)
+// What bounds the kernel besides HBM are chains, not rates: an MMA of 128 x N x 16 with A in
+// TMEM takes 65 cycles for any N up to 128 (measured; 47 with A in shared memory), so a tile's
+// 16 take 1040, and a tile's softmax from scores to weights as long again. Up to 64
+// rows the two softmax warpgroups therefore take even and odd tiles with references,
+// sums and O of their own (two streams, joined with the segments); above, they share
+// each tile's columns.
 // A softmax thread has one key and a run of rows (columns). It does not look for
-// a tile's maxima: a row's reference stands until some score exceeds it by 2^8, which
-// the warps find out with a vote at the tile's barrier; only then (and in a segment's first
-// tile) maxima are taken across lanes and O is rescaled. Weights are held 2^7 times
-// their size, so that f16's range covers 2^-31 .. 2^8 of the reference.
+// a tile's maxima: a row's reference stands until some key's weights, summed over the
+// thread's rows, reach 2^15, which the warps tell each other at the tile's barrier; only
+// then (and in a segment's first tile) maxima are taken across lanes and O is rescaled.
+// Weights are held 2^7 times their size, so that f16's range covers 2^-31 .. 2^8 of the
+// reference.
+//
+// Everything that runs once per segment is a rolled loop: five roles share an SM
+// quarter's instruction cache, and cold code costs more than what it does. With the
+// loops unrolled and every wait's clock inline, 128 K tokens x 4 took 497 us, rolled 247.
 #include <algorithm>
 #include <atomic>
 
@@ -35,51 +47,58 @@ namespace {
 using namespace kv4;
 
 constexpr int kKeys = 128, kPieces = kKeys / kPiece;
-constexpr int kInfo = 16;   // ring of tile infos: more than tiles in flight (stages, and two behind them)
-constexpr int kSegs = 8;    // ring of segment infos: more than the segments that Q and S run ahead
+// Rings. Copies run at most kMaxStages tiles ahead of V, V two ahead of its products, so the
+// infos of 11 tiles, and of as many segments, are in use at most. Q, with its factors, runs
+// at most two segments ahead of the scores and those two ahead of the weights.
+constexpr int kInfo = 16, kSegs = 16, kF = 8;
 constexpr int kMaxStages = 8;
+constexpr int kThreads = 640;
+constexpr int kSoftmaxWarp = 8, kLoadWarp = 16, kScoreWarp = 17, kOutWarp = 18;  // 19 lays out Q
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 128, kColK = 256, kColV = 384;  // K and V: two of 64 columns
 constexpr float kLift = 7.f;    // weights are 2^kLift times their size ...
-constexpr float kSlack = 8.f;   // ... and at most 2^kSlack above the reference's
+constexpr float kTop = 32768.f; // ... and below this, so that f16 (65504) holds them
+// References move when a key's weights sum up to more than kTop: one of at most 64 is
+// above 2^9 then, its score more than 2 (log2) above its reference. kSlack lies below
+// that, so that the move always ends the cause.
+constexpr float kSlack = 1.9f;
 
 // What the loading warp tells the others of a tile: tokens that count of each piece
-// (a byte each), and whether a segment begins or ends with it.
+// (a byte each), its place in the segment, and the segment.
 struct TileInfo {
   uint64_t valid;
-  uint32_t flags;
+  uint32_t flags, seg;
 };
-constexpr uint32_t kFirst = 1, kLast = 2;
+constexpr uint32_t kBegin = 1, kEnd = 2;          // the segment's first and last tile
+constexpr uint32_t kFirst = 4, kLast = 8;         // ... the stream's
+constexpr uint32_t kOnly = 16;                    // the other stream has none
 constexpr uint64_t kAllValid = 0x1010101010101010ull;
 
 struct SegInfo {
-  long long slot;
-  int rows;
+  int slot, rows;
 };
 
 struct Control {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t k_full[2], k_empty[2], v_full[2], s_full[2], s_empty[2], p_full[2], pv_done[2];
-  uint64_t q_full[2], q_empty[2], o_empty, drained, meet[2];
+  uint64_t s_ready[2], k_empty[2], s_full[2];  // K (and room for S) is there; S = K Q^T is done
+  uint64_t o_ready[2], pv_done[2], o_empty[2]; // V and P are there; O += V P is done; O has been read
+  uint64_t q_first, q_full[2], q_empty[2], drained[2], meet[2];
   uint32_t tmem;
   int abort;
-  uint32_t over[2][2];                   // by warpgroup and tile parity: 1 + the tile whose references move
+  uint32_t over[2][2];                    // by warpgroup and turn: 1 + the tile whose references move
   TileInfo info[kInfo];
   SegInfo seg[kSegs];
-  alignas(16) float f[kSegs][kTc4Rows];  // factor of a row's scores
-  alignas(16) float nm[kTc4Rows];        // minus (reference - kLift) of a row, log2 domain
-  float corr[kTc4Rows];
-  float mx[4][kTc4Rows];                 // by warp of a softmax warpgroup (also: sums)
-  int cu[kMaxB4 + 1];
+  alignas(16) float f[kF][kTc4Rows];   // factor of a row's scores
+  alignas(16) float nm[kTc4Rows];         // minus (reference - kLift) of a column, log2 domain
+  alignas(16) float corr[kTc4Rows];
+  float mx[4][kTc4Rows];                  // by warp of a softmax warpgroup (also: sums)
+  int cu[kMaxB4 + 1], ctx[kMaxB4];
 };
 
 template <int N>
 struct Cfg {
-  static constexpr int kGroups = N <= 32 ? 1 : 2;    // softmax warpgroups
-  static constexpr int kCols = N / kGroups;          // rows (columns) of a warpgroup
-  static constexpr int kThreads = 256 + 128 * kGroups + 64;
-  static constexpr int kLoadWarp = 8 + 4 * kGroups, kMmaWarp = kLoadWarp + 1;
-  static constexpr int kS = N <= 64 ? 2 : 1;         // S buffers
+  static constexpr bool kAlt = N <= 64;              // even and odd tiles apart
+  static constexpr int kCols = kAlt ? N : N / 2;     // rows (columns) of a softmax warpgroup
   static constexpr int kQ = N <= 64 ? 2 : 1;         // Q buffers
   static constexpr int kQBytes = 2 * N * 128;        // two blocks of 64 dims
   static constexpr int kPBytes = (N > 64 ? 2 : 1) * kKeys * 128;
@@ -93,6 +112,16 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+// r[0 .. 8) times half H of s (the multiplication picks the half itself).
+template <int H>
+__device__ __forceinline__ void scale_f16x2(uint32_t* r, uint32_t s) {
+  const __half2 ss = *reinterpret_cast<const __half2*>(&s), f = H ? __high2half2(ss) : __low2half2(ss);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&r[e]), f);
+    r[e] = *reinterpret_cast<const uint32_t*>(&x);
+  }
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -117,6 +146,13 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
   return r;
 }
+// Bytes at .. at + 3 of a row whose last index is `last`.
+__device__ __forceinline__ uint32_t lds8x4(uint32_t row, int at, int last) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r |= lds8(row + min(at + j, last)) << (8 * j);
+  return r;
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
@@ -139,17 +175,84 @@ __device__ __forceinline__ float redux_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
-// The rest of a wait, out of line: four roles' loops share an SM quarter's instruction
-// cache, and with every wait's clock and limit inline (and the loops unrolled) they did
-// not fit. 128 K tokens x 4 took 495 us, most of it waiting for instructions.
+// 32 lanes x 8 (N) columns of TMEM.
+__device__ __forceinline__ void ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t* r) {
+  if constexpr (N == 16) {
+    tc::ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(r));
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; c += 32) tc::ld32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(r + c));
+  }
+}
+
+// The rest of a wait, out of line (a wait's clock and limit inline would fill the
+// instruction cache).
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* status,
                                      unsigned site) {
-  return mbar_wait_abortable(bar, parity, abort, status, site);
+  return __all_sync(0xffffffffu, mbar_wait_abortable(bar, parity, abort, status, site));
+}
+
+__device__ __noinline__ Segment next_segment(const Attend4Args& a, const Control& sh, int x, int end) {
+  return segment_at(a, sh.cu, sh.ctx, x, end, blockIdx.x);
+}
+
+// Q of a segment into shared memory as halves, K-major with the 128-byte swizzle, and the
+// factors of its rows' scores: warp `part` of `parts`, a row by 16 lanes, 8 dims each.
+__device__ __noinline__ void lay_out_q(const Attend4Args& a, const Segment& s, int n, uint32_t to, float* f, int part,
+                                       int parts) {
+  const int lane = threadIdx.x & 31, c = lane & 15;
+  const int row0 = s.rt * a.rows, rows = min(a.rows, a.T * a.G - row0);
+  const float scale = a.scale_log2 * exp2i(head_exp(a.k_exp, s.h));
+  constexpr int kFlight = 4;
+#pragma unroll 1
+  for (int r0 = part * 2 + (lane >> 4); r0 - (lane >> 4) < n; r0 += 2 * parts * kFlight) {
+    uint4 w[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int r = r0 + 2 * parts * u;
+      w[u] = make_uint4(0, 0, 0, 0);
+      if (r < rows && 8 * c < a.d)
+        w[u] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                     row_at(a, s.b, s.h, row0 + r) * a.d) + c);
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int r = r0 + 2 * parts * u;
+      // the largest element's bits (of positive floats they compare as integers; a NaN's are
+      // the largest and leave the row as it is)
+      const uint32_t two[4] = {w[u].x & 0x7fff7fffu, w[u].y & 0x7fff7fffu, w[u].z & 0x7fff7fffu, w[u].w & 0x7fff7fffu};
+      const uint32_t m01 = __vmaxu2(two[0], two[1]), m23 = __vmaxu2(two[2], two[3]), m4 = __vmaxu2(m01, m23);
+      uint32_t top = max(m4 & 0xffffu, m4 >> 16);
+#pragma unroll
+      for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // the power of two that takes it into [2^14, 2^15)
+      const int e = (int)(top >> 7), up = e == 0 || e == 255 ? 0 : min(100, 127 + 14 - e);
+      const float k = exp2i(up);
+      const uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        h[i] = pack_f16(__uint_as_float(ww[i] << 16) * k, __uint_as_float(ww[i] & 0xffff0000u) * k);
+      if (r < n) {
+        sts128(to + (c >> 3) * (n * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+        if (c == 0) f[r] = scale * exp2i(-up);
+      }
+    }
+  }
+  fence_proxy_async_shared();
+  __syncwarp();
 }
 
 // DG: groups of 16 dims (8: d = 128), 0: any number up to 8.
 template <int N, int DG>
-__global__ void __launch_bounds__(Cfg<N>::kThreads, 1) attend4_tc_kernel(const __grid_constant__ Attend4Args a, int stages) {
+__global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_constant__ Attend4Args a, int stages) {
   using C = Cfg<N>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -160,38 +263,41 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) attend4_tc_kernel(const _
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int groups = DG ? DG : a.d / 16;
   const uint32_t pb = (uint32_t)piece_bytes(groups * 16), side = kPieces * pb, stage_bytes = 2 * side;
+  constexpr uint32_t kSharers = C::kAlt ? 4 : 8;  // softmax warps of a tile
 
-  if (warp == C::kMmaWarp) tc::alloc(smem_u32(&sh.tmem), kTmemCols);
+  if (warp == kScoreWarp) {
+    tc::alloc(smem_u32(&sh.tmem), kTmemCols);
+    tc::relinquish();
+  }
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(smem_u32(&sh.full[i]), 1);
       mbar_init(smem_u32(&sh.empty[i]), 8);
     }
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sh.k_full[i]), 4);
+      mbar_init(smem_u32(&sh.s_ready[i]), 4 + kSharers);
       mbar_init(smem_u32(&sh.k_empty[i]), 1);
-      mbar_init(smem_u32(&sh.v_full[i]), 4);
       mbar_init(smem_u32(&sh.s_full[i]), 1);
-      mbar_init(smem_u32(&sh.s_empty[i]), 4 * C::kGroups);
-      mbar_init(smem_u32(&sh.p_full[i]), 4 * C::kGroups);
+      mbar_init(smem_u32(&sh.o_ready[i]), 4 + kSharers);
       mbar_init(smem_u32(&sh.pv_done[i]), 1);
+      mbar_init(smem_u32(&sh.o_empty[i]), kSharers);
       mbar_init(smem_u32(&sh.q_full[i]), 1);
+      mbar_init(smem_u32(&sh.drained[i]), 1);
       mbar_init(smem_u32(&sh.q_empty[i]), 1);
-    }
-    mbar_init(smem_u32(&sh.o_empty), 4 * C::kGroups);
-    mbar_init(smem_u32(&sh.drained), 1);
-    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.meet[i]), 4);
       sh.over[i][0] = sh.over[i][1] = 0;
     }
+    mbar_init(smem_u32(&sh.q_first), 8);
     sh.abort = 0;
     fence_barrier_init();
   }
   pdl_wait();
   pdl_trigger();
   bool bad = false;
-  if (warp == C::kLoadWarp) {
-    bad = scan_tiles(a, sh.cu);
+  if (warp == kLoadWarp) {
+    bad = scan_tiles(a, sh.cu, sh.ctx);
     __syncwarp();
   }
   tc::fence_before();
@@ -199,14 +305,19 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) attend4_tc_kernel(const _
   tc::fence_after();
   const uint32_t tmem = sh.tmem;
   if (blockIdx.x == 0)
-    for (int b = tid; b <= a.B; b += C::kThreads) a.cu[b] = sh.cu[b];
+    for (int b = tid; b <= a.B; b += kThreads) a.cu[b] = sh.cu[b];
   const Line line = line_of(a, sh.cu[a.B]);
-  const int cta = blockIdx.x;
-  const long long begin = cta < line.ctas ? line.first(cta) : 0, end = cta < line.ctas ? line.first(cta + 1) : 0;
+  const bool idle = (int)blockIdx.x >= line.ctas;
+  const int begin = idle ? 0 : line.first(blockIdx.x), end = idle ? 0 : line.first(blockIdx.x + 1);
   const uint32_t tiles = (uint32_t)(end - begin);
   auto wait = [&](uint64_t& bar, uint32_t parity, unsigned site) {
     const uint32_t addr = smem_u32(&bar);
-    return mbar_try_wait(addr, parity & 1u) || wait_on(addr, parity & 1u, &sh.abort, a.status, site);
+    return __all_sync(0xffffffffu, mbar_try_wait(addr, parity & 1u)) ||
+           wait_on(addr, parity & 1u, &sh.abort, a.status, site);
+  };
+  auto arrive = [&](uint64_t& bar) {  // once for the warp
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bar));
   };
 
   if (warp < 4) {
@@ -217,36 +328,35 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) attend4_tc_kernel(const _
       if (!wait(sh.full[st], ph, 1u)) break;
       if (!wait(sh.k_empty[i & 1], (i >> 1) ^ 1u, 2u)) break;
       tc::fence_after();
-      const uint32_t codes = ring + st * stage_bytes + piece * pb, scales = codes + groups * 128 + tok * groups;
+      const uint32_t at = ring + st * stage_bytes + piece * pb;
+      const uint32_t codes = at + tok * 8, scales = at + groups * 128 + tok * groups;
       const uint32_t to = tmem + tlane + kColK + (i & 1) * 64;
 #pragma unroll 1
-      for (int g = 0; g < groups; g += 2) {
-        uint32_t r[16];
+      for (int g = 0; g < groups; g += 4) {  // (behind the last group: columns that no product reads)
+        uint32_t r[32];
+        uint2 w[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (!DG && g + j >= groups) {  // the second half of the last pair
+        for (int j = 0; j < 4; ++j) w[j] = lds64(codes + (DG ? g + j : min(g + j, groups - 1)) * 128);
+        uint32_t s01, s23;
+        e4m3x4_to_f16(DG ? lds32(scales + g) : lds8x4(scales, g, groups - 1), s01, s23);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[8 * j + e] = 0;
-            continue;
-          }
-          const uint32_t two = __byte_perm(e4m3x2_to_f16x2(lds8(scales + g + j)), 0, 0x1010);
-          const uint2 w = lds64(codes + (g + j) * 128 + tok * 8);
-          e2m1x8_to_f16(w.x, r + 8 * j);
-          e2m1x8_to_f16(w.y, r + 8 * j + 4);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) r[8 * j + e] = mul_f16x2(r[8 * j + e], two);
+        for (int j = 0; j < 4; ++j) {
+          e2m1x8_to_f16(w[j].x, r + 8 * j);
+          e2m1x8_to_f16(w[j].y, r + 8 * j + 4);
         }
-        tc::st16(to + g * 8, r);
+        scale_f16x2<0>(r, s01);
+        scale_f16x2<1>(r + 8, s01);
+        scale_f16x2<0>(r + 16, s23);
+        scale_f16x2<1>(r + 24, s23);
+        tc::st32(to + g * 8, r);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.empty[st]));
+      arrive(sh.empty[st]);
       tc::wait_st();
       tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.k_full[i & 1]));
+      arrive(sh.s_ready[i & 1]);
       if (++st == (uint32_t)stages) st = 0, ph ^= 1u;
     }
-  } else if (warp < 8) {
+  } else if (warp < kSoftmaxWarp) {
     // ------------------------------------------------------------ V: lane = dim
     const int w = warp - 4;
     const uint32_t t4 = lane & 3;  // code row lane / 4 (that dim and the one 8 behind), tokens 4 t4 ..
@@ -268,399 +378,387 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1) attend4_tc_kernel(const _
         __syncwarp();
       }
 #pragma unroll 1
-      for (int q = 0; q < 4; ++q) {  // group q / 2 of the warp's two, half q % 2 of the keys
-        const int g = 2 * w + (q >> 1);
+      for (int q = 0; q < 2; ++q) {  // the warp's two groups
+        const int g = 2 * w + q;
         if (!DG && g >= groups) break;
-        const uint32_t code = from + (q & 1) * 4 * pb + g * 128 + lane * 4;
-        const uint32_t scale = from + (q & 1) * 4 * pb + groups * 128 + g * 16 + t4 * 4;
-        uint32_t r[16];
+        const uint32_t code = from + g * 128 + lane * 4, scale = from + groups * 128 + g * 16 + t4 * 4;
+        uint32_t c[8], sc[8], r[2][16];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const uint32_t c = lds32(code + p * pb), s = lds32(scale + p * pb), c4 = c >> 4, c8 = c >> 8;
-          const uint32_t lo = (c & 0x000f000fu) | (c4 & 0xfff0fff0u);   // bytes 0, 2: tokens (0, 1), (2, 3)
-          const uint32_t hi = (c4 & 0x000f000fu) | (c8 & 0xfff0fff0u);  // ... of the dim 8 behind
-          uint32_t s01, s23;
-          e4m3x4_to_f16(s, s01, s23);
-          e2m1x4_to_f16(lo, r[4 * p], r[4 * p + 1]);
-          e2m1x4_to_f16(hi, r[4 * p + 2], r[4 * p + 3]);
-          r[4 * p] = mul_f16x2(r[4 * p], s01);
-          r[4 * p + 1] = mul_f16x2(r[4 * p + 1], s23);
-          r[4 * p + 2] = mul_f16x2(r[4 * p + 2], s01);
-          r[4 * p + 3] = mul_f16x2(r[4 * p + 3], s23);
+        for (int p = 0; p < 8; ++p) {
+          c[p] = lds32(code + p * pb);
+          sc[p] = lds32(scale + p * pb);
         }
-        st_16x256b_x4(tmem + ((uint32_t)(w * 32 + (q >> 1) * 16) << 16) + kColV + (i & 1) * 64 + (q & 1) * 32, r);
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const uint32_t c4 = c[p] << 4, c8 = c[p] << 8;
+          // bytes 1 and 3: tokens (0, 1) and (2, 3) of the one dim, and of the other
+          const uint32_t lo = (c8 & 0x0f000f00u) | (c4 & 0xf0fff0ffu), hi = (c4 & 0x0f000f00u) | (c[p] & 0xf0fff0ffu);
+          uint32_t s01, s23, *to = r[p >> 2] + 4 * (p & 3);
+          e4m3x4_to_f16(sc[p], s01, s23);
+          e2m1x4_to_f16(lo, to[0], to[1]);
+          e2m1x4_to_f16(hi, to[2], to[3]);
+          to[0] = mul_f16x2(to[0], s01);
+          to[1] = mul_f16x2(to[1], s23);
+          to[2] = mul_f16x2(to[2], s01);
+          to[3] = mul_f16x2(to[3], s23);
+        }
+        const uint32_t at = tmem + ((uint32_t)(w * 32 + q * 16) << 16) + kColV + (i & 1) * 64;
+        st_16x256b_x4(at, r[0]);
+        st_16x256b_x4(at + 32, r[1]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.empty[st]));
+      arrive(sh.empty[st]);
       tc::wait_st();
       tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.v_full[i & 1]));
+      arrive(sh.o_ready[i & 1]);
       if (++st == (uint32_t)stages) st = 0, ph ^= 1u;
     }
-  } else if (warp < C::kLoadWarp) {
+  } else if (warp < kLoadWarp) {
     // ------------------------------------------------------------ softmax: lane = key
-    constexpr int CH = C::kCols <= 32 ? C::kCols : 16;  // columns in registers at a time
-    constexpr int NCH = C::kCols / CH;
-    const int wg = (warp - 8) >> 2, quad = warp & 3, col0 = wg * C::kCols;
+    // columns in registers at a time: all of up to 32; of 64 (with their 64 sums) 16, and
+    // the scores are read from TMEM a second time
+    constexpr int NC = C::kCols, CH = NC <= 32 ? NC : 16, NCH = NC / CH;
+    const int wg = (warp - kSoftmaxWarp) >> 2, quad = warp & 3, in_wg = (warp - kSoftmaxWarp) & 3;
+    // columns of S and of P, and of O, references and sums
+    const int col0 = C::kAlt ? 0 : wg * NC, own0 = wg * NC;
     const int key = quad * 32 + lane;
-    const uint32_t tlane = (uint32_t)(quad * 32) << 16;
-    float l[C::kCols];
-    bool first = true;  // no key of the segment has counted yet
-    uint32_t seg = 0, met = 0;
-    bool ok = true;
+    const uint32_t tlane = (uint32_t)(quad * 32) << 16, tmem_o = tmem + tlane + kColO + own0;
+    if (!idle) {  // the first segment's Q, which everybody else waits for (later ones: one warp, ahead)
+      const Segment s = next_segment(a, sh, begin, end);
+      lay_out_q(a, s, N, q_base, sh.f[0], warp - kSoftmaxWarp, 8);
+      arrive(sh.q_first);
+    }
+    arrive(sh.s_ready[C::kAlt ? wg : 0]);  // S is free
+    uint64_t l[NC / 2];  // sums of two columns each
+    bool first = true;   // no key of the stream has counted yet
+    uint32_t met = 0;
     // the warpgroup's four warps wait for each other (no named barrier: that wait has no limit)
     auto meet = [&] {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.meet[wg]));
+      arrive(sh.meet[wg]);
       return wait(sh.meet[wg], met++, 17u);
     };
-    for (uint32_t i = 0; i < tiles; ++i) {
-      const uint32_t sb = i % C::kS;
-      if (!(ok = wait(sh.s_full[sb], i / C::kS, 5u))) break;
+    for (uint32_t i = C::kAlt ? wg : 0; i < tiles; i += C::kAlt ? 2 : 1) {
+      const uint32_t sb = C::kAlt ? wg : 0;  // S buffer, used every (or every other) tile
+      const uint32_t turn = C::kAlt ? i >> 1 : i;
+      if (!wait(sh.s_full[sb], turn, 5u)) break;
       tc::fence_after();
       const TileInfo info = sh.info[i % kInfo];
-      const uint32_t flags = info.flags;
-      const float* f = sh.f[seg % kSegs] + col0;
-      if (flags & kFirst) {
+      const float* f = sh.f[info.seg % kF] + col0;
+      if (info.flags & kFirst) {
         first = true;
 #pragma unroll
-        for (int c = 0; c < C::kCols; ++c) l[c] = 0.f;
+        for (int c = 0; c < NC / 2; ++c) l[c] = 0;
       }
       const bool counts = key % kPiece < (int)(info.valid >> (8 * (key / kPiece)) & 0xff);
       const bool any = info.valid != 0;  // a key of the tile counts
       uint32_t s[CH];
       auto load = [&](int ch) {
-        const uint32_t at = tmem + tlane + kColS + sb * 64 + col0 + ch * CH;
-        if constexpr (CH == 32) tc::ld32(at, s);
-        else if constexpr (CH == 16) tc::ld16(at, s);
-        else {
-          asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                       : "=r"(s[0]), "=r"(s[1]), "=r"(s[2]), "=r"(s[3]), "=r"(s[4]), "=r"(s[5]), "=r"(s[6]), "=r"(s[7])
-                       : "r"(at)
-                       : "memory");
-        }
+        ld_cols<CH>(tmem + tlane + kColS + sb * 64 + col0 + ch * CH, s);
         tc::wait_ld();
-        if (!counts) {
-#pragma unroll
-          for (int c = 0; c < CH; ++c) s[c] = 0xff800000u;
-        }
       };
-      // x = s f - (m - kLift), in place
-      auto relative = [&](int ch) {
+      // weights in place of the scores of a run of columns, and their sum: it tells whether
+      // a reference has to move
+      auto weigh = [&](int ch) {
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int c = 0; c < CH; c += 4) {
-          const float4 ff = *reinterpret_cast<const float4*>(f + ch * CH + c);
-          const float4 nn = *reinterpret_cast<const float4*>(sh.nm + col0 + ch * CH + c);
-          s[c] = __float_as_uint(__fmaf_rn(__uint_as_float(s[c]), ff.x, nn.x));
-          s[c + 1] = __float_as_uint(__fmaf_rn(__uint_as_float(s[c + 1]), ff.y, nn.y));
-          s[c + 2] = __float_as_uint(__fmaf_rn(__uint_as_float(s[c + 2]), ff.z, nn.z));
-          s[c + 3] = __float_as_uint(__fmaf_rn(__uint_as_float(s[c + 3]), ff.w, nn.w));
+          const ulonglong2 ff = *reinterpret_cast<const ulonglong2*>(f + ch * CH + c);
+          const ulonglong2 nn = *reinterpret_cast<const ulonglong2*>(sh.nm + own0 + ch * CH + c);
+          const float2 x = unpack2(fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), ff.x, nn.x));
+          const float2 y = unpack2(fma2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), ff.y, nn.y));
+          const float e[4] = {ex2(x.x), ex2(x.y), ex2(y.x), ex2(y.y)};
+          sum[0] = add2(sum[0], pack2(e[0], e[1]));
+          sum[1] = add2(sum[1], pack2(e[2], e[3]));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[c + k] = __float_as_uint(e[k]);
         }
+        const float2 t = unpack2(add2(sum[0], sum[1]));
+        return t.x + t.y;
       };
-      bool over = first && any;
-      if (!over) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-          load(ch);
-          relative(ch);
-#pragma unroll
-          for (int c = 0; c < CH; ++c) top = fmaxf(top, __uint_as_float(s[c]));
-        }
-        if (__any_sync(0xffffffffu, !first && counts && top > kLift + kSlack) && lane == 0) sh.over[wg][i & 1] = i + 1;
-        if (!(ok = meet())) break;
-        over = *(volatile uint32_t*)&sh.over[wg][i & 1] == i + 1;
-      }
-      if (over) {
-        // the references move: maxima over the tile's keys, then O and the sums follow
+      // References move when the stream begins and when the vote says so: maxima over the
+      // tile's keys, then O and the sums follow.
+      bool ok = true;
 #pragma unroll 1
+      for (bool over = first && any;; over = true) {
+        if (over) {
+#pragma unroll 1
+          for (int c = 0; c < NC; c += 8) {
+            uint32_t x[8];
+            ld8(tmem + tlane + kColS + sb * 64 + col0 + c, x);
+            tc::wait_ld();
+            float m[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m[e] = redux_max(counts ? __uint_as_float(x[e]) * f[c + e] : -INFINITY);
+            if (lane == 0) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) sh.mx[in_wg][own0 + c + e] = m[e];
+            }
+          }
+          if (!(ok = meet())) break;
+          const int c = in_wg * 32 + lane;
+          if (c < NC) {
+            const int col = own0 + c;
+            const float top = fmaxf(fmaxf(sh.mx[0][col], sh.mx[1][col]), fmaxf(sh.mx[2][col], sh.mx[3][col]));
+            const float old = kLift - sh.nm[col];
+            const bool up = first || top > old + kSlack;
+            sh.corr[col] = up && !first ? ex2(old - top) : 1.f;
+            if (up) sh.nm[col] = kLift - top;
+          }
+          if (!(ok = meet())) break;
+          if (!first) {
+            // every product into O is complete
+            if (!(ok = C::kAlt ? wait(sh.pv_done[sb], turn ^ 1u, 6u) : wait(sh.pv_done[(i - 1) & 1], (i - 1) >> 1, 6u)))
+              break;
+            tc::fence_after();
+#pragma unroll
+            for (int c0 = 0; c0 < NC; c0 += 8) {
+              uint32_t o[8];
+              ld8(tmem_o + c0, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int c = 0; c < 8; c += 2) {
+                const float2 k = *reinterpret_cast<const float2*>(sh.corr + own0 + c0 + c), sums = unpack2(l[(c0 + c) / 2]);
+                o[c] = __float_as_uint(__uint_as_float(o[c]) * k.x);
+                o[c + 1] = __float_as_uint(__uint_as_float(o[c + 1]) * k.y);
+                l[(c0 + c) / 2] = pack2(sums.x * k.x, sums.y * k.y);
+              }
+              tc::st8(tmem_o + c0, o);
+            }
+            tc::wait_st();
+          }
+          first = false;
+        }
+        float top = 0.f;
+#pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
           load(ch);
-#pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            const float m = redux_max(counts ? __uint_as_float(s[c]) * f[ch * CH + c] : -INFINITY);
-            if (lane == 0) sh.mx[quad][col0 + ch * CH + c] = m;
-          }
+          top += weigh(ch);
         }
-        if (!(ok = meet())) break;
-        const int c = (warp - 8 - 4 * wg) * 32 + lane;
-        if (c < C::kCols) {
-          const int col = col0 + c;
-          const float top = fmaxf(fmaxf(sh.mx[0][col], sh.mx[1][col]), fmaxf(sh.mx[2][col], sh.mx[3][col]));
-          const float old = kLift - sh.nm[col];
-          const bool move = first || top > old + kSlack;
-          sh.corr[col] = move && !first ? ex2(old - top) : 1.f;
-          if (move) sh.nm[col] = kLift - top;
-        }
-        if (!(ok = meet())) break;
-        if (!first) {
-          if (!(ok = wait(sh.pv_done[(i - 1) & 1], (i - 1) >> 1, 6u))) break;
-          tc::fence_after();
-#pragma unroll
-          for (int c0 = 0; c0 < C::kCols; c0 += 8) {
-            uint32_t o[8];
-            const uint32_t at = tmem + tlane + kColO + col0 + c0;
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                         : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7])
-                         : "r"(at)
-                         : "memory");
-            tc::wait_ld();
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const float k = sh.corr[col0 + c0 + c];
-              o[c] = __float_as_uint(__uint_as_float(o[c]) * k);
-              l[c0 + c] *= k;
-            }
-            tc::st8(at, o);
-          }
-          tc::wait_st();
-        }
-        first = false;
+        if (over) break;  // weights are 2^kLift at most now
+        if (__any_sync(0xffffffffu, !first && counts && top > kTop) && lane == 0) sh.over[wg][turn & 1] = i + 1;
+        if (!(ok = meet()) || *(volatile uint32_t*)&sh.over[wg][turn & 1] != i + 1) break;
       }
-      // weights, their sums, and P^T into shared memory (row = key, 128 bytes of 64 columns)
-      if (!(ok = wait(sh.pv_done[i & 1], (i >> 1) ^ 1u, 7u))) break;
-      const uint32_t row = p_base + (i & 1) * C::kPBytes + (uint32_t)key * 128;
+      if (!ok) break;
+      // sums, and P^T into shared memory (row = key, 128 bytes of 64 columns)
+      const uint32_t row = p_base + (i & 1) * C::kPBytes + (uint32_t)key * 128 + (uint32_t)(col0 >> 6) * (kKeys * 128);
 #pragma unroll
       for (int ch = 0; ch < NCH; ++ch) {
-        if (NCH > 1 || over) {
+        if (NCH > 1) {
           load(ch);
-          relative(ch);
+          weigh(ch);
         }
         if (ch == NCH - 1) {
           tc::fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh.s_empty[sb]));
+          arrive(sh.s_ready[C::kAlt ? sb : (i + 1) & 1]);  // S has been read: room for the next in its place
         }
+        if (ch == 0 && !(ok = wait(sh.pv_done[i & 1], (i >> 1) ^ 1u, 7u))) break;
+        if (counts) {
 #pragma unroll
-        for (int c = 0; c < CH; c += 8) {
-          uint32_t p[4] = {0, 0, 0, 0};
-          if (counts) {
+          for (int c = 0; c < CH; c += 8) {
+            uint32_t p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float x = ex2(__uint_as_float(s[c + 2 * e])), y = ex2(__uint_as_float(s[c + 2 * e + 1]));
-              l[ch * CH + c + 2 * e] += x;
-              l[ch * CH + c + 2 * e + 1] += y;
+              const float x = __uint_as_float(s[c + 2 * e]), y = __uint_as_float(s[c + 2 * e + 1]);
+              uint64_t& sums = l[(ch * CH + c) / 2 + e];
+              sums = add2(sums, pack2(x, y));
               p[e] = pack_f16(x, y);
             }
+            sts128(row + ((((ch * CH + c) >> 3) ^ (key & 7)) << 4), p[0], p[1], p[2], p[3]);
           }
-          const uint32_t col = (uint32_t)(col0 + ch * CH + c);
-          sts128(row + (col >> 6) * (kKeys * 128) + ((((col & 63) >> 3) ^ (key & 7)) << 4), p[0], p[1], p[2], p[3]);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < CH; c += 8) sts128(row + ((((ch * CH + c) >> 3) ^ (key & 7)) << 4), 0, 0, 0, 0);
         }
       }
+      if (!ok) break;
       fence_proxy_async_shared();
       tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[i & 1]));
-      if (flags & kLast) {
-        // the segment's sums: l over the 128 keys' threads, O from TMEM (lane = dim)
-        const SegInfo info2 = sh.seg[seg % kSegs];
-#pragma unroll
-        for (int c = 0; c < C::kCols; ++c) {
-          float x = l[c];
-#pragma unroll
-          for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-          if (lane == 0) sh.mx[quad][col0 + c] = x;
-        }
-        if (!(ok = meet())) break;
-        const int c = (warp - 8 - 4 * wg) * 32 + lane, r = col0 + c;
-        const long long out = info2.slot * a.rows;
-        if (c < C::kCols && r < info2.rows) {
-          const float x = (sh.mx[0][r] + sh.mx[1][r]) + (sh.mx[2][r] + sh.mx[3][r]);
-          a.part_ml[out + r] = first ? make_float2(-INFINITY, 0.f) : make_float2(-sh.nm[r], x);
-        }
-        if (!(ok = wait(sh.pv_done[i & 1], i >> 1, 8u))) break;
+      arrive(sh.o_ready[i & 1]);
+      if (info.flags & kLast) {
+        // the stream's sums: O from TMEM (lane = dim), l over the 128 keys' threads
+        if (!wait(sh.pv_done[i & 1], i >> 1, 8u)) break;
         tc::fence_after();
+        const SegInfo si = sh.seg[info.seg % kSegs];
+        const long long out = ((long long)si.slot * (C::kAlt ? 2 : 1) + (C::kAlt ? wg : 0)) * a.rows;
 #pragma unroll 1
-        for (int c0 = 0; c0 < C::kCols && col0 + c0 < info2.rows; c0 += 8) {
+        for (int c0 = 0; c0 < NC; c0 += 8) {
           uint32_t o[8];
-          const uint32_t at = tmem + tlane + kColO + col0 + c0;
-          asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                       : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7])
-                       : "r"(at)
-                       : "memory");
+          ld8(tmem_o + c0, o);
           tc::wait_ld();
           if (key < groups * 16) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (col0 + c0 + e < info2.rows) a.part_o[(out + col0 + c0 + e) * (groups * 16) + key] = __uint_as_float(o[e]);
+              if (col0 + c0 + e < si.rows)
+                a.part_o[(out + col0 + c0 + e) * (groups * 16) + key] = __uint_as_float(o[e]);
           }
         }
         tc::fence_before();
-        if (!(ok = meet())) break;  // the exchange arrays are free again, and O has been read
-        if (lane == 0) mbar_arrive(smem_u32(&sh.o_empty));
-        ++seg;
-      }
-    }
-    (void)ok;
-  } else if (warp == C::kLoadWarp) {
-    // ------------------------------------------------------------ segments, pages, copies, Q
-    unsigned flags = bad ? SV_FLAG_BAD_LENGTH : 0u;
-    uint32_t i = 0, st = 0, ph = 0, seg = 0;
-    bool ok = true;
-    for (long long x = begin; ok && x < end; ++seg) {
-      const Segment s = segment_at(a, sh.cu, x, end, cta);
-      x += s.tiles;
-      const int row0 = s.rt * a.rows, rows = min(a.rows, a.T * a.G - row0);
-      if (lane == 0) {
-        sh.seg[seg % kSegs].slot = s.slot;
-        sh.seg[seg % kSegs].rows = rows;
-      }
-      // four tiles' pages at a time: lane = piece
-      int valid;
-      long long at = piece_at(a, s, s.tile0 * kPieces + lane, &valid, &flags);
-      if (s.tiles * kPieces <= lane) at = -1, valid = 0;
-      for (int t0 = 0; ok && t0 < s.tiles; t0 += 4) {
-        const long long now = at;
-        const int v = valid;
-        if (t0 + 4 < s.tiles) {
-          at = piece_at(a, s, (s.tile0 + t0 + 4) * kPieces + lane, &valid, &flags);
-          if ((s.tiles - t0 - 4) * kPieces <= lane) at = -1, valid = 0;
-        }
-        const long long prev = __shfl_up_sync(0xffffffffu, now, 1);
-        const bool there = now >= 0;
-        // a run of pieces that follow each other in the pool is one copy
-        const uint32_t heads = __ballot_sync(0xffffffffu, there && ((lane & 7) == 0 || prev < 0 || now != prev + 1));
-        const uint32_t have = __ballot_sync(0xffffffffu, there);
-        const uint32_t stop = (heads | ~have | 0x01010101u) & ~((2u << lane) - 1u);  // where a run of this lane ends
-        const int run = (stop ? __ffs(stop) - 1 : 32) - lane;
-        for (int t = 0; t < 4 && t0 + t < s.tiles; ++t, ++i) {
-          if (!(ok = wait(sh.empty[st], ph ^ 1u, 9u))) break;
-          const uint32_t nibble = (lane >> 3) == t ? (uint32_t)v : 0u;
-          uint32_t lo = __reduce_or_sync(0xffffffffu, (lane & 4) == 0 ? nibble << (8 * (lane & 3)) : 0u);
-          uint32_t hi = __reduce_or_sync(0xffffffffu, (lane & 4) != 0 ? nibble << (8 * (lane & 3)) : 0u);
-          if (lane == 0) {
-            TileInfo& ti = sh.info[i % kInfo];
-            ti.valid = (uint64_t)hi << 32 | lo;
-            ti.flags = (t0 + t == 0 ? kFirst : 0u) | (t0 + t == s.tiles - 1 ? kLast : 0u);
-            mbar_arrive_expect_tx(smem_u32(&sh.full[st]), 2u * pb * __popc(have >> (8 * t) & 0xffu));
+        arrive(sh.o_empty[C::kAlt ? wg : 0]);
+        constexpr int LC = NC < 32 ? NC : 32;
+#pragma unroll
+        for (int h = 0; h < NC / LC; ++h) {
+#pragma unroll
+          for (int c = 0; c < LC; c += 4) {
+            const float2 x = unpack2(l[(h * LC + c) / 2]), y = unpack2(l[(h * LC + c) / 2 + 1]);
+            sts128(row + (((c >> 2) ^ (key & 7)) << 4), __float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x),
+                   __float_as_uint(y.y));
           }
           __syncwarp();
-          if ((lane >> 3) == t && (heads >> lane & 1u)) {
-            const uint32_t dst = ring + st * stage_bytes + (lane & 7) * pb;
-            bulk_load(dst, a.k_pool + now * pb, run * pb, smem_u32(&sh.full[st]));
-            bulk_load(dst + side, a.v_pool + now * pb, run * pb, smem_u32(&sh.full[st]));
-          }
-          if (++st == (uint32_t)stages) st = 0, ph ^= 1u;
-        }
-        if (t0 == 0 && ok) {
-          // Q of the segment: rows of 16 lanes, 8 dims each, as halves (128-byte swizzle)
-          const uint32_t qb = seg % C::kQ;
-          if (!(ok = wait(sh.q_empty[qb], (seg / C::kQ) ^ 1u, 10u))) break;
-          const int c = lane & 15, half = lane >> 4;
-          const float scale = a.scale_log2 * exp2i(head_exp(a.k_exp, s.h));
-#pragma unroll 1
-          for (int r0 = 0; r0 < N; r0 += 16) {
-            uint4 w[8];
+          float x[4] = {0.f, 0.f, 0.f, 0.f};  // column `lane` over the warp's 32 keys
+          const uint32_t rows = row - (uint32_t)lane * 128 + (lane & 3) * 4;
+#pragma unroll 2
+          for (int k = 0; k < 32; k += 4)
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const int r = r0 + 2 * u + half;
-              w[u] = make_uint4(0, 0, 0, 0);
-              if (r < rows && c < 2 * groups)
-                w[u] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                             row_at(a, s.b, s.h, row0 + r) * a.d) + c);
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const int r = r0 + 2 * u + half;
-              const uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-              float y[8], top = 0.f;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                y[2 * e] = __uint_as_float(ww[e] << 16);
-                y[2 * e + 1] = __uint_as_float(ww[e] & 0xffff0000u);
-                top = fmaxf(top, fmaxf(fabsf(y[2 * e]), fabsf(y[2 * e + 1])));
-              }
-#pragma unroll
-              for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-              // the power of two that takes top into [2^14, 2^15)
-              const int e2 = (int)(__float_as_uint(top) >> 23);
-              const int up = e2 == 0 || e2 == 255 ? 0 : min(100, 127 + 14 - e2);
-              const float k = exp2i(up);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] *= k;
-              sts128(q_base + qb * C::kQBytes + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                     pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7]));
-              if (c == 0) sh.f[seg % kSegs][r] = scale * exp2i(-up);
-            }
-          }
-          fence_proxy_async_shared();
+            for (int e = 0; e < 4; ++e)
+              x[e] += __uint_as_float(lds32(rows + (k + e) * 128 + (((lane >> 2) ^ ((k + e) & 7)) << 4)));
+          if (lane < LC) sh.mx[in_wg][own0 + h * LC + lane] = (x[0] + x[1]) + (x[2] + x[3]);
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[qb]));
         }
-      }
-    }
-    if (flags) atomicOr(a.status, flags);
-    if (sh.abort) {  // copies in flight end before the CTA does
-      for (uint32_t k = 0; k < (uint32_t)stages && k < i; ++k) {
-        const uint32_t j = i - 1 - k;
-        mbar_wait_drain(smem_u32(&sh.full[j % stages]), (j / stages) & 1u);
+        if (!meet()) break;
+        const int c = in_wg * 32 + lane, r = col0 + c;
+        if (c < NC && r < si.rows) {
+          const int col = own0 + c;
+          const float x = (sh.mx[0][col] + sh.mx[1][col]) + (sh.mx[2][col] + sh.mx[3][col]);
+          a.part_ml[out + r] = first ? make_float2(-INFINITY, 0.f) : make_float2(-sh.nm[col], x);
+          if (info.flags & kOnly) a.part_ml[out + r + (wg ? -a.rows : a.rows)] = make_float2(-INFINITY, 0.f);
+        }
+        if (!meet()) break;  // the exchange array is free again
       }
     }
   } else {
-    // ------------------------------------------------------------ MMA issue
-    constexpr uint32_t id_s = idesc_f16(N, false), id_o = idesc_f16(N, true);
-    const uint64_t dq = tc::smem_desc(q_base, 16, 1024);
-    const uint64_t dp = tc::smem_desc(p_base, kKeys * 128, 1024);
-    const uint32_t lead = elect_lead();
-    uint32_t seg_s = 0, seg_o = 0;  // segments begun by S and by O
-    bool ok = true;
-    auto issue_s = [&](uint32_t i) {
-      if (!wait(sh.k_full[i & 1], i >> 1, 11u)) return false;
-      const uint32_t flags = sh.info[i % kInfo].flags;
-      const uint32_t sb = i % C::kS, qb = seg_s % C::kQ;
-      if ((flags & kFirst) && !wait(sh.q_full[qb], seg_s / C::kQ, 12u)) return false;
-      if (!wait(sh.s_empty[sb], (i / C::kS) ^ 1u, 13u)) return false;
-      tc::fence_after();
-      const uint64_t q = dq + (uint64_t)(qb * (C::kQBytes >> 4));
-#pragma unroll
-      for (int kk = 0; kk < (DG ? DG : 8); ++kk)
-        if (DG || kk < groups)
-          lead_mma_ts(lead, tmem + kColS + sb * 64, tmem + kColK + (i & 1) * 64 + kk * 8,
-                      q + (uint64_t)(((kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4), id_s, kk > 0 ? 1u : 0u);
-      lead_commit(lead, smem_u32(&sh.s_full[sb]));
-      lead_commit(lead, smem_u32(&sh.k_empty[i & 1]));
-      if (flags & kLast) {
-        lead_commit(lead, smem_u32(&sh.q_empty[qb]));
-        ++seg_s;
+    if (warp == kLoadWarp) {
+      // ------------------------------------------------------------ segments, pages, copies
+      // earlier kernels' plain stores to the pools come before this one's bulk copies
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      unsigned flags = bad ? SV_FLAG_BAD_LENGTH : 0u;
+      uint32_t i = 0, st = 0, ph = 0, seg = 0;
+      bool ok = true;
+      for (int x = begin; ok && x < end; ++seg) {
+        const Segment s = next_segment(a, sh, x, end);
+        x += s.tiles;
+        if (lane == 0) {
+          sh.seg[seg % kSegs].slot = s.slot;
+          sh.seg[seg % kSegs].rows = min(a.rows, a.T * a.G - s.rt * a.rows);
+        }
+        // four tiles' pages at a time: lane = piece
+        long long next = -1;
+        int next_valid = 0;
+#pragma unroll 1
+        for (int t0 = -4; ok && t0 < s.tiles; t0 += 4) {
+          const long long now = next;
+          const int v = next_valid;
+          if (t0 + 4 < s.tiles) {
+            next = piece_at(a, s, (s.tile0 + t0 + 4) * kPieces + lane, &next_valid, &flags);
+            if ((s.tiles - t0 - 4) * kPieces <= lane) next = -1, next_valid = 0;
+          }
+          if (t0 < 0) continue;
+          const long long prev = __shfl_up_sync(0xffffffffu, now, 1);
+          const bool there = now >= 0;
+          // a run of pieces that follow each other in the pool is one copy
+          const uint32_t heads = __ballot_sync(0xffffffffu, there && ((lane & 7) == 0 || prev < 0 || now != prev + 1));
+          const uint32_t have = __ballot_sync(0xffffffffu, there);
+          const uint32_t stop = (heads | ~have | 0x01010101u) & ~((2u << lane) - 1u);  // where a run of this lane ends
+          const int run = (stop ? __ffs(stop) - 1 : 32) - lane;
+#pragma unroll 1
+          for (int t = 0; t < 4 && t0 + t < s.tiles; ++t, ++i) {
+            if (!(ok = wait(sh.empty[st], ph ^ 1u, 9u))) break;
+            const uint32_t count = (lane >> 3) == t ? (uint32_t)v << (8 * (lane & 3)) : 0u;
+            const uint32_t lo = __reduce_or_sync(0xffffffffu, (lane & 4) == 0 ? count : 0u);
+            const uint32_t hi = __reduce_or_sync(0xffffffffu, (lane & 4) != 0 ? count : 0u);
+            if (lane == 0) {
+              const int at = t0 + t, left = s.tiles - at, per = C::kAlt ? 2 : 1;
+              TileInfo& ti = sh.info[i % kInfo];
+              ti.valid = (uint64_t)hi << 32 | lo;
+              ti.flags = (at == 0 ? kBegin : 0u) | (left == 1 ? kEnd : 0u) | (at < per ? kFirst : 0u) |
+                         (left <= per ? kLast : 0u) | (C::kAlt && s.tiles == 1 ? kOnly : 0u);
+              ti.seg = seg;
+              mbar_arrive_expect_tx(smem_u32(&sh.full[st]), 2u * pb * __popc(have >> (8 * t) & 0xffu));
+            }
+            __syncwarp();
+            if ((lane >> 3) == t && (heads >> lane & 1u)) {
+              const uint32_t dst = ring + st * stage_bytes + (lane & 7) * pb;
+              bulk_load(dst, a.k_pool + now * pb, run * pb, smem_u32(&sh.full[st]));
+              bulk_load(dst + side, a.v_pool + now * pb, run * pb, smem_u32(&sh.full[st]));
+            }
+            if (++st == (uint32_t)stages) st = 0, ph ^= 1u;
+          }
+        }
       }
-      return true;
-    };
-    auto issue_o = [&](uint32_t i) {
-      if (!wait(sh.v_full[i & 1], i >> 1, 14u)) return false;
-      const bool first = sh.info[i % kInfo].flags & kFirst;
-      if (first) {
-        if (!wait(sh.o_empty, seg_o ^ 1u, 15u)) return false;
-        ++seg_o;
+      if (flags) atomicOr(a.status, flags);
+      if (sh.abort) {  // copies in flight end before the CTA does
+        for (uint32_t k = 0; k < (uint32_t)stages && k < i; ++k) {
+          const uint32_t j = i - 1 - k;
+          mbar_wait_drain(smem_u32(&sh.full[j % stages]), (j / stages) & 1u);
+        }
       }
-      if (!wait(sh.p_full[i & 1], i >> 1, 16u)) return false;
-      tc::fence_after();
-      const uint64_t p = dp + (uint64_t)((i & 1) * (C::kPBytes >> 4));
+    } else if (warp == kScoreWarp) {
+      // ------------------------------------------------------------ S^T = K Q^T
+      constexpr uint32_t id_s = idesc_f16(N, false);
+      const uint64_t dq = tc::smem_desc(q_base, 16, 1024);
+      const uint32_t lead = elect_lead();
+      for (uint32_t i = 0; i < tiles; ++i) {
+        if (!wait(sh.s_ready[i & 1], i >> 1, 11u)) break;
+        const TileInfo info = sh.info[i % kInfo];
+        const uint32_t sb = C::kAlt ? i & 1 : 0, qb = info.seg % C::kQ;
+        if ((info.flags & kBegin) &&
+            !(info.seg ? wait(sh.q_full[qb], (info.seg / C::kQ - (qb == 0)) & 1u, 12u) : wait(sh.q_first, 0, 12u)))
+          break;
+        tc::fence_after();
+        const uint64_t q = dq + (uint64_t)(qb * (C::kQBytes >> 4));
 #pragma unroll
-      for (int kk = 0; kk < kKeys / 16; ++kk)
-        lead_mma_ts(lead, tmem + kColO, tmem + kColV + (i & 1) * 64 + kk * 8, p + (uint64_t)((kk * 2048) >> 4),
-                    id_o, first && kk == 0 ? 0u : 1u);
-      lead_commit(lead, smem_u32(&sh.pv_done[i & 1]));
-      return true;
-    };
-    if (tiles > 0) ok = issue_s(0);
-    for (uint32_t i = 0; ok && i < tiles; ++i) {
-      // with one S buffer the next S waits for this tile's weights, else it goes ahead of them
-      if (i + 1 < tiles && !(ok = issue_s(i + 1))) break;
-      ok = issue_o(i);
-    }
-    if (!ok) {  // products in flight end before TMEM is given back
-      lead_commit(lead, smem_u32(&sh.drained));
-      mbar_wait_drain(smem_u32(&sh.drained), 0);
+        for (int kk = 0; kk < (DG ? DG : 8); ++kk)
+          if (DG || kk < groups)
+            lead_mma_ts(lead, tmem + kColS + sb * 64, tmem + kColK + (i & 1) * 64 + kk * 8,
+                        q + (uint64_t)(((kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4), id_s, kk > 0 ? 1u : 0u);
+        lead_commit(lead, smem_u32(&sh.s_full[sb]));
+        lead_commit(lead, smem_u32(&sh.k_empty[i & 1]));
+        if (info.flags & kEnd) lead_commit(lead, smem_u32(&sh.q_empty[qb]));
+      }
+      if (sh.abort) {  // products in flight end before TMEM is given back
+        lead_commit(lead, smem_u32(&sh.drained[0]));
+        mbar_wait_drain(smem_u32(&sh.drained[0]), 0);
+      }
+    } else if (warp == kOutWarp) {
+      // ------------------------------------------------------------ O^T += V^T P^T
+      constexpr uint32_t id_o = idesc_f16(N, true);
+      const uint64_t dp = tc::smem_desc(p_base, kKeys * 128, 1024);
+      const uint32_t lead = elect_lead();
+      uint32_t begun[2] = {0, 0};  // segments that O's streams have begun
+      for (uint32_t i = 0; i < tiles; ++i) {
+        if (!wait(sh.o_ready[i & 1], i >> 1, 14u)) break;
+        const bool first = sh.info[i % kInfo].flags & kFirst;
+        const uint32_t ob = C::kAlt ? i & 1 : 0;
+        if (first && !wait(sh.o_empty[ob], begun[ob]++ ^ 1u, 15u)) break;
+        tc::fence_after();
+        const uint64_t p = dp + (uint64_t)((i & 1) * (C::kPBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          lead_mma_ts(lead, tmem + kColO + ob * N, tmem + kColV + (i & 1) * 64 + kk * 8, p + (uint64_t)((kk * 2048) >> 4),
+                      id_o, first && kk == 0 ? 0u : 1u);
+        lead_commit(lead, smem_u32(&sh.pv_done[i & 1]));
+      }
+      if (sh.abort) {
+        lead_commit(lead, smem_u32(&sh.drained[1]));
+        mbar_wait_drain(smem_u32(&sh.drained[1]), 0);
+      }
+    } else {
+      // ------------------------------------------------------------ Q of the segments behind the first
+      uint32_t seg = 0;
+      for (int x = begin; x < end; ++seg) {
+        const Segment s = next_segment(a, sh, x, end);
+        x += s.tiles;
+        if (seg == 0) continue;
+        const uint32_t qb = seg % C::kQ;
+        // the buffer's segment before (the first ones' too) has been multiplied
+        if (seg >= (uint32_t)C::kQ && !wait(sh.q_empty[qb], seg / C::kQ - 1, 10u)) break;
+        lay_out_q(a, s, N, q_base + qb * C::kQBytes, sh.f[seg % kF], 0, 1);
+        arrive(sh.q_full[qb]);
+      }
     }
   }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (warp == C::kMmaWarp) {
-    tc::relinquish();
-    tc::dealloc(tmem, kTmemCols);
-  }
+  if (warp == kScoreWarp) tc::dealloc(tmem, kTmemCols);
 }
 
 template <int N, int DG>
@@ -677,7 +775,7 @@ cudaError_t launch(const Attend4Args& a, cudaStream_t st) {
   }
   const int stage = 2 * kPieces * piece_bytes(a.d), fixed = 1024 + C::kFixed + 128;
   const int stages = std::min(kMaxStages, (kMost - fixed) / stage);
-  return launch_pdl(attend4_tc_kernel<N, DG>, dim3(a.ctas), dim3(C::kThreads), (size_t)kMost, st, a, stages);
+  return launch_pdl(attend4_tc_kernel<N, DG>, dim3(a.ctas), dim3(kThreads), (size_t)kMost, st, a, stages);
 }
 
 template <int N>
@@ -693,7 +791,9 @@ cudaError_t launch_attend4_tc(Attend4Args a, cudaStream_t st) {
   const int stacked = a.T * a.G;
   a.row_tiles = (stacked + kTc4Rows - 1) / kTc4Rows;
   a.rows = (stacked + a.row_tiles - 1) / a.row_tiles;
+  a.streams = a.rows <= 64 ? 2 : 1;
   a.ppt = kPieces;
+  a.ppt_shift = 3;
   a.ctas = std::min(kMaxTc4Ctas, sm_count());
   const cudaError_t e = a.rows <= 16   ? launch_n<16>(a, st)
                         : a.rows <= 32 ? launch_n<32>(a, st)
