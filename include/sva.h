@@ -563,7 +563,7 @@ sv_status sv_prefix_attend(const sv_shape* shape, const void* q, const sv_kv* kv
  *     at the row's position p. The other dims stay.
  * All of it in fp32, rounded once. rot: a multiple of 8 in [0, d]; 0 rotates
  * nothing, and table and positions may be NULL. table: DEVICE fp32
- * [max_pos, rot]. (A table and not frequencies: angles of far positions need
+ * [max_pos, rot], 16-byte aligned. (A table and not frequencies: angles of far positions need
  * more than 32 bits, and every model scales them in its own way.) */
 typedef struct {
   const void* q_weight;
@@ -614,7 +614,8 @@ sv_status sv_rope_write_kv(const sv_shape* shape, const sv_rope* rope, const int
  *           2 j + 1 of the group; scales [16 tokens][d / 16]
  *   v_pool: codes [d / 16][8][16 tokens], byte c = dims c (low 4 bits) and
  *           c + 8 of the group; scales [d / 16][16 tokens]
- * Every byte belongs to one token. Needs d % 16 == 0 and blk % 16 == 0. Pools
+ * Every byte belongs to one token. Needs d % 16 == 0, blk % 16 == 0, Hkv <= 4096
+ * and B <= 65535 (1024 in sv_attend_kv4). Pools
  * are 16-byte aligned device memory; any bytes are a valid page. block_table:
  * [B, nb_max] as in sv_kv; seq_ctx: DEVICE int32 [B], the tokens of each
  * sequence. The row calls (sv_write_kv4, sv_read_kv4) use neither. */

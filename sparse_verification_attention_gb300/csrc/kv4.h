@@ -19,8 +19,8 @@ struct RopeArgs {
   unsigned* status;            // may be null
   long long q_stride, k_stride, v_stride, qo_stride, ko_stride;  // elements
   int n, Hq, Hkv, d, blk, num_pages, rot, max_pos, interleaved;
-  int parts;                   // warps that share a token's heads
-  float eps;
+  int parts_shift;             // log2 of the warps that share a token's heads
+  float eps, inv_d;
 };
 cudaError_t launch_rope(RopeArgs a, int dtype, cudaStream_t st);
 

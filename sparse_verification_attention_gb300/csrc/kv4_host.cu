@@ -49,9 +49,9 @@ sv_status check_rope(const sv_shape* s, const sv_rope* r, const int32_t* positio
   if (r->rot && (!r->table || r->max_pos < 1 || !positions))
     return fail(SV_ERR_INVALID_ARG, "a rotation needs table, max_pos >= 1 (%d) and positions", r->max_pos);
   if (!(r->eps >= 0.f) || std::isinf(r->eps)) return fail(SV_ERR_INVALID_ARG, "eps=%g", (double)r->eps);
-  if (!aligned(r->q_weight, 16) || !aligned(r->k_weight, 16))
-    return fail(SV_ERR_INVALID_ARG, "q_weight/k_weight must be 16-byte aligned");
-  return check_words4("table and positions", {r->table, positions});
+  if (!aligned(r->q_weight, 16) || !aligned(r->k_weight, 16) || !aligned(r->table, 16))
+    return fail(SV_ERR_INVALID_ARG, "table/q_weight/k_weight must be 16-byte aligned");
+  return check_words4("positions", {positions});
 }
 
 void fill_rope(RopeArgs* a, const sv_shape* s, const sv_rope* r, const int32_t* positions, int n, void* ws) {
@@ -78,6 +78,8 @@ sv_status check_shape4(const sv_shape* s) {
   if (s->d % 16) return fail(SV_ERR_UNSUPPORTED, "head dim %d of a 4-bit cache must be a multiple of 16", s->d);
   if (s->blk % kPiece)
     return fail(SV_ERR_UNSUPPORTED, "pages of %d tokens of a 4-bit cache: need a multiple of %d", s->blk, kPiece);
+  if (s->Hkv > 4096 || s->B > 65535)
+    return fail(SV_ERR_UNSUPPORTED, "Hkv=%d heads or B=%d sequences of a 4-bit cache exceed 4096 and 65535", s->Hkv, s->B);
   return SV_OK;
 }
 sv_status check_kv4(const sv_shape* s, const sv_kv4* kv) {

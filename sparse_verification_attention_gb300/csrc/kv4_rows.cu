@@ -44,201 +44,227 @@ __device__ __forceinline__ void store16(T* p, const float (&x)[16]) {
 // A lane has one group of one token's head; a warp 16 tokens and two neighbouring
 // groups, so that rows are read in runs of 64 bytes, K codes written in runs of 128
 // and the bytes of a V code row in runs of 16 when the tokens' slots follow each
-// other (nothing depends on it).
+// other (nothing depends on it). Blocks: 16 tokens (x), eight pairs of groups (y): those
+// of K, then those of V.
 struct Place {
-  const int32_t* slot;
-  long long token;
-  int h, g, is_v;
-  bool ok;
+  int token, h, g, is_v, tok;
+  uint8_t* piece;  // null: nothing to do
 };
 __device__ __forceinline__ Place place_of(const Rows4Args& a) {
   const int lane = threadIdx.x & 31;
-  const int groups = a.d / kGroup, cols = a.Hkv * groups * 2;  // K groups, then V groups
-  const int pairs = (cols + 1) / 2;                            // pairs of groups
-  const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const long long tb = w / pairs;
-  int col = (int)(w - tb * pairs) * 2 + (lane & 1);
+  const int groups = a.d / kGroup, cols = a.Hkv * groups;
+  int col = (blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5)) * 2 + (lane & 1);
   Place p;
-  p.token = tb * 16 + (lane >> 1);
-  p.ok = p.token < a.n && col < cols;
-  p.is_v = col >= a.Hkv * groups;
-  col -= p.is_v ? a.Hkv * groups : 0;
-  p.h = col / groups;
+  p.token = blockIdx.x * 16 + (lane >> 1);
+  p.is_v = col >= cols;
+  col -= p.is_v ? cols : 0;
+  p.h = (unsigned)col / (unsigned)groups;
   p.g = col - p.h * groups;
-  return p;
-}
-// The piece and token within it of a slot, or null.
-__device__ __forceinline__ uint8_t* piece_of(const Rows4Args& a, const Place& p, int* tok) {
+  p.piece = nullptr;
+  p.tok = 0;
+  pdl_wait();
+  pdl_trigger();
+  if (p.token >= a.n || col >= cols) return p;
   const int slot = a.slots[p.token];
-  const int page = slot < 0 ? -1 : slot / a.blk;
+  const int page = slot < 0 ? -1 : (int)((unsigned)slot / (unsigned)a.blk);
   if (page < 0 || page >= a.num_pages) {
     if (slot != -1 && p.h == 0 && p.g == 0 && a.status) atomicOr(a.status, SV_FLAG_BAD_PAGE);
-    return nullptr;
+    return p;
   }
   const int in = slot - page * a.blk;
-  *tok = in & (kPiece - 1);
-  return (p.is_v ? a.v_pool : a.k_pool) +
-         (((long long)page * a.Hkv + p.h) * (a.blk / kPiece) + in / kPiece) * piece_bytes(a.d);
+  p.tok = in % kPiece;
+  p.piece = (p.is_v ? a.v_pool : a.k_pool) +
+            (((long long)page * a.Hkv + p.h) * (a.blk / kPiece) + in / kPiece) * piece_bytes(a.d);
+  return p;
 }
 
 // Rounding: the scale of a group is amax / 6 to the nearest E4M3 value, a code the
-// nearest E2M1 value of element / scale. Both quotients are rounded correctly in 32
-// bits, and that never moves one onto a border between two codes: a border times a
-// scale has at most seven significant bits, so a 24-bit element differs from it by
-// a unit in its last place at least, which is more than half a unit of the quotient.
+// nearest E2M1 value of x / (scale 2^exp). Quotients in 32 bits never move one onto a
+// border between two codes or over it: a border times a scale has at most seven
+// significant bits, so an x that is not on the border differs from it by a unit in its last
+// place at least, 2^-23 / 1.875 relatively, and the quotient by more than half a unit. x times
+// the reciprocal is off by up to two units; one step of Newton's on the quotient, whose
+// remainder x - q s the fma gives exactly, leaves 2^-45 before the last rounding.
+// (A division each took 550 instructions a group, 33 us for 13,343 rows of 8 heads.)
 template <typename T>
 __global__ void __launch_bounds__(kThreads) write_kv4_kernel(const __grid_constant__ Rows4Args a) {
   const Place p = place_of(a);
-  pdl_wait();
-  pdl_trigger();
-  if (!p.ok) return;
-  int tok;
-  uint8_t* piece = piece_of(a, p, &tok);
-  if (!piece) return;
+  if (!p.piece) return;
   float x[16];
   load16(static_cast<const T*>(p.is_v ? a.v : a.k) + p.token * (p.is_v ? a.v_stride : a.k_stride) +
              (long long)p.h * a.d + p.g * kGroup,
          x);
-  const float unit = exp2i(-head_exp(p.is_v ? a.v_exp : a.k_exp, p.h));
-  float amax = 0.f;
-  bool nan = false;
+  const int e = head_exp(p.is_v ? a.v_exp : a.k_exp, p.h);
+  uint32_t top = 0;  // magnitudes compare as integers, a NaN's above all
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  const float amax = __uint_as_float(top) * exp2i(-e);
+  const uint32_t sb = top > 0x7f800000u ? 0x7fu : f32_to_e4m3(__fdiv_rn(amax, 6.f));
+  const float s = e4m3_to_f32(sb) * exp2i(e);
+  if (amax > 6.5f * 448.f) {  // beyond the largest code: no infinities below
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -8.f * s), 8.f * s);
+  }
+  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+  uint32_t c[8];  // dims 2 j, 2 j + 1 of K, j, j + 8 of V
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    x[i] *= unit;
-    nan |= x[i] != x[i];
-    amax = fmaxf(amax, fabsf(x[i]));
+    const float q = x[i] * r;
+    x[i] = __fmaf_rn(__fmaf_rn(-q, s, x[i]), r, q);
   }
-  const uint32_t sb = nan ? 0x7fu : f32_to_e4m3(__fdiv_rn(amax, 6.f));
-  const float s = e4m3_to_f32(sb);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = s > 0.f ? __fdiv_rn(x[i], s) : 0.f;
-  uint8_t* codes = piece + p.g * 128;
+  for (int j = 0; j < 8; ++j) c[j] = p.is_v ? f32x2_to_e2m1x2(x[j], x[j + 8]) : f32x2_to_e2m1x2(x[2 * j], x[2 * j + 1]);
+  uint8_t* codes = p.piece + p.g * 128;
   if (p.is_v) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) codes[c * 16 + tok] = (uint8_t)f32x2_to_e2m1x2(x[c], x[c + 8]);
-    piece[8 * a.d + p.g * 16 + tok] = (uint8_t)sb;
+    for (int j = 0; j < 8; ++j) codes[j * 16 + p.tok] = (uint8_t)c[j];
+    p.piece[8 * a.d + p.g * 16 + p.tok] = (uint8_t)sb;
   } else {
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j / 4] |= f32x2_to_e2m1x2(x[2 * j], x[2 * j + 1]) << (j % 4 * 8);
-    *reinterpret_cast<uint2*>(codes + tok * 8) = make_uint2(w[0], w[1]);
-    piece[8 * a.d + tok * (a.d / kGroup) + p.g] = (uint8_t)sb;
+    const uint32_t lo = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, hi = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
+    *reinterpret_cast<uint2*>(codes + p.tok * 8) = make_uint2(lo, hi);
+    p.piece[8 * a.d + p.tok * (a.d / kGroup) + p.g] = (uint8_t)sb;
   }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) read_kv4_kernel(const __grid_constant__ Rows4Args a) {
   const Place p = place_of(a);
-  pdl_wait();
-  pdl_trigger();
-  if (!p.ok) return;
-  int tok;
-  const uint8_t* piece = piece_of(a, p, &tok);
-  if (!piece) return;
-  const uint8_t* codes = piece + p.g * 128;
-  float x[16];
-  const float unit = exp2i(head_exp(p.is_v ? a.v_exp : a.k_exp, p.h));
-  const float s =
-      e4m3_to_f32(__ldcg(piece + 8 * a.d + (p.is_v ? p.g * 16 + tok : tok * (a.d / kGroup) + p.g))) * unit;
+  if (!p.piece) return;
+  const uint8_t* codes = p.piece + p.g * 128;
+  uint32_t w[2], h[8];
+  const uint32_t sb = __ldcg(p.piece + 8 * a.d + (p.is_v ? p.g * 16 + p.tok : p.tok * (a.d / kGroup) + p.g));
   if (p.is_v) {
+    uint32_t c[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const float2 f = f16x2_to_f32(e2m1x2_to_f16x2(__ldcg(codes + c * 16 + tok)));
-      x[c] = f.x * s;
-      x[c + 8] = f.y * s;
-    }
+    for (int j = 0; j < 8; ++j) c[j] = __ldcg(codes + j * 16 + p.tok);
+    w[0] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+    w[1] = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
   } else {
-    const uint2 v = __ldcg(reinterpret_cast<const uint2*>(codes + tok * 8));
+    const uint2 v = __ldcg(reinterpret_cast<const uint2*>(codes + p.tok * 8));
+    w[0] = v.x;
+    w[1] = v.y;
+  }
+  e2m1x8_to_f16(w[0], h);
+  e2m1x8_to_f16(w[1], h + 4);
+  const float s = e4m3_to_f32(sb) * exp2i(head_exp(p.is_v ? a.v_exp : a.k_exp, p.h));
+  float x[16];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 f = f16x2_to_f32(e2m1x2_to_f16x2((j < 4 ? v.x : v.y) >> (j % 4 * 8) & 0xffu));
-      x[2 * j] = f.x * s;
-      x[2 * j + 1] = f.y * s;
-    }
+  for (int j = 0; j < 8; ++j) {
+    const float2 f = f16x2_to_f32(h[j]);
+    x[2 * j] = f.x * s;
+    x[2 * j + 1] = f.y * s;
+  }
+  if (p.is_v) {  // dims j, j + 8 stand side by side
+    float y[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = x[2 * j], y[j + 8] = x[2 * j + 1];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = y[j];
   }
   store16(static_cast<T*>(p.is_v ? a.v_out : a.k_out) + p.token * (p.is_v ? a.v_stride : a.k_stride) +
               (long long)p.h * a.d + p.g * kGroup,
           x);
 }
 
-// One warp per (sequence, head, block): lanes are groups x token subsets, 16 sums a
-// lane, the subsets folded at the end (always in the same order).
-__global__ void __launch_bounds__(kThreads) reps_kv4_kernel(const __grid_constant__ Reps4Args a, int gp) {
-  const int lane = threadIdx.x & 31, g = lane & (gp - 1), sub = lane / gp, subs = 32 / gp;
-  const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+// x += the halves of h (low, high) times the half s, in fp32.
+__device__ __forceinline__ void fma_f32_f16x2(float& x, float& y, uint32_t h, uint16_t s) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "fma.rn.f32.f16 %0, a, %3, %0;\n\t"
+      "fma.rn.f32.f16 %1, b, %3, %1;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "r"(h), "h"(s));
+}
+
+// One warp per (sequence, head, block): a lane has a group of 4 tokens of every piece (so
+// 16 sums), `gp` lanes side by side the groups (those of d > 128 in two rounds). The four
+// token subsets are folded at the end, always in the same order.
+// Bound by HBM, and nearly as much by issue: the products are fp32 sums of halves.
+__global__ void __launch_bounds__(kThreads) reps_kv4_kernel(const __grid_constant__ Reps4Args a) {
+  const int lane = threadIdx.x & 31, sub = lane & 3;
+  const int jb = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int h = blockIdx.y, b = blockIdx.z;
   pdl_wait();
   pdl_trigger();
-  const long long bh = w / a.max_blocks;
-  const int b = (int)(bh / a.Hkv), h = (int)(bh - (long long)b * a.Hkv);
-  if (b >= a.B) return;
-  const int most = a.nb_max * a.blk;
-  const int len = min(max(a.seq_ctx[b], 0), most), from = a.from_len ? min(max(a.from_len[b], 0), most) : 0;
-  if (lane == 0 && h == 0 && w == bh * a.max_blocks && a.status &&
-      (len != a.seq_ctx[b] || (a.from_len && from != a.from_len[b])))
+  const int most = a.nb_max * a.blk, len0 = a.seq_ctx[b], from0 = a.from_len ? a.from_len[b] : 0;
+  const int len = min(max(len0, 0), most), from = min(max(from0, 0), most);
+  if (threadIdx.x == 0 && h == 0 && blockIdx.x == 0 && a.status && (len != len0 || from != from0))
     atomicOr(a.status, SV_FLAG_BAD_LENGTH);
-  const int j = from / a.blk + (int)(w - bh * a.max_blocks);
-  if (j >= len / a.blk) return;
+  const int j = from / a.blk + jb;
+  if (jb >= a.max_blocks || j >= len / a.blk) return;
   const int page = a.block_table[(long long)b * a.nb_max + j];
   if (page < 0 || page >= a.num_pages) {
     if (lane == 0 && a.status) atomicOr(a.status, SV_FLAG_BAD_PAGE);
     return;
   }
-  const int groups = a.d / kGroup, pb = piece_bytes(a.d);
-  const uint8_t* p = a.k_pool + ((long long)page * a.Hkv + h) * (a.blk / kPiece) * pb;
-  float x[16];
+  const int groups = a.d / kGroup, pb = piece_bytes(a.d), pieces = a.blk / kPiece;
+  const uint8_t* p = a.k_pool + ((long long)page * a.Hkv + h) * pieces * pb;
+  const float unit = __fdiv_rn(exp2i(head_exp(a.k_exp, h)), (float)a.blk);
+  float* to = a.reps + (((long long)b * a.Hkv + h) * a.nb_max + j) * a.d;
+#pragma unroll 1
+  for (int g0 = 0; g0 < groups; g0 += 8) {
+    const int g = g0 + (lane >> 2);
+    const bool on = g < groups;
+    float x[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = 0.f;
-  if (g < groups) {
-    for (int t = sub; t < a.blk; t += subs) {
-      const uint8_t* piece = p + (t / kPiece) * pb;
-      const int tok = t % kPiece;
-      const uint2 v = __ldcg(reinterpret_cast<const uint2*>(piece + g * 128 + tok * 8));
-      const float s = e4m3_to_f32(__ldcg(piece + 8 * a.d + tok * groups + g));
+    for (int i = 0; i < 16; ++i) x[i] = 0.f;
+    if (on) {
+      const uint8_t *codes = p + g * 128 + sub * 32, *scales = p + 8 * a.d + sub * 4 * groups + g;
+#pragma unroll 2
+      for (int t = 0; t < pieces; ++t, codes += pb, scales += pb) {
+        const uint4 c[2] = {__ldcg(reinterpret_cast<const uint4*>(codes)), __ldcg(reinterpret_cast<const uint4*>(codes) + 1)};
+        const uint32_t sc = __ldcg(scales) | __ldcg(scales + groups) << 8 | __ldcg(scales + 2 * groups) << 16 |
+                            (uint32_t)__ldcg(scales + 3 * groups) << 24;
+        uint32_t s[2];
+        e4m3x4_to_f16(sc, s[0], s[1]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 f = f16x2_to_f32(e2m1x2_to_f16x2((i < 4 ? v.x : v.y) >> (i % 4 * 8) & 0xffu));
-        x[2 * i] += f.x * s;
-        x[2 * i + 1] += f.y * s;
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t w0 = k % 2 ? c[k / 2].z : c[k / 2].x, w1 = k % 2 ? c[k / 2].w : c[k / 2].y;
+          uint32_t f[8];
+          e2m1x8_to_f16(w0, f);
+          e2m1x8_to_f16(w1, f + 4);
+          const uint16_t sk = (uint16_t)(k % 2 ? s[k / 2] >> 16 : s[k / 2]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) fma_f32_f16x2(x[2 * i], x[2 * i + 1], f[i], sk);
+        }
       }
     }
+    // fold: the lane keeps 4 of the 16 sums of its group
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      x[i] += __shfl_xor_sync(0xffffffffu, x[i], 1);
+      x[i] += __shfl_xor_sync(0xffffffffu, x[i], 2);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      y[i] = (sub == 0 ? x[i] : sub == 1 ? x[4 + i] : sub == 2 ? x[8 + i] : x[12 + i]) * unit;
+    if (on) *reinterpret_cast<float4*>(to + g * kGroup + sub * 4) = make_float4(y[0], y[1], y[2], y[3]);
   }
-  for (int o = 16; o >= gp; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
-  if (sub || g >= groups) return;
-  const float unit = exp2i(head_exp(a.k_exp, h));
-  float* to = a.reps + (((long long)b * a.Hkv + h) * a.nb_max + j) * a.d + g * kGroup;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i] * unit, (float)a.blk);
-  store16(to, x);
 }
 
-unsigned row_blocks(const Rows4Args& a) {
-  const long long pairs = (long long)a.Hkv * (a.d / kGroup);
-  const long long warps = (a.n + 15ll) / 16 * pairs;
-  return (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
+dim3 row_grid(const Rows4Args& a) {
+  const int pairs = a.Hkv * (a.d / kGroup);  // K and V: two groups each
+  return dim3((unsigned)((a.n + 15ll) / 16), (unsigned)((pairs + kThreads / 32 - 1) / (kThreads / 32)));
 }
 
 }  // namespace
 
 cudaError_t launch_write_kv4(const Rows4Args& a, int dtype, cudaStream_t st) {
-  const dim3 grid(row_blocks(a)), block(kThreads);
-  return dtype == SV_BF16 ? launch_pdl(write_kv4_kernel<__nv_bfloat16>, grid, block, 0, st, a)
-                          : launch_pdl(write_kv4_kernel<float>, grid, block, 0, st, a);
+  const dim3 block(kThreads);
+  return dtype == SV_BF16 ? launch_pdl(write_kv4_kernel<__nv_bfloat16>, row_grid(a), block, 0, st, a)
+                          : launch_pdl(write_kv4_kernel<float>, row_grid(a), block, 0, st, a);
 }
 
 cudaError_t launch_read_kv4(const Rows4Args& a, int dtype, cudaStream_t st) {
-  const dim3 grid(row_blocks(a)), block(kThreads);
-  return dtype == SV_BF16 ? launch_pdl(read_kv4_kernel<__nv_bfloat16>, grid, block, 0, st, a)
-                          : launch_pdl(read_kv4_kernel<float>, grid, block, 0, st, a);
+  const dim3 block(kThreads);
+  return dtype == SV_BF16 ? launch_pdl(read_kv4_kernel<__nv_bfloat16>, row_grid(a), block, 0, st, a)
+                          : launch_pdl(read_kv4_kernel<float>, row_grid(a), block, 0, st, a);
 }
 
 cudaError_t launch_reps_kv4(const Reps4Args& a, cudaStream_t st) {
-  int gp = 1;
-  while (gp < a.d / kGroup) gp <<= 1;
-  const long long warps = (long long)a.B * a.Hkv * a.max_blocks;
-  return launch_pdl(reps_kv4_kernel, dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32))),
-                    dim3(kThreads), 0, st, a, gp);
+  const dim3 grid((unsigned)((a.max_blocks + kThreads / 32 - 1) / (kThreads / 32)), (unsigned)a.Hkv, (unsigned)a.B);
+  return launch_pdl(reps_kv4_kernel, grid, dim3(kThreads), 0, st, a);
 }
 
 }  // namespace sva

@@ -192,6 +192,20 @@ __device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t* r) {
   }
 }
 
+// A wait that may suspend the warp for up to a millisecond: without the hint it comes back
+// after a fraction of a tile, and the polls of the twenty warps took issue slots from those
+// that had work.
+__device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
 // The rest of a wait, out of line (a wait's clock and limit inline would fill the
 // instruction cache).
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* status,
@@ -312,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
   const uint32_t tiles = (uint32_t)(end - begin);
   auto wait = [&](uint64_t& bar, uint32_t parity, unsigned site) {
     const uint32_t addr = smem_u32(&bar);
-    return __all_sync(0xffffffffu, mbar_try_wait(addr, parity & 1u)) ||
+    return __all_sync(0xffffffffu, try_wait_long(addr, parity & 1u)) ||
            wait_on(addr, parity & 1u, &sh.abort, a.status, site);
   };
   auto arrive = [&](uint64_t& bar) {  // once for the warp

@@ -5,12 +5,18 @@
 
 #include "kv4.h"
 #include "ptx.h"
+#include "tc_issue.cuh"
 
 namespace sva {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFlight = 4;  // rows that a thread has in flight
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // V elements (8 or 4) of bf16 or fp32, as 32-bit floats and back. (Loads past L1:
 // under a programmatic launch the rows may be written while this grid is already
@@ -41,13 +47,13 @@ struct Chunk {
         reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
     }
   }
-  __device__ __forceinline__ void get(float (&f)[V]) const {
+  __device__ __forceinline__ void get(float* f) const {
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if constexpr (sizeof(T) == 4) f[i] = __uint_as_float(w[i]);
       else f[i] = __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
-  __device__ __forceinline__ void put(const float (&f)[V]) {
+  __device__ __forceinline__ void put(const float* f) {
 #pragma unroll
     for (int i = 0; i < kWords; ++i)
       if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[i]);
@@ -58,125 +64,179 @@ struct Chunk {
 // A segment of `width` lanes takes a head's row, each lane two chunks of V
 // elements: the two halves that rotate with each other, or neighbouring chunks when
 // neighbours do (and behind the rotated dims). So a pair's elements meet in one
-// lane, its angle's V cosines and sines stay in the lane's registers for all heads
-// of the token, and a head's sum of squares needs log2(width) exchanges. `parts`
-// warps share a token's heads.
-template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, int width) {
+// lane, and a head's sum of squares needs log2(width) exchanges. `parts` warps share a
+// token's heads, side by side: queries, keys, values (copied).
+//
+// Norm and rotation of a pair (a, b) with weights m, n are four products
+//   r (a (m c) - b (n s)),  r (b (n c) + a (m s)),
+// of which the four in brackets are the same for all heads of a side and token: a lane
+// makes them once and keeps them in registers, r is the row's 1 / sqrt(mean + eps).
+//
+// Bound by HBM: every row is read and written once.
+// FULL: every lane has two chunks and all of them turn.
+template <typename T, int V, bool INTER, bool FULL>
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeArgs a, int width) {
+  constexpr int kFlight = 4;  // rows that a lane has in flight
   const int lane = threadIdx.x & 31, l = lane & (width - 1), seg = lane / width, segs = 32 / width;
   const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const long long token = w / a.parts;
-  const int part = (int)(w - token * a.parts);
+  const int token = (int)(w >> a.parts_shift), part = (int)w & ((1 << a.parts_shift) - 1);
   pdl_wait();
   pdl_trigger();
   if (token >= a.n) return;
   const int pos = a.positions ? a.positions[token] : 0;
+  const int slot = a.k_pool ? a.slots[token] : 0;
   if (pos < 0 || (a.rot && pos >= a.max_pos)) {
     if (pos != -1 && lane == 0 && part == 0 && a.status) atomicOr(a.status, SV_FLAG_BAD_LENGTH);
     return;
   }
-  long long page = -1, off = 0;
-  if (a.k_pool) {
-    const int slot = a.slots[token];
-    if (slot >= 0) {
-      page = slot / a.blk;
-      off = slot - page * a.blk;
-    }
-    if (slot < -1 || page >= a.num_pages) {
-      if (lane == 0 && part == 0 && a.status) atomicOr(a.status, SV_FLAG_BAD_PAGE);
-      page = -1;
-    }
-  }
-  // the lane's chunks
+  const int page = slot < 0 ? -1 : slot / a.blk;
+  const bool stored = page >= 0 && page < a.num_pages;
+  if (a.k_pool && !stored && slot != -1 && lane == 0 && part == 0 && a.status) atomicOr(a.status, SV_FLAG_BAD_PAGE);
+  // the lane's chunks, and its pairs' cosines and sines
   const int chunks = a.d / V, half = INTER ? 0 : a.rot / (2 * V);
   const int c0 = INTER || l >= half ? 2 * l : l;
   const int c1 = INTER || l >= half ? 2 * l + 1 : l + half;
-  const bool has0 = c0 < chunks, has1 = c1 < chunks;
+  const bool has0 = FULL || c0 < chunks, has1 = FULL || c1 < chunks;
+  const int turning = FULL ? V : a.rot / 2 - l * V;  // pairs of the lane that turn (at most V)
   float cos[V], sin[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const int i = l * V + e;
-    const bool turns = i < a.rot / 2;
-    cos[e] = turns ? __ldcg(a.table + (long long)pos * a.rot + i) : 1.f;
-    sin[e] = turns ? __ldcg(a.table + (long long)pos * a.rot + a.rot / 2 + i) : 0.f;
+    cos[e] = 1.f;
+    sin[e] = 0.f;
   }
-  const int hq = a.q ? a.Hq : 0, hk = hq + a.Hkv, heads = a.v ? hk + a.Hkv : hk;
-  const T *q = static_cast<const T*>(a.q) + token * a.q_stride, *k = static_cast<const T*>(a.k) + token * a.k_stride,
-          *v = static_cast<const T*>(a.v) + token * a.v_stride;
-  const int step = segs * a.parts;
-  for (int h0 = part * segs + seg; h0 - seg < heads; h0 += step * kFlight) {
-    Chunk<T, V> x[kFlight][2];
-    T* to[kFlight];
+  if (turning > 0) {  // (four pairs at a time: rot is a multiple of 8)
+    const float* t = a.table + (long long)pos * a.rot + l * V;
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      const int h = h0 + f * step;
-      to[f] = nullptr;
-      if (h >= heads) continue;
-      const T* from;
-      if (h < hq) {
-        from = q + (long long)h * a.d;
-        to[f] = static_cast<T*>(a.q_out) + token * a.qo_stride + (long long)h * a.d;
+    for (int e = 0; e < V; e += 4)
+      if (e < turning) {
+        const float4 c = __ldcg(reinterpret_cast<const float4*>(t + e));
+        const float4 s = __ldcg(reinterpret_cast<const float4*>(t + a.rot / 2 + e));
+        cos[e] = c.x, cos[e + 1] = c.y, cos[e + 2] = c.z, cos[e + 3] = c.w;
+        sin[e] = s.x, sin[e + 1] = s.y, sin[e + 2] = s.z, sin[e + 3] = s.w;
+      }
+  }
+  // element i of the pair e: which of the lane's 2 V elements
+  auto first = [](int e) { return INTER ? 2 * e : e; };
+  auto second = [](int e) { return INTER ? 2 * e + 1 : e + V; };
+#pragma unroll 1
+  for (int side = 0; side < 3; ++side) {
+    const T* from;
+    T* to;
+    long long to_step = a.d;
+    int heads = a.Hkv;
+    const void* weight = nullptr;
+    if (side == 0) {
+      if (!a.q) continue;
+      from = static_cast<const T*>(a.q) + token * a.q_stride;
+      to = static_cast<T*>(a.q_out) + token * a.qo_stride;
+      heads = a.Hq;
+      weight = a.q_weight;
+    } else {
+      if (side == 2 && !a.v) break;
+      from = side == 1 ? static_cast<const T*>(a.k) + token * a.k_stride : static_cast<const T*>(a.v) + token * a.v_stride;
+      if (side == 1) weight = a.k_weight;
+      if (a.k_pool) {
+        if (!stored) break;
+        to_step = (long long)a.blk * a.d;
+        to = static_cast<T*>(side == 1 ? a.k_pool : a.v_pool) +
+             (page * (long long)a.Hkv * a.blk + (slot - page * a.blk)) * a.d;
       } else {
-        const bool is_v = h >= hk;
-        const int kh = h - (is_v ? hk : hq);
-        from = (is_v ? v : k) + (long long)kh * a.d;
-        if (!a.k_pool) to[f] = static_cast<T*>(a.k_out) + token * a.ko_stride + (long long)kh * a.d;
-        else if (page >= 0)
-          to[f] = static_cast<T*>(is_v ? a.v_pool : a.k_pool) + ((page * a.Hkv + kh) * a.blk + off) * a.d;
+        to = static_cast<T*>(a.k_out) + token * a.ko_stride;
       }
-      if (!to[f]) continue;
-      if (has0) x[f][0].load(from + c0 * V);
-      if (has1) x[f][1].load(from + c1 * V);
     }
+    // (two pairs' factors each)
+    uint64_t mc[V / 2], ns[V / 2], nc[V / 2], ms[V / 2];
+    if (side < 2) {
+      float m[2 * V];
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      const int h = h0 + f * step;
-      const bool turn = h < hk;
-      const void* weight = h < hq ? a.q_weight : a.k_weight;
-      float y0[V], y1[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) y0[e] = y1[e] = 0.f;
-      if (to[f] && has0) x[f][0].get(y0);
-      if (to[f] && has1) x[f][1].get(y1);
-      if (a.q_weight || a.k_weight) {  // (all lanes take part in the exchange)
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) sum += y0[e] * y0[e] + y1[e] * y1[e];
-        for (int o = width / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (weight && turn && to[f]) {
-          const float r = rsqrtf(sum / (float)a.d + a.eps);
-          Chunk<T, V> g;
-          float m[V];
-          if (has0) {
-            g.load(static_cast<const T*>(weight) + c0 * V);
-            g.get(m);
-#pragma unroll
-            for (int e = 0; e < V; ++e) y0[e] = y0[e] * r * m[e];
-          }
-          if (has1) {
-            g.load(static_cast<const T*>(weight) + c1 * V);
-            g.get(m);
-#pragma unroll
-            for (int e = 0; e < V; ++e) y1[e] = y1[e] * r * m[e];
-          }
+      for (int e = 0; e < 2 * V; ++e) m[e] = 1.f;
+      if (weight) {
+        Chunk<T, V> g;
+        if (has0) {
+          g.load(static_cast<const T*>(weight) + c0 * V);
+          g.get(m);
+        }
+        if (has1) {
+          g.load(static_cast<const T*>(weight) + c1 * V);
+          g.get(m + V);
         }
       }
-      if (!to[f]) continue;
-      if (turn) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          if (l * V + e >= a.rot / 2) continue;
-          float &p = INTER ? (2 * e < V ? y0[2 * e % V] : y1[2 * e % V]) : y0[e];
-          float &r = INTER ? (2 * e < V ? y0[(2 * e + 1) % V] : y1[(2 * e + 1) % V]) : y1[e];
-          const float p0 = p, r0 = r;
-          p = p0 * cos[e] - r0 * sin[e];
-          r = r0 * cos[e] + p0 * sin[e];
-        }
-        x[f][0].put(y0);
-        x[f][1].put(y1);
+      for (int e = 0; e < V; e += 2) {
+        const float m0 = m[first(e)], m1 = m[first(e + 1)], n0 = m[second(e)], n1 = m[second(e + 1)];
+        mc[e / 2] = pack2(m0 * cos[e], m1 * cos[e + 1]);
+        ms[e / 2] = pack2(m0 * sin[e], m1 * sin[e + 1]);
+        nc[e / 2] = pack2(n0 * cos[e], n1 * cos[e + 1]);
+        ns[e / 2] = pack2(-n0 * sin[e], -n1 * sin[e + 1]);
       }
-      if (has0) x[f][0].store(to[f] + c0 * V);
-      if (has1) x[f][1].store(to[f] + c1 * V);
+    }
+    const int step = segs << a.parts_shift;
+    const long long from_step = (long long)step * a.d, out_step = step * to_step;
+    const int apart = (c1 - c0) * V;  // of the lane's two chunks
+    from += (long long)(part * segs + seg) * a.d + c0 * V;
+    to += (part * segs + seg) * to_step + c0 * V;
+#pragma unroll 1
+    for (int h0 = part * segs; h0 < heads; h0 += step * kFlight) {
+      Chunk<T, V> x[kFlight][2];
+#pragma unroll
+      for (int f = 0; f < kFlight; ++f, from += from_step)
+        if (h0 + f * step + seg < heads) {
+          if (has0) x[f][0].load(from);
+          if (has1) x[f][1].load(from + apart);
+        }
+#pragma unroll
+      for (int f = 0; f < kFlight; ++f, to += out_step) {
+        if (h0 + f * step >= heads) break;  // (the same for all lanes)
+        if (side < 2) {
+          float y[2 * V];
+          x[f][0].get(y);
+          x[f][1].get(y + V);
+          uint64_t u[V / 2], v[V / 2];
+#pragma unroll
+          for (int e = 0; e < V; e += 2) {
+            u[e / 2] = pack2(y[first(e)], y[first(e + 1)]);
+            v[e / 2] = pack2(y[second(e)], y[second(e + 1)]);
+          }
+          uint64_t r = pack2(1.f, 1.f);
+          if (weight) {  // (all lanes take part in the exchange, a head's among themselves)
+            float sum = 0.f;
+            if (FULL) {
+              uint64_t s2 = 0;
+#pragma unroll
+              for (int e = 0; e < V / 2; ++e) s2 = fma2(v[e], v[e], fma2(u[e], u[e], s2));
+              const float2 t = unpack2(s2);
+              sum = t.x + t.y;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 2 * V; ++e) sum += (e < V ? has0 : has1) ? y[e] * y[e] : 0.f;
+            }
+            for (int o = width / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const float inv = rsqrtf(sum * a.inv_d + a.eps);
+            r = pack2(inv, inv);
+          }
+#pragma unroll
+          for (int e = 0; e < V; e += 2) {
+            // (a dim that does not turn takes nothing of another, which may be infinite;
+            // pairs turn or do not in fours)
+            uint64_t p = mul2(u[e / 2], mc[e / 2]), q = mul2(v[e / 2], nc[e / 2]);
+            if (FULL || turning > 0) {
+              p = fma2(v[e / 2], ns[e / 2], p);
+              q = fma2(u[e / 2], ms[e / 2], q);
+            }
+            const float2 pp = unpack2(mul2(p, r)), qq = unpack2(mul2(q, r));
+            y[first(e)] = pp.x;
+            y[first(e + 1)] = pp.y;
+            y[second(e)] = qq.x;
+            y[second(e + 1)] = qq.y;
+          }
+          x[f][0].put(y);
+          x[f][1].put(y + V);
+        }
+        if (h0 + f * step + seg < heads) {
+          if (has0) x[f][0].store(to);
+          if (has1) x[f][1].store(to + apart);
+        }
+      }
     }
   }
 }
@@ -186,22 +246,22 @@ cudaError_t launch(RopeArgs a, cudaStream_t st) {
   const int lanes = (a.d / V + 1) / 2;
   int width = 1;
   while (width < lanes) width <<= 1;
-  const int heads = (a.q ? a.Hq : 0) + a.Hkv + (a.v ? a.Hkv : 0);
-  const int rounds = std::max(1, (heads * width + 31) / 32);  // of a warp alone with a token
-  // One warp a token for many tokens; for few, as many as the heads give work, so that
-  // a decoding step's loads are all in flight at once.
-  a.parts = 1;
-  while (a.parts < rounds && (long long)a.n * a.parts < 152 * 32) a.parts *= 2;
-  const long long warps = (long long)a.n * a.parts;
-  return launch_pdl(rope_kernel<T, V, INTER>, dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32))),
+  const int heads = std::max(a.q ? a.Hq : 0, a.Hkv);
+  // One warp a token for many tokens; for few, as many as a side's heads give work, so
+  // that a decoding step's loads are all in flight at once.
+  a.parts_shift = 0;
+  while ((32 << a.parts_shift) < heads * width && ((long long)a.n << a.parts_shift) < 152 * 32)
+    ++a.parts_shift;
+  a.inv_d = 1.f / (float)a.d;
+  const long long warps = (long long)a.n << a.parts_shift;
+  const bool full = a.rot == a.d && a.d == 2 * V * width;
+  return launch_pdl(full ? rope_kernel<T, V, INTER, true> : rope_kernel<T, V, INTER, false>, dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32))),
                     dim3(kThreads), 0, st, a, width);
 }
 
 template <typename T>
 cudaError_t launch_as(const RopeArgs& a, cudaStream_t st) {
-  // 8 elements a chunk where both halves are whole chunks, else 4
-  if (a.interleaved) return launch<T, 8, true>(a, st);
-  return a.rot % 16 == 0 ? launch<T, 8, false>(a, st) : launch<T, 4, false>(a, st);
+  return a.interleaved ? launch<T, 4, true>(a, st) : launch<T, 4, false>(a, st);
 }
 
 }  // namespace

@@ -124,7 +124,8 @@ def test_sequence_refusals(L, bad, status, word):
 
 
 @pytest.mark.parametrize("kw,word", [(dict(d=24), "multiple of 16"), (dict(blk=24), "multiple of 16"),
-                                     (dict(d=272), "head dim"), (dict(T=65), "T=65")])
+                                     (dict(d=272), "head dim"), (dict(T=65), "T=65"),
+                                     (dict(Hq=4097, Hkv=4097), "exceed"), (dict(B=65536), "exceed")])
 def test_shapes_without_a_4bit_cache(L, kw, word):
     s = shape(**kw)
     for f, args in calls4(L, s, kv4()):
