@@ -146,30 +146,6 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
     }
     // (two pairs' factors each)
     uint64_t mc[V / 2], ns[V / 2], nc[V / 2], ms[V / 2];
-    if (side < 2) {
-      float m[2 * V];
-#pragma unroll
-      for (int e = 0; e < 2 * V; ++e) m[e] = 1.f;
-      if (weight) {
-        Chunk<T, V> g;
-        if (has0) {
-          g.load(static_cast<const T*>(weight) + c0 * V);
-          g.get(m);
-        }
-        if (has1) {
-          g.load(static_cast<const T*>(weight) + c1 * V);
-          g.get(m + V);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < V; e += 2) {
-        const float m0 = m[first(e)], m1 = m[first(e + 1)], n0 = m[second(e)], n1 = m[second(e + 1)];
-        mc[e / 2] = pack2(m0 * cos[e], m1 * cos[e + 1]);
-        ms[e / 2] = pack2(m0 * sin[e], m1 * sin[e + 1]);
-        nc[e / 2] = pack2(n0 * cos[e], n1 * cos[e + 1]);
-        ns[e / 2] = pack2(-n0 * sin[e], -n1 * sin[e + 1]);
-      }
-    }
     const int step = segs << a.parts_shift;
     const long long from_step = (long long)step * a.d, out_step = step * to_step;
     const int apart = (c1 - c0) * V;  // of the lane's two chunks
@@ -184,6 +160,49 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
           if (has0) x[f][0].load(from);
           if (has1) x[f][1].load(from + apart);
         }
+      if (side < 2 && h0 == part * segs) {  // (behind the first loads, which wait for neither angles nor weights)
+        float m[2 * V];
+#pragma unroll
+        for (int e = 0; e < 2 * V; ++e) m[e] = 1.f;
+        if (weight) {
+          Chunk<T, V> g;
+          if (has0) {
+            g.load(static_cast<const T*>(weight) + c0 * V);
+            g.get(m);
+          }
+          if (has1) {
+            g.load(static_cast<const T*>(weight) + c1 * V);
+            g.get(m + V);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          const float m0 = m[first(e)], m1 = m[first(e + 1)], n0 = m[second(e)], n1 = m[second(e + 1)];
+          mc[e / 2] = pack2(m0 * cos[e], m1 * cos[e + 1]);
+          ms[e / 2] = pack2(m0 * sin[e], m1 * sin[e + 1]);
+          nc[e / 2] = pack2(n0 * cos[e], n1 * cos[e + 1]);
+          ns[e / 2] = pack2(-n0 * sin[e], -n1 * sin[e + 1]);
+        }
+      }
+      // 1 / sqrt of the rows' mean squares: the rows' exchanges side by side (one row after
+      // the other, with its rotation in between, took 78 us where this takes 73: 20,011 rows of 36 heads)
+      float inv[kFlight];
+      if (weight) {
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+          float y[2 * V], sum = 0.f;
+          x[f][0].get(y);
+          x[f][1].get(y + V);
+#pragma unroll
+          for (int e = 0; e < 2 * V; ++e) sum += FULL || (e < V ? has0 : has1) ? y[e] * y[e] : 0.f;
+          inv[f] = sum;
+        }
+        for (int o = width / 2; o; o >>= 1)
+#pragma unroll
+          for (int f = 0; f < kFlight; ++f) inv[f] += __shfl_xor_sync(0xffffffffu, inv[f], o);
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) inv[f] = rsqrtf(inv[f] * a.inv_d + a.eps);
+      }
 #pragma unroll
       for (int f = 0; f < kFlight; ++f, to += out_step) {
         if (h0 + f * step >= heads) break;  // (the same for all lanes)
@@ -197,23 +216,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
             u[e / 2] = pack2(y[first(e)], y[first(e + 1)]);
             v[e / 2] = pack2(y[second(e)], y[second(e + 1)]);
           }
-          uint64_t r = pack2(1.f, 1.f);
-          if (weight) {  // (all lanes take part in the exchange, a head's among themselves)
-            float sum = 0.f;
-            if (FULL) {
-              uint64_t s2 = 0;
-#pragma unroll
-              for (int e = 0; e < V / 2; ++e) s2 = fma2(v[e], v[e], fma2(u[e], u[e], s2));
-              const float2 t = unpack2(s2);
-              sum = t.x + t.y;
-            } else {
-#pragma unroll
-              for (int e = 0; e < 2 * V; ++e) sum += (e < V ? has0 : has1) ? y[e] * y[e] : 0.f;
-            }
-            for (int o = width / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float inv = rsqrtf(sum * a.inv_d + a.eps);
-            r = pack2(inv, inv);
-          }
+          const uint64_t r = weight ? pack2(inv[f], inv[f]) : pack2(1.f, 1.f);
 #pragma unroll
           for (int e = 0; e < V; e += 2) {
             // (a dim that does not turn takes nothing of another, which may be infinite;
