@@ -54,6 +54,16 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
   return r;
 }
+// r[0 .. 8) times half H of s (the multiplication picks the half itself).
+template <int H>
+__device__ __forceinline__ void scale_f16x2(uint32_t* r, uint32_t s) {
+  const __half2 ss = *reinterpret_cast<const __half2*>(&s), f = H ? __high2half2(ss) : __low2half2(ss);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&r[e]), f);
+    r[e] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+}
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t x) {
   return __half22float2(*reinterpret_cast<const __half2*>(&x));
 }

@@ -47,9 +47,11 @@ struct Rows4Args {
   unsigned* status;              // may be null
   long long k_stride, v_stride;  // elements
   int n, Hkv, d, blk, num_pages;
+  int heads;                     // of a block (set by the launch)
+  int wide;                      // rows lie on 32-byte boundaries (set by the launch)
 };
-cudaError_t launch_write_kv4(const Rows4Args& a, int dtype, cudaStream_t st);
-cudaError_t launch_read_kv4(const Rows4Args& a, int dtype, cudaStream_t st);
+cudaError_t launch_write_kv4(Rows4Args a, int dtype, cudaStream_t st);
+cudaError_t launch_read_kv4(Rows4Args a, int dtype, cudaStream_t st);
 
 struct Reps4Args {
   const uint8_t* k_pool;

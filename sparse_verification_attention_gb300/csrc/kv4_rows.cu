@@ -10,71 +10,88 @@ using namespace kv4;
 constexpr int kThreads = 256;
 constexpr int kGroup = 16;  // dims that share a scale
 
-// 16 elements of bf16 or fp32.
+// 16 elements of bf16 or fp32, in 32-byte accesses where the rows allow it (`wide`): in two
+// halves every sector is asked for, or written, twice.
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
-  constexpr int kVecs = (int)sizeof(T);  // 16-byte vectors
+__device__ __forceinline__ void load16(const T* p, bool wide, float (&x)[16]) {
+  uint32_t w[4 * sizeof(T)];
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p) + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if constexpr (sizeof(T) == 4) {
-        x[4 * i + j] = __uint_as_float(w[j]);
-      } else {
-        x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-        x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
+  for (int i = 0; i < (int)sizeof(T); i += 2) {
+    uint32_t* v = w + 4 * i;
+    const uint4* q = reinterpret_cast<const uint4*>(p) + i;
+    if (wide) {
+      asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                   : "l"(q));
+    } else {
+      const uint4 a = __ldcg(q), b = __ldcg(q + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
   }
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if constexpr (sizeof(T) == 4) x[i] = __uint_as_float(w[i]);
+    else x[i] = __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
 }
 template <typename T>
-__device__ __forceinline__ void store16(T* p, const float (&x)[16]) {
+__device__ __forceinline__ void store16(T* p, bool wide, const float (&x)[16]) {
+  uint32_t w[4 * sizeof(T)];
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T); ++i) {
-    uint32_t w[4];
+  for (int i = 0; i < (int)(4 * sizeof(T)); ++i)
+    if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(x[i]);
+    else w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(x[4 * i + j]);
-      else w[j] = pack_bf16(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
-    reinterpret_cast<uint4*>(p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < (int)sizeof(T); i += 2) {
+    const uint32_t* v = w + 4 * i;
+    uint4* q = reinterpret_cast<uint4*>(p) + i;
+    if (wide) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                   "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                   : "memory");
+    } else {
+      q[0] = make_uint4(v[0], v[1], v[2], v[3]);
+      q[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
   }
 }
 
-// A lane has one group of one token's head; a warp 16 tokens and two neighbouring
-// groups, so that rows are read in runs of 64 bytes, K codes written in runs of 128
-// and the bytes of a V code row in runs of 16 when the tokens' slots follow each
-// other (nothing depends on it). Blocks: 16 tokens (x), eight pairs of groups (y): those
-// of K, then those of V.
+// A lane has one group of one token, in `heads` heads one after the other; a warp 16
+// tokens and two neighbouring groups, so that rows are read in runs of 64 bytes, K codes
+// written in runs of 128 and the bytes of a V code row in runs of 16 when the tokens'
+// slots follow each other (nothing depends on it). Blocks: 16 tokens (x), four pairs of
+// groups of K and of V, or less (y), heads (z). Places are worked out once for all heads:
+// one head a lane, with its divisions, took 347 instructions a group.
 struct Place {
-  int token, h, g, is_v, tok;
-  uint8_t* piece;  // null: nothing to do
+  int token, g, is_v, tok, h0, h1;
+  long long step;  // from a head's piece to the next head's
+  uint8_t* piece;  // of head h0; null: nothing to do
 };
+constexpr int kPairs = 4;  // pairs of groups of one side in a block
 __device__ __forceinline__ Place place_of(const Rows4Args& a) {
-  const int lane = threadIdx.x & 31;
-  const int groups = a.d / kGroup, cols = a.Hkv * groups;
-  int col = (blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5)) * 2 + (lane & 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = a.d / kGroup;
   Place p;
   p.token = blockIdx.x * 16 + (lane >> 1);
-  p.is_v = col >= cols;
-  col -= p.is_v ? cols : 0;
-  p.h = (unsigned)col / (unsigned)groups;
-  p.g = col - p.h * groups;
+  p.is_v = warp >= kPairs;
+  p.g = (blockIdx.y * kPairs + warp % kPairs) * 2 + (lane & 1);
+  p.h0 = blockIdx.z * a.heads;
+  p.h1 = min(p.h0 + a.heads, a.Hkv);
   p.piece = nullptr;
   p.tok = 0;
+  p.step = (long long)(a.blk / kPiece) * piece_bytes(a.d);
   pdl_wait();
   pdl_trigger();
-  if (p.token >= a.n || col >= cols) return p;
+  if (p.token >= a.n || p.g >= groups) return p;
   const int slot = a.slots[p.token];
   const int page = slot < 0 ? -1 : (int)((unsigned)slot / (unsigned)a.blk);
   if (page < 0 || page >= a.num_pages) {
-    if (slot != -1 && p.h == 0 && p.g == 0 && a.status) atomicOr(a.status, SV_FLAG_BAD_PAGE);
+    if (slot != -1 && p.h0 == 0 && p.g == 0 && a.status) atomicOr(a.status, SV_FLAG_BAD_PAGE);
     return p;
   }
   const int in = slot - page * a.blk;
   p.tok = in % kPiece;
-  p.piece = (p.is_v ? a.v_pool : a.k_pool) +
-            (((long long)page * a.Hkv + p.h) * (a.blk / kPiece) + in / kPiece) * piece_bytes(a.d);
+  p.piece = (p.is_v ? a.v_pool : a.k_pool) + ((long long)page * a.Hkv + p.h0) * p.step +
+            (in / kPiece) * piece_bytes(a.d);
   return p;
 }
 
@@ -85,101 +102,105 @@ __device__ __forceinline__ Place place_of(const Rows4Args& a) {
 // place at least, 2^-23 / 1.875 relatively, and the quotient by more than half a unit. x times
 // the reciprocal is off by up to two units; one step of Newton's on the quotient, whose
 // remainder x - q s the fma gives exactly, leaves 2^-45 before the last rounding.
-// (A division each took 550 instructions a group, 33 us for 13,343 rows of 8 heads.)
+// (With a division each a group took 550 instructions, and 13,343 rows of 8 heads 33 us.)
+template <typename T, bool IS_V>
+__device__ __forceinline__ void write_groups(const Rows4Args& a, const Place& p) {
+  const T* from = static_cast<const T*>(IS_V ? a.v : a.k) + p.token * (IS_V ? a.v_stride : a.k_stride) +
+                  (long long)p.h0 * a.d + p.g * kGroup;
+  uint8_t *codes = p.piece + p.g * 128 + (IS_V ? p.tok : p.tok * 8),
+          *scale = p.piece + 8 * a.d + (IS_V ? p.g * 16 + p.tok : p.tok * (a.d / kGroup) + p.g);
+#pragma unroll 2
+  for (int h = p.h0; h < p.h1; ++h, from += a.d, codes += p.step, scale += p.step) {
+    float x[16];
+    load16(from, a.wide, x);
+    const int e = head_exp(IS_V ? a.v_exp : a.k_exp, h);
+    uint32_t top = 0;  // magnitudes compare as integers, a NaN's above all
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    const float amax = __uint_as_float(top) * exp2i(-e);
+    const uint32_t sb = top > 0x7f800000u ? 0x7fu : f32_to_e4m3(__fdiv_rn(amax, 6.f));
+    const float s = e4m3_to_f32(sb) * exp2i(e);
+    if (amax > 6.5f * 448.f) {  // beyond the largest code: no infinities below
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -8.f * s), 8.f * s);
+    }
+    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float q = x[i] * r;
+      x[i] = __fmaf_rn(__fmaf_rn(-q, s, x[i]), r, q);
+    }
+    if (IS_V) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) codes[j * 16] = (uint8_t)f32x2_to_e2m1x2(x[j], x[j + 8]);
+    } else {
+      uint32_t c[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = f32x2_to_e2m1x2(x[2 * j], x[2 * j + 1]);
+      const uint32_t lo = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, hi = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
+      *reinterpret_cast<uint2*>(codes) = make_uint2(lo, hi);
+    }
+    *scale = (uint8_t)sb;
+  }
+}
 template <typename T>
 __global__ void __launch_bounds__(kThreads) write_kv4_kernel(const __grid_constant__ Rows4Args a) {
   const Place p = place_of(a);
   if (!p.piece) return;
-  float x[16];
-  load16(static_cast<const T*>(p.is_v ? a.v : a.k) + p.token * (p.is_v ? a.v_stride : a.k_stride) +
-             (long long)p.h * a.d + p.g * kGroup,
-         x);
-  const int e = head_exp(p.is_v ? a.v_exp : a.k_exp, p.h);
-  uint32_t top = 0;  // magnitudes compare as integers, a NaN's above all
-#pragma unroll
-  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-  const float amax = __uint_as_float(top) * exp2i(-e);
-  const uint32_t sb = top > 0x7f800000u ? 0x7fu : f32_to_e4m3(__fdiv_rn(amax, 6.f));
-  const float s = e4m3_to_f32(sb) * exp2i(e);
-  if (amax > 6.5f * 448.f) {  // beyond the largest code: no infinities below
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -8.f * s), 8.f * s);
-  }
-  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-  uint32_t c[8];  // dims 2 j, 2 j + 1 of K, j, j + 8 of V
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float q = x[i] * r;
-    x[i] = __fmaf_rn(__fmaf_rn(-q, s, x[i]), r, q);
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) c[j] = p.is_v ? f32x2_to_e2m1x2(x[j], x[j + 8]) : f32x2_to_e2m1x2(x[2 * j], x[2 * j + 1]);
-  uint8_t* codes = p.piece + p.g * 128;
-  if (p.is_v) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) codes[j * 16 + p.tok] = (uint8_t)c[j];
-    p.piece[8 * a.d + p.g * 16 + p.tok] = (uint8_t)sb;
-  } else {
-    const uint32_t lo = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, hi = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
-    *reinterpret_cast<uint2*>(codes + p.tok * 8) = make_uint2(lo, hi);
-    p.piece[8 * a.d + p.tok * (a.d / kGroup) + p.g] = (uint8_t)sb;
-  }
+  if (p.is_v) write_groups<T, true>(a, p);
+  else write_groups<T, false>(a, p);
 }
 
+template <typename T, bool IS_V>
+__device__ __forceinline__ void read_groups(const Rows4Args& a, const Place& p) {
+  T* to = static_cast<T*>(IS_V ? a.v_out : a.k_out) + p.token * (IS_V ? a.v_stride : a.k_stride) +
+          (long long)p.h0 * a.d + p.g * kGroup;
+  const uint8_t *codes = p.piece + p.g * 128 + (IS_V ? p.tok : p.tok * 8),
+                *scale = p.piece + 8 * a.d + (IS_V ? p.g * 16 + p.tok : p.tok * (a.d / kGroup) + p.g);
+#pragma unroll 2
+  for (int h = p.h0; h < p.h1; ++h, to += a.d, codes += p.step, scale += p.step) {
+    uint32_t w[2], f16[8];
+    const float s = e4m3_to_f32(__ldcg(scale)) * exp2i(head_exp(IS_V ? a.v_exp : a.k_exp, h));
+    if (IS_V) {
+      uint32_t c[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = __ldcg(codes + j * 16);
+      w[0] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+      w[1] = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
+    } else {
+      const uint2 v = __ldcg(reinterpret_cast<const uint2*>(codes));
+      w[0] = v.x;
+      w[1] = v.y;
+    }
+    e2m1x8_to_f16(w[0], f16);
+    e2m1x8_to_f16(w[1], f16 + 4);
+    float x[16];  // (V: byte j holds dims j and j + 8)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 f = f16x2_to_f32(f16[j]);
+      x[IS_V ? j : 2 * j] = f.x * s;
+      x[IS_V ? j + 8 : 2 * j + 1] = f.y * s;
+    }
+    store16(to, a.wide, x);
+  }
+}
 template <typename T>
 __global__ void __launch_bounds__(kThreads) read_kv4_kernel(const __grid_constant__ Rows4Args a) {
   const Place p = place_of(a);
   if (!p.piece) return;
-  const uint8_t* codes = p.piece + p.g * 128;
-  uint32_t w[2], h[8];
-  const uint32_t sb = __ldcg(p.piece + 8 * a.d + (p.is_v ? p.g * 16 + p.tok : p.tok * (a.d / kGroup) + p.g));
-  if (p.is_v) {
-    uint32_t c[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = __ldcg(codes + j * 16 + p.tok);
-    w[0] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
-    w[1] = c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24;
-  } else {
-    const uint2 v = __ldcg(reinterpret_cast<const uint2*>(codes + p.tok * 8));
-    w[0] = v.x;
-    w[1] = v.y;
-  }
-  e2m1x8_to_f16(w[0], h);
-  e2m1x8_to_f16(w[1], h + 4);
-  const float s = e4m3_to_f32(sb) * exp2i(head_exp(p.is_v ? a.v_exp : a.k_exp, p.h));
-  float x[16];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float2 f = f16x2_to_f32(h[j]);
-    x[2 * j] = f.x * s;
-    x[2 * j + 1] = f.y * s;
-  }
-  if (p.is_v) {  // dims j, j + 8 stand side by side
-    float y[16];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = x[2 * j], y[j + 8] = x[2 * j + 1];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = y[j];
-  }
-  store16(static_cast<T*>(p.is_v ? a.v_out : a.k_out) + p.token * (p.is_v ? a.v_stride : a.k_stride) +
-              (long long)p.h * a.d + p.g * kGroup,
-          x);
-}
-
-// x += the halves of h (low, high) times the half s, in fp32.
-__device__ __forceinline__ void fma_f32_f16x2(float& x, float& y, uint32_t h, uint16_t s) {
-  asm("{\n\t.reg .b16 a, b;\n\t"
-      "mov.b32 {a, b}, %2;\n\t"
-      "fma.rn.f32.f16 %0, a, %3, %0;\n\t"
-      "fma.rn.f32.f16 %1, b, %3, %1;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "r"(h), "h"(s));
+  if (p.is_v) read_groups<T, true>(a, p);
+  else read_groups<T, false>(a, p);
 }
 
 // One warp per (sequence, head, block): a lane has a group of 4 tokens of every piece (so
 // 16 sums), `gp` lanes side by side the groups (those of d > 128 in two rounds). The four
 // token subsets are folded at the end, always in the same order.
-// Bound by HBM, and nearly as much by issue: the products are fp32 sums of halves.
+//
+// Code times scale is exact in f16. What costs is to sum halves in fp32: a conversion each
+// and an addition, 62 us for 5,102 blocks of 8 heads. A product with the identity does it
+// instead: in m16n8k8 a lane's two A registers lie at the same rows and columns as its four
+// sums, so S += A I adds the four halves to the lane's own sums. (A NaN reaches the sums in
+// its row of 4 lanes, which are the same dims of the group's other tokens.)
 __global__ void __launch_bounds__(kThreads) reps_kv4_kernel(const __grid_constant__ Reps4Args a) {
   const int lane = threadIdx.x & 31, sub = lane & 3;
   const int jb = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -200,37 +221,45 @@ __global__ void __launch_bounds__(kThreads) reps_kv4_kernel(const __grid_constan
   const int groups = a.d / kGroup, pb = piece_bytes(a.d), pieces = a.blk / kPiece;
   const uint8_t* p = a.k_pool + ((long long)page * a.Hkv + h) * pieces * pb;
   const float unit = __fdiv_rn(exp2i(head_exp(a.k_exp, h)), (float)a.blk);
+  // B: rows 2 sub and 2 sub + 1 of column lane / 4
+  const uint32_t identity = (lane >> 2 == 2 * sub ? 0x3c00u : 0u) | (lane >> 2 == 2 * sub + 1 ? 0x3c000000u : 0u);
   float* to = a.reps + (((long long)b * a.Hkv + h) * a.nb_max + j) * a.d;
 #pragma unroll 1
   for (int g0 = 0; g0 < groups; g0 += 8) {
     const int g = g0 + (lane >> 2);
     const bool on = g < groups;
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.f;
-    if (on) {
-      const uint8_t *codes = p + g * 128 + sub * 32, *scales = p + 8 * a.d + sub * 4 * groups + g;
+    float sum[4][4] = {};  // dims 4 i .. 4 i + 3
+    const uint8_t *codes = p + g * 128 + sub * 32, *scales = p + 8 * a.d + sub * 4 * groups + g;
 #pragma unroll 2
-      for (int t = 0; t < pieces; ++t, codes += pb, scales += pb) {
-        const uint4 c[2] = {__ldcg(reinterpret_cast<const uint4*>(codes)), __ldcg(reinterpret_cast<const uint4*>(codes) + 1)};
-        const uint32_t sc = __ldcg(scales) | __ldcg(scales + groups) << 8 | __ldcg(scales + 2 * groups) << 16 |
-                            (uint32_t)__ldcg(scales + 3 * groups) << 24;
-        uint32_t s[2];
-        e4m3x4_to_f16(sc, s[0], s[1]);
+    for (int t = 0; t < pieces; ++t, codes += pb, scales += pb) {
+      uint4 c[2] = {};
+      uint32_t sc = 0, s[2];
+      if (on) {
+        c[0] = __ldcg(reinterpret_cast<const uint4*>(codes));
+        c[1] = __ldcg(reinterpret_cast<const uint4*>(codes) + 1);
+        sc = __ldcg(scales) | __ldcg(scales + groups) << 8 | __ldcg(scales + 2 * groups) << 16 |
+             (uint32_t)__ldcg(scales + 3 * groups) << 24;
+      }
+      e4m3x4_to_f16(sc, s[0], s[1]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t w0 = k % 2 ? c[k / 2].z : c[k / 2].x, w1 = k % 2 ? c[k / 2].w : c[k / 2].y;
-          uint32_t f[8];
-          e2m1x8_to_f16(w0, f);
-          e2m1x8_to_f16(w1, f + 4);
-          const uint16_t sk = (uint16_t)(k % 2 ? s[k / 2] >> 16 : s[k / 2]);
+      for (int k = 0; k < 4; ++k) {
+        uint32_t f[8];
+        e2m1x8_to_f16(k % 2 ? c[k / 2].z : c[k / 2].x, f);
+        e2m1x8_to_f16(k % 2 ? c[k / 2].w : c[k / 2].y, f + 4);
+        if (k % 2) scale_f16x2<1>(f, s[k / 2]);
+        else scale_f16x2<0>(f, s[k / 2]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) fma_f32_f16x2(x[2 * i], x[2 * i + 1], f[i], sk);
-        }
+        for (int i = 0; i < 4; ++i)
+          asm volatile(
+              "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+              : "+f"(sum[i][0]), "+f"(sum[i][1]), "+f"(sum[i][2]), "+f"(sum[i][3])
+              : "r"(f[2 * i]), "r"(f[2 * i + 1]), "r"(identity));
       }
     }
     // fold: the lane keeps 4 of the 16 sums of its group
-    float y[4];
+    float x[16], y[4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = sum[i / 4][i % 4];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       x[i] += __shfl_xor_sync(0xffffffffu, x[i], 1);
@@ -243,23 +272,35 @@ __global__ void __launch_bounds__(kThreads) reps_kv4_kernel(const __grid_constan
   }
 }
 
-dim3 row_grid(const Rows4Args& a) {
-  const int pairs = a.Hkv * (a.d / kGroup);  // K and V: two groups each
-  return dim3((unsigned)((a.n + 15ll) / 16), (unsigned)((pairs + kThreads / 32 - 1) / (kThreads / 32)));
+bool wide_rows(const void* p, long long stride, int elt) {
+  return reinterpret_cast<uintptr_t>(p) % 32 == 0 && stride * elt % 32 == 0;
+}
+
+// Many tokens: all heads in one block; few: heads in as many blocks as the GPU takes.
+dim3 row_grid(Rows4Args* a) {
+  const unsigned x = (unsigned)((a->n + 15ll) / 16), y = (unsigned)((a->d / kGroup + 2 * kPairs - 1) / (2 * kPairs));
+  int z = 1;
+  while (z < a->Hkv && (long long)x * y * z < 8 * 152) z *= 2;
+  a->heads = (a->Hkv + z - 1) / z;
+  return dim3(x, y, (unsigned)((a->Hkv + a->heads - 1) / a->heads));
 }
 
 }  // namespace
 
-cudaError_t launch_write_kv4(const Rows4Args& a, int dtype, cudaStream_t st) {
-  const dim3 block(kThreads);
-  return dtype == SV_BF16 ? launch_pdl(write_kv4_kernel<__nv_bfloat16>, row_grid(a), block, 0, st, a)
-                          : launch_pdl(write_kv4_kernel<float>, row_grid(a), block, 0, st, a);
+cudaError_t launch_write_kv4(Rows4Args a, int dtype, cudaStream_t st) {
+  const dim3 grid = row_grid(&a), block(kThreads);
+  const int elt = dtype == SV_BF16 ? 2 : 4;
+  a.wide = wide_rows(a.k, a.k_stride, elt) && wide_rows(a.v, a.v_stride, elt);
+  return dtype == SV_BF16 ? launch_pdl(write_kv4_kernel<__nv_bfloat16>, grid, block, 0, st, a)
+                          : launch_pdl(write_kv4_kernel<float>, grid, block, 0, st, a);
 }
 
-cudaError_t launch_read_kv4(const Rows4Args& a, int dtype, cudaStream_t st) {
-  const dim3 block(kThreads);
-  return dtype == SV_BF16 ? launch_pdl(read_kv4_kernel<__nv_bfloat16>, row_grid(a), block, 0, st, a)
-                          : launch_pdl(read_kv4_kernel<float>, row_grid(a), block, 0, st, a);
+cudaError_t launch_read_kv4(Rows4Args a, int dtype, cudaStream_t st) {
+  const dim3 grid = row_grid(&a), block(kThreads);
+  const int elt = dtype == SV_BF16 ? 2 : 4;
+  a.wide = wide_rows(a.k_out, a.k_stride, elt) && wide_rows(a.v_out, a.v_stride, elt);
+  return dtype == SV_BF16 ? launch_pdl(read_kv4_kernel<__nv_bfloat16>, grid, block, 0, st, a)
+                          : launch_pdl(read_kv4_kernel<float>, grid, block, 0, st, a);
 }
 
 cudaError_t launch_reps_kv4(const Reps4Args& a, cudaStream_t st) {

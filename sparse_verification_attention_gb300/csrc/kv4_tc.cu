@@ -113,16 +113,6 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// r[0 .. 8) times half H of s (the multiplication picks the half itself).
-template <int H>
-__device__ __forceinline__ void scale_f16x2(uint32_t* r, uint32_t s) {
-  const __half2 ss = *reinterpret_cast<const __half2*>(&s), f = H ? __high2half2(ss) : __low2half2(ss);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&r[e]), f);
-    r[e] = *reinterpret_cast<const uint32_t*>(&x);
-  }
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

@@ -7,7 +7,8 @@ Rotation: an output a c - b s of normed elements a, b takes two products and a s
 by d u, halved by the root, and the division, root and sums around it by less than
 8 u. Together (d / 2 + 16) u of |a c| + |b s|, and half a step of the output's type.
 4-bit values: the rounding is defined bit by bit and the values are exact.
-Representatives: blk - 1 sums and a division, (blk + 1) u of the mean of |x|.
+Representatives: blk sums on the tensor cores, which may cut off instead of rounding (a
+whole step, 2 u, each), and a factor: (2 blk + 2) u of the mean of |x|.
 Attention: as in paged_util.attend for the scores, weights, sums and the division;
 scores may be summed with whole steps (2 u) on the tensor cores. There a weight is
 rounded to f16, 2^-11 of it, and below f16's normal range by half a step of 2^-24 at

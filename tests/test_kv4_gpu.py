@@ -175,7 +175,7 @@ def test_reps(lens, old, Hkv, d, blk):
             for j in range(j0, min(n // blk, j0 + cut)):
                 x = k[b][j * blk:(j + 1) * blk]
                 want[b, :, j] = x.mean(0)
-                tol[b, :, j] = (blk + 1) * U.U * x.abs().mean(0)
+                tol[b, :, j] = (2 * blk + 2) * U.U * x.abs().mean(0)
         U.check(reps.cpu(), want, tol)
 
 
