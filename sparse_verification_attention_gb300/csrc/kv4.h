@@ -94,6 +94,7 @@ struct Attend4Args {
   int rows, row_tiles;  // rows of a row tile (of all but the last), row tiles of a (b, h)
   int streams;    // 2: a segment's even and odd tiles are summed apart
   int ppb, ppt, ppt_shift;  // pieces of a block and of a key tile (a power of two)
+  int ppb_shift;            // log2(ppb), -1 if it is no power of two
   int ctas;
   float scale_log2;  // log2(e) / sqrt(d)
   unsigned long long anc[kMaxT];

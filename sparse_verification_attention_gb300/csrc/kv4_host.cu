@@ -354,6 +354,7 @@ sv_status sv_attend_kv4(const sv_shape* shape, const void* q, const sv_kv4* kv, 
   a.n_sel = n_sel;
   a.sel_stride = sel_stride;
   a.ppb = shape->blk / kPiece;
+  a.ppb_shift = a.ppb & (a.ppb - 1) ? -1 : __builtin_ctz(a.ppb);
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)shape->d));
   fill_ancestors(draft_parent, shape->T, a.anc);
   const cudaError_t e = attend4_tc_applies(a, shape->dtype) ? launch_attend4_tc(a, (cudaStream_t)stream)

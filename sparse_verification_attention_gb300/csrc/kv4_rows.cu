@@ -200,8 +200,9 @@ __global__ void __launch_bounds__(kThreads) read_kv4_kernel(const __grid_constan
 // and an addition, 62 us for 5,102 blocks of 8 heads. A product with the identity does it
 // instead: in m16n8k8 a lane's two A registers lie at the same rows and columns as its four
 // sums, so S += A I adds the four halves to the lane's own sums. (A NaN reaches the sums in
-// its row of 4 lanes, which are the same dims of the group's other tokens.)
-__global__ void __launch_bounds__(kThreads) reps_kv4_kernel(const __grid_constant__ Reps4Args a) {
+// its row of 4 lanes, which are the same dims of the group's other tokens.) Six CTAs an SM, a
+// piece at a time, 51.6 us; three, two pieces at a time, 67.
+__global__ void __launch_bounds__(kThreads, 6) reps_kv4_kernel(const __grid_constant__ Reps4Args a) {
   const int lane = threadIdx.x & 31, sub = lane & 3;
   const int jb = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int h = blockIdx.y, b = blockIdx.z;
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) reps_kv4_kernel(const __grid_constan
     const bool on = g < groups;
     float sum[4][4] = {};  // dims 4 i .. 4 i + 3
     const uint8_t *codes = p + g * 128 + sub * 32, *scales = p + 8 * a.d + sub * 4 * groups + g;
-#pragma unroll 2
+#pragma unroll 1
     for (int t = 0; t < pieces; ++t, codes += pb, scales += pb) {
       uint4 c[2] = {};
       uint32_t sc = 0, s[2];

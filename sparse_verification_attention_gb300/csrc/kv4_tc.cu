@@ -52,8 +52,8 @@ constexpr int kKeys = 128, kPieces = kKeys / kPiece;
 // at most two segments ahead of the scores and those two ahead of the weights.
 constexpr int kInfo = 16, kSegs = 16, kF = 8;
 constexpr int kMaxStages = 8;
-constexpr int kThreads = 640;
-constexpr int kSoftmaxWarp = 8, kLoadWarp = 16, kScoreWarp = 17, kOutWarp = 18;  // 19 lays out Q
+constexpr int kThreads = 768;
+constexpr int kSoftmaxWarp = 12, kLoadWarp = 20, kScoreWarp = 21, kOutWarp = 22;  // 23 lays out Q
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 128, kColK = 256, kColV = 384;  // K and V: two of 64 columns
 constexpr float kLift = 7.f;    // weights are 2^kLift times their size ...
@@ -362,9 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
     }
   } else if (warp < kSoftmaxWarp) {
     // ------------------------------------------------------------ V: lane = dim
-    const int w = warp - 4;
+    const int w = warp & 3, odd = (warp - 4) >> 2;  // two warpgroups, every other tile each
     const uint32_t t4 = lane & 3;  // code row lane / 4 (that dim and the one 8 behind), tokens 4 t4 ..
-    for (uint32_t i = 0, st = 0, ph = 0; i < tiles; ++i) {
+    for (uint32_t i = odd; i < tiles; i += 2) {
+      const uint32_t st = i % stages, ph = i / stages;
       if (!wait(sh.full[st], ph, 3u)) break;
       if (!wait(sh.pv_done[i & 1], (i >> 1) ^ 1u, 4u)) break;
       tc::fence_after();
@@ -414,7 +415,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       tc::wait_st();
       tc::fence_before();
       arrive(sh.o_ready[i & 1]);
-      if (++st == (uint32_t)stages) st = 0, ph ^= 1u;
     }
   } else if (warp < kLoadWarp) {
     // ------------------------------------------------------------ softmax: lane = key
@@ -643,45 +643,87 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
           sh.seg[seg % kSegs].slot = s.slot;
           sh.seg[seg % kSegs].rows = min(a.rows, a.T * a.G - s.rt * a.rows);
         }
-        // four tiles' pages at a time: lane = piece
-        long long next = -1;
-        int next_valid = 0;
-#pragma unroll 1
-        for (int t0 = -4; ok && t0 < s.tiles; t0 += 4) {
-          const long long now = next;
-          const int v = next_valid;
-          if (t0 + 4 < s.tiles) {
-            next = piece_at(a, s, (s.tile0 + t0 + 4) * kPieces + lane, &next_valid, &flags);
-            if ((s.tiles - t0 - 4) * kPieces <= lane) next = -1, next_valid = 0;
+        // Four tiles at a time: lane = piece. A selected block is read two batches ahead, its
+        // page one, and neither is looked at before it is due, so that a batch's copies wait
+        // for no load of their own (when they did, the loading warp took 1000 cycles a tile).
+        const int32_t* sel = a.sel ? a.sel + ((long long)s.b * a.Hkv + s.h) * a.sel_stride : nullptr;
+        const int32_t* row = a.block_table + (long long)s.b * a.nb_max;
+        const int slots = sel ? a.n_sel : s.full, i0 = s.tile0 * kPieces + lane;
+        const int last = min((s.tile0 + s.tiles) * kPieces, s.pieces);
+        auto slot_of = [&](int p) { return a.ppb_shift >= 0 ? p >> a.ppb_shift : quotient(p, a.ppb); };
+        auto entry_of = [&](int p) {
+          const int at = sel && p < last ? slot_of(p) : slots;
+          return at < slots ? __ldcg(sel + at) : -1;
+        };
+        struct Look {
+          int valid, sub, page;  // tokens that count, piece of its block, page (not checked)
+        };
+        auto look = [&](int p, int entry) {
+          Look k = {0, 0, 0};
+          if (p >= last) return k;
+          const int at = slot_of(p);
+          int block = sel ? entry : at;
+          k.sub = p - at * a.ppb;
+          k.valid = kPiece;
+          if (at >= slots) {  // the partial last block
+            block = s.full;
+            k.sub = p - slots * a.ppb;
+            k.valid = min(kPiece, s.ctx - s.full * a.blk - k.sub * kPiece);
+          } else if (block < 0 || block >= s.full) {
+            if (block != -1) flags |= SV_FLAG_BAD_BLOCK_INDEX;
+            k.valid = 0;
+            return k;
           }
-          if (t0 < 0) continue;
-          const long long prev = __shfl_up_sync(0xffffffffu, now, 1);
-          const bool there = now >= 0;
-          // a run of pieces that follow each other in the pool is one copy
-          const uint32_t heads = __ballot_sync(0xffffffffu, there && ((lane & 7) == 0 || prev < 0 || now != prev + 1));
+          k.page = __ldcg(row + block);
+          return k;
+        };
+        int entry = entry_of(i0);
+        Look next = look(i0, entry);
+        entry = entry_of(i0 + 32);
+#pragma unroll 1
+        for (int t0 = 0; ok && t0 < s.tiles; t0 += 4) {
+          Look now = next;
+          next = look(i0 + (t0 + 4) * kPieces, entry);
+          entry = entry_of(i0 + (t0 + 8) * kPieces);
+          if (now.valid && (now.page < 0 || now.page >= a.num_pages)) {
+            flags |= SV_FLAG_BAD_PAGE;
+            now.valid = 0;
+          }
+          const bool there = now.valid > 0;
+          const int at = now.page * a.Hkv * a.ppb + s.h * a.ppb + now.sub;  // piece of the pool (below 2^31: the call's limits)
+          const int prev = __shfl_up_sync(0xffffffffu, at, 1);
           const uint32_t have = __ballot_sync(0xffffffffu, there);
+          // a run of pieces that follow each other in the pool is one copy
+          const uint32_t heads = __ballot_sync(0xffffffffu, there && ((lane & 7) == 0 || !(have >> (lane - 1) & 1u) || at != prev + 1));
           const uint32_t stop = (heads | ~have | 0x01010101u) & ~((2u << lane) - 1u);  // where a run of this lane ends
           const int run = (stop ? __ffs(stop) - 1 : 32) - lane;
+          const bool full = __all_sync(0xffffffffu, now.valid == kPiece);
+          const uint8_t *k_from = a.k_pool + (long long)at * pb, *v_from = a.v_pool + (long long)at * pb;
 #pragma unroll 1
           for (int t = 0; t < 4 && t0 + t < s.tiles; ++t, ++i) {
             if (!(ok = wait(sh.empty[st], ph ^ 1u, 9u))) break;
-            const uint32_t count = (lane >> 3) == t ? (uint32_t)v << (8 * (lane & 3)) : 0u;
-            const uint32_t lo = __reduce_or_sync(0xffffffffu, (lane & 4) == 0 ? count : 0u);
-            const uint32_t hi = __reduce_or_sync(0xffffffffu, (lane & 4) != 0 ? count : 0u);
+            uint64_t valid = kAllValid;
+            if (!full) {
+              const uint32_t count = (lane >> 3) == t ? (uint32_t)now.valid << (8 * (lane & 3)) : 0u;
+              const uint32_t lo = __reduce_or_sync(0xffffffffu, (lane & 4) == 0 ? count : 0u);
+              const uint32_t hi = __reduce_or_sync(0xffffffffu, (lane & 4) != 0 ? count : 0u);
+              valid = (uint64_t)hi << 32 | lo;
+            }
+            const uint32_t bar = smem_u32(&sh.full[st]);
             if (lane == 0) {
-              const int at = t0 + t, left = s.tiles - at, per = C::kAlt ? 2 : 1;
+              const int tile = t0 + t, left = s.tiles - tile, per = C::kAlt ? 2 : 1;
               TileInfo& ti = sh.info[i % kInfo];
-              ti.valid = (uint64_t)hi << 32 | lo;
-              ti.flags = (at == 0 ? kBegin : 0u) | (left == 1 ? kEnd : 0u) | (at < per ? kFirst : 0u) |
+              ti.valid = valid;
+              ti.flags = (tile == 0 ? kBegin : 0u) | (left == 1 ? kEnd : 0u) | (tile < per ? kFirst : 0u) |
                          (left <= per ? kLast : 0u) | (C::kAlt && s.tiles == 1 ? kOnly : 0u);
               ti.seg = seg;
-              mbar_arrive_expect_tx(smem_u32(&sh.full[st]), 2u * pb * __popc(have >> (8 * t) & 0xffu));
+              mbar_arrive_expect_tx(bar, 2u * pb * __popc(have >> (8 * t) & 0xffu));
             }
             __syncwarp();
             if ((lane >> 3) == t && (heads >> lane & 1u)) {
               const uint32_t dst = ring + st * stage_bytes + (lane & 7) * pb;
-              bulk_load(dst, a.k_pool + now * pb, run * pb, smem_u32(&sh.full[st]));
-              bulk_load(dst + side, a.v_pool + now * pb, run * pb, smem_u32(&sh.full[st]));
+              bulk_load(dst, k_from, run * pb, bar);
+              bulk_load(dst + side, v_from, run * pb, bar);
             }
             if (++st == (uint32_t)stages) st = 0, ph ^= 1u;
           }
