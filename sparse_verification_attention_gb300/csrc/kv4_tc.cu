@@ -52,8 +52,8 @@ constexpr int kKeys = 128, kPieces = kKeys / kPiece;
 // at most two segments ahead of the scores and those two ahead of the weights.
 constexpr int kInfo = 16, kSegs = 16, kF = 8;
 constexpr int kMaxStages = 8;
-constexpr int kThreads = 768;
-constexpr int kSoftmaxWarp = 12, kLoadWarp = 20, kScoreWarp = 21, kOutWarp = 22;  // 23 lays out Q
+constexpr int kThreads = 640;
+constexpr int kSoftmaxWarp = 8, kLoadWarp = 16, kScoreWarp = 17, kOutWarp = 18;  // 19 lays out Q
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 128, kColK = 256, kColV = 384;  // K and V: two of 64 columns
 constexpr float kLift = 7.f;    // weights are 2^kLift times their size ...
@@ -102,7 +102,9 @@ struct Cfg {
   static constexpr int kQ = N <= 64 ? 2 : 1;         // Q buffers
   static constexpr int kQBytes = 2 * N * 128;        // two blocks of 64 dims
   static constexpr int kPBytes = (N > 64 ? 2 : 1) * kKeys * 128;
-  static constexpr int kFixed = kQ * kQBytes + 2 * kPBytes + (int)sizeof(Control);
+  static constexpr bool kVSmem = N <= 64;            // V as halves in shared memory, not in TMEM
+  static constexpr int kVBytes = kVSmem ? 2 * kKeys * 128 : 0;
+  static constexpr int kFixed = kQ * kQBytes + 2 * kPBytes + 2 * kVBytes + (int)sizeof(Control);
 };
 
 __device__ __forceinline__ void fence_proxy_async_shared() {
@@ -143,6 +145,25 @@ __device__ __forceinline__ uint32_t lds8x4(uint32_t row, int at, int last) {
   for (int j = 0; j < 4; ++j) r |= lds8(row + min(at + j, last)) << (8 * j);
   return r;
 }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t first_bytes(int n) {  // a mask of the first n bytes of a word
+  return n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+}
+template <int H>
+__device__ __forceinline__ uint32_t mul_by_half(uint32_t x, uint32_t s) {
+  const __half2 ss = *reinterpret_cast<const __half2*>(&s);
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), H ? __high2half2(ss) : __low2half2(ss));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+// The dim of a head that row m of V^T in shared memory holds.
+__device__ __forceinline__ int dim_of(int m) {
+  const int g = m >> 4;
+  return g * 16 + (m >> 3 & 1) * 4 + (((m >> 1) + g) & 3) + (m & 1) * 8;
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
@@ -157,8 +178,8 @@ __device__ __forceinline__ void st_16x256b_x4(uint32_t taddr, const uint32_t (&r
       : "memory");
 }
 // Instruction descriptor of kind::f16 with f16 operands and fp32 sums, M = 128.
-__host__ __device__ constexpr uint32_t idesc_f16(int n, bool b_mn) {
-  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+__host__ __device__ constexpr uint32_t idesc_f16(int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 __device__ __forceinline__ float redux_max(float x) {
   float r;
@@ -261,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t q_base = base, p_base = q_base + C::kQ * C::kQBytes;
-  const uint32_t ctl = p_base + 2 * C::kPBytes;
+  const uint32_t v_base = p_base + 2 * C::kPBytes, ctl = v_base + 2 * C::kVBytes;
   Control& sh = *reinterpret_cast<Control*>(smem_raw + (ctl - smem_u32(smem_raw)));
   const uint32_t ring = ctl + (uint32_t)((sizeof(Control) + 127) / 128 * 128);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -362,59 +383,101 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
     }
   } else if (warp < kSoftmaxWarp) {
     // ------------------------------------------------------------ V: lane = dim
-    const int w = warp & 3, odd = (warp - 4) >> 2;  // two warpgroups, every other tile each
+    const int w = warp & 3;
     const uint32_t t4 = lane & 3;  // code row lane / 4 (that dim and the one 8 behind), tokens 4 t4 ..
-    for (uint32_t i = odd; i < tiles; i += 2) {
-      const uint32_t st = i % stages, ph = i / stages;
+    for (uint32_t i = 0, st = 0, ph = 0; i < tiles; ++i) {
       if (!wait(sh.full[st], ph, 3u)) break;
       if (!wait(sh.pv_done[i & 1], (i >> 1) ^ 1u, 4u)) break;
       tc::fence_after();
       const uint64_t valid = sh.info[i % kInfo].valid;
       const uint32_t from = ring + st * stage_bytes + side;
-      if (valid != kAllValid) {
-        // tokens that do not count get a scale of zero, whatever their bytes hold: the
-        // warp's two groups x 128 tokens, 4 tokens at a time
-        for (int e = lane; e < 64; e += 32) {
-          const int g = 2 * w + (e >> 5), p = e >> 2 & 7, n = (int)(valid >> (8 * p) & 0xff) - (e & 3) * 4;
-          const uint32_t at = from + p * pb + groups * 128 + g * 16 + (e & 3) * 4;
-          if (g < groups && n < 4) sts32(at, n <= 0 ? 0u : lds32(at) & ((1u << (8 * n)) - 1u));
+      if constexpr (C::kVSmem) {
+        // A thread has 4 code rows (8 dims: rows c .. c + 3 hold them and those 8 behind) of a
+        // piece's 16 tokens: row = key, 128 bytes of 64 dims, 128-byte swizzle. The rows are taken
+        // in an order that differs from group to group, so that the loads of 8 lanes fall
+        // into different banks; dim_of() undoes it.
+        const uint32_t cb = lane & 1, gq = lane >> 1 & 3, half = lane >> 3 & 1, p = 2 * w + (lane >> 4), g = half * 4 + gq;
+        if (DG || (int)g < groups) {
+          const uint32_t at = from + p * pb;
+          uint4 c[4], sc = lds128(at + groups * 128 + g * 16);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) c[r] = lds128(at + g * 128 + (4 * cb + ((r + gq) & 3)) * 16);
+          if (valid != kAllValid) {  // tokens that do not count: a scale of zero, whatever the bytes hold
+            const int n = (int)(valid >> (8 * p) & 0xff);
+            sc.x &= first_bytes(n), sc.y &= first_bytes(n - 4), sc.z &= first_bytes(n - 8), sc.w &= first_bytes(n - 12);
+          }
+          const uint32_t to = v_base + (i & 1) * C::kVBytes + half * (kKeys * 128) + p * kPiece * 128;
+          auto four = [&](int k, uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t s4) {  // tokens 4 k ..
+            uint32_t f[4][4], s01, s23;
+            e4m3x4_to_f16(s4, s01, s23);
+            e2m1x8_to_f16(c0, f[0]);
+            e2m1x8_to_f16(c1, f[1]);
+            e2m1x8_to_f16(c2, f[2]);
+            e2m1x8_to_f16(c3, f[3]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t s1 = j < 2 ? s01 : s23;
+              uint32_t h[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) h[r] = j & 1 ? mul_by_half<1>(f[r][j], s1) : mul_by_half<0>(f[r][j], s1);
+              const uint32_t tok = 4 * k + j;
+              sts128(to + tok * 128 + (((2 * gq + cb) ^ (tok & 7)) << 4), h[0], h[1], h[2], h[3]);
+            }
+          };
+          four(0, c[0].x, c[1].x, c[2].x, c[3].x, sc.x);
+          four(1, c[0].y, c[1].y, c[2].y, c[3].y, sc.y);
+          four(2, c[0].z, c[1].z, c[2].z, c[3].z, sc.z);
+          four(3, c[0].w, c[1].w, c[2].w, c[3].w, sc.w);
         }
-        fence_proxy_async_shared();  // ahead of the next copy into the stage
-        __syncwarp();
-      }
+        arrive(sh.empty[st]);
+        fence_proxy_async_shared();
+      } else {
+        if (valid != kAllValid) {
+          // tokens that do not count get a scale of zero, whatever their bytes hold: the
+          // warp's two groups x 128 tokens, 4 tokens at a time
+          for (int e = lane; e < 64; e += 32) {
+            const int g = 2 * w + (e >> 5), p = e >> 2 & 7, n = (int)(valid >> (8 * p) & 0xff) - (e & 3) * 4;
+            const uint32_t at = from + p * pb + groups * 128 + g * 16 + (e & 3) * 4;
+            if (g < groups && n < 4) sts32(at, n <= 0 ? 0u : lds32(at) & ((1u << (8 * n)) - 1u));
+          }
+          fence_proxy_async_shared();  // ahead of the next copy into the stage
+          __syncwarp();
+        }
 #pragma unroll 1
-      for (int q = 0; q < 2; ++q) {  // the warp's two groups
-        const int g = 2 * w + q;
-        if (!DG && g >= groups) break;
-        const uint32_t code = from + g * 128 + lane * 4, scale = from + groups * 128 + g * 16 + t4 * 4;
-        uint32_t c[8], sc[8], r[2][16];
+        for (int q = 0; q < 2; ++q) {  // the warp's two groups
+          const int g = 2 * w + q;
+          if (!DG && g >= groups) break;
+          const uint32_t code = from + g * 128 + lane * 4, scale = from + groups * 128 + g * 16 + t4 * 4;
+          uint32_t c[8], sc[8], r[2][16];
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          c[p] = lds32(code + p * pb);
-          sc[p] = lds32(scale + p * pb);
-        }
+          for (int p = 0; p < 8; ++p) {
+            c[p] = lds32(code + p * pb);
+            sc[p] = lds32(scale + p * pb);
+          }
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          const uint32_t c4 = c[p] << 4, c8 = c[p] << 8;
-          // bytes 1 and 3: tokens (0, 1) and (2, 3) of the one dim, and of the other
-          const uint32_t lo = (c8 & 0x0f000f00u) | (c4 & 0xf0fff0ffu), hi = (c4 & 0x0f000f00u) | (c[p] & 0xf0fff0ffu);
-          uint32_t s01, s23, *to = r[p >> 2] + 4 * (p & 3);
-          e4m3x4_to_f16(sc[p], s01, s23);
-          e2m1x4_to_f16(lo, to[0], to[1]);
-          e2m1x4_to_f16(hi, to[2], to[3]);
-          to[0] = mul_f16x2(to[0], s01);
-          to[1] = mul_f16x2(to[1], s23);
-          to[2] = mul_f16x2(to[2], s01);
-          to[3] = mul_f16x2(to[3], s23);
+          for (int p = 0; p < 8; ++p) {
+            const uint32_t c4 = c[p] << 4, c8 = c[p] << 8;
+            // bytes 1 and 3: tokens (0, 1) and (2, 3) of the one dim, and of the other
+            const uint32_t lo = (c8 & 0x0f000f00u) | (c4 & 0xf0fff0ffu), hi = (c4 & 0x0f000f00u) | (c[p] & 0xf0fff0ffu);
+            uint32_t s01, s23, *to = r[p >> 2] + 4 * (p & 3);
+            e4m3x4_to_f16(sc[p], s01, s23);
+            e2m1x4_to_f16(lo, to[0], to[1]);
+            e2m1x4_to_f16(hi, to[2], to[3]);
+            to[0] = mul_f16x2(to[0], s01);
+            to[1] = mul_f16x2(to[1], s23);
+            to[2] = mul_f16x2(to[2], s01);
+            to[3] = mul_f16x2(to[3], s23);
+          }
+          const uint32_t at = tmem + ((uint32_t)(w * 32 + q * 16) << 16) + kColV + (i & 1) * 64;
+          st_16x256b_x4(at, r[0]);
+          st_16x256b_x4(at + 32, r[1]);
         }
-        const uint32_t at = tmem + ((uint32_t)(w * 32 + q * 16) << 16) + kColV + (i & 1) * 64;
-        st_16x256b_x4(at, r[0]);
-        st_16x256b_x4(at + 32, r[1]);
+        arrive(sh.empty[st]);
+        tc::wait_st();
+        tc::fence_before();
       }
-      arrive(sh.empty[st]);
-      tc::wait_st();
-      tc::fence_before();
       arrive(sh.o_ready[i & 1]);
+      if (++st == (uint32_t)stages) st = 0, ph ^= 1u;
     }
   } else if (warp < kLoadWarp) {
     // ------------------------------------------------------------ softmax: lane = key
@@ -592,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               if (col0 + c0 + e < si.rows)
-                a.part_o[(out + col0 + c0 + e) * (groups * 16) + key] = __uint_as_float(o[e]);
+                a.part_o[(out + col0 + c0 + e) * (groups * 16) + (C::kVSmem ? dim_of(key) : key)] = __uint_as_float(o[e]);
           }
         }
         tc::fence_before();
@@ -738,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       }
     } else if (warp == kScoreWarp) {
       // ------------------------------------------------------------ S^T = K Q^T
-      constexpr uint32_t id_s = idesc_f16(N, false);
+      constexpr uint32_t id_s = idesc_f16(N, false, false);
       const uint64_t dq = tc::smem_desc(q_base, 16, 1024);
       const uint32_t lead = elect_lead();
       for (uint32_t i = 0; i < tiles; ++i) {
@@ -765,8 +828,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       }
     } else if (warp == kOutWarp) {
       // ------------------------------------------------------------ O^T += V^T P^T
-      constexpr uint32_t id_o = idesc_f16(N, true);
-      const uint64_t dp = tc::smem_desc(p_base, kKeys * 128, 1024);
+      constexpr uint32_t id_o = idesc_f16(N, C::kVSmem, true);
+      const uint64_t dp = tc::smem_desc(p_base, kKeys * 128, 1024), dv = tc::smem_desc(v_base, kKeys * 128, 1024);
       const uint32_t lead = elect_lead();
       uint32_t begun[2] = {0, 0};  // segments that O's streams have begun
       for (uint32_t i = 0; i < tiles; ++i) {
@@ -778,8 +841,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
         const uint64_t p = dp + (uint64_t)((i & 1) * (C::kPBytes >> 4));
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          lead_mma_ts(lead, tmem + kColO + ob * N, tmem + kColV + (i & 1) * 64 + kk * 8, p + (uint64_t)((kk * 2048) >> 4),
-                      id_o, first && kk == 0 ? 0u : 1u);
+          if constexpr (C::kVSmem)
+            lead_mma_ss(lead, tmem + kColO + ob * N, dv + (uint64_t)(((i & 1) * C::kVBytes + kk * 2048) >> 4),
+                        p + (uint64_t)((kk * 2048) >> 4), id_o, first && kk == 0 ? 0u : 1u);
+          else
+            lead_mma_ts(lead, tmem + kColO + ob * N, tmem + kColV + (i & 1) * 64 + kk * 8,
+                        p + (uint64_t)((kk * 2048) >> 4), id_o, first && kk == 0 ? 0u : 1u);
         lead_commit(lead, smem_u32(&sh.pv_done[i & 1]));
       }
       if (sh.abort) {
