@@ -35,6 +35,7 @@
 // loops unrolled and every wait's clock inline, 128 K tokens x 4 took 497 us, rolled 247.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "host.h"
 #include "kv4.cuh"
@@ -89,9 +90,7 @@ struct Control {
   TileInfo info[kInfo];
   SegInfo seg[kSegs];
   alignas(16) float f[kF][kTc4Rows];   // factor of a row's scores
-  alignas(16) float nm[kTc4Rows];         // minus (reference - kLift) of a column, log2 domain
-  alignas(16) float corr[kTc4Rows];
-  float mx[4][kTc4Rows];                  // by warp of a softmax warpgroup (also: sums)
+  alignas(16) float mx[4][kTc4Rows], sum[4][kTc4Rows];  // by warp of a softmax warpgroup
   int cu[kMaxB4 + 1], ctx[kMaxB4];
 };
 
@@ -181,26 +180,47 @@ __device__ __forceinline__ void st_16x256b_x4(uint32_t taddr, const uint32_t (&r
 __host__ __device__ constexpr uint32_t idesc_f16(int n, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
-__device__ __forceinline__ float redux_max(float x) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-  return r;
-}
-// 32 lanes x 8 (N) columns of TMEM.
+// 32 lanes x 8 columns of TMEM.
 __device__ __forceinline__ void ld8(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr)
                : "memory");
 }
+// 16 lanes x 8 N columns of TMEM into 4 N registers (see st_16x256b_x4).
 template <int N>
-__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t* r) {
-  if constexpr (N == 16) {
-    tc::ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(r));
+__device__ __forceinline__ void ld_16x256b(uint32_t taddr, uint32_t* r) {
+  if constexpr (N == 1) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr)
+                 : "memory");
+  } else if constexpr (N == 2) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
   } else {
-#pragma unroll
-    for (int c = 0; c < N; c += 32) tc::ld32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(r + c));
+    static_assert(N == 4, "columns");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
   }
+}
+__device__ __forceinline__ void st_16x256b_x1(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+// Four 8 x 8 blocks of halves, a row of block b at the address in lane 8 b + row.
+__device__ __forceinline__ void put(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1), "r"(r2),
+               "r"(r3)
+               : "memory");
 }
 
 // A wait that may suspend the warp for up to a millisecond: without the hint it comes back
@@ -480,28 +500,42 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       if (++st == (uint32_t)stages) st = 0, ph ^= 1u;
     }
   } else if (warp < kLoadWarp) {
-    // ------------------------------------------------------------ softmax: lane = key
-    // columns in registers at a time: all of up to 32; of 64 (with their 64 sums) 16, and
-    // the scores are read from TMEM a second time
-    constexpr int NC = C::kCols, CH = NC <= 32 ? NC : 16, NCH = NC / CH;
+    // ------------------------------------------------------------ softmax
+    // TMEM gives a thread the scores of 4 keys (lane / 4 and those 8, 16 and 24 behind) and of
+    // two neighbouring columns in every eight: the factors, references and sums of NC / 4
+    // columns stay in registers. (With a key a thread and all columns they came from shared
+    // memory, 16 loads of 16 bytes a tile that the other roles' traffic held up: 800 to
+    // 1200 cycles for 80 instructions.)
+    constexpr int NC = C::kCols, CH = NC < 32 ? NC : 32, NCH = NC / CH, J = NC / 8;
     const int wg = (warp - kSoftmaxWarp) >> 2, quad = warp & 3, in_wg = (warp - kSoftmaxWarp) & 3;
-    // columns of S and of P, and of O, references and sums
+    // columns of S and of P, and of O and the exchange arrays
     const int col0 = C::kAlt ? 0 : wg * NC, own0 = wg * NC;
-    const int key = quad * 32 + lane;
+    const int g = lane >> 2, t2 = (lane & 3) * 2;  // key in eight, column in eight
     const uint32_t tlane = (uint32_t)(quad * 32) << 16, tmem_o = tmem + tlane + kColO + own0;
+    // this lane's row of the 8 x 8 blocks that it addresses for P's stores (see put)
+    const int prow = quad * 32 + (NC == 16 ? (lane >> 4) * 8 : 0) + (lane & 7), pchunk = NC == 16 ? lane >> 3 & 1 : lane >> 3;
     if (!idle) {  // the first segment's Q, which everybody else waits for (later ones: one warp, ahead)
       const Segment s = next_segment(a, sh, begin, end);
       lay_out_q(a, s, N, q_base, sh.f[0], warp - kSoftmaxWarp, 8);
       arrive(sh.q_first);
     }
     arrive(sh.s_ready[C::kAlt ? wg : 0]);  // S is free
-    uint64_t l[NC / 2];  // sums of two columns each
-    bool first = true;   // no key of the stream has counted yet
+    uint64_t f[J], nm[J], l[J];  // factor, minus (reference - kLift), sum: two columns each
+    bool first = true;           // no key of the stream has counted yet
     uint32_t met = 0;
     // the warpgroup's four warps wait for each other (no named barrier: that wait has no limit)
     auto meet = [&] {
       arrive(sh.meet[wg]);
       return wait(sh.meet[wg], met++, 17u);
+    };
+    // The four sums over lane / 4 of a pair of columns, in lanes 0 .. 3.
+    auto fold = [&](float2 x, auto op) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        x.x = op(x.x, __shfl_xor_sync(0xffffffffu, x.x, o));
+        x.y = op(x.y, __shfl_xor_sync(0xffffffffu, x.y, o));
+      }
+      return x;
     };
     for (uint32_t i = C::kAlt ? wg : 0; i < tiles; i += C::kAlt ? 2 : 1) {
       const uint32_t sb = C::kAlt ? wg : 0;  // S buffer, used every (or every other) tile
@@ -509,37 +543,48 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       if (!wait(sh.s_full[sb], turn, 5u)) break;
       tc::fence_after();
       const TileInfo info = sh.info[i % kInfo];
-      const float* f = sh.f[info.seg % kF] + col0;
       if (info.flags & kFirst) {
         first = true;
+        const float* ff = sh.f[info.seg % kF] + col0 + t2;
 #pragma unroll
-        for (int c = 0; c < NC / 2; ++c) l[c] = 0;
+        for (int j = 0; j < J; ++j) {
+          f[j] = *reinterpret_cast<const uint64_t*>(ff + 8 * j);
+          nm[j] = l[j] = 0;
+        }
       }
-      const bool counts = key % kPiece < (int)(info.valid >> (8 * (key / kPiece)) & 0xff);
-      const bool any = info.valid != 0;  // a key of the tile counts
-      uint32_t s[CH];
+      const bool any = info.valid != 0, partial = info.valid != kAllValid;  // keys of the tile that count
+      bool on[4] = {true, true, true, true};  // keys g, g + 8, g + 16, g + 24 count
+      if (partial) {
+        const int v0 = (int)(info.valid >> (16 * quad) & 0xff), v1 = (int)(info.valid >> (16 * quad + 8) & 0xff);
+        on[0] = g < v0, on[1] = g + 8 < v0, on[2] = g < v1, on[3] = g + 8 < v1;
+      }
+      const uint32_t tmem_s = tmem + tlane + kColS + sb * 64 + col0;
+      uint32_t s[2][CH / 2], p[NCH][2][CH / 4];
+      uint64_t sums[J];
+      // scores of keys 0 .. 15 and 16 .. 31 of the warp's: columns 8 j + t2 (+ 1) of key g in
+      // s[.][4 j] (4 j + 1), of key g + 8 in 4 j + 2 (4 j + 3)
       auto load = [&](int ch) {
-        ld_cols<CH>(tmem + tlane + kColS + sb * 64 + col0 + ch * CH, s);
+        ld_16x256b<CH / 8>(tmem_s + ch * CH, s[0]);
+        ld_16x256b<CH / 8>(tmem_s + ch * CH + (16u << 16), s[1]);
         tc::wait_ld();
       };
-      // weights in place of the scores of a run of columns, and their sum: it tells whether
-      // a reference has to move
-      auto weigh = [&](int ch) {
-        uint64_t sum[2] = {0, 0};
+      // weights of a run of columns as halves, and their sums over the thread's keys
+      auto weigh = [&](int ch, auto masked) {
 #pragma unroll
-        for (int c = 0; c < CH; c += 4) {
-          const ulonglong2 ff = *reinterpret_cast<const ulonglong2*>(f + ch * CH + c);
-          const ulonglong2 nn = *reinterpret_cast<const ulonglong2*>(sh.nm + own0 + ch * CH + c);
-          const float2 x = unpack2(fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), ff.x, nn.x));
-          const float2 y = unpack2(fma2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), ff.y, nn.y));
-          const float e[4] = {ex2(x.x), ex2(x.y), ex2(y.x), ex2(y.y)};
-          sum[0] = add2(sum[0], pack2(e[0], e[1]));
-          sum[1] = add2(sum[1], pack2(e[2], e[3]));
+        for (int j = 0; j < CH / 8; ++j) {
+          const int col = ch * (CH / 8) + j;
+          uint64_t sum = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[c + k] = __float_as_uint(e[k]);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t* v = &s[k >> 1][4 * j + 2 * (k & 1)];
+            const float2 x = unpack2(fma2(pack2(__uint_as_float(v[0]), __uint_as_float(v[1])), f[col], nm[col]));
+            float2 e = make_float2(ex2(x.x), ex2(x.y));
+            if (decltype(masked)::value && !on[k]) e = make_float2(0.f, 0.f);
+            sum = add2(sum, pack2(e.x, e.y));
+            p[ch][k >> 1][2 * j + (k & 1)] = pack_f16(e.x, e.y);
+          }
+          sums[col] = sum;
         }
-        const float2 t = unpack2(add2(sum[0], sum[1]));
-        return t.x + t.y;
       };
       // References move when the stream begins and when the vote says so: maxima over the
       // tile's keys, then O and the sums follow.
@@ -547,96 +592,107 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
 #pragma unroll 1
       for (bool over = first && any;; over = true) {
         if (over) {
-#pragma unroll 1
-          for (int c = 0; c < NC; c += 8) {
-            uint32_t x[8];
-            ld8(tmem + tlane + kColS + sb * 64 + col0 + c, x);
-            tc::wait_ld();
-            float m[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m[e] = redux_max(counts ? __uint_as_float(x[e]) * f[c + e] : -INFINITY);
-            if (lane == 0) {
+          for (int ch = 0; ch < NCH; ++ch) {
+            load(ch);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) sh.mx[in_wg][own0 + c + e] = m[e];
+            for (int j = 0; j < CH / 8; ++j) {
+              const float2 ff = unpack2(f[ch * (CH / 8) + j]);
+              float2 m = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t* v = &s[k >> 1][4 * j + 2 * (k & 1)];
+                if (on[k]) m = make_float2(fmaxf(m.x, __uint_as_float(v[0]) * ff.x), fmaxf(m.y, __uint_as_float(v[1]) * ff.y));
+              }
+              m = fold(m, [](float x, float y) { return fmaxf(x, y); });
+              if (lane < 4) *reinterpret_cast<float2*>(&sh.mx[in_wg][own0 + ch * CH + 8 * j + t2]) = m;
             }
           }
           if (!(ok = meet())) break;
-          const int c = in_wg * 32 + lane;
-          if (c < NC) {
-            const int col = own0 + c;
-            const float top = fmaxf(fmaxf(sh.mx[0][col], sh.mx[1][col]), fmaxf(sh.mx[2][col], sh.mx[3][col]));
-            const float old = kLift - sh.nm[col];
-            const bool up = first || top > old + kSlack;
-            sh.corr[col] = up && !first ? ex2(old - top) : 1.f;
-            if (up) sh.nm[col] = kLift - top;
+          float2 corr[J];
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            float2 top = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float2 m = *reinterpret_cast<const float2*>(&sh.mx[w][own0 + 8 * j + t2]);
+              top = make_float2(fmaxf(top.x, m.x), fmaxf(top.y, m.y));
+            }
+            float2 n = unpack2(nm[j]);
+            auto follow = [&](float& n, float top) {
+              const float old = kLift - n;
+              const bool up = first || top > old + kSlack;
+              if (up) n = kLift - top;
+              return up && !first ? ex2(old - top) : 1.f;
+            };
+            corr[j].x = follow(n.x, top.x);
+            corr[j].y = follow(n.y, top.y);
+            nm[j] = pack2(n.x, n.y);
           }
-          if (!(ok = meet())) break;
           if (!first) {
             // every product into O is complete
             if (!(ok = C::kAlt ? wait(sh.pv_done[sb], turn ^ 1u, 6u) : wait(sh.pv_done[(i - 1) & 1], (i - 1) >> 1, 6u)))
               break;
             tc::fence_after();
 #pragma unroll
-            for (int c0 = 0; c0 < NC; c0 += 8) {
-              uint32_t o[8];
-              ld8(tmem_o + c0, o);
-              tc::wait_ld();
-#pragma unroll
-              for (int c = 0; c < 8; c += 2) {
-                const float2 k = *reinterpret_cast<const float2*>(sh.corr + own0 + c0 + c), sums = unpack2(l[(c0 + c) / 2]);
-                o[c] = __float_as_uint(__uint_as_float(o[c]) * k.x);
-                o[c + 1] = __float_as_uint(__uint_as_float(o[c + 1]) * k.y);
-                l[(c0 + c) / 2] = pack2(sums.x * k.x, sums.y * k.y);
-              }
-              tc::st8(tmem_o + c0, o);
+            for (int j = 0; j < J; ++j) {
+              const float2 x = unpack2(l[j]);
+              l[j] = pack2(x.x * corr[j].x, x.y * corr[j].y);
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j = 0; j < J; ++j) {
+                uint32_t o[4];
+                const uint32_t at = tmem_o + (h ? 16u << 16 : 0u) + 8 * j;
+                ld_16x256b<1>(at, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  o[k] = __float_as_uint(__uint_as_float(o[k]) * (k & 1 ? corr[j].y : corr[j].x));
+                st_16x256b_x1(at, o);
+              }
             tc::wait_st();
           }
           first = false;
         }
-        float top = 0.f;
+        uint64_t all = 0;
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
           load(ch);
-          top += weigh(ch);
+          if (partial) weigh(ch, std::true_type());
+          else weigh(ch, std::false_type());
         }
         if (over) break;  // weights are 2^kLift at most now
-        if (__any_sync(0xffffffffu, !first && counts && top > kTop) && lane == 0) sh.over[wg][turn & 1] = i + 1;
+#pragma unroll
+        for (int j = 0; j < J; ++j) all = add2(all, sums[j]);
+        const float2 top = unpack2(all);
+        if (__any_sync(0xffffffffu, !first && top.x + top.y > kTop) && lane == 0) sh.over[wg][turn & 1] = i + 1;
         if (!(ok = meet()) || *(volatile uint32_t*)&sh.over[wg][turn & 1] != i + 1) break;
       }
       if (!ok) break;
-      // sums, and P^T into shared memory (row = key, 128 bytes of 64 columns)
-      const uint32_t row = p_base + (i & 1) * C::kPBytes + (uint32_t)key * 128 + (uint32_t)(col0 >> 6) * (kKeys * 128);
+      tc::fence_before();
+      arrive(sh.s_ready[C::kAlt ? sb : (i + 1) & 1]);  // S has been read: room for the next in its place
+#pragma unroll
+      for (int j = 0; j < J; ++j) l[j] = add2(l[j], sums[j]);
+      // P^T into shared memory: row = key, 128 bytes of 64 columns, 128-byte swizzle; 8 x 8 blocks
+      // as they lie in the registers
+      if (!wait(sh.pv_done[i & 1], (i >> 1) ^ 1u, 7u)) break;
+      const uint32_t row = p_base + (i & 1) * C::kPBytes + (uint32_t)(col0 >> 6) * (kKeys * 128) + (uint32_t)prow * 128;
 #pragma unroll
       for (int ch = 0; ch < NCH; ++ch) {
-        if (NCH > 1) {
-          load(ch);
-          weigh(ch);
-        }
-        if (ch == NCH - 1) {
-          tc::fence_before();
-          arrive(sh.s_ready[C::kAlt ? sb : (i + 1) & 1]);  // S has been read: room for the next in its place
-        }
-        if (ch == 0 && !(ok = wait(sh.pv_done[i & 1], (i >> 1) ^ 1u, 7u))) break;
-        if (counts) {
+        const uint32_t at = row + (uint32_t)(((ch * (CH / 8) + pchunk) ^ (lane & 7)) << 4);
 #pragma unroll
-          for (int c = 0; c < CH; c += 8) {
-            uint32_t p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = __uint_as_float(s[c + 2 * e]), y = __uint_as_float(s[c + 2 * e + 1]);
-              uint64_t& sums = l[(ch * CH + c) / 2 + e];
-              sums = add2(sums, pack2(x, y));
-              p[e] = pack_f16(x, y);
-            }
-            sts128(row + ((((ch * CH + c) >> 3) ^ (key & 7)) << 4), p[0], p[1], p[2], p[3]);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t* r = p[ch][h];
+          if constexpr (NC == 16) {
+            put(at + h * 16 * 128, r[0], r[2], r[1], r[3]);  // (columns 0 and 8 of keys 0 .., then of keys 8 ..)
+          } else {
+            put(at + h * 16 * 128, r[0], r[2], r[4], r[6]);
+            put(at + (h * 16 + 8) * 128, r[1], r[3], r[5], r[7]);
           }
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < CH; c += 8) sts128(row + ((((ch * CH + c) >> 3) ^ (key & 7)) << 4), 0, 0, 0, 0);
         }
       }
-      if (!ok) break;
       fence_proxy_async_shared();
       tc::fence_before();
       arrive(sh.o_ready[i & 1]);
@@ -646,47 +702,39 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
         tc::fence_after();
         const SegInfo si = sh.seg[info.seg % kSegs];
         const long long out = ((long long)si.slot * (C::kAlt ? 2 : 1) + (C::kAlt ? wg : 0)) * a.rows;
+        const int m = quad * 32 + lane, dim = C::kVSmem ? dim_of(m) : m;
 #pragma unroll 1
         for (int c0 = 0; c0 < NC; c0 += 8) {
           uint32_t o[8];
           ld8(tmem_o + c0, o);
           tc::wait_ld();
-          if (key < groups * 16) {
+          if (m < groups * 16) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (col0 + c0 + e < si.rows)
-                a.part_o[(out + col0 + c0 + e) * (groups * 16) + (C::kVSmem ? dim_of(key) : key)] = __uint_as_float(o[e]);
+              if (col0 + c0 + e < si.rows) a.part_o[(out + col0 + c0 + e) * (groups * 16) + dim] = __uint_as_float(o[e]);
           }
         }
         tc::fence_before();
         arrive(sh.o_empty[C::kAlt ? wg : 0]);
-        constexpr int LC = NC < 32 ? NC : 32;
 #pragma unroll
-        for (int h = 0; h < NC / LC; ++h) {
-#pragma unroll
-          for (int c = 0; c < LC; c += 4) {
-            const float2 x = unpack2(l[(h * LC + c) / 2]), y = unpack2(l[(h * LC + c) / 2 + 1]);
-            sts128(row + (((c >> 2) ^ (key & 7)) << 4), __float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x),
-                   __float_as_uint(y.y));
-          }
-          __syncwarp();
-          float x[4] = {0.f, 0.f, 0.f, 0.f};  // column `lane` over the warp's 32 keys
-          const uint32_t rows = row - (uint32_t)lane * 128 + (lane & 3) * 4;
-#pragma unroll 2
-          for (int k = 0; k < 32; k += 4)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[e] += __uint_as_float(lds32(rows + (k + e) * 128 + (((lane >> 2) ^ ((k + e) & 7)) << 4)));
-          if (lane < LC) sh.mx[in_wg][own0 + h * LC + lane] = (x[0] + x[1]) + (x[2] + x[3]);
-          __syncwarp();
+        for (int j = 0; j < J; ++j) {
+          const float2 x = fold(unpack2(l[j]), [](float x, float y) { return x + y; });
+          if (lane < 4) *reinterpret_cast<float2*>(&sh.sum[in_wg][own0 + 8 * j + t2]) = x;
         }
         if (!meet()) break;
-        const int c = in_wg * 32 + lane, r = col0 + c;
-        if (c < NC && r < si.rows) {
-          const int col = own0 + c;
-          const float x = (sh.mx[0][col] + sh.mx[1][col]) + (sh.mx[2][col] + sh.mx[3][col]);
-          a.part_ml[out + r] = first ? make_float2(-INFINITY, 0.f) : make_float2(-sh.nm[col], x);
-          if (info.flags & kOnly) a.part_ml[out + r + (wg ? -a.rows : a.rows)] = make_float2(-INFINITY, 0.f);
+        if (in_wg == 0 && lane < 4) {
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const float2 n = unpack2(nm[j]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int c = 8 * j + t2 + e, r = col0 + c;
+              if (r >= si.rows) continue;
+              const float x = (sh.sum[0][own0 + c] + sh.sum[1][own0 + c]) + (sh.sum[2][own0 + c] + sh.sum[3][own0 + c]);
+              a.part_ml[out + r] = first ? make_float2(-INFINITY, 0.f) : make_float2(e ? -n.y : -n.x, x);
+              if (info.flags & kOnly) a.part_ml[out + r + (wg ? -a.rows : a.rows)] = make_float2(-INFINITY, 0.f);
+            }
+          }
         }
         if (!meet()) break;  // the exchange array is free again
       }
