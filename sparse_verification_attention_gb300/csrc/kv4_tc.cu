@@ -216,6 +216,13 @@ __device__ __forceinline__ void st_16x256b_x1(uint32_t taddr, const uint32_t (&r
                "r"(r[2]), "r"(r[3])
                : "memory");
 }
+// bulk_load under an L2 policy.
+__device__ __forceinline__ void bulk_load_once(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
 // Four 8 x 8 blocks of halves, a row of block b at the address in lane 8 b + row.
 __device__ __forceinline__ void put(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1), "r"(r2),
@@ -745,6 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       // earlier kernels' plain stores to the pools come before this one's bulk copies
       asm volatile("fence.proxy.async.global;" ::: "memory");
       unsigned flags = bad ? SV_FLAG_BAD_LENGTH : 0u;
+      const uint64_t once = l2_evict_first_policy();
       uint32_t i = 0, st = 0, ph = 0, seg = 0;
       bool ok = true;
       for (int x = begin; ok && x < end; ++seg) {
@@ -833,8 +841,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
             __syncwarp();
             if ((lane >> 3) == t && (heads >> lane & 1u)) {
               const uint32_t dst = ring + st * stage_bytes + (lane & 7) * pb;
-              bulk_load(dst, k_from, run * pb, bar);
-              bulk_load(dst + side, v_from, run * pb, bar);
+              bulk_load_once(dst, k_from, run * pb, bar, once);
+              bulk_load_once(dst + side, v_from, run * pb, bar, once);
             }
             if (++st == (uint32_t)stages) st = 0, ph ^= 1u;
           }
