@@ -94,8 +94,12 @@ __device__ __forceinline__ float exp2i(int e) { return __int_as_float((127 + e) 
 // what runs once costs the fetch of its code (about 12 cycles an instruction).
 static __device__ __noinline__ int quotient(int x, int y) { return x / y; }
 
+// (Pages and groups of query heads are powers of two nearly always.)
+__device__ __forceinline__ int blocks_in(const Attend4Args& a, int ctx) {
+  return a.ppb_shift >= 0 ? ctx >> (a.ppb_shift + 4) : quotient(ctx, a.blk);
+}
 __device__ __forceinline__ int pieces_of(const Attend4Args& a, int ctx) {
-  const int full = quotient(ctx, a.blk), rest = ctx - full * a.blk;
+  const int full = blocks_in(a, ctx), rest = ctx - full * a.blk;
   return (a.sel ? a.n_sel : full) * a.ppb + (rest + kPiece - 1) / kPiece;
 }
 
@@ -156,11 +160,11 @@ struct Segment {
 __device__ __forceinline__ Segment segment_at(const Attend4Args& a, const int* cu, const int* ctx, int x, int end,
                                               int cta) {
   Segment s;
-  const int per = a.Hkv * a.row_tiles, y = quotient(x, per);
-  int lo = 0, hi = a.B;  // the last b with cu[b] <= y; the sequences without keys before it do not count
+  const int per = a.Hkv * a.row_tiles;
+  int lo = 0, hi = a.B;  // the last sequence that begins at x or before (those without keys do not count)
   while (hi - lo > 1) {
     const int m = (lo + hi) >> 1;
-    if (cu[m] <= y) lo = m;
+    if (cu[m] * per <= x) lo = m;
     else hi = m;
   }
   s.b = lo;
@@ -170,7 +174,7 @@ __device__ __forceinline__ Segment segment_at(const Attend4Args& a, const int* c
   s.rt = pair - s.h * a.row_tiles;
   s.tiles = min(n - s.tile0, end - x);
   s.ctx = ctx[lo];
-  s.full = quotient(s.ctx, a.blk);
+  s.full = blocks_in(a, s.ctx);
   s.pieces = (a.sel ? a.n_sel : s.full) * a.ppb + (s.ctx - s.full * a.blk + kPiece - 1) / kPiece;
   s.slot = lo * per + pair + cta;
   return s;
@@ -182,7 +186,7 @@ __device__ __forceinline__ long long piece_at(const Attend4Args& a, const Segmen
                                               unsigned* flags) {
   *valid = 0;
   if (i >= s.pieces) return -1;
-  const int slots = a.sel ? a.n_sel : s.full, at = quotient(i, a.ppb);
+  const int slots = a.sel ? a.n_sel : s.full, at = a.ppb_shift >= 0 ? i >> a.ppb_shift : quotient(i, a.ppb);
   int block = at, sub = i - at * a.ppb;
   if (at >= slots) {  // the partial last block
     block = s.full;
@@ -209,7 +213,7 @@ __device__ __forceinline__ long long piece_at(const Attend4Args& a, const Segmen
 
 // Row r of a (sequence, head): draft t, query head h * G + g, r = t * G + g.
 __device__ __forceinline__ long long row_at(const Attend4Args& a, int b, int h, int r) {
-  const int t = quotient(r, a.G);
+  const int t = a.g_shift >= 0 ? r >> a.g_shift : quotient(r, a.G);
   return ((long long)b * a.T + t) * a.Hq + h * a.G + (r - t * a.G);
 }
 

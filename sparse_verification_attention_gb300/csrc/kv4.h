@@ -68,7 +68,7 @@ cudaError_t launch_reps_kv4(const Reps4Args& a, cudaStream_t st);
 // ---------------------------------------------------------------- attention
 constexpr int kMaxB4 = 1024;         // sequences of a call
 constexpr int kSimt4Rows = 32;       // row tile on the CUDA cores
-constexpr int kTc4Rows = 128;        // ... and on the tensor cores, at most
+constexpr int kTc4Rows = 64;         // ... and on the tensor cores, at most
 constexpr int kMaxSimt4Ctas = 640;   // CTAs of a launch at most
 constexpr int kMaxTc4Ctas = 160;
 
@@ -94,7 +94,7 @@ struct Attend4Args {
   int rows, row_tiles;  // rows of a row tile (of all but the last), row tiles of a (b, h)
   int streams;    // 2: a segment's even and odd tiles are summed apart
   int ppb, ppt, ppt_shift;  // pieces of a block and of a key tile (a power of two)
-  int ppb_shift;            // log2(ppb), -1 if it is no power of two
+  int ppb_shift, g_shift;   // log2 of ppb and of G, -1 where it is no power of two
   int ctas;
   float scale_log2;  // log2(e) / sqrt(d)
   unsigned long long anc[kMaxT];

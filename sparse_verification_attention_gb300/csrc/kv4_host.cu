@@ -133,9 +133,7 @@ Layout4 layout4(const sv_shape& s) {
   const int most[2] = {kSimt4Rows, kTc4Rows}, ctas[2] = {kMaxSimt4Ctas, kMaxTc4Ctas};
   for (int i = 0; i < 2; ++i) {
     const long long tiles = (stacked + most[i] - 1) / most[i], r = std::min<long long>(most[i], stacked);
-    // (up to 64 rows the tensor cores sum in two streams)
-    const int streams = i == 1 && r <= 64 ? 2 : 1;
-    rows = std::max(rows, (size_t)((tiles * pairs + ctas[i]) * streams * r));
+    rows = std::max(rows, (size_t)((tiles * pairs + ctas[i]) * (i + 1) * r));  // (two streams on the tensor cores)
   }
   Layout4 L;
   L.cu = kStatusBytes;
@@ -355,6 +353,7 @@ sv_status sv_attend_kv4(const sv_shape* shape, const void* q, const sv_kv4* kv, 
   a.sel_stride = sel_stride;
   a.ppb = shape->blk / kPiece;
   a.ppb_shift = a.ppb & (a.ppb - 1) ? -1 : __builtin_ctz(a.ppb);
+  a.g_shift = a.G & (a.G - 1) ? -1 : __builtin_ctz(a.G);
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)shape->d));
   fill_ancestors(draft_parent, shape->T, a.anc);
   const cudaError_t e = attend4_tc_applies(a, shape->dtype) ? launch_attend4_tc(a, (cudaStream_t)stream)

@@ -9,6 +9,7 @@ namespace {
 using namespace kv4;
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 4;  // drafts, or parts of a row, whose loads are under way together
 
 // Four consecutive elements as floats, and back.
 __device__ __forceinline__ float4 load4(const float* p) { return __ldcg(reinterpret_cast<const float4*>(p)); }
@@ -44,11 +45,10 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) join4_kernel(const __grid_constant__ Attend4Args a) {
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  pdl_wait();
-  pdl_trigger();
   if (row >= (long long)a.B * a.T * a.Hq) return;
-  const int tok = (int)(row / a.Hq), head = (int)(row - (long long)tok * a.Hq), b = tok / a.T, t = tok - b * a.T;
-  const int h = head / a.G, r = t * a.G + head - h * a.G, rt = r / a.rows;
+  const int tok = quotient((int)row, a.Hq), head = (int)row - tok * a.Hq, b = quotient(tok, a.T), t = tok - b * a.T;
+  const int h = a.g_shift >= 0 ? head >> a.g_shift : quotient(head, a.G), r = t * a.G + head - h * a.G;
+  const int rt = a.row_tiles == 1 ? 0 : quotient(r, a.rows);
   const bool has[2] = {lane * 4 < a.d, 128 + lane * 4 < a.d};
   float4 q[2], o[2];
 #pragma unroll
@@ -63,16 +63,31 @@ __global__ void __launch_bounds__(kThreads) join4_kernel(const __grid_constant__
   const T* dv = static_cast<const T*>(a.draft_v) + ((long long)b * a.T * a.Hkv + h) * a.d;
   const long long step = (long long)a.Hkv * a.d;
   float s0 = -INFINITY, s1 = -INFINITY;
-  int i = 0;
-  for (unsigned long long w = see; w; w &= w - 1, ++i) {
-    const T* k = dk + (__ffsll(w) - 1) * step;
-    float x = 0.f;
+  int u[kBatch];
+#pragma unroll 1
+  for (unsigned long long w = see, i = 0; w; i += kBatch) {
+    float x[kBatch];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (has[j]) x += dot4(q[j], load4(k + 128 * j + lane * 4));
-    x = warp_sum(x) * a.scale_log2;
-    if (lane == (i & 31)) (i < 32 ? s0 : s1) = x;
+    for (int e = 0; e < kBatch; ++e) {  // (a batch's loads are under way together)
+      u[e] = w ? __ffsll(w) - 1 : -1;
+      w &= w - 1;
+      x[e] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (u[e] >= 0 && has[j]) x[e] += dot4(q[j], load4(dk + u[e] * step + 128 * j + lane * 4));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) x[e] += __shfl_xor_sync(0xffffffffu, x[e], o);
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e)
+      if (u[e] >= 0 && lane == (((int)i + e) & 31)) ((int)i < 32 ? s0 : s1) = x[e] * a.scale_log2;
   }
+  // What comes above is older than the attention kernel, which began to let this one in
+  // only behind its own wait for its predecessors; what follows is the attention's.
+  pdl_wait();
+  pdl_trigger();
   // the row's segments: CTAs c0 .. c1 of the line
   const int start = a.cu[b], tiles = a.cu[b + 1] - start, per = a.Hkv * a.row_tiles;
   const int pair = h * a.row_tiles + rt;
@@ -92,23 +107,47 @@ __global__ void __launch_bounds__(kThreads) join4_kernel(const __grid_constant__
   const float p0 = lane < n ? exp2f(s0 - m) : 0.f, p1 = lane + 32 < n ? exp2f(s1 - m) : 0.f;
   float l = warp_sum(p0 + p1);
   const float unit = exp2i(head_exp(a.v_exp, h));
-  for (int c = 0; c < parts; ++c) {
-    const long long at = at0 + (long long)c * a.rows;
-    const float2 ml = __ldcg(a.part_ml + at);
-    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // no key of the segment counted
-    const float w = exp2f(ml.x - m);
-    l += w * ml.y;
+#pragma unroll 1
+  for (int c0 = 0; c0 < parts; c0 += kBatch) {
+    float2 ml[kBatch];
+    float4 x[kBatch][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (has[j]) axpy4(o[j], w * unit, load4(a.part_o + at * a.d + 128 * j + lane * 4));
+    for (int e = 0; e < kBatch; ++e) {
+      const long long at = at0 + (long long)(c0 + e) * a.rows;
+      if (c0 + e >= parts) continue;
+      ml[e] = __ldcg(a.part_ml + at);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (has[j]) x[e][j] = load4(a.part_o + at * a.d + 128 * j + lane * 4);
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      if (c0 + e >= parts || (ml[e].x == -INFINITY && ml[e].y == 0.f)) continue;  // no key of the part counted
+      const float w = exp2f(ml[e].x - m);
+      l += w * ml[e].y;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (has[j]) axpy4(o[j], w * unit, x[e][j]);
+    }
   }
-  i = 0;
-  for (unsigned long long w = see; w; w &= w - 1, ++i) {
-    const T* v = dv + (__ffsll(w) - 1) * step;
-    const float p = __shfl_sync(0xffffffffu, i < 32 ? p0 : p1, i & 31);
+#pragma unroll 1
+  for (unsigned long long w = see, i = 0; w; i += kBatch) {
+    float4 x[kBatch][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (has[j]) axpy4(o[j], p, load4(v + 128 * j + lane * 4));
+    for (int e = 0; e < kBatch; ++e) {
+      u[e] = w ? __ffsll(w) - 1 : -1;
+      w &= w - 1;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (u[e] >= 0 && has[j]) x[e][j] = load4(dv + u[e] * step + 128 * j + lane * 4);
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const float p = __shfl_sync(0xffffffffu, (int)i < 32 ? p0 : p1, ((int)i + e) & 31);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (u[e] >= 0 && has[j]) axpy4(o[j], p, x[e][j]);
+    }
   }
   const float inv = __frcp_rn(l);
 #pragma unroll

@@ -54,9 +54,9 @@ constexpr int kKeys = 128, kPieces = kKeys / kPiece;
 constexpr int kInfo = 16, kSegs = 16, kF = 8;
 constexpr int kMaxStages = 8;
 constexpr int kThreads = 640;
-constexpr int kSoftmaxWarp = 8, kLoadWarp = 16, kScoreWarp = 17, kOutWarp = 18;  // 19 lays out Q
+constexpr int kSoftmaxWarp = 8, kKLoadWarp = 16, kVLoadWarp = 17, kScoreWarp = 18;  // 19: O
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 0, kColS = 128, kColK = 256, kColV = 384;  // K and V: two of 64 columns
+constexpr uint32_t kColO = 0, kColS = 128, kColK = 256;  // two of at most 64 columns each
 constexpr float kLift = 7.f;    // weights are 2^kLift times their size ...
 constexpr float kTop = 32768.f; // ... and below this, so that f16 (65504) holds them
 // References move when a key's weights sum up to more than kTop: one of at most 64 is
@@ -90,29 +90,20 @@ struct Control {
   TileInfo info[kInfo];
   SegInfo seg[kSegs];
   alignas(16) float f[kF][kTc4Rows];   // factor of a row's scores
-  alignas(16) float mx[4][kTc4Rows], sum[4][kTc4Rows];  // by warp of a softmax warpgroup
+  alignas(16) float mx[4][2 * kTc4Rows], sum[4][2 * kTc4Rows];  // by warp of a warpgroup: both streams' columns
   int cu[kMaxB4 + 1], ctx[kMaxB4];
 };
 
 template <int N>
 struct Cfg {
-  static constexpr bool kAlt = N <= 64;              // even and odd tiles apart
-  static constexpr int kCols = kAlt ? N : N / 2;     // rows (columns) of a softmax warpgroup
-  static constexpr int kQ = N <= 64 ? 2 : 1;         // Q buffers
-  static constexpr int kQBytes = 2 * N * 128;        // two blocks of 64 dims
-  static constexpr int kPBytes = (N > 64 ? 2 : 1) * kKeys * 128;
-  static constexpr bool kVSmem = N <= 64;            // V as halves in shared memory, not in TMEM
-  static constexpr int kVBytes = kVSmem ? 2 * kKeys * 128 : 0;
-  static constexpr int kFixed = kQ * kQBytes + 2 * kPBytes + 2 * kVBytes + (int)sizeof(Control);
+  static constexpr int kQBytes = 2 * N * 128;       // two blocks of 64 dims
+  static constexpr int kPBytes = kKeys * 128;       // a key's 64 columns
+  static constexpr int kVBytes = 2 * kKeys * 128;   // two blocks of 64 dims
+  static constexpr int kFixed = 2 * (kQBytes + kPBytes + kVBytes) + (int)sizeof(Control);
 };
 
 __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -128,9 +119,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 r;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
   return r;
-}
-__device__ __forceinline__ void sts32(uint32_t a, uint32_t x) {
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   uint32_t r;
@@ -166,16 +154,6 @@ __device__ __forceinline__ int dim_of(int m) {
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-// 16 lanes x 32 columns of TMEM: four blocks of 8 columns; of a block, the lane's
-// registers are row lane / 4 (columns 2 (lane % 4), + 1) and row lane / 4 + 8.
-__device__ __forceinline__ void st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 // Instruction descriptor of kind::f16 with f16 operands and fp32 sums, M = 128.
 __host__ __device__ constexpr uint32_t idesc_f16(int n, bool a_mn, bool b_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
@@ -187,7 +165,8 @@ __device__ __forceinline__ void ld8(uint32_t taddr, uint32_t* r) {
                : "r"(taddr)
                : "memory");
 }
-// 16 lanes x 8 N columns of TMEM into 4 N registers (see st_16x256b_x4).
+// 16 lanes x 8 N columns of TMEM into 4 N registers: of eight columns, a lane has those at
+// 2 (lane % 4) and behind it in row lane / 4, and the same in row lane / 4 + 8.
 template <int N>
 __device__ __forceinline__ void ld_16x256b(uint32_t taddr, uint32_t* r) {
   if constexpr (N == 1) {
@@ -308,14 +287,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
   using C = Cfg<N>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t q_base = base, p_base = q_base + C::kQ * C::kQBytes;
-  const uint32_t v_base = p_base + 2 * C::kPBytes, ctl = v_base + 2 * C::kVBytes;
+  const uint32_t q_base = base, p_base = q_base + 2 * C::kQBytes, v_base = p_base + 2 * C::kPBytes;
+  const uint32_t ctl = v_base + 2 * C::kVBytes;
   Control& sh = *reinterpret_cast<Control*>(smem_raw + (ctl - smem_u32(smem_raw)));
   const uint32_t ring = ctl + (uint32_t)((sizeof(Control) + 127) / 128 * 128);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int groups = DG ? DG : a.d / 16;
   const uint32_t pb = (uint32_t)piece_bytes(groups * 16), side = kPieces * pb, stage_bytes = 2 * side;
-  constexpr uint32_t kSharers = C::kAlt ? 4 : 8;  // softmax warps of a tile
 
   if (warp == kScoreWarp) {
     tc::alloc(smem_u32(&sh.tmem), kTmemCols);
@@ -324,17 +302,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
   if (tid == 0) {
 #pragma unroll 1
     for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.full[i]), 2);
       mbar_init(smem_u32(&sh.empty[i]), 8);
     }
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sh.s_ready[i]), 4 + kSharers);
+      mbar_init(smem_u32(&sh.s_ready[i]), 8);
       mbar_init(smem_u32(&sh.k_empty[i]), 1);
       mbar_init(smem_u32(&sh.s_full[i]), 1);
-      mbar_init(smem_u32(&sh.o_ready[i]), 4 + kSharers);
+      mbar_init(smem_u32(&sh.o_ready[i]), 8);
       mbar_init(smem_u32(&sh.pv_done[i]), 1);
-      mbar_init(smem_u32(&sh.o_empty[i]), kSharers);
+      mbar_init(smem_u32(&sh.o_empty[i]), 4);
       mbar_init(smem_u32(&sh.q_full[i]), 1);
       mbar_init(smem_u32(&sh.drained[i]), 1);
       mbar_init(smem_u32(&sh.q_empty[i]), 1);
@@ -348,8 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
   pdl_wait();
   pdl_trigger();
   bool bad = false;
-  if (warp == kLoadWarp) {
+  if (warp == kKLoadWarp) {
     bad = scan_tiles(a, sh.cu, sh.ctx);
+    if (bad) atomicOr(a.status, SV_FLAG_BAD_LENGTH);
     __syncwarp();
   }
   tc::fence_before();
@@ -409,114 +388,67 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       if (++st == (uint32_t)stages) st = 0, ph ^= 1u;
     }
   } else if (warp < kSoftmaxWarp) {
-    // ------------------------------------------------------------ V: lane = dim
+    // ------------------------------------------------------------ V: halves into shared memory
     const int w = warp & 3;
-    const uint32_t t4 = lane & 3;  // code row lane / 4 (that dim and the one 8 behind), tokens 4 t4 ..
     for (uint32_t i = 0, st = 0, ph = 0; i < tiles; ++i) {
       if (!wait(sh.full[st], ph, 3u)) break;
       if (!wait(sh.pv_done[i & 1], (i >> 1) ^ 1u, 4u)) break;
       tc::fence_after();
       const uint64_t valid = sh.info[i % kInfo].valid;
       const uint32_t from = ring + st * stage_bytes + side;
-      if constexpr (C::kVSmem) {
-        // A thread has 4 code rows (8 dims: rows c .. c + 3 hold them and those 8 behind) of a
-        // piece's 16 tokens: row = key, 128 bytes of 64 dims, 128-byte swizzle. The rows are taken
-        // in an order that differs from group to group, so that the loads of 8 lanes fall
-        // into different banks; dim_of() undoes it.
-        const uint32_t cb = lane & 1, gq = lane >> 1 & 3, half = lane >> 3 & 1, p = 2 * w + (lane >> 4), g = half * 4 + gq;
-        if (DG || (int)g < groups) {
-          const uint32_t at = from + p * pb;
-          uint4 c[4], sc = lds128(at + groups * 128 + g * 16);
+      // A thread has 4 code rows (8 dims: rows c .. c + 3 hold them and those 8 behind) of a
+      // piece's 16 tokens: row = key, 128 bytes of 64 dims, 128-byte swizzle. The rows are taken
+      // in an order that differs from group to group, so that the loads of 8 lanes fall
+      // into different banks; dim_of() undoes it.
+      const uint32_t cb = lane & 1, gq = lane >> 1 & 3, half = lane >> 3 & 1, p = 2 * w + (lane >> 4), g = half * 4 + gq;
+      if (DG || (int)g < groups) {
+        const uint32_t at = from + p * pb;
+        uint4 c[4], sc = lds128(at + groups * 128 + g * 16);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) c[r] = lds128(at + g * 128 + (4 * cb + ((r + gq) & 3)) * 16);
-          if (valid != kAllValid) {  // tokens that do not count: a scale of zero, whatever the bytes hold
-            const int n = (int)(valid >> (8 * p) & 0xff);
-            sc.x &= first_bytes(n), sc.y &= first_bytes(n - 4), sc.z &= first_bytes(n - 8), sc.w &= first_bytes(n - 12);
-          }
-          const uint32_t to = v_base + (i & 1) * C::kVBytes + half * (kKeys * 128) + p * kPiece * 128;
-          auto four = [&](int k, uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t s4) {  // tokens 4 k ..
-            uint32_t f[4][4], s01, s23;
-            e4m3x4_to_f16(s4, s01, s23);
-            e2m1x8_to_f16(c0, f[0]);
-            e2m1x8_to_f16(c1, f[1]);
-            e2m1x8_to_f16(c2, f[2]);
-            e2m1x8_to_f16(c3, f[3]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t s1 = j < 2 ? s01 : s23;
-              uint32_t h[4];
-#pragma unroll
-              for (int r = 0; r < 4; ++r) h[r] = j & 1 ? mul_by_half<1>(f[r][j], s1) : mul_by_half<0>(f[r][j], s1);
-              const uint32_t tok = 4 * k + j;
-              sts128(to + tok * 128 + (((2 * gq + cb) ^ (tok & 7)) << 4), h[0], h[1], h[2], h[3]);
-            }
-          };
-          four(0, c[0].x, c[1].x, c[2].x, c[3].x, sc.x);
-          four(1, c[0].y, c[1].y, c[2].y, c[3].y, sc.y);
-          four(2, c[0].z, c[1].z, c[2].z, c[3].z, sc.z);
-          four(3, c[0].w, c[1].w, c[2].w, c[3].w, sc.w);
+        for (int r = 0; r < 4; ++r) c[r] = lds128(at + g * 128 + (4 * cb + ((r + gq) & 3)) * 16);
+        if (valid != kAllValid) {  // tokens that do not count: a scale of zero, whatever the bytes hold
+          const int n = (int)(valid >> (8 * p) & 0xff);
+          sc.x &= first_bytes(n), sc.y &= first_bytes(n - 4), sc.z &= first_bytes(n - 8), sc.w &= first_bytes(n - 12);
         }
-        arrive(sh.empty[st]);
-        fence_proxy_async_shared();
-      } else {
-        if (valid != kAllValid) {
-          // tokens that do not count get a scale of zero, whatever their bytes hold: the
-          // warp's two groups x 128 tokens, 4 tokens at a time
-          for (int e = lane; e < 64; e += 32) {
-            const int g = 2 * w + (e >> 5), p = e >> 2 & 7, n = (int)(valid >> (8 * p) & 0xff) - (e & 3) * 4;
-            const uint32_t at = from + p * pb + groups * 128 + g * 16 + (e & 3) * 4;
-            if (g < groups && n < 4) sts32(at, n <= 0 ? 0u : lds32(at) & ((1u << (8 * n)) - 1u));
-          }
-          fence_proxy_async_shared();  // ahead of the next copy into the stage
-          __syncwarp();
-        }
-#pragma unroll 1
-        for (int q = 0; q < 2; ++q) {  // the warp's two groups
-          const int g = 2 * w + q;
-          if (!DG && g >= groups) break;
-          const uint32_t code = from + g * 128 + lane * 4, scale = from + groups * 128 + g * 16 + t4 * 4;
-          uint32_t c[8], sc[8], r[2][16];
+        const uint32_t to = v_base + (i & 1) * C::kVBytes + half * (kKeys * 128) + p * kPiece * 128;
+        auto four = [&](int k, uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t s4) {  // tokens 4 k ..
+          uint32_t f[4][4], s01, s23;
+          e4m3x4_to_f16(s4, s01, s23);
+          e2m1x8_to_f16(c0, f[0]);
+          e2m1x8_to_f16(c1, f[1]);
+          e2m1x8_to_f16(c2, f[2]);
+          e2m1x8_to_f16(c3, f[3]);
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            c[p] = lds32(code + p * pb);
-            sc[p] = lds32(scale + p * pb);
-          }
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t s1 = j < 2 ? s01 : s23;
+            uint32_t h[4];
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            const uint32_t c4 = c[p] << 4, c8 = c[p] << 8;
-            // bytes 1 and 3: tokens (0, 1) and (2, 3) of the one dim, and of the other
-            const uint32_t lo = (c8 & 0x0f000f00u) | (c4 & 0xf0fff0ffu), hi = (c4 & 0x0f000f00u) | (c[p] & 0xf0fff0ffu);
-            uint32_t s01, s23, *to = r[p >> 2] + 4 * (p & 3);
-            e4m3x4_to_f16(sc[p], s01, s23);
-            e2m1x4_to_f16(lo, to[0], to[1]);
-            e2m1x4_to_f16(hi, to[2], to[3]);
-            to[0] = mul_f16x2(to[0], s01);
-            to[1] = mul_f16x2(to[1], s23);
-            to[2] = mul_f16x2(to[2], s01);
-            to[3] = mul_f16x2(to[3], s23);
+            for (int r = 0; r < 4; ++r) h[r] = j & 1 ? mul_by_half<1>(f[r][j], s1) : mul_by_half<0>(f[r][j], s1);
+            const uint32_t tok = 4 * k + j;
+            sts128(to + tok * 128 + (((2 * gq + cb) ^ (tok & 7)) << 4), h[0], h[1], h[2], h[3]);
           }
-          const uint32_t at = tmem + ((uint32_t)(w * 32 + q * 16) << 16) + kColV + (i & 1) * 64;
-          st_16x256b_x4(at, r[0]);
-          st_16x256b_x4(at + 32, r[1]);
-        }
-        arrive(sh.empty[st]);
-        tc::wait_st();
-        tc::fence_before();
+        };
+        four(0, c[0].x, c[1].x, c[2].x, c[3].x, sc.x);
+        four(1, c[0].y, c[1].y, c[2].y, c[3].y, sc.y);
+        four(2, c[0].z, c[1].z, c[2].z, c[3].z, sc.z);
+        four(3, c[0].w, c[1].w, c[2].w, c[3].w, sc.w);
       }
+      arrive(sh.empty[st]);
+      fence_proxy_async_shared();
       arrive(sh.o_ready[i & 1]);
       if (++st == (uint32_t)stages) st = 0, ph ^= 1u;
     }
-  } else if (warp < kLoadWarp) {
+  } else if (warp < kKLoadWarp) {
     // ------------------------------------------------------------ softmax
     // TMEM gives a thread the scores of 4 keys (lane / 4 and those 8, 16 and 24 behind) and of
     // two neighbouring columns in every eight: the factors, references and sums of NC / 4
     // columns stay in registers. (With a key a thread and all columns they came from shared
     // memory, 16 loads of 16 bytes a tile that the other roles' traffic held up: 800 to
     // 1200 cycles for 80 instructions.)
-    constexpr int NC = C::kCols, CH = NC < 32 ? NC : 32, NCH = NC / CH, J = NC / 8;
+    constexpr int NC = N, CH = NC < 32 ? NC : 32, NCH = NC / CH, J = NC / 8;
     const int wg = (warp - kSoftmaxWarp) >> 2, quad = warp & 3, in_wg = (warp - kSoftmaxWarp) & 3;
-    // columns of S and of P, and of O and the exchange arrays
-    const int col0 = C::kAlt ? 0 : wg * NC, own0 = wg * NC;
+    // the stream's columns of O and of the exchange arrays
+    const int own0 = wg * NC;
     const int g = lane >> 2, t2 = (lane & 3) * 2;  // key in eight, column in eight
     const uint32_t tlane = (uint32_t)(quad * 32) << 16, tmem_o = tmem + tlane + kColO + own0;
     // this lane's row of the 8 x 8 blocks that it addresses for P's stores (see put)
@@ -526,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       lay_out_q(a, s, N, q_base, sh.f[0], warp - kSoftmaxWarp, 8);
       arrive(sh.q_first);
     }
-    arrive(sh.s_ready[C::kAlt ? wg : 0]);  // S is free
+    arrive(sh.s_ready[wg]);  // S is free
     uint64_t f[J], nm[J], l[J];  // factor, minus (reference - kLift), sum: two columns each
     bool first = true;           // no key of the stream has counted yet
     uint32_t met = 0;
@@ -544,15 +476,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       }
       return x;
     };
-    for (uint32_t i = C::kAlt ? wg : 0; i < tiles; i += C::kAlt ? 2 : 1) {
-      const uint32_t sb = C::kAlt ? wg : 0;  // S buffer, used every (or every other) tile
-      const uint32_t turn = C::kAlt ? i >> 1 : i;
-      if (!wait(sh.s_full[sb], turn, 5u)) break;
+    for (uint32_t i = wg; i < tiles; i += 2) {  // (i & 1 = wg: the buffers of S, P and O)
+      const uint32_t turn = i >> 1;
+      if (!wait(sh.s_full[wg], turn, 5u)) break;
       tc::fence_after();
       const TileInfo info = sh.info[i % kInfo];
       if (info.flags & kFirst) {
         first = true;
-        const float* ff = sh.f[info.seg % kF] + col0 + t2;
+        const float* ff = sh.f[info.seg % kF] + t2;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           f[j] = *reinterpret_cast<const uint64_t*>(ff + 8 * j);
@@ -565,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
         const int v0 = (int)(info.valid >> (16 * quad) & 0xff), v1 = (int)(info.valid >> (16 * quad + 8) & 0xff);
         on[0] = g < v0, on[1] = g + 8 < v0, on[2] = g < v1, on[3] = g + 8 < v1;
       }
-      const uint32_t tmem_s = tmem + tlane + kColS + sb * 64 + col0;
+      const uint32_t tmem_s = tmem + tlane + kColS + wg * 64;
       uint32_t s[2][CH / 2], p[NCH][2][CH / 4];
       uint64_t sums[J];
       // scores of keys 0 .. 15 and 16 .. 31 of the warp's: columns 8 j + t2 (+ 1) of key g in
@@ -638,8 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
           }
           if (!first) {
             // every product into O is complete
-            if (!(ok = C::kAlt ? wait(sh.pv_done[sb], turn ^ 1u, 6u) : wait(sh.pv_done[(i - 1) & 1], (i - 1) >> 1, 6u)))
-              break;
+            if (!(ok = wait(sh.pv_done[wg], turn ^ 1u, 6u))) break;
             tc::fence_after();
 #pragma unroll
             for (int j = 0; j < J; ++j) {
@@ -679,13 +609,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       }
       if (!ok) break;
       tc::fence_before();
-      arrive(sh.s_ready[C::kAlt ? sb : (i + 1) & 1]);  // S has been read: room for the next in its place
+      arrive(sh.s_ready[wg]);  // S has been read: room for the next in its place
 #pragma unroll
       for (int j = 0; j < J; ++j) l[j] = add2(l[j], sums[j]);
       // P^T into shared memory: row = key, 128 bytes of 64 columns, 128-byte swizzle; 8 x 8 blocks
       // as they lie in the registers
-      if (!wait(sh.pv_done[i & 1], (i >> 1) ^ 1u, 7u)) break;
-      const uint32_t row = p_base + (i & 1) * C::kPBytes + (uint32_t)(col0 >> 6) * (kKeys * 128) + (uint32_t)prow * 128;
+      if (!wait(sh.pv_done[wg], turn ^ 1u, 7u)) break;
+      const uint32_t row = p_base + wg * C::kPBytes + (uint32_t)prow * 128;
 #pragma unroll
       for (int ch = 0; ch < NCH; ++ch) {
         const uint32_t at = row + (uint32_t)(((ch * (CH / 8) + pchunk) ^ (lane & 7)) << 4);
@@ -702,14 +632,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       }
       fence_proxy_async_shared();
       tc::fence_before();
-      arrive(sh.o_ready[i & 1]);
+      arrive(sh.o_ready[wg]);
       if (info.flags & kLast) {
         // the stream's sums: O from TMEM (lane = dim), l over the 128 keys' threads
-        if (!wait(sh.pv_done[i & 1], i >> 1, 8u)) break;
+        if (!wait(sh.pv_done[wg], turn, 8u)) break;
         tc::fence_after();
         const SegInfo si = sh.seg[info.seg % kSegs];
-        const long long out = ((long long)si.slot * (C::kAlt ? 2 : 1) + (C::kAlt ? wg : 0)) * a.rows;
-        const int m = quad * 32 + lane, dim = C::kVSmem ? dim_of(m) : m;
+        const long long out = (2ll * si.slot + wg) * a.rows;
+        const int m = quad * 32 + lane, dim = dim_of(m);
 #pragma unroll 1
         for (int c0 = 0; c0 < NC; c0 += 8) {
           uint32_t o[8];
@@ -718,11 +648,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
           if (m < groups * 16) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (col0 + c0 + e < si.rows) a.part_o[(out + col0 + c0 + e) * (groups * 16) + dim] = __uint_as_float(o[e]);
+              if (c0 + e < si.rows) a.part_o[(out + c0 + e) * (groups * 16) + dim] = __uint_as_float(o[e]);
           }
         }
         tc::fence_before();
-        arrive(sh.o_empty[C::kAlt ? wg : 0]);
+        arrive(sh.o_empty[wg]);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           const float2 x = fold(unpack2(l[j]), [](float x, float y) { return x + y; });
@@ -735,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
             const float2 n = unpack2(nm[j]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int c = 8 * j + t2 + e, r = col0 + c;
+              const int c = 8 * j + t2 + e, r = c;
               if (r >= si.rows) continue;
               const float x = (sh.sum[0][own0 + c] + sh.sum[1][own0 + c]) + (sh.sum[2][own0 + c] + sh.sum[3][own0 + c]);
               a.part_ml[out + r] = first ? make_float2(-INFINITY, 0.f) : make_float2(e ? -n.y : -n.x, x);
@@ -747,18 +677,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       }
     }
   } else {
-    if (warp == kLoadWarp) {
+    if (warp == kKLoadWarp || warp == kVLoadWarp) {
       // ------------------------------------------------------------ segments, pages, copies
+      // One warp copies K and tells the others of a tile, one copies V and lays out Q of the
+      // segments behind the first. (A copy takes its warp 110 cycles, and a tile of two pages
+      // is four.)
+      const bool is_v = warp == kVLoadWarp;
+      const uint8_t* pool = is_v ? a.v_pool : a.k_pool;
       // earlier kernels' plain stores to the pools come before this one's bulk copies
       asm volatile("fence.proxy.async.global;" ::: "memory");
-      unsigned flags = bad ? SV_FLAG_BAD_LENGTH : 0u;
+      unsigned flags = 0;
       const uint64_t once = l2_evict_first_policy();
       uint32_t i = 0, st = 0, ph = 0, seg = 0;
       bool ok = true;
       for (int x = begin; ok && x < end; ++seg) {
         const Segment s = next_segment(a, sh, x, end);
         x += s.tiles;
-        if (lane == 0) {
+        if (is_v) {
+          if (seg > 0) {
+            // (its buffer's segment before, the first one too, has been multiplied)
+            if (seg > 1 && !(ok = wait(sh.q_empty[seg & 1], (seg >> 1) - 1, 10u))) break;
+            lay_out_q(a, s, N, q_base + (seg & 1) * C::kQBytes, sh.f[seg % kF], 0, 1);
+            arrive(sh.q_full[seg & 1]);
+          }
+        } else if (lane == 0) {
           sh.seg[seg % kSegs].slot = s.slot;
           sh.seg[seg % kSegs].rows = min(a.rows, a.T * a.G - s.rt * a.rows);
         }
@@ -817,33 +759,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
           const uint32_t stop = (heads | ~have | 0x01010101u) & ~((2u << lane) - 1u);  // where a run of this lane ends
           const int run = (stop ? __ffs(stop) - 1 : 32) - lane;
           const bool full = __all_sync(0xffffffffu, now.valid == kPiece);
-          const uint8_t *k_from = a.k_pool + (long long)at * pb, *v_from = a.v_pool + (long long)at * pb;
+          const uint8_t* from = pool + (long long)at * pb;
 #pragma unroll 1
           for (int t = 0; t < 4 && t0 + t < s.tiles; ++t, ++i) {
             if (!(ok = wait(sh.empty[st], ph ^ 1u, 9u))) break;
-            uint64_t valid = kAllValid;
-            if (!full) {
-              const uint32_t count = (lane >> 3) == t ? (uint32_t)now.valid << (8 * (lane & 3)) : 0u;
-              const uint32_t lo = __reduce_or_sync(0xffffffffu, (lane & 4) == 0 ? count : 0u);
-              const uint32_t hi = __reduce_or_sync(0xffffffffu, (lane & 4) != 0 ? count : 0u);
-              valid = (uint64_t)hi << 32 | lo;
+            const uint32_t bar = smem_u32(&sh.full[st]), bytes = pb * __popc(have >> (8 * t) & 0xffu);
+            if (!is_v) {
+              uint64_t valid = kAllValid;
+              if (!full) {
+                const uint32_t count = (lane >> 3) == t ? (uint32_t)now.valid << (8 * (lane & 3)) : 0u;
+                const uint32_t lo = __reduce_or_sync(0xffffffffu, (lane & 4) == 0 ? count : 0u);
+                const uint32_t hi = __reduce_or_sync(0xffffffffu, (lane & 4) != 0 ? count : 0u);
+                valid = (uint64_t)hi << 32 | lo;
+              }
+              if (lane == 0) {
+                const int tile = t0 + t, left = s.tiles - tile;
+                TileInfo& ti = sh.info[i % kInfo];
+                ti.valid = valid;
+                ti.flags = (tile == 0 ? kBegin : 0u) | (left == 1 ? kEnd : 0u) | (tile < 2 ? kFirst : 0u) |
+                           (left <= 2 ? kLast : 0u) | (s.tiles == 1 ? kOnly : 0u);
+                ti.seg = seg;
+              }
             }
-            const uint32_t bar = smem_u32(&sh.full[st]);
-            if (lane == 0) {
-              const int tile = t0 + t, left = s.tiles - tile, per = C::kAlt ? 2 : 1;
-              TileInfo& ti = sh.info[i % kInfo];
-              ti.valid = valid;
-              ti.flags = (tile == 0 ? kBegin : 0u) | (left == 1 ? kEnd : 0u) | (tile < per ? kFirst : 0u) |
-                         (left <= per ? kLast : 0u) | (C::kAlt && s.tiles == 1 ? kOnly : 0u);
-              ti.seg = seg;
-              mbar_arrive_expect_tx(bar, 2u * pb * __popc(have >> (8 * t) & 0xffu));
-            }
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
             __syncwarp();
-            if ((lane >> 3) == t && (heads >> lane & 1u)) {
-              const uint32_t dst = ring + st * stage_bytes + (lane & 7) * pb;
-              bulk_load_once(dst, k_from, run * pb, bar, once);
-              bulk_load_once(dst + side, v_from, run * pb, bar, once);
-            }
+            if ((lane >> 3) == t && (heads >> lane & 1u))
+              bulk_load_once(ring + st * stage_bytes + (is_v ? side : 0u) + (lane & 7) * pb, from, run * pb, bar, once);
             if (++st == (uint32_t)stages) st = 0, ph ^= 1u;
           }
         }
@@ -863,9 +804,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       for (uint32_t i = 0; i < tiles; ++i) {
         if (!wait(sh.s_ready[i & 1], i >> 1, 11u)) break;
         const TileInfo info = sh.info[i % kInfo];
-        const uint32_t sb = C::kAlt ? i & 1 : 0, qb = info.seg % C::kQ;
+        const uint32_t sb = i & 1, qb = info.seg & 1;
+        // (the first segment's Q has a barrier of its own: buffer 0 completes once less)
         if ((info.flags & kBegin) &&
-            !(info.seg ? wait(sh.q_full[qb], (info.seg / C::kQ - (qb == 0)) & 1u, 12u) : wait(sh.q_first, 0, 12u)))
+            !(info.seg ? wait(sh.q_full[qb], (info.seg >> 1) - (qb ^ 1u), 12u) : wait(sh.q_first, 0, 12u)))
           break;
         tc::fence_after();
         const uint64_t q = dq + (uint64_t)(qb * (C::kQBytes >> 4));
@@ -882,45 +824,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
         lead_commit(lead, smem_u32(&sh.drained[0]));
         mbar_wait_drain(smem_u32(&sh.drained[0]), 0);
       }
-    } else if (warp == kOutWarp) {
+    } else {
       // ------------------------------------------------------------ O^T += V^T P^T
-      constexpr uint32_t id_o = idesc_f16(N, C::kVSmem, true);
+      constexpr uint32_t id_o = idesc_f16(N, true, true);
       const uint64_t dp = tc::smem_desc(p_base, kKeys * 128, 1024), dv = tc::smem_desc(v_base, kKeys * 128, 1024);
       const uint32_t lead = elect_lead();
       uint32_t begun[2] = {0, 0};  // segments that O's streams have begun
       for (uint32_t i = 0; i < tiles; ++i) {
         if (!wait(sh.o_ready[i & 1], i >> 1, 14u)) break;
         const bool first = sh.info[i % kInfo].flags & kFirst;
-        const uint32_t ob = C::kAlt ? i & 1 : 0;
+        const uint32_t ob = i & 1;
         if (first && !wait(sh.o_empty[ob], begun[ob]++ ^ 1u, 15u)) break;
         tc::fence_after();
         const uint64_t p = dp + (uint64_t)((i & 1) * (C::kPBytes >> 4));
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          if constexpr (C::kVSmem)
-            lead_mma_ss(lead, tmem + kColO + ob * N, dv + (uint64_t)(((i & 1) * C::kVBytes + kk * 2048) >> 4),
-                        p + (uint64_t)((kk * 2048) >> 4), id_o, first && kk == 0 ? 0u : 1u);
-          else
-            lead_mma_ts(lead, tmem + kColO + ob * N, tmem + kColV + (i & 1) * 64 + kk * 8,
-                        p + (uint64_t)((kk * 2048) >> 4), id_o, first && kk == 0 ? 0u : 1u);
+          lead_mma_ss(lead, tmem + kColO + ob * N, dv + (uint64_t)((ob * C::kVBytes + kk * 2048) >> 4),
+                      p + (uint64_t)((kk * 2048) >> 4), id_o, first && kk == 0 ? 0u : 1u);
         lead_commit(lead, smem_u32(&sh.pv_done[i & 1]));
       }
       if (sh.abort) {
         lead_commit(lead, smem_u32(&sh.drained[1]));
         mbar_wait_drain(smem_u32(&sh.drained[1]), 0);
-      }
-    } else {
-      // ------------------------------------------------------------ Q of the segments behind the first
-      uint32_t seg = 0;
-      for (int x = begin; x < end; ++seg) {
-        const Segment s = next_segment(a, sh, x, end);
-        x += s.tiles;
-        if (seg == 0) continue;
-        const uint32_t qb = seg % C::kQ;
-        // the buffer's segment before (the first ones' too) has been multiplied
-        if (seg >= (uint32_t)C::kQ && !wait(sh.q_empty[qb], seg / C::kQ - 1, 10u)) break;
-        lay_out_q(a, s, N, q_base + qb * C::kQBytes, sh.f[seg % kF], 0, 1);
-        arrive(sh.q_full[qb]);
       }
     }
   }
@@ -960,14 +885,13 @@ cudaError_t launch_attend4_tc(Attend4Args a, cudaStream_t st) {
   const int stacked = a.T * a.G;
   a.row_tiles = (stacked + kTc4Rows - 1) / kTc4Rows;
   a.rows = (stacked + a.row_tiles - 1) / a.row_tiles;
-  a.streams = a.rows <= 64 ? 2 : 1;
+  a.streams = 2;
   a.ppt = kPieces;
   a.ppt_shift = 3;
   a.ctas = std::min(kMaxTc4Ctas, sm_count());
   const cudaError_t e = a.rows <= 16   ? launch_n<16>(a, st)
                         : a.rows <= 32 ? launch_n<32>(a, st)
-                        : a.rows <= 64 ? launch_n<64>(a, st)
-                                       : launch_n<128>(a, st);
+                                       : launch_n<64>(a, st);
   return e == cudaSuccess ? launch_join4(a, SV_BF16, st) : e;
 }
 
