@@ -66,7 +66,7 @@ constexpr float kSlack = 1.9f;
 
 // What the loading warp tells the others of a tile: tokens that count of each piece
 // (a byte each), its place in the segment, and the segment.
-struct TileInfo {
+struct alignas(16) TileInfo {
   uint64_t valid;
   uint32_t flags, seg;
 };
@@ -688,6 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       asm volatile("fence.proxy.async.global;" ::: "memory");
       unsigned flags = 0;
       const uint64_t once = l2_evict_first_policy();
+      const int unit_shift = a.ppb_shift < 0 ? 0 : min(a.ppb_shift, 3);  // log2 of a unit's pieces
       uint32_t i = 0, st = 0, ph = 0, seg = 0;
       bool ok = true;
       for (int x = begin; ok && x < end; ++seg) {
@@ -704,20 +705,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
           sh.seg[seg % kSegs].slot = s.slot;
           sh.seg[seg % kSegs].rows = min(a.rows, a.T * a.G - s.rt * a.rows);
         }
-        // Four tiles at a time: lane = piece. A selected block is read two batches ahead, its
+        // Lane = unit, the pieces of a tile that lie in one page: one copy. 32 units (16 tiles for
+        // pages of 64 tokens) are a batch. A selected block is read two batches ahead, its
         // page one, and neither is looked at before it is due, so that a batch's copies wait
         // for no load of their own (when they did, the loading warp took 1000 cycles a tile).
         const int32_t* sel = a.sel ? a.sel + ((long long)s.b * a.Hkv + s.h) * a.sel_stride : nullptr;
         const int32_t* row = a.block_table + (long long)s.b * a.nb_max;
-        const int slots = sel ? a.n_sel : s.full, i0 = s.tile0 * kPieces + lane;
-        const int last = min((s.tile0 + s.tiles) * kPieces, s.pieces);
+        const int slots = sel ? a.n_sel : s.full, p0 = s.tile0 * kPieces + (lane << unit_shift);
+        const int last = min((s.tile0 + s.tiles) * kPieces, s.pieces), batch = 32 << unit_shift;
         auto slot_of = [&](int p) { return a.ppb_shift >= 0 ? p >> a.ppb_shift : quotient(p, a.ppb); };
         auto entry_of = [&](int p) {
           const int at = sel && p < last ? slot_of(p) : slots;
           return at < slots ? __ldcg(sel + at) : -1;
         };
         struct Look {
-          int valid, sub, page;  // tokens that count, piece of its block, page (not checked)
+          int valid, sub, page;  // tokens that count, first piece within its block, page (not checked)
         };
         auto look = [&](int p, int entry) {
           Look k = {0, 0, 0};
@@ -725,11 +727,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
           const int at = slot_of(p);
           int block = sel ? entry : at;
           k.sub = p - at * a.ppb;
-          k.valid = kPiece;
+          k.valid = kPiece << unit_shift;
           if (at >= slots) {  // the partial last block
             block = s.full;
             k.sub = p - slots * a.ppb;
-            k.valid = min(kPiece, s.ctx - s.full * a.blk - k.sub * kPiece);
+            k.valid = min(k.valid, s.ctx - s.full * a.blk - k.sub * kPiece);
           } else if (block < 0 || block >= s.full) {
             if (block != -1) flags |= SV_FLAG_BAD_BLOCK_INDEX;
             k.valid = 0;
@@ -738,53 +740,56 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
           k.page = __ldcg(row + block);
           return k;
         };
-        int entry = entry_of(i0);
-        Look next = look(i0, entry);
-        entry = entry_of(i0 + 32);
+        int entry = entry_of(p0);
+        Look next = look(p0, entry);
+        entry = entry_of(p0 + batch);
 #pragma unroll 1
-        for (int t0 = 0; ok && t0 < s.tiles; t0 += 4) {
+        for (int t0 = 0, p = p0; ok && t0 < s.tiles; t0 += batch / kPieces, p += batch) {
           Look now = next;
-          next = look(i0 + (t0 + 4) * kPieces, entry);
-          entry = entry_of(i0 + (t0 + 8) * kPieces);
+          next = look(p + batch, entry);
+          entry = entry_of(p + 2 * batch);
           if (now.valid && (now.page < 0 || now.page >= a.num_pages)) {
             flags |= SV_FLAG_BAD_PAGE;
             now.valid = 0;
           }
-          const bool there = now.valid > 0;
-          const int at = now.page * a.Hkv * a.ppb + s.h * a.ppb + now.sub;  // piece of the pool (below 2^31: the call's limits)
-          const int prev = __shfl_up_sync(0xffffffffu, at, 1);
-          const uint32_t have = __ballot_sync(0xffffffffu, there);
-          // a run of pieces that follow each other in the pool is one copy
-          const uint32_t heads = __ballot_sync(0xffffffffu, there && ((lane & 7) == 0 || !(have >> (lane - 1) & 1u) || at != prev + 1));
-          const uint32_t stop = (heads | ~have | 0x01010101u) & ~((2u << lane) - 1u);  // where a run of this lane ends
-          const int run = (stop ? __ffs(stop) - 1 : 32) - lane;
-          const bool full = __all_sync(0xffffffffu, now.valid == kPiece);
-          const uint8_t* from = pool + (long long)at * pb;
+          const uint8_t* from = pool + ((long long)now.page * a.Hkv * a.ppb + s.h * a.ppb + now.sub) * pb;
+          const uint32_t bytes = (uint32_t)(now.valid + kPiece - 1) / kPiece * pb;
+          const uint32_t to = (is_v ? side : 0u) + ((uint32_t)(lane << unit_shift) % kPieces) * pb;
+          const bool full = __all_sync(0xffffffffu, now.valid == kPiece << unit_shift);
+          const int tile = (lane << unit_shift) / kPieces, n = min(batch / kPieces, s.tiles - t0);
 #pragma unroll 1
-          for (int t = 0; t < 4 && t0 + t < s.tiles; ++t, ++i) {
+          for (int t = 0; t < n; ++t, ++i) {
             if (!(ok = wait(sh.empty[st], ph ^ 1u, 9u))) break;
-            const uint32_t bar = smem_u32(&sh.full[st]), bytes = pb * __popc(have >> (8 * t) & 0xffu);
-            if (!is_v) {
-              uint64_t valid = kAllValid;
-              if (!full) {
-                const uint32_t count = (lane >> 3) == t ? (uint32_t)now.valid << (8 * (lane & 3)) : 0u;
-                const uint32_t lo = __reduce_or_sync(0xffffffffu, (lane & 4) == 0 ? count : 0u);
-                const uint32_t hi = __reduce_or_sync(0xffffffffu, (lane & 4) != 0 ? count : 0u);
-                valid = (uint64_t)hi << 32 | lo;
+            const uint32_t bar = smem_u32(&sh.full[st]);
+            uint32_t all = kPieces * pb;
+            uint64_t valid = kAllValid;
+            if (!full) {
+              uint32_t lo = 0, hi = 0;
+              if (tile == t) {
+#pragma unroll 1
+                for (int j = 0; j < 1 << unit_shift; ++j) {
+                  const uint32_t v = (uint32_t)min(max(now.valid - j * kPiece, 0), kPiece);
+                  const int at = (lane << unit_shift) % kPieces + j;
+                  if (at < 4) lo |= v << (8 * at);
+                  else hi |= v << (8 * (at - 4));
+                }
               }
-              if (lane == 0) {
-                const int tile = t0 + t, left = s.tiles - tile;
-                TileInfo& ti = sh.info[i % kInfo];
-                ti.valid = valid;
-                ti.flags = (tile == 0 ? kBegin : 0u) | (left == 1 ? kEnd : 0u) | (tile < 2 ? kFirst : 0u) |
-                           (left <= 2 ? kLast : 0u) | (s.tiles == 1 ? kOnly : 0u);
-                ti.seg = seg;
-              }
+              lo = __reduce_or_sync(0xffffffffu, lo);
+              hi = __reduce_or_sync(0xffffffffu, hi);
+              valid = (uint64_t)hi << 32 | lo;
+              all = __reduce_add_sync(0xffffffffu, tile == t ? bytes : 0u);
             }
-            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+            if (lane == 0) {
+              if (!is_v) {
+                const int at = t0 + t, left = s.tiles - at;
+                const uint32_t place = (at == 0 ? kBegin : 0u) | (left == 1 ? kEnd : 0u) | (at < 2 ? kFirst : 0u) |
+                                       (left <= 2 ? kLast : 0u) | (s.tiles == 1 ? kOnly : 0u);
+                sh.info[i % kInfo] = {valid, place, seg};
+              }
+              mbar_arrive_expect_tx(bar, all);
+            }
             __syncwarp();
-            if ((lane >> 3) == t && (heads >> lane & 1u))
-              bulk_load_once(ring + st * stage_bytes + (is_v ? side : 0u) + (lane & 7) * pb, from, run * pb, bar, once);
+            if (tile == t && bytes) bulk_load_once(ring + st * stage_bytes + to, from, bytes, bar, once);
             if (++st == (uint32_t)stages) st = 0, ph ^= 1u;
           }
         }
