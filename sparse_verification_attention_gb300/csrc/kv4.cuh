@@ -103,81 +103,110 @@ __device__ __forceinline__ int pieces_of(const Attend4Args& a, int ctx) {
   return (a.sel ? a.n_sel : full) * a.ppb + (rest + kPiece - 1) / kPiece;
 }
 
-// Prefix sums of the key tiles (one warp): cu[0 .. B], and the contexts. Returns whether
-// a length was clamped, in any lane that saw one.
-__device__ __forceinline__ bool scan_tiles(const Attend4Args& a, int* cu, int* ctx) {
+// The line that the CTAs share: the pairs' key tiles, and ahead of each pair's as many units
+// as beginning it takes (a.pair_cost; pairs without keys have none). In shared memory:
+struct Line {
+  int first[kMaxB4 + 1];  // units of one pair, summed over the sequences before
+  int ctx[kMaxB4];
+  int ctas, each, more;   // CTAs with a share; its units, and how many CTAs have one unit more
+
+  __device__ __forceinline__ int begin(int cta) const { return cta < ctas ? cta * each + min(cta, more) : ctas * each + more; }
+  // the CTA that has unit x
+  __device__ __forceinline__ int cta_of(int x) const {
+    const int big = more * (each + 1);
+    return x < big ? quotient(x, each + 1) : more + quotient(x - big, each);
+  }
+};
+
+// Fill it (one warp). Returns whether a length was clamped, in any lane that saw one.
+__device__ __forceinline__ bool make_line(const Attend4Args& a, Line* line) {
   const int lane = threadIdx.x & 31;
   int carry = 0;
   bool bad = false;
-  if (lane == 0) cu[0] = 0;
+  if (lane == 0) line->first[0] = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
     int x = 0;
     if (b < a.B) {
       const int c = a.seq_ctx[b], n = min(max(c, 0), a.nb_max * a.blk);
       bad |= c != n;
-      ctx[b] = n;
+      line->ctx[b] = n;
       x = (pieces_of(a, n) + a.ppt - 1) >> a.ppt_shift;
+      if (x) x += a.pair_cost;
     }
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, off);
       if (lane >= off) x += y;
     }
-    if (b < a.B) cu[b + 1] = carry + x;
+    if (b < a.B) line->first[b + 1] = carry + x;
     carry += __shfl_sync(0xffffffffu, x, 31);
+  }
+  const int total = carry * a.Hkv * a.row_tiles;  // (below 2^31: the call's limits)
+  const int ctas = min(a.ctas, total), each = ctas ? quotient(total, ctas) : 0;
+  if (lane == 0) {
+    line->ctas = ctas;
+    line->each = each;
+    line->more = total - each * ctas;
   }
   return bad;
 }
 
-// The line of all key tiles and the CTAs that share it: the first `more` have one tile
-// more than the others, none has none.
-struct Line {
-  int ctas, each, more;
-  __device__ __forceinline__ int first(int c) const { return c * each + min(c, more); }
-  // the CTA that has tile x
-  __device__ __forceinline__ int cta_of(int x) const {
-    const int big = more * (each + 1);
-    return x < big ? quotient(x, each + 1) : more + quotient(x - big, each);
-  }
-};
-__device__ __forceinline__ Line line_of(const Attend4Args& a, int tiles) {
-  const int total = tiles * a.Hkv * a.row_tiles;  // (below 2^31: the call's limits)
-  Line l;
-  l.ctas = min(a.ctas, total);
-  l.each = l.ctas ? quotient(total, l.ctas) : 0;
-  l.more = total - l.each * l.ctas;
-  return l;
-}
-
 struct Segment {
   int b, h, rt;      // the pair
-  int tile0, tiles;  // its key tiles
+  int tile0, tiles;  // its key tiles (none if the share ends ahead of them)
   int ctx, full, pieces;  // tokens, full blocks, pieces of the (sequence, head)
   int slot;
+  int next;          // where the next segment begins
 };
 // The segment that begins at position x of the line (x < end, the end of the CTA's share).
-__device__ __forceinline__ Segment segment_at(const Attend4Args& a, const int* cu, const int* ctx, int x, int end,
-                                              int cta) {
+__device__ __forceinline__ Segment segment_at(const Attend4Args& a, const Line& line, int x, int end, int cta) {
   Segment s;
   const int per = a.Hkv * a.row_tiles;
   int lo = 0, hi = a.B;  // the last sequence that begins at x or before (those without keys do not count)
   while (hi - lo > 1) {
     const int m = (lo + hi) >> 1;
-    if (cu[m] * per <= x) lo = m;
+    if (line.first[m] * per <= x) lo = m;
     else hi = m;
   }
   s.b = lo;
-  const int n = cu[lo + 1] - cu[lo], in = x - cu[lo] * per, pair = quotient(in, n);
-  s.tile0 = in - pair * n;
+  const int n = line.first[lo + 1] - line.first[lo], in = x - line.first[lo] * per, pair = quotient(in, n);
+  const int unit = in - pair * n;
+  s.tile0 = max(unit - a.pair_cost, 0);
   s.h = a.row_tiles == 1 ? pair : quotient(pair, a.row_tiles);
   s.rt = pair - s.h * a.row_tiles;
-  s.tiles = min(n - s.tile0, end - x);
-  s.ctx = ctx[lo];
+  s.next = min(x - unit + n, end);
+  s.tiles = max(s.next - (x - unit) - a.pair_cost - s.tile0, 0);
+  s.ctx = line.ctx[lo];
   s.full = blocks_in(a, s.ctx);
   s.pieces = (a.sel ? a.n_sel : s.full) * a.ppb + (s.ctx - s.full * a.blk + kPiece - 1) / kPiece;
   s.slot = lo * per + pair + cta;
   return s;
+}
+// Key tiles of the line that lie before position x.
+__device__ __forceinline__ int tiles_before(const Attend4Args& a, const Line& line, int x) {
+  const int per = a.Hkv * a.row_tiles;
+  int tiles = 0;
+  for (int b = 0; b < a.B; ++b) {
+    const int n = line.first[b + 1] - line.first[b], in = x - line.first[b] * per;
+    if (in <= 0) break;
+    if (n == 0) continue;
+    if (in >= n * per) {
+      tiles += (n - a.pair_cost) * per;
+      continue;
+    }
+    const int pair = quotient(in, n);
+    tiles += pair * (n - a.pair_cost) + max(in - pair * n - a.pair_cost, 0);
+  }
+  return tiles;
+}
+// What the join needs of pair p (of all sequences): its first slot and the number of slots.
+__device__ __forceinline__ int2 slots_of(const Attend4Args& a, const Line& line, int p) {
+  const int per = a.Hkv * a.row_tiles, b = quotient(p, per), n = line.first[b + 1] - line.first[b];
+  if (n == 0) return make_int2(0, 0);
+  const int x = line.first[b] * per + (p - b * per) * n;
+  const int c0 = line.cta_of(x + a.pair_cost), c1 = line.cta_of(x + n - 1);
+  return make_int2(p + c0, c1 - c0 + 1);
 }
 
 // Where piece i of a segment's (sequence, head) lies in the pools (in pieces, -1:

@@ -71,13 +71,16 @@ constexpr int kSimt4Rows = 32;       // row tile on the CUDA cores
 constexpr int kTc4Rows = 64;         // ... and on the tensor cores, at most
 constexpr int kMaxSimt4Ctas = 640;   // CTAs of a launch at most
 constexpr int kMaxTc4Ctas = 160;
+constexpr int kMaxPairCost = 8;      // of Attend4Args::pair_cost
 
-// The T * G stacked rows of a (sequence, KV head) are cut into row tiles; a pair
-// is one row tile of one (sequence, head). A pair's pieces (16 keys each) make
-// key tiles of `ppt` pieces. The pairs' key tiles are laid end to end and cut into
-// equal shares, one per CTA; what a CTA has of a pair is a segment. Segment
-// (pair p, CTA c) leaves its rows' sums in slot p + c (p and c only grow along the
-// line, so no two segments share one), once for each of its `streams`.
+// The T * G stacked rows of a (sequence, KV head) are cut into row tiles; a pair is one row
+// tile of one (sequence, head). A pair's pieces (16 keys each) make key tiles of `ppt` pieces.
+// The pairs' key tiles are laid end to end, with what beginning a pair costs ahead of them, and
+// cut into equal shares, one per CTA; what a CTA has of a pair is a segment. (That cost left
+// out: 16 sequences of 1 to 32768 tokens, 8 heads each, 82 us; counted as 3 tiles 70, as 8
+// tiles 58: the CTAs whose share holds several short pairs were last.) Segment (pair p, CTA c)
+// leaves its rows' sums in slot p + c (p and c only grow along the line, so no two segments
+// share one), once for each of its `streams`.
 struct Attend4Args {
   const void *q, *draft_k, *draft_v;
   void* out;
@@ -87,7 +90,7 @@ struct Attend4Args {
   const int32_t* sel;            // [B, Hkv, sel_stride] or null: every full block
   const int32_t *k_exp, *v_exp;  // [Hkv] or null
   unsigned* status;
-  int* cu;        // workspace [B + 1]: key tiles of one pair, summed over the sequences before
+  int2* slots;    // workspace [pairs]: first slot of a pair and number of slots
   float2* part_ml;  // [slots, streams, rows]: reference (log2 domain) and sum
   float* part_o;    // [slots, streams, rows, d], in units of 2^v_exp
   int B, T, Hq, Hkv, G, d, blk, nb_max, num_pages, n_sel, sel_stride;
@@ -95,6 +98,7 @@ struct Attend4Args {
   int streams;    // 2: a segment's even and odd tiles are summed apart
   int ppb, ppt, ppt_shift;  // pieces of a block and of a key tile (a power of two)
   int ppb_shift, g_shift;   // log2 of ppb and of G, -1 where it is no power of two
+  int pair_cost;  // key tiles' time that beginning a pair takes
   int ctas;
   float scale_log2;  // log2(e) / sqrt(d)
   unsigned long long anc[kMaxT];

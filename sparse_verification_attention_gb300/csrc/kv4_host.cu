@@ -122,10 +122,10 @@ sv_status check_row_count(const sv_shape* s, int n) {
   return SV_OK;
 }
 
-// Workspace of the attention: status word, prefix sums of the key tiles, then the
-// segments' (reference, sum) and sums of values, one slot per pair and CTA at most.
+// Workspace of the attention: status word, the pairs' slots, then the segments' (reference,
+// sum) and sums of values, one slot per pair and CTA at most.
 struct Layout4 {
-  size_t cu, ml, o, total;
+  size_t slots, ml, o, total;
 };
 Layout4 layout4(const sv_shape& s) {
   size_t rows = 0;
@@ -136,8 +136,8 @@ Layout4 layout4(const sv_shape& s) {
     rows = std::max(rows, (size_t)((tiles * pairs + ctas[i]) * (i + 1) * r));  // (two streams on the tensor cores)
   }
   Layout4 L;
-  L.cu = kStatusBytes;
-  L.ml = L.cu + align256((s.B + 1) * sizeof(int));
+  L.slots = kStatusBytes;
+  L.ml = L.slots + align256((stacked + kSimt4Rows - 1) / kSimt4Rows * pairs * sizeof(int2));
   L.o = L.ml + align256(rows * sizeof(float2));
   L.total = L.o + align256(rows * s.d * sizeof(float));
   return L;
@@ -306,7 +306,7 @@ sv_status sv_attend_kv4(const sv_shape* shape, const void* q, const sv_kv4* kv, 
     return fail(SV_ERR_UNSUPPORTED, "B=%d: the batch's tokens are too many", shape->B);
   // the line of key tiles (64 tokens at least, 32 rows at least) is counted in 31 bits
   const long long row_tiles = (shape->T * (shape->Hq / shape->Hkv) + kSimt4Rows - 1) / kSimt4Rows;
-  if (((long long)shape->B * (kv->nb_max + 1ll) * shape->blk >> 6) + shape->B >= kInt / (shape->Hkv * row_tiles))
+  if (((long long)shape->B * (kv->nb_max + 1ll) * shape->blk >> 6) + shape->B * (1ll + kMaxPairCost) >= kInt / (shape->Hkv * row_tiles))
     return fail(SV_ERR_UNSUPPORTED, "B=%d, %d heads: the batch's tokens are too many", shape->B, shape->Hkv);
   if (sel && (n_sel < 0 || n_sel > sel_stride || n_sel > kv->nb_max))
     return fail(SV_ERR_INVALID_ARG, "n_sel=%d outside [0, sel_stride=%d] or beyond nb_max=%d", n_sel, sel_stride,
@@ -337,7 +337,7 @@ sv_status sv_attend_kv4(const sv_shape* shape, const void* q, const sv_kv4* kv, 
   a.k_exp = kv->k_exp;
   a.v_exp = kv->v_exp;
   a.status = reinterpret_cast<unsigned*>(w);
-  a.cu = reinterpret_cast<int*>(w + L.cu);
+  a.slots = reinterpret_cast<int2*>(w + L.slots);
   a.part_ml = reinterpret_cast<float2*>(w + L.ml);
   a.part_o = reinterpret_cast<float*>(w + L.o);
   a.B = shape->B;

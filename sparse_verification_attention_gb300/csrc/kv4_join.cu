@@ -40,19 +40,21 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
-// One warp per output row; a lane has dims 4 lane .. + 3 (and 128 + that for d > 128).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) join4_kernel(const __grid_constant__ Attend4Args a) {
+// One warp per output row; a lane has dims 4 lane .. + 3 (and 128 + that for NJ = 2, d > 128).
+template <typename T, int NJ>
+__global__ void __launch_bounds__(kThreads, NJ == 1 ? 4 : 2) join4_kernel(const __grid_constant__ Attend4Args a) {
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   if (row >= (long long)a.B * a.T * a.Hq) return;
   const int tok = quotient((int)row, a.Hq), head = (int)row - tok * a.Hq, b = quotient(tok, a.T), t = tok - b * a.T;
   const int h = a.g_shift >= 0 ? head >> a.g_shift : quotient(head, a.G), r = t * a.G + head - h * a.G;
   const int rt = a.row_tiles == 1 ? 0 : quotient(r, a.rows);
-  const bool has[2] = {lane * 4 < a.d, 128 + lane * 4 < a.d};
-  float4 q[2], o[2];
+  bool has[NJ];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int j = 0; j < NJ; ++j) has[j] = 128 * j + lane * 4 < a.d;
+  float4 q[NJ], o[NJ];
+#pragma unroll
+  for (int i = 0; i < NJ; ++i) {
     q[i] = o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (has[i]) q[i] = load4(static_cast<const T*>(a.q) + row * a.d + 128 * i + lane * 4);
   }
@@ -73,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) join4_kernel(const __grid_constant__
       w &= w - 1;
       x[e] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < NJ; ++j)
         if (u[e] >= 0 && has[j]) x[e] += dot4(q[j], load4(dk + u[e] * step + 128 * j + lane * 4));
     }
 #pragma unroll
@@ -88,18 +90,10 @@ __global__ void __launch_bounds__(kThreads) join4_kernel(const __grid_constant__
   // only behind its own wait for its predecessors; what follows is the attention's.
   pdl_wait();
   pdl_trigger();
-  // the row's segments: CTAs c0 .. c1 of the line
-  const int start = a.cu[b], tiles = a.cu[b + 1] - start, per = a.Hkv * a.row_tiles;
-  const int pair = h * a.row_tiles + rt;
-  const Line line = line_of(a, a.cu[a.B]);
-  const int first = start * per + pair * tiles;
-  int c0 = 0, c1 = -1;
-  if (tiles) {
-    c0 = line.cta_of(first);
-    c1 = line.cta_of(first + tiles - 1);
-  }
-  const long long at0 = ((long long)b * per + pair + c0) * a.streams * a.rows + r - rt * a.rows;
-  const int parts = (c1 - c0 + 1) * a.streams;
+  // the row's parts
+  const int2 slots = __ldcg(a.slots + (b * a.Hkv + h) * a.row_tiles + rt);
+  const int parts = slots.y * a.streams;
+  const long long at0 = (long long)slots.x * a.streams * a.rows + r - rt * a.rows;
   // the largest reference, of the segments and of the drafts
   float m = fmaxf(s0, s1);
   for (int c = lane; c < parts; c += 32) m = fmaxf(m, a.part_ml[at0 + (long long)c * a.rows].x);
@@ -110,14 +104,14 @@ __global__ void __launch_bounds__(kThreads) join4_kernel(const __grid_constant__
 #pragma unroll 1
   for (int c0 = 0; c0 < parts; c0 += kBatch) {
     float2 ml[kBatch];
-    float4 x[kBatch][2];
+    float4 x[kBatch][NJ];
 #pragma unroll
     for (int e = 0; e < kBatch; ++e) {
       const long long at = at0 + (long long)(c0 + e) * a.rows;
       if (c0 + e >= parts) continue;
       ml[e] = __ldcg(a.part_ml + at);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < NJ; ++j)
         if (has[j]) x[e][j] = load4(a.part_o + at * a.d + 128 * j + lane * 4);
     }
 #pragma unroll
@@ -126,45 +120,50 @@ __global__ void __launch_bounds__(kThreads) join4_kernel(const __grid_constant__
       const float w = exp2f(ml[e].x - m);
       l += w * ml[e].y;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < NJ; ++j)
         if (has[j]) axpy4(o[j], w * unit, x[e][j]);
     }
   }
 #pragma unroll 1
   for (unsigned long long w = see, i = 0; w; i += kBatch) {
-    float4 x[kBatch][2];
+    float4 x[kBatch][NJ];
 #pragma unroll
     for (int e = 0; e < kBatch; ++e) {
       u[e] = w ? __ffsll(w) - 1 : -1;
       w &= w - 1;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < NJ; ++j)
         if (u[e] >= 0 && has[j]) x[e][j] = load4(dv + u[e] * step + 128 * j + lane * 4);
     }
 #pragma unroll
     for (int e = 0; e < kBatch; ++e) {
       const float p = __shfl_sync(0xffffffffu, (int)i < 32 ? p0 : p1, ((int)i + e) & 31);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < NJ; ++j)
         if (u[e] >= 0 && has[j]) axpy4(o[j], p, x[e][j]);
     }
   }
   const float inv = __frcp_rn(l);
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+  for (int j = 0; j < NJ; ++j)
     if (has[j]) {
       const float4 y = make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv);
       store4(static_cast<T*>(a.out) + row * a.d + 128 * j + lane * 4, y);
     }
 }
 
+template <typename T>
+cudaError_t launch_as(const Attend4Args& a, cudaStream_t st) {
+  const long long rows = (long long)a.B * a.T * a.Hq;
+  const dim3 grid((unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32)));
+  return a.d <= 128 ? launch_pdl(join4_kernel<T, 1>, grid, dim3(kThreads), 0, st, a)
+                    : launch_pdl(join4_kernel<T, 2>, grid, dim3(kThreads), 0, st, a);
+}
+
 }  // namespace
 
 cudaError_t launch_join4(const Attend4Args& a, int dtype, cudaStream_t st) {
-  const long long rows = (long long)a.B * a.T * a.Hq;
-  const dim3 grid((unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32)));
-  return dtype == SV_BF16 ? launch_pdl(join4_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, a)
-                          : launch_pdl(join4_kernel<float>, grid, dim3(kThreads), 0, st, a);
+  return dtype == SV_BF16 ? launch_as<__nv_bfloat16>(a, st) : launch_as<float>(a, st);
 }
 
 }  // namespace sva

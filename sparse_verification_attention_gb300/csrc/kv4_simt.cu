@@ -18,7 +18,7 @@ constexpr int kKeys = 64, kPieces = kKeys / kPiece;  // (ppt_shift)
 constexpr int kGroup = 16;
 
 struct Control {
-  int cu[kMaxB4 + 1], ctx[kMaxB4];
+  Line line;
   long long piece[kPieces];
   int valid[kPieces];
   float m[kRows], l[kRows];
@@ -49,18 +49,17 @@ __global__ void __launch_bounds__(kThreads) attend4_simt_kernel(const __grid_con
   pdl_wait();
   pdl_trigger();
   if (tid < 32) {
-    const bool bad = scan_tiles(a, sh.cu, sh.ctx);
+    const bool bad = make_line(a, &sh.line);
     if (bad) flags |= SV_FLAG_BAD_LENGTH;
   }
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int b = tid; b <= a.B; b += kThreads) a.cu[b] = sh.cu[b];
-  const Line line = line_of(a, sh.cu[a.B]);
-  const int cta = blockIdx.x;
-  const int end = cta < line.ctas ? line.first(cta + 1) : 0;
-  for (int x = cta < line.ctas ? line.first(cta) : 0; x < end;) {
-    const Segment s = segment_at(a, sh.cu, sh.ctx, x, end, cta);
-    x += s.tiles;
+  const int pairs = a.B * a.Hkv * a.row_tiles, cta = blockIdx.x;
+  for (int p = cta * kThreads + tid; p < pairs; p += gridDim.x * kThreads) a.slots[p] = slots_of(a, sh.line, p);
+  const int end = sh.line.begin(cta + 1);
+  for (int x = sh.line.begin(cta); x < end;) {
+    const Segment s = segment_at(a, sh.line, x, end, cta);
+    x = s.next;
+    if (s.tiles == 0) continue;
     const int row0 = s.rt * a.rows, rows = min(a.rows, a.T * a.G - row0);
     const float scale = a.scale_log2 * exp2i(head_exp(a.k_exp, s.h));
     for (int i = tid; i < kRows * a.d; i += kThreads) {
@@ -219,6 +218,7 @@ cudaError_t launch_attend4_simt(Attend4Args a, int dtype, cudaStream_t st) {
   a.ppt = kPieces;
   a.ppt_shift = 2;
   a.streams = 1;
+  a.pair_cost = 1;
   return dtype == SV_BF16 ? launch_as<__nv_bfloat16>(a, st) : launch_as<float>(a, st);
 }
 

@@ -47,6 +47,8 @@ namespace {
 
 using namespace kv4;
 
+constexpr int kPairCost = 8;  // key tiles' time that beginning a pair takes
+static_assert(kPairCost <= kMaxPairCost, "the calls' limits count this many");
 constexpr int kKeys = 128, kPieces = kKeys / kPiece;
 // Rings. Copies run at most kMaxStages tiles ahead of V, V two ahead of its products, so the
 // infos of 11 tiles, and of as many segments, are in use at most. Q, with its factors, runs
@@ -91,7 +93,8 @@ struct Control {
   SegInfo seg[kSegs];
   alignas(16) float f[kF][kTc4Rows];   // factor of a row's scores
   alignas(16) float mx[4][2 * kTc4Rows], sum[4][2 * kTc4Rows];  // by warp of a warpgroup: both streams' columns
-  int cu[kMaxB4 + 1], ctx[kMaxB4];
+  int tiles;                              // of the CTA's share
+  Line line;
 };
 
 template <int N>
@@ -231,22 +234,23 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int
 }
 
 __device__ __noinline__ Segment next_segment(const Attend4Args& a, const Control& sh, int x, int end) {
-  return segment_at(a, sh.cu, sh.ctx, x, end, blockIdx.x);
+  return segment_at(a, sh.line, x, end, blockIdx.x);
 }
 
 // Q of a segment into shared memory as halves, K-major with the 128-byte swizzle, and the
-// factors of its rows' scores: warp `part` of `parts`, a row by 16 lanes, 8 dims each.
+// factors of its rows' scores: warp `part` of `parts`, a row by 16 lanes, 8 dims each, FLIGHT
+// rows' loads under way together. (Short code where it comes first, see above.)
+template <int FLIGHT>
 __device__ __noinline__ void lay_out_q(const Attend4Args& a, const Segment& s, int n, uint32_t to, float* f, int part,
                                        int parts) {
   const int lane = threadIdx.x & 31, c = lane & 15;
   const int row0 = s.rt * a.rows, rows = min(a.rows, a.T * a.G - row0);
   const float scale = a.scale_log2 * exp2i(head_exp(a.k_exp, s.h));
-  constexpr int kFlight = 4;
 #pragma unroll 1
-  for (int r0 = part * 2 + (lane >> 4); r0 - (lane >> 4) < n; r0 += 2 * parts * kFlight) {
-    uint4 w[kFlight];
+  for (int r0 = part * 2 + (lane >> 4); r0 - (lane >> 4) < n; r0 += 2 * parts * FLIGHT) {
+    uint4 w[FLIGHT];
 #pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
+    for (int u = 0; u < FLIGHT; ++u) {
       const int r = r0 + 2 * parts * u;
       w[u] = make_uint4(0, 0, 0, 0);
       if (r < rows && 8 * c < a.d)
@@ -254,7 +258,7 @@ __device__ __noinline__ void lay_out_q(const Attend4Args& a, const Segment& s, i
                                                      row_at(a, s.b, s.h, row0 + r) * a.d) + c);
     }
 #pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
+    for (int u = 0; u < FLIGHT; ++u) {
       const int r = r0 + 2 * parts * u;
       // the largest element's bits (of positive floats they compare as integers; a NaN's are
       // the largest and leave the row as it is)
@@ -319,28 +323,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       mbar_init(smem_u32(&sh.meet[i]), 4);
       sh.over[i][0] = sh.over[i][1] = 0;
     }
-    mbar_init(smem_u32(&sh.q_first), 8);
+    mbar_init(smem_u32(&sh.q_first), kKLoadWarp);
     sh.abort = 0;
     fence_barrier_init();
   }
   pdl_wait();
   pdl_trigger();
-  bool bad = false;
   if (warp == kKLoadWarp) {
-    bad = scan_tiles(a, sh.cu, sh.ctx);
-    if (bad) atomicOr(a.status, SV_FLAG_BAD_LENGTH);
+    if (make_line(a, &sh.line)) atomicOr(a.status, SV_FLAG_BAD_LENGTH);
+    __syncwarp();
+    const int before = lane < 2 ? tiles_before(a, sh.line, sh.line.begin(blockIdx.x + lane)) : 0;
+    const int share = __shfl_sync(0xffffffffu, before, 1) - before;
+    if (lane == 0) sh.tiles = share;
     __syncwarp();
   }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = sh.tmem;
-  if (blockIdx.x == 0)
-    for (int b = tid; b <= a.B; b += kThreads) a.cu[b] = sh.cu[b];
-  const Line line = line_of(a, sh.cu[a.B]);
-  const bool idle = (int)blockIdx.x >= line.ctas;
-  const int begin = idle ? 0 : line.first(blockIdx.x), end = idle ? 0 : line.first(blockIdx.x + 1);
-  const uint32_t tiles = (uint32_t)(end - begin);
+  const int begin = sh.line.begin(blockIdx.x), end = sh.line.begin(blockIdx.x + 1);
+  const uint32_t tiles = (uint32_t)sh.tiles;
   auto wait = [&](uint64_t& bar, uint32_t parity, unsigned site) {
     const uint32_t addr = smem_u32(&bar);
     return __all_sync(0xffffffffu, try_wait_long(addr, parity & 1u)) ||
@@ -351,6 +353,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
     if (lane == 0) mbar_arrive(smem_u32(&bar));
   };
 
+  if (warp < kKLoadWarp && tiles) {
+    // the first segment's Q, which everybody waits for (later ones: one warp, ahead)
+    Segment s = next_segment(a, sh, begin, end);
+    if (s.tiles == 0) s = next_segment(a, sh, s.next, end);
+    lay_out_q<1>(a, s, N, q_base, sh.f[0], warp, kKLoadWarp);
+    arrive(sh.q_first);
+  }
   if (warp < 4) {
     // ------------------------------------------------------------ K: lane = key
     const uint32_t piece = (uint32_t)tid / kPiece, tok = (uint32_t)tid % kPiece;
@@ -453,11 +462,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
     const uint32_t tlane = (uint32_t)(quad * 32) << 16, tmem_o = tmem + tlane + kColO + own0;
     // this lane's row of the 8 x 8 blocks that it addresses for P's stores (see put)
     const int prow = quad * 32 + (NC == 16 ? (lane >> 4) * 8 : 0) + (lane & 7), pchunk = NC == 16 ? lane >> 3 & 1 : lane >> 3;
-    if (!idle) {  // the first segment's Q, which everybody else waits for (later ones: one warp, ahead)
-      const Segment s = next_segment(a, sh, begin, end);
-      lay_out_q(a, s, N, q_base, sh.f[0], warp - kSoftmaxWarp, 8);
-      arrive(sh.q_first);
-    }
     arrive(sh.s_ready[wg]);  // S is free
     uint64_t f[J], nm[J], l[J];  // factor, minus (reference - kLift), sum: two columns each
     bool first = true;           // no key of the stream has counted yet
@@ -691,14 +695,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       const int unit_shift = a.ppb_shift < 0 ? 0 : min(a.ppb_shift, 3);  // log2 of a unit's pieces
       uint32_t i = 0, st = 0, ph = 0, seg = 0;
       bool ok = true;
-      for (int x = begin; ok && x < end; ++seg) {
+      for (int x = begin; ok && x < end;) {
         const Segment s = next_segment(a, sh, x, end);
-        x += s.tiles;
+        x = s.next;
+        if (s.tiles == 0) continue;
         if (is_v) {
           if (seg > 0) {
             // (its buffer's segment before, the first one too, has been multiplied)
             if (seg > 1 && !(ok = wait(sh.q_empty[seg & 1], (seg >> 1) - 1, 10u))) break;
-            lay_out_q(a, s, N, q_base + (seg & 1) * C::kQBytes, sh.f[seg % kF], 0, 1);
+            lay_out_q<4>(a, s, N, q_base + (seg & 1) * C::kQBytes, sh.f[seg % kF], 0, 1);
             arrive(sh.q_full[seg & 1]);
           }
         } else if (lane == 0) {
@@ -793,6 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
             if (++st == (uint32_t)stages) st = 0, ph ^= 1u;
           }
         }
+        ++seg;
       }
       if (flags) atomicOr(a.status, flags);
       if (sh.abort) {  // copies in flight end before the CTA does
@@ -831,6 +837,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       }
     } else {
       // ------------------------------------------------------------ O^T += V^T P^T
+      const int pairs = a.B * a.Hkv * a.row_tiles;
+      for (int p = blockIdx.x * 32 + lane; p < pairs; p += gridDim.x * 32) a.slots[p] = slots_of(a, sh.line, p);
+      __syncwarp();
       constexpr uint32_t id_o = idesc_f16(N, true, true);
       const uint64_t dp = tc::smem_desc(p_base, kKeys * 128, 1024), dv = tc::smem_desc(v_base, kKeys * 128, 1024);
       const uint32_t lead = elect_lead();
@@ -891,6 +900,7 @@ cudaError_t launch_attend4_tc(Attend4Args a, cudaStream_t st) {
   a.row_tiles = (stacked + kTc4Rows - 1) / kTc4Rows;
   a.rows = (stacked + a.row_tiles - 1) / a.row_tiles;
   a.streams = 2;
+  a.pair_cost = kPairCost;
   a.ppt = kPieces;
   a.ppt_shift = 3;
   a.ctas = std::min(kMaxTc4Ctas, sm_count());
