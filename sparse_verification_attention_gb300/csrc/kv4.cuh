@@ -183,11 +183,12 @@ __device__ __forceinline__ Segment segment_at(const Attend4Args& a, const Line& 
   s.slot = lo * per + pair + cta;
   return s;
 }
-// Key tiles of the line that lie before position x.
+// Key tiles of the line that lie before position x (by one warp).
 __device__ __forceinline__ int tiles_before(const Attend4Args& a, const Line& line, int x) {
   const int per = a.Hkv * a.row_tiles;
   int tiles = 0;
-  for (int b = 0; b < a.B; ++b) {
+#pragma unroll 1
+  for (int b = threadIdx.x & 31; b < a.B; b += 32) {
     const int n = line.first[b + 1] - line.first[b], in = x - line.first[b] * per;
     if (in <= 0) break;
     if (n == 0) continue;
@@ -198,7 +199,7 @@ __device__ __forceinline__ int tiles_before(const Attend4Args& a, const Line& li
     const int pair = quotient(in, n);
     tiles += pair * (n - a.pair_cost) + max(in - pair * n - a.pair_cost, 0);
   }
-  return tiles;
+  return __reduce_add_sync(0xffffffffu, tiles);
 }
 // What the join needs of pair p (of all sequences): its first slot and the number of slots.
 __device__ __forceinline__ int2 slots_of(const Attend4Args& a, const Line& line, int p) {

@@ -56,7 +56,7 @@ constexpr int kKeys = 128, kPieces = kKeys / kPiece;
 constexpr int kInfo = 16, kSegs = 16, kF = 8;
 constexpr int kMaxStages = 8;
 constexpr int kThreads = 640;
-constexpr int kSoftmaxWarp = 8, kKLoadWarp = 16, kVLoadWarp = 17, kScoreWarp = 18;  // 19: O
+constexpr int kSoftmaxWarp = 8, kKLoadWarp = 16, kVLoadWarp = 17, kScoreWarp = 18, kOutWarp = 19;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 128, kColK = 256;  // two of at most 64 columns each
 constexpr float kLift = 7.f;    // weights are 2^kLift times their size ...
@@ -92,8 +92,11 @@ struct Control {
   TileInfo info[kInfo];
   SegInfo seg[kSegs];
   alignas(16) float f[kF][kTc4Rows];   // factor of a row's scores
-  alignas(16) float mx[4][2 * kTc4Rows], sum[4][2 * kTc4Rows];  // by warp of a warpgroup: both streams' columns
+  // both streams' columns: minus (reference - kLift), what O and the sums shrink by as it
+  // moves, and by warp of a warpgroup the maxima and sums
+  alignas(16) float nm[2 * kTc4Rows], corr[2 * kTc4Rows], mx[4][2 * kTc4Rows], sum[4][2 * kTc4Rows];
   int tiles;                              // of the CTA's share
+  Segment first;                          // its first
   Line line;
 };
 
@@ -233,53 +236,75 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int
   return __all_sync(0xffffffffu, mbar_wait_abortable(bar, parity, abort, status, site));
 }
 
-__device__ __noinline__ Segment next_segment(const Attend4Args& a, const Control& sh, int x, int end) {
-  return segment_at(a, sh.line, x, end, blockIdx.x);
+// The first segment with key tiles at position x of the line or behind it (without: the
+// CTA's share ends first).
+__device__ __noinline__ Segment segment_from(const Attend4Args& a, const Line& line, int x, int end) {
+  Segment s;
+  s.tiles = 0;
+  while (x < end && s.tiles == 0) {
+    s = segment_at(a, line, x, end, blockIdx.x);
+    x = s.next;
+  }
+  return s;
 }
 
 // Q of a segment into shared memory as halves, K-major with the 128-byte swizzle, and the
-// factors of its rows' scores: warp `part` of `parts`, a row by 16 lanes, 8 dims each, FLIGHT
-// rows' loads under way together. (Short code where it comes first, see above.)
-template <int FLIGHT>
-__device__ __noinline__ void lay_out_q(const Attend4Args& a, const Segment& s, int n, uint32_t to, float* f, int part,
-                                       int parts) {
-  const int lane = threadIdx.x & 31, c = lane & 15;
-  const int row0 = s.rt * a.rows, rows = min(a.rows, a.T * a.G - row0);
-  const float scale = a.scale_log2 * exp2i(head_exp(a.k_exp, s.h));
+// factors of its rows' scores: warp `part` of `parts`, a row by 4 lanes, 32 dims each, the next
+// row's loads under way meanwhile. (It takes its arguments by value: read through a
+// reference to the kernel's parameters, 64 rows took a warp 39000 cycles.)
+struct QRows {
+  const __nv_bfloat16* q;  // the (sequence, head)'s first row
+  float scale;
+  int row0, rows, d, G, g_shift, skip;  // skip: from a token's last row of the head to the next token's first
+};
+__device__ __forceinline__ QRows q_rows(const Attend4Args& a, const Segment& s) {
+  QRows x;
+  x.q = static_cast<const __nv_bfloat16*>(a.q) + row_at(a, s.b, s.h, 0) * a.d;
+  x.scale = a.scale_log2 * exp2i(head_exp(a.k_exp, s.h));
+  x.row0 = s.rt * a.rows;
+  x.rows = min(a.rows, a.T * a.G - x.row0);
+  x.d = a.d, x.G = a.G, x.g_shift = a.g_shift, x.skip = a.Hq - a.G;
+  return x;
+}
+__device__ __noinline__ void lay_out_q(const QRows x, int n, uint32_t to, float* f, int part, int parts) {
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  auto load = [&](int r, uint4 (&w)[4]) {
+    const int at = x.row0 + r, t = x.g_shift >= 0 ? at >> x.g_shift : quotient(at, x.G);
+    const __nv_bfloat16* from = x.q + (long long)(at + t * x.skip) * x.d;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      w[k] = make_uint4(0, 0, 0, 0);
+      if (r < x.rows && 8 * (c + 4 * k) < x.d) w[k] = __ldcg(reinterpret_cast<const uint4*>(from) + c + 4 * k);
+    }
+  };
+  int r = part * 8 + (lane >> 2);
+  uint4 next[4];
+  load(r, next);
 #pragma unroll 1
-  for (int r0 = part * 2 + (lane >> 4); r0 - (lane >> 4) < n; r0 += 2 * parts * FLIGHT) {
-    uint4 w[FLIGHT];
+  for (; part * 8 < n; part += parts, r += 8 * parts) {
+    uint32_t w[16], m = 0;
 #pragma unroll
-    for (int u = 0; u < FLIGHT; ++u) {
-      const int r = r0 + 2 * parts * u;
-      w[u] = make_uint4(0, 0, 0, 0);
-      if (r < rows && 8 * c < a.d)
-        w[u] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                     row_at(a, s.b, s.h, row0 + r) * a.d) + c);
+    for (int k = 0; k < 4; ++k) {
+      w[4 * k] = next[k].x, w[4 * k + 1] = next[k].y, w[4 * k + 2] = next[k].z, w[4 * k + 3] = next[k].w;
     }
+    if ((part + parts) * 8 < n) load(r + 8 * parts, next);
+    // the largest element's bits (of positive floats they compare as integers; a NaN's are
+    // the largest and leave the row as it is)
 #pragma unroll
-    for (int u = 0; u < FLIGHT; ++u) {
-      const int r = r0 + 2 * parts * u;
-      // the largest element's bits (of positive floats they compare as integers; a NaN's are
-      // the largest and leave the row as it is)
-      const uint32_t two[4] = {w[u].x & 0x7fff7fffu, w[u].y & 0x7fff7fffu, w[u].z & 0x7fff7fffu, w[u].w & 0x7fff7fffu};
-      const uint32_t m01 = __vmaxu2(two[0], two[1]), m23 = __vmaxu2(two[2], two[3]), m4 = __vmaxu2(m01, m23);
-      uint32_t top = max(m4 & 0xffffu, m4 >> 16);
+    for (int i = 0; i < 16; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    uint32_t top = max(m & 0xffffu, m >> 16);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // the power of two that takes it into [2^14, 2^15)
+    const int e = (int)(top >> 7), up = e == 0 || e == 255 ? 0 : min(100, 127 + 14 - e);
+    const float k2 = exp2i(up);
 #pragma unroll
-      for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // the power of two that takes it into [2^14, 2^15)
-      const int e = (int)(top >> 7), up = e == 0 || e == 255 ? 0 : min(100, 127 + 14 - e);
-      const float k = exp2i(up);
-      const uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-      uint32_t h[4];
+    for (int i = 0; i < 16; ++i) w[i] = pack_f16(__uint_as_float(w[i] << 16) * k2, __uint_as_float(w[i] & 0xffff0000u) * k2);
+    const uint32_t row = to + r * 128, chunk = (uint32_t)(c ^ (r & 7)) << 4;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        h[i] = pack_f16(__uint_as_float(ww[i] << 16) * k, __uint_as_float(ww[i] & 0xffff0000u) * k);
-      if (r < n) {
-        sts128(to + (c >> 3) * (n * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-        if (c == 0) f[r] = scale * exp2i(-up);
-      }
-    }
+    for (int k = 0; k < 4; ++k)
+      sts128(row + (k >> 1) * (n * 128) + (chunk ^ (k & 1) << 6), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    if (c == 0) f[r] = x.scale * exp2i(-up);
   }
   fence_proxy_async_shared();
   __syncwarp();
@@ -317,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       mbar_init(smem_u32(&sh.o_ready[i]), 8);
       mbar_init(smem_u32(&sh.pv_done[i]), 1);
       mbar_init(smem_u32(&sh.o_empty[i]), 4);
-      mbar_init(smem_u32(&sh.q_full[i]), 1);
+      mbar_init(smem_u32(&sh.q_full[i]), 2);
       mbar_init(smem_u32(&sh.drained[i]), 1);
       mbar_init(smem_u32(&sh.q_empty[i]), 1);
       mbar_init(smem_u32(&sh.meet[i]), 4);
@@ -329,19 +354,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
   }
   pdl_wait();
   pdl_trigger();
-  if (warp == kKLoadWarp) {
+  if (warp == kOutWarp) {
     if (make_line(a, &sh.line)) atomicOr(a.status, SV_FLAG_BAD_LENGTH);
     __syncwarp();
-    const int before = lane < 2 ? tiles_before(a, sh.line, sh.line.begin(blockIdx.x + lane)) : 0;
-    const int share = __shfl_sync(0xffffffffu, before, 1) - before;
-    if (lane == 0) sh.tiles = share;
-    __syncwarp();
+    const int x = sh.line.begin(blockIdx.x), end = sh.line.begin(blockIdx.x + 1);
+    int tiles = 0;
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) tiles = tiles_before(a, sh.line, i ? end : x) - tiles;
+    if (lane == 0) sh.tiles = tiles;
+    const Segment s = segment_from(a, sh.line, x, end);
+    if (lane == 0) sh.first = s;
+  } else if (warp == kKLoadWarp || warp == kVLoadWarp) {
+    // earlier kernels' plain stores to the pools come before this one's bulk copies
+    asm volatile("fence.proxy.async.global;" ::: "memory");
   }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = sh.tmem;
-  const int begin = sh.line.begin(blockIdx.x), end = sh.line.begin(blockIdx.x + 1);
   const uint32_t tiles = (uint32_t)sh.tiles;
   auto wait = [&](uint64_t& bar, uint32_t parity, unsigned site) {
     const uint32_t addr = smem_u32(&bar);
@@ -354,10 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
   };
 
   if (warp < kKLoadWarp && tiles) {
-    // the first segment's Q, which everybody waits for (later ones: one warp, ahead)
-    Segment s = next_segment(a, sh, begin, end);
-    if (s.tiles == 0) s = next_segment(a, sh, s.next, end);
-    lay_out_q<1>(a, s, N, q_base, sh.f[0], warp, kKLoadWarp);
+    // the first segment's Q, which everybody waits for (later ones: the loading warps, ahead)
+    lay_out_q(q_rows(a, sh.first), N, q_base, sh.f[0], warp, kKLoadWarp);
     arrive(sh.q_first);
   }
   if (warp < 4) {
@@ -471,15 +499,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       arrive(sh.meet[wg]);
       return wait(sh.meet[wg], met++, 17u);
     };
-    // The four sums over lane / 4 of a pair of columns, in lanes 0 .. 3.
-    auto fold = [&](float2 x, auto op) {
+    // What `op` makes of the warp's values of each pair of columns, x[j] in lane (g, t2) that of
+    // columns 8 j + t2: to row[own0 + ..]. Lanes halve their columns with every exchange.
+    auto fold = [&](float2* x, float* row, auto op) {
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        x.x = op(x.x, __shfl_xor_sync(0xffffffffu, x.x, o));
-        x.y = op(x.y, __shfl_xor_sync(0xffffffffu, x.y, o));
+      for (int o = 16, n = J / 2; o >= 4; o >>= 1, n >>= 1) {
+        const bool up = lane & o;
+        if (n) {
+#pragma unroll
+          for (int j = 0; j < n; ++j) {
+            const float2 keep = up ? x[j + n] : x[j], give = up ? x[j] : x[j + n];
+            x[j].x = op(keep.x, __shfl_xor_sync(0xffffffffu, give.x, o));
+            x[j].y = op(keep.y, __shfl_xor_sync(0xffffffffu, give.y, o));
+          }
+        } else {
+          x[0].x = op(x[0].x, __shfl_xor_sync(0xffffffffu, x[0].x, o));
+          x[0].y = op(x[0].y, __shfl_xor_sync(0xffffffffu, x[0].y, o));
+        }
       }
-      return x;
+      if (g % (8 / J) == 0) *reinterpret_cast<float2*>(row + own0 + g / (8 / J) * 8 + t2) = x[0];
     };
+    const int mine = own0 + in_wg * 32 + lane;  // the column whose reference the thread keeps
+    const bool keeps = in_wg * 32 + lane < NC;
     for (uint32_t i = wg; i < tiles; i += 2) {  // (i & 1 = wg: the buffers of S, P and O)
       const uint32_t turn = i >> 1;
       if (!wait(sh.s_full[wg], turn, 5u)) break;
@@ -534,49 +575,42 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
 #pragma unroll 1
       for (bool over = first && any;; over = true) {
         if (over) {
+          float2 m[J];
 #pragma unroll
           for (int ch = 0; ch < NCH; ++ch) {
             load(ch);
 #pragma unroll
             for (int j = 0; j < CH / 8; ++j) {
               const float2 ff = unpack2(f[ch * (CH / 8) + j]);
-              float2 m = make_float2(-INFINITY, -INFINITY);
+              float2 x = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const uint32_t* v = &s[k >> 1][4 * j + 2 * (k & 1)];
-                if (on[k]) m = make_float2(fmaxf(m.x, __uint_as_float(v[0]) * ff.x), fmaxf(m.y, __uint_as_float(v[1]) * ff.y));
+                if (on[k]) x = make_float2(fmaxf(x.x, __uint_as_float(v[0]) * ff.x), fmaxf(x.y, __uint_as_float(v[1]) * ff.y));
               }
-              m = fold(m, [](float x, float y) { return fmaxf(x, y); });
-              if (lane < 4) *reinterpret_cast<float2*>(&sh.mx[in_wg][own0 + ch * CH + 8 * j + t2]) = m;
+              m[ch * (CH / 8) + j] = x;
             }
+          }
+          fold(m, sh.mx[in_wg], [](float x, float y) { return fmaxf(x, y); });
+          if (!(ok = meet())) break;
+          if (keeps) {
+            const float top = fmaxf(fmaxf(sh.mx[0][mine], sh.mx[1][mine]), fmaxf(sh.mx[2][mine], sh.mx[3][mine]));
+            const float old = kLift - sh.nm[mine];
+            const bool up = first || top > old + kSlack;
+            if (up) sh.nm[mine] = kLift - top;
+            sh.corr[mine] = up ? ex2(old - top) : 1.f;  // (not read for a stream's first)
           }
           if (!(ok = meet())) break;
-          float2 corr[J];
 #pragma unroll
-          for (int j = 0; j < J; ++j) {
-            float2 top = make_float2(-INFINITY, -INFINITY);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const float2 m = *reinterpret_cast<const float2*>(&sh.mx[w][own0 + 8 * j + t2]);
-              top = make_float2(fmaxf(top.x, m.x), fmaxf(top.y, m.y));
-            }
-            float2 n = unpack2(nm[j]);
-            auto follow = [&](float& n, float top) {
-              const float old = kLift - n;
-              const bool up = first || top > old + kSlack;
-              if (up) n = kLift - top;
-              return up && !first ? ex2(old - top) : 1.f;
-            };
-            corr[j].x = follow(n.x, top.x);
-            corr[j].y = follow(n.y, top.y);
-            nm[j] = pack2(n.x, n.y);
-          }
+          for (int j = 0; j < J; ++j) nm[j] = *reinterpret_cast<const uint64_t*>(&sh.nm[own0 + 8 * j + t2]);
           if (!first) {
             // every product into O is complete
             if (!(ok = wait(sh.pv_done[wg], turn ^ 1u, 6u))) break;
             tc::fence_after();
+            float2 corr[J];
 #pragma unroll
             for (int j = 0; j < J; ++j) {
+              corr[j] = *reinterpret_cast<const float2*>(&sh.corr[own0 + 8 * j + t2]);
               const float2 x = unpack2(l[j]);
               l[j] = pack2(x.x * corr[j].x, x.y * corr[j].y);
             }
@@ -657,56 +691,42 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
         }
         tc::fence_before();
         arrive(sh.o_empty[wg]);
+        float2 x[J];
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const float2 x = fold(unpack2(l[j]), [](float x, float y) { return x + y; });
-          if (lane < 4) *reinterpret_cast<float2*>(&sh.sum[in_wg][own0 + 8 * j + t2]) = x;
-        }
+        for (int j = 0; j < J; ++j) x[j] = unpack2(l[j]);
+        fold(x, sh.sum[in_wg], [](float x, float y) { return x + y; });
         if (!meet()) break;
-        if (in_wg == 0 && lane < 4) {
-#pragma unroll
-          for (int j = 0; j < J; ++j) {
-            const float2 n = unpack2(nm[j]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int c = 8 * j + t2 + e, r = c;
-              if (r >= si.rows) continue;
-              const float x = (sh.sum[0][own0 + c] + sh.sum[1][own0 + c]) + (sh.sum[2][own0 + c] + sh.sum[3][own0 + c]);
-              a.part_ml[out + r] = first ? make_float2(-INFINITY, 0.f) : make_float2(e ? -n.y : -n.x, x);
-              if (info.flags & kOnly) a.part_ml[out + r + (wg ? -a.rows : a.rows)] = make_float2(-INFINITY, 0.f);
-            }
-          }
+        // (the sums' next writer comes behind a vote of the next tile's, and with it all these reads)
+        const int r = in_wg * 32 + lane;
+        if (r < si.rows) {
+          const float sum = (sh.sum[0][mine] + sh.sum[1][mine]) + (sh.sum[2][mine] + sh.sum[3][mine]);
+          a.part_ml[out + r] = first ? make_float2(-INFINITY, 0.f) : make_float2(-sh.nm[mine], sum);
+          if (info.flags & kOnly) a.part_ml[out + r + (wg ? -a.rows : a.rows)] = make_float2(-INFINITY, 0.f);
         }
-        if (!meet()) break;  // the exchange array is free again
       }
     }
   } else {
     if (warp == kKLoadWarp || warp == kVLoadWarp) {
       // ------------------------------------------------------------ segments, pages, copies
-      // One warp copies K and tells the others of a tile, one copies V and lays out Q of the
-      // segments behind the first. (A copy takes its warp 110 cycles, and a tile of two pages
-      // is four.)
+      // One warp copies K and tells the others of a tile, one copies V (a copy takes its warp
+      // 110 cycles, and a tile of two pages is four); both lay out Q of the segments behind
+      // the first.
       const bool is_v = warp == kVLoadWarp;
       const uint8_t* pool = is_v ? a.v_pool : a.k_pool;
-      // earlier kernels' plain stores to the pools come before this one's bulk copies
-      asm volatile("fence.proxy.async.global;" ::: "memory");
       unsigned flags = 0;
       const uint64_t once = l2_evict_first_policy();
       const int unit_shift = a.ppb_shift < 0 ? 0 : min(a.ppb_shift, 3);  // log2 of a unit's pieces
       uint32_t i = 0, st = 0, ph = 0, seg = 0;
       bool ok = true;
-      for (int x = begin; ok && x < end;) {
-        const Segment s = next_segment(a, sh, x, end);
-        x = s.next;
-        if (s.tiles == 0) continue;
-        if (is_v) {
-          if (seg > 0) {
-            // (its buffer's segment before, the first one too, has been multiplied)
-            if (seg > 1 && !(ok = wait(sh.q_empty[seg & 1], (seg >> 1) - 1, 10u))) break;
-            lay_out_q<4>(a, s, N, q_base + (seg & 1) * C::kQBytes, sh.f[seg % kF], 0, 1);
-            arrive(sh.q_full[seg & 1]);
-          }
-        } else if (lane == 0) {
+      const int end = sh.line.begin(blockIdx.x + 1);
+      for (Segment s = sh.first; ok && s.tiles; s = segment_from(a, sh.line, s.next, end)) {
+        if (seg > 0) {
+          // (its buffer's segment before, the first one too, has been multiplied)
+          if (seg > 1 && !(ok = wait(sh.q_empty[seg & 1], (seg >> 1) - 1, 10u))) break;
+          lay_out_q(q_rows(a, s), N, q_base + (seg & 1) * C::kQBytes, sh.f[seg % kF], is_v, 2);
+          arrive(sh.q_full[seg & 1]);
+        }
+        if (!is_v && lane == 0) {
           sh.seg[seg % kSegs].slot = s.slot;
           sh.seg[seg % kSegs].rows = min(a.rows, a.T * a.G - s.rt * a.rows);
         }
