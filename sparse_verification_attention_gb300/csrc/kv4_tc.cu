@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
         on[0] = g < v0, on[1] = g + 8 < v0, on[2] = g < v1, on[3] = g + 8 < v1;
       }
       const uint32_t tmem_s = tmem + tlane + kColS + wg * 64;
-      uint32_t s[2][CH / 2], p[NCH][2][CH / 4];
+      uint32_t s[2][CH / 2];
       uint64_t sums[J];
       // scores of keys 0 .. 15 and 16 .. 31 of the warp's: columns 8 j + t2 (+ 1) of key g in
       // s[.][4 j] (4 j + 1), of key g + 8 in 4 j + 2 (4 j + 3)
@@ -551,8 +551,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
         ld_16x256b<CH / 8>(tmem_s + ch * CH + (16u << 16), s[1]);
         tc::wait_ld();
       };
-      // weights of a run of columns as halves, and their sums over the thread's keys
+      // Weights of a run of columns, their sums over the thread's keys, and P^T into shared
+      // memory: row = key, 128 bytes of 64 columns, 128-byte swizzle; 8 x 8 blocks of halves as
+      // they lie in the registers.
+      const uint32_t row = p_base + wg * C::kPBytes + (uint32_t)prow * 128;
       auto weigh = [&](int ch, auto masked) {
+        uint32_t p[2][CH / 4];
 #pragma unroll
         for (int j = 0; j < CH / 8; ++j) {
           const int col = ch * (CH / 8) + j;
@@ -564,14 +568,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
             float2 e = make_float2(ex2(x.x), ex2(x.y));
             if (decltype(masked)::value && !on[k]) e = make_float2(0.f, 0.f);
             sum = add2(sum, pack2(e.x, e.y));
-            p[ch][k >> 1][2 * j + (k & 1)] = pack_f16(e.x, e.y);
+            p[k >> 1][2 * j + (k & 1)] = pack_f16(e.x, e.y);
           }
           sums[col] = sum;
+        }
+        const uint32_t at = row + (uint32_t)(((ch * (CH / 8) + pchunk) ^ (lane & 7)) << 4);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t* r = p[h];
+          if constexpr (NC == 16) {
+            put(at + h * 16 * 128, r[0], r[2], r[1], r[3]);  // (columns 0 and 8 of keys 0 .., then of keys 8 ..)
+          } else {
+            put(at + h * 16 * 128, r[0], r[2], r[4], r[6]);
+            put(at + (h * 16 + 8) * 128, r[1], r[3], r[5], r[7]);
+          }
         }
       };
       // References move when the stream begins and when the vote says so: maxima over the
       // tile's keys, then O and the sums follow.
-      bool ok = true;
+      // The products of the stream's tile before, which read P and write O, are complete.
+      bool ok = wait(sh.pv_done[wg], turn ^ 1u, 6u);
+      if (!ok) break;
+      tc::fence_after();
 #pragma unroll 1
       for (bool over = first && any;; over = true) {
         if (over) {
@@ -604,9 +622,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
 #pragma unroll
           for (int j = 0; j < J; ++j) nm[j] = *reinterpret_cast<const uint64_t*>(&sh.nm[own0 + 8 * j + t2]);
           if (!first) {
-            // every product into O is complete
-            if (!(ok = wait(sh.pv_done[wg], turn ^ 1u, 6u))) break;
-            tc::fence_after();
             float2 corr[J];
 #pragma unroll
             for (int j = 0; j < J; ++j) {
@@ -650,24 +665,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
       arrive(sh.s_ready[wg]);  // S has been read: room for the next in its place
 #pragma unroll
       for (int j = 0; j < J; ++j) l[j] = add2(l[j], sums[j]);
-      // P^T into shared memory: row = key, 128 bytes of 64 columns, 128-byte swizzle; 8 x 8 blocks
-      // as they lie in the registers
-      if (!wait(sh.pv_done[wg], turn ^ 1u, 7u)) break;
-      const uint32_t row = p_base + wg * C::kPBytes + (uint32_t)prow * 128;
-#pragma unroll
-      for (int ch = 0; ch < NCH; ++ch) {
-        const uint32_t at = row + (uint32_t)(((ch * (CH / 8) + pchunk) ^ (lane & 7)) << 4);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t* r = p[ch][h];
-          if constexpr (NC == 16) {
-            put(at + h * 16 * 128, r[0], r[2], r[1], r[3]);  // (columns 0 and 8 of keys 0 .., then of keys 8 ..)
-          } else {
-            put(at + h * 16 * 128, r[0], r[2], r[4], r[6]);
-            put(at + (h * 16 + 8) * 128, r[1], r[3], r[5], r[7]);
-          }
-        }
-      }
       fence_proxy_async_shared();
       tc::fence_before();
       arrive(sh.o_ready[wg]);
@@ -677,17 +674,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
         tc::fence_after();
         const SegInfo si = sh.seg[info.seg % kSegs];
         const long long out = (2ll * si.slot + wg) * a.rows;
-        const int m = quad * 32 + lane, dim = dim_of(m);
+        const int m = quad * 32 + lane;
+        float* to = a.part_o + out * (groups * 16) + dim_of(m);
+        const int cols = m < groups * 16 ? si.rows : 0;
 #pragma unroll 1
-        for (int c0 = 0; c0 < NC; c0 += 8) {
+        for (int c0 = 0; c0 < NC; c0 += 8, to += 8 * groups * 16) {
           uint32_t o[8];
           ld8(tmem_o + c0, o);
           tc::wait_ld();
-          if (m < groups * 16) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (c0 + e < si.rows) a.part_o[(out + c0 + e) * (groups * 16) + dim] = __uint_as_float(o[e]);
-          }
+          for (int e = 0; e < 8; ++e)
+            if (c0 + e < cols) to[e * groups * 16] = __uint_as_float(o[e]);
         }
         tc::fence_before();
         arrive(sh.o_empty[wg]);
