@@ -47,7 +47,7 @@ namespace {
 
 using namespace kv4;
 
-constexpr int kPairCost = 8;  // key tiles' time that beginning a pair takes
+constexpr int kPairCost = 5;  // key tiles' time that beginning a pair takes
 static_assert(kPairCost <= kMaxPairCost, "the calls' limits count this many");
 constexpr int kKeys = 128, kPieces = kKeys / kPiece;
 // Rings. Copies run at most kMaxStages tiles ahead of V, V two ahead of its products, so the
@@ -482,14 +482,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
     // columns stay in registers. (With a key a thread and all columns they came from shared
     // memory, 16 loads of 16 bytes a tile that the other roles' traffic held up: 800 to
     // 1200 cycles for 80 instructions.)
-    constexpr int NC = N, CH = NC < 32 ? NC : 32, NCH = NC / CH, J = NC / 8;
+    constexpr int NC = N, CH = 16, NCH = NC / CH, J = NC / 8;  // (in runs of 32 columns the registers spilled)
     const int wg = (warp - kSoftmaxWarp) >> 2, quad = warp & 3, in_wg = (warp - kSoftmaxWarp) & 3;
     // the stream's columns of O and of the exchange arrays
     const int own0 = wg * NC;
     const int g = lane >> 2, t2 = (lane & 3) * 2;  // key in eight, column in eight
     const uint32_t tlane = (uint32_t)(quad * 32) << 16, tmem_o = tmem + tlane + kColO + own0;
     // this lane's row of the 8 x 8 blocks that it addresses for P's stores (see put)
-    const int prow = quad * 32 + (NC == 16 ? (lane >> 4) * 8 : 0) + (lane & 7), pchunk = NC == 16 ? lane >> 3 & 1 : lane >> 3;
+    const int prow = quad * 32 + (lane >> 4) * 8 + (lane & 7), pchunk = lane >> 3 & 1;
     arrive(sh.s_ready[wg]);  // S is free
     uint64_t f[J], nm[J], l[J];  // factor, minus (reference - kLift), sum: two columns each
     bool first = true;           // no key of the stream has counted yet
@@ -574,15 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
         }
         const uint32_t at = row + (uint32_t)(((ch * (CH / 8) + pchunk) ^ (lane & 7)) << 4);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t* r = p[h];
-          if constexpr (NC == 16) {
-            put(at + h * 16 * 128, r[0], r[2], r[1], r[3]);  // (columns 0 and 8 of keys 0 .., then of keys 8 ..)
-          } else {
-            put(at + h * 16 * 128, r[0], r[2], r[4], r[6]);
-            put(at + (h * 16 + 8) * 128, r[1], r[3], r[5], r[7]);
-          }
-        }
+        for (int h = 0; h < 2; ++h)  // (columns 0 and 8 of keys 0 .., then of keys 8 ..)
+          put(at + h * 16 * 128, p[h][0], p[h][2], p[h][1], p[h][3]);
       };
       // References move when the stream begins and when the vote says so: maxima over the
       // tile's keys, then O and the sums follow.
