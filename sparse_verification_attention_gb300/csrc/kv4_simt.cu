@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(kThreads) attend4_simt_kernel(const __grid_con
   Control& sh = *reinterpret_cast<Control*>(p + kRows * (kKeys + 1));
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int stride = tile_stride(a.d), groups = a.d / kGroup, pb = piece_bytes(a.d);
+  const int inv = quotient(65535, groups) + 1;  // x * inv >> 16 = x / groups for x < 64, groups <= 16
   unsigned flags = 0;
   pdl_wait();
   pdl_trigger();
@@ -62,9 +63,10 @@ __global__ void __launch_bounds__(kThreads) attend4_simt_kernel(const __grid_con
     if (s.tiles == 0) continue;
     const int row0 = s.rt * a.rows, rows = min(a.rows, a.T * a.G - row0);
     const float scale = a.scale_log2 * exp2i(head_exp(a.k_exp, s.h));
-    for (int i = tid; i < kRows * a.d; i += kThreads) {
-      const int r = i / a.d, c = i - r * a.d;
-      q[i] = r < rows ? as_float(static_cast<const T*>(a.q)[row_at(a, s.b, s.h, row0 + r) * a.d + c]) * scale : 0.f;
+#pragma unroll 1
+    for (int r = ty; r < kRows; r += 16) {
+      const T* from = static_cast<const T*>(a.q) + (r < rows ? row_at(a, s.b, s.h, row0 + r) : 0) * a.d;
+      for (int c = tx; c < a.d; c += 16) q[r * a.d + c] = r < rows ? as_float(from[c]) * scale : 0.f;
     }
     // rows ty and ty + 16: reference and sum (the same in the row's 16 threads), outputs
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -79,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) attend4_simt_kernel(const __grid_con
       __syncthreads();
       // K: a thread takes 8 bytes (a group of a token) at a time
       for (int i = tid; i < kKeys * groups; i += kThreads) {
-        const int key = i & 15, rest = i >> 4, g = rest % groups, pc = rest / groups;
+        const int key = i & 15, rest = i >> 4, pc = rest * inv >> 16, g = rest - pc * groups;
         float f[16];
         const bool on = key < sh.valid[pc];
         const uint8_t* piece = a.k_pool + (on ? sh.piece[pc] : 0) * pb;
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) attend4_simt_kernel(const __grid_con
       // V: a thread takes one byte (dims c and c + 8 of a token) at a time; tokens that
       // do not count are zero whatever their bytes hold
       for (int i = tid; i < kKeys * groups * 8; i += kThreads) {
-        const int key = i & 15, c = i >> 4 & 7, rest = i >> 7, g = rest % groups, pc = rest / groups;
+        const int key = i & 15, c = i >> 4 & 7, rest = i >> 7, pc = rest * inv >> 16, g = rest - pc * groups;
         float2 v = make_float2(0.f, 0.f);
         if (key < sh.valid[pc]) {
           const uint8_t* piece = a.v_pool + sh.piece[pc] * pb;
