@@ -673,9 +673,10 @@ size_t sv_kv4_workspace_bytes(const sv_shape* shape);
  * cache stands for. T = 1 is a decoding step: the token's own key and value are
  * the one draft. The drafts are not quantised.
  * sel == NULL attends to every block; else [B, Hkv, sel_stride] with n_sel
- * entries a row, n_sel <= sel_stride and nb_max, of which -1 holds nothing (the
- * rows of sequences with smaller budgets) and others outside the sequence's full
- * blocks are left out and raise SV_FLAG_BAD_BLOCK_INDEX. A partial last block is
+ * entries a row in any order, n_sel <= sel_stride and nb_max, of which -1 holds
+ * nothing (the rows of sequences with smaller budgets) and others outside the
+ * sequence's full blocks are left out and raise SV_FLAG_BAD_BLOCK_INDEX; a block
+ * that a row names twice counts twice. A partial last block is
  * attended in every case, its first seq_ctx % blk tokens; the rest of its page
  * may hold anything. Keys on a page outside the pool are left out
  * (SV_FLAG_BAD_PAGE), lengths are clamped as above.

@@ -25,7 +25,7 @@ sv_status check_words4(const char* names, std::initializer_list<const void*> arr
 sv_status check_rows4(const sv_shape* s, const char* name, const void* p, long long stride, int heads) {
   if (!p) return fail(SV_ERR_INVALID_ARG, "%s is NULL", name);
   if (!aligned(p, 16)) return fail(SV_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
-  if (stride < (long long)heads * s->d || stride * (long long)elt_bytes(s) % 16 || stride >= (1ll << 38))
+  if (stride < (long long)heads * s->d || stride >= (1ll << 38) || stride * (long long)elt_bytes(s) % 16)
     return fail(SV_ERR_INVALID_ARG,
                 "%s rows are %lld elements apart: need at least %d and a multiple of 16 bytes", name, stride,
                 heads * s->d);

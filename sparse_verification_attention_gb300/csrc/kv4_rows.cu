@@ -11,7 +11,7 @@ constexpr int kThreads = 256;
 constexpr int kGroup = 16;  // dims that share a scale
 
 // 16 elements of bf16 or fp32, in 32-byte accesses where the rows allow it (`wide`): in two
-// halves every sector is asked for, or written, twice.
+// halves every sector is asked for, or written, twice. (Loads past L1, as with __ldcg.)
 template <typename T>
 __device__ __forceinline__ void load16(const T* p, bool wide, float (&x)[16]) {
   uint32_t w[4 * sizeof(T)];
@@ -20,7 +20,7 @@ __device__ __forceinline__ void load16(const T* p, bool wide, float (&x)[16]) {
     uint32_t* v = w + 4 * i;
     const uint4* q = reinterpret_cast<const uint4*>(p) + i;
     if (wide) {
-      asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      asm volatile("ld.relaxed.gpu.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                    : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                    : "l"(q));
     } else {

@@ -139,6 +139,24 @@ def test_bad_slots():
     assert not any(p.any() for p in pools)
 
 
+def test_reading_slots_that_repeat():
+    """From a second stream, into rows that are parts of wider ones."""
+    s = api.make_shape(1, 3, 3, 48, 32, 1, BF16)
+    x = torch.randn(64, 3, 48, generator=gen(4)).to(BF16)
+    kv = api.make_kv4(*[api.alloc_kv4_pool(s, 2) for _ in range(2)])
+    api.sv_write_kv4(s, x.cuda(), -x.cuda(), torch.arange(64, dtype=torch.int32, device="cuda"), kv)
+    slots = torch.randint(0, 64, (200,), generator=gen(5)).to(torch.int32)
+    wide = torch.full((200, 2, 3, 48), 7, dtype=BF16, device="cuda")
+    on_gpu = slots.cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        api.sv_read_kv4(s, kv, on_gpu, wide[:, 0], wide[:, 1])
+    torch.cuda.current_stream().wait_stream(side)
+    w = U.values(*U.quantise(x))[slots.long()]
+    assert torch.equal(wide[:, 0].cpu().double(), w) and torch.equal(wide[:, 1].cpu().double(), -w)
+
+
 def test_pool_past_4_gib():
     s = api.make_shape(1, 1, 1, 128, 16, 1, BF16)
     pages = 3_800_000  # 1152 bytes each
@@ -292,6 +310,50 @@ def test_attend_selection(shape, n_sel, short):
     out, ws = run(s, kv, dev, sel, parents, n_sel=n_sel)
     assert api.sv_read_status(ws) == 0
     compare(out, x, k, v, lens, Hkv, blk, sel[:, :, :n_sel], parents, on_tensor_cores(Hq, Hkv, d, dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("blk", [16, 48])
+def test_attend_selection_in_any_order(dtype, blk):
+    """Long rows with gaps, blocks out of order and some of them twice: a block counts as
+    often as its row names it."""
+    lens, Hkv, n_sel, T = [3000, 2500, 900], 2, 3000 // blk, 4
+    s, kv, x, dev, k, v = problem(15, lens, 8, Hkv, 64, blk, T, dtype, True)
+    r = random.Random(blk)
+    sel = torch.full((3, Hkv, n_sel), -1, dtype=torch.int32)
+    for b, n in enumerate(lens):
+        for h in range(Hkv):
+            for i in range(n_sel):
+                if r.random() < (0.9, 0.5, 0.02)[b]:
+                    sel[b, h, i] = r.randrange(n // blk)
+    out, ws = run(s, kv, dev, sel, None)
+    assert api.sv_read_status(ws) == 0
+    G = 4
+    for b, n in enumerate(lens):
+        for h in range(Hkv):
+            named = [t for j in sel[b, h].tolist() if j >= 0 for t in range(j * blk, (j + 1) * blk)]
+            at = torch.tensor(named + list(range(n // blk * blk, n)), dtype=torch.long)
+            kk, vv = (torch.cat([c[b][at, h], x[d][b, :, h].double()])[:, None].cuda()
+                      for c, d in ((k, "draft_k"), (v, "draft_v")))
+            see = torch.ones(T, 1, len(at) + T, dtype=torch.bool)
+            see[:, :, len(at):] = P.draft_mask(None, T, "cpu")[:, None]
+            q = x["q"][b, :, h * G:(h + 1) * G]
+            U.check(out[b, :, h * G:(h + 1) * G], *U.attend(q.cuda(), kk, vv, see.cuda(), dtype == BF16))
+
+
+@pytest.mark.parametrize("blk", [80, 256])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attend_page_sizes(blk, dtype):
+    """Pages that end inside a key tile, and pages of several tiles."""
+    lens = [1234, blk, blk - 1, 3 * blk + 17]
+    s, kv, x, dev, k, v = problem(16, lens, 8, 2, 64, blk, 3, dtype)
+    out, ws = run(s, kv, dev, None, None)
+    assert api.sv_read_status(ws) == 0
+    compare(out, x, k, v, lens, 2, blk, None, None, dtype == BF16)
+    sel = selection(gen(17), lens, 2, blk, 3, True)[:, :, :3].contiguous()
+    out, ws = run(s, kv, dev, sel, None)
+    assert api.sv_read_status(ws) == 0
+    compare(out, x, k, v, lens, 2, blk, sel, None, dtype == BF16)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
