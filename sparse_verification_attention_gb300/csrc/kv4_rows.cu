@@ -198,10 +198,11 @@ __global__ void __launch_bounds__(kThreads) read_kv4_kernel(const __grid_constan
 //
 // Code times scale is exact in f16. What costs is to sum halves in fp32: a conversion each
 // and an addition, 62 us for 5,102 blocks of 8 heads. A product with the identity does it
-// instead: in m16n8k8 a lane's two A registers lie at the same rows and columns as its four
-// sums, so S += A I adds the four halves to the lane's own sums. (A NaN reaches the sums in
-// its row of 4 lanes, which are the same dims of the group's other tokens.) Six CTAs an SM, a
-// piece at a time, 51.6 us; three, two pieces at a time, 67.
+// instead: in m16n8k16 a lane's A registers lie at the rows and columns of its four sums and
+// at those 8 columns behind, so S += A (I above I) adds two tokens' halves to the lane's own
+// sums. (A NaN reaches the sums in its row of 4 lanes, which are the same dims of the group's
+// other tokens.) Six CTAs an SM, a piece at a time, 50.8 us (a token to a product of k = 8, 51.6);
+// four CTAs 55.5; three, two pieces at a time, 67.
 __global__ void __launch_bounds__(kThreads, 6) reps_kv4_kernel(const __grid_constant__ Reps4Args a) {
   const int lane = threadIdx.x & 31, sub = lane & 3;
   const int jb = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 6) reps_kv4_kernel(const __grid_cons
   const int groups = a.d / kGroup, pb = piece_bytes(a.d), pieces = a.blk / kPiece;
   const uint8_t* p = a.k_pool + ((long long)page * a.Hkv + h) * pieces * pb;
   const float unit = __fdiv_rn(exp2i(head_exp(a.k_exp, h)), (float)a.blk);
-  // B: rows 2 sub and 2 sub + 1 of column lane / 4
+  // B: rows 2 sub and 2 sub + 1 of column lane / 4, and the same 8 rows below
   const uint32_t identity = (lane >> 2 == 2 * sub ? 0x3c00u : 0u) | (lane >> 2 == 2 * sub + 1 ? 0x3c000000u : 0u);
   float* to = a.reps + (((long long)b * a.Hkv + h) * a.nb_max + j) * a.d;
 #pragma unroll 1
@@ -243,18 +244,20 @@ __global__ void __launch_bounds__(kThreads, 6) reps_kv4_kernel(const __grid_cons
       }
       e4m3x4_to_f16(sc, s[0], s[1]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t f[8];
-        e2m1x8_to_f16(k % 2 ? c[k / 2].z : c[k / 2].x, f);
-        e2m1x8_to_f16(k % 2 ? c[k / 2].w : c[k / 2].y, f + 4);
-        if (k % 2) scale_f16x2<1>(f, s[k / 2]);
-        else scale_f16x2<0>(f, s[k / 2]);
+      for (int k = 0; k < 2; ++k) {  // tokens 2 k, 2 k + 1
+        uint32_t f[2][8];
+        e2m1x8_to_f16(c[k].x, f[0]);
+        e2m1x8_to_f16(c[k].y, f[0] + 4);
+        e2m1x8_to_f16(c[k].z, f[1]);
+        e2m1x8_to_f16(c[k].w, f[1] + 4);
+        scale_f16x2<0>(f[0], s[k]);
+        scale_f16x2<1>(f[1], s[k]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           asm volatile(
-              "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+              "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%8}, {%0,%1,%2,%3};"
               : "+f"(sum[i][0]), "+f"(sum[i][1]), "+f"(sum[i][2]), "+f"(sum[i][3])
-              : "r"(f[2 * i]), "r"(f[2 * i + 1]), "r"(identity));
+              : "r"(f[0][2 * i]), "r"(f[0][2 * i + 1]), "r"(f[1][2 * i]), "r"(f[1][2 * i + 1]), "r"(identity));
       }
     }
     // fold: the lane keeps 4 of the 16 sums of its group
