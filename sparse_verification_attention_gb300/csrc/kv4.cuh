@@ -83,6 +83,17 @@ __device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
   return r & 0xffu;
 }
 
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+  return r;
+}
+
 constexpr int kMaxExp = 32;  // a head's exponent lies in [-32, 32]
 __device__ __forceinline__ int head_exp(const int32_t* e, int h) {
   return e ? min(max(e[h], -kMaxExp), kMaxExp) : 0;

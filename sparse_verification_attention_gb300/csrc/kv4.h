@@ -62,8 +62,9 @@ struct Reps4Args {
   float* reps;                 // [B, Hkv, nb_max, d]
   unsigned* status;            // may be null
   int B, Hkv, d, blk, nb_max, num_pages, max_blocks;
+  int heads, blk_shift;        // of a CTA; log2 of blk or -1 (both set by the launch)
 };
-cudaError_t launch_reps_kv4(const Reps4Args& a, cudaStream_t st);
+cudaError_t launch_reps_kv4(Reps4Args a, cudaStream_t st);
 
 // ---------------------------------------------------------------- attention
 constexpr int kMaxB4 = 1024;         // sequences of a call

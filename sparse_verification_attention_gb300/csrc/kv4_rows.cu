@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(64 * PAIRS) read_kv4_kernel(const __grid_const
   else read_groups<T, false>(a, p);
 }
 
-// One warp per (sequence, head, block): a lane has a group of 4 tokens of every piece (so
-// 16 sums), `gp` lanes side by side the groups (those of d > 128 in two rounds). The four
+// One warp per (sequence, block) and a few of its heads: a lane has a group of 4 tokens of
+// every piece (so 16 sums), 8 groups side by side (those of d > 128 in two rounds). The four
 // token subsets are folded at the end, always in the same order.
 //
 // Code times scale is exact in f16. What costs is to sum halves in fp32: a conversion each
@@ -204,78 +204,99 @@ __global__ void __launch_bounds__(64 * PAIRS) read_kv4_kernel(const __grid_const
 // instead: in m16n8k16 a lane's A registers lie at the rows and columns of its four sums and
 // at those 8 columns behind, so S += A (I above I) adds two tokens' halves to the lane's own
 // sums. (A NaN reaches the sums in its row of 4 lanes, which are the same dims of the group's
-// other tokens.) Six CTAs an SM, a piece at a time, 50.8 us (a token to a product of k = 8, 51.6);
-// four CTAs 55.5; three, two pieces at a time, 67.
-__global__ void __launch_bounds__(kThreads, 6) reps_kv4_kernel(const __grid_constant__ Reps4Args a) {
+// other tokens.)
+// The same blocks: 51 us with one head a warp, whose lengths, page and places took as many
+// instructions as a third of its sums (72% of the issue slots, HBM at 0.6 of its rate); 41.7 us
+// now, 5.0 TB/s. Five CTAs an SM; six spill (44.7), four 42.8.
+constexpr int kSlot = 4608;  // bytes of a block that a warp has under way together, at most
+// DG: groups of 16 dims (8: d = 128), 0: any number.
+template <int DG>
+__global__ void __launch_bounds__(kThreads, 5) reps_kv4_kernel(const __grid_constant__ Reps4Args a) {
+  __shared__ __align__(16) uint8_t slots[kThreads / 32][kSlot];
+  const uint32_t slot = smem_u32(slots[threadIdx.x >> 5]);
   const int lane = threadIdx.x & 31, sub = lane & 3;
   const int jb = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int h = blockIdx.y, b = blockIdx.z;
+  const int h0 = blockIdx.y * a.heads, h1 = min(h0 + a.heads, a.Hkv), b = blockIdx.z;
   pdl_wait();
   pdl_trigger();
   const int most = a.nb_max * a.blk, len0 = a.seq_ctx[b], from0 = a.from_len ? a.from_len[b] : 0;
   const int len = min(max(len0, 0), most), from = min(max(from0, 0), most);
-  if (threadIdx.x == 0 && h == 0 && blockIdx.x == 0 && a.status && (len != len0 || from != from0))
+  if (threadIdx.x == 0 && h0 == 0 && blockIdx.x == 0 && a.status && (len != len0 || from != from0))
     atomicOr(a.status, SV_FLAG_BAD_LENGTH);
-  const int j = from / a.blk + jb;
-  if (jb >= a.max_blocks || j >= len / a.blk) return;
+  const int j = (a.blk_shift >= 0 ? from >> a.blk_shift : quotient(from, a.blk)) + jb;
+  if (jb >= a.max_blocks || j >= (a.blk_shift >= 0 ? len >> a.blk_shift : quotient(len, a.blk))) return;
   const int page = a.block_table[(long long)b * a.nb_max + j];
   if (page < 0 || page >= a.num_pages) {
     if (lane == 0 && a.status) atomicOr(a.status, SV_FLAG_BAD_PAGE);
     return;
   }
-  const int groups = a.d / kGroup, pb = piece_bytes(a.d), pieces = a.blk / kPiece;
-  const uint8_t* p = a.k_pool + ((long long)page * a.Hkv + h) * pieces * pb;
-  const float unit = __fdiv_rn(exp2i(head_exp(a.k_exp, h)), (float)a.blk);
+  const int groups = DG ? DG : a.d / kGroup, pb = piece_bytes(groups * kGroup), pieces = a.blk / kPiece;
+  const int chunk = DG ? kSlot / piece_bytes(DG * kGroup) : quotient(kSlot, pb);  // pieces
+  const uint8_t* p = a.k_pool + ((long long)page * a.Hkv + h0) * pieces * pb + lane * 16;
+  float* to = a.reps + (((long long)b * a.Hkv + h0) * a.nb_max + j) * (groups * kGroup) + sub * 4;
+  const float inv = __fdiv_rn(1.f, (float)a.blk);
   // B: rows 2 sub and 2 sub + 1 of column lane / 4, and the same 8 rows below
   const uint32_t identity = (lane >> 2 == 2 * sub ? 0x3c00u : 0u) | (lane >> 2 == 2 * sub + 1 ? 0x3c000000u : 0u);
-  float* to = a.reps + (((long long)b * a.Hkv + h) * a.nb_max + j) * a.d;
 #pragma unroll 1
-  for (int g0 = 0; g0 < groups; g0 += 8) {
-    const int g = g0 + (lane >> 2);
-    const bool on = g < groups;
-    float sum[4][4] = {};  // dims 4 i .. 4 i + 3
-    const uint8_t *codes = p + g * 128 + sub * 32, *scales = p + 8 * a.d + sub * 4 * groups + g;
+  for (int h = h0; h < h1; ++h, p += pieces * pb, to += (long long)a.nb_max * (groups * kGroup)) {
+    const int e = head_exp(a.k_exp, h);
 #pragma unroll 1
-    for (int t = 0; t < pieces; ++t, codes += pb, scales += pb) {
-      uint4 c[2] = {};
-      uint32_t sc = 0, s[2];
-      if (on) {
-        c[0] = __ldcg(reinterpret_cast<const uint4*>(codes));
-        c[1] = __ldcg(reinterpret_cast<const uint4*>(codes) + 1);
-        sc = __ldcg(scales) | __ldcg(scales + groups) << 8 | __ldcg(scales + 2 * groups) << 16 |
-             (uint32_t)__ldcg(scales + 3 * groups) << 24;
+    for (int g0 = 0; g0 < groups; g0 += 8) {
+      const int g = DG ? lane >> 2 : min(g0 + (lane >> 2), groups - 1);  // (behind the last: not stored)
+      float sum[4][4] = {};  // dims 4 i .. 4 i + 3
+#pragma unroll 1
+      for (int t0 = 0; t0 < pieces; t0 += chunk) {
+        const int n = min(chunk, pieces - t0);
+        if (pieces > chunk || g0 == 0) {
+          __syncwarp();
+          const uint8_t* src = p + (long long)t0 * pb;
+          const int bytes = n * pb;
+          for (int i = lane * 16; i < bytes; i += 512, src += 512)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + i), "l"(src) : "memory");
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          __syncwarp();
+        }
+        // (groups with odd numbers take their tokens the other way round: 8 lanes' loads fall
+        // into different banks)
+        const uint32_t odd = (uint32_t)g & 1u;
+        uint32_t c0 = slot + g * 128 + sub * 32 + odd * 16, c1 = c0 + 16 - odd * 32;
+        uint32_t s0 = slot + groups * 128 + sub * 4 * groups + g + odd * 2 * groups, s1 = s0 + 2 * groups - odd * 4 * groups;
+#pragma unroll 1
+        for (int t = 0; t < n; ++t, c0 += pb, c1 += pb, s0 += pb, s1 += pb) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {  // two tokens
+            const uint4 c = lds128(k ? c1 : c0);
+            uint32_t f[2][8], s, unused;
+            e4m3x4_to_f16(lds8(k ? s1 : s0) | lds8((k ? s1 : s0) + groups) << 8, s, unused);
+            e2m1x8_to_f16(c.x, f[0]);
+            e2m1x8_to_f16(c.y, f[0] + 4);
+            e2m1x8_to_f16(c.z, f[1]);
+            e2m1x8_to_f16(c.w, f[1] + 4);
+            scale_f16x2<0>(f[0], s);
+            scale_f16x2<1>(f[1], s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              asm volatile(
+                  "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%8}, {%0,%1,%2,%3};"
+                  : "+f"(sum[i][0]), "+f"(sum[i][1]), "+f"(sum[i][2]), "+f"(sum[i][3])
+                  : "r"(f[0][2 * i]), "r"(f[0][2 * i + 1]), "r"(f[1][2 * i]), "r"(f[1][2 * i + 1]), "r"(identity));
+          }
+        }
       }
-      e4m3x4_to_f16(sc, s[0], s[1]);
+      // fold: the lane keeps 4 of the 16 sums of its group
+      float x[8], y[4];
+      const bool up2 = sub & 2, up1 = sub & 1;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {  // tokens 2 k, 2 k + 1
-        uint32_t f[2][8];
-        e2m1x8_to_f16(c[k].x, f[0]);
-        e2m1x8_to_f16(c[k].y, f[0] + 4);
-        e2m1x8_to_f16(c[k].z, f[1]);
-        e2m1x8_to_f16(c[k].w, f[1] + 4);
-        scale_f16x2<0>(f[0], s[k]);
-        scale_f16x2<1>(f[1], s[k]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          asm volatile(
-              "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%8}, {%0,%1,%2,%3};"
-              : "+f"(sum[i][0]), "+f"(sum[i][1]), "+f"(sum[i][2]), "+f"(sum[i][3])
-              : "r"(f[0][2 * i]), "r"(f[0][2 * i + 1]), "r"(f[1][2 * i]), "r"(f[1][2 * i + 1]), "r"(identity));
+      for (int i = 0; i < 8; ++i) {
+        const float lo = sum[i / 4][i % 4], hi = sum[2 + i / 4][i % 4];
+        x[i] = (up2 ? hi : lo) + __shfl_xor_sync(0xffffffffu, up2 ? lo : hi, 2);
       }
+      const float unit = inv * exp2i(e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        y[i] = ((up1 ? x[4 + i] : x[i]) + __shfl_xor_sync(0xffffffffu, up1 ? x[i] : x[4 + i], 1)) * unit;
+      if (DG || g0 + (lane >> 2) < groups) *reinterpret_cast<float4*>(to + g * kGroup) = make_float4(y[0], y[1], y[2], y[3]);
     }
-    // fold: the lane keeps 4 of the 16 sums of its group
-    float x[16], y[4];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = sum[i / 4][i % 4];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      x[i] += __shfl_xor_sync(0xffffffffu, x[i], 1);
-      x[i] += __shfl_xor_sync(0xffffffffu, x[i], 2);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      y[i] = (sub == 0 ? x[i] : sub == 1 ? x[4 + i] : sub == 2 ? x[8 + i] : x[12 + i]) * unit;
-    if (on) *reinterpret_cast<float4*>(to + g * kGroup + sub * 4) = make_float4(y[0], y[1], y[2], y[3]);
   }
 }
 
@@ -313,9 +334,16 @@ cudaError_t launch_read_kv4(Rows4Args a, int dtype, cudaStream_t st) {
                           : launch_rows(a, st, read_kv4_kernel<float, 1>, read_kv4_kernel<float, kPairs>);
 }
 
-cudaError_t launch_reps_kv4(const Reps4Args& a, cudaStream_t st) {
-  const dim3 grid((unsigned)((a.max_blocks + kThreads / 32 - 1) / (kThreads / 32)), (unsigned)a.Hkv, (unsigned)a.B);
-  return launch_pdl(reps_kv4_kernel, grid, dim3(kThreads), 0, st, a);
+cudaError_t launch_reps_kv4(Reps4Args a, cudaStream_t st) {
+  const unsigned x = (unsigned)((a.max_blocks + kThreads / 32 - 1) / (kThreads / 32));
+  a.blk_shift = a.blk & (a.blk - 1) ? -1 : __builtin_ctz(a.blk);
+  // a block's heads one after the other (what is worked out for the block counts once), in as
+  // many CTAs as the GPU takes
+  int y = 1;
+  while (y < a.Hkv && (long long)x * y * a.B < 8 * 152) y *= 2;
+  a.heads = (a.Hkv + y - 1) / y;
+  const dim3 grid(x, (unsigned)((a.Hkv + a.heads - 1) / a.heads), (unsigned)a.B);
+  return launch_pdl(a.d == 128 ? reps_kv4_kernel<8> : reps_kv4_kernel<0>, grid, dim3(kThreads), 0, st, a);
 }
 
 }  // namespace sva

@@ -126,21 +126,11 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
   return r;
 }
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t r;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
-  return r;
-}
 // Bytes at .. at + 3 of a row whose last index is `last`.
 __device__ __forceinline__ uint32_t lds8x4(uint32_t row, int at, int last) {
   uint32_t r = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) r |= lds8(row + min(at + j, last)) << (8 * j);
-  return r;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 r;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
   return r;
 }
 __device__ __forceinline__ uint32_t first_bytes(int n) {  // a mask of the first n bytes of a word
