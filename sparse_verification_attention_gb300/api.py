@@ -403,7 +403,7 @@ def _call(fn, tensors, stream, *args):
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -433,6 +433,21 @@ def _rows(name: str, t: torch.Tensor, dtype: torch.dtype, heads: int, d: int) ->
             (shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != d))):
         raise ValueError(f"{name} must be rows [n, {heads}, {d}] of dtype {dtype}, each row dense")
     return stride[0] if shape[0] > 1 else heads * d
+
+
+def _row_array(name: str, t: torch.Tensor, dtype: torch.dtype, heads: int, d: int):
+    """The number of t's rows [n, heads, d], their address and distance (see _rows)."""
+    shape, stride = t.shape, t.stride()
+    n = shape[0] if shape else 0
+    if t.dtype != dtype or shape != (n, heads, d) or (n and (stride[2] != 1 or (heads > 1 and stride[1] != d))):
+        raise ValueError(f"{name} must be rows [n, {heads}, {d}] of dtype {dtype}, each row dense")
+    return n, t.data_ptr(), stride[0] if n > 1 else heads * d
+
+
+def _same_device(dev: int, tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("the tensors of a call must lie on one CUDA device")
 
 
 def _workspace(ws: Optional[torch.Tensor]):
@@ -577,28 +592,34 @@ def make_rope(table: Optional[torch.Tensor] = None, rot: Optional[int] = None, i
     return r
 
 
-def _check_rope(rope: Rope, dtype: torch.dtype, d: int):
-    """The tensors of a rope descriptor, the weights checked against the call's heads."""
+def _check_rope(rope: Rope, dtype: torch.dtype, d: int, dev: int):
+    """The tensors of a rope descriptor against a call's heads and device; the descriptor
+    remembers what it was last checked against."""
+    fits = dtype, d, dev
+    if getattr(rope, "_fits", None) == fits:
+        return
     kept = getattr(rope, "_tensors", ())  # none in a descriptor filled by hand
     for w in kept[1:]:
         if w is not None and (w.dtype != dtype or w.shape != (d,) or not w.is_contiguous()):
             raise ValueError(f"norm weights must be contiguous, of dtype {dtype} and of shape [{d}]")
-    return kept
+    _same_device(dev, kept)
+    rope._fits = fits
 
 
 def sv_norm_rope(shape: Shape, rope: Rope, positions, q, k, q_out, k_out, ws=None, stream=None):
     """Norm and rotate the heads of the rows q [n, Hq, d] (or None) and k [n, Hkv,
     d]; rows may be strided, q_out may be q and k_out k. positions: int32 [n],
     -1 leaves a row out (None when nothing is rotated)."""
-    d, dtype = shape.d, _DTYPES[shape.dtype]
-    n = k.shape[0]
-    ks, kos = _rows("k", k, dtype, shape.Hkv, d), _rows("k_out", k_out, dtype, shape.Hkv, d)
-    if k_out.shape[0] != n:
-        raise ValueError(f"{n} key rows and {k_out.shape[0]} rows to write")
+    H, d, dtype = shape.Hkv, shape.d, _DTYPES[shape.dtype]
+    n, kp, ks = _row_array("k", k, dtype, H, d)
+    no, kop, kos = _row_array("k_out", k_out, dtype, H, d)
+    if no != n:
+        raise ValueError(f"{n} key rows and {no} rows to write")
     qp, qs, qop, qos = _q_rows(shape, dtype, n, q, q_out)
-    _call(lib().sv_norm_rope, (k, q, q_out, k_out, positions, ws, *_check_rope(rope, dtype, d)), stream,
+    _check_rope(rope, dtype, d, k.get_device())
+    _call(lib().sv_norm_rope, (k, q, q_out, k_out, positions, ws), stream,
           C.byref(shape), C.byref(rope), None if positions is None else _ints("positions", positions, n),
-          n, qp, qs, k.data_ptr(), ks, qop, qos, k_out.data_ptr(), kos, _workspace(ws)[0])
+          n, qp, qs, kp, ks, qop, qos, kop, kos, _workspace(ws)[0])
 
 
 def _q_rows(shape: Shape, dtype: torch.dtype, n: int, q, q_out):
@@ -607,10 +628,11 @@ def _q_rows(shape: Shape, dtype: torch.dtype, n: int, q, q_out):
         raise ValueError("q and q_out are given together")
     if q is None:
         return None, 0, None, 0
-    qs, qos = _rows("q", q, dtype, shape.Hq, shape.d), _rows("q_out", q_out, dtype, shape.Hq, shape.d)
-    if q.shape[0] != n or q_out.shape[0] != n:
-        raise ValueError(f"{n} key rows, {q.shape[0]} query rows and {q_out.shape[0]} rows to write")
-    return q.data_ptr(), qs, q_out.data_ptr(), qos
+    nq, qp, qs = _row_array("q", q, dtype, shape.Hq, shape.d)
+    no, qop, qos = _row_array("q_out", q_out, dtype, shape.Hq, shape.d)
+    if nq != n or no != n:
+        raise ValueError(f"{n} key rows, {nq} query rows and {no} rows to write")
+    return qp, qs, qop, qos
 
 
 def sv_rope_write_kv(shape: Shape, rope: Rope, positions, q, k, v, q_out, slot_map, k_pool, v_pool, ws=None,
@@ -618,16 +640,17 @@ def sv_rope_write_kv(shape: Shape, rope: Rope, positions, q, k, v, q_out, slot_m
     """sv_norm_rope with the keys, and the values v [n, Hkv, d] beside them, stored
     at their slots of the paged cache; q and q_out may be None."""
     H, d, dtype = shape.Hkv, shape.d, _DTYPES[shape.dtype]
-    n, pages = k.shape[0], k_pool.shape[0]
-    ks, vs = _rows("k", k, dtype, H, d), _rows("v", v, dtype, H, d)
-    if v.shape[0] != n:
-        raise ValueError(f"{n} key rows and {v.shape[0]} value rows")
+    pages = k_pool.shape[0]
+    n, kp, ks = _row_array("k", k, dtype, H, d)
+    nv, vp, vs = _row_array("v", v, dtype, H, d)
+    if nv != n:
+        raise ValueError(f"{n} key rows and {nv} value rows")
     qp, qs, qop, qos = _q_rows(shape, dtype, n, q, q_out)
     pool = (pages, H, shape.blk, d)
-    _call(lib().sv_rope_write_kv,
-          (k, v, q, q_out, positions, slot_map, k_pool, v_pool, ws, *_check_rope(rope, dtype, d)), stream,
+    _check_rope(rope, dtype, d, k.get_device())
+    _call(lib().sv_rope_write_kv, (k, v, q, q_out, positions, slot_map, k_pool, v_pool, ws), stream,
           C.byref(shape), C.byref(rope), None if positions is None else _ints("positions", positions, n),
-          n, qp, qs, qop, qos, k.data_ptr(), ks, v.data_ptr(), vs, _ints("slot_map", slot_map, n),
+          n, qp, qs, qop, qos, kp, ks, vp, vs, _ints("slot_map", slot_map, n),
           _dense("k_pool", k_pool, dtype, *pool), _dense("v_pool", v_pool, dtype, *pool), pages,
           _workspace(ws)[0])
 
@@ -651,12 +674,15 @@ def make_kv4(k_pool: torch.Tensor, v_pool: torch.Tensor, block_table: Optional[t
     return kv
 
 
-def _check_kv4(shape: Shape, kv: KV4, seqs: bool):
-    """A descriptor's tensors, which must be a 4-bit cache of this shape (and hold
-    shape.B sequences)."""
+def _check_kv4(shape: Shape, kv: KV4, seqs: bool, dev: int):
+    """A descriptor's tensors, which must be a 4-bit cache of this shape on the call's
+    device (and hold shape.B sequences); it remembers what it was last checked against."""
+    fits = shape.Hkv, shape.blk, shape.d, shape.B if seqs else None, dev
+    if getattr(kv, "_fits", None) == fits:
+        return
     kept = getattr(kv, "_tensors", ())  # none in a descriptor filled by hand
     if not kept:
-        return kept
+        return
     k_pool, v_pool, table, seq_ctx, k_exp, v_exp = kept
     pool = (k_pool.shape[0], shape.Hkv, shape.blk // 16, 9 * shape.d)
     for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
@@ -670,31 +696,34 @@ def _check_kv4(shape: Shape, kv: KV4, seqs: bool):
             raise ValueError("kv needs a block_table and seq_ctx for this call")
         _ints("the block_table of kv", table, shape.B, table.shape[-1])
         _ints("the seq_ctx of kv", seq_ctx, shape.B)
-    return kept
+    _same_device(dev, kept)
+    kv._fits = fits
 
 
 def sv_write_kv4(shape: Shape, k, v, slot_map, kv: KV4, ws=None, stream=None):
     """Store the rows k, v [n, Hkv, d] (slices of a fused projection are fine) in 4
     bits at their slots; slots of -1 are skipped."""
     H, d, dtype = shape.Hkv, shape.d, _DTYPES[shape.dtype]
-    ks, vs, n = _rows("k", k, dtype, H, d), _rows("v", v, dtype, H, d), k.shape[0]
-    if v.shape[0] != n:
-        raise ValueError(f"{n} key rows and {v.shape[0]} value rows")
-    _call(lib().sv_write_kv4, (k, v, slot_map, ws, *_check_kv4(shape, kv, False)), stream, C.byref(shape),
-          k.data_ptr(), ks, v.data_ptr(), vs, _ints("slot_map", slot_map, n), n, C.byref(kv),
-          _workspace(ws)[0])
+    n, kp, ks = _row_array("k", k, dtype, H, d)
+    nv, vp, vs = _row_array("v", v, dtype, H, d)
+    if nv != n:
+        raise ValueError(f"{n} key rows and {nv} value rows")
+    _check_kv4(shape, kv, False, k.get_device())
+    _call(lib().sv_write_kv4, (k, v, slot_map, ws), stream, C.byref(shape), kp, ks, vp, vs,
+          _ints("slot_map", slot_map, n), n, C.byref(kv), _workspace(ws)[0])
 
 
 def sv_read_kv4(shape: Shape, kv: KV4, slot_map, k_out, v_out, ws=None, stream=None):
     """The rows k_out, v_out [n, Hkv, d] of the values at the slots of a 4-bit cache;
     rows of slots -1 stay as they are."""
     H, d, dtype = shape.Hkv, shape.d, _DTYPES[shape.dtype]
-    ks, vs, n = _rows("k_out", k_out, dtype, H, d), _rows("v_out", v_out, dtype, H, d), k_out.shape[0]
-    if v_out.shape[0] != n:
-        raise ValueError(f"{n} key rows and {v_out.shape[0]} value rows")
-    _call(lib().sv_read_kv4, (k_out, v_out, slot_map, ws, *_check_kv4(shape, kv, False)), stream,
-          C.byref(shape), C.byref(kv), _ints("slot_map", slot_map, n), n, k_out.data_ptr(), ks,
-          v_out.data_ptr(), vs, _workspace(ws)[0])
+    n, kp, ks = _row_array("k_out", k_out, dtype, H, d)
+    nv, vp, vs = _row_array("v_out", v_out, dtype, H, d)
+    if nv != n:
+        raise ValueError(f"{n} key rows and {nv} value rows")
+    _check_kv4(shape, kv, False, k_out.get_device())
+    _call(lib().sv_read_kv4, (k_out, v_out, slot_map, ws), stream, C.byref(shape), C.byref(kv),
+          _ints("slot_map", slot_map, n), n, kp, ks, vp, vs, _workspace(ws)[0])
 
 
 def sv_build_reps_kv4(shape: Shape, kv: KV4, max_blocks: int, reps, from_len=None, ws=None, stream=None):
@@ -702,7 +731,8 @@ def sv_build_reps_kv4(shape: Shape, kv: KV4, max_blocks: int, reps, from_len=Non
     tokens (int32 [B], None: since the beginning), at most max_blocks each. reps:
     float32 [B, Hkv, nb_max, d]."""
     B = shape.B
-    _call(lib().sv_build_reps_kv4, (reps, from_len, ws, *_check_kv4(shape, kv, True)), stream,
+    _check_kv4(shape, kv, True, reps.get_device())
+    _call(lib().sv_build_reps_kv4, (reps, from_len, ws), stream,
           C.byref(shape), C.byref(kv), None if from_len is None else _ints("from_len", from_len, B),
           max_blocks, _dense("reps", reps, torch.float32, B, shape.Hkv, kv.nb_max, shape.d),
           _workspace(ws)[0])
@@ -725,10 +755,12 @@ def sv_attend_kv4(shape: Shape, q, kv: KV4, sel, draft_k, draft_v, parents, out,
     stride = 0 if sel is None else sel.shape[-1]
     # an empty selection has no address, and none would mean every block: any other does, as no entry is read
     sel_ptr = None if sel is None else _ints("sel", sel, B, H, stride) or kv.block_table
-    _call(lib().sv_attend_kv4, (q, sel, draft_k, draft_v, out, ws, *_check_kv4(shape, kv, True)), stream,
-          C.byref(shape), _dense("q", q, dtype, *rows), C.byref(kv),
-          sel_ptr, stride if n_sel is None else n_sel, stride, _dense("draft_k", draft_k, dtype, *drafts), _dense("draft_v", draft_v, dtype, *drafts),
-          _parents(parents), _dense("out", out, dtype, *rows), *_workspace(ws))
+    _check_kv4(shape, kv, True, q.get_device())
+    _call(lib().sv_attend_kv4, (q, sel, draft_k, draft_v, out, ws), stream,
+          C.byref(shape), _dense("q", q, dtype, *rows), C.byref(kv), sel_ptr,
+          stride if n_sel is None else n_sel, stride, _dense("draft_k", draft_k, dtype, *drafts),
+          _dense("draft_v", draft_v, dtype, *drafts), _parents(parents), _dense("out", out, dtype, *rows),
+          *_workspace(ws))
 
 
 VERIFY_COMPUTE, VERIFY_REUSE, VERIFY_FULL = 0, 1, 2  # sv_verify_layer's reuse values
