@@ -78,10 +78,10 @@ constexpr int kMaxPairCost = 8;      // of Attend4Args::pair_cost
 // tile of one (sequence, head). A pair's pieces (16 keys each) make key tiles of `ppt` pieces.
 // The pairs' key tiles are laid end to end, with what beginning a pair costs ahead of them, and
 // cut into equal shares, one per CTA; what a CTA has of a pair is a segment. (That cost left
-// out: 16 sequences of 1 to 32768 tokens, 8 heads each, 82 us; counted as 3 tiles 70, as 8
-// tiles 58: the CTAs whose share holds several short pairs were last.) Segment (pair p, CTA c)
-// leaves its rows' sums in slot p + c (p and c only grow along the line, so no two segments
-// share one), once for each of its `streams`.
+// out: 16 sequences of 1 to 32768 tokens, 8 heads each, 82 us, as the CTAs whose share held
+// several short pairs were last; counted as 2 tiles 64, as 4 to 8 tiles 58.) Segment (pair p,
+// CTA c) leaves its rows' sums in slot p + c (p and c only grow along the line, so no two
+// segments share one), once for each of its `streams`.
 struct Attend4Args {
   const void *q, *draft_k, *draft_v;
   void* out;

@@ -1,6 +1,9 @@
 // The drafts, and the join of a row's segments: what sv_attend_kv4 does behind the
 // attention over the cache. A row's own drafts stay in the call's type; there are at
 // most 64 of them, so fp32 on the CUDA cores costs little and needs no tile.
+// Bound by latency: a row's loads (q, drafts, slots, parts) come one after the other, so that
+// rows in flight are what counts (4096 rows of 16 drafts and 7 parts: 11.6 us in 64 registers,
+// 17 in 87).
 #include "kv4.cuh"
 
 namespace sva {

@@ -60,7 +60,9 @@ __device__ __forceinline__ void store16(T* p, bool wide, const float (&x)[16]) {
 // written in runs of 128 and the bytes of a V code row in runs of 16 when the tokens'
 // slots follow each other (nothing depends on it). Blocks: 16 tokens (x), four pairs of
 // groups of K and of V, or less (y), heads (z). Places are worked out once for all heads:
-// one head a lane, with its divisions, took 347 instructions a group.
+// one head a lane, with its divisions, took 347 instructions a group. 13,343 rows of 8 heads
+// of 128 in bf16: 18 us written and 14 read back, 4.4 TB/s; the grid's last wave and the start
+// are a fifth of it. (Two heads at a time need more registers: 34.4 us for both.)
 struct Place {
   int token, g, is_v, tok, h0, h1;
   long long step;  // from a head's piece to the next head's

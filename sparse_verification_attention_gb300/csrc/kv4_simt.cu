@@ -1,7 +1,11 @@
 // Attention over a 4-bit cache on the CUDA cores, for every type and shape: keys
 // and values are taken apart into 32-bit tiles in shared memory, all sums are fp32.
-// The reference for the tensor-core path, and the path of fp32 and of head dims
-// above 128.
+// The path of fp32 and of head dims above 128.
+//
+// A tile of 64 keys and 32 rows: a thread has 2 rows and 4 keys of the scores, 2 rows and
+// 4 dims (in every 64) of the outputs. Bound by shared memory (12 wavefronts a warp for 4 dims of
+// the scores) where contexts are long, by the latency of one round and its cold code where
+// they are short: 5 sequences of 0 to 1500 tokens, 4 heads of 64, 18 us a call.
 #include <algorithm>
 #include <atomic>
 

@@ -3,36 +3,42 @@
 //
 // Rows are few (T drafts x G heads of a KV head) and the cache is long, so the
 // products are taken transposed: S^T = K Q^T with the 128 keys of a tile as the
-// M rows and the rows as the N columns, O^T += V^T P^T with the head's dims as M.
-// The cost of a product then follows the rows (N = 16 .. 128), not a padded 128,
-// and K and V^T are the A operands, which tcgen05 takes from TMEM: a code goes
-// from the ring of pages through a thread's registers, where it becomes a half, into
-// TMEM, and never back into shared memory. That is why V's pages keep a dim's tokens
-// together: a TMEM lane of V^T is one dim.
+// M rows and up to 64 rows as the N columns, O^T += V^T P^T with the head's dims as M.
+// K goes from the ring of pages through a thread's registers, where codes become halves,
+// into TMEM and is the A operand from there; V goes into shared memory as halves, a key a
+// row. (V^T in TMEM as well: 190 us instead of 188 in the case below, as an MMA of 128 x N x 16
+// takes 65 cycles with A in TMEM, for any N up to 128, and 47 with A in shared memory, N up
+// to 64.)
 // Code times scale has at most five significant bits and is exact in f16. Q is
 // scaled by a power of two per row so that its largest element lies in [2^14, 2^15),
 // exact as well; factor and exponents go into the softmax's scale.
 //
-// Warpgroups: K and V (codes to halves), two of softmax, and one whose warps copy (take
-// the CTA's segments off the line, look pages up), issue the MMAs of the one and of the other
-// product, and lay out Q. (One warp for both products spent 1750 cycles a tile on its own
-// waits, issue and commits, 216 us; two: see below.)
-// What bounds the kernel besides HBM are chains, not rates: an MMA of 128 x N x 16 with A in
-// TMEM takes 65 cycles for any N up to 128 (measured; 47 with A in shared memory), so a tile's
-// 16 take 1040, and a tile's softmax from scores to weights as long again. Up to 64
-// rows the two softmax warpgroups therefore take even and odd tiles with references,
-// sums and O of their own (two streams, joined with the segments); above, they share
-// each tile's columns.
-// A softmax thread has one key and a run of rows (columns). It does not look for
+// Twenty warps: four for K and four for V (codes to halves), eight of softmax, and four that
+// copy K, copy V and lay out Q of later segments, issue the MMAs of the scores, issue those of
+// the outputs. Even and odd tiles are two streams with a softmax warpgroup, references, sums
+// and an O of their own, joined with the segments: a tile's chain from scores to weights is
+// as long as its products.
+// A softmax thread has 4 keys and every fourth pair of columns. It does not look for
 // a tile's maxima: a row's reference stands until some key's weights, summed over the
-// thread's rows, reach 2^15, which the warps tell each other at the tile's barrier; only
+// thread's rows, reach 2^15, which the warps tell each other by a vote; only
 // then (and in a segment's first tile) maxima are taken across lanes and O is rescaled.
 // Weights are held 2^7 times their size, so that f16's range covers 2^-31 .. 2^8 of the
 // reference.
 //
-// Everything that runs once per segment is a rolled loop: five roles share an SM
-// quarter's instruction cache, and cold code costs more than what it does. With the
-// loops unrolled and every wait's clock inline, 128 K tokens x 4 took 497 us, rolled 247.
+// What bounds it. Four sequences of 131072 tokens, 8 heads of 128, 32 rows: 156 us, 3.9 TB/s
+// of pages, 0.57 of the copy rate. A tile of 128 keys takes about 1400 cycles, of which the MMA
+// pipe needs 900 (8 x 65 + 8 x 47), shared memory about 900 (bytes in, V as halves in
+// and out, P) and the issue slots about 900. (When it was 161 us: without the products 145,
+// without the conversions 129, without softmax 147, without any of them 108.) More
+// warps for K and V gained nothing (768 threads 166 us, 896 171: fewer registers each). Two MMA
+// warps instead of one: 197 instead of 216; softmax with a key a thread and factors in shared
+// memory: 188; pages past L2's reach evict-first 164, before 170.
+// Short calls: everything that runs once is fetched from a cold instruction cache at 12 to 30
+// cycles an instruction, so it is rolled, short and split among the warps. Eight
+// sequences of 64 selected blocks, trees of 16, 128 rows a head: 35 us, of which a CTA spends
+// 10 until its first scores (lengths, pages and first copies one after the other), 2 a tile and 2 at a
+// segment's end; 63 when one warp laid out Q, all threads tracked all references, and the
+// weights of a tile waited in registers that spilled.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>

@@ -586,6 +586,74 @@ def test_serving_loop(sparse):
     assert api.sv_read_status(status) == 0
 
 
+def test_captured_step():
+    """Pages, rotation, rows, representatives and attention of a step in one graph, which
+    follows the lengths and padding in device memory; the same calls one at a time, each
+    waited for, give the same bits."""
+    B, Hq, Hkv, d, blk, nb_max, pages, rows = 3, 16, 4, 128, 32, 12, 40, 8
+    g = gen(31)
+    s = api.make_shape(B, Hq, Hkv, d, blk, 1, BF16)
+    rope = api.make_rope(api.rope_table(512, d), q_weight=torch.ones(d, dtype=BF16, device="cuda"))
+    free = torch.randperm(pages, generator=g).to(torch.int32).cuda()
+
+    class Side:
+        def __init__(self):
+            self.pools = [api.alloc_kv4_pool(s, pages) for _ in range(2)]
+            self.table = torch.full((B, nb_max), -1, dtype=torch.int32, device="cuda")
+            self.lens, self.new = i32([0] * B), i32([0] * B)
+            self.free, self.count = free.clone(), i32([pages])
+            self.reps = torch.zeros(B, Hkv, nb_max, d, device="cuda")
+            self.kv = api.make_kv4(*self.pools, self.table, self.lens)
+            self.cu, self.slots, self.pos = i32([0] * (B + 1)), i32([-1] * rows), i32([-1] * rows)
+            self.qkv = torch.zeros(rows, Hq + 2 * Hkv, d, dtype=BF16, device="cuda")
+            self.q, self.k, self.v = self.qkv.split([Hq, Hkv, Hkv], 1)
+            self.out = torch.zeros(B, 1, Hq, d, dtype=BF16, device="cuda")
+            self.ws, self.status = api.alloc_kv4_workspace(s), status_ws()
+
+        def step(self, wait):
+            old = self.lens.clone()
+            for call in (
+                    lambda: api.sv_build_tables(blk, self.lens, self.new, self.table, self.free, self.count,
+                                                self.count, self.cu, self.slots, self.pos, ws=self.status),
+                    lambda: api.sv_norm_rope(s, rope, self.pos, self.q, self.k, self.q, self.k, self.status),
+                    # every sequence's last row attends to what is there before the rows enter
+                    lambda: api.sv_attend_kv4(s, self.q[:B, None].contiguous(), self.kv, None,
+                                              self.k[:B, None].contiguous(), self.v[:B, None].contiguous(), None,
+                                              self.out, self.ws),
+                    lambda: api.sv_write_kv4(s, self.k, self.v, self.slots, self.kv, self.status),
+                    lambda: self.lens.copy_(self.new),
+                    lambda: api.sv_build_reps_kv4(s, self.kv, nb_max, self.reps, old, self.status)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+
+    graph, eager = Side(), Side()
+    stream = torch.cuda.Stream()
+    captured = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream):
+        graph.step(False)  # (nothing grows: lengths of 0)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(captured):
+        graph.step(False)
+    now = [0] * B
+    for grow in ([3, 2, 0], [1, 1, 1], [0, 7, 1], [1, 0, 0], [0, 0, 8]):
+        x = torch.randn(rows, Hq + 2 * Hkv, d, generator=g).to(BF16)
+        now = [a + b for a, b in zip(now, grow)]
+        for side in (graph, eager):
+            side.qkv.copy_(x)
+            side.new.copy_(i32(now))
+            side.slots.fill_(-1)
+            side.pos.fill_(-1)
+        torch.cuda.synchronize()
+        captured.replay()
+        eager.step(True)
+        torch.cuda.synchronize()
+        for name in ("qkv", "out", "lens", "reps", "table"):
+            assert torch.equal(getattr(graph, name), getattr(eager, name)), name
+        assert all(torch.equal(x, y) for x, y in zip(graph.pools, eager.pools))
+        assert api.sv_read_status(graph.status) == 0 and api.sv_read_status(graph.ws) == 0
+
+
 def test_prompt_over_a_copy_of_the_cache():
     """A chunk of a prompt over a sequence in 4 bits: its rows read back into a paged bf16
     cache, the chunk's keys rotated into it, attention there."""
