@@ -1,10 +1,10 @@
 // Attention over a 4-bit cache on the CUDA cores, for every type and shape: the path of
 // fp32 and of head dims above 128. All sums are fp32.
 //
-// Neither K nor V passes through shared memory. Scores: a lane has a key and 4 dims of every
-// group of 16 (so that four lanes read 64 neighbouring bytes of a row of Q, the same for the
-// 8 keys of a warp), and dots them with all rows. Outputs: a thread has two dims (a code row
-// of V, 16 tokens a load) of some rows, and reads weights that its warp has in common. Rows are
+// Neither K nor V passes through shared memory. Scores: a lane has a key and every fourth
+// group of dims, and dots them with all rows of Q, which it reads with its whole warp; the
+// four parts of a score meet in shared memory. Outputs: a thread has two dims (a code row of V, 16
+// tokens a load) of some rows, and reads weights that its warp has in common. Rows are
 // tiles of 4 to 32, the smallest that holds them.
 //
 // Bound by issue slots (a quarter of the scores' instructions are loads of Q, an eighth of the
@@ -22,7 +22,8 @@ using namespace kv4;
 constexpr int kThreads = 256;
 constexpr int kKeys = 64, kPieces = kKeys / kPiece;  // (ppt_shift)
 constexpr int kGroup = 16;
-static_assert(kThreads == 4 * kKeys, "four lanes a key");
+constexpr int kSlices = 4;  // warps that share a key's dims
+static_assert(kThreads == kSlices * kKeys, "a lane a key and slice");
 
 struct Control {
   Line line;
@@ -38,7 +39,7 @@ struct P {
 };
 template <int RT>
 size_t smem_bytes(int d) {
-  return sizeof(Control) + sizeof(float) * (RT * d + kKeys * P<RT>::kStride);
+  return sizeof(Control) + sizeof(float) * (RT * d + kSlices * kKeys * P<RT>::kStride);
 }
 
 // RT: rows of a tile at most. GR: groups of threads that share the tile's rows in the product
@@ -48,8 +49,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend4_simt_kernel(const __grid_
   constexpr int PS = P<RT>::kStride, RG = RT < GR ? 1 : RT / GR;
   extern __shared__ float4 smem4[];
   float* q = reinterpret_cast<float*>(smem4);  // [RT][d], times scale
-  float* p = q + RT * a.d;                     // [kKeys][PS]: scores, then weights
-  Control& sh = *reinterpret_cast<Control*>(p + kKeys * PS);
+  float* p = q + RT * a.d;                     // [kSlices][kKeys][PS]: parts of scores; weights in the first
+  Control& sh = *reinterpret_cast<Control*>(p + kSlices * kKeys * PS);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int groups = a.d / kGroup, pb = piece_bytes(a.d);
   unsigned flags = 0;
@@ -59,9 +60,9 @@ __global__ void __launch_bounds__(kThreads, 2) attend4_simt_kernel(const __grid_
   __syncthreads();
   const int pairs = a.B * a.Hkv * a.row_tiles, cta = blockIdx.x;
   for (int i = cta * kThreads + tid; i < pairs; i += gridDim.x * kThreads) a.slots[i] = slots_of(a, sh.line, i);
-  // scores: key and dims (4 slice .. + 3 of every group); softmax: row and keys part + 8 j; outputs:
-  // rows r0 .. and dims 16 vg + vc and 8 behind
-  const int key = warp * 8 + (lane >> 2), slice = lane & 3, row = tid >> 3, part = tid & 7;
+  // scores: key and every fourth group of dims; softmax: row and keys part + 8 j; outputs: rows
+  // r0 .. and dims 16 vg + vc and 8 behind
+  const int key = warp / kSlices * 32 + lane, slice = warp % kSlices, row = tid >> 3, part = tid & 7;
   const int vgrp = quotient(tid, a.d / 2), vx = tid - vgrp * (a.d / 2), vc = vx & 7, vg = vx >> 3, r0 = vgrp * RG;
   const bool has_v = vgrp < GR && r0 < RT, has_row = row < RT;
   const int end = sh.line.begin(cta + 1);
@@ -99,36 +100,35 @@ __global__ void __launch_bounds__(kThreads, 2) attend4_simt_kernel(const __grid_
 #pragma unroll
         for (int r = 0; r < RT; ++r) acc[r] = 0.f;
         const bool on = (key & 15) < valid[key >> 4];
-        const uint8_t* from = a.k_pool + (on ? piece[key >> 4] : 0) * pb + (key & 15) * 8 + slice * 2;
+        const uint8_t* from = a.k_pool + (on ? piece[key >> 4] : 0) * pb + (key & 15) * 8;
         const uint8_t* sc = a.k_pool + (on ? piece[key >> 4] : 0) * pb + 8 * a.d + (key & 15) * groups;
-        const float* qq = q + slice * 4;
-#pragma unroll 4
-        for (int g = 0; g < groups; ++g) {
-          uint32_t w = 0, e = 0;
+#pragma unroll 2
+        for (int g = slice; g < groups; g += kSlices) {
+          uint2 w = make_uint2(0, 0);
+          uint32_t e = 0;
           if (on) {
-            w = __ldcg(reinterpret_cast<const uint16_t*>(from + g * 128));
+            w = __ldcg(reinterpret_cast<const uint2*>(from + g * 128));
             e = __ldcg(sc + g);
           }
           const float f = e4m3_to_f32(e);
-          const float2 k01 = f16x2_to_f32(e2m1x2_to_f16x2(w & 0xffu)), k23 = f16x2_to_f32(e2m1x2_to_f16x2(w >> 8));
-          const float k0 = k01.x * f, k1 = k01.y * f, k2 = k23.x * f, k3 = k23.y * f;
+          const float* qq = q + g * kGroup;
+          uint32_t h[8];
+          e2m1x8_to_f16(w.x, h);
+          e2m1x8_to_f16(w.y, h + 4);
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const float4 y = *reinterpret_cast<const float4*>(qq + r * a.d + g * kGroup);
-            acc[r] = fmaf(y.x, k0, fmaf(y.y, k1, fmaf(y.z, k2, fmaf(y.w, k3, acc[r]))));
+          for (int c = 0; c < 4; ++c) {
+            const float2 k01 = f16x2_to_f32(h[2 * c]), k23 = f16x2_to_f32(h[2 * c + 1]);
+            const float k0 = k01.x * f, k1 = k01.y * f, k2 = k23.x * f, k3 = k23.y * f;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+              const float4 y = *reinterpret_cast<const float4*>(qq + r * a.d + 4 * c);
+              acc[r] = fmaf(y.x, k0, fmaf(y.y, k1, fmaf(y.z, k2, fmaf(y.w, k3, acc[r]))));
+            }
           }
         }
-        // over the key's four lanes; lane `slice` keeps the rows RT / 4 slice ..
+        float4* to = reinterpret_cast<float4*>(p + (slice * kKeys + key) * PS);
 #pragma unroll
-        for (int i = 0; i < RT / 2; ++i) {
-          const float give = slice & 2 ? acc[i] : acc[i + RT / 2], mine = slice & 2 ? acc[i + RT / 2] : acc[i];
-          acc[i] = mine + __shfl_xor_sync(0xffffffffu, give, 2);
-        }
-#pragma unroll
-        for (int i = 0; i < RT / 4; ++i) {
-          const float give = slice & 1 ? acc[i] : acc[i + RT / 4], mine = slice & 1 ? acc[i + RT / 4] : acc[i];
-          p[key * PS + slice * (RT / 4) + i] = mine + __shfl_xor_sync(0xffffffffu, give, 1);
-        }
+        for (int i = 0; i < RT; i += 4) to[i / 4] = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
       }
       // V's bytes are on their way while the weights are made
       uint4 w[kPieces], sv[kPieces];
@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend4_simt_kernel(const __grid_
 #pragma unroll
         for (int j = 0; j < kKeys / 8; ++j) {
           const int k = part + 8 * j;
-          y[j] = (k & 15) < valid[k >> 4] ? p[k * PS + row] : -INFINITY;
+          const float* x = p + k * PS + row;
+          y[j] = (k & 15) < valid[k >> 4] ? (x[0] + x[kKeys * PS]) + (x[2 * kKeys * PS] + x[3 * kKeys * PS]) : -INFINITY;
           mx = fmaxf(mx, y[j]);
         }
 #pragma unroll
