@@ -7,8 +7,13 @@
 // tokens a load) of some rows, and reads weights that its warp has in common. Rows are
 // tiles of 4 to 32, the smallest that holds them.
 //
-// Bound by issue slots (a quarter of the scores' instructions are loads of Q, an eighth of the
-// outputs' loads of weights), where contexts are short by the latency of one round.
+// Bound by issue slots (a fifth of the scores' instructions are loads of Q, an eighth of the
+// outputs' loads of weights): fp32, 16384 tokens, 32 rows of 8 heads of 128, 95 us, 23 TFLOP/s;
+// bf16 heads of 256, 2 x 131072 tokens, 8 tokens each, 517 us, one, 155. K a tile ahead in
+// registers gained nothing. Where contexts are short by the latency of one round: 5 sequences
+// of 0 to 1500 tokens, 8 rows of 4 heads of 64, 14 us.
+// (With K and V taken apart into 32-bit tiles in shared memory for both products: 123, 1264,
+// 1260 and 18 us.)
 #include <algorithm>
 #include <atomic>
 
@@ -102,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend4_simt_kernel(const __grid_
         const bool on = (key & 15) < valid[key >> 4];
         const uint8_t* from = a.k_pool + (on ? piece[key >> 4] : 0) * pb + (key & 15) * 8;
         const uint8_t* sc = a.k_pool + (on ? piece[key >> 4] : 0) * pb + 8 * a.d + (key & 15) * groups;
-#pragma unroll 2
+#pragma unroll(RT <= 8 ? 2 : 1)
         for (int g = slice; g < groups; g += kSlices) {
           uint2 w = make_uint2(0, 0);
           uint32_t e = 0;
