@@ -10,7 +10,7 @@
 namespace sva {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 32;  // a warp: its place is taken again as soon as its token is done
 
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
@@ -73,11 +73,12 @@ struct Chunk {
 // makes them once and keeps them in registers, r is the row's 1 / sqrt(mean + eps).
 //
 // Bound by HBM: every row is read and written once. 20,011 rows of 36 normed heads of 128 in
-// bf16: 73 us, 5.2 TB/s, 0.76 of the copy rate; 15,439 rows of 32 + 8 + 8 heads into the
-// cache: 67.7 us, 0.84.
+// bf16: 64.7 us, 5.9 TB/s, 0.86 of the copy rate; 15,439 rows of 32 + 8 + 8 heads into the
+// cache: 61.9 us, 0.92. (28 CTAs of a warp an SM; 24 66.1 and 64.3, 32, in fewer registers, 65.9 and
+// 64.8; CTAs of eight warps 74.5 and 68.4. Two or three rows in flight a lane: 84 and 80 us.)
 // FULL: every lane has two chunks and all of them turn.
 template <typename T, int V, bool INTER, bool FULL>
-__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeArgs a, int width) {
+__global__ void __launch_bounds__(kThreads, 28) rope_kernel(const __grid_constant__ RopeArgs a, int width) {
   constexpr int kFlight = 4;  // rows that a lane has in flight
   const int lane = threadIdx.x & 31, l = lane & (width - 1), seg = lane / width, segs = 32 / width;
   const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
         }
       }
       // 1 / sqrt of the rows' mean squares: the rows' exchanges side by side (one row after
-      // the other, with its rotation in between, took 78 us where this takes 73: 20,011 rows of 36 heads)
+      // the other, with its rotation in between, took 78 us where this took 73: 20,011 rows of 36 heads)
       float inv[kFlight];
       if (weight) {
 #pragma unroll
@@ -262,10 +263,10 @@ cudaError_t launch(RopeArgs a, cudaStream_t st) {
   const long long warps = (long long)a.n << a.parts_shift;
   const bool full = a.rot == a.d && a.d == 2 * V * width;
   const unsigned blocks = (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
-  // Few blocks take a side each: one side's rows after the other's wait for memory three
-  // times (23 tokens of 16 heads: 2.9 us a call, 5.0 in one block; 32 of 40, without values:
-  // 2.1 and 2.5).
-  const dim3 grid(blocks, blocks < 2 * 152 ? 3 : 1);
+  // Few warps take a side each: one side's rows after the other's wait for memory three
+  // times (23 tokens of 16 heads: 2.9 us a call, 5.0 with the sides in turn; 32 of 40, without
+  // values: 2.1 and 2.5).
+  const dim3 grid(blocks, warps < 16 * 152 ? 3 : 1);
   return launch_pdl(full ? rope_kernel<T, V, INTER, true> : rope_kernel<T, V, INTER, false>, grid, dim3(kThreads), 0, st, a,
                     width);
 }
