@@ -7,7 +7,8 @@ namespace {
 
 using namespace kv4;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of the representatives
+constexpr int kRowThreads = 64;
 constexpr int kGroup = 16;  // dims that share a scale
 
 // 16 elements of bf16 or fp32, in 32-byte accesses where the rows allow it (`wide`): in two
@@ -58,27 +59,22 @@ __device__ __forceinline__ void store16(T* p, bool wide, const float (&x)[16]) {
 // A lane has one group of one token, in `heads` heads one after the other; a warp 16
 // tokens and two neighbouring groups, so that rows are read in runs of 64 bytes, K codes
 // written in runs of 128 and the bytes of a V code row in runs of 16 when the tokens'
-// slots follow each other (nothing depends on it). Blocks: 16 tokens (x), four pairs of
-// groups of K and of V, or less (y), heads (z). Places are worked out once for all heads:
+// slots follow each other (nothing depends on it). Blocks: 16 tokens (x), a pair of groups
+// of K in one warp and of V in the other (y), heads (z). Places are worked out once for all heads:
 // one head a lane, with its divisions, took 347 instructions a group. 13,343 rows of 8 heads
-// of 128 in bf16: 18 us written and 14 read back, 4.4 TB/s; the grid's last wave and the start
-// are a fifth of it. (Two heads at a time need more registers: 34.4 us for both.)
+// of 128 in bf16: 18 us written and 13 read back, 4.5 TB/s. (All heads and four pairs of groups in a
+// block, whose last wave is a fifth: 31.7 us for both; two heads at a time, in more registers, 34.4.)
 struct Place {
   int token, g, is_v, tok, h0, h1;
   long long step;  // from a head's piece to the next head's
   uint8_t* piece;  // of head h0; null: nothing to do
 };
-// PAIRS: pairs of groups of one side in a block, a constant (as a run-time number it cost 34.2 us
-// instead of 31.6).
-constexpr int kPairs = 4;
-template <int PAIRS>
 __device__ __forceinline__ Place place_of(const Rows4Args& a) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int groups = a.d / kGroup;
+  const int lane = threadIdx.x & 31, groups = a.d / kGroup;
   Place p;
   p.token = blockIdx.x * 16 + (lane >> 1);
-  p.is_v = warp >= PAIRS;
-  p.g = (blockIdx.y * PAIRS + warp % PAIRS) * 2 + (lane & 1);
+  p.is_v = threadIdx.x >= 32;
+  p.g = blockIdx.y * 2 + (lane & 1);
   p.h0 = blockIdx.z * a.heads;
   p.h1 = min(p.h0 + a.heads, a.Hkv);
   p.piece = nullptr;
@@ -148,9 +144,9 @@ __device__ __forceinline__ void write_groups(const Rows4Args& a, const Place& p)
     *scale = (uint8_t)sb;
   }
 }
-template <typename T, int PAIRS>
-__global__ void __launch_bounds__(64 * PAIRS) write_kv4_kernel(const __grid_constant__ Rows4Args a) {
-  const Place p = place_of<PAIRS>(a);
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) write_kv4_kernel(const __grid_constant__ Rows4Args a) {
+  const Place p = place_of(a);
   if (!p.piece) return;
   if (p.is_v) write_groups<T, true>(a, p);
   else write_groups<T, false>(a, p);
@@ -189,9 +185,9 @@ __device__ __forceinline__ void read_groups(const Rows4Args& a, const Place& p) 
     store16(to, a.wide, x);
   }
 }
-template <typename T, int PAIRS>
-__global__ void __launch_bounds__(64 * PAIRS) read_kv4_kernel(const __grid_constant__ Rows4Args a) {
-  const Place p = place_of<PAIRS>(a);
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) read_kv4_kernel(const __grid_constant__ Rows4Args a) {
+  const Place p = place_of(a);
   if (!p.piece) return;
   if (p.is_v) read_groups<T, true>(a, p);
   else read_groups<T, false>(a, p);
@@ -306,17 +302,17 @@ bool wide_rows(const void* p, long long stride, int elt) {
   return reinterpret_cast<uintptr_t>(p) % 32 == 0 && stride * elt % 32 == 0;
 }
 
-// Many tokens: all heads in one block; few: heads and pairs of groups in as many blocks as
-// the GPU takes (64 tokens of 8 heads written and read: 4.0 us; all pairs in one block, 5.2).
-template <typename F1, typename F4>
-cudaError_t launch_rows(Rows4Args a, cudaStream_t st, F1 few, F4 many) {
-  const unsigned x = (unsigned)((a.n + 15ll) / 16), all = (unsigned)(a.d / kGroup + 1) / 2;
-  const unsigned pairs = (long long)x * all * a.Hkv < 8 * 152 ? 1 : kPairs, y = (all + pairs - 1) / pairs;
+// Heads in as many blocks as keep the GPU busy to the end (eight times as many lose more by
+// working out places than the last wave costs; one pair of groups a block and not four:
+// 64 tokens of 8 heads written and read 4.0 us, not 5.2).
+template <typename F>
+cudaError_t launch_rows(Rows4Args a, cudaStream_t st, F kernel) {
+  const unsigned x = (unsigned)((a.n + 15ll) / 16), y = (unsigned)(a.d / kGroup + 1) / 2;
   int z = 1;
-  while (z < a.Hkv && (long long)x * y * z < 8 * 152) z *= 2;
+  while (z < a.Hkv && (long long)x * y * z < 32 * 152) z *= 2;
   a.heads = (a.Hkv + z - 1) / z;
   const dim3 grid(x, y, (unsigned)((a.Hkv + a.heads - 1) / a.heads));
-  return pairs == 1 ? launch_pdl(few, grid, dim3(64), 0, st, a) : launch_pdl(many, grid, dim3(64 * kPairs), 0, st, a);
+  return launch_pdl(kernel, grid, dim3(kRowThreads), 0, st, a);
 }
 
 }  // namespace
@@ -324,16 +320,13 @@ cudaError_t launch_rows(Rows4Args a, cudaStream_t st, F1 few, F4 many) {
 cudaError_t launch_write_kv4(Rows4Args a, int dtype, cudaStream_t st) {
   const int elt = dtype == SV_BF16 ? 2 : 4;
   a.wide = wide_rows(a.k, a.k_stride, elt) && wide_rows(a.v, a.v_stride, elt);
-  return dtype == SV_BF16
-             ? launch_rows(a, st, write_kv4_kernel<__nv_bfloat16, 1>, write_kv4_kernel<__nv_bfloat16, kPairs>)
-             : launch_rows(a, st, write_kv4_kernel<float, 1>, write_kv4_kernel<float, kPairs>);
+  return dtype == SV_BF16 ? launch_rows(a, st, write_kv4_kernel<__nv_bfloat16>) : launch_rows(a, st, write_kv4_kernel<float>);
 }
 
 cudaError_t launch_read_kv4(Rows4Args a, int dtype, cudaStream_t st) {
   const int elt = dtype == SV_BF16 ? 2 : 4;
   a.wide = wide_rows(a.k_out, a.k_stride, elt) && wide_rows(a.v_out, a.v_stride, elt);
-  return dtype == SV_BF16 ? launch_rows(a, st, read_kv4_kernel<__nv_bfloat16, 1>, read_kv4_kernel<__nv_bfloat16, kPairs>)
-                          : launch_rows(a, st, read_kv4_kernel<float, 1>, read_kv4_kernel<float, kPairs>);
+  return dtype == SV_BF16 ? launch_rows(a, st, read_kv4_kernel<__nv_bfloat16>) : launch_rows(a, st, read_kv4_kernel<float>);
 }
 
 cudaError_t launch_reps_kv4(Reps4Args a, cudaStream_t st) {
