@@ -19,9 +19,9 @@
 // and an O of their own, joined with the segments: a tile's chain from scores to weights is
 // as long as its products.
 // A softmax thread has 4 keys and every fourth pair of columns. It does not look for
-// a tile's maxima: a row's reference stands until some key's weights, summed over the
-// thread's rows, reach 2^15, which the warps tell each other by a vote; only
-// then (and in a segment's first tile) maxima are taken across lanes and O is rescaled.
+// a tile's maxima: references stand until some row's weights, summed over a thread's
+// 4 keys, pass 2^15, which the warps tell each other by a vote; only then (and in a
+// segment's first tile) maxima are taken across lanes and O is rescaled.
 // Weights are held 2^7 times their size, so that f16's range covers 2^-31 .. 2^8 of the
 // reference.
 //
@@ -67,9 +67,10 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 128, kColK = 256;  // two of at most 64 columns each
 constexpr float kLift = 7.f;    // weights are 2^kLift times their size ...
 constexpr float kTop = 32768.f; // ... and below this, so that f16 (65504) holds them
-// References move when a key's weights sum up to more than kTop: one of at most 64 is
-// above 2^9 then, its score more than 2 (log2) above its reference. kSlack lies below
-// that, so that the move always ends the cause.
+// References move when a row's weights of a thread's 4 keys sum up to more than kTop: one
+// of them is above 2^13 then, its score more than 6 (log2) above its reference. kSlack lies
+// below that, so that the move always ends the cause. (Rows vote one by one: in a sum over
+// several, a row that is not finite would hide those that have to move.)
 constexpr float kSlack = 1.9f;
 
 // What the loading warp tells the others of a tile: tokens that count of each piece
@@ -635,7 +636,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
           }
           first = false;
         }
-        uint64_t all = 0;
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
           load(ch);
@@ -643,10 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
           else weigh(ch, std::false_type());
         }
         if (over) break;  // weights are 2^kLift at most now
+        float most = 0.f;
 #pragma unroll
-        for (int j = 0; j < J; ++j) all = add2(all, sums[j]);
-        const float2 top = unpack2(all);
-        if (__any_sync(0xffffffffu, !first && top.x + top.y > kTop) && lane == 0) sh.over[wg][turn & 1] = i + 1;
+        for (int j = 0; j < J; ++j) {
+          const float2 x = unpack2(sums[j]);
+          most = max3(most, x.x, x.y);  // (leaves NaNs out)
+        }
+        if (__any_sync(0xffffffffu, !first && most > kTop) && lane == 0) sh.over[wg][turn & 1] = i + 1;
         if (!(ok = meet()) || *(volatile uint32_t*)&sh.over[wg][turn & 1] != i + 1) break;
       }
       if (!ok) break;

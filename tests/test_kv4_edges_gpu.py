@@ -1,0 +1,107 @@
+"""The 4-bit cache's attention where rows, lengths or sizes go wrong first: rows that are
+not finite beside others, references of the softmax that have to move, very large and very
+small queries. Against the 64-bit forms of tests/kv4_util.py (where the tolerances stand)."""
+import math
+
+import pytest
+import torch
+
+from sparse_verification_attention_gb300 import api, build_lib
+from tests import kv4_util as U
+from tests import paged_util as P
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA device required for -m gpu tests")
+    build_lib.build()
+    api.lib()
+    torch.cuda.set_device(0)
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def cache(g, s, k, v, k_exp=None):
+    """A 4-bit cache of the rows k, v [B, n, Hkv, d] on pages in any order, and the rows as
+    the cache holds them, in 64 bits."""
+    B, n, H, d = k.shape
+    blk = s.blk
+    nb = -(-n // blk)
+    table = torch.randperm(B * nb, generator=g, device="cuda").to(torch.int32).view(B, nb)
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    kv = api.make_kv4(*[api.alloc_kv4_pool(s, B * nb) for _ in range(2)], table, lens, k_exp)
+    i = torch.arange(n, device="cuda")
+    slots = (table.long()[:, i // blk] * blk + i % blk).flatten().to(torch.int32)
+    rows = [x.flatten(0, 1) for x in (k, v)]
+    api.sv_write_kv4(s, *rows, slots, kv)
+    held = [U.values(*U.quantise(x, e), e).view(B, n, H, d) for x, e in zip(rows, (k_exp, None))]
+    return kv, *held
+
+
+def attend(s, q, kv, dk, dv):
+    out, ws = torch.full_like(q, 7), api.alloc_kv4_workspace(s)
+    api.sv_attend_kv4(s, q, kv, None, dk, dv, None, out, ws)
+    assert api.sv_read_status(ws) == 0
+    return out
+
+
+def all_keys(T, Hkv, n):
+    see = torch.ones(T, Hkv, n + T, dtype=torch.bool)
+    see[:, :, n:] = P.draft_mask(None, T, "cpu")[:, None]
+    return see.cuda()
+
+
+# ------------------------------------------------------------------ rows that are not finite
+# A head's stacked row is r = t * G + g. The tensor cores' softmax has rows 8 j + 2 i and
+# 8 j + 2 i + 1 (i fixed) in one thread.
+def mates(r):
+    return [x for x in range(64) if x % 8 // 2 == r % 8 // 2]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,G,row", [(16, 4, 0), (16, 4, 27), (8, 4, 9), (4, 4, 14), (3, 5, 2)])
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+def test_a_row_that_is_not_finite_reaches_no_other(dtype, T, G, row, what):
+    """The rows that share their threads with it have scores that rise all the way, a dozen
+    powers of two in a tile of 128 keys, so that each share of the keys moves their references
+    many times; the other rows' scores stay small and move none."""
+    B, Hkv, d, n, blk = 8, 8, 128, 3000, 64
+    g = gen(row + T)
+    s = api.make_shape(B, G * Hkv, Hkv, d, blk, T, dtype)
+    k, v = randn(g, B, n, Hkv, d) / 2, randn(g, B, n, Hkv, d)
+    # 16 dims of 3 in the rows: 48 k / sqrt(128) log2(e) = 6.1 k
+    k[..., :16] = (torch.arange(n, device="cuda") * (2 / 128))[None, :, None, None]
+    kv, hk, hv = cache(g, s, k.to(dtype), v.to(dtype))
+    q = randn(g, B, T, Hkv, G, d) / 2
+    q[..., :16] = 0
+    for r in mates(row):
+        if r < T * G:
+            q[:, r // G, :, r % G, :16] = 3
+    q = q.to(dtype)
+    dk, dv = (randn(g, B, T, Hkv, d).to(dtype) for _ in range(2))
+    dk[..., :16] = 0
+    odd = q.clone()
+    odd[:, row // G, :, row % G] = what
+    q[:, row // G, :, row % G] = 0
+    got, plain = (attend(s, x.flatten(2, 3), kv, dk, dv).view(B, T, Hkv, G, d) for x in (odd, q))
+    assert got[:, row // G, :, row % G].isnan().all()
+    rest = torch.ones(T, Hkv, G, dtype=torch.bool, device="cuda")
+    rest[row // G, :, row % G] = False
+    if math.isnan(what):  # such a row takes no part in when references move
+        assert torch.equal(got[:, rest], plain[:, rest])
+    see = all_keys(T, Hkv, n)
+    for b in range(B):
+        o, tol = U.attend(q[b].flatten(1, 2), torch.cat([hk[b], dk[b].double()]), torch.cat([hv[b], dv[b].double()]),
+                          see, dtype == BF16)
+        for x in (got, plain):
+            U.check(x[b][rest], *(y.view(T, Hkv, G, d)[rest] for y in (o, tol)))
