@@ -104,6 +104,20 @@ struct Attend4Args {
   float scale_log2;  // log2(e) / sqrt(d)
   unsigned long long anc[kMaxT];
 };
+// Ends the copies of a CTA that gave up, when nobody waits on its barriers any more. A stage's
+// barrier counts one arrival for K's copies and one for V's; the warps that issue them may have
+// stopped some tiles apart, and a stage that only one of them armed would never complete:
+// arrive(stage) stands in for the other. wait(stage, parity) then ends as the bytes land.
+#ifdef __CUDACC__
+#pragma nv_exec_check_disable
+#endif
+template <typename Arrive, typename Wait>
+__host__ __device__ inline void end_copies(uint32_t k_tiles, uint32_t v_tiles, uint32_t stages, Arrive arrive, Wait wait) {
+  const uint32_t some = k_tiles < v_tiles ? v_tiles : k_tiles, both = k_tiles + v_tiles - some;
+  for (uint32_t i = both; i < some; ++i) arrive(i % stages);
+  for (uint32_t i = some > stages ? some - stages : 0; i < some; ++i) wait(i % stages, i / stages & 1u);
+}
+
 // Each launches the attention over the cache and then the join with the drafts.
 cudaError_t launch_attend4_simt(Attend4Args a, int dtype, cudaStream_t st);
 // bf16, head dims up to 128.

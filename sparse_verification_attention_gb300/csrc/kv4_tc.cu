@@ -103,6 +103,7 @@ struct Control {
   // moves, and by warp of a warpgroup the maxima and sums
   alignas(16) float nm[2 * kTc4Rows], corr[2 * kTc4Rows], mx[4][2 * kTc4Rows], sum[4][2 * kTc4Rows];
   int tiles;                              // of the CTA's share
+  uint32_t copied[2];                     // ... of which K's and V's copies were issued, once both warps are done
   Segment first;                          // its first
   Line line;
 };
@@ -810,12 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
         ++seg;
       }
       if (flags) atomicOr(a.status, flags);
-      if (sh.abort) {  // copies in flight end before the CTA does
-        for (uint32_t k = 0; k < (uint32_t)stages && k < i; ++k) {
-          const uint32_t j = i - 1 - k;
-          mbar_wait_drain(smem_u32(&sh.full[j % stages]), (j / stages) & 1u);
-        }
-      }
+      if (lane == 0) sh.copied[is_v] = i;
     } else if (warp == kScoreWarp) {
       // ------------------------------------------------------------ S^T = K Q^T
       constexpr uint32_t id_s = idesc_f16(N, false, false);
@@ -876,6 +872,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_tc_kernel(const __grid_co
   __syncthreads();
   tc::fence_after();
   if (warp == kScoreWarp) tc::dealloc(tmem, kTmemCols);
+  if (sh.abort && warp == kKLoadWarp && lane == 0)  // copies in flight end before the CTA does
+    end_copies(
+        sh.copied[0], sh.copied[1], (uint32_t)stages, [&](uint32_t st) { mbar_arrive(smem_u32(&sh.full[st])); },
+        [&](uint32_t st, uint32_t parity) { mbar_wait_drain(smem_u32(&sh.full[st]), parity); });
 }
 
 template <int N, int DG>
