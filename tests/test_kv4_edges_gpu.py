@@ -105,3 +105,45 @@ def test_a_row_that_is_not_finite_reaches_no_other(dtype, T, G, row, what):
                           see, dtype == BF16)
         for x in (got, plain):
             U.check(x[b][rest], *(y.view(T, Hkv, G, d)[rest] for y in (o, tol)))
+
+
+# ------------------------------------------------------------------ long contexts
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_every_part_of_a_long_context_counts(dtype):
+    """Dim j of the values is 1.5 in the j-th of 128 runs of keys and 0 elsewhere, so that output
+    j is the weight of that run, to within a thousandth or so of itself: a piece of 16 keys
+    left out or counted twice is 14 thousandths of its run.
+
+    The tolerance is U.attend's with the additions that a sum goes through in place of one a
+    key. On the tensor cores a stream takes every second of its CTA's key tiles in 8 products
+    of 16 keys, each cut off like 17 additions at most (2 u). On the CUDA cores a thread adds
+    a key at a time (u). Both then add a part for each CTA, at most 640. Factors of moved
+    references, two roundings a tile, are counted with them."""
+    n, T, Hq, d, blk = 150_001, 4, 4, 128, 64
+    g = gen(5)
+    s = api.make_shape(1, Hq, 1, d, blk, T, dtype)
+    k = randn(g, 1, n, 1, d).to(dtype)
+    run = torch.arange(n, device="cuda") * 128 // n
+    v = (1.5 * torch.nn.functional.one_hot(run, 128)).to(dtype)[None, :, None]
+    kv, hk, hv = cache(g, s, k, v)
+    assert torch.equal(hv, v.double())
+    q = randn(g, 1, T, Hq, d).to(dtype)
+    dk, dv = randn(g, 1, T, 1, d).to(dtype), torch.zeros(1, T, 1, d, dtype=dtype, device="cuda")
+    out = attend(s, q, kv, dk, dv)[0]
+    f16 = dtype == BF16
+    tiles = -(-n // (128 if f16 else 64))
+    share = tiles // 152 + 2  # (of a CTA, at least so many CTAs have one)
+    additions = (2 * (8 * 17 + 2) * (share // 2 + 1) if f16 else 66 * share) + 2 * 640
+    kk = torch.cat([hk[0], dk[0].double()])[:, 0]
+    see = all_keys(T, 1, n)[:, 0]
+    runs = torch.cat([run, run.new_full((T,), 128)])
+    for h in range(Hq):
+        qh = q[0, :, h].double()
+        x = (qh @ kk.T / math.sqrt(d)).masked_fill(~see, -math.inf)
+        p = torch.softmax(x, -1)
+        o = torch.zeros(T, 129, dtype=torch.float64, device="cuda").index_add_(1, runs, 1.5 * p)[:, :128]
+        big = (qh.abs() @ kk.abs().T / math.sqrt(d)).masked_fill(~see, 0).amax(-1, keepdim=True)
+        w = 2 * ((d + 4) * (2 if f16 else 1) * U.U * big + 12 * U.U + additions * U.U) + (2.0 ** -11 if f16 else 0)
+        tol = (w + U.half_step(dtype)) * o + (2.0 ** -32 * 1.5 * n / 128 if f16 else 0)
+        assert (tol < 0.007 * o).all()  # half of what a piece is
+        U.check(out[:, h], o, tol)
