@@ -35,6 +35,7 @@ struct Control {
   long long piece[2][kPieces];  // of this tile and the next
   int valid[2][kPieces];
   float keep[kSimt4Rows];       // what a row's sums shrink by
+  float unit;                   // of a segment's scores: Q times more than 1 may overflow where no score does
 };
 
 // Rows of p: keys, their lanes' rows in different banks.
@@ -76,8 +77,10 @@ __global__ void __launch_bounds__(kThreads, 2) attend4_simt_kernel(const __grid_
     x = s.next;
     if (s.tiles == 0) continue;
     const int row0 = s.rt * a.rows, rows = min(a.rows, a.T * a.G - row0);
-    const float scale = a.scale_log2 * exp2i(head_exp(a.k_exp, s.h));
+    const int k_exp = head_exp(a.k_exp, s.h);
+    const float scale = a.scale_log2 * exp2i(min(k_exp, 0));
     __syncthreads();  // the segment before has read q and p
+    if (tid == 0) sh.unit = exp2i(max(k_exp, 0));
 #pragma unroll 1
     for (int r = warp; r < RT; r += kThreads / 32) {
       const long long from = (r < rows ? row_at(a, s.b, s.h, row0 + r) : 0) * a.d;
@@ -132,8 +135,9 @@ __global__ void __launch_bounds__(kThreads, 2) attend4_simt_kernel(const __grid_
           }
         }
         float4* to = reinterpret_cast<float4*>(p + (slice * kKeys + key) * PS);
+        const float unit = sh.unit;
 #pragma unroll
-        for (int i = 0; i < RT; i += 4) to[i / 4] = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        for (int i = 0; i < RT; i += 4) to[i / 4] = make_float4(acc[i] * unit, acc[i + 1] * unit, acc[i + 2] * unit, acc[i + 3] * unit);
       }
       // V's bytes are on their way while the weights are made
       uint4 w[kPieces], sv[kPieces];

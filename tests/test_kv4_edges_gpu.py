@@ -107,6 +107,33 @@ def test_a_row_that_is_not_finite_reaches_no_other(dtype, T, G, row, what):
             U.check(x[b][rest], *(y.view(T, Hkv, G, d)[rest] for y in (o, tol)))
 
 
+# ------------------------------------------------------------------ sizes of queries
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("power", [32, -32])
+def test_queries_of_any_size(dtype, d, power):
+    """Queries 2^power times their size over keys 2^-power times theirs (by the heads'
+    exponents), so that the scores are ordinary ones; and a row that is nothing but 1e30 in a dim
+    that no key has, all of whose scores are zero."""
+    B, T, Hkv, G, n = 2, 4, 2, 4, 700
+    g = gen(d)
+    s = api.make_shape(B, G * Hkv, Hkv, d, 64, T, dtype)
+    k, v = randn(g, B, n, Hkv, d), randn(g, B, n, Hkv, d)
+    k[..., 0] = 0
+    e = torch.full((Hkv,), -power, dtype=torch.int32, device="cuda")
+    kv, hk, hv = cache(g, s, (k * 2.0 ** -power).to(dtype), v.to(dtype), e)
+    q, dk, dv = randn(g, B, T, Hkv * G, d), randn(g, B, T, Hkv, d), randn(g, B, T, Hkv, d)
+    dk[..., 0] = 0
+    q, dk, dv = (q * 2.0 ** power).to(dtype), (dk * 2.0 ** -power).to(dtype), dv.to(dtype)
+    q[1, 2, 3] = 0
+    q[1, 2, 3, 0] = 1e30
+    out = attend(s, q, kv, dk, dv)
+    see = all_keys(T, Hkv, n)
+    for b in range(B):
+        U.check(out[b], *U.attend(q[b], torch.cat([hk[b], dk[b].double()]), torch.cat([hv[b], dv[b].double()]), see,
+                                  dtype == BF16))
+
+
 # ------------------------------------------------------------------ long contexts
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_every_part_of_a_long_context_counts(dtype):
