@@ -41,6 +41,7 @@
 // weights of a tile waited in registers that spilled.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <type_traits>
 
 #include "host.h"
@@ -302,7 +303,9 @@ __device__ __noinline__ void lay_out_q(const QRows x, int n, uint32_t to, float*
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       sts128(row + (k >> 1) * (n * 128) + (chunk ^ (k & 1) << 6), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-    if (c == 0) f[r] = x.scale * exp2i(-up);
+    // (the factor stays finite, as scores of zero have to stay zero: where it would not, others
+    // are beyond 2^90 either way)
+    if (c == 0) f[r] = fminf(x.scale * exp2i(-up), FLT_MAX);
   }
   fence_proxy_async_shared();
   __syncwarp();

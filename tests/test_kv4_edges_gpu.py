@@ -134,6 +134,26 @@ def test_queries_of_any_size(dtype, d, power):
                                   dtype == BF16))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("size", [1e30, 3e38])
+def test_largest_queries_under_the_largest_exponent(dtype, size):
+    """A row of one huge element in a dim that neither keys nor drafts have: its scores are
+    zero, whatever the keys' exponent, and its output is the mean of the values."""
+    n, d = 300, 128
+    g = gen(8)
+    s = api.make_shape(1, 4, 1, d, 16, 2, dtype)
+    k, v = randn(g, 1, n, 1, d).to(dtype), randn(g, 1, n, 1, d).to(dtype)
+    k[..., 5] = 0
+    kv, hk, hv = cache(g, s, k, v, torch.full((1,), 32, dtype=torch.int32, device="cuda"))
+    q, dk, dv = torch.zeros(1, 2, 4, d), randn(g, 1, 2, 1, d), randn(g, 1, 2, 1, d).to(dtype)
+    dk[..., 5] = 0
+    q[0, :, ::2, 5], q[0, :, 3, 5] = size, -size
+    q, dk = q.to(dtype).cuda(), dk.to(dtype)
+    out = attend(s, q, kv, dk, dv)[0]
+    U.check(out, *U.attend(q[0], torch.cat([hk[0], dk[0].double()]), torch.cat([hv[0], dv[0].double()]),
+                           all_keys(2, 1, n), dtype == BF16))
+
+
 # ------------------------------------------------------------------ long contexts
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_every_part_of_a_long_context_counts(dtype):
