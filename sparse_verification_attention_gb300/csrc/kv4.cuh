@@ -24,22 +24,6 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t* r) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
       : "r"(w));
 }
-// ... of bytes 1 and 3 alone.
-__device__ __forceinline__ void e2m1x4_to_f16(uint32_t w, uint32_t& r1, uint32_t& r3) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "mov.b32 {a, b, c, d}, %2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, d;\n\t}"
-      : "=r"(r1), "=r"(r3)
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
-      : "=r"(r)
-      : "r"(byte));
-  return r;
-}
 // E4M3 scales of the four bytes of a word as two pairs of halves, exact.
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& r01, uint32_t& r23) {
   asm("{\n\t.reg .b16 a, b;\n\t"

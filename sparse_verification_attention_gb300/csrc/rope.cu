@@ -18,7 +18,7 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// V elements (8 or 4) of bf16 or fp32, as 32-bit floats and back. (Loads past L1:
+// V elements (4) of bf16 or fp32, as 32-bit floats and back. (Loads past L1:
 // under a programmatic launch the rows may be written while this grid is already
 // resident, and a row that is rotated in place is.)
 template <typename T, int V>
