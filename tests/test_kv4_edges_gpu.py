@@ -107,6 +107,30 @@ def test_a_row_that_is_not_finite_reaches_no_other(dtype, T, G, row, what):
             U.check(x[b][rest], *(y.view(T, Hkv, G, d)[rest] for y in (o, tol)))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("of", ["draft_k", "draft_v"])
+def test_a_draft_that_is_not_finite_reaches_those_that_see_it(dtype, of):
+    """A tree of drafts, one of them NaN in one head: its own rows of that head and its
+    children's are NaN, the others the same bits as without."""
+    B, T, Hkv, G, d, n = 2, 6, 2, 4, 64, 200
+    parents = [-1, 0, 0, 1, 1, 2]
+    g = gen(3)
+    s = api.make_shape(B, G * Hkv, Hkv, d, 16, T, dtype)
+    kv, _, _ = cache(g, s, randn(g, B, n, Hkv, d).to(dtype), randn(g, B, n, Hkv, d).to(dtype))
+    q = randn(g, B, T, Hkv * G, d).to(dtype)
+    x = dict(draft_k=randn(g, B, T, Hkv, d).to(dtype), draft_v=randn(g, B, T, Hkv, d).to(dtype))
+    outs = []
+    for what in (0.0, math.nan):
+        x[of][1, 1, 1] = what
+        out, ws = torch.full_like(q, 7), api.alloc_kv4_workspace(s)
+        api.sv_attend_kv4(s, q, kv, None, x["draft_k"], x["draft_v"], parents, out, ws)
+        assert api.sv_read_status(ws) == 0
+        outs.append(out.view(B, T, Hkv, G, d))
+    hit = torch.zeros(B, T, Hkv, dtype=torch.bool, device="cuda")
+    hit[1, [1, 3, 4], 1] = True
+    assert outs[1][hit].isnan().all() and torch.equal(outs[1][~hit], outs[0][~hit])
+
+
 # ------------------------------------------------------------------ sizes of queries
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("d", [64, 128, 256])
