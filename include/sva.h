@@ -658,7 +658,9 @@ sv_status sv_read_kv4(const sv_shape* shape, const sv_kv4* kv, const int32_t* sl
  * reps: [B, Hkv, nb_max, d] fp32; the scoring calls take them as they are (their
  * sv_kv descriptor names any pool: they read none). Blocks on a page outside the pool
  * raise SV_FLAG_BAD_PAGE and are left out, lengths outside [0, nb_max * blk]
- * raise SV_FLAG_BAD_LENGTH and are clamped (workspace may be NULL). */
+ * raise SV_FLAG_BAD_LENGTH and are clamped (workspace may be NULL). The sums are
+ * fp32 on the tensor cores, whose additions may cut off instead of rounding (a
+ * last-place unit of the sum so far each). */
 sv_status sv_build_reps_kv4(const sv_shape* shape, const sv_kv4* kv, const int32_t* from_len,
                             int max_blocks, float* reps, void* workspace, void* stream);
 
@@ -680,6 +682,7 @@ size_t sv_kv4_workspace_bytes(const sv_shape* shape);
  * attended in every case, its first seq_ctx % blk tokens; the rest of its page
  * may hold anything. Keys on a page outside the pool are left out
  * (SV_FLAG_BAD_PAGE), lengths are clamped as above.
+ * A row of q or of the drafts that is not finite reaches only the rows that see it.
  * On the tensor cores the products take values and weights in f16: values are
  * exact, q is scaled by a power of two per row (exact down to 2^-24 of the row's
  * largest element), a softmax weight is rounded to f16 (2^-11) ahead of the

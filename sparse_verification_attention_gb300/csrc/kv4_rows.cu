@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(kRowThreads) read_kv4_kernel(const __grid_cons
 // instead: in m16n8k16 a lane's A registers lie at the rows and columns of its four sums and
 // at those 8 columns behind, so S += A (I above I) adds two tokens' halves to the lane's own
 // sums. (A NaN reaches the sums in its row of 4 lanes, which are the same dims of the group's
-// other tokens.)
+// other tokens. The tensor cores' fp32 sums may be cut off where an addition rounds: a step, not
+// half of one, of each of the blk / 4 sums that a lane adds up.)
 // The same blocks: 51 us with one head a warp, whose lengths, page and places took as many
 // instructions as a third of its sums (72% of the issue slots, HBM at 0.6 of its rate); 41.7 us
 // now, 5.0 TB/s. Five CTAs an SM; six spill (44.7), four 42.8.

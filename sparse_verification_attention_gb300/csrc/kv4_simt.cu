@@ -8,7 +8,7 @@
 // tiles of 4 to 32, the smallest that holds them.
 //
 // Bound by issue slots (a fifth of the scores' instructions are loads of Q, an eighth of the
-// outputs' loads of weights): fp32, 16384 tokens, 32 rows of 8 heads of 128, 95 us, 23 TFLOP/s;
+// outputs' loads of weights): fp32, 16384 tokens, 32 rows of 8 heads of 128, 92 us, 23 TFLOP/s;
 // bf16 heads of 256, 2 x 131072 tokens, 8 tokens each, 517 us, one, 155. K a tile ahead in
 // registers gained nothing. Where contexts are short by the latency of one round: 5 sequences
 // of 0 to 1500 tokens, 8 rows of 4 heads of 64, 14 us.
@@ -273,6 +273,8 @@ cudaError_t launch_attend4_simt(Attend4Args a, int dtype, cudaStream_t st) {
   a.ppt = kPieces;
   a.ppt_shift = 2;
   a.streams = 1;
+  // (1, 2 and 4 tiles: 16 sequences of 1 to 32768 tokens, 8 heads of 128, one token, 243, 245 and
+  // 248 us; 64 of 50 to 3000, 4 heads of 64, 8 rows, 55, 56 and 62)
   a.pair_cost = 1;
   if (a.rows <= 4) return launch_rows<4>(a, dtype, st);
   if (a.rows <= 8) return launch_rows<8>(a, dtype, st);

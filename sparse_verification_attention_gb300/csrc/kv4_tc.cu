@@ -9,9 +9,10 @@
 // row. (V^T in TMEM as well: 190 us instead of 188 in the case below, as an MMA of 128 x N x 16
 // takes 65 cycles with A in TMEM, for any N up to 128, and 47 with A in shared memory, N up
 // to 64.)
-// Code times scale has at most five significant bits and is exact in f16. Q is
-// scaled by a power of two per row so that its largest element lies in [2^14, 2^15),
-// exact as well; factor and exponents go into the softmax's scale.
+// Code times scale has at most six significant bits and is exact in f16. Q is
+// scaled by a power of two per row so that its largest element lies in [2^14, 2^15):
+// exact for elements down to 2^-24 of it, below within 2^-39 of it (half of f16's smallest
+// step); factor and exponents go into the softmax's scale.
 //
 // Twenty warps: four for K and four for V (codes to halves), eight of softmax, and four that
 // copy K, copy V and lay out Q of later segments, issue the MMAs of the scores, issue those of
@@ -23,10 +24,11 @@
 // 4 keys, pass 2^15, which the warps tell each other by a vote; only then (and in a
 // segment's first tile) maxima are taken across lanes and O is rescaled.
 // Weights are held 2^7 times their size, so that f16's range covers 2^-31 .. 2^8 of the
-// reference.
+// reference. As an operand of the products a weight has f16's 11 bits (2^-11, an eighth of the
+// output's own rounding to bf16), which is what lets V be halves; its sum is fp32's.
 //
-// What bounds it. Four sequences of 131072 tokens, 8 heads of 128, 32 rows: 156 us, 3.9 TB/s
-// of pages, 0.57 of the copy rate. A tile of 128 keys takes about 1400 cycles, of which the MMA
+// What bounds it. Four sequences of 131072 tokens, 8 heads of 128, 32 rows: 154 us, 3.9 TB/s
+// of pages, 0.58 of the copy rate. A tile of 128 keys takes about 1400 cycles, of which the MMA
 // pipe needs 900 (8 x 65 + 8 x 47), shared memory about 900 (bytes in, V as halves in
 // and out, P) and the issue slots about 900. (When it was 161 us: without the products 145,
 // without the conversions 129, without softmax 147, without any of them 108.) More
@@ -35,7 +37,7 @@
 // memory: 188; pages past L2's reach evict-first 164, before 170.
 // Short calls: everything that runs once is fetched from a cold instruction cache at 12 to 30
 // cycles an instruction, so it is rolled, short and split among the warps. Eight
-// sequences of 64 selected blocks, trees of 16, 128 rows a head: 35 us, of which a CTA spends
+// sequences of 64 selected blocks, trees of 16, 128 rows a head: 34 us, of which a CTA spends
 // 10 until its first scores (lengths, pages and first copies one after the other), 2 a tile and 2 at a
 // segment's end; 63 when one warp laid out Q, all threads tracked all references, and the
 // weights of a tile waited in registers that spilled.
@@ -54,7 +56,11 @@ namespace {
 
 using namespace kv4;
 
-constexpr int kPairCost = 5;  // key tiles' time that beginning a pair takes
+// Key tiles' time that beginning a pair takes. 3, 5 and 8 of them: 16 ragged sequences of 1 to
+// 32768 tokens 59, 55 and 56 us (8 heads of 128, one token), 37, 34 and 34 (4 heads of 64), 117,
+// 101 and 97 (4 heads of 128, 128 rows); 64 sequences of 50 to 3000 36, 37 and 39 (one token) and
+// 129, 119 and 119 (128 rows).
+constexpr int kPairCost = 5;
 static_assert(kPairCost <= kMaxPairCost, "the calls' limits count this many");
 constexpr int kKeys = 128, kPieces = kKeys / kPiece;
 // Rings. Copies run at most kMaxStages tiles ahead of V, V two ahead of its products, so the

@@ -73,9 +73,12 @@ struct Chunk {
 // makes them once and keeps them in registers, r is the row's 1 / sqrt(mean + eps).
 //
 // Bound by HBM: every row is read and written once. 20,011 rows of 36 normed heads of 128 in
-// bf16: 64.7 us, 5.9 TB/s, 0.86 of the copy rate; 15,439 rows of 32 + 8 + 8 heads into the
+// bf16: 63.9 us, 5.9 TB/s, 0.87 of the copy rate; 15,439 rows of 32 + 8 + 8 heads into the
 // cache: 61.9 us, 0.92. (28 CTAs of a warp an SM; 24 66.1 and 64.3, 32, in fewer registers, 65.9 and
 // 64.8; CTAs of eight warps 74.5 and 68.4. Two or three rows in flight a lane: 84 and 80 us.)
+// fp32 spills in the 72 registers that this leaves: 10,007 rows of 36 normed heads 63 us (floor 55),
+// half of each head rotated 84, neighbours paired without a norm 77; 20 CTAs, which spill nothing,
+// 61, 62 and 63.
 // FULL: every lane has two chunks and all of them turn.
 template <typename T, int V, bool INTER, bool FULL>
 __global__ void __launch_bounds__(kThreads, 28) rope_kernel(const __grid_constant__ RopeArgs a, int width) {
@@ -264,7 +267,7 @@ cudaError_t launch(RopeArgs a, cudaStream_t st) {
   const bool full = a.rot == a.d && a.d == 2 * V * width;
   const unsigned blocks = (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
   // Few warps take a side each: one side's rows after the other's wait for memory three
-  // times (23 tokens of 16 heads: 2.9 us a call, 5.0 with the sides in turn; 32 of 40, without
+  // times (23 tokens of 16 heads: 2.6 us a call, 5.0 with the sides in turn; 32 of 40, without
   // values: 2.1 and 2.5).
   const dim3 grid(blocks, warps < 16 * 152 ? 3 : 1);
   return launch_pdl(full ? rope_kernel<T, V, INTER, true> : rope_kernel<T, V, INTER, false>, grid, dim3(kThreads), 0, st, a,
